@@ -16,6 +16,10 @@ Per decode step (HyperQwen context-lookup article, "lookup 草稿的原理：三
 
 plus the fused launches ``propose_fuse_sched`` and ``verify_append`` that the
 ``Step`` driver uses (two kernels per step).
+
+Beside the step, the target's side of it: a paged K/V cache (``Cache`` and the
+``cache_*`` calls), trees of drafted tokens (``tree_masks``, ``tree_accept``)
+and the attention that reads both (``tree_attend``, ``prompt_attend``).
 """
 from __future__ import annotations
 
@@ -30,10 +34,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libclk.so")
 
 OK, EINVAL, ECAPACITY, ECUDA, ENOTIMPL, ESTATE = 0, -1, -2, -3, -4, -5
-BF16, F32 = 0, 1
+BF16, F32, F16 = 0, 1, 2
 SENT = -1
 BLOCK = 16
 MAX_BATCH = 8192
+TREE_MAX = 64
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -82,6 +87,19 @@ class SlotInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n", "mode", "streak", "miss", "has_prev", "cur_len", "n_indexed")]
 
 
+class PoolDesc(ctypes.Structure):
+    """clk_pool"""
+    _fields_ = [("d_base", _P), ("dtype", _I32), ("planes", _I32), ("heads", _I32), ("dim", _I32),
+                ("plane_stride", _I64), ("page_stride", _I64), ("head_stride", _I64), ("tok_stride", _I64)]
+
+
+class AttnDesc(ctypes.Structure):
+    """clk_attn"""
+    _fields_ = [(n, _I32) for n in ("dtype", "q_heads", "kv_heads", "dim")] + [("scale", ctypes.c_float)] + \
+               [(n, _P) for n in ("d_q", "d_k", "d_v", "d_out")] + \
+               [(n, _I64) for n in ("q_req", "q_row", "q_head", "k_req", "k_row", "k_head", "v_req", "v_row", "v_head")]
+
+
 # (name, restype, argtypes) of every exported entry point
 _SIGS = [
     ("clk_params_default", None, [_P]),
@@ -123,6 +141,23 @@ _SIGS = [
     ("clk_lookup_read_history", ctypes.c_int, [_P, _I32, _P, _I64, ctypes.POINTER(_I64), _P]),
     ("clk_lookup_restore_state", ctypes.c_int, [_P, _I32, _P, _P, _P]),
     ("clk_lookup_destroy", None, [_P]),
+    ("clk_cache_workspace_bytes", ctypes.c_int, [_I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]),
+    ("clk_cache_create", ctypes.c_int, [ctypes.POINTER(_P), _I32, _I32, _I32, _I32, _P, ctypes.c_size_t]),
+    ("clk_cache_reset", ctypes.c_int, [_P, _P]),
+    ("clk_cache_buffers", ctypes.c_int, [_P, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_P)]),
+    ("clk_cache_grow", ctypes.c_int, [_P, _P, _I32, _P, _P]),
+    ("clk_cache_append", ctypes.c_int, [_P, _P, _I32, _P, _I32, _I32, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
+    ("clk_cache_fork", ctypes.c_int, [_P, _P, _P, _I32, _P, _P]),
+    ("clk_cache_free", ctypes.c_int, [_P, _P, _I32, _P]),
+    ("clk_cache_compact", ctypes.c_int, [_P, _P, _P, _P]),
+    ("clk_cache_status", ctypes.c_int, [_P, ctypes.POINTER(_I32), ctypes.POINTER(_I32), _P]),
+    ("clk_cache_status_clear", ctypes.c_int, [_P, _P]),
+    ("clk_cache_destroy", None, [_P]),
+    ("clk_tree_masks", ctypes.c_int, [_I32, _I32, _P, _P, _P, _P]),
+    ("clk_tree_accept", ctypes.c_int, [_I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    ("clk_attend_scratch_bytes", ctypes.c_int, [_I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]),
+    ("clk_tree_attend", ctypes.c_int, [_P, _P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("clk_prompt_attend", ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _P, _I32, _P, _P, ctypes.c_size_t, _P]),
 ]
 
 
@@ -486,6 +521,234 @@ def verify_append(h: Lookup, slots, logits, block, length, argmax, accept, emitt
                                    _ptr(length_hint, shape=(B,), name="length_hint"),
                                    _ptr(argmax, shape=(B, BLOCK)), _ptr(accept, shape=(B,)),
                                    _ptr(emitted, shape=(B,)), _ptr(out_tok, shape=(B, BLOCK)), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The target's paged K/V cache
+# ---------------------------------------------------------------------------
+_POOL_DTYPES = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}
+
+
+class Cache:
+    """Page tables of up to `max_slots` requests over the pages of a pool.
+
+    The pool is the caller's tensor [2 * layers, >= num_pages, kv_heads,
+    page_tokens, dim] (any strides with the rows contiguous), handed to the
+    calls that move rows or read them.  ``length`` [max_slots], ``table``
+    [max_slots, max_pages] and ``refs`` [num_pages] are int32 views of the
+    workspace, to be read in stream order."""
+
+    def __init__(self, max_slots: int, max_pages: int, num_pages: int, page_tokens: int = 64, device="cuda",
+                 stream=None):
+        L = lib()
+        n = ctypes.c_size_t()
+        _check("clk_cache_workspace_bytes", L.clk_cache_workspace_bytes(max_slots, max_pages, num_pages, ctypes.byref(n)))
+        self.workspace_bytes = n.value
+        self.workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
+        h = _P()
+        base = self.workspace.data_ptr()
+        _check("clk_cache_create", L.clk_cache_create(ctypes.byref(h), max_slots, max_pages, num_pages, page_tokens,
+                                                      base, n.value))
+        self.handle = h
+        self.max_slots, self.max_pages, self.num_pages = max_slots, max_pages, num_pages
+        self.page_tokens = page_tokens
+        at = [_P(), _P(), _P()]
+        _check("clk_cache_buffers", L.clk_cache_buffers(h, *(ctypes.byref(p) for p in at)))
+        words = self.workspace[:n.value // 4 * 4].view(torch.int32)
+
+        def view(p, *shape):
+            first = (p.value - base) // 4
+            size = 1
+            for x in shape:
+                size *= x
+            return words[first:first + size].view(*shape)
+
+        self.length, self.table = view(at[0], max_slots), view(at[1], max_slots, max_pages)
+        self.refs = view(at[2], num_pages)
+        self.reset(stream)
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h:
+            try:
+                lib().clk_cache_destroy(h)
+            except Exception:
+                pass
+            self.handle = None
+
+    def reset(self, stream=None):
+        """Every slot empty, every page free."""
+        _check("clk_cache_reset", lib().clk_cache_reset(self.handle, _stream(stream)))
+
+    # -- inspection (status synchronises) ---------------------------------
+    def status(self, stream=None):
+        st, det = _I32(), _I32()
+        _check("clk_cache_status", lib().clk_cache_status(self.handle, ctypes.byref(st), ctypes.byref(det),
+                                                          _stream(stream)))
+        return st.value, det.value
+
+    def status_clear(self, stream=None):
+        _check("clk_cache_status_clear", lib().clk_cache_status_clear(self.handle, _stream(stream)))
+
+
+def _pool_desc(h: Cache, pool: torch.Tensor) -> PoolDesc:
+    if not pool.is_cuda or pool.dim() != 5:
+        raise ValueError("pool must be a CUDA tensor [planes, pages, heads, page_tokens, dim]")
+    planes, pages, heads, tokens, dim = pool.shape
+    st = pool.stride()
+    if pool.dtype not in _POOL_DTYPES or st[4] != 1 or pages < h.num_pages or tokens != h.page_tokens:
+        raise ValueError(f"pool must be bfloat16, float16 or float32 with contiguous rows, >= {h.num_pages} pages and "
+                         f"{h.page_tokens} tokens a page, got {pool.dtype} {tuple(pool.shape)}")
+    return PoolDesc(pool.data_ptr(), _POOL_DTYPES[pool.dtype], planes, heads, dim, st[0], st[1], st[2], st[3])
+
+
+def cache_grow(h: Cache, slots, count, stream=None):
+    """Room for count[b] more tokens in each slot (clk_cache_grow)."""
+    B = slots.numel()
+    _check("clk_cache_grow", lib().clk_cache_grow(h.handle, _ptr(slots, name="slots"), B,
+                                                  _ptr(count, shape=(B,), name="count"), _stream(stream)))
+
+
+def cache_append(h: Cache, slots, pool, k, v, count, layer: int = 0, path=None, offsets=None, stream=None):
+    """K and V rows into the slots' last count[b] positions (clk_cache_append).
+
+    k, v: [layers, B, N, kv_heads, dim], row ``path[b, i]`` (or i) of request
+    b; or, with ``offsets`` (int64 [B+1]), [layers, T, kv_heads, dim]."""
+    B = slots.numel()
+    d = _pool_desc(h, pool)
+    lead = 2 if offsets is not None else 3
+    if k.dim() != lead + 2 or k.shape != v.shape or k.stride() != v.stride() or not (k.is_cuda and v.is_cuda):
+        raise ValueError("k and v must be CUDA tensors of one shape and layout, "
+                         "[layers, B, N, heads, dim] or, with offsets, [layers, T, heads, dim]")
+    if k.dtype != pool.dtype or v.dtype != pool.dtype or tuple(k.shape[lead:]) != (d.heads, d.dim):
+        raise ValueError("k and v must have the pool's type, heads and dim")
+    st = k.stride()
+    if d.dim > 1 and st[-1] != 1:
+        raise ValueError("rows of k and v must be contiguous")
+    if offsets is None:
+        if k.shape[1] != B or (B > 1 and st[1] != k.shape[2] * st[2]):
+            raise ValueError("k and v must hold B requests of N rows, one request's rows after another's")
+        N, row = k.shape[2], st[2]
+    else:
+        N, row = k.shape[1], st[1]
+    _check("clk_cache_append",
+           lib().clk_cache_append(h.handle, _ptr(slots, name="slots"), B, ctypes.byref(d), layer, k.shape[0],
+                                  k.data_ptr(), v.data_ptr(), st[0], row, st[-2], N,
+                                  _ptr(offsets, torch.int64, (B + 1,), "offsets"),
+                                  _ptr(path, shape=(B, N), name="path"), _ptr(count, shape=(B,), name="count"),
+                                  _stream(stream)))
+
+
+def cache_fork(h: Cache, src, dst, pool, stream=None):
+    """Slots dst[b] (empty) become copies of src[b] (clk_cache_fork)."""
+    B = src.numel()
+    d = _pool_desc(h, pool)
+    _check("clk_cache_fork", lib().clk_cache_fork(h.handle, _ptr(src, name="src"), _ptr(dst, shape=(B,), name="dst"), B,
+                                                  ctypes.byref(d), _stream(stream)))
+
+
+def cache_free(h: Cache, slots, stream=None):
+    """Empties the slots (clk_cache_free)."""
+    _check("clk_cache_free", lib().clk_cache_free(h.handle, _ptr(slots, name="slots"), slots.numel(), _stream(stream)))
+
+
+def cache_compact(h: Cache, pool, moved=None, stream=None):
+    """Moves the pages in use to the lowest numbers (clk_cache_compact);
+    ``moved`` (int32 [1] or None) receives how many moved."""
+    d = _pool_desc(h, pool)
+    _check("clk_cache_compact", lib().clk_cache_compact(h.handle, ctypes.byref(d), _ptr(moved, shape=(1,), name="moved"),
+                                                        _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Trees of drafted tokens, and attention
+# ---------------------------------------------------------------------------
+def tree_masks(parent, nodes, mask, stream=None):
+    """Ancestor masks (int64 [B, N]) of trees given by their nodes' parents."""
+    B, N = parent.shape
+    _check("clk_tree_masks", lib().clk_tree_masks(B, N, _ptr(parent, name="parent"), _ptr(nodes, shape=(B,), name="nodes"),
+                                                  _ptr(mask, torch.int64, (B, N), "mask"), _stream(stream)))
+
+
+def tree_accept(tok, parent, nodes, argmax, accept, path, emitted, out_tok, stream=None):
+    """Greedy verification of trees (clk_tree_accept); argmax: the target's
+    answers at the nodes, e.g. verify_greedy's."""
+    B, N = tok.shape
+    _check("clk_tree_accept",
+           lib().clk_tree_accept(B, N, _ptr(tok, name="tok"), _ptr(parent, shape=(B, N), name="parent"),
+                                 _ptr(nodes, shape=(B,), name="nodes"), _ptr(argmax, shape=(B, N), name="argmax"),
+                                 _ptr(accept, shape=(B,), name="accept"), _ptr(path, shape=(B, N), name="path"),
+                                 _ptr(emitted, shape=(B,), name="emitted"), _ptr(out_tok, shape=(B, N), name="out_tok"),
+                                 _stream(stream)))
+
+
+def attend_scratch(q_heads: int, kv_heads: int, dim: int, device="cuda") -> torch.Tensor:
+    """A scratch buffer for tree_attend / prompt_attend with these heads."""
+    n = ctypes.c_size_t()
+    _check("clk_attend_scratch_bytes", lib().clk_attend_scratch_bytes(q_heads, kv_heads, dim, ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _attn_desc(q, k, v, out, scale: float) -> AttnDesc:
+    """q [.., q_heads, dim], k and v [.., kv_heads, dim], with 1 or 2 leading axes (prompt, tree)."""
+    n = q.dim()
+    if k.dim() != n or v.dim() != n or out.shape != q.shape or not out.is_contiguous() or k.shape != v.shape \
+            or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and out (contiguous) must have one shape, k and v another that differs in the heads only")
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda):
+        raise ValueError("q, k, v and out must be CUDA tensors")
+    dt = q.dtype
+    if dt not in _POOL_DTYPES or k.dtype != dt or v.dtype != dt or out.dtype != dt:
+        raise ValueError("q, k, v and out must have one type of bfloat16, float16 or float32")
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    if q.shape[-1] > 1 and (sq[-1] != 1 or sk[-1] != 1 or sv[-1] != 1):
+        raise ValueError("rows of q, k and v must be contiguous")
+    if n == 3:
+        sq, sk, sv = (0,) + sq, (0,) + sk, (0,) + sv
+    return AttnDesc(_POOL_DTYPES[dt], q.shape[-2], k.shape[-2], q.shape[-1], scale, q.data_ptr(), k.data_ptr(),
+                    v.data_ptr(), out.data_ptr(), sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], sv[0], sv[1], sv[2])
+
+
+def tree_attend(h: Cache, slots, pool, layer: int, q, k, v, nodes, mask, scale: float, out, scratch, ctx=None,
+                stream=None):
+    """Attention of drafted trees over the cache (clk_tree_attend).
+
+    q [B, N, q_heads, dim], k and v [B, N, kv_heads, dim] of the new tokens
+    (strided), mask int64 [B, N], out [B, N, q_heads, dim]; ctx (int32 [B] or
+    None: the slots' lengths) cached rows that are seen."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, q_heads, dim]")
+    B, N = q.shape[0], q.shape[1]
+    d = _pool_desc(h, pool)
+    a = _attn_desc(q, k, v, out, scale)
+    _check("clk_tree_attend",
+           lib().clk_tree_attend(h.handle, _ptr(slots, shape=(B,), name="slots"), B, ctypes.byref(d), layer,
+                                 ctypes.byref(a), N, _ptr(nodes, shape=(B,), name="nodes"),
+                                 _ptr(mask, torch.int64, (B, N), "mask"), _ptr(ctx, shape=(B,), name="ctx"),
+                                 _ptr(scratch, torch.uint8, name="scratch"), scratch.numel(), _stream(stream)))
+
+
+def prompt_attend(q, k, v, offsets, scale: float, out, scratch, cache: Optional[Cache] = None, slots=None, pool=None,
+                  layer: int = 0, ctx=None, stream=None):
+    """Causal attention of packed prompts (clk_prompt_attend).
+
+    q [T, q_heads, dim], k and v [T, kv_heads, dim] (strided), request b's
+    rows offsets[b] .. offsets[b+1] (int64 [B+1]), out [T, q_heads, dim].
+    With cache, slots, pool and ctx (int32 [B]) the rows also see the slots'
+    first ctx cached rows."""
+    if q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, dim]")
+    B = offsets.numel() - 1
+    if cache is None and (slots is not None or pool is not None or ctx is not None):
+        raise ValueError("slots, pool and ctx need a cache")
+    d = _pool_desc(cache, pool) if cache is not None else None
+    a = _attn_desc(q, k, v, out, scale)
+    _check("clk_prompt_attend",
+           lib().clk_prompt_attend(ctypes.byref(a), _ptr(offsets, torch.int64, (B + 1,), "offsets"), B, q.shape[0],
+                                   cache.handle if cache is not None else None, _ptr(slots, shape=(B,), name="slots"),
+                                   ctypes.byref(d) if d is not None else None, layer,
+                                   _ptr(ctx, shape=(B,), name="ctx"), _ptr(scratch, torch.uint8, name="scratch"),
+                                   scratch.numel(), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

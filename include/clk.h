@@ -73,7 +73,7 @@ enum {
     CLK_ESTATE = -5     /* call out of order (e.g. handle not set up) */
 };
 
-enum { CLK_DTYPE_BF16 = 0, CLK_DTYPE_F32 = 1 };
+enum { CLK_DTYPE_BF16 = 0, CLK_DTYPE_F32 = 1, CLK_DTYPE_F16 = 2 /* pools and attention only */ };
 
 #define CLK_SENT (-1)
 #define CLK_BLOCK 16        /* slots in a verify block and in a lookup draft */
@@ -485,6 +485,206 @@ CLK_API int clk_verify_sample_exact_append(clk_lookup* h, const int32_t* d_slots
                                            const float* d_inv_temp, const float* d_uniform, int32_t* d_accept,
                                            int32_t* d_emitted, int32_t* d_out_tok, void* d_scratch,
                                            size_t scratch_bytes, clk_stream_t s);
+
+/* ---------------------------------------------------------------------- */
+/* The target's paged K/V cache                                            */
+/* ---------------------------------------------------------------------- */
+/* Verification asks the target for every drafted position's logits; its
+ * attention reads the K and V rows of the tokens that were committed.  They
+ * lie in pages of `page_tokens` rows that the caller owns (a clk_pool).  A
+ * clk_cache keeps, in a caller-owned device workspace, which pages each slot
+ * holds (a page table and a length per slot) and how many slots hold each
+ * page.  Drafted tokens' K and V are not written to pages: they stay in the
+ * caller's block buffers until the accepted ones are known
+ * (clk_cache_append), so a rejected draft costs no page and no clean-up.
+ *
+ * Free pages are handed out lowest number first, request by request in batch
+ * order, so that page tables depend on the calls alone and not on timing.
+ * Only whole pages are shared between slots (clk_cache_fork): the page that a
+ * slot still writes to is its own.  All entry points enqueue on the stream;
+ * only clk_cache_status synchronises.  Device-side problems are latched in
+ * the workspace as clk_lookup's are (first one wins, with the slot, or the
+ * batch position where the slot itself is bad).  A handle is used from one
+ * stream at a time. */
+typedef struct clk_cache clk_cache; /* opaque host handle */
+
+/* The pages of every plane: element (plane, page, head, token, d) lies at
+ * d_base + plane*plane_stride + page*page_stride + head*head_stride +
+ * token*tok_stride + d (strides in elements, >= 0; any order of the four).
+ * Layer l's K is plane 2l and its V plane 2l + 1.  Rows of one page must not
+ * overlap. */
+typedef struct clk_pool {
+    void* d_base;
+    int32_t dtype;  /* CLK_DTYPE_BF16, CLK_DTYPE_F16 or CLK_DTYPE_F32 */
+    int32_t planes; /* 2 * layers */
+    int32_t heads;  /* K/V heads */
+    int32_t dim;    /* elements of a row, 1 .. 256 */
+    int64_t plane_stride, page_stride, head_stride, tok_stride;
+} clk_pool;
+
+/* Bytes of workspace for max_slots page tables of up to max_pages pages each
+ * over num_pages pages (each of the three at least 1; num_pages and
+ * max_slots * max_pages at most 2^30). */
+CLK_API int clk_cache_workspace_bytes(int32_t max_slots, int32_t max_pages, int32_t num_pages, size_t* bytes);
+
+/* Creates a host handle over a caller-owned workspace (256-byte aligned).
+ * page_tokens: 16, 32, 64 or 128 rows a page; max_pages * page_tokens at most
+ * 2^30.  The content is undefined until clk_cache_reset has run on it. */
+CLK_API int clk_cache_create(clk_cache** h, int32_t max_slots, int32_t max_pages, int32_t num_pages,
+                             int32_t page_tokens, void* d_workspace, size_t bytes);
+
+/* Every slot empty, every page free, status clear. */
+CLK_API int clk_cache_reset(clk_cache* h, clk_stream_t s);
+
+/* Device arrays of the workspace, for the caller to read (in stream order):
+ * d_len [max_slots] tokens held, d_table [max_slots, max_pages] page numbers
+ * (-1 past the last one held), d_refs [num_pages] slots that hold the page.
+ * Any of the three may be NULL. */
+CLK_API int clk_cache_buffers(clk_cache* h, int32_t** d_len, int32_t** d_table, int32_t** d_refs);
+
+/* Makes room: slot d_slots[b] grows by d_count[b] tokens, and takes the free
+ * pages that this needs.  The rows' content is what clk_cache_append writes.
+ * A request that its table (max_pages) cannot hold, or whose pages and those
+ * of the requests before it in the batch outnumber the free pages, is left
+ * as it was and latches CLK_ECAPACITY; a negative count or a bad slot
+ * latches CLK_EINVAL. */
+CLK_API int clk_cache_grow(clk_cache* h, const int32_t* d_slots, int32_t B, const int32_t* d_count, clk_stream_t s);
+
+/* Writes K and V rows of `layers` layers from `layer0` on: request b's rows
+ * i < d_count[b] go to its slot's last d_count[b] positions, len - count + i.
+ * Row i is source row r = d_path[b*N + i] of request b, or r = i where d_path
+ * is NULL (d_path: the accepted nodes of a tree, clk_tree_accept); 0 <= r <
+ * the request's rows.  The request's rows start at row b*N of the source (N
+ * rows each), or at d_off[b] where d_off is given (int64 [B+1], N is then
+ * the total number of rows, d_path must be NULL and request b has
+ * d_off[b+1] - d_off[b] rows).  Source element (layer l, row, head, d) lies
+ * at d_k + l*layer_stride + row*row_stride + head*head_stride + d, and the
+ * same for d_v (elements of the pool's type).  A count outside 0 .. min(len,
+ * rows), offsets outside 0 .. N or falling, a path entry out of range or a
+ * bad slot latches CLK_EINVAL; the rows concerned are not written.  Source
+ * and pool must not overlap. */
+CLK_API int clk_cache_append(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool, int32_t layer0,
+                             int32_t layers, const void* d_k, const void* d_v, int64_t layer_stride,
+                             int64_t row_stride, int64_t head_stride, int64_t N, const int64_t* d_off,
+                             const int32_t* d_path, const int32_t* d_count, clk_stream_t s);
+
+/* Slot d_dst[b] (empty) becomes a copy of slot d_src[b]: it shares the whole
+ * pages, and the rows of a last page that is not full are copied to a page
+ * of its own, in every plane.  One source may be forked into several slots
+ * of a batch; no slot is both a source and a destination of it.  A bad slot
+ * or a destination that is not empty latches CLK_EINVAL, a lack of pages
+ * CLK_ECAPACITY (as in clk_cache_grow), and that destination stays as it
+ * was. */
+CLK_API int clk_cache_fork(clk_cache* h, const int32_t* d_src, const int32_t* d_dst, int32_t B, const clk_pool* pool,
+                           clk_stream_t s);
+
+/* Empties the slots; pages that no slot holds any more are free again.  A bad
+ * slot latches CLK_EINVAL. */
+CLK_API int clk_cache_free(clk_cache* h, const int32_t* d_slots, int32_t B, clk_stream_t s);
+
+/* Moves the pages in use to the lowest numbers: with L pages in use, those
+ * numbered L and above move, in ascending order, to the free ones below L, in
+ * ascending order; their rows are copied in every plane (the rows that hold
+ * tokens), and tables and counts follow.  Afterwards pages 0 .. L-1 are in
+ * use, and the pool's end can be given back.  d_moved (nullable) receives the
+ * number of pages moved. */
+CLK_API int clk_cache_compact(clk_cache* h, const clk_pool* pool, int32_t* d_moved, clk_stream_t s);
+
+/* As clk_status and clk_status_clear, for the cache's status word. */
+CLK_API int clk_cache_status(clk_cache* h, int32_t* dev_status, int32_t* detail, clk_stream_t s);
+CLK_API int clk_cache_status_clear(clk_cache* h, clk_stream_t s);
+
+/* Frees the host handle (not the workspace). */
+CLK_API void clk_cache_destroy(clk_cache* h);
+
+/* ---------------------------------------------------------------------- */
+/* Trees of drafted tokens                                                 */
+/* ---------------------------------------------------------------------- */
+#define CLK_TREE_MAX 64 /* nodes of a tree */
+
+/* A request's tree has d_nodes[b] nodes (0 .. N, N <= CLK_TREE_MAX).  Node 0 is the
+ * last committed token; node n > 0 is a drafted token that follows node
+ * d_parent[b*N + n], which is below n.  A chain (the verify block of
+ * clk_fuse) has parents n - 1.  d_parent[b*N] is not read. */
+
+/* Ancestor masks: bit m of d_mask[b*N + n] is set where m is n or one of its
+ * ancestors; 0 for n >= d_nodes[b].  A node whose parent is not in 0 .. n-1
+ * starts a tree of its own (it sees itself and no node above it).  A node
+ * count outside 0 .. N gives masks of 0. */
+CLK_API int clk_tree_masks(int32_t B, int32_t N, const int32_t* d_parent, const int32_t* d_nodes, int64_t* d_mask,
+                           clk_stream_t s);
+
+/* Greedy verification of a tree, from the target's answers d_argmax [B,N]
+ * (clk_verify_greedy's, at every node).  Node 0 is accepted; node n is
+ * accepted where its parent is and its token d_tok[b*N + n] (>= 0) is the
+ * target's answer at the parent; of siblings that both match, the lowest.
+ * Outputs: d_path [B,N] the accepted nodes from node 0 on, then -1; d_accept
+ * [B] accepted drafts a; d_emitted [B] a + 1; d_out_tok [B,N] the target's
+ * answers at the path's nodes (a accepted drafts and the token after them),
+ * then CLK_SENT.  A node count of 0 or outside 0 .. N gives accept 0, emitted
+ * 0, and -1 / CLK_SENT. */
+CLK_API int clk_tree_accept(int32_t B, int32_t N, const int32_t* d_tok, const int32_t* d_parent,
+                            const int32_t* d_nodes, const int32_t* d_argmax, int32_t* d_accept, int32_t* d_path,
+                            int32_t* d_emitted, int32_t* d_out_tok, clk_stream_t s);
+
+/* ---------------------------------------------------------------------- */
+/* Attention over the cache                                                */
+/* ---------------------------------------------------------------------- */
+/* What both attentions read and write for the new tokens: q [.., q_heads,
+ * dim], k and v [.., kv_heads, dim], out [.., q_heads, dim] contiguous.  Query
+ * head h reads K/V head h / (q_heads / kv_heads).  Row r of request b lies at
+ * d_q + b*q_req + r*q_row + head*q_head + d (element strides >= 0; k and v
+ * alike).  dtype: CLK_DTYPE_BF16, CLK_DTYPE_F16 or CLK_DTYPE_F32; dim 1 ..
+ * 256.
+ *
+ *   out[r, h] = sum_j p_j v_j,  p = softmax over the visible j of
+ *   scale * <q[r, h], k_j>
+ *
+ * over the slot's first ctx cached rows and the visible new rows.  A row that
+ * sees nothing gives 0.  What is not visible does not count, whatever it holds
+ * (rows of a page past ctx, nodes off the mask, other requests): with one
+ * rule, a row that does see a new token with an infinity or a NaN in its v
+ * may be NaN in every element.  Scores, the softmax's maximum and sum and
+ * the accumulators are float32; each weight is rounded to the inputs' type
+ * for the product with v, and the sum of weights is of the unrounded ones. */
+typedef struct clk_attn {
+    int32_t dtype, q_heads, kv_heads, dim;
+    float scale; /* finite */
+    const void *d_q, *d_k, *d_v;
+    void* d_out;
+    int64_t q_req, q_row, q_head;
+    int64_t k_req, k_row, k_head;
+    int64_t v_req, v_row, v_head;
+} clk_attn;
+
+/* Scratch bytes for clk_tree_attend / clk_prompt_attend with these heads and
+ * this dim on the current device, for any batch.  16-byte aligned; no
+ * initialisation; calls that share it must not overlap on the GPU. */
+CLK_API int clk_attend_scratch_bytes(int32_t q_heads, int32_t kv_heads, int32_t dim, size_t* bytes);
+
+/* Attention of a step's block: request b has d_nodes[b] new tokens (0 .. N,
+ * N <= CLK_TREE_MAX), of which token n sees the slot's first ctx rows (plane
+ * 2*layer and 2*layer + 1 of the pool) and the new tokens m < d_nodes[b] whose
+ * bit m of d_mask[b*N + n] is set (clk_tree_masks, or any other mask).
+ * d_ctx [B] (nullable): ctx per request, 0 .. the slot's length; NULL: the
+ * slot's length.  Rows n >= d_nodes[b] of out are 0.  N = 1 is plain decoding
+ * by single tokens.  A bad slot, ctx or node count latches CLK_EINVAL in the
+ * cache's status, and the request's rows are 0. */
+CLK_API int clk_tree_attend(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool, int32_t layer,
+                            const clk_attn* a, int32_t N, const int32_t* d_nodes, const int64_t* d_mask,
+                            const int32_t* d_ctx, void* d_scratch, size_t scratch_bytes, clk_stream_t s);
+
+/* Causal attention of packed prompts: request b's new tokens are rows
+ * d_off[b] .. d_off[b+1] - 1 of q, k, v and out (T rows in all; the *_req
+ * strides are not used); its token t sees the slot's first ctx rows and its
+ * own new tokens 0 .. t.  d_ctx [B]: cached rows before the prompt (0 .. the
+ * slot's length); NULL: none.  h, d_slots and pool may be NULL where d_ctx is
+ * NULL.  Offsets that fall or leave 0 .. T, a bad slot or a bad ctx: the
+ * request's rows are not written, and CLK_EINVAL is latched where h is given.
+ * Rows of no request are not written. */
+CLK_API int clk_prompt_attend(const clk_attn* a, const int64_t* d_off, int32_t B, int64_t T, clk_cache* h,
+                              const int32_t* d_slots, const clk_pool* pool, int32_t layer, const int32_t* d_ctx,
+                              void* d_scratch, size_t scratch_bytes, clk_stream_t s);
 
 /* ---------------------------------------------------------------------- */
 /* Status, counters, inspection (these synchronise the stream)             */
