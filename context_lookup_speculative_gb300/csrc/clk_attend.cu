@@ -160,8 +160,11 @@ int launch_rows(const Attend& A, cudaStream_t s)
 
 int launch_attend(const Attend& A, void* scratch, size_t bytes, cudaStream_t s)
 {
-    (void)scratch;
-    (void)bytes;
+    if (attend_mma_takes(A)) {
+        if (scratch == nullptr || !aligned(scratch, 16) || bytes < attend_mma_scratch(A.q_heads, A.kv_heads, A.dim))
+            return CLK_EINVAL;
+        return attend_mma_launch(A, scratch, s);
+    }
     switch (A.dtype) {
     case CLK_DTYPE_BF16: return launch_rows<__nv_bfloat16>(A, s);
     case CLK_DTYPE_F16: return launch_rows<__half>(A, s);
@@ -235,7 +238,8 @@ extern "C" int clk_attend_scratch_bytes(int32_t q_heads, int32_t kv_heads, int32
 {
     if (bytes == nullptr || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || dim < 1 || dim > kMaxDim)
         return CLK_EINVAL;
-    *bytes = 16;
+    const size_t n = attend_mma_scratch(q_heads, kv_heads, dim);
+    *bytes = n > 0 ? n : 16;
     return CLK_OK;
 }
 

@@ -1,0 +1,1084 @@
+// Attention of new tokens over a paged cache on the tensor cores (sm_103a).
+//
+// Rows.  The query heads that share a K/V head are packed with the tokens
+// into the rows of one product: row r of a tile is token r / group, head
+// r % group of the group, so K and V are read once for all of them and a
+// step's 16 nodes times a group of 8 fill the 128 rows.
+//
+// Work.  An item is one (request, K/V head, row tile); its work is a list of
+// 128-key tiles, those of the cached rows first, then those of the new
+// tokens.  All items' tiles in order form one line, which the CTAs (one per
+// SM) cut into equal shares: ragged contexts, causal rows of every length
+// and a single long request all balance, whatever the batch.  An item that
+// a cut falls into is left as partial results (float32 sums and the
+// softmax's reference and sum per row) that a second kernel joins in a fixed
+// order.
+//
+// A CTA.  One warp copies tiles into two rings in shared memory (pages and
+// packed rows are boxes of tensor maps, 128-byte swizzle); one thread issues
+// the products; two groups of four warps do the softmax, a thread per row;
+// two warps look after V tiles.  The two groups work on two accumulator
+// streams so that the tensor cores run on one while the other is
+// exponentiated: for trees the streams take alternate key tiles of one row
+// tile, for prompts two row tiles share every key tile.  Scores
+// S = Q K^T arrive in tensor memory in float32; a thread reads its row,
+// keeps the running maximum and sum, and writes the weights P back over S in
+// 16 bits, from where the second product O += P V takes them.  O is rescaled
+// only when a row's maximum has grown by more than a factor of 2^8 over the
+// reference in use: between that, weights are up to 2^8 (which costs no
+// precision in floating point).  float16 weights carry another factor of
+// 2^7, so that small ones keep their bits (2^15 stays below the type's
+// largest).
+//
+// What is not visible.  Scores of hidden keys are replaced by -inf, so K may
+// hold anything there; but 0 * V is not 0 for an infinity or a NaN.  So the V
+// warps clear the rows past a tile's end (the rest of a page, the next
+// request's tokens), and in tiles of new tokens whose keys not all rows see,
+// they clear rows that are not finite and note them: a row that sees such a
+// key gets NaN for its sum.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "clk.h"
+#include "clk_attend.h"
+#include "clk_cache.h"
+#include "clk_host.h"
+#include "clk_mma.cuh"
+
+namespace clk {
+namespace {
+
+constexpr int kTile = 128;     // keys of a tile, rows of a row tile
+constexpr int kWarps = 12;     // 8 softmax, 1 copies, 1 products, 2 V tiles
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kValueWarp = 10;
+constexpr int kNear = 16;      // requests whose data a CTA keeps
+constexpr int kJoinThreads = 256;
+
+struct Maps {
+    CUtensorMap q, k, v, kc, vc;
+};
+
+// How a call's rows are tiled.
+struct Shape {
+    int32_t tok;    // tokens of a row tile: 128 / group
+    int32_t block;  // tokens of an item: tok, or 2 tok for prompts
+    int32_t qbox, kbox;  // tokens of a box of q, rows of a box of new keys
+    int32_t ctas;
+    float log2_scale;  // scale * log2(e)
+};
+
+// Scratch: join records, row statistics and partial sums, two parts a CTA.
+struct Join {
+    int32_t b, h, rt;   // the item that a CTA's share begins in the middle of; b < 0: none
+    int32_t c0, c1;     // its first and last CTA
+    int32_t first;      // part of c0 that holds its beginning
+};
+
+struct Scratch {
+    Join* join;   // [ctas]
+    float2* ml;   // [ctas][2][rows]
+    float* sums;  // [ctas][2][DP / 4][rows][4]
+};
+
+constexpr size_t kJoinBytes = 32;
+static_assert(sizeof(Join) <= kJoinBytes, "join record");
+
+__host__ __device__ inline int pad_dim(int dim) { return dim <= 64 ? 64 : 128; }
+
+__host__ __device__ inline Scratch scratch_of(void* base, int ctas, int rows)
+{
+    Scratch s;
+    char* p = static_cast<char*>(base);
+    s.join = reinterpret_cast<Join*>(p);
+    p += (size_t)ctas * kJoinBytes;
+    s.ml = reinterpret_cast<float2*>(p);
+    p += (size_t)ctas * 2 * rows * sizeof(float2);
+    s.sums = reinterpret_cast<float*>(p);
+    return s;
+}
+
+// sum over i < n of floor((a i + b) / m), for n >= 0, m > 0, a, b >= 0 (a
+// step of Euclid's algorithm at a time).
+__device__ long long floor_sum(long long n, long long m, long long a, long long b)
+{
+    long long s = 0;
+    while (n > 0) {
+        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const long long y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+    return s;
+}
+
+// A request's tiles: per K/V head, `items` row tiles; item i has ctx_tiles
+// tiles of cached keys and new_tiles(i) of new ones.
+struct Reach {
+    int32_t ctx, rows, slot;
+    int32_t ctx_tiles, items;
+    int64_t base;
+};
+
+template <bool PROMPT>
+__device__ __forceinline__ Reach reach_of(const Request& r, const Shape& S)
+{
+    Reach x;
+    x.ctx = r.ctx;
+    x.rows = r.rows;
+    x.slot = r.slot;
+    x.base = r.base;
+    x.ctx_tiles = (r.ctx + kTile - 1) / kTile;
+    x.items = (r.rows + S.block - 1) / S.block;
+    return x;
+}
+
+template <bool PROMPT>
+__device__ __forceinline__ int new_tiles(const Reach& x, const Shape& S, int item)
+{
+    if (!PROMPT) return 1;  // at most 64 new tokens
+    const int end = (item + 1) * S.block < x.rows ? (item + 1) * S.block : x.rows;
+    return (end - 1) / kTile + 1;
+}
+
+// Tiles of the items before `item` of one K/V head.
+template <bool PROMPT>
+__device__ __forceinline__ long long tiles_before(const Reach& x, const Shape& S, int item)
+{
+    if (!PROMPT) return (long long)item * (x.ctx_tiles + 1);
+    if (item <= 0) return 0;
+    const bool all = item >= x.items;
+    const int whole = all ? x.items - 1 : item;
+    long long n = (long long)item * x.ctx_tiles + whole + floor_sum(whole, kTile, S.block, S.block - 1);
+    if (all) n += (x.rows - 1) / kTile + 1;
+    return n;
+}
+
+template <bool PROMPT>
+__device__ __forceinline__ long long tiles_of(const Reach& x, const Shape& S)
+{
+    return x.items == 0 ? 0 : tiles_before<PROMPT>(x, S, x.items);
+}
+
+// First tile of CTA c's share of `all` tiles.
+__device__ __forceinline__ long long share(long long all, int c, int ctas) { return all * c / ctas; }
+// The CTA whose share holds tile g.
+__device__ __forceinline__ int cta_of(long long all, long long g, int ctas) { return (int)(((g + 1) * ctas - 1) / all); }
+
+// What a CTA knows after planning (in shared memory).
+struct Plan {
+    long long all, g0, g1;  // tiles in all, this CTA's share
+    int ctas;               // CTAs that have work
+    int b, h, item, t;      // where the share begins
+};
+
+// The CTA's way through its share, the same in every warp.
+template <bool PROMPT>
+struct Walk {
+    const Attend& A;
+    const Shape& S;
+    const Plan& P;
+    const Reach* near;
+    Reach x;
+    int b, h, item, t0, t1, total;
+    long long left;
+
+    __device__ Walk(const Attend& a, const Shape& s, const Plan& p, const Reach* n) : A(a), S(s), P(p), near(n)
+    {
+        left = p.g1 - p.g0;
+        b = p.b;
+        h = p.h;
+        item = p.item;
+        if (left > 0) {
+            load();
+            cut(p.t);
+        }
+    }
+    __device__ void load()
+    {
+        const int i = b - P.b;
+        x = i < kNear ? near[i] : reach_of<PROMPT>(attend_request(A, b, false), S);
+    }
+    __device__ void cut(int from)
+    {
+        total = x.ctx_tiles + new_tiles<PROMPT>(x, S, item);
+        t0 = from;
+        t1 = total - from < left ? total : from + (int)left;
+    }
+    __device__ bool more() const { return left > 0; }
+    __device__ void next()
+    {
+        left -= t1 - t0;
+        if (left <= 0) return;
+        if (++item == x.items) {
+            item = 0;
+            if (++h == A.kv_heads) {
+                h = 0;
+                do {
+                    ++b;
+                    load();
+                } while (x.items == 0);
+            }
+        }
+        cut(0);
+    }
+    // Tiles [t0, last(s)) of this segment are stream s's, with prompts.
+    __device__ int last(int s) const
+    {
+        const int first = item * S.block + s * S.tok;
+        if (first >= x.rows) return t0;
+        const int end = first + S.tok < x.rows ? first + S.tok : x.rows;
+        const int n = x.ctx_tiles + (end - 1) / kTile + 1;
+        return n < t0 ? t0 : n < t1 ? n : t1;
+    }
+};
+
+template <int DP, bool PROMPT>
+struct Lay {
+    static constexpr int kHalves = DP / 64;
+    static constexpr int kHalf = kTile * 128;  // bytes of 64 columns of a tile
+    static constexpr int kBytes = kHalves * kHalf;
+    static constexpr int kQ = PROMPT ? 2 : 1;
+    static constexpr int kK = DP == 128 ? 3 : 6;                   // K tiles in the ring
+    static constexpr int kV = DP == 128 ? (PROMPT ? 2 : 3) : (PROMPT ? 5 : 6);
+    static constexpr int kTiles = kQ + kK + kV;
+    // after the tiles
+    static constexpr int oKFull = kTiles * kBytes, oKEmpty = oKFull + 8 * kK;
+    static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
+    static constexpr int oQFull = oVEmpty + 8 * kV, oQEmpty = oQFull + 8;
+    static constexpr int oSFull = oQEmpty + 8, oPReady = oSFull + 16, oODone = oPReady + 16;
+    static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
+    static constexpr int oBars = oDrain + 8;  // end of the barriers
+    static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
+    static constexpr int oNear = oBad + 16 * kV;                      // Reach[kNear]
+    static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
+    static constexpr int oStop = oPlan + (int)sizeof(Plan), oTmem = oStop + 4;
+    static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;          // float2[2][128] for trees
+    static constexpr int kTotal = oStat + (PROMPT ? 0 : 2 * kTile * 8);
+    static_assert(kTotal <= 232448, "shared memory");
+};
+
+template <int DP, bool BF16, bool PROMPT>
+__global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ Maps M, const __grid_constant__ Attend A,
+                                                        const __grid_constant__ Shape S, void* scratch)
+{
+    using L = Lay<DP, PROMPT>;
+    extern __shared__ __align__(1024) char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_addr(sm);
+    Plan& plan = *reinterpret_cast<Plan*>(sm + L::oPlan);
+    Reach* const near = reinterpret_cast<Reach*>(sm + L::oNear);
+    volatile int* const stop = reinterpret_cast<volatile int*>(sm + L::oStop);
+    volatile uint32_t* const bad = reinterpret_cast<volatile uint32_t*>(sm + L::oBad);
+    const Scratch W = scratch_of(scratch, S.ctas, PROMPT ? 2 * kTile : kTile);
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this one's end
+
+    // ---- Plan: all requests' tiles, this CTA's share, where it begins. ----
+    {
+        long long* const sums = reinterpret_cast<long long*>(sm);  // the rings are not in use yet
+        long long before = 0, all = 0, mine = 0;
+        for (int pass = 0; pass < 2; ++pass) {
+            // a batch of up to kThreads requests needs one pass
+            if (pass == 1 && A.B <= kThreads) break;
+            before = 0;
+            for (int at = 0; at < A.B; at += kThreads) {
+                const int b = at + tid;
+                long long u = 0;
+                if (b < A.B)
+                    u = tiles_of<PROMPT>(reach_of<PROMPT>(attend_request(A, b, pass == 0 && blockIdx.x == 0), S), S) * A.kv_heads;
+                long long x = u;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+                    if (lane >= d) x += y;
+                }
+                if (lane == 31) sums[warp] = x;
+                __syncthreads();
+                long long lower = before;
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) lower += sums[w];
+                    before += sums[w];
+                }
+                mine = lower + x - u;
+                if (pass == 1 && u > 0 && mine <= plan.g0 && plan.g0 < mine + u) {
+                    plan.b = b;
+                    plan.all = mine;  // for now: tiles before this request
+                }
+                if (A.B <= kThreads && u > 0) {
+                    all = before;
+                    const int ctas = all < S.ctas ? (int)all : S.ctas;
+                    const long long g0 = (int)blockIdx.x < ctas ? share(all, blockIdx.x, ctas) : all;
+                    if (mine <= g0 && g0 < mine + u) {
+                        plan.b = b;
+                        plan.all = mine;
+                    }
+                }
+                __syncthreads();
+            }
+            if (pass == 0) {
+                all = before;
+                if (tid == 0) {
+                    const int ctas = all < S.ctas ? (int)all : S.ctas;
+                    plan.ctas = ctas;
+                    plan.g0 = (int)blockIdx.x < ctas ? share(all, blockIdx.x, ctas) : all;
+                    plan.g1 = (int)blockIdx.x < ctas ? share(all, blockIdx.x + 1, ctas) : all;
+                }
+                __syncthreads();
+            }
+        }
+        const long long start = plan.all;
+        __syncthreads();
+        if (plan.g0 < plan.g1) {
+            if (tid < kNear) {
+                const int b = plan.b + tid;
+                if (b < A.B) near[tid] = reach_of<PROMPT>(attend_request(A, b, false), S);
+            }
+            __syncthreads();
+            if (warp == 0) {
+                const Reach x = near[0];
+                const long long off = plan.g0 - start, per = tiles_of<PROMPT>(x, S);
+                const int h = (int)(off / per);
+                const long long o = off - h * per;
+                // the last item with tiles_before <= o, 32 ways at a time
+                int lo = 0, span = x.items;
+                while (span > 1) {
+                    const int step = (span + 31) / 32;
+                    const int i = lo + lane * step;
+                    const bool le = lane * step < span && tiles_before<PROMPT>(x, S, i) <= o;
+                    const int n = __popc(__ballot_sync(0xffffffffu, le));
+                    const int end = lo + span;
+                    lo += (n - 1) * step;
+                    span = lo + step < end ? step : end - lo;
+                }
+                if (lane == 0) {
+                    plan.h = h;
+                    plan.item = lo;
+                    plan.t = (int)(o - tiles_before<PROMPT>(x, S, lo));
+                }
+            }
+        }
+        if (tid == 0) {
+            plan.all = all;
+            *stop = 0;
+        }
+        __syncthreads();
+    }
+
+    // ---- Barriers and tensor memory. ----
+    if (tid == 0) {
+        for (int i = 0; i < L::kK; ++i) {
+            bar_init(base + L::oKFull + 8 * i, 1);
+            bar_init(base + L::oKEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < L::kV; ++i) {
+            bar_init(base + L::oVFull + 8 * i, 1);
+            bar_init(base + L::oVReady + 8 * i, 2);
+            bar_init(base + L::oVEmpty + 8 * i, 1);
+        }
+        bar_init(base + L::oQFull, 1);
+        bar_init(base + L::oQEmpty, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(base + L::oSFull + 8 * i, 1);
+            bar_init(base + L::oPReady + 8 * i, 4);
+            bar_init(base + L::oODone + 8 * i, 1);
+        }
+        bar_init(base + L::oStatReady, 8);
+        bar_init(base + L::oDrain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the planning scratch lies where tiles go
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::oTmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tmem_before();
+    __syncthreads();
+    tmem_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::oTmem);
+    const uint32_t qs = base, ks = base + L::kQ * L::kBytes, vs = ks + L::kK * L::kBytes;
+    Walk<PROMPT> w(A, S, plan, near);
+
+    // Registers: 384 threads x 168 at launch; 256 x 208 + 128 x 80 after the split.
+    if (warp < kCopyWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ---- Softmax: a thread per row. ----
+        const int s = warp >> 2, row = tid & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t tS = lanes + 128 * s, tO = lanes + 256 + s * DP;
+        const int tk = row / A.group, g = row - tk * A.group;  // token of the row tile, head of the group
+        const float cs = S.log2_scale;
+        constexpr float lift = BF16 ? 0.0f : 7.0f;
+        const float slack = 8.0f / cs;
+        uint32_t sp = 0, od = 0;
+        int gi = 0;
+        bool ok = true;
+        for (; ok && w.more(); w.next()) {
+            const int len = w.t1 - w.t0;
+            const int mine = PROMPT ? w.last(s) - w.t0 : (len + 1 - s) / 2;
+            const int token = w.item * S.block + (PROMPT ? s * S.tok : 0) + tk;
+            const bool real = tk < S.tok && token < w.x.rows;
+            unsigned long long seen = 0;
+            if (!PROMPT && real && w.t1 > w.x.ctx_tiles) {
+                seen = (unsigned long long)A.mask[(int64_t)w.b * A.N + token];
+                if (w.x.rows < 64) seen &= (1ull << w.x.rows) - 1;
+            }
+            float ref = -INFINITY, sum = 0.0f;
+            for (int j = 0; j < mine; ++j) {
+                const int jj = PROMPT ? j : 2 * j + s;
+                const int t = w.t0 + jj;
+                if (!(ok = warp_wait(base + L::oSFull + 8 * s, sp, stop))) break;
+                sp ^= 1;
+                tmem_after();
+                uint32_t x[kTile];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_load(tS + 32 * c, x + 32 * c);
+                tmem_load_wait();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_loaded(x + 32 * c);
+                // Hidden keys: a limit for most tiles, a mask for a tree's.
+                const bool cached = t < w.x.ctx_tiles;
+                const int n0 = (t - w.x.ctx_tiles) * kTile;
+                const int first = w.item * S.block + (PROMPT ? s * S.tok : 0);
+                if (cached || PROMPT) {
+                    const int most = cached ? w.x.ctx - t * kTile : n0 + kTile - 1 > first ? token - n0 + 1 : kTile;
+                    if (!cached ? n0 + kTile - 1 > first : most < kTile) {
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c)
+                            if (c >= most) x[c] = 0xff800000u;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (!(seen >> c & 1)) x[c] = 0xff800000u;
+#pragma unroll
+                    for (int c = 64; c < kTile; ++c) x[c] = 0xff800000u;
+                }
+                float top = -INFINITY;
+                {
+                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(x[c]));
+                    top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                }
+                const bool grow = top > ref + slack || (ref == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? top : ref;
+                    const float fix = grow ? exp2_fast((ref - to) * cs) : 1.0f;
+                    ref = to;
+                    sum *= fix;
+                    if (j > 0) {
+                        // The scores' product was issued after this stream's last P V, so O is complete.
+#pragma unroll
+                        for (int c = 0; c < DP / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_load(tO + 32 * c, o);
+                            tmem_load_wait();
+                            tmem_loaded(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                            tmem_store(tO + 32 * c, o);
+                        }
+                    }
+                }
+                const float shift = ref == -INFINITY ? 0.0f : lift - ref * cs;
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < kTile; ++c) {
+                    const float p = exp2_fast(fmaf(__uint_as_float(x[c]), cs, shift));
+                    part[c & 3] += p;
+                    x[c] = __float_as_uint(p);
+                }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t y[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        y[e] = pack2<BF16>(__uint_as_float(x[64 * c + 2 * e]), __uint_as_float(x[64 * c + 2 * e + 1]));
+                    tmem_store(tS + 32 * c, y);
+                }
+                if (!cached && (!PROMPT || n0 + kTile - 1 > w.item * S.block)) {
+                    // Rows of V that were not finite: NaN for those who see them.
+                    const int vi = (gi + jj) % L::kV;
+                    if (!(ok = warp_wait(base + L::oVReady + 8 * vi, (uint32_t)((gi + jj) / L::kV & 1), stop))) break;
+                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], bad[4 * vi + 2], bad[4 * vi + 3]};
+                    if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
+                        bool hit = false;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t vis;
+                            if (PROMPT) {
+                                const int upto = token - n0 + 1 - 32 * u;
+                                vis = upto >= 32 ? 0xffffffffu : upto > 0 ? (1u << upto) - 1u : 0u;
+                            } else {
+                                vis = u < 2 ? (uint32_t)(seen >> (32 * u)) : 0u;
+                            }
+                            hit |= (odd[u] & vis) != 0;
+                        }
+                        if (hit) sum = NAN;
+                    }
+                }
+                tmem_store_wait();
+                tmem_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(base + L::oPReady + 8 * s);
+            }
+            if (!ok) break;
+            if (mine > 0) {
+                if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
+                od ^= 1;
+                tmem_after();
+            }
+            // ---- The segment's result: to the output, or as a part. ----
+            const bool whole = w.t0 == 0 && w.t1 == w.total;
+            const int slot = 2 * (int)blockIdx.x + (w.left == plan.g1 - plan.g0 ? 0 : 1);
+            constexpr int rows = PROMPT ? 2 * kTile : kTile;
+            const int64_t out_row = (PROMPT ? w.x.base : (int64_t)w.b * A.N) + token;
+            char* const out = static_cast<char*>(A.out) + ((out_row * A.q_heads + w.h * A.group + g) * A.dim) * 2;
+            float w0 = 1.0f, w1 = 0.0f, m = ref, l = sum;
+            if (!PROMPT) {
+                // both streams' statistics, to weigh their sums
+                float2* const stat = reinterpret_cast<float2*>(sm + L::oStat);
+                stat[s * kTile + row] = make_float2(ref, sum);
+                tmem_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(base + L::oStatReady);
+                if (!(ok = warp_wait(base + L::oStatReady, 0, stop))) break;
+                tmem_after();
+                const float2 a = stat[row], c = stat[kTile + row];
+                m = fmaxf(a.x, c.x);
+                w0 = a.x == -INFINITY ? 0.0f : exp2_fast((a.x - m) * cs);
+                w1 = c.x == -INFINITY ? 0.0f : exp2_fast((c.x - m) * cs);
+                l = a.y * w0 + c.y * w1;
+                // a stream without a visible key has no sum of products (or one of zeros)
+            }
+            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            const int c0 = PROMPT ? 0 : s * (DP / 64), c1 = PROMPT ? DP / 32 : (s + 1) * (DP / 64);
+            const uint32_t tA = PROMPT ? tO : lanes + 256, tB = lanes + 256 + DP;
+            for (int c = c0; c < c1; ++c) {
+                uint32_t o[32] = {}, o1[32] = {};
+                if (PROMPT ? mine > 0 : true) tmem_load(tA + 32 * c, o);
+                if (!PROMPT && len > 1) tmem_load(tB + 32 * c, o1);
+                tmem_load_wait();
+                tmem_loaded(o);
+                tmem_loaded(o1);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float v = 0.0f;
+                    if (PROMPT) {
+                        if (mine > 0 && l != 0.0f) v = __uint_as_float(o[e]);
+                    } else {
+                        if (w0 != 0.0f) v = __uint_as_float(o[e]) * w0;
+                        if (len > 1 && w1 != 0.0f) v = fmaf(__uint_as_float(o1[e]), w1, v);
+                        if (l != l) v = l;
+                    }
+                    o[e] = __float_as_uint(v * inv);
+                }
+                if (real) {
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            if (32 * c + e < A.dim) {
+                                uint4 y;
+                                y.x = pack2<BF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+                                y.y = pack2<BF16>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                                y.z = pack2<BF16>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+                                y.w = pack2<BF16>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+                                *reinterpret_cast<uint4*>(out + (32 * c + e) * 2) = y;
+                            }
+                        }
+                    } else {
+                        float4* const to = reinterpret_cast<float4*>(W.sums) + (int64_t)slot * (DP / 4) * rows +
+                                           (PROMPT ? s * kTile : 0) + row;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            to[(int64_t)(8 * c + e / 4) * rows] =
+                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                            __uint_as_float(o[e + 3]));
+                    }
+                }
+            }
+            if (!whole && real && (PROMPT || s == 0))
+                W.ml[(int64_t)slot * rows + (PROMPT ? s * kTile : 0) + row] = make_float2(m * cs, l);
+            // Neither stream's next sums may overwrite what the other still reads.
+            tmem_before();
+            if (!PROMPT) {
+                __syncwarp();
+                if (lane == 0) bar_arrive(base + L::oStatReady);
+                if (!(ok = warp_wait(base + L::oStatReady, 1, stop))) break;
+            }
+            gi += len;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == kCopyWarp) {
+            // ---- Copies. ----
+            int i = 0, seg = 0, nk = 0, nv = 0, nq = 0;  // n*: tiles asked for
+            bool ok = (base & 1023) == 0;  // the swizzle's period
+            if (!ok) *stop = 1;
+            const int pages = kTile >> A.C.shift;  // of a tile
+            for (; ok && w.more(); w.next(), ++seg) {
+                const int32_t* const table = w.x.slot >= 0 ? A.C.table + (int64_t)w.x.slot * A.C.max_pages : nullptr;
+                auto page_of = [&](int t) {
+                    const int64_t p = (int64_t)t * pages + lane;
+                    if (t >= w.x.ctx_tiles || t >= w.t1 || lane >= pages || (p << A.C.shift) >= w.x.ctx) return -1;
+                    int32_t page = table[p];
+                    if (page < 0 || page >= A.C.num_pages) {
+                        latch(A.C.status, CLK_EINVAL, w.x.slot);
+                        page = A.C.num_pages;  // reads as zeros
+                    }
+                    return page;
+                };
+                int page = page_of(w.t0);
+                if (!(ok = warp_wait(base + L::oQEmpty, (seg & 1) ^ 1, stop))) break;
+                ++nq;
+                const int tok = w.item * S.block;
+                const int z = PROMPT ? 0 : w.b;
+                const int row0 = PROMPT ? (int)w.x.base : 0;
+                if (lane == 0) {
+                    bar_expect(base + L::oQFull, (uint32_t)(L::kQ * L::kHalves) * (uint32_t)(S.qbox * A.group) * 128u);
+                    for (int s = 0; s < L::kQ; ++s)
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+                            copy_box(qs + s * L::kBytes + hf * L::kHalf, &M.q, 64 * hf, w.h * A.group, row0 + tok + s * S.tok, z,
+                                     base + L::oQFull);
+                }
+                for (int t = w.t0; t < w.t1; ++t, ++i) {
+                    const int next = page_of(t + 1);
+                    const int ki = i % L::kK, vi = i % L::kV;
+                    const uint32_t kd = ks + ki * L::kBytes, vd = vs + vi * L::kBytes;
+                    const uint32_t kb = base + L::oKFull + 8 * ki, vb = base + L::oVFull + 8 * vi;
+                    const bool cached = t < w.x.ctx_tiles;
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                    const uint32_t bytes = (uint32_t)L::kHalves * 128u * (uint32_t)(cached ? boxes << A.C.shift : S.kbox);
+                    const int n0 = row0 + (t - w.x.ctx_tiles) * kTile;
+                    if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
+                    ++nk;
+                    if (lane == 0) bar_expect(kb, bytes);
+                    __syncwarp();
+                    if (cached) {
+                        if (page >= 0)
+                            for (int hf = 0; hf < L::kHalves; ++hf)
+                                copy_box(kd + hf * L::kHalf + (lane << A.C.shift) * 128, &M.kc, 64 * hf, 0, w.h, page, kb);
+                    } else if (lane < L::kHalves) {
+                        copy_box(kd + lane * L::kHalf, &M.k, 64 * lane, w.h, n0, z, kb);
+                    }
+                    if (!(ok = warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(i / L::kV & 1) ^ 1, stop))) break;
+                    ++nv;
+                    if (lane == 0) bar_expect(vb, bytes);
+                    __syncwarp();
+                    if (cached) {
+                        if (page >= 0)
+                            for (int hf = 0; hf < L::kHalves; ++hf)
+                                copy_box(vd + hf * L::kHalf + (lane << A.C.shift) * 128, &M.vc, 64 * hf, 0, w.h, page, vb);
+                    } else if (lane < L::kHalves) {
+                        copy_box(vd + lane * L::kHalf, &M.v, 64 * lane, w.h, n0, z, vb);
+                    }
+                    page = next;
+                }
+                if (!ok) break;
+            }
+            if (!ok) {
+                // Leave no copy in flight.
+                const long long t0 = clock64();
+                auto drain = [&](uint32_t bar, uint32_t parity) {
+                    while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {}
+                };
+                if (nq > 0) drain(base + L::oQFull, (uint32_t)(nq - 1) & 1);
+                for (int j = nk > L::kK ? nk - L::kK : 0; j < nk; ++j) drain(base + L::oKFull + 8 * (j % L::kK), (uint32_t)(j / L::kK & 1));
+                for (int j = nv > L::kV ? nv - L::kV : 0; j < nv; ++j) drain(base + L::oVFull + 8 * (j % L::kV), (uint32_t)(j / L::kV & 1));
+            }
+        } else if (warp == kMmaWarp) {
+            // ---- Products: one thread. ----
+            if (lane == 0) {
+                constexpr uint32_t types = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((kTile >> 4) << 24);
+                constexpr uint32_t kind_s = types | ((kTile >> 3) << 17);
+                constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
+                uint32_t ps[2] = {0, 0};  // phases of PReady
+                int gi = 0, seg = 0;
+                bool ok = true;
+                auto scores = [&](int s, int tile) {
+                    const int ki = tile % L::kK;
+                    const uint32_t q = qs + (PROMPT ? s * L::kBytes : 0), k = ks + ki * L::kBytes;
+    #pragma unroll
+                    for (int e = 0; e < DP / 16; ++e) {
+                        const uint32_t at = (e / 4) * L::kHalf + (e % 4) * 32;
+                        mma_ss(tmem + 128 * s, operand(q + at, 16), operand(k + at, 16), kind_s, e > 0);
+                    }
+                    mma_commit(base + L::oSFull + 8 * s);
+                };
+                auto values = [&](int s, int tile, bool add) {
+                    const uint32_t v = vs + (tile % L::kV) * L::kBytes;
+    #pragma unroll
+                    for (int e = 0; e < kTile / 16; ++e)
+                        mma_ts(tmem + 256 + s * DP, tmem + 128 * s + 8 * e, operand(v + e * 2048, L::kHalf), kind_o, add || e > 0);
+                };
+                auto wait_k = [&](int tile) {
+                    return bar_wait(base + L::oKFull + 8 * (tile % L::kK), (uint32_t)(tile / L::kK & 1), stop);
+                };
+                for (; ok && w.more(); w.next(), ++seg) {
+                    const int len = w.t1 - w.t0;
+                    if (!(ok = bar_wait(base + L::oQFull, seg & 1, stop))) break;
+                    tmem_after();
+                    if (PROMPT) {
+                        const int n[2] = {w.last(0) - w.t0, w.last(1) - w.t0};
+                        if (!(ok = wait_k(gi))) break;
+                        tmem_after();
+                        for (int s = 0; s < 2; ++s)
+                            if (n[s] > 0) scores(s, gi);
+                        mma_commit(base + L::oKEmpty + 8 * (gi % L::kK));
+                        if (len == 1) mma_commit(base + L::oQEmpty);
+                        for (int j = 0; ok && j < len; ++j) {
+                            for (int s = 0; ok && s < 2; ++s) {
+                                if (j >= n[s]) continue;
+                                ok = bar_wait(base + L::oVReady + 8 * ((gi + j) % L::kV), (uint32_t)((gi + j) / L::kV & 1), stop) &&
+                                     bar_wait(base + L::oPReady + 8 * s, ps[s], stop);
+                                if (!ok) break;
+                                ps[s] ^= 1;
+                                tmem_after();
+                                values(s, gi + j, j > 0);
+                                if (j + 1 == n[s]) mma_commit(base + L::oODone + 8 * s);
+                                if (j + 1 < n[s]) {
+                                    if (!(ok = wait_k(gi + j + 1))) break;
+                                    tmem_after();
+                                    scores(s, gi + j + 1);
+                                }
+                            }
+                            if (!ok) break;
+                            mma_commit(base + L::oVEmpty + 8 * ((gi + j) % L::kV));
+                            if (j + 1 < len) mma_commit(base + L::oKEmpty + 8 * ((gi + j + 1) % L::kK));
+                            if (j + 2 == len) mma_commit(base + L::oQEmpty);
+                        }
+                    } else {
+                        for (int j = 0; ok && j < 2 && j < len; ++j) {
+                            if (!(ok = wait_k(gi + j))) break;
+                            tmem_after();
+                            scores(j, gi + j);
+                            mma_commit(base + L::oKEmpty + 8 * ((gi + j) % L::kK));
+                        }
+                        if (ok && len <= 2) mma_commit(base + L::oQEmpty);
+                        for (int j = 0; ok && j < len; ++j) {
+                            const int s = j & 1;
+                            ok = bar_wait(base + L::oVReady + 8 * ((gi + j) % L::kV), (uint32_t)((gi + j) / L::kV & 1), stop) &&
+                                 bar_wait(base + L::oPReady + 8 * s, ps[s], stop);
+                            if (!ok) break;
+                            ps[s] ^= 1;
+                            tmem_after();
+                            values(s, gi + j, j >= 2);
+                            mma_commit(base + L::oVEmpty + 8 * ((gi + j) % L::kV));
+                            if (j + 2 >= len) mma_commit(base + L::oODone + 8 * s);
+                            if (j + 2 < len) {
+                                if (!(ok = wait_k(gi + j + 2))) break;
+                                tmem_after();
+                                scores(s, gi + j + 2);
+                                mma_commit(base + L::oKEmpty + 8 * ((gi + j + 2) % L::kK));
+                                if (j + 3 == len) mma_commit(base + L::oQEmpty);
+                            }
+                        }
+                    }
+                    gi += len;
+                }
+                if (!ok) {
+                    // Products in flight end before tensor memory is given up.
+                    mma_commit(base + L::oDrain);
+                    const long long t0 = clock64();
+                    while (!bar_try(base + L::oDrain, 0) && clock64() - t0 < kWaitClocks) {}
+                }
+            }
+            __syncwarp();
+        } else if (warp >= kValueWarp) {
+            // ---- V tiles: rows past the end, and rows that are not finite. ----
+            constexpr uint32_t top = BF16 ? 0x7f807f80u : 0x7c007c00u;
+            const int half = warp - kValueWarp;
+            int i = 0;
+            bool ok = true;
+            for (; ok && w.more(); w.next()) {
+                for (int t = w.t0; t < w.t1; ++t, ++i) {
+                    const int vi = i % L::kV;
+                    if (!(ok = warp_wait(base + L::oVFull + 8 * vi, (uint32_t)(i / L::kV & 1), stop))) break;
+                    const bool cached = t < w.x.ctx_tiles;
+                    const int n0 = (t - w.x.ctx_tiles) * kTile;
+                    const int have = cached ? w.x.ctx - t * kTile : w.x.rows - n0;
+                    const bool look = !cached && (!PROMPT || n0 + kTile - 1 > w.item * S.block);
+                    if (have < kTile || look) {
+                        char* const tile = sm + (vs - base) + vi * L::kBytes;
+    #pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int r = 64 * half + 32 * u + lane;
+                            bool clear = r >= have, odd = false;
+                            if (look && !clear) {
+                                uint32_t hit = 0;
+    #pragma unroll
+                                for (int c = 0; c < 8 * L::kHalves; ++c) {
+                                    // lanes start at different chunks of their rows: no two in one bank
+                                    const int at = (c & 8) * (L::kHalf / 8) + r * 128 + (((c & 7) + lane) & 7) * 16;
+                                    const uint4 x = *reinterpret_cast<const uint4*>(tile + at);
+                                    hit |= __vcmpeq2(x.x & top, top) | __vcmpeq2(x.y & top, top) | __vcmpeq2(x.z & top, top) |
+                                           __vcmpeq2(x.w & top, top);
+                                }
+                                odd = hit != 0;
+                            }
+                            if (clear || odd)
+    #pragma unroll
+                                for (int c = 0; c < 8 * L::kHalves; ++c) {
+                                    const int at = (c & 8) * (L::kHalf / 8) + r * 128 + (((c & 7) + lane) & 7) * 16;
+                                    *reinterpret_cast<uint4*>(tile + at) = make_uint4(0, 0, 0, 0);
+                                }
+                            const uint32_t word = __ballot_sync(0xffffffffu, odd);
+                            if (lane == 0) bad[4 * vi + 2 * half + u] = word;
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(base + L::oVReady + 8 * vi);
+                }
+            }
+        }
+    }
+
+    // ---- The join record, and the end. ----
+    __syncthreads();
+    if (tid == 0) {
+        Join j{-1, 0, 0, 0, 0, 0};
+        if (plan.g0 < plan.g1 && plan.t > 0) {
+            const Reach x = near[0];
+            const long long begin = plan.g0 - plan.t;
+            const long long end = begin + x.ctx_tiles + new_tiles<PROMPT>(x, S, plan.item);
+            j.b = plan.b;
+            j.h = plan.h;
+            j.rt = plan.item;
+            j.c0 = cta_of(plan.all, begin, plan.ctas);
+            j.c1 = cta_of(plan.all, end - 1, plan.ctas);
+            j.first = share(plan.all, j.c0, plan.ctas) == begin ? 0 : 1;
+        }
+        *reinterpret_cast<Join*>(reinterpret_cast<char*>(scratch) + blockIdx.x * kJoinBytes) = j;
+        if (*stop != 0 && A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
+    }
+    tmem_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tmem_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// Joins the parts of the items that were cut.  CTA c belongs to the cut
+// between CTAs c - 1 and c; the cuts of one item share its rows.  Parts are
+// added in the order of their keys.  It also clears a tree's rows past the
+// node count.
+template <int DP, bool BF16, bool PROMPT>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ Attend A, const __grid_constant__ Shape S,
+                                                              void* scratch)
+{
+    constexpr int rows = PROMPT ? 2 * kTile : kTile;
+    if (!PROMPT) {
+        // does not depend on the first kernel
+        const int step = gridDim.x * kJoinThreads;
+        const int vecs = A.q_heads * A.dim / 8;
+        for (int i = blockIdx.x * kJoinThreads + threadIdx.x; i < A.B * A.N; i += step) {
+            const int b = i / A.N, n = i - b * A.N;
+            if (n < attend_request(A, b, false).rows) continue;
+            uint4* const out = reinterpret_cast<uint4*>(static_cast<char*>(A.out) + (int64_t)i * A.q_heads * A.dim * 2);
+            for (int c = 0; c < vecs; ++c) out[c] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Scratch W = scratch_of(scratch, S.ctas, rows);
+    const Join j = *reinterpret_cast<const Join*>(reinterpret_cast<const char*>(scratch) + blockIdx.x * kJoinBytes);
+    if (j.b < 0) return;
+    const Request R = attend_request(A, j.b, false);
+    const int cuts = j.c1 - j.c0, mine = (int)blockIdx.x - j.c0 - 1;
+    const int quads = A.dim / 4;
+    const int tokens = R.rows - j.rt * S.block < S.block ? R.rows - j.rt * S.block : S.block;
+    const int used = tokens * A.group;  // rows of the item, tile after tile
+    const int all = used * quads;
+    const int lo = (int)((long long)all * mine / cuts), hi = (int)((long long)all * (mine + 1) / cuts);
+    const float4* const sums = reinterpret_cast<const float4*>(W.sums);
+    const int full = S.tok * A.group;  // rows in use of a whole row tile
+    for (int i = lo + threadIdx.x; i < hi; i += kJoinThreads) {
+        const int q = i / used, r = i - q * used;
+        const int row = r < full ? r : kTile + r - full;
+        auto part = [&](int c) { return 2 * c + (c == j.c0 ? j.first : 0); };
+        float top = -INFINITY;
+        for (int c = j.c0; c <= j.c1; ++c) top = fmaxf(top, W.ml[(int64_t)part(c) * rows + row].x);
+        float l = 0.0f;
+        float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int c = j.c0; c <= j.c1; ++c) {
+            const float2 ml = W.ml[(int64_t)part(c) * rows + row];
+            const float4 x = sums[((int64_t)part(c) * (DP / 4) + q) * rows + row];
+            if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // it saw nothing
+            const float f = exp2_fast(ml.x - top);
+            l = fmaf(ml.y, f, l);
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int tok = j.rt * S.block + r / A.group, head = j.h * A.group + r % A.group;
+        const int64_t out_row = (PROMPT ? R.base : (int64_t)j.b * A.N) + tok;
+        uint2 y;
+        y.x = pack2<BF16>(o.x * inv, o.y * inv);
+        y.y = pack2<BF16>(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<char*>(A.out) + ((out_row * A.q_heads + head) * A.dim + 4 * q) * 2) = y;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder()
+{
+    static std::atomic<void*> found{nullptr};
+    void* p = found.load(std::memory_order_acquire);
+    if (p == nullptr) {
+        cudaDriverEntryPointQueryResult st;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+            st != cudaDriverEntryPointSuccess)
+            return nullptr;
+        found.store(p, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeFn>(p);
+}
+
+// A map over [n3][n2][n1][dim] elements with the given strides (in
+// elements), copied in boxes of 64 x b1 x b2 (x 1).
+bool encode(EncodeFn f, CUtensorMap* m, int32_t dtype, const void* base, int64_t dim, const int64_t n[3], const int64_t st[3],
+            int b1, int b2)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)n[0], (cuuint64_t)n[1], (cuuint64_t)n[2]};
+    cuuint64_t strides[3];
+    // the stride of an axis of one is not used; it still has to be a valid one
+    for (int i = 0; i < 3; ++i) strides[i] = n[i] > 1 ? (cuuint64_t)st[i] * 2 : 256;
+    const cuuint32_t box[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1}, one[4] = {1, 1, 1, 1};
+    return f(m, dtype == CLK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A stride (in elements of 2 bytes) that a tensor map can take, for an axis of n.
+bool map_stride(int64_t st, int64_t n) { return n <= 1 || (st > 0 && st % 8 == 0 && st < ((int64_t)1 << 38)); }
+
+template <int DP, bool BF16, bool PROMPT>
+int launch_mma(const Attend& A, const Shape& S, const Maps& M, void* scratch, cudaStream_t s)
+{
+    using L = Lay<DP, PROMPT>;
+    static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return CLK_ECUDA;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit) || dev > 63) {
+        if (cudaFuncSetAttribute(k_attend<DP, BF16, PROMPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) != cudaSuccess)
+            return CLK_ECUDA;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    k_attend<DP, BF16, PROMPT><<<S.ctas, kThreads, L::kTotal, s>>>(M, A, S, scratch);
+    int rc = launch_status();
+    if (rc != CLK_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)S.ctas);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_attend_join<DP, BF16, PROMPT>, A, S, scratch));
+}
+
+bool mma_dim(int32_t dim) { return dim >= 64 && dim <= 128 && dim % 8 == 0; }
+
+}  // namespace
+
+// Rows of 64 to 128 elements of 16 bits in whole 16-byte vectors, groups of
+// at most a row tile, and strides that tensor maps can take.  A scale that
+// is not positive would turn the running maximum around; it is left to the
+// general kernel.
+bool attend_mma_takes(const Attend& A)
+{
+    if (A.dtype == CLK_DTYPE_F32 || !mma_dim(A.dim) || A.group > kTile || !(A.scale > 0.0f)) return false;
+    for (const void* p : {A.q, A.k, A.v, (const void*)A.out, A.kc, A.vc})
+        if (!aligned(p, 16)) return false;
+    const int64_t rows = A.off != nullptr ? A.T : A.N, reqs = A.off != nullptr ? 1 : A.B;
+    if (!map_stride(A.q_req, reqs) || !map_stride(A.q_row, rows) || !map_stride(A.q_head, A.q_heads)) return false;
+    if (!map_stride(A.k_req, reqs) || !map_stride(A.k_row, rows) || !map_stride(A.k_head, A.kv_heads)) return false;
+    if (!map_stride(A.v_req, reqs) || !map_stride(A.v_row, rows) || !map_stride(A.v_head, A.kv_heads)) return false;
+    if (A.kc != nullptr && (!map_stride(A.page_stride, A.C.num_pages) || !map_stride(A.head_stride, A.kv_heads) ||
+                            !map_stride(A.tok_stride, 2)))
+        return false;
+    return true;
+}
+
+size_t attend_mma_scratch(int32_t q_heads, int32_t kv_heads, int32_t dim)
+{
+    if (!mma_dim(dim) || q_heads / kv_heads > kTile) return 0;
+    const size_t rows = 2 * kTile;
+    return (size_t)num_sms() * (kJoinBytes + 2 * rows * (sizeof(float2) + (size_t)pad_dim(dim) * sizeof(float)));
+}
+
+int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)
+{
+    const bool prompt = A.off != nullptr;
+    const EncodeFn f = encoder();
+    if (f == nullptr) return CLK_ECUDA;
+    Shape S;
+    S.tok = kTile / A.group;
+    S.block = prompt ? 2 * S.tok : S.tok;
+    const int64_t rows = prompt ? A.T : A.N, reqs = prompt ? 1 : A.B;
+    S.qbox = (int32_t)(S.tok < rows ? S.tok : rows);
+    S.kbox = (int32_t)(kTile < rows ? kTile : rows);
+    S.ctas = num_sms();
+    S.log2_scale = (float)((double)A.scale * 1.4426950408889634);
+    if (S.ctas < 1) return CLK_ECUDA;
+    Maps M;
+    const int64_t nq[3] = {A.q_heads, rows, reqs}, nk[3] = {A.kv_heads, rows, reqs};
+    const int64_t sq[3] = {A.q_head, A.q_row, A.q_req}, sk[3] = {A.k_head, A.k_row, A.k_req}, sv[3] = {A.v_head, A.v_row, A.v_req};
+    bool ok = encode(f, &M.q, A.dtype, A.q, A.dim, nq, sq, A.group, S.qbox) &&
+              encode(f, &M.k, A.dtype, A.k, A.dim, nk, sk, 1, S.kbox) && encode(f, &M.v, A.dtype, A.v, A.dim, nk, sv, 1, S.kbox);
+    if (A.kc != nullptr) {
+        const int64_t np[3] = {A.C.page_tokens(), A.kv_heads, A.C.num_pages};
+        const int64_t sp[3] = {A.tok_stride, A.head_stride, A.page_stride};
+        ok = ok && encode(f, &M.kc, A.dtype, A.kc, A.dim, np, sp, A.C.page_tokens(), 1) &&
+             encode(f, &M.vc, A.dtype, A.vc, A.dim, np, sp, A.C.page_tokens(), 1);
+    } else {
+        M.kc = M.vc = M.k;  // not read: no request has cached rows
+    }
+    if (!ok) return CLK_EINVAL;
+    const bool wide = A.dim > 64, bf = A.dtype == CLK_DTYPE_BF16;
+#define CLK_GO(D, T, P) return launch_mma<D, T, P>(A, S, M, scratch, s)
+    if (prompt) {
+        if (wide) {
+            if (bf) CLK_GO(128, true, true);
+            CLK_GO(128, false, true);
+        }
+        if (bf) CLK_GO(64, true, true);
+        CLK_GO(64, false, true);
+    }
+    if (wide) {
+        if (bf) CLK_GO(128, true, false);
+        CLK_GO(128, false, false);
+    }
+    if (bf) CLK_GO(64, true, false);
+    CLK_GO(64, false, false);
+#undef CLK_GO
+}
+
+}  // namespace clk
