@@ -129,7 +129,7 @@ __device__ long long floor_sum(long long n, long long m, long long a, long long 
 struct Reach {
     int32_t ctx, rows, slot;
     int32_t ctx_tiles, items;
-    int64_t base;
+    int32_t base;
 };
 
 template <bool PROMPT>
@@ -139,7 +139,7 @@ __device__ __forceinline__ Reach reach_of(const Request& r, const Shape& S)
     x.ctx = r.ctx;
     x.rows = r.rows;
     x.slot = r.slot;
-    x.base = r.base;
+    x.base = (int32_t)r.base;  // at most 2^30 rows
     x.ctx_tiles = (r.ctx + kTile - 1) / kTile;
     x.items = (r.rows + S.block - 1) / S.block;
     return x;
@@ -192,12 +192,11 @@ struct Walk {
     const Plan& P;
     const Reach* near;
     Reach x;
-    int b, h, item, t0, t1, total;
-    long long left;
+    int b, h, item, t0, t1, total, left;  // left: tiles of the share from t0 on
 
     __device__ Walk(const Attend& a, const Shape& s, const Plan& p, const Reach* n) : A(a), S(s), P(p), near(n)
     {
-        left = p.g1 - p.g0;
+        left = (int)(p.g1 - p.g0);
         b = p.b;
         h = p.h;
         item = p.item;
@@ -215,7 +214,7 @@ struct Walk {
     {
         total = x.ctx_tiles + new_tiles<PROMPT>(x, S, item);
         t0 = from;
-        t1 = total - from < left ? total : from + (int)left;
+        t1 = total - from < left ? total : from + left;
     }
     __device__ bool more() const { return left > 0; }
     __device__ void next()
@@ -482,14 +481,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     if (j > 0) {
                         // The scores' product was issued after this stream's last P V, so O is complete.
 #pragma unroll
-                        for (int c = 0; c < DP / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_load(tO + 32 * c, o);
+                        for (int c = 0; c < DP / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_load16(tO + 16 * c, o);
                             tmem_load_wait();
-                            tmem_loaded(o);
+                            tmem_loaded16(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
-                            tmem_store(tO + 32 * c, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                            tmem_store16(tO + 16 * c, o);
                         }
                     }
                 }
@@ -546,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             const bool whole = w.t0 == 0 && w.t1 == w.total;
             const int slot = 2 * (int)blockIdx.x + (w.left == plan.g1 - plan.g0 ? 0 : 1);
             constexpr int rows = PROMPT ? 2 * kTile : kTile;
-            const int64_t out_row = (PROMPT ? w.x.base : (int64_t)w.b * A.N) + token;
+            const int64_t out_row = (PROMPT ? (int64_t)w.x.base : (int64_t)w.b * A.N) + token;
             char* const out = static_cast<char*>(A.out) + ((out_row * A.q_heads + w.h * A.group + g) * A.dim) * 2;
             float w0 = 1.0f, w1 = 0.0f, m = ref, l = sum;
             if (!PROMPT) {
@@ -647,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 ++nq;
                 const int tok = w.item * S.block;
                 const int z = PROMPT ? 0 : w.b;
-                const int row0 = PROMPT ? (int)w.x.base : 0;
+                const int row0 = PROMPT ? w.x.base : 0;
                 if (lane == 0) {
                     bar_expect(base + L::oQFull, (uint32_t)(L::kQ * L::kHalves) * (uint32_t)(S.qbox * A.group) * 128u);
                     for (int s = 0; s < L::kQ; ++s)

@@ -111,6 +111,8 @@ __device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::afte
 __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+#define CLK_R16(x) \
+    x(0), x(1), x(2), x(3), x(4), x(5), x(6), x(7), x(8), x(9), x(10), x(11), x(12), x(13), x(14), x(15)
 #define CLK_R32(x)                                                                                                      \
     x(0), x(1), x(2), x(3), x(4), x(5), x(6), x(7), x(8), x(9), x(10), x(11), x(12), x(13), x(14), x(15), x(16), x(17), \
         x(18), x(19), x(20), x(21), x(22), x(23), x(24), x(25), x(26), x(27), x(28), x(29), x(30), x(31)
@@ -125,6 +127,28 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r)
         : CLK_R32(CLK_OUT)
         : "r"(addr));
 #undef CLK_OUT
+}
+
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r)
+{
+#define CLK_OUT(i) "=r"(r[i])
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : CLK_R16(CLK_OUT)
+        : "r"(addr));
+#undef CLK_OUT
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r)
+{
+#define CLK_IN(i) "r"(r[i])
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::CLK_R16(CLK_IN),
+        "r"(addr)
+        : "memory");
+#undef CLK_IN
 }
 
 __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t* r)
@@ -145,7 +169,15 @@ __device__ __forceinline__ void tmem_loaded(uint32_t* r)
     asm volatile("" : CLK_R32(CLK_HOLD));
 #undef CLK_HOLD
 }
+
+__device__ __forceinline__ void tmem_loaded16(uint32_t* r)
+{
+#define CLK_HOLD(i) "+r"(r[i])
+    asm volatile("" : CLK_R16(CLK_HOLD));
+#undef CLK_HOLD
+}
 #undef CLK_R32
+#undef CLK_R16
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
