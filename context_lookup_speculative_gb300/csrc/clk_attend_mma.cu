@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
 {
     using L = Lay<DP, PROMPT>;
     extern __shared__ __align__(1024) char sm[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the shuffle tells the compiler that a warp has one role
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_addr(sm);
     Plan& plan = *reinterpret_cast<Plan*>(sm + L::oPlan);
     Reach* const near = reinterpret_cast<Reach*>(sm + L::oNear);
@@ -700,90 +701,99 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 for (int j = nv > L::kV ? nv - L::kV : 0; j < nv; ++j) drain(base + L::oVFull + 8 * (j % L::kV), (uint32_t)(j / L::kV & 1));
             }
         } else if (warp == kMmaWarp) {
-            // ---- Products: one thread. ----
-            if (lane == 0) {
+            // ---- Products: one lane issues them, the warp goes along. ----
+            {
+                // Shuffled values are the same in every lane for the compiler too.
+                auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+                const uint32_t lead = lane == 0;
+                const uint32_t tm = (uint32_t)same((int)tmem);
                 constexpr uint32_t types = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((kTile >> 4) << 24);
                 constexpr uint32_t kind_s = types | ((kTile >> 3) << 17);
                 constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
                 uint32_t ps[2] = {0, 0};  // phases of PReady
                 int gi = 0, seg = 0;
                 bool ok = true;
+                // descriptors count in 16 bytes
+                const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, L::kHalf);
                 auto scores = [&](int s, int tile) {
-                    const int ki = tile % L::kK;
-                    const uint32_t q = qs + (PROMPT ? s * L::kBytes : 0), k = ks + ki * L::kBytes;
-    #pragma unroll
+                    const uint64_t q = q0 + (PROMPT ? s * (L::kBytes / 16) : 0), k = k0 + tile % L::kK * (L::kBytes / 16);
+#pragma unroll
                     for (int e = 0; e < DP / 16; ++e) {
-                        const uint32_t at = (e / 4) * L::kHalf + (e % 4) * 32;
-                        mma_ss(tmem + 128 * s, operand(q + at, 16), operand(k + at, 16), kind_s, e > 0);
+                        constexpr int next = L::kHalf / 16;
+                        const int at = (e / 4) * next + (e % 4) * 2;
+                        mma_ss(lead, tm + 128 * s, q + at, k + at, kind_s, e > 0);
                     }
-                    mma_commit(base + L::oSFull + 8 * s);
+                    mma_commit(lead, base + L::oSFull + 8 * s);
                 };
                 auto values = [&](int s, int tile, bool add) {
-                    const uint32_t v = vs + (tile % L::kV) * L::kBytes;
-    #pragma unroll
+                    const uint64_t v = v0 + tile % L::kV * (L::kBytes / 16);
+#pragma unroll
                     for (int e = 0; e < kTile / 16; ++e)
-                        mma_ts(tmem + 256 + s * DP, tmem + 128 * s + 8 * e, operand(v + e * 2048, L::kHalf), kind_o, add || e > 0);
+                        mma_ts(lead, tm + 256 + s * DP, tm + 128 * s + 8 * e, v + 128 * e, kind_o, add || e > 0);
                 };
                 auto wait_k = [&](int tile) {
-                    return bar_wait(base + L::oKFull + 8 * (tile % L::kK), (uint32_t)(tile / L::kK & 1), stop);
+                    return warp_wait(base + L::oKFull + 8 * (tile % L::kK), (uint32_t)(tile / L::kK & 1), stop);
                 };
-                for (; ok && w.more(); w.next(), ++seg) {
-                    const int len = w.t1 - w.t0;
-                    if (!(ok = bar_wait(base + L::oQFull, seg & 1, stop))) break;
+                for (; ok; w.next(), ++seg) {
+                    const int len = same(w.more() ? w.t1 - w.t0 : 0);
+                    if (len == 0) break;
+                    if (!(ok = warp_wait(base + L::oQFull, seg & 1, stop))) break;
                     tmem_after();
                     if (PROMPT) {
-                        const int n[2] = {w.last(0) - w.t0, w.last(1) - w.t0};
+                        const int n[2] = {same(w.last(0) - w.t0), same(w.last(1) - w.t0)};
                         if (!(ok = wait_k(gi))) break;
                         tmem_after();
+#pragma unroll
                         for (int s = 0; s < 2; ++s)
                             if (n[s] > 0) scores(s, gi);
-                        mma_commit(base + L::oKEmpty + 8 * (gi % L::kK));
-                        if (len == 1) mma_commit(base + L::oQEmpty);
+                        mma_commit(lead, base + L::oKEmpty + 8 * (gi % L::kK));
+                        if (len == 1) mma_commit(lead, base + L::oQEmpty);
                         for (int j = 0; ok && j < len; ++j) {
-                            for (int s = 0; ok && s < 2; ++s) {
-                                if (j >= n[s]) continue;
-                                ok = bar_wait(base + L::oVReady + 8 * ((gi + j) % L::kV), (uint32_t)((gi + j) / L::kV & 1), stop) &&
-                                     bar_wait(base + L::oPReady + 8 * s, ps[s], stop);
-                                if (!ok) break;
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                if (!ok || j >= n[s]) continue;
+                                ok = warp_wait(base + L::oVReady + 8 * ((gi + j) % L::kV), (uint32_t)((gi + j) / L::kV & 1), stop) &&
+                                     warp_wait(base + L::oPReady + 8 * s, ps[s], stop);
+                                if (!ok) continue;
                                 ps[s] ^= 1;
                                 tmem_after();
                                 values(s, gi + j, j > 0);
-                                if (j + 1 == n[s]) mma_commit(base + L::oODone + 8 * s);
+                                if (j + 1 == n[s]) mma_commit(lead, base + L::oODone + 8 * s);
                                 if (j + 1 < n[s]) {
-                                    if (!(ok = wait_k(gi + j + 1))) break;
+                                    if (!(ok = wait_k(gi + j + 1))) continue;
                                     tmem_after();
                                     scores(s, gi + j + 1);
                                 }
                             }
                             if (!ok) break;
-                            mma_commit(base + L::oVEmpty + 8 * ((gi + j) % L::kV));
-                            if (j + 1 < len) mma_commit(base + L::oKEmpty + 8 * ((gi + j + 1) % L::kK));
-                            if (j + 2 == len) mma_commit(base + L::oQEmpty);
+                            mma_commit(lead, base + L::oVEmpty + 8 * ((gi + j) % L::kV));
+                            if (j + 1 < len) mma_commit(lead, base + L::oKEmpty + 8 * ((gi + j + 1) % L::kK));
+                            if (j + 2 == len) mma_commit(lead, base + L::oQEmpty);
                         }
                     } else {
                         for (int j = 0; ok && j < 2 && j < len; ++j) {
                             if (!(ok = wait_k(gi + j))) break;
                             tmem_after();
                             scores(j, gi + j);
-                            mma_commit(base + L::oKEmpty + 8 * ((gi + j) % L::kK));
+                            mma_commit(lead, base + L::oKEmpty + 8 * ((gi + j) % L::kK));
                         }
-                        if (ok && len <= 2) mma_commit(base + L::oQEmpty);
+                        if (ok && len <= 2) mma_commit(lead, base + L::oQEmpty);
                         for (int j = 0; ok && j < len; ++j) {
                             const int s = j & 1;
-                            ok = bar_wait(base + L::oVReady + 8 * ((gi + j) % L::kV), (uint32_t)((gi + j) / L::kV & 1), stop) &&
-                                 bar_wait(base + L::oPReady + 8 * s, ps[s], stop);
+                            ok = warp_wait(base + L::oVReady + 8 * ((gi + j) % L::kV), (uint32_t)((gi + j) / L::kV & 1), stop) &&
+                                 warp_wait(base + L::oPReady + 8 * s, ps[s], stop);
                             if (!ok) break;
                             ps[s] ^= 1;
                             tmem_after();
                             values(s, gi + j, j >= 2);
-                            mma_commit(base + L::oVEmpty + 8 * ((gi + j) % L::kV));
-                            if (j + 2 >= len) mma_commit(base + L::oODone + 8 * s);
+                            mma_commit(lead, base + L::oVEmpty + 8 * ((gi + j) % L::kV));
+                            if (j + 2 >= len) mma_commit(lead, base + L::oODone + 8 * s);
                             if (j + 2 < len) {
                                 if (!(ok = wait_k(gi + j + 2))) break;
                                 tmem_after();
                                 scores(s, gi + j + 2);
-                                mma_commit(base + L::oKEmpty + 8 * ((gi + j + 2) % L::kK));
-                                if (j + 3 == len) mma_commit(base + L::oQEmpty);
+                                mma_commit(lead, base + L::oKEmpty + 8 * ((gi + j + 2) % L::kK));
+                                if (j + 3 == len) mma_commit(lead, base + L::oQEmpty);
                             }
                         }
                     }
@@ -791,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 }
                 if (!ok) {
                     // Products in flight end before tensor memory is given up.
-                    mma_commit(base + L::oDrain);
+                    mma_commit(lead, base + L::oDrain);
                     const long long t0 = clock64();
                     while (!bar_try(base + L::oDrain, 0) && clock64() - t0 < kWaitClocks) {}
                 }
