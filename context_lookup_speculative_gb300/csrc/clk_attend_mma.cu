@@ -257,7 +257,7 @@ struct Lay {
     static constexpr int oKFull = kTiles * kBytes, oKEmpty = oKFull + 8 * kK;
     static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
     static constexpr int oQFull = oVEmpty + 8 * kV, oQEmpty = oQFull + 8;
-    static constexpr int oSFull = oQEmpty + 8, oPReady = oSFull + 16, oODone = oPReady + 16;
+    static constexpr int oSFull = oQEmpty + 8, oPReady = oSFull + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
     static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
     static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         bar_init(base + L::oQEmpty, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(base + L::oSFull + 8 * i, 1);
+            bar_init(base + L::oPHalf + 8 * i, 4);
             bar_init(base + L::oPReady + 8 * i, 4);
             bar_init(base + L::oODone + 8 * i, 1);
         }
@@ -466,13 +467,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
 #pragma unroll
                     for (int c = 64; c < kTile; ++c) x[c] = 0xff800000u;
                 }
-                float top = -INFINITY;
-                {
-                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(x[c]));
-                    top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-                }
+                for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        m[e] = max3(m[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+                const float top = max3(m[0], m[1], fmaxf(m[2], m[3]));
                 const bool grow = top > ref + slack || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float to = grow ? top : ref;
@@ -494,22 +495,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     }
                 }
                 const float shift = ref == -INFINITY ? 0.0f : lift - ref * cs;
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                // Weights, 64 keys at a time: the first half's product starts while the second is computed.
+                const uint64_t cs2 = pair(__float_as_uint(cs), __float_as_uint(cs));
+                const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
+                uint64_t part[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < kTile; ++c) {
-                    const float p = exp2_fast(fmaf(__uint_as_float(x[c]), cs, shift));
-                    part[c & 3] += p;
-                    x[c] = __float_as_uint(p);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t y[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 z = unpair(fma2(pair(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), cs2, shift2));
+                        const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
+                        part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                        y[e] = pack2<BF16>(p0, p1);
+                    }
+                    tmem_store16(tS + 16 * c, y);
+                    if (c == 1) {
+                        tmem_store_wait();
+                        tmem_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
+                    }
                 }
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t y[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        y[e] = pack2<BF16>(__uint_as_float(x[64 * c + 2 * e]), __uint_as_float(x[64 * c + 2 * e + 1]));
-                    tmem_store(tS + 32 * c, y);
-                }
+                const float2 both = unpair(add2(part[0], part[1]));
+                sum += both.x + both.y;
                 if (!cached && (!PROMPT || n0 + kTile - 1 > w.item * S.block)) {
                     // Rows of V that were not finite: NaN for those who see them.
                     const int vi = (gi + jj) % L::kV;
@@ -725,11 +734,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     }
                     mma_commit(lead, base + L::oSFull + 8 * s);
                 };
+                // Both halves of a tile's weights; the V tile is there.
                 auto values = [&](int s, int tile, bool add) {
                     const uint64_t v = v0 + tile % L::kV * (L::kBytes / 16);
 #pragma unroll
-                    for (int e = 0; e < kTile / 16; ++e)
+                    for (int e = 0; e < kTile / 16; ++e) {
+                        if (e % 4 == 0) {
+                            if (!warp_wait(base + (e == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
+                            tmem_after();
+                        }
                         mma_ts(lead, tm + 256 + s * DP, tm + 128 * s + 8 * e, v + 128 * e, kind_o, add || e > 0);
+                    }
+                    ps[s] ^= 1;
+                    return true;
+                };
+                auto wait_v = [&](int tile) {
+                    return warp_wait(base + L::oVReady + 8 * (tile % L::kV), (uint32_t)(tile / L::kV & 1), stop);
                 };
                 auto wait_k = [&](int tile) {
                     return warp_wait(base + L::oKFull + 8 * (tile % L::kK), (uint32_t)(tile / L::kK & 1), stop);
@@ -752,12 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
                                 if (!ok || j >= n[s]) continue;
-                                ok = warp_wait(base + L::oVReady + 8 * ((gi + j) % L::kV), (uint32_t)((gi + j) / L::kV & 1), stop) &&
-                                     warp_wait(base + L::oPReady + 8 * s, ps[s], stop);
-                                if (!ok) continue;
-                                ps[s] ^= 1;
-                                tmem_after();
-                                values(s, gi + j, j > 0);
+                                if (!(ok = wait_v(gi + j) && values(s, gi + j, j > 0))) continue;
                                 if (j + 1 == n[s]) mma_commit(lead, base + L::oODone + 8 * s);
                                 if (j + 1 < n[s]) {
                                     if (!(ok = wait_k(gi + j + 1))) continue;
@@ -780,12 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         if (ok && len <= 2) mma_commit(lead, base + L::oQEmpty);
                         for (int j = 0; ok && j < len; ++j) {
                             const int s = j & 1;
-                            ok = warp_wait(base + L::oVReady + 8 * ((gi + j) % L::kV), (uint32_t)((gi + j) / L::kV & 1), stop) &&
-                                 warp_wait(base + L::oPReady + 8 * s, ps[s], stop);
-                            if (!ok) break;
-                            ps[s] ^= 1;
-                            tmem_after();
-                            values(s, gi + j, j >= 2);
+                            if (!(ok = wait_v(gi + j) && values(s, gi + j, j >= 2))) break;
                             mma_commit(lead, base + L::oVEmpty + 8 * ((gi + j) % L::kV));
                             if (j + 2 >= len) mma_commit(lead, base + L::oODone + 8 * s);
                             if (j + 2 < len) {
