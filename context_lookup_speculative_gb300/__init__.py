@@ -595,11 +595,12 @@ def _pool_desc(h: Cache, pool: torch.Tensor) -> PoolDesc:
     if not pool.is_cuda or pool.dim() != 5:
         raise ValueError("pool must be a CUDA tensor [planes, pages, heads, page_tokens, dim]")
     planes, pages, heads, tokens, dim = pool.shape
-    st = pool.stride()
-    if pool.dtype not in _POOL_DTYPES or st[4] != 1 or pages < h.num_pages or tokens != h.page_tokens:
+    plane_st, page_st, head_st, tok_st, one = pool.stride()
+    code = _POOL_DTYPES.get(pool.dtype)
+    if code is None or one != 1 or pages < h.num_pages or tokens != h.page_tokens:
         raise ValueError(f"pool must be bfloat16, float16 or float32 with contiguous rows, >= {h.num_pages} pages and "
                          f"{h.page_tokens} tokens a page, got {pool.dtype} {tuple(pool.shape)}")
-    return PoolDesc(pool.data_ptr(), _POOL_DTYPES[pool.dtype], planes, heads, dim, st[0], st[1], st[2], st[3])
+    return PoolDesc(pool.data_ptr(), code, planes, heads, dim, plane_st, page_st, head_st, tok_st)
 
 
 def cache_grow(h: Cache, slots, count, stream=None):
@@ -616,24 +617,25 @@ def cache_append(h: Cache, slots, pool, k, v, count, layer: int = 0, path=None, 
     b; or, with ``offsets`` (int64 [B+1]), [layers, T, kv_heads, dim]."""
     B = slots.numel()
     d = _pool_desc(h, pool)
-    lead = 2 if offsets is not None else 3
-    if k.dim() != lead + 2 or k.shape != v.shape or k.stride() != v.stride() or not (k.is_cuda and v.is_cuda):
+    if k.dim() != (4 if offsets is not None else 5) or k.shape != v.shape or k.stride() != v.stride() \
+            or not (k.is_cuda and v.is_cuda):
         raise ValueError("k and v must be CUDA tensors of one shape and layout, "
                          "[layers, B, N, heads, dim] or, with offsets, [layers, T, heads, dim]")
-    if k.dtype != pool.dtype or v.dtype != pool.dtype or tuple(k.shape[lead:]) != (d.heads, d.dim):
-        raise ValueError("k and v must have the pool's type, heads and dim")
-    st = k.stride()
-    if d.dim > 1 and st[-1] != 1:
-        raise ValueError("rows of k and v must be contiguous")
     if offsets is None:
-        if k.shape[1] != B or (B > 1 and st[1] != k.shape[2] * st[2]):
+        layers, Bk, N, heads, dim = k.shape
+        layer_st, req, row, head, one = k.stride()
+        if Bk != B or (B > 1 and req != N * row):
             raise ValueError("k and v must hold B requests of N rows, one request's rows after another's")
-        N, row = k.shape[2], st[2]
     else:
-        N, row = k.shape[1], st[1]
+        layers, N, heads, dim = k.shape
+        layer_st, row, head, one = k.stride()
+    if k.dtype != pool.dtype or v.dtype != pool.dtype or heads != d.heads or dim != d.dim:
+        raise ValueError("k and v must have the pool's type, heads and dim")
+    if dim > 1 and one != 1:
+        raise ValueError("rows of k and v must be contiguous")
     _check("clk_cache_append",
-           lib().clk_cache_append(h.handle, _ptr(slots, name="slots"), B, ctypes.byref(d), layer, k.shape[0],
-                                  k.data_ptr(), v.data_ptr(), st[0], row, st[-2], N,
+           lib().clk_cache_append(h.handle, _ptr(slots, name="slots"), B, ctypes.byref(d), layer, layers,
+                                  k.data_ptr(), v.data_ptr(), layer_st, row, head, N,
                                   _ptr(offsets, torch.int64, (B + 1,), "offsets"),
                                   _ptr(path, shape=(B, N), name="path"), _ptr(count, shape=(B,), name="count"),
                                   _stream(stream)))
@@ -683,30 +685,36 @@ def tree_accept(tok, parent, nodes, argmax, accept, path, emitted, out_tok, stre
 
 
 def attend_scratch(q_heads: int, kv_heads: int, dim: int, device="cuda") -> torch.Tensor:
-    """A scratch buffer for tree_attend / prompt_attend with these heads."""
+    """A zeroed scratch buffer for tree_attend / prompt_attend with these heads."""
     n = ctypes.c_size_t()
     _check("clk_attend_scratch_bytes", lib().clk_attend_scratch_bytes(q_heads, kv_heads, dim, ctypes.byref(n)))
-    return torch.empty(n.value, dtype=torch.uint8, device=device)
+    return torch.zeros(n.value, dtype=torch.uint8, device=device)
 
 
 def _attn_desc(q, k, v, out, scale: float) -> AttnDesc:
     """q [.., q_heads, dim], k and v [.., kv_heads, dim], with 1 or 2 leading axes (prompt, tree)."""
-    n = q.dim()
-    if k.dim() != n or v.dim() != n or out.shape != q.shape or not out.is_contiguous() or k.shape != v.shape \
-            or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+    if q.dim() == 4:
+        B, N, Hq, D = q.shape
+        lead = (B, N)
+        (q0, q1, q2, qd), (k0, k1, k2, kd), (v0, v1, v2, vd) = q.stride(), k.stride(), v.stride()
+    else:
+        N, Hq, D = q.shape
+        lead = (N,)
+        q0 = k0 = v0 = 0
+        (q1, q2, qd), (k1, k2, kd), (v1, v2, vd) = q.stride(), k.stride(), v.stride()
+    Hkv = k.shape[-2]
+    if k.shape != lead + (Hkv, D) or v.shape != k.shape or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("q and out (contiguous) must have one shape, k and v another that differs in the heads only")
     if not (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda):
         raise ValueError("q, k, v and out must be CUDA tensors")
     dt = q.dtype
-    if dt not in _POOL_DTYPES or k.dtype != dt or v.dtype != dt or out.dtype != dt:
+    code = _POOL_DTYPES.get(dt)
+    if code is None or k.dtype != dt or v.dtype != dt or out.dtype != dt:
         raise ValueError("q, k, v and out must have one type of bfloat16, float16 or float32")
-    sq, sk, sv = q.stride(), k.stride(), v.stride()
-    if q.shape[-1] > 1 and (sq[-1] != 1 or sk[-1] != 1 or sv[-1] != 1):
+    if D > 1 and not qd == kd == vd == 1:
         raise ValueError("rows of q, k and v must be contiguous")
-    if n == 3:
-        sq, sk, sv = (0,) + sq, (0,) + sk, (0,) + sv
-    return AttnDesc(_POOL_DTYPES[dt], q.shape[-2], k.shape[-2], q.shape[-1], scale, q.data_ptr(), k.data_ptr(),
-                    v.data_ptr(), out.data_ptr(), sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], sv[0], sv[1], sv[2])
+    return AttnDesc(code, Hq, Hkv, D, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                    q0, q1, q2, k0, k1, k2, v0, v1, v2)
 
 
 def tree_attend(h: Cache, slots, pool, layer: int, q, k, v, nodes, mask, scale: float, out, scratch, ctx=None,
@@ -716,9 +724,9 @@ def tree_attend(h: Cache, slots, pool, layer: int, q, k, v, nodes, mask, scale: 
     q [B, N, q_heads, dim], k and v [B, N, kv_heads, dim] of the new tokens
     (strided), mask int64 [B, N], out [B, N, q_heads, dim]; ctx (int32 [B] or
     None: the slots' lengths) cached rows that are seen."""
-    if q.dim() != 4:
-        raise ValueError("q must be [B, N, q_heads, dim]")
-    B, N = q.shape[0], q.shape[1]
+    if not q.dim() == k.dim() == v.dim() == 4:
+        raise ValueError("q, k and v must be [B, N, heads, dim]")
+    B, N = q.shape[:2]
     d = _pool_desc(h, pool)
     a = _attn_desc(q, k, v, out, scale)
     _check("clk_tree_attend",
@@ -736,8 +744,8 @@ def prompt_attend(q, k, v, offsets, scale: float, out, scratch, cache: Optional[
     rows offsets[b] .. offsets[b+1] (int64 [B+1]), out [T, q_heads, dim].
     With cache, slots, pool and ctx (int32 [B]) the rows also see the slots'
     first ctx cached rows."""
-    if q.dim() != 3:
-        raise ValueError("q must be [T, q_heads, dim]")
+    if not q.dim() == k.dim() == v.dim() == 3:
+        raise ValueError("q, k and v must be [T, heads, dim]")
     B = offsets.numel() - 1
     if cache is None and (slots is not None or pool is not None or ctx is not None):
         raise ValueError("slots, pool and ctx need a cache")

@@ -11,8 +11,10 @@
 // SM) cut into equal shares: ragged contexts, causal rows of every length
 // and a single long request all balance, whatever the batch.  An item that
 // a cut falls into is left as partial results (float32 sums and the
-// softmax's reference and sum per row) that a second kernel joins in a fixed
-// order.
+// softmax's reference and sum per row).  The grid is launched cooperatively;
+// a CTA that has written its parts raises its flag, waits for the flags of
+// the CTAs that share its cut items (there are at most two), and joins its
+// share of their rows, the parts in the order of their keys.
 //
 // A CTA.  One warp copies tiles into two rings in shared memory (pages and
 // packed rows are boxes of tensor maps, 128-byte swizzle); one thread issues
@@ -58,8 +60,7 @@ constexpr int kTile = 128;     // keys of a tile, rows of a row tile
 constexpr int kWarps = 12;     // 8 softmax, 1 copies, 1 products, 2 V tiles
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kValueWarp = 10;
-constexpr int kNear = 16;      // requests whose data a CTA keeps
-constexpr int kJoinThreads = 256;
+constexpr int kNear = 12;      // requests whose data a CTA keeps
 
 struct Maps {
     CUtensorMap q, k, v, kc, vc;
@@ -74,52 +75,57 @@ struct Shape {
     float log2_scale;  // scale * log2(e)
 };
 
-// Scratch: join records, row statistics and partial sums, two parts a CTA.
-struct Join {
-    int32_t b, h, rt;   // the item that a CTA's share begins in the middle of; b < 0: none
-    int32_t c0, c1;     // its first and last CTA
-    int32_t first;      // part of c0 that holds its beginning
-};
-
+// Scratch: a flag per CTA (a count of calls), row statistics and partial
+// sums, two parts a CTA.
 struct Scratch {
-    Join* join;   // [ctas]
-    float2* ml;   // [ctas][2][rows]
-    float* sums;  // [ctas][2][DP / 4][rows][4]
+    uint32_t* flag;  // [ctas]
+    float2* ml;      // [ctas][2][rows]
+    float* sums;     // [ctas][2][DP / 4][rows][4]
 };
-
-constexpr size_t kJoinBytes = 32;
-static_assert(sizeof(Join) <= kJoinBytes, "join record");
 
 __host__ __device__ inline int pad_dim(int dim) { return dim <= 64 ? 64 : 128; }
+
+__host__ __device__ inline size_t flag_bytes(int ctas) { return ((size_t)ctas * sizeof(uint32_t) + 127) / 128 * 128; }
 
 __host__ __device__ inline Scratch scratch_of(void* base, int ctas, int rows)
 {
     Scratch s;
     char* p = static_cast<char*>(base);
-    s.join = reinterpret_cast<Join*>(p);
-    p += (size_t)ctas * kJoinBytes;
+    s.flag = reinterpret_cast<uint32_t*>(p);
+    p += flag_bytes(ctas);
     s.ml = reinterpret_cast<float2*>(p);
     p += (size_t)ctas * 2 * rows * sizeof(float2);
     s.sums = reinterpret_cast<float*>(p);
     return s;
 }
 
-// sum over i < n of floor((a i + b) / m), for n >= 0, m > 0, a, b >= 0 (a
+// a / b for a >= 0, b > 0, in 32 bits where they fit.
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// sum over i < n of floor((a i + b) / m), for m > 0 and a n + b < 2^32 (a
 // step of Euclid's algorithm at a time).
-__device__ long long floor_sum(long long n, long long m, long long a, long long b)
+__device__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b)
 {
     long long s = 0;
     while (n > 0) {
-        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const long long y = a * n + b;
+        if (a >= m) {
+            s += ((long long)n * (n - 1) >> 1) * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            s += (long long)n * (b / m);
+            b %= m;
+        }
+        const uint32_t y = a * n + b;
         if (y < m) break;
         n = y / m;
         b = y % m;
-        const long long t = m;
+        const uint32_t u = m;
         m = a;
-        a = t;
+        a = u;
     }
     return s;
 }
@@ -172,16 +178,37 @@ __device__ __forceinline__ long long tiles_of(const Reach& x, const Shape& S)
     return x.items == 0 ? 0 : tiles_before<PROMPT>(x, S, x.items);
 }
 
-// First tile of CTA c's share of `all` tiles.
-__device__ __forceinline__ long long share(long long all, int c, int ctas) { return all * c / ctas; }
-// The CTA whose share holds tile g.
-__device__ __forceinline__ int cta_of(long long all, long long g, int ctas) { return (int)(((g + 1) * ctas - 1) / all); }
+// `all` tiles in shares of q or q + 1: the first r CTAs have one more.
+struct Cuts {
+    long long q;
+    int r;
+    __device__ Cuts(long long all, int ctas)
+    {
+        q = ctas > 0 ? quotient(all, ctas) : 0;
+        r = (int)(all - q * ctas);
+    }
+    __device__ long long begin(int c) const { return q * c + (c < r ? c : r); }
+    // the CTA whose share holds tile g
+    __device__ int holder(long long g) const
+    {
+        const long long big = (q + 1) * r;
+        return (int)(g < big ? quotient(g, q + 1) : r + quotient(g - big, q));
+    }
+};
 
 // What a CTA knows after planning (in shared memory).
 struct Plan {
     long long all, g0, g1;  // tiles in all, this CTA's share
     int ctas;               // CTAs that have work
     int b, h, item, t;      // where the share begins
+    uint32_t call;          // this CTA's flag before this call
+};
+
+// An item whose tiles lie in several CTAs' shares.
+struct Cut {
+    Reach x;
+    int b, h, item, total;  // total: its tiles, 0 for none
+    long long begin;        // its first one
 };
 
 // The CTA's way through its share, the same in every warp.
@@ -263,11 +290,78 @@ struct Lay {
     static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
     static constexpr int oNear = oBad + 16 * kV;                      // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
-    static constexpr int oStop = oPlan + (int)sizeof(Plan), oTmem = oStop + 4;
+    static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: where the share begins, where it ends
+    static constexpr int oStop = oCut + 2 * (int)sizeof(Cut), oTmem = oStop + 4;
     static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;          // float2[2][128] for trees
     static constexpr int kTotal = oStat + (PROMPT ? 0 : 2 * kTile * 8);
     static_assert(kTotal <= 232448, "shared memory");
 };
+
+// This CTA's share of an item whose `total` tiles, from tile `begin` of the
+// line on, lie in several CTAs' shares.
+template <int DP, bool BF16, bool PROMPT>
+__device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const Scratch& W, uint32_t call, const Cuts& cuts,
+                                          const Cut& cut, volatile int* stop)
+{
+    constexpr int rows = PROMPT ? 2 * kTile : kTile;
+    const int tid = threadIdx.x;
+    const int c0 = cuts.holder(cut.begin), c1 = cuts.holder(cut.begin + cut.total - 1), parts = c1 - c0 + 1;
+    // A CTA's second part begins after its share does.
+    const int first = 2 * c0 + (cuts.begin(c0) == cut.begin ? 0 : 1);
+    auto part = [&](int c) { return c == 0 ? first : 2 * (c0 + c); };
+    // All CTAs of the grid are resident, and none waits before it has raised its own flag.
+    for (int c = tid; c < parts; c += kThreads) {
+        uint32_t seen;
+        const long long t0 = clock64();
+        for (;;) {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(W.flag + c0 + c) : "memory");
+            if (seen != call || *stop != 0) break;
+            if (clock64() - t0 > kWaitClocks) *stop = 1;
+        }
+    }
+    __syncthreads();
+    if (*stop != 0) {
+        if (tid == 0 && A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
+        return;
+    }
+    const int quads = A.dim / 4;
+    const int left = cut.x.rows - cut.item * S.block, tokens = left < S.block ? left : S.block;
+    const int used = tokens * A.group;   // rows of the item, tile after tile
+    const int full = S.tok * A.group;    // rows in use of a whole row tile
+    const int mine = (int)blockIdx.x - c0;
+    const int all = used * quads;
+    const int lo = (int)((long long)all * mine / parts), hi = (int)((long long)all * (mine + 1) / parts);
+    const float4* const sums = reinterpret_cast<const float4*>(W.sums);
+    for (int i = lo + tid; i < hi; i += kThreads) {
+        const int q = i / used, r = i - q * used;
+        const int row = r < full ? r : kTile + r - full;
+        // The running reference keeps the order of the parts and reads each once.
+        float top = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int c = 0; c < parts; ++c) {
+            const int64_t at = part(c);
+            const float2 ml = __ldcg(W.ml + at * rows + row);
+            const float4 v = __ldcg(sums + (at * (DP / 4) + q) * rows + row);
+            if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // it saw nothing
+            const float to = fmaxf(top, ml.x);
+            const float f = top == -INFINITY ? 0.0f : exp2_fast(top - to), g = exp2_fast(ml.x - to);
+            top = to;
+            l = l * f + ml.y * g;
+            o.x = o.x * f + v.x * g;
+            o.y = o.y * f + v.y * g;
+            o.z = o.z * f + v.z * g;
+            o.w = o.w * f + v.w * g;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int tok = cut.item * S.block + r / A.group, head = cut.h * A.group + r % A.group;
+        const int64_t out_row = (PROMPT ? (int64_t)cut.x.base : (int64_t)cut.b * A.N) + tok;
+        uint2 y;
+        y.x = pack2<BF16>(o.x * inv, o.y * inv);
+        y.y = pack2<BF16>(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<char*>(A.out) + ((out_row * A.q_heads + head) * A.dim + 4 * q) * 2) = y;
+    }
+}
 
 template <int DP, bool BF16, bool PROMPT>
 __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ Maps M, const __grid_constant__ Attend A,
@@ -280,105 +374,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     const uint32_t base = smem_addr(sm);
     Plan& plan = *reinterpret_cast<Plan*>(sm + L::oPlan);
     Reach* const near = reinterpret_cast<Reach*>(sm + L::oNear);
+    Cut* const cut = reinterpret_cast<Cut*>(sm + L::oCut);
     volatile int* const stop = reinterpret_cast<volatile int*>(sm + L::oStop);
     volatile uint32_t* const bad = reinterpret_cast<volatile uint32_t*>(sm + L::oBad);
     const Scratch W = scratch_of(scratch, S.ctas, PROMPT ? 2 * kTile : kTile);
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this one's end
-
-    // ---- Plan: all requests' tiles, this CTA's share, where it begins. ----
-    {
-        long long* const sums = reinterpret_cast<long long*>(sm);  // the rings are not in use yet
-        long long before = 0, all = 0, mine = 0;
-        for (int pass = 0; pass < 2; ++pass) {
-            // a batch of up to kThreads requests needs one pass
-            if (pass == 1 && A.B <= kThreads) break;
-            before = 0;
-            for (int at = 0; at < A.B; at += kThreads) {
-                const int b = at + tid;
-                long long u = 0;
-                if (b < A.B)
-                    u = tiles_of<PROMPT>(reach_of<PROMPT>(attend_request(A, b, pass == 0 && blockIdx.x == 0), S), S) * A.kv_heads;
-                long long x = u;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, x, d);
-                    if (lane >= d) x += y;
-                }
-                if (lane == 31) sums[warp] = x;
-                __syncthreads();
-                long long lower = before;
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w < warp) lower += sums[w];
-                    before += sums[w];
-                }
-                mine = lower + x - u;
-                if (pass == 1 && u > 0 && mine <= plan.g0 && plan.g0 < mine + u) {
-                    plan.b = b;
-                    plan.all = mine;  // for now: tiles before this request
-                }
-                if (A.B <= kThreads && u > 0) {
-                    all = before;
-                    const int ctas = all < S.ctas ? (int)all : S.ctas;
-                    const long long g0 = (int)blockIdx.x < ctas ? share(all, blockIdx.x, ctas) : all;
-                    if (mine <= g0 && g0 < mine + u) {
-                        plan.b = b;
-                        plan.all = mine;
-                    }
-                }
-                __syncthreads();
-            }
-            if (pass == 0) {
-                all = before;
-                if (tid == 0) {
-                    const int ctas = all < S.ctas ? (int)all : S.ctas;
-                    plan.ctas = ctas;
-                    plan.g0 = (int)blockIdx.x < ctas ? share(all, blockIdx.x, ctas) : all;
-                    plan.g1 = (int)blockIdx.x < ctas ? share(all, blockIdx.x + 1, ctas) : all;
-                }
-                __syncthreads();
-            }
-        }
-        const long long start = plan.all;
-        __syncthreads();
-        if (plan.g0 < plan.g1) {
-            if (tid < kNear) {
-                const int b = plan.b + tid;
-                if (b < A.B) near[tid] = reach_of<PROMPT>(attend_request(A, b, false), S);
-            }
-            __syncthreads();
-            if (warp == 0) {
-                const Reach x = near[0];
-                const long long off = plan.g0 - start, per = tiles_of<PROMPT>(x, S);
-                const int h = (int)(off / per);
-                const long long o = off - h * per;
-                // the last item with tiles_before <= o, 32 ways at a time
-                int lo = 0, span = x.items;
-                while (span > 1) {
-                    const int step = (span + 31) / 32;
-                    const int i = lo + lane * step;
-                    const bool le = lane * step < span && tiles_before<PROMPT>(x, S, i) <= o;
-                    const int n = __popc(__ballot_sync(0xffffffffu, le));
-                    const int end = lo + span;
-                    lo += (n - 1) * step;
-                    span = lo + step < end ? step : end - lo;
-                }
-                if (lane == 0) {
-                    plan.h = h;
-                    plan.item = lo;
-                    plan.t = (int)(o - tiles_before<PROMPT>(x, S, lo));
-                }
-            }
-        }
-        if (tid == 0) {
-            plan.all = all;
-            *stop = 0;
-        }
-        __syncthreads();
-    }
-
-    // ---- Barriers and tensor memory. ----
-    if (tid == 0) {
+    // ---- Start: tensor memory, barriers and descriptors, while the requests' data is on its way. ----
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::oTmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (warp == kCopyWarp) {
+        if (lane < 5)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char*>(&M) + lane * sizeof(CUtensorMap)) : "memory");
+    } else if (tid == 32 * kValueWarp) {
         for (int i = 0; i < L::kK; ++i) {
             bar_init(base + L::oKFull + 8 * i, 1);
             bar_init(base + L::oKEmpty + 8 * i, 1);
@@ -400,11 +408,99 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         bar_init(base + L::oDrain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the planning scratch lies where tiles go
-    if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::oTmem) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+
+    // ---- Plan: all requests' tiles, this CTA's share, where it begins. ----
+    {
+        long long* const sums = reinterpret_cast<long long*>(sm);  // the rings are not in use yet
+        const bool once = A.B <= kThreads;  // the batch is seen in one pass
+        long long all = 0;
+        Reach x{};
+        for (int pass = 0;; ++pass) {
+            long long before = 0;
+            for (int at = 0; at < A.B; at += kThreads) {
+                const int b = at + tid;
+                long long u = 0;
+                if (b < A.B) {
+                    x = reach_of<PROMPT>(attend_request(A, b, pass == 0 && blockIdx.x == 0), S);
+                    u = tiles_of<PROMPT>(x, S) * A.kv_heads;
+                }
+                long long y = u;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const long long z = __shfl_up_sync(0xffffffffu, y, d);
+                    if (lane >= d) y += z;
+                }
+                if (lane == 31) sums[warp] = y;
+                __syncthreads();
+                long long mine = before + y - u;
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) mine += sums[w];
+                    before += sums[w];
+                }
+                if (once) all = before;
+                if (once || pass == 1) {
+                    // The warp that has the share's first request finds the place in it.
+                    const int ctas = all < S.ctas ? (int)all : S.ctas;
+                    const long long g0 = (int)blockIdx.x < ctas ? Cuts(all, ctas).begin(blockIdx.x) : all;
+                    const unsigned who = __ballot_sync(0xffffffffu, u > 0 && mine <= g0 && g0 < mine + u);
+                    if (who != 0) {
+                        const int src = __ffs((int)who) - 1;
+                        Reach z;
+                        z.rows = __shfl_sync(0xffffffffu, x.rows, src);
+                        z.ctx_tiles = __shfl_sync(0xffffffffu, x.ctx_tiles, src);
+                        z.items = __shfl_sync(0xffffffffu, x.items, src);
+                        const long long off = __shfl_sync(0xffffffffu, g0 - mine, src), per = tiles_of<PROMPT>(z, S);
+                        const int h = (int)quotient(off, per);
+                        const long long o = off - h * per;
+                        // the last item with tiles_before <= o, 32 ways at a time
+                        int lo = 0, span = z.items;
+                        if (!PROMPT) {
+                            lo = (int)quotient(o, z.ctx_tiles + 1);
+                            span = 1;
+                        }
+                        while (span > 1) {
+                            const int step = (span + 31) / 32;
+                            const bool le = lane * step < span && tiles_before<PROMPT>(z, S, lo + lane * step) <= o;
+                            const int n = __popc(__ballot_sync(0xffffffffu, le));
+                            const int end = lo + span;
+                            lo += (n - 1) * step;
+                            span = lo + step < end ? step : end - lo;
+                        }
+                        if (lane == 0) {
+                            plan.b = at + 32 * warp + src;
+                            plan.h = h;
+                            plan.item = lo;
+                            plan.t = (int)(o - tiles_before<PROMPT>(z, S, lo));
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+            if (pass == 0) all = before;
+            if (once || pass == 1) break;
+        }
+        const int ctas = all < S.ctas ? (int)all : S.ctas;
+        const Cuts cuts(all, ctas);
+        const bool busy = (int)blockIdx.x < ctas;
+        if (tid == 0) {
+            plan.all = all;
+            plan.ctas = ctas;
+            plan.g0 = busy ? cuts.begin(blockIdx.x) : all;
+            plan.g1 = busy ? cuts.begin(blockIdx.x + 1) : all;
+            plan.call = __ldcg(W.flag + blockIdx.x);
+            *stop = 0;
+            cut[0].total = cut[1].total = 0;
+        }
+        if (busy) {
+            if (once) {
+                const int i = tid - plan.b;
+                if (i >= 0 && i < kNear) near[i] = x;
+            } else if (tid < kNear && plan.b + tid < A.B) {
+                near[tid] = reach_of<PROMPT>(attend_request(A, plan.b + tid, false), S);
+            }
+        }
     }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the planning scratch lies where tiles go
     tmem_before();
     __syncthreads();
     tmem_after();
@@ -553,6 +649,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             }
             // ---- The segment's result: to the output, or as a part. ----
             const bool whole = w.t0 == 0 && w.t1 == w.total;
+            if (!whole && tid == 0) {
+                // an item may fill the share: its cuts at both ends are one join
+                const long long end = plan.g1 - w.left + (w.t1 - w.t0);
+                cut[w.left == (int)(plan.g1 - plan.g0) ? 0 : 1] = Cut{w.x, w.b, w.h, w.item, w.total, end - w.t1};
+            }
             const int slot = 2 * (int)blockIdx.x + (w.left == plan.g1 - plan.g0 ? 0 : 1);
             constexpr int rows = PROMPT ? 2 * kTile : kTile;
             const int64_t out_row = (PROMPT ? (int64_t)w.x.base : (int64_t)w.b * A.N) + token;
@@ -821,6 +922,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             // ---- V tiles: rows past the end, and rows that are not finite. ----
             constexpr uint32_t top = BF16 ? 0x7f807f80u : 0x7c007c00u;
             const int half = warp - kValueWarp;
+            if (!PROMPT) {
+                // Rows past the node counts are 0; the requests are dealt out to the CTAs.
+                for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
+                    const int rows = attend_request(A, b, false).rows;
+                    const int64_t row = (int64_t)A.q_heads * A.dim / 8;
+                    uint4* const out = static_cast<uint4*>(A.out) + ((int64_t)b * A.N + rows) * row;
+                    for (int64_t e = 32 * half + lane; e < (A.N - rows) * row; e += 64) out[e] = make_uint4(0, 0, 0, 0);
+                }
+            }
             int i = 0;
             bool ok = true;
             for (; ok && w.more(); w.next()) {
@@ -867,93 +977,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         }
     }
 
-    // ---- The join record, and the end. ----
-    __syncthreads();
-    if (tid == 0) {
-        Join j{-1, 0, 0, 0, 0, 0};
-        if (plan.g0 < plan.g1 && plan.t > 0) {
-            const Reach x = near[0];
-            const long long begin = plan.g0 - plan.t;
-            const long long end = begin + x.ctx_tiles + new_tiles<PROMPT>(x, S, plan.item);
-            j.b = plan.b;
-            j.h = plan.h;
-            j.rt = plan.item;
-            j.c0 = cta_of(plan.all, begin, plan.ctas);
-            j.c1 = cta_of(plan.all, end - 1, plan.ctas);
-            j.first = share(plan.all, j.c0, plan.ctas) == begin ? 0 : 1;
-        }
-        *reinterpret_cast<Join*>(reinterpret_cast<char*>(scratch) + blockIdx.x * kJoinBytes) = j;
-        if (*stop != 0 && A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
-    }
+    // ---- Parts are written: raise the flag, join what was cut. ----
     tmem_before();
     __syncthreads();
     if (warp == kMmaWarp) {
         tmem_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-}
-
-// Joins the parts of the items that were cut.  CTA c belongs to the cut
-// between CTAs c - 1 and c; the cuts of one item share its rows.  Parts are
-// added in the order of their keys.  It also clears a tree's rows past the
-// node count.
-template <int DP, bool BF16, bool PROMPT>
-__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ Attend A, const __grid_constant__ Shape S,
-                                                              void* scratch)
-{
-    constexpr int rows = PROMPT ? 2 * kTile : kTile;
-    if (!PROMPT) {
-        // does not depend on the first kernel
-        const int step = gridDim.x * kJoinThreads;
-        const int vecs = A.q_heads * A.dim / 8;
-        for (int i = blockIdx.x * kJoinThreads + threadIdx.x; i < A.B * A.N; i += step) {
-            const int b = i / A.N, n = i - b * A.N;
-            if (n < attend_request(A, b, false).rows) continue;
-            uint4* const out = reinterpret_cast<uint4*>(static_cast<char*>(A.out) + (int64_t)i * A.q_heads * A.dim * 2);
-            for (int c = 0; c < vecs; ++c) out[c] = make_uint4(0, 0, 0, 0);
-        }
+    if (tid == 0) {
+        __threadfence();
+        asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(W.flag + blockIdx.x), "r"(plan.call + 1) : "memory");
+        if (*stop != 0 && A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Scratch W = scratch_of(scratch, S.ctas, rows);
-    const Join j = *reinterpret_cast<const Join*>(reinterpret_cast<const char*>(scratch) + blockIdx.x * kJoinBytes);
-    if (j.b < 0) return;
-    const Request R = attend_request(A, j.b, false);
-    const int cuts = j.c1 - j.c0, mine = (int)blockIdx.x - j.c0 - 1;
-    const int quads = A.dim / 4;
-    const int tokens = R.rows - j.rt * S.block < S.block ? R.rows - j.rt * S.block : S.block;
-    const int used = tokens * A.group;  // rows of the item, tile after tile
-    const int all = used * quads;
-    const int lo = (int)((long long)all * mine / cuts), hi = (int)((long long)all * (mine + 1) / cuts);
-    const float4* const sums = reinterpret_cast<const float4*>(W.sums);
-    const int full = S.tok * A.group;  // rows in use of a whole row tile
-    for (int i = lo + threadIdx.x; i < hi; i += kJoinThreads) {
-        const int q = i / used, r = i - q * used;
-        const int row = r < full ? r : kTile + r - full;
-        auto part = [&](int c) { return 2 * c + (c == j.c0 ? j.first : 0); };
-        float top = -INFINITY;
-        for (int c = j.c0; c <= j.c1; ++c) top = fmaxf(top, W.ml[(int64_t)part(c) * rows + row].x);
-        float l = 0.0f;
-        float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-        for (int c = j.c0; c <= j.c1; ++c) {
-            const float2 ml = W.ml[(int64_t)part(c) * rows + row];
-            const float4 x = sums[((int64_t)part(c) * (DP / 4) + q) * rows + row];
-            if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // it saw nothing
-            const float f = exp2_fast(ml.x - top);
-            l = fmaf(ml.y, f, l);
-            o.x = fmaf(x.x, f, o.x);
-            o.y = fmaf(x.y, f, o.y);
-            o.z = fmaf(x.z, f, o.z);
-            o.w = fmaf(x.w, f, o.w);
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int tok = j.rt * S.block + r / A.group, head = j.h * A.group + r % A.group;
-        const int64_t out_row = (PROMPT ? R.base : (int64_t)j.b * A.N) + tok;
-        uint2 y;
-        y.x = pack2<BF16>(o.x * inv, o.y * inv);
-        y.y = pack2<BF16>(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<char*>(A.out) + ((out_row * A.q_heads + head) * A.dim + 4 * q) * 2) = y;
-    }
+    if (*stop != 0 || plan.g0 >= plan.g1) return;
+    const Cuts cuts(plan.all, plan.ctas);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+        if (cut[i].total > 0) join_item<DP, BF16, PROMPT>(A, S, W, plan.call, cuts, cut[i], stop);
 }
 
 // ---------------------------------------------------------------------------
@@ -1008,19 +1048,17 @@ int launch_mma(const Attend& A, const Shape& S, const Maps& M, void* scratch, cu
             return CLK_ECUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    k_attend<DP, BF16, PROMPT><<<S.ctas, kThreads, L::kTotal, s>>>(M, A, S, scratch);
-    int rc = launch_status();
-    if (rc != CLK_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)S.ctas);
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kTotal;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].id = cudaLaunchAttributeCooperative;  // the joins wait on one another
+    attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, k_attend_join<DP, BF16, PROMPT>, A, S, scratch));
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_attend<DP, BF16, PROMPT>, M, A, S, scratch));
 }
 
 bool mma_dim(int32_t dim) { return dim >= 64 && dim <= 128 && dim % 8 == 0; }
@@ -1050,7 +1088,8 @@ size_t attend_mma_scratch(int32_t q_heads, int32_t kv_heads, int32_t dim)
 {
     if (!mma_dim(dim) || q_heads / kv_heads > kTile) return 0;
     const size_t rows = 2 * kTile;
-    return (size_t)num_sms() * (kJoinBytes + 2 * rows * (sizeof(float2) + (size_t)pad_dim(dim) * sizeof(float)));
+    const int n = num_sms();
+    return flag_bytes(n) + (size_t)n * 2 * rows * (sizeof(float2) + (size_t)pad_dim(dim) * sizeof(float));
 }
 
 int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)

@@ -658,8 +658,10 @@ typedef struct clk_attn {
 } clk_attn;
 
 /* Scratch bytes for clk_tree_attend / clk_prompt_attend with these heads and
- * this dim on the current device, for any batch.  16-byte aligned; no
- * initialisation; calls that share it must not overlap on the GPU. */
+ * this dim on the current device, for any batch.  16-byte aligned; zeroed once
+ * before its first use (e.g. clk_verify_scratch_init) and left ready by every
+ * call; calls that share it must not overlap on the GPU.  Zero it again after
+ * a call that failed. */
 CLK_API int clk_attend_scratch_bytes(int32_t q_heads, int32_t kv_heads, int32_t dim, size_t* bytes);
 
 /* Attention of a step's block: request b has d_nodes[b] new tokens (0 .. N,
