@@ -60,7 +60,8 @@ constexpr int kTile = 128;     // keys of a tile, rows of a row tile
 constexpr int kWarps = 12;     // 8 softmax, 1 copies, 1 products, 2 V tiles
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kValueWarp = 10;
-constexpr int kNear = 12;      // requests whose data a CTA keeps
+constexpr int kFlight = 8;     // parts that a join reads at a time
+constexpr int kNear = 4;            // requests whose data a CTA keeps
 
 struct Maps {
     CUtensorMap q, k, v, kc, vc;
@@ -211,40 +212,36 @@ struct Cut {
     long long begin;        // its first one
 };
 
-// The CTA's way through its share, the same in every warp.
+// The CTA's way through its share, the same in every warp.  The softmax
+// warps keep theirs in shared memory: their registers are full.
 template <bool PROMPT>
 struct Walk {
-    const Attend& A;
-    const Shape& S;
-    const Plan& P;
-    const Reach* near;
     Reach x;
     int b, h, item, t0, t1, total, left;  // left: tiles of the share from t0 on
 
-    __device__ Walk(const Attend& a, const Shape& s, const Plan& p, const Reach* n) : A(a), S(s), P(p), near(n)
+    __device__ void start(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
-        left = (int)(p.g1 - p.g0);
-        b = p.b;
-        h = p.h;
-        item = p.item;
+        left = (int)(P.g1 - P.g0);
+        b = P.b;
+        h = P.h;
+        item = P.item;
         if (left > 0) {
-            load();
-            cut(p.t);
+            load(A, S, P, near);
+            cut(S, P.t);
         }
     }
-    __device__ void load()
+    __device__ void load(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
         const int i = b - P.b;
         x = i < kNear ? near[i] : reach_of<PROMPT>(attend_request(A, b, false), S);
     }
-    __device__ void cut(int from)
+    __device__ void cut(const Shape& S, int from)
     {
         total = x.ctx_tiles + new_tiles<PROMPT>(x, S, item);
         t0 = from;
         t1 = total - from < left ? total : from + left;
     }
-    __device__ bool more() const { return left > 0; }
-    __device__ void next()
+    __device__ void next(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
         left -= t1 - t0;
         if (left <= 0) return;
@@ -254,14 +251,14 @@ struct Walk {
                 h = 0;
                 do {
                     ++b;
-                    load();
+                    load(A, S, P, near);
                 } while (x.items == 0);
             }
         }
-        cut(0);
+        cut(S, 0);
     }
     // Tiles [t0, last(s)) of this segment are stream s's, with prompts.
-    __device__ int last(int s) const
+    __device__ int last(const Shape& S, int s) const
     {
         const int first = item * S.block + s * S.tok;
         if (first >= x.rows) return t0;
@@ -276,22 +273,28 @@ struct Lay {
     static constexpr int kHalves = DP / 64;
     static constexpr int kHalf = kTile * 128;  // bytes of 64 columns of a tile
     static constexpr int kBytes = kHalves * kHalf;
-    static constexpr int kQ = PROMPT ? 2 : 1;
-    static constexpr int kK = DP == 128 ? 3 : 6;                   // K tiles in the ring
-    static constexpr int kV = DP == 128 ? (PROMPT ? 2 : 3) : (PROMPT ? 5 : 6);
-    static constexpr int kTiles = kQ + kK + kV;
+    // Rows of 64 leave room in tensor memory for weights beside the scores (two streams of 128 + 64 + 64
+    // columns), so that the next scores are computed while this tile's are exponentiated; with rows of 128
+    // the weights lie over the scores.
+    static constexpr bool kApart = DP == 64;
+    static constexpr int kQ = PROMPT ? 2 : 1;                      // row tiles of an item
+    static constexpr int kQB = DP == 128 ? 1 : 2;                  // items whose Q is held
+    static constexpr int kK = DP == 128 ? 3 : (PROMPT ? 5 : 6);    // K tiles in the ring
+    static constexpr int kV = DP == 128 ? (PROMPT ? 2 : 3) : 5;
+    static constexpr int kTiles = kQ * kQB + kK + kV;
     // after the tiles
     static constexpr int oKFull = kTiles * kBytes, oKEmpty = oKFull + 8 * kK;
     static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
-    static constexpr int oQFull = oVEmpty + 8 * kV, oQEmpty = oQFull + 8;
-    static constexpr int oSFull = oQEmpty + 8, oPReady = oSFull + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
+    static constexpr int oQFull = oVEmpty + 8 * kV, oQEmpty = oQFull + 8 * kQB;
+    static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
     static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
     static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
     static constexpr int oNear = oBad + 16 * kV;                      // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
     static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: where the share begins, where it ends
-    static constexpr int oStop = oCut + 2 * (int)sizeof(Cut), oTmem = oStop + 4;
+    static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[8]
+    static constexpr int oStop = oWalk + 8 * (int)sizeof(Walk<PROMPT>), oTmem = oStop + 4;
     static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;          // float2[2][128] for trees
     static constexpr int kTotal = oStat + (PROMPT ? 0 : 2 * kTile * 8);
     static_assert(kTotal <= 232448, "shared memory");
@@ -335,23 +338,37 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
     for (int i = lo + tid; i < hi; i += kThreads) {
         const int q = i / used, r = i - q * used;
         const int row = r < full ? r : kTile + r - full;
-        // The running reference keeps the order of the parts and reads each once.
+        // In the order of the parts, eight parts' loads in flight.
         float top = -INFINITY, l = 0.0f;
         float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int c = 0; c < parts; ++c) {
-            const int64_t at = part(c);
-            const float2 ml = __ldcg(W.ml + at * rows + row);
-            const float4 v = __ldcg(sums + (at * (DP / 4) + q) * rows + row);
-            if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // it saw nothing
-            const float to = fmaxf(top, ml.x);
-            const float f = top == -INFINITY ? 0.0f : exp2_fast(top - to), g = exp2_fast(ml.x - to);
+        for (int c = 0; c < parts; c += kFlight) {
+            float2 ml[kFlight];
+            float4 v[kFlight];
+#pragma unroll
+            for (int e = 0; e < kFlight; ++e) {
+                // past the end the last part is read again, with no weight
+                const int64_t at = part(c + e < parts ? c + e : parts - 1);
+                ml[e] = __ldcg(W.ml + at * rows + row);
+                v[e] = __ldcg(sums + (at * (DP / 4) + q) * rows + row);
+            }
+            float to = top;
+#pragma unroll
+            for (int e = 0; e < kFlight; ++e) to = fmaxf(to, ml[e].x);
+            const float f = top == -INFINITY ? 0.0f : exp2_fast(top - to);
             top = to;
-            l = l * f + ml.y * g;
-            o.x = o.x * f + v.x * g;
-            o.y = o.y * f + v.y * g;
-            o.z = o.z * f + v.z * g;
-            o.w = o.w * f + v.w * g;
+            l *= f;
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+            for (int e = 0; e < kFlight; ++e) {
+                // a part that saw nothing has no weight (and its reference is -inf)
+                const bool use = c + e < parts && !(ml[e].x == -INFINITY && ml[e].y == 0.0f);
+                const float g = exp2_fast(ml[e].x - to);
+                l += use ? ml[e].y * g : 0.0f;
+                o.x += use ? v[e].x * g : 0.0f;
+                o.y += use ? v[e].y * g : 0.0f;
+                o.z += use ? v[e].z * g : 0.0f;
+                o.w += use ? v[e].w * g : 0.0f;
+            }
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int tok = cut.item * S.block + r / A.group, head = cut.h * A.group + r % A.group;
@@ -379,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     volatile uint32_t* const bad = reinterpret_cast<volatile uint32_t*>(sm + L::oBad);
     const Scratch W = scratch_of(scratch, S.ctas, PROMPT ? 2 * kTile : kTile);
 
+    const uint32_t call = tid == 0 ? __ldcg(W.flag + blockIdx.x) : 0;
     // ---- Start: tensor memory, barriers and descriptors, while the requests' data is on its way. ----
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::oTmem) : "memory");
@@ -396,10 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             bar_init(base + L::oVReady + 8 * i, 2);
             bar_init(base + L::oVEmpty + 8 * i, 1);
         }
-        bar_init(base + L::oQFull, 1);
-        bar_init(base + L::oQEmpty, 1);
+        for (int i = 0; i < L::kQB; ++i) {
+            bar_init(base + L::oQFull + 8 * i, 1);
+            bar_init(base + L::oQEmpty + 8 * i, 1);
+        }
         for (int i = 0; i < 2; ++i) {
             bar_init(base + L::oSFull + 8 * i, 1);
+            bar_init(base + L::oSFree + 8 * i, 4);
             bar_init(base + L::oPHalf + 8 * i, 4);
             bar_init(base + L::oPReady + 8 * i, 4);
             bar_init(base + L::oODone + 8 * i, 1);
@@ -414,6 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         long long* const sums = reinterpret_cast<long long*>(sm);  // the rings are not in use yet
         const bool once = A.B <= kThreads;  // the batch is seen in one pass
         long long all = 0;
+        int ctas = 0;
+        Cuts cuts(0, 0);
         Reach x{};
         for (int pass = 0;; ++pass) {
             long long before = 0;
@@ -440,8 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 if (once) all = before;
                 if (once || pass == 1) {
                     // The warp that has the share's first request finds the place in it.
-                    const int ctas = all < S.ctas ? (int)all : S.ctas;
-                    const long long g0 = (int)blockIdx.x < ctas ? Cuts(all, ctas).begin(blockIdx.x) : all;
+                    if (at == 0) {
+                        ctas = all < S.ctas ? (int)all : S.ctas;
+                        cuts = Cuts(all, ctas);
+                    }
+                    const long long g0 = (int)blockIdx.x < ctas ? cuts.begin(blockIdx.x) : all;
                     const unsigned who = __ballot_sync(0xffffffffu, u > 0 && mine <= g0 && g0 < mine + u);
                     if (who != 0) {
                         const int src = __ffs((int)who) - 1;
@@ -479,15 +505,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             if (pass == 0) all = before;
             if (once || pass == 1) break;
         }
-        const int ctas = all < S.ctas ? (int)all : S.ctas;
-        const Cuts cuts(all, ctas);
         const bool busy = (int)blockIdx.x < ctas;
         if (tid == 0) {
             plan.all = all;
             plan.ctas = ctas;
             plan.g0 = busy ? cuts.begin(blockIdx.x) : all;
             plan.g1 = busy ? cuts.begin(blockIdx.x + 1) : all;
-            plan.call = __ldcg(W.flag + blockIdx.x);
+            plan.call = call;
             *stop = 0;
             cut[0].total = cut[1].total = 0;
         }
@@ -505,8 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     __syncthreads();
     tmem_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::oTmem);
-    const uint32_t qs = base, ks = base + L::kQ * L::kBytes, vs = ks + L::kK * L::kBytes;
-    Walk<PROMPT> w(A, S, plan, near);
+    const uint32_t qs = base, ks = base + L::kQ * L::kQB * L::kBytes, vs = ks + L::kK * L::kBytes;
 
     // Registers: 384 threads x 168 at launch; 256 x 208 + 128 x 80 after the split.
     if (warp < kCopyWarp) {
@@ -514,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         // ---- Softmax: a thread per row. ----
         const int s = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-        const uint32_t tS = lanes + 128 * s, tO = lanes + 256 + s * DP;
+        const uint32_t tS = lanes + 128 * s, tO = lanes + 256 + s * DP, tP = L::kApart ? lanes + 384 + 64 * s : tS;
         const int tk = row / A.group, g = row - tk * A.group;  // token of the row tile, head of the group
         const float cs = S.log2_scale;
         constexpr float lift = BF16 ? 0.0f : 7.0f;
@@ -522,20 +545,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         uint32_t sp = 0, od = 0;
         int gi = 0;
         bool ok = true;
-        for (; ok && w.more(); w.next()) {
-            const int len = w.t1 - w.t0;
-            const int mine = PROMPT ? w.last(s) - w.t0 : (len + 1 - s) / 2;
-            const int token = w.item * S.block + (PROMPT ? s * S.tok : 0) + tk;
+        Walk<PROMPT>& w = reinterpret_cast<Walk<PROMPT>*>(sm + L::oWalk)[warp];
+        if (lane == 0) w.start(A, S, plan, near);
+        __syncwarp();
+        while (ok && w.left > 0) {
+            const int len = w.t1 - w.t0, t0 = w.t0;
+            const int mine = PROMPT ? w.last(S, s) - t0 : (len + 1 - s) / 2;
+            const int first = w.item * S.block + (PROMPT ? s * S.tok : 0);  // first token of the row tile
+            const int token = first + tk;
+            const int ctx = w.x.ctx, ctx_tiles = w.x.ctx_tiles;
             const bool real = tk < S.tok && token < w.x.rows;
             unsigned long long seen = 0;
-            if (!PROMPT && real && w.t1 > w.x.ctx_tiles) {
+            if (!PROMPT && real && w.t1 > ctx_tiles) {
                 seen = (unsigned long long)A.mask[(int64_t)w.b * A.N + token];
                 if (w.x.rows < 64) seen &= (1ull << w.x.rows) - 1;
             }
             float ref = -INFINITY, sum = 0.0f;
             for (int j = 0; j < mine; ++j) {
                 const int jj = PROMPT ? j : 2 * j + s;
-                const int t = w.t0 + jj;
+                const int t = t0 + jj;
                 if (!(ok = warp_wait(base + L::oSFull + 8 * s, sp, stop))) break;
                 sp ^= 1;
                 tmem_after();
@@ -545,12 +573,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 tmem_load_wait();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_loaded(x + 32 * c);
+                if (L::kApart) {
+                    tmem_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(base + L::oSFree + 8 * s);
+                }
                 // Hidden keys: a limit for most tiles, a mask for a tree's.
-                const bool cached = t < w.x.ctx_tiles;
-                const int n0 = (t - w.x.ctx_tiles) * kTile;
-                const int first = w.item * S.block + (PROMPT ? s * S.tok : 0);
+                const bool cached = t < ctx_tiles;
+                const int n0 = (t - ctx_tiles) * kTile;
                 if (cached || PROMPT) {
-                    const int most = cached ? w.x.ctx - t * kTile : n0 + kTile - 1 > first ? token - n0 + 1 : kTile;
+                    const int most = cached ? ctx - t * kTile : n0 + kTile - 1 > first ? token - n0 + 1 : kTile;
                     if (!cached ? n0 + kTile - 1 > first : most < kTile) {
 #pragma unroll
                         for (int c = 0; c < kTile; ++c)
@@ -570,6 +602,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     for (int e = 0; e < 4; ++e)
                         m[e] = max3(m[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
                 const float top = max3(m[0], m[1], fmaxf(m[2], m[3]));
+                if (L::kApart && j > 0) {
+                    // this stream's last product is done with O and the weights
+                    if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
+                    od ^= 1;
+                    tmem_after();
+                }
                 const bool grow = top > ref + slack || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float to = grow ? top : ref;
@@ -577,7 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     ref = to;
                     sum *= fix;
                     if (j > 0) {
-                        // The scores' product was issued after this stream's last P V, so O is complete.
+                        // O is complete: weights over the scores mean that these scores' product was issued after
+                        // this stream's last P V; else it was waited for.
 #pragma unroll
                         for (int c = 0; c < DP / 16; ++c) {
                             uint32_t o[16];
@@ -605,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
                         y[e] = pack2<BF16>(p0, p1);
                     }
-                    tmem_store16(tS + 16 * c, y);
+                    tmem_store16(tP + 16 * c, y);
                     if (c == 1) {
                         tmem_store_wait();
                         tmem_before();
@@ -615,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 }
                 const float2 both = unpair(add2(part[0], part[1]));
                 sum += both.x + both.y;
-                if (!cached && (!PROMPT || n0 + kTile - 1 > w.item * S.block)) {
+                if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
                     // Rows of V that were not finite: NaN for those who see them.
                     const int vi = (gi + jj) % L::kV;
                     if (!(ok = warp_wait(base + L::oVReady + 8 * vi, (uint32_t)((gi + jj) / L::kV & 1), stop))) break;
@@ -731,8 +770,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 if (!(ok = warp_wait(base + L::oStatReady, 1, stop))) break;
             }
             gi += len;
+            __syncwarp();
+            if (lane == 0) w.next(A, S, plan, near);
+            __syncwarp();
         }
     } else {
+        Walk<PROMPT> w;
+        w.start(A, S, plan, near);
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == kCopyWarp) {
             // ---- Copies. ----
@@ -740,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             bool ok = (base & 1023) == 0;  // the swizzle's period
             if (!ok) *stop = 1;
             const int pages = kTile >> A.C.shift;  // of a tile
-            for (; ok && w.more(); w.next(), ++seg) {
+            for (; ok && w.left > 0; w.next(A, S, plan, near), ++seg) {
                 const int32_t* const table = w.x.slot >= 0 ? A.C.table + (int64_t)w.x.slot * A.C.max_pages : nullptr;
                 auto page_of = [&](int t) {
                     const int64_t p = (int64_t)t * pages + lane;
@@ -753,17 +797,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     return page;
                 };
                 int page = page_of(w.t0);
-                if (!(ok = warp_wait(base + L::oQEmpty, (seg & 1) ^ 1, stop))) break;
+                const int qi = seg % L::kQB;
+                if (!(ok = warp_wait(base + L::oQEmpty + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop))) break;
                 ++nq;
                 const int tok = w.item * S.block;
                 const int z = PROMPT ? 0 : w.b;
                 const int row0 = PROMPT ? w.x.base : 0;
                 if (lane == 0) {
-                    bar_expect(base + L::oQFull, (uint32_t)(L::kQ * L::kHalves) * (uint32_t)(S.qbox * A.group) * 128u);
+                    bar_expect(base + L::oQFull + 8 * qi, (uint32_t)(L::kQ * L::kHalves) * (uint32_t)(S.qbox * A.group) * 128u);
                     for (int s = 0; s < L::kQ; ++s)
                         for (int hf = 0; hf < L::kHalves; ++hf)
-                            copy_box(qs + s * L::kBytes + hf * L::kHalf, &M.q, 64 * hf, w.h * A.group, row0 + tok + s * S.tok, z,
-                                     base + L::oQFull);
+                            copy_box(qs + (qi * L::kQ + s) * L::kBytes + hf * L::kHalf, &M.q, 64 * hf, w.h * A.group,
+                                     row0 + tok + s * S.tok, z, base + L::oQFull + 8 * qi);
                 }
                 for (int t = w.t0; t < w.t1; ++t, ++i) {
                     const int next = page_of(t + 1);
@@ -806,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 auto drain = [&](uint32_t bar, uint32_t parity) {
                     while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {}
                 };
-                if (nq > 0) drain(base + L::oQFull, (uint32_t)(nq - 1) & 1);
+                for (int j = nq > L::kQB ? nq - L::kQB : 0; j < nq; ++j) drain(base + L::oQFull + 8 * (j % L::kQB), (uint32_t)(j / L::kQB & 1));
                 for (int j = nk > L::kK ? nk - L::kK : 0; j < nk; ++j) drain(base + L::oKFull + 8 * (j % L::kK), (uint32_t)(j / L::kK & 1));
                 for (int j = nv > L::kV ? nv - L::kV : 0; j < nv; ++j) drain(base + L::oVFull + 8 * (j % L::kV), (uint32_t)(j / L::kV & 1));
             }
@@ -820,13 +865,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 constexpr uint32_t types = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((kTile >> 4) << 24);
                 constexpr uint32_t kind_s = types | ((kTile >> 3) << 17);
                 constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
-                uint32_t ps[2] = {0, 0};  // phases of PReady
+                uint32_t ps[2] = {0, 0}, fs[2] = {1, 1};  // phases of PReady and SFree
                 int gi = 0, seg = 0;
                 bool ok = true;
                 // descriptors count in 16 bytes
                 const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, L::kHalf);
                 auto scores = [&](int s, int tile) {
-                    const uint64_t q = q0 + (PROMPT ? s * (L::kBytes / 16) : 0), k = k0 + tile % L::kK * (L::kBytes / 16);
+                    if (L::kApart) {
+                        if (!warp_wait(base + L::oSFree + 8 * s, fs[s], stop)) return false;
+                        fs[s] ^= 1;
+                        tmem_after();
+                    }
+                    const uint64_t q = q0 + (seg % L::kQB * L::kQ + (PROMPT ? s : 0)) * (L::kBytes / 16), k = k0 + tile % L::kK * (L::kBytes / 16);
 #pragma unroll
                     for (int e = 0; e < DP / 16; ++e) {
                         constexpr int next = L::kHalf / 16;
@@ -834,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         mma_ss(lead, tm + 128 * s, q + at, k + at, kind_s, e > 0);
                     }
                     mma_commit(lead, base + L::oSFull + 8 * s);
+                    return true;
                 };
                 // Both halves of a tile's weights; the V tile is there.
                 auto values = [&](int s, int tile, bool add) {
@@ -844,9 +895,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                             if (!warp_wait(base + (e == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
                             tmem_after();
                         }
-                        mma_ts(lead, tm + 256 + s * DP, tm + 128 * s + 8 * e, v + 128 * e, kind_o, add || e > 0);
+                        mma_ts(lead, tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * e, v + 128 * e, kind_o,
+                               add || e > 0);
                     }
                     ps[s] ^= 1;
+                    if (L::kApart) mma_commit(lead, base + L::oODone + 8 * s);
                     return true;
                 };
                 auto wait_v = [&](int tile) {
@@ -855,56 +908,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 auto wait_k = [&](int tile) {
                     return warp_wait(base + L::oKFull + 8 * (tile % L::kK), (uint32_t)(tile / L::kK & 1), stop);
                 };
-                for (; ok; w.next(), ++seg) {
-                    const int len = same(w.more() ? w.t1 - w.t0 : 0);
+                for (; ok; w.next(A, S, plan, near), ++seg) {
+                    const int len = same(w.left > 0 ? w.t1 - w.t0 : 0);
                     if (len == 0) break;
-                    if (!(ok = warp_wait(base + L::oQFull, seg & 1, stop))) break;
+                    if (!(ok = warp_wait(base + L::oQFull + 8 * (seg % L::kQB), (uint32_t)(seg / L::kQB & 1), stop))) break;
                     tmem_after();
                     if (PROMPT) {
-                        const int n[2] = {same(w.last(0) - w.t0), same(w.last(1) - w.t0)};
+                        const int n[2] = {same(w.last(S, 0) - w.t0), same(w.last(S, 1) - w.t0)};
                         if (!(ok = wait_k(gi))) break;
                         tmem_after();
 #pragma unroll
                         for (int s = 0; s < 2; ++s)
-                            if (n[s] > 0) scores(s, gi);
+                            if (ok && n[s] > 0) ok = scores(s, gi);
+                        if (!ok) break;
                         mma_commit(lead, base + L::oKEmpty + 8 * (gi % L::kK));
-                        if (len == 1) mma_commit(lead, base + L::oQEmpty);
+                        if (len == 1) mma_commit(lead, base + L::oQEmpty + 8 * (seg % L::kQB));
                         for (int j = 0; ok && j < len; ++j) {
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
-                                if (!ok || j >= n[s]) continue;
-                                if (!(ok = wait_v(gi + j) && values(s, gi + j, j > 0))) continue;
-                                if (j + 1 == n[s]) mma_commit(lead, base + L::oODone + 8 * s);
-                                if (j + 1 < n[s]) {
-                                    if (!(ok = wait_k(gi + j + 1))) continue;
+                                auto ahead = [&] {
+                                    if (j + 1 >= n[s]) return true;
+                                    if (!wait_k(gi + j + 1)) return false;
                                     tmem_after();
-                                    scores(s, gi + j + 1);
+                                    return scores(s, gi + j + 1);
+                                };
+                                if (!ok || j >= n[s]) continue;
+                                if (L::kApart && !(ok = ahead())) continue;
+                                if (!(ok = wait_v(gi + j) && values(s, gi + j, j > 0))) continue;
+                                if (!L::kApart) {
+                                    if (j + 1 == n[s]) mma_commit(lead, base + L::oODone + 8 * s);
+                                    ok = ahead();
                                 }
                             }
                             if (!ok) break;
                             mma_commit(lead, base + L::oVEmpty + 8 * ((gi + j) % L::kV));
                             if (j + 1 < len) mma_commit(lead, base + L::oKEmpty + 8 * ((gi + j + 1) % L::kK));
-                            if (j + 2 == len) mma_commit(lead, base + L::oQEmpty);
+                            if (j + 2 == len) mma_commit(lead, base + L::oQEmpty + 8 * (seg % L::kQB));
                         }
                     } else {
-                        for (int j = 0; ok && j < 2 && j < len; ++j) {
-                            if (!(ok = wait_k(gi + j))) break;
+                        auto ahead = [&](int j) {
+                            if (j >= len) return true;
+                            if (!wait_k(gi + j)) return false;
                             tmem_after();
-                            scores(j, gi + j);
+                            if (!scores(j & 1, gi + j)) return false;
                             mma_commit(lead, base + L::oKEmpty + 8 * ((gi + j) % L::kK));
-                        }
-                        if (ok && len <= 2) mma_commit(lead, base + L::oQEmpty);
+                            if (j + 1 == len) mma_commit(lead, base + L::oQEmpty + 8 * (seg % L::kQB));
+                            return true;
+                        };
+                        ok = ahead(0) && ahead(1);
                         for (int j = 0; ok && j < len; ++j) {
                             const int s = j & 1;
+                            if (L::kApart && !(ok = ahead(j + 2))) break;
                             if (!(ok = wait_v(gi + j) && values(s, gi + j, j >= 2))) break;
                             mma_commit(lead, base + L::oVEmpty + 8 * ((gi + j) % L::kV));
-                            if (j + 2 >= len) mma_commit(lead, base + L::oODone + 8 * s);
-                            if (j + 2 < len) {
-                                if (!(ok = wait_k(gi + j + 2))) break;
-                                tmem_after();
-                                scores(s, gi + j + 2);
-                                mma_commit(lead, base + L::oKEmpty + 8 * ((gi + j + 2) % L::kK));
-                                if (j + 3 == len) mma_commit(lead, base + L::oQEmpty);
+                            if (!L::kApart) {
+                                if (j + 2 >= len) mma_commit(lead, base + L::oODone + 8 * s);
+                                ok = ahead(j + 2);
                             }
                         }
                     }
@@ -933,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             }
             int i = 0;
             bool ok = true;
-            for (; ok && w.more(); w.next()) {
+            for (; ok && w.left > 0; w.next(A, S, plan, near)) {
                 for (int t = w.t0; t < w.t1; ++t, ++i) {
                     const int vi = i % L::kV;
                     if (!(ok = warp_wait(base + L::oVFull + 8 * vi, (uint32_t)(i / L::kV & 1), stop))) break;
@@ -985,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
     if (tid == 0) {
-        __threadfence();
+        // after the barrier above, the release covers the whole CTA's parts
         asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(W.flag + blockIdx.x), "r"(plan.call + 1) : "memory");
         if (*stop != 0 && A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
     }
