@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         y[e] = pack2<BF16>(p0, p1);
                     }
                     tmem_store16(tP + 16 * c, y);
-                    if (c == 1) {
+                    if (c == 1 && !L::kApart) {
                         tmem_store_wait();
                         tmem_before();
                         __syncwarp();
@@ -866,17 +866,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 constexpr uint32_t kind_s = types | ((kTile >> 3) << 17);
                 constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
                 uint32_t ps[2] = {0, 0}, fs[2] = {1, 1};  // phases of PReady and SFree
-                int gi = 0, seg = 0;
+                int seg = 0, qi = 0;
+                uint32_t qp = 0;
                 bool ok = true;
+                // This warp's instructions bound the rate at which short products follow one another: ring places
+                // and phases are counted along, and a tile is waited for once for both streams.
+                int ki = 0, vi = 0;
+                uint32_t kp = 0, vp = 0;
+                auto step = [](int& i, uint32_t& phase, int n) {
+                    if (++i == n) {
+                        i = 0;
+                        phase ^= 1;
+                    }
+                };
                 // descriptors count in 16 bytes
                 const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, L::kHalf);
-                auto scores = [&](int s, int tile) {
+                auto wait_k = [&] { return warp_wait(base + L::oKFull + 8 * ki, kp, stop); };
+                auto wait_v = [&] { return warp_wait(base + L::oVReady + 8 * vi, vp, stop); };
+                // Stream s's scores with K tile ki.
+                auto scores = [&](int s) {
                     if (L::kApart) {
                         if (!warp_wait(base + L::oSFree + 8 * s, fs[s], stop)) return false;
                         fs[s] ^= 1;
-                        tmem_after();
                     }
-                    const uint64_t q = q0 + (seg % L::kQB * L::kQ + (PROMPT ? s : 0)) * (L::kBytes / 16), k = k0 + tile % L::kK * (L::kBytes / 16);
+                    tmem_after();
+                    const uint64_t q = q0 + (qi * L::kQ + (PROMPT ? s : 0)) * (L::kBytes / 16), k = k0 + ki * (L::kBytes / 16);
 #pragma unroll
                     for (int e = 0; e < DP / 16; ++e) {
                         constexpr int next = L::kHalf / 16;
@@ -886,88 +900,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     mma_commit(lead, base + L::oSFull + 8 * s);
                     return true;
                 };
-                // Both halves of a tile's weights; the V tile is there.
-                auto values = [&](int s, int tile, bool add) {
-                    const uint64_t v = v0 + tile % L::kV * (L::kBytes / 16);
+                // Stream s's weights with V tile vi.  Where the weights lie over the scores, the chain of one stream
+                // is what counts, and their first half's product does not wait for the second.
+                auto values = [&](int s, bool add) {
+                    const uint64_t v = v0 + vi * (L::kBytes / 16);
 #pragma unroll
                     for (int e = 0; e < kTile / 16; ++e) {
-                        if (e % 4 == 0) {
-                            if (!warp_wait(base + (e == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
+                        if (e == 0 || (e == 4 && !L::kApart)) {
+                            if (!warp_wait(base + (e == 0 && !L::kApart ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
                             tmem_after();
                         }
                         mma_ts(lead, tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * e, v + 128 * e, kind_o,
                                add || e > 0);
                     }
                     ps[s] ^= 1;
-                    if (L::kApart) mma_commit(lead, base + L::oODone + 8 * s);
                     return true;
-                };
-                auto wait_v = [&](int tile) {
-                    return warp_wait(base + L::oVReady + 8 * (tile % L::kV), (uint32_t)(tile / L::kV & 1), stop);
-                };
-                auto wait_k = [&](int tile) {
-                    return warp_wait(base + L::oKFull + 8 * (tile % L::kK), (uint32_t)(tile / L::kK & 1), stop);
                 };
                 for (; ok; w.next(A, S, plan, near), ++seg) {
                     const int len = same(w.left > 0 ? w.t1 - w.t0 : 0);
                     if (len == 0) break;
-                    if (!(ok = warp_wait(base + L::oQFull + 8 * (seg % L::kQB), (uint32_t)(seg / L::kQB & 1), stop))) break;
-                    tmem_after();
+                    if (!(ok = warp_wait(base + L::oQFull + 8 * qi, qp, stop))) break;
                     if (PROMPT) {
                         const int n[2] = {same(w.last(S, 0) - w.t0), same(w.last(S, 1) - w.t0)};
-                        if (!(ok = wait_k(gi))) break;
-                        tmem_after();
+                        if (!(ok = wait_k())) break;
 #pragma unroll
                         for (int s = 0; s < 2; ++s)
-                            if (ok && n[s] > 0) ok = scores(s, gi);
+                            if (ok && n[s] > 0) ok = scores(s);
                         if (!ok) break;
-                        mma_commit(lead, base + L::oKEmpty + 8 * (gi % L::kK));
-                        if (len == 1) mma_commit(lead, base + L::oQEmpty + 8 * (seg % L::kQB));
-                        for (int j = 0; ok && j < len; ++j) {
+                        mma_commit(lead, base + L::oKEmpty + 8 * ki);
+                        step(ki, kp, L::kK);
+                        if (len == 1) mma_commit(lead, base + L::oQEmpty + 8 * qi);
+                        for (int j = 0; j < len; ++j) {
+                            const bool more = j + 1 < len;
+                            if (L::kApart && more && !(ok = wait_k())) break;
+                            if (!(ok = wait_v())) break;
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
-                                auto ahead = [&] {
-                                    if (j + 1 >= n[s]) return true;
-                                    if (!wait_k(gi + j + 1)) return false;
-                                    tmem_after();
-                                    return scores(s, gi + j + 1);
-                                };
-                                if (!ok || j >= n[s]) continue;
-                                if (L::kApart && !(ok = ahead())) continue;
-                                if (!(ok = wait_v(gi + j) && values(s, gi + j, j > 0))) continue;
-                                if (!L::kApart) {
-                                    if (j + 1 == n[s]) mma_commit(lead, base + L::oODone + 8 * s);
-                                    ok = ahead();
+                                if (!ok) continue;
+                                if (L::kApart && j + 1 < n[s]) ok = scores(s);
+                                if (ok && j < n[s]) {
+                                    ok = values(s, j > 0);
+                                    if (ok && (L::kApart || j + 1 == n[s])) mma_commit(lead, base + L::oODone + 8 * s);
+                                }
+                                if (!L::kApart && ok && more) {
+                                    if (s == 0) ok = wait_k();
+                                    if (ok && j + 1 < n[s]) ok = scores(s);
                                 }
                             }
                             if (!ok) break;
-                            mma_commit(lead, base + L::oVEmpty + 8 * ((gi + j) % L::kV));
-                            if (j + 1 < len) mma_commit(lead, base + L::oKEmpty + 8 * ((gi + j + 1) % L::kK));
-                            if (j + 2 == len) mma_commit(lead, base + L::oQEmpty + 8 * (seg % L::kQB));
+                            mma_commit(lead, base + L::oVEmpty + 8 * vi);
+                            step(vi, vp, L::kV);
+                            if (more) {
+                                mma_commit(lead, base + L::oKEmpty + 8 * ki);
+                                step(ki, kp, L::kK);
+                            }
+                            if (j + 2 == len) mma_commit(lead, base + L::oQEmpty + 8 * qi);
                         }
                     } else {
                         auto ahead = [&](int j) {
                             if (j >= len) return true;
-                            if (!wait_k(gi + j)) return false;
-                            tmem_after();
-                            if (!scores(j & 1, gi + j)) return false;
-                            mma_commit(lead, base + L::oKEmpty + 8 * ((gi + j) % L::kK));
-                            if (j + 1 == len) mma_commit(lead, base + L::oQEmpty + 8 * (seg % L::kQB));
+                            if (!wait_k() || !scores(j & 1)) return false;
+                            mma_commit(lead, base + L::oKEmpty + 8 * ki);
+                            step(ki, kp, L::kK);
+                            if (j + 1 == len) mma_commit(lead, base + L::oQEmpty + 8 * qi);
                             return true;
                         };
                         ok = ahead(0) && ahead(1);
                         for (int j = 0; ok && j < len; ++j) {
                             const int s = j & 1;
                             if (L::kApart && !(ok = ahead(j + 2))) break;
-                            if (!(ok = wait_v(gi + j) && values(s, gi + j, j >= 2))) break;
-                            mma_commit(lead, base + L::oVEmpty + 8 * ((gi + j) % L::kV));
-                            if (!L::kApart) {
-                                if (j + 2 >= len) mma_commit(lead, base + L::oODone + 8 * s);
-                                ok = ahead(j + 2);
-                            }
+                            if (!(ok = wait_v() && values(s, j >= 2))) break;
+                            if (L::kApart || j + 2 >= len) mma_commit(lead, base + L::oODone + 8 * s);
+                            mma_commit(lead, base + L::oVEmpty + 8 * vi);
+                            step(vi, vp, L::kV);
+                            if (!L::kApart) ok = ahead(j + 2);
                         }
                     }
-                    gi += len;
+                    step(qi, qp, L::kQB);
                 }
                 if (!ok) {
                     // Products in flight end before tensor memory is given up.
