@@ -860,7 +860,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             {
                 // Shuffled values are the same in every lane for the compiler too.
                 auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-                const uint32_t lead = lane == 0;
                 const uint32_t tm = (uint32_t)same((int)tmem);
                 constexpr uint32_t types = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((kTile >> 4) << 24);
                 constexpr uint32_t kind_s = types | ((kTile >> 3) << 17);
@@ -879,6 +878,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         phase ^= 1;
                     }
                 };
+                auto done = [](uint32_t bar) {
+                    if (elect()) mma_commit(bar);
+                    __syncwarp();
+                };
                 // descriptors count in 16 bytes
                 const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, L::kHalf);
                 auto wait_k = [&] { return warp_wait(base + L::oKFull + 8 * ki, kp, stop); };
@@ -891,27 +894,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     }
                     tmem_after();
                     const uint64_t q = q0 + (qi * L::kQ + (PROMPT ? s : 0)) * (L::kBytes / 16), k = k0 + ki * (L::kBytes / 16);
+                    if (elect()) {
 #pragma unroll
-                    for (int e = 0; e < DP / 16; ++e) {
-                        constexpr int next = L::kHalf / 16;
-                        const int at = (e / 4) * next + (e % 4) * 2;
-                        mma_ss(lead, tm + 128 * s, q + at, k + at, kind_s, e > 0);
+                        for (int e = 0; e < DP / 16; ++e) {
+                            constexpr int next = L::kHalf / 16;
+                            const int at = (e / 4) * next + (e % 4) * 2;
+                            mma_ss(tm + 128 * s, q + at, k + at, kind_s, e > 0);
+                        }
+                        mma_commit(base + L::oSFull + 8 * s);
                     }
-                    mma_commit(lead, base + L::oSFull + 8 * s);
+                    __syncwarp();
                     return true;
                 };
                 // Stream s's weights with V tile vi.  Where the weights lie over the scores, the chain of one stream
                 // is what counts, and their first half's product does not wait for the second.
                 auto values = [&](int s, bool add) {
                     const uint64_t v = v0 + vi * (L::kBytes / 16);
+                    constexpr int steps = L::kApart ? 8 : 4;  // 16 keys each
 #pragma unroll
-                    for (int e = 0; e < kTile / 16; ++e) {
-                        if (e == 0 || (e == 4 && !L::kApart)) {
-                            if (!warp_wait(base + (e == 0 && !L::kApart ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
-                            tmem_after();
+                    for (int part = 0; part < 8; part += steps) {
+                        if (!warp_wait(base + (part + steps < 8 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
+                        tmem_after();
+                        if (elect()) {
+#pragma unroll
+                            for (int e = part; e < part + steps; ++e)
+                                mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * e, v + 128 * e, kind_o,
+                                       add || e > 0);
                         }
-                        mma_ts(lead, tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * e, v + 128 * e, kind_o,
-                               add || e > 0);
+                        __syncwarp();
                     }
                     ps[s] ^= 1;
                     return true;
@@ -927,9 +937,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         for (int s = 0; s < 2; ++s)
                             if (ok && n[s] > 0) ok = scores(s);
                         if (!ok) break;
-                        mma_commit(lead, base + L::oKEmpty + 8 * ki);
+                        done(base + L::oKEmpty + 8 * ki);
                         step(ki, kp, L::kK);
-                        if (len == 1) mma_commit(lead, base + L::oQEmpty + 8 * qi);
+                        if (len == 1) done(base + L::oQEmpty + 8 * qi);
                         for (int j = 0; j < len; ++j) {
                             const bool more = j + 1 < len;
                             if (L::kApart && more && !(ok = wait_k())) break;
@@ -940,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                                 if (L::kApart && j + 1 < n[s]) ok = scores(s);
                                 if (ok && j < n[s]) {
                                     ok = values(s, j > 0);
-                                    if (ok && (L::kApart || j + 1 == n[s])) mma_commit(lead, base + L::oODone + 8 * s);
+                                    if (ok && (L::kApart || j + 1 == n[s])) done(base + L::oODone + 8 * s);
                                 }
                                 if (!L::kApart && ok && more) {
                                     if (s == 0) ok = wait_k();
@@ -948,21 +958,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                                 }
                             }
                             if (!ok) break;
-                            mma_commit(lead, base + L::oVEmpty + 8 * vi);
+                            done(base + L::oVEmpty + 8 * vi);
                             step(vi, vp, L::kV);
                             if (more) {
-                                mma_commit(lead, base + L::oKEmpty + 8 * ki);
+                                done(base + L::oKEmpty + 8 * ki);
                                 step(ki, kp, L::kK);
                             }
-                            if (j + 2 == len) mma_commit(lead, base + L::oQEmpty + 8 * qi);
+                            if (j + 2 == len) done(base + L::oQEmpty + 8 * qi);
                         }
                     } else {
                         auto ahead = [&](int j) {
                             if (j >= len) return true;
                             if (!wait_k() || !scores(j & 1)) return false;
-                            mma_commit(lead, base + L::oKEmpty + 8 * ki);
+                            done(base + L::oKEmpty + 8 * ki);
                             step(ki, kp, L::kK);
-                            if (j + 1 == len) mma_commit(lead, base + L::oQEmpty + 8 * qi);
+                            if (j + 1 == len) done(base + L::oQEmpty + 8 * qi);
                             return true;
                         };
                         ok = ahead(0) && ahead(1);
@@ -970,8 +980,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                             const int s = j & 1;
                             if (L::kApart && !(ok = ahead(j + 2))) break;
                             if (!(ok = wait_v() && values(s, j >= 2))) break;
-                            if (L::kApart || j + 2 >= len) mma_commit(lead, base + L::oODone + 8 * s);
-                            mma_commit(lead, base + L::oVEmpty + 8 * vi);
+                            if (L::kApart || j + 2 >= len) done(base + L::oODone + 8 * s);
+                            done(base + L::oVEmpty + 8 * vi);
                             step(vi, vp, L::kV);
                             if (!L::kApart) ok = ahead(j + 2);
                         }
@@ -980,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 }
                 if (!ok) {
                     // Products in flight end before tensor memory is given up.
-                    mma_commit(lead, base + L::oDrain);
+                    done(base + L::oDrain);
                     const long long t0 = clock64();
                     while (!bar_try(base + L::oDrain, 0) && clock64() - t0 < kWaitClocks) {}
                 }

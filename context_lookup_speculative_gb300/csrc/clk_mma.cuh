@@ -80,35 +80,42 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t next)
            (1ull << 46) | (2ull << 61);
 }
 
-// D[tmem] (+)= A[smem] B[smem], issued by the lane whose `lead` is set: the
-// whole warp comes here, so that the operands can live in uniform registers.
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t kind, uint32_t add)
+// One lane of a converged warp, always the same one.  Products are issued
+// inside `if (elect())`: the compiler knows that one thread runs there and
+// keeps their operands in uniform registers.  (With a lane's own predicate on
+// each product an issue took 59 cycles; here 30 to 40, less than the 64 that
+// a 128 x 128 x 16 product runs.)
+__device__ __forceinline__ bool elect()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, uint32_t add)
 {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 q, %5, 0;\n setp.ne.u32 p, %4, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(kind), "r"(add), "r"(lead)
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"(add)
         : "memory");
 }
 
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t kind, uint32_t add)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, uint32_t add)
 {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 q, %5, 0;\n setp.ne.u32 p, %4, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(kind), "r"(add), "r"(lead)
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(kind), "r"(add)
         : "memory");
 }
 
 // Arrives on bar once the products that this lane issued so far are done.
-__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar)
+__device__ __forceinline__ void mma_commit(uint32_t bar)
 {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
-        "r"(lead)
-        : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
