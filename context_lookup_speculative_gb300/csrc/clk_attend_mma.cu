@@ -57,10 +57,9 @@ namespace clk {
 namespace {
 
 constexpr int kTile = 128;     // keys of a tile, rows of a row tile
-constexpr int kWarps = 12;     // 8 softmax, 1 copies, 1 products, 2 V tiles
+constexpr int kWarps = 12;     // 8 softmax, 2 copies, 1 products, 1 V tiles
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kValueWarp = 10;
-constexpr int kFlight = 8;     // parts that a join reads at a time
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kValueWarp = 11;
 constexpr int kNear = 4;            // requests whose data a CTA keeps
 
 struct Maps {
@@ -312,6 +311,11 @@ struct Lay {
     static_assert(kTotal <= 232448, "shared memory");
 };
 
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
+
 // This CTA's share of an item whose `total` tiles, from tile `begin` of the
 // line on, lie in several CTAs' shares.
 template <int DP, bool BF16, bool PROMPT>
@@ -347,50 +351,79 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
     const int all = used * quads;
     const int lo = (int)((long long)all * mine / parts), hi = (int)((long long)all * (mine + 1) / parts);
     const float4* const sums = reinterpret_cast<const float4*>(W.sums);
-    for (int i = lo + tid; i < hi; i += kThreads) {
-        const int q = (int)quotient((uint32_t)i, (uint32_t)used), r = i - q * used;
-        const int row = r < full ? r : kTile + r - full;
-        // In the order of the parts, eight parts' loads in flight.
-        float top = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0, 0, 0, 0);
-        for (int c = 0; c < parts; c += kFlight) {
-            float2 ml[kFlight];
-            float4 v[kFlight];
+    // U elements of four columns a thread, F parts of each: eight loads in flight.
+    auto rows_of = [&](auto fc, auto uc) {
+        constexpr int F = decltype(fc)::value, U = decltype(uc)::value;
+        for (int i0 = lo + tid; i0 < hi; i0 += U * kThreads) {
+            float top[U], l[U];
+            float4 o[U];
+            int64_t at[U];
+            int row[U];
 #pragma unroll
-            for (int e = 0; e < kFlight; ++e) {
-                // past the end the last part is read again, with no weight
-                const int64_t at = part(c + e < parts ? c + e : parts - 1);
-                ml[e] = __ldcg(W.ml + at * rows + row);
-                v[e] = __ldcg(sums + (at * (DP / 4) + q) * rows + row);
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kThreads < hi ? i0 + u * kThreads : i0;
+                const int q = (int)quotient((uint32_t)i, (uint32_t)used), r = i - q * used;
+                row[u] = r < full ? r : kTile + r - full;
+                at[u] = (int64_t)q * rows + row[u];
+                top[u] = -INFINITY;
+                l[u] = 0.0f;
+                o[u] = make_float4(0, 0, 0, 0);
             }
-            float to = top;
+            // in the order of the parts
+            for (int c = 0; c < parts; c += F) {
+                float2 ml[U][F];
+                float4 v[U][F];
 #pragma unroll
-            for (int e = 0; e < kFlight; ++e) to = fmaxf(to, ml[e].x);
-            const float f = top == -INFINITY ? 0.0f : exp2_fast(top - to);
-            top = to;
-            l *= f;
-            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < kFlight; ++e) {
-                // a part that saw nothing has no weight (and its reference is -inf)
-                const bool use = c + e < parts && !(ml[e].x == -INFINITY && ml[e].y == 0.0f);
-                const float g = exp2_fast(ml[e].x - to);
-                l += use ? ml[e].y * g : 0.0f;
-                o.x += use ? v[e].x * g : 0.0f;
-                o.y += use ? v[e].y * g : 0.0f;
-                o.z += use ? v[e].z * g : 0.0f;
-                o.w += use ? v[e].w * g : 0.0f;
+                    for (int e = 0; e < F; ++e) {
+                        // past the end the last part is read again, with no weight
+                        const int64_t p = part(c + e < parts ? c + e : parts - 1);
+                        ml[u][e] = __ldcg(W.ml + p * rows + row[u]);
+                        v[u][e] = __ldcg(sums + p * (DP / 4) * rows + at[u]);
+                    }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float to = top[u];
+#pragma unroll
+                    for (int e = 0; e < F; ++e) to = fmaxf(to, ml[u][e].x);
+                    const float f = top[u] == -INFINITY ? 0.0f : exp2_fast(top[u] - to);
+                    top[u] = to;
+                    l[u] *= f;
+                    o[u] = make_float4(o[u].x * f, o[u].y * f, o[u].z * f, o[u].w * f);
+#pragma unroll
+                    for (int e = 0; e < F; ++e) {
+                        // a part that saw nothing has no weight (and its reference is -inf)
+                        const bool use = c + e < parts && !(ml[u][e].x == -INFINITY && ml[u][e].y == 0.0f);
+                        const float g = exp2_fast(ml[u][e].x - to);
+                        l[u] += use ? ml[u][e].y * g : 0.0f;
+                        o[u].x += use ? v[u][e].x * g : 0.0f;
+                        o[u].y += use ? v[u][e].y * g : 0.0f;
+                        o[u].z += use ? v[u][e].z * g : 0.0f;
+                        o[u].w += use ? v[u][e].w * g : 0.0f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kThreads;
+                if (i >= hi) break;
+                const int q = (int)quotient((uint32_t)i, (uint32_t)used), r = i - q * used;
+                const float inv = l[u] == 0.0f ? 0.0f : 1.0f / l[u];
+                const int rt = (int)quotient((uint32_t)r, (uint32_t)A.group);
+                const int tok = cut.item * S.block + rt, head = cut.h * A.group + r - rt * A.group;
+                const int64_t out_row = (PROMPT ? (int64_t)cut.x.base : (int64_t)cut.b * A.N) + tok;
+                uint2 y;
+                y.x = pack2<BF16>(o[u].x * inv, o[u].y * inv);
+                y.y = pack2<BF16>(o[u].z * inv, o[u].w * inv);
+                *reinterpret_cast<uint2*>(static_cast<char*>(A.out) + ((out_row * A.q_heads + head) * A.dim + 4 * q) * 2) = y;
             }
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int rt = (int)quotient((uint32_t)r, (uint32_t)A.group);
-        const int tok = cut.item * S.block + rt, head = cut.h * A.group + r - rt * A.group;
-        const int64_t out_row = (PROMPT ? (int64_t)cut.x.base : (int64_t)cut.b * A.N) + tok;
-        uint2 y;
-        y.x = pack2<BF16>(o.x * inv, o.y * inv);
-        y.y = pack2<BF16>(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<char*>(A.out) + ((out_row * A.q_heads + head) * A.dim + 4 * q) * 2) = y;
-    }
+    };
+    if (parts <= 2)
+        rows_of(Count<2>{}, Count<4>{});
+    else
+        rows_of(Count<8>{}, Count<1>{});
 }
 
 template <int DP, bool BF16, bool PROMPT>
@@ -424,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         }
         for (int i = 0; i < L::kV; ++i) {
             bar_init(base + L::oVFull + 8 * i, 1);
-            bar_init(base + L::oVReady + 8 * i, 2);
+            bar_init(base + L::oVReady + 8 * i, 1);
             bar_init(base + L::oVEmpty + 8 * i, 1);
         }
         for (int i = 0; i < L::kQB; ++i) {
@@ -791,9 +824,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         Walk<PROMPT> w;
         w.start(A, S, plan, near);
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == kCopyWarp) {
-            // ---- Copies. ----
-            int i = 0, seg = 0, nk = 0, nv = 0, nq = 0;  // n*: tiles asked for
+        if (warp == kCopyWarp || warp == kCopyWarp2) {
+            // ---- Copies: two warps (a copy costs its warp about 65 cycles, and pages of 16 rows need 16 a tile). ----
+            // With trees one brings K and the other V, so that small pages' copies go side by side (256 short requests,
+            // pages of 16: 119 us, by alternate tiles 155); with prompts they take alternate tiles, which keeps K and
+            // V in step (a 25,000-token prompt: 3.16 ms, by K and V 3.26).  The first also brings Q.
+            const int odd = warp == kCopyWarp ? 0 : 1;
+            const bool brings_k = PROMPT || odd == 0, brings_v = PROMPT || odd == 1;
+            auto my = [&](int tile) { return !PROMPT || (tile & 1) == odd; };
+            int i = 0, seg = 0, nk = 0, nv = 0, nq = 0;  // n*: one past the last tile or item asked for
             bool ok = (base & 1023) == 0;  // the swizzle's period
             if (!ok) *stop = 1;
             const int pages = kTile >> A.C.shift;  // of a tile
@@ -811,58 +850,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     return page;
                 };
                 int at = w.t0 * pages & ~31, now = batch(at), then = batch(at + 32);
-                const int qi = seg % L::kQB;
-                if (!(ok = warp_wait(base + L::oQEmpty + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop))) break;
-                ++nq;
-                const int tok = w.item * S.block;
-                const int z = PROMPT ? 0 : w.b;
-                const int row0 = PROMPT ? w.x.base : 0;
-                if (lane == 0) {
-                    bar_expect(base + L::oQFull + 8 * qi, (uint32_t)(L::kQ * L::kHalves) * (uint32_t)(S.qbox * A.group) * 128u);
-                    for (int s = 0; s < L::kQ; ++s)
-                        for (int hf = 0; hf < L::kHalves; ++hf)
-                            copy_box(qs + (qi * L::kQ + s) * L::kBytes + hf * L::kHalf, &M.q, 64 * hf, w.h * A.group,
-                                     row0 + tok + s * S.tok, z, base + L::oQFull + 8 * qi);
+                const int z = PROMPT ? 0 : w.b, row0 = PROMPT ? w.x.base : 0;
+                // the first K goes out before the first V
+                if (!PROMPT && odd == 1 && seg == 0 && !(ok = warp_wait(base + L::oQFull, 0, stop))) break;
+                if (odd == 0) {
+                    const int qi = seg % L::kQB;
+                    const uint32_t qb = base + L::oQFull + 8 * qi;
+                    if (!(ok = warp_wait(base + L::oQEmpty + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop))) break;
+                    ++nq;
+                    if (lane == 0) bar_expect(qb, (uint32_t)(L::kQ * L::kHalves) * (uint32_t)(S.qbox * A.group) * 128u);
+                    __syncwarp();
+                    if (lane < L::kQ * L::kHalves) {
+                        const int s = lane / L::kHalves, hf = lane % L::kHalves;
+                        copy_box(qs + (qi * L::kQ + s) * L::kBytes + hf * L::kHalf, &M.q, 64 * hf, w.h * A.group,
+                                 row0 + w.item * S.block + s * S.tok, z, qb);
+                    }
                 }
                 for (int t = w.t0; t < w.t1; ++t, ++i) {
-                    const int ki = i % L::kK, vi = i % L::kV;
-                    const uint32_t kd = ks + ki * L::kBytes, vd = vs + vi * L::kBytes;
-                    const uint32_t kb = base + L::oKFull + 8 * ki, vb = base + L::oVFull + 8 * vi;
                     const bool cached = t < w.x.ctx_tiles;
                     if (cached && t * pages - at >= 32) {
                         at += 32;
                         now = then;
                         then = batch(at + 32);
                     }
+                    if (!my(i)) continue;
                     int page = __shfl_sync(0xffffffffu, now, (t * pages - at + lane) & 31);
                     if (!cached || lane >= pages) page = -1;
                     const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
                     const uint32_t bytes = (uint32_t)L::kHalves * 128u * (uint32_t)(cached ? boxes << A.C.shift : S.kbox);
                     const int n0 = row0 + (t - w.x.ctx_tiles) * kTile;
-                    if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
-                    ++nk;
-                    if (lane == 0) bar_expect(kb, bytes);
-                    __syncwarp();
-                    if (cached) {
-                        if (page >= 0)
+                    auto bring = [&](uint32_t bar, uint32_t dst, const CUtensorMap* pool, const CUtensorMap* fresh) {
+                        if (lane == 0) bar_expect(bar, bytes);
+                        __syncwarp();
+                        if (page >= 0) {
+#pragma unroll
                             for (int hf = 0; hf < L::kHalves; ++hf)
-                                copy_box(kd + hf * L::kHalf + (lane << A.C.shift) * 128, &M.kc, 64 * hf, 0, w.h, page, kb);
-                    } else if (lane < L::kHalves) {
-                        copy_box(kd + lane * L::kHalf, &M.k, 64 * lane, w.h, n0, z, kb);
+                                copy_box(dst + hf * L::kHalf + (lane << A.C.shift) * 128, pool, 64 * hf, 0, w.h, page, bar);
+                        } else if (!cached && lane < L::kHalves) {
+                            copy_box(dst + lane * L::kHalf, fresh, 64 * lane, w.h, n0, z, bar);
+                        }
+                    };
+                    const int ki = i % L::kK, vi = i % L::kV;
+                    if (brings_k) {
+                        if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
+                        nk = i + 1;
+                        bring(base + L::oKFull + 8 * ki, ks + ki * L::kBytes, &M.kc, &M.k);
                     }
-                    if (!(ok = warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(i / L::kV & 1) ^ 1, stop))) break;
-                    ++nv;
-                    if (lane == 0) bar_expect(vb, bytes);
-                    __syncwarp();
-                    if (cached) {
-                        if (page >= 0)
-                            for (int hf = 0; hf < L::kHalves; ++hf)
-                                copy_box(vd + hf * L::kHalf + (lane << A.C.shift) * 128, &M.vc, 64 * hf, 0, w.h, page, vb);
-                    } else if (lane < L::kHalves) {
-                        copy_box(vd + lane * L::kHalf, &M.v, 64 * lane, w.h, n0, z, vb);
+                    if (brings_v) {
+                        if (!(ok = warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(i / L::kV & 1) ^ 1, stop))) break;
+                        nv = i + 1;
+                        bring(base + L::oVFull + 8 * vi, vs + vi * L::kBytes, &M.vc, &M.v);
                     }
                 }
-                if (!ok) break;
             }
             if (!ok) {
                 // Leave no copy in flight.
@@ -871,8 +910,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {}
                 };
                 for (int j = nq > L::kQB ? nq - L::kQB : 0; j < nq; ++j) drain(base + L::oQFull + 8 * (j % L::kQB), (uint32_t)(j / L::kQB & 1));
-                for (int j = nk > L::kK ? nk - L::kK : 0; j < nk; ++j) drain(base + L::oKFull + 8 * (j % L::kK), (uint32_t)(j / L::kK & 1));
-                for (int j = nv > L::kV ? nv - L::kV : 0; j < nv; ++j) drain(base + L::oVFull + 8 * (j % L::kV), (uint32_t)(j / L::kV & 1));
+                for (int j = nk > L::kK ? nk - L::kK : 0; j < nk; ++j)
+                    if (my(j)) drain(base + L::oKFull + 8 * (j % L::kK), (uint32_t)(j / L::kK & 1));
+                for (int j = nv > L::kV ? nv - L::kV : 0; j < nv; ++j)
+                    if (my(j)) drain(base + L::oVFull + 8 * (j % L::kV), (uint32_t)(j / L::kV & 1));
             }
         } else if (warp == kMmaWarp) {
             // ---- Products: one lane issues them, the warp goes along. ----
@@ -1015,17 +1056,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 }
             }
             __syncwarp();
-        } else if (warp >= kValueWarp) {
+        } else {
             // ---- V tiles: rows past the end, and rows that are not finite. ----
-            constexpr uint32_t top = BF16 ? 0x7f807f80u : 0x7c007c00u;
-            const int half = warp - kValueWarp;
+            // a value is not finite where its exponent is all ones: one more there carries into the sign
+            constexpr uint32_t expo = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
             if (!PROMPT) {
                 // Rows past the node counts are 0; the requests are dealt out to the CTAs.
                 for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
                     const int rows = attend_request(A, b, false).rows;
                     const int64_t row = (int64_t)A.q_heads * A.dim / 8;
                     uint4* const out = static_cast<uint4*>(A.out) + ((int64_t)b * A.N + rows) * row;
-                    for (int64_t e = 32 * half + lane; e < (A.N - rows) * row; e += 64) out[e] = make_uint4(0, 0, 0, 0);
+                    for (int64_t e = lane; e < (A.N - rows) * row; e += 32) out[e] = make_uint4(0, 0, 0, 0);
                 }
             }
             int i = 0;
@@ -1040,30 +1081,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     const bool look = !cached && (!PROMPT || n0 + kTile - 1 > w.item * S.block);
                     if (have < kTile || look) {
                         char* const tile = sm + (vs - base) + vi * L::kBytes;
-    #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int r = 64 * half + 32 * u + lane;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int r = 32 * u + lane;
                             bool clear = r >= have, odd = false;
-                            if (look && !clear) {
+                            if (look && 32 * u < have) {
                                 uint32_t hit = 0;
-    #pragma unroll
+#pragma unroll
                                 for (int c = 0; c < 8 * L::kHalves; ++c) {
                                     // lanes start at different chunks of their rows: no two in one bank
                                     const int at = (c & 8) * (L::kHalf / 8) + r * 128 + (((c & 7) + lane) & 7) * 16;
                                     const uint4 x = *reinterpret_cast<const uint4*>(tile + at);
-                                    hit |= __vcmpeq2(x.x & top, top) | __vcmpeq2(x.y & top, top) | __vcmpeq2(x.z & top, top) |
-                                           __vcmpeq2(x.w & top, top);
+                                    hit |= ((x.x & expo) + one) | ((x.y & expo) + one) | ((x.z & expo) + one) | ((x.w & expo) + one);
                                 }
-                                odd = hit != 0;
+                                odd = !clear && (hit & 0x80008000u) != 0;
                             }
                             if (clear || odd)
-    #pragma unroll
+#pragma unroll
                                 for (int c = 0; c < 8 * L::kHalves; ++c) {
                                     const int at = (c & 8) * (L::kHalf / 8) + r * 128 + (((c & 7) + lane) & 7) * 16;
                                     *reinterpret_cast<uint4*>(tile + at) = make_uint4(0, 0, 0, 0);
                                 }
                             const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                            if (lane == 0) bad[4 * vi + 2 * half + u] = word;
+                            if (lane == 0) bad[4 * vi + u] = word;
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
