@@ -130,13 +130,16 @@ __device__ __forceinline__ void take_page(const CacheDev& C, int32_t page)
 
 // Plans a call's pages, as one CTA.  FORK = false: clk_cache_grow's whole
 // work.  FORK = true: clk_cache_fork's tail pages; req[b].y becomes the tail
-// page, -1 without one, kFailed for a request that is left out.
+// page, -1 without one, kFailed for a request that is left out, and req[b].x
+// the tails' rows before it.
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheDev C, const int32_t* slots, const int32_t* dst,
                                                              const int32_t* count, int32_t B)
 {
+    chained();
     __shared__ int sm[33];
     __shared__ int2 near[kPlanThreads];
+    __shared__ int32_t few[kPlanThreads];
     const int tid = threadIdx.x;
     const int32_t part = C.page_tokens() - 1;
     // Pages of each request: req = (those of the requests before it, its own or kFailed).
@@ -183,7 +186,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheDev C, const i
         want += total;
     }
     __syncthreads();
-    const int have = want > 0 ? lowest_free(C, want < C.num_pages ? want : C.num_pages, C.list, sm) : 0;
+    int32_t* const list = want <= kPlanThreads ? few : C.list;
+    const int have = want > 0 ? lowest_free(C, want < C.num_pages ? want : C.num_pages, list, sm) : 0;
     if (!FORK) {
         // Rank r's page goes to the last request whose pages start at or before r.
         for (int r = tid; r < have; r += kPlanThreads) {
@@ -197,36 +201,50 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheDev C, const i
             }
             const int2 q = req[lo];
             if (q.x + q.y > have) continue;
-            const int32_t s = slots[lo], page = C.list[r];
+            const int32_t s = slots[lo], page = list[r];
             C.table[(int64_t)s * C.max_pages + C.pages(C.len[s]) + (r - q.x)] = page;
             take_page(C, page);
         }
         __syncthreads();
     }
-    for (int b = tid; b < B; b += kPlanThreads) {
-        const int2 q = req[b];
-        int tail = kFailed;
-        if (q.y >= 0) {
-            if (q.y > 0 && q.x + q.y > have) {
-                latch(C.status, CLK_ECAPACITY, FORK ? dst[b] : slots[b]);
-            } else if (!FORK) {
-                C.len[slots[b]] += count[b];
-            } else {
-                tail = -1;
-                if (q.y > 0) {
-                    tail = C.list[q.x];
-                    take_page(C, tail);
+    int rows = 0;  // FORK: rows that the copying kernel moves, request after request
+    for (int base = 0; base < B; base += kPlanThreads) {
+        const int b = base + tid;
+        int tail = kFailed, own = 0;
+        if (b < B) {
+            const int2 q = req[b];
+            if (q.y >= 0) {
+                if (q.y > 0 && q.x + q.y > have) {
+                    latch(C.status, CLK_ECAPACITY, FORK ? dst[b] : slots[b]);
+                } else if (!FORK) {
+                    C.len[slots[b]] += count[b];
+                } else {
+                    const int32_t n = C.len[slots[b]];
+                    tail = -1;
+                    if (q.y > 0) {
+                        tail = list[q.x];
+                        take_page(C, tail);
+                        own = n & part;
+                    }
+                    C.len[dst[b]] = n;
                 }
-                C.len[dst[b]] = C.len[slots[b]];
             }
         }
-        if (FORK) C.req[b] = make_int2(q.x, tail);
+        if (FORK) {
+            int total;
+            const int before = block_scan(own, sm, &total);
+            if (b < B) C.req[b] = make_int2(rows + before, tail);
+            rows += total;
+        }
     }
-    if (FORK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (FORK) {
+        if (tid == 0) C.list[3 * (int64_t)C.num_pages + 2] = rows;
+        }
 }
 
 __global__ void __launch_bounds__(kCopyThreads) k_cache_free(CacheDev C, const int32_t* slots, int32_t B)
 {
+    chained();
     const int b = blockIdx.x;
     const int32_t s = slots[b];
     if (!slot_ok(C, s)) {
@@ -252,73 +270,145 @@ struct VecPool {
     int32_t planes, heads, row;
 };
 
-// Copies the first `rows` rows of page src to page dst for planes p0 .. p1-1;
-// the CTA's threads take `row` vectors of as many rows at a time as they can.
+// Copies the first `rows` rows of page src to page dst in one plane; the
+// CTA's threads take `row` vectors of as many rows at a time as they can,
+// eight of them in flight.
 template <typename V>
-__device__ __forceinline__ void copy_page(const VecPool<V>& A, int64_t src, int64_t dst, int32_t rows, int32_t p0, int32_t p1)
+__device__ __forceinline__ void copy_page(const VecPool<V>& A, int64_t src, int64_t dst, int32_t rows, int32_t plane)
 {
+    constexpr int kFlight = 8;
     const int wide = A.row < kCopyThreads ? A.row : kCopyThreads;
     const int tall = kCopyThreads / wide;
     const int c0 = threadIdx.x % wide, t0 = threadIdx.x / wide;
     if (t0 >= tall) return;
     const int lines = A.heads * rows;
+    V* const base = A.base + plane * A.plane;
     const int64_t from = src * A.page, to = dst * A.page;
-    for (int p = p0; p < p1; ++p) {
-        V* const base = A.base + p * A.plane;
+    for (int i = t0; i < lines; i += kFlight * tall) {
+        int64_t off[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int line = i + u * tall;
+            const int head = line / rows;
+            off[u] = line < lines ? head * A.head + (int64_t)(line - head * rows) * A.tok : -1;
+        }
+        for (int c = c0; c < A.row; c += wide) {
+            V x[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (off[u] >= 0) x[u] = base[from + off[u] + c];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (off[u] >= 0) base[to + off[u] + c] = x[u];
+        }
+    }
+}
+
+// A CTA moves kRows rows at a time in every head of planes p0 .. p1-1: their
+// sources and places (in vectors, -1 for none) are found once, by as many
+// threads, and lie in shared memory.
+constexpr int kRows = 8;
+
+template <typename V, typename Plane>
+__device__ __forceinline__ void move_rows(const int64_t* from, const int64_t* to, const VecPool<V>& A, int64_t src_head, int p0,
+                                          int p1, Plane plane_of)
+{
+    const int wide = A.row < kCopyThreads ? A.row : kCopyThreads;
+    const int tall = kCopyThreads / wide;
+    const int c0 = threadIdx.x % wide, t0 = threadIdx.x / wide;
+    if (t0 >= tall) return;
+    int live = 0;  // rows past the last one that moves need no turn
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (to[r] >= 0) live = r + 1;
+    const int lines = live * A.heads;
+    for (int plane = p0; plane < p1; ++plane) {
+        const V* src;
+        V* dst;
+        plane_of(plane, src, dst);
         for (int i = t0; i < lines; i += 4 * tall) {
-            // four rows in flight
-            int64_t off[4];
+            // rows follow one another in a page, so the rows of one head go together
+            int64_t a[4], z[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int line = i + u * tall;
-                const int head = line / rows;
-                off[u] = line < lines ? head * A.head + (int64_t)(line - head * rows) * A.tok : -1;
+                const int head = line / live, r = line - head * live;
+                const bool take = line < lines && to[r] >= 0;
+                a[u] = take ? from[r] + head * src_head : -1;
+                z[u] = take ? to[r] + head * A.head : -1;
             }
             for (int c = c0; c < A.row; c += wide) {
                 V x[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    if (off[u] >= 0) x[u] = base[from + off[u] + c];
+                    if (z[u] >= 0) x[u] = src[a[u] + c];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    if (off[u] >= 0) base[to + off[u] + c] = x[u];
+                    if (z[u] >= 0) dst[z[u] + c] = x[u];
             }
         }
     }
 }
 
-// Destination b shares the source's whole pages and copies its tail's rows.
-// blockIdx.y takes a share of the planes; y = 0 also writes the table.
+// Destination b shares the source's whole pages (the CTAs with blockIdx.y = 0
+// write the tables) and its tail's rows are copied: the tails of all
+// requests lie one after the other, kRows rows a CTA, so that tails of every
+// length balance; blockIdx.y takes a share of the planes.
 template <typename V>
-__global__ void __launch_bounds__(kCopyThreads) k_cache_fork(CacheDev C, const int32_t* src, const int32_t* dst,
+__global__ void __launch_bounds__(kCopyThreads) k_cache_fork(CacheDev C, const int32_t* src, const int32_t* dst, int32_t B,
                                                              VecPool<V> A)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.x;
-    const int32_t tail = C.req[b].y;
-    if (tail == kFailed) return;
-    const int32_t s = src[b], d = dst[b], n = C.len[s];
-    const int32_t whole = C.held(n) - (tail >= 0 ? 1 : 0);
-    const int32_t* const from = C.table + (int64_t)s * C.max_pages;
-    if (blockIdx.y == 0) {
-        int32_t* const to = C.table + (int64_t)d * C.max_pages;
-        for (int i = threadIdx.x; i < whole; i += kCopyThreads) {
-            const int32_t page = from[i];
-            to[i] = page;
-            atomicAdd(C.refs + page, 1);
+    chained();
+    __shared__ int64_t from[kRows], to[kRows];
+    __shared__ int32_t before[kCopyThreads];
+    const int rows = C.list[3 * (int64_t)C.num_pages + 2];
+    const bool few = B <= kCopyThreads;
+    if (few && threadIdx.x < B) before[threadIdx.x] = C.req[threadIdx.x].x;
+    __syncthreads();
+    const int64_t at = (int64_t)blockIdx.x * kRows + threadIdx.x;
+    if (threadIdx.x < kRows) {
+        int64_t a = -1, z = -1;
+        if (at < rows) {
+            // the last request whose rows start at or before this one
+            int lo = 0, hi = B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((few ? before[mid] : C.req[mid].x) <= at)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int2 q = C.req[lo];
+            const int32_t s = src[lo], whole = C.held(C.len[s]) - 1;
+            const int64_t row = (at - q.x) * A.tok;
+            a = C.table[(int64_t)s * C.max_pages + whole] * A.page + row;
+            z = q.y * A.page + row;
         }
-        if (threadIdx.x == 0 && tail >= 0) to[whole] = tail;
+        from[threadIdx.x] = a;
+        to[threadIdx.x] = z;
     }
-    if (tail < 0) return;
-    const int per = (A.planes + gridDim.y - 1) / gridDim.y;
-    const int p0 = blockIdx.y * per;
-    copy_page(A, from[whole], tail, n & (C.page_tokens() - 1), p0, p0 + per < A.planes ? p0 + per : A.planes);
+    if (blockIdx.y == 0 && blockIdx.x < B) {
+        const int b = blockIdx.x;
+        const int32_t tail = C.req[b].y;
+        if (tail != kFailed) {
+            const int32_t whole = C.held(C.len[src[b]]) - (tail >= 0 ? 1 : 0);
+            const int32_t* const have = C.table + (int64_t)src[b] * C.max_pages;
+            int32_t* const row = C.table + (int64_t)dst[b] * C.max_pages;
+            for (int i = threadIdx.x; i < whole; i += kCopyThreads) {
+                const int32_t page = have[i];
+                row[i] = page;
+                atomicAdd(C.refs + page, 1);
+            }
+            if (threadIdx.x == 0 && tail >= 0) row[whole] = tail;
+        }
+    }
+    __syncthreads();
+    if ((int64_t)blockIdx.x * kRows >= rows) return;
+    const int p0 = (int)((int64_t)A.planes * blockIdx.y / gridDim.y), p1 = (int)((int64_t)A.planes * (blockIdx.y + 1) / gridDim.y);
+    move_rows(from, to, A, A.head, p0, p1, [&](int plane, const V*& s, V*& d) { s = d = A.base + plane * A.plane; });
 }
 
-// Rows of the new tokens into the pages.  A CTA takes kRows rows of one
-// plane: their sources and places are found once, by as many threads, and
-// kept in shared memory.
-constexpr int kRows = 8;
+// Rows of the new tokens into the pages; blockIdx.y takes a share of the planes.
 
 // Whether n rows of a request with source rows base .. base + rows - 1 can go to the end of len tokens.
 __device__ __forceinline__ bool append_ok(int32_t n, int32_t len, int64_t base, int64_t rows, int64_t total)
@@ -334,13 +424,19 @@ struct VecSrc {
 
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const int32_t* slots, int32_t B, VecPool<V> A,
-                                                               int32_t layer0, VecSrc<V> S, int64_t N, const int64_t* off,
+                                                               int32_t layer0, int32_t planes, VecSrc<V> S, int64_t N, const int64_t* off,
                                                                const int32_t* path, const int32_t* count)
 {
+    chained();
     __shared__ int64_t from[kRows], to[kRows];
     const int64_t total = off != nullptr ? N : (int64_t)B * N;
     const int64_t first = (int64_t)blockIdx.x * kRows;
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    __shared__ int64_t begin[kCopyThreads];
+    const bool few = off != nullptr && B < kCopyThreads;
+    if (few && threadIdx.x <= B) begin[threadIdx.x] = off[threadIdx.x];
+    __syncthreads();
+    const int64_t* const starts = few ? begin : off;
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) {
         // one CTA reports the requests that are left out
         for (int b = threadIdx.x; b < B; b += kCopyThreads) {
             const int32_t s = slots[b];
@@ -361,20 +457,20 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
                 b = (int)(at / N);
                 i = at - b * N;
                 base = b * N;
-            } else if (off[0] <= at) {
+            } else if (starts[0] <= at) {
                 // the last request that starts at or before this row
                 int lo = 0, hi = B - 1;
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) >> 1;
-                    if (off[mid] <= at)
+                    if (starts[mid] <= at)
                         lo = mid;
                     else
                         hi = mid - 1;
                 }
                 b = lo;
-                base = off[lo];
+                base = starts[lo];
                 i = at - base;
-                rows = off[lo + 1] - base;
+                rows = starts[lo + 1] - base;
             }
         }
         if (b >= 0) {
@@ -397,35 +493,11 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
         to[threadIdx.x] = place;
     }
     __syncthreads();
-    const int plane = blockIdx.y;
-    const V* const src = (plane & 1 ? S.v : S.k) + (plane >> 1) * S.layer;
-    V* const dst = A.base + (2 * (int64_t)layer0 + plane) * A.plane;
-    const int wide = A.row < kCopyThreads ? A.row : kCopyThreads;
-    const int tall = kCopyThreads / wide;
-    const int c0 = threadIdx.x % wide, t0 = threadIdx.x / wide;
-    if (t0 >= tall) return;
-    const int lines = kRows * A.heads;
-    for (int i = t0; i < lines; i += 4 * tall) {
-        // rows follow one another in a page, so the rows of one head go together
-        int64_t a[4], z[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int line = i + u * tall;
-            const int r = line % kRows, head = line / kRows;
-            const bool take = line < lines && to[r] >= 0;
-            a[u] = take ? from[r] + head * S.head : -1;
-            z[u] = take ? to[r] + head * A.head : -1;
-        }
-        for (int c = c0; c < A.row; c += wide) {
-            V x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (z[u] >= 0) x[u] = src[a[u] + c];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (z[u] >= 0) dst[z[u] + c] = x[u];
-        }
-    }
+    const int p0 = (int)((int64_t)planes * blockIdx.y / gridDim.y), p1 = (int)((int64_t)planes * (blockIdx.y + 1) / gridDim.y);
+    move_rows(from, to, A, S.head, p0, p1, [&](int plane, const V*& s, V*& d) {
+        s = (plane & 1 ? S.v : S.k) + (plane >> 1) * S.layer;
+        d = A.base + (2 * (int64_t)layer0 + plane) * A.plane;
+    });
 }
 
 // Compaction, step 1 (one CTA): with L pages in use, list[0] holds the free
@@ -434,6 +506,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
 // bits become what they are after the move.
 __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(CacheDev C, int32_t* moved)
 {
+    chained();
     __shared__ int sm[33];
     const int tid = threadIdx.x;
     const int words = C.words();
@@ -477,14 +550,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(CacheDev C, int32
         C.list[3 * (int64_t)C.num_pages + 1] = live;
         if (moved != nullptr) *moved = nm;
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Step 2: tables follow, and rank[hole] receives the rows that the moving
 // page holds (holes are free, so their ranks are not in use).
 __global__ void __launch_bounds__(kCopyThreads) k_compact_table(CacheDev C)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chained();
     const int s = blockIdx.x;
     const int32_t n = C.len[s], live = C.list[3 * (int64_t)C.num_pages + 1];
     int32_t* const rank = C.list + 2 * (int64_t)C.num_pages;
@@ -497,7 +569,6 @@ __global__ void __launch_bounds__(kCopyThreads) k_compact_table(CacheDev C)
         const int32_t left = n - (i << C.shift);
         rank[to] = left < C.page_tokens() ? left : C.page_tokens();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Step 3: rows and counts move.  A CTA takes one plane of one moving page at
@@ -505,13 +576,13 @@ __global__ void __launch_bounds__(kCopyThreads) k_compact_table(CacheDev C)
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) k_compact_copy(CacheDev C, VecPool<V> A)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chained();
     const int32_t *const holes = C.list, *const movers = C.list + C.num_pages, *const rank = C.list + 2 * (int64_t)C.num_pages;
     const int64_t units = (int64_t)C.list[3 * (int64_t)C.num_pages] * A.planes;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int r = (int)(u / A.planes), p = (int)(u - (int64_t)r * A.planes);
         const int32_t src = movers[r], dst = holes[r];
-        copy_page(A, src, dst, rank[dst], p, p + 1);
+        copy_page(A, src, dst, rank[dst], p);
         if (p == 0 && threadIdx.x == 0) {
             C.refs[dst] = C.refs[src];
             C.refs[src] = 0;
@@ -557,21 +628,13 @@ int with_vector(int bytes, F f)
     }
 }
 
-// A launch that may begin while the call's own previous kernel finishes; it
-// waits for it by itself.
-template <typename... P, typename... T>
-int launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, T... args)
+// Shares of the planes for `groups` groups of rows: until there are about
+// eight CTAs an SM, one wave (more would only find the same rows' places
+// again).
+unsigned plane_shares(int64_t groups, int32_t planes)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
+    const int64_t want = (8 * (int64_t)num_sms() + groups - 1) / groups;
+    return (unsigned)(want < 1 ? 1 : want < planes ? want : planes);
 }
 
 }  // namespace
@@ -667,8 +730,7 @@ extern "C" int clk_cache_grow(clk_cache* h, const int32_t* d_slots, int32_t B, c
     const int rc = check_cache_batch(h, B);
     if (rc != CLK_OK || B == 0) return rc;
     if (!ok_i32(d_slots) || !ok_i32(d_count)) return CLK_EINVAL;
-    k_cache_plan<false><<<1, kPlanThreads, 0, (cudaStream_t)s>>>(h->dev, d_slots, nullptr, d_count, B);
-    return launch_status();
+    return launch_chained(k_cache_plan<false>, 1, kPlanThreads, (cudaStream_t)s, h->dev, d_slots, (const int32_t*)nullptr, d_count, B);
 }
 
 extern "C" int clk_cache_free(clk_cache* h, const int32_t* d_slots, int32_t B, clk_stream_t s)
@@ -676,8 +738,7 @@ extern "C" int clk_cache_free(clk_cache* h, const int32_t* d_slots, int32_t B, c
     const int rc = check_cache_batch(h, B);
     if (rc != CLK_OK || B == 0) return rc;
     if (!ok_i32(d_slots)) return CLK_EINVAL;
-    k_cache_free<<<(unsigned)B, kCopyThreads, 0, (cudaStream_t)s>>>(h->dev, d_slots, B);
-    return launch_status();
+    return launch_chained(k_cache_free, (unsigned)B, kCopyThreads, (cudaStream_t)s, h->dev, d_slots, B);
 }
 
 extern "C" int clk_cache_fork(clk_cache* h, const int32_t* d_src, const int32_t* d_dst, int32_t B, const clk_pool* pool,
@@ -688,15 +749,14 @@ extern "C" int clk_cache_fork(clk_cache* h, const int32_t* d_src, const int32_t*
     if (check_pool(pool) != CLK_OK) return CLK_EINVAL;
     if (B == 0) return CLK_OK;
     if (!ok_i32(d_src) || !ok_i32(d_dst)) return CLK_EINVAL;
-    k_cache_plan<true><<<1, kPlanThreads, 0, (cudaStream_t)s>>>(h->dev, d_src, d_dst, nullptr, B);
-    if ((rc = launch_status()) != CLK_OK) return rc;
-    // Planes are shared out until there are about eight CTAs an SM.
-    const int want = (8 * num_sms() + B - 1) / B;
-    const unsigned y = (unsigned)(want < 1 ? 1 : want < pool->planes ? want : pool->planes);
+    rc = launch_chained(k_cache_plan<true>, 1, kPlanThreads, (cudaStream_t)s, h->dev, d_src, d_dst, (const int32_t*)nullptr, B);
+    if (rc != CLK_OK) return rc;
+    const int64_t groups = ((int64_t)B * (h->dev.page_tokens() - 1) + kRows - 1) / kRows;
+    const unsigned x = (unsigned)(groups > B ? groups : B);
     return with_vector(vector_bytes(*pool, 0), [&](auto v) {
         using V = decltype(v);
-        return launch_after(k_cache_fork<V>, dim3((unsigned)B, y), kCopyThreads, (cudaStream_t)s, h->dev, d_src, d_dst,
-                            vec_pool<V>(*pool));
+        return launch_chained(k_cache_fork<V>, dim3(x, plane_shares(x, pool->planes)), kCopyThreads, (cudaStream_t)s, h->dev, d_src,
+                            d_dst, B, vec_pool<V>(*pool));
     });
 }
 
@@ -724,9 +784,9 @@ extern "C" int clk_cache_append(clk_cache* h, const int32_t* d_slots, int32_t B,
         const int64_t w = (int64_t)sizeof(V);
         const VecSrc<V> src{static_cast<const V*>(d_k), static_cast<const V*>(d_v), layer_stride * b / w, row_stride * b / w,
                             head_stride * b / w};
-        k_cache_append<V><<<dim3((unsigned)blocks, (unsigned)(2 * layers)), kCopyThreads, 0, (cudaStream_t)s>>>(
-            h->dev, d_slots, B, vec_pool<V>(*pool), layer0, src, N, d_off, d_path, d_count);
-        return launch_status();
+        return launch_chained(k_cache_append<V>, dim3((unsigned)blocks, plane_shares(blocks, 2 * layers)), kCopyThreads,
+                              (cudaStream_t)s, h->dev, d_slots, B, vec_pool<V>(*pool), layer0, 2 * layers, src, N, d_off, d_path,
+                              d_count);
     });
 }
 
@@ -736,11 +796,10 @@ extern "C" int clk_cache_compact(clk_cache* h, const clk_pool* pool, int32_t* d_
     if (rc != CLK_OK) return rc;
     if (check_pool(pool) != CLK_OK || !aligned(d_moved, 4)) return CLK_EINVAL;
     cudaStream_t cs = (cudaStream_t)s;
-    k_compact_plan<<<1, kPlanThreads, 0, cs>>>(h->dev, d_moved);
-    if ((rc = launch_status()) != CLK_OK) return rc;
-    if ((rc = launch_after(k_compact_table, dim3((unsigned)h->dev.max_slots), kCopyThreads, cs, h->dev)) != CLK_OK) return rc;
+    if ((rc = launch_chained(k_compact_plan, 1, kPlanThreads, cs, h->dev, d_moved)) != CLK_OK) return rc;
+    if ((rc = launch_chained(k_compact_table, dim3((unsigned)h->dev.max_slots), kCopyThreads, cs, h->dev)) != CLK_OK) return rc;
     return with_vector(vector_bytes(*pool, 0), [&](auto v) {
         using V = decltype(v);
-        return launch_after(k_compact_copy<V>, dim3((unsigned)(8 * num_sms())), kCopyThreads, cs, h->dev, vec_pool<V>(*pool));
+        return launch_chained(k_compact_copy<V>, dim3((unsigned)(8 * num_sms())), kCopyThreads, cs, h->dev, vec_pool<V>(*pool));
     });
 }

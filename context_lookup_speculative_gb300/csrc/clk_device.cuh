@@ -103,6 +103,15 @@ __device__ __forceinline__ void latch(int32_t* status, int32_t code, int32_t det
     if (atomicCAS(status, 0, code) == 0) atomicExch(status + 1, detail);
 }
 
+// First statement of a kernel that launch_chained launches.  It waits before
+// it lets the next launch begin, so that whatever a next launch reads before
+// its own wait (a verify's logits) was complete when this one began to work.
+__device__ __forceinline__ void chained()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ int32_t* hist_of(const LookupDev& L, int32_t slot)
 {
     return L.hist + (int64_t)slot * L.hstride;

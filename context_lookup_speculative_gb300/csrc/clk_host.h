@@ -66,6 +66,24 @@ inline int check_batch(const clk_lookup* h, int32_t B)
     return CLK_OK;
 }
 
+// Launches a kernel that begins with chained(): it may be set up while the
+// preceding launch on the stream runs, waits for that one's end itself, and
+// lets the next such launch be set up in turn.
+template <typename... P, typename... T>
+int launch_chained(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, T... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
+}
+
 // Registers one CTA of the fused proposal launch (clk_propose_fuse_sched)
 // takes for nlev match lengths (allocation granularity included), or -1 on
 // a CUDA error.  Defined with the kernel in clk_lookup.cu.

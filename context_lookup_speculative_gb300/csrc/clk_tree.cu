@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "clk.h"
+#include "clk_device.cuh"
 #include "clk_host.h"
 
 namespace clk {
@@ -24,6 +25,7 @@ __device__ __forceinline__ int tree_parent(const int32_t* parent, int64_t at, in
 __global__ void __launch_bounds__(kNodes) k_tree_masks(int32_t N, const int32_t* parent, const int32_t* nodes,
                                                        int64_t* mask)
 {
+    chained();
     __shared__ int up[kNodes];
     const int b = blockIdx.x, n = threadIdx.x;
     const int count = nodes[b] >= 0 && nodes[b] <= N ? nodes[b] : 0;
@@ -41,6 +43,7 @@ __global__ void __launch_bounds__(kNodes) k_tree_accept(int32_t N, const int32_t
                                                         const int32_t* nodes, const int32_t* argmax, int32_t* accept,
                                                         int32_t* path, int32_t* emitted, int32_t* out_tok)
 {
+    chained();
     __shared__ int up[kNodes], text[kNodes];
     __shared__ bool fits[kNodes];
     __shared__ unsigned hits[2];
@@ -96,8 +99,7 @@ extern "C" int clk_tree_masks(int32_t B, int32_t N, const int32_t* d_parent, con
     const int rc = check_tree(B, N);
     if (rc != CLK_OK || B == 0) return rc;
     if (!ok_i32(d_parent) || !ok_i32(d_nodes) || d_mask == nullptr || !aligned(d_mask, 8)) return CLK_EINVAL;
-    k_tree_masks<<<(unsigned)B, kNodes, 0, (cudaStream_t)s>>>(N, d_parent, d_nodes, d_mask);
-    return launch_status();
+    return launch_chained(k_tree_masks, (unsigned)B, kNodes, (cudaStream_t)s, N, d_parent, d_nodes, d_mask);
 }
 
 extern "C" int clk_tree_accept(int32_t B, int32_t N, const int32_t* d_tok, const int32_t* d_parent,
@@ -109,7 +111,6 @@ extern "C" int clk_tree_accept(int32_t B, int32_t N, const int32_t* d_tok, const
     if (!ok_i32(d_tok) || !ok_i32(d_parent) || !ok_i32(d_nodes) || !ok_i32(d_argmax) || !ok_i32(d_accept) ||
         !ok_i32(d_path) || !ok_i32(d_emitted) || !ok_i32(d_out_tok))
         return CLK_EINVAL;
-    k_tree_accept<<<(unsigned)B, kNodes, 0, (cudaStream_t)s>>>(N, d_tok, d_parent, d_nodes, d_argmax, d_accept, d_path,
-                                                              d_emitted, d_out_tok);
-    return launch_status();
+    return launch_chained(k_tree_accept, (unsigned)B, kNodes, (cudaStream_t)s, N, d_tok, d_parent, d_nodes, d_argmax, d_accept,
+                          d_path, d_emitted, d_out_tok);
 }
