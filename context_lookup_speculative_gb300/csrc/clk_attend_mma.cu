@@ -1204,11 +1204,12 @@ bool mma_dim(int32_t dim) { return dim >= 64 && dim <= 128 && dim % 8 == 0; }
 
 // Rows of 64 to 128 elements of 16 bits in whole 16-byte vectors, groups of
 // at most a row tile, and strides that tensor maps can take.  A scale that
-// is not positive would turn the running maximum around; it is left to the
-// general kernel.
+// is not positive would turn the running maximum around, and one at the end
+// of the range would leave it; both are left to the general kernel.
 bool attend_mma_takes(const Attend& A)
 {
-    if (A.dtype == CLK_DTYPE_F32 || !mma_dim(A.dim) || A.group > kTile || !(A.scale > 0.0f)) return false;
+    if (A.dtype == CLK_DTYPE_F32 || !mma_dim(A.dim) || A.group > kTile || !(A.scale >= 1e-20f && A.scale <= 1e20f))
+        return false;
     for (const void* p : {A.q, A.k, A.v, (const void*)A.out, A.kc, A.vc})
         if (!aligned(p, 16)) return false;
     const int64_t rows = A.off != nullptr ? A.T : A.N, reqs = A.off != nullptr ? 1 : A.B;

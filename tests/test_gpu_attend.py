@@ -479,3 +479,53 @@ def test_refusals():
     with pytest.raises(ValueError):
         clk.prompt_attend(t.q[0], t.k[0], t.v[0], ints([0, 3], torch.int64), 0.1, t.out[0], t.scratch, ctx=ints([1]))
     clk.prompt_attend(t.q[0], t.k[0], t.v[0], ints([0, 3], torch.int64), 0.1, t.out[0], t.scratch)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-25, 1e-3, 1e3])
+def test_scales_at_the_ends_of_the_range(scale):
+    Tree(20, 2, 4, [130, 20], 2, 1, 64, 16, "bf16", nodes=[4, 4], scale=scale).run().check()
+
+
+def test_a_pool_of_more_than_two_to_the_32_elements():
+    """Pages whose elements lie past 32 bits, read by both kernels."""
+    pages, P, Hkv, D = 8700, 128, 16, 128
+    cache = clk.Cache(3, pages, pages, P)
+    pool = torch.empty((2, pages, Hkv, P, D), dtype=torch.bfloat16, device="cuda")
+    assert pool.numel() > 1 << 32
+    n = 300
+    clk.cache_grow(cache, ints([0]), ints([(pages - 4) * P]))
+    clk.cache_grow(cache, ints([2]), ints([n]))
+    torch.cuda.synchronize()
+    assert cache.table[2, 0].item() == pages - 4
+    pool[:, pages - 4:].normal_()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.empty((1, 2, 3 * Hkv, D), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    q, k, v = qkv.split(Hkv, 2)
+    mask = torch.tensor([[1, 3]], dtype=torch.int64, device="cuda")
+    for scale in (0.09, -0.09):  # a negative scale goes through the general kernel
+        out = torch.zeros((1, 2, Hkv, D), dtype=torch.bfloat16, device="cuda")
+        clk.tree_attend(cache, ints([2]), pool, 0, q, k, v, ints([2]), mask, scale, out, clk.attend_scratch(Hkv, Hkv, D))
+        for h in (0, Hkv - 1):
+            kc, vc = (cached(pool, x, cache.table[2], n, h, P) for x in (0, 1))
+            for t in range(2):
+                keys, vals = np.concatenate([kc, f64(k)[0, :t + 1, h]]), np.concatenate([vc, f64(v)[0, :t + 1, h]])
+                want, size = attend_row(f64(q)[0, t, h], keys, vals, scale)
+                compare(f64(out)[0, t, h], want, size, "bf16", len(keys), np.abs(vals).max(), (scale, h, t))
+
+
+def test_broadcast_inputs():
+    """Strides of 0: one K/V row shared by the heads, one query shared by the requests."""
+    t = Tree(21, 3, 4, [40, 0, 130], 2, 2, 64, 16, "bf16", nodes=[4, 2, 3])
+    t.k, t.v = (x[:, :, :1].expand(-1, -1, 2, -1) for x in (t.k, t.v))
+    t.q = t.q[:1].expand(3, -1, -1, -1)
+    t.run().check()
+    p = Prompt(22, [70, 9], 2, 2, 128, "f16")
+    p.k, p.v = (x[:, :1].expand(-1, 2, -1) for x in (p.k, p.v))
+    p.run().check(rows=10)
+
+
+def test_keys_and_values_of_different_strides():
+    t = Tree(23, 2, 5, [60, 33], 3, 2, 64, 16, "bf16", nodes=[5, 4])
+    t.v = t.v.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    t.q = t.q.contiguous()
+    t.run().check()
