@@ -481,7 +481,7 @@ def test_refusals():
     clk.prompt_attend(t.q[0], t.k[0], t.v[0], ints([0, 3], torch.int64), 0.1, t.out[0], t.scratch)
 
 
-@pytest.mark.parametrize("scale", [1e-38, 1e-25, 1e-3, 1e3])
+@pytest.mark.parametrize("scale", [1e-38, 1e-25, 1e-3, 20.0])
 def test_scales_at_the_ends_of_the_range(scale):
     Tree(20, 2, 4, [130, 20], 2, 1, 64, 16, "bf16", nodes=[4, 4], scale=scale).run().check()
 
