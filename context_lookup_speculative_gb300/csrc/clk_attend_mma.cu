@@ -289,9 +289,9 @@ struct Lay {
     // the weights lie over the scores.
     static constexpr bool kApart = DP == 64;
     static constexpr int kQ = PROMPT ? 2 : 1;                      // row tiles of an item
-    static constexpr int kQB = DP == 128 ? 1 : 2;                  // items whose Q is held
-    static constexpr int kK = DP == 128 ? 3 : (PROMPT ? 5 : 6);    // K tiles in the ring
-    static constexpr int kV = DP == 128 ? (PROMPT ? 2 : 3) : 5;
+    static constexpr int kQB = DP == 128 && PROMPT ? 1 : 2;        // items whose Q is held
+    static constexpr int kK = DP == 128 ? (PROMPT ? 3 : 2) : (PROMPT ? 5 : 4);  // K tiles in the ring
+    static constexpr int kV = DP == 128 ? 2 : (PROMPT ? 5 : 4);
     static constexpr int kTiles = kQ * kQB + kK + kV;
     // after the tiles
     static constexpr int oKFull = kTiles * kBytes, oKEmpty = oKFull + 8 * kK;
