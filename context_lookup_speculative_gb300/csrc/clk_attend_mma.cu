@@ -7,8 +7,9 @@
 //
 // Work.  An item is one (request, K/V head, row tile); its work is a list of
 // 128-key tiles, those of the cached rows first, then those of the new
-// tokens.  All items' tiles in order form one line, which the CTAs (one per
-// SM) cut into equal shares: ragged contexts, causal rows of every length
+// tokens.  All items' tiles in order, with a few units before each item for
+// what it costs besides them, form one line, which the CTAs (one per SM) cut
+// into equal shares: ragged contexts, causal rows of every length
 // and a single long request all balance, whatever the batch.  An item that
 // a cut falls into is left as partial results (float32 sums and the
 // softmax's reference and sum per row).  The grid is launched cooperatively;
@@ -73,6 +74,7 @@ struct Shape {
     int32_t qbox, kbox;  // tokens of a box of q, rows of a box of new keys
     int32_t ctas;
     float log2_scale;  // scale * log2(e)
+    bool wide_out;     // rows of out are whole 32-byte sectors
 };
 
 // Scratch: a flag per CTA (a count of calls), row statistics and partial
@@ -171,26 +173,34 @@ __device__ __forceinline__ int new_tiles(const Reach& x, const Shape& S, int ite
     return (end - 1) / kTile + 1;
 }
 
-// Tiles of the items before `item` of one K/V head.
+// What an item costs besides its tiles (its result, the next one's start),
+// in tiles: about 6,000 cycles beside 2,100 a tile with prompts and 4,300
+// beside 1,800 with trees, rows of 64.  Counting it balances short items
+// with long ones: 16 prompts of 1,000 tokens on average 162 -> 102 us, 16
+// chunks behind prefixes 349 -> 293, 256 short requests 129 -> 114.
 template <bool PROMPT>
-__device__ __forceinline__ long long tiles_before(const Reach& x, const Shape& S, int item)
+constexpr int kExtra = PROMPT ? 4 : 3;
+
+// Units of the items before `item` of one K/V head.
+template <bool PROMPT>
+__device__ __forceinline__ long long units_before(const Reach& x, const Shape& S, int item)
 {
-    if (!PROMPT) return (long long)item * (x.ctx_tiles + 1);
+    if (!PROMPT) return (long long)item * (x.ctx_tiles + 1 + kExtra<PROMPT>);
     if (item <= 0) return 0;
     const bool all = item >= x.items;
     const int whole = all ? x.items - 1 : item;
-    long long n = (long long)item * x.ctx_tiles + whole + floor_sum(whole, kTile, S.block, S.block - 1);
+    long long n = (long long)item * (x.ctx_tiles + kExtra<PROMPT>) + whole + floor_sum(whole, kTile, S.block, S.block - 1);
     if (all) n += (x.rows - 1) / kTile + 1;
     return n;
 }
 
 template <bool PROMPT>
-__device__ __forceinline__ long long tiles_of(const Reach& x, const Shape& S)
+__device__ __forceinline__ long long units_of(const Reach& x, const Shape& S)
 {
-    return x.items == 0 ? 0 : tiles_before<PROMPT>(x, S, x.items);
+    return x.items == 0 ? 0 : units_before<PROMPT>(x, S, x.items);
 }
 
-// `all` tiles in shares of q or q + 1: the first r CTAs have one more.
+// `all` units in shares of q or q + 1: the first r CTAs have one more.
 struct Cuts {
     long long q;
     int r;
@@ -200,7 +210,7 @@ struct Cuts {
         r = (int)(all - q * ctas);
     }
     __device__ long long begin(int c) const { return q * c + (c < r ? c : r); }
-    // the CTA whose share holds tile g
+    // the CTA whose share holds unit g
     __device__ int holder(long long g) const
     {
         const long long big = (q + 1) * r;
@@ -210,9 +220,9 @@ struct Cuts {
 
 // What a CTA knows after planning (in shared memory).
 struct Plan {
-    long long all, g0, g1;  // tiles in all, this CTA's share
-    int ctas;               // CTAs that have work
-    int b, h, item, t;      // where the share begins
+    long long all, g0, g1;  // units in all, this CTA's share
+    int ctas;               // CTAs that have a share
+    int b, h, item, at;     // where the share begins: unit `at` of the item
     uint32_t call;          // this CTA's flag before this call
 };
 
@@ -220,53 +230,72 @@ struct Plan {
 struct Cut {
     Reach x;
     int b, h, item, total;  // total: its tiles, 0 for none
-    long long begin;        // its first one
+    long long begin;        // its first unit
 };
 
-// The CTA's way through its share, the same in every warp.  The softmax
-// warps keep theirs in shared memory: their registers are full.
+// The CTA's way through its share, segment by segment (an item's tiles t0 ..
+// t1-1), the same in every warp.  The softmax warps keep theirs in shared
+// memory: their registers are full.
 template <bool PROMPT>
 struct Walk {
     Reach x;
-    int b, h, item, t0, t1, total, left;  // left: tiles of the share from t0 on
+    int b, h, item, t0, t1, total;
+    int left;  // units of the share from this segment's on; 0 at the end
+    int took;  // this segment's units
+    int nth;   // segments before this one
 
     __device__ void start(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
         left = (int)(P.g1 - P.g0);
+        took = nth = 0;
         b = P.b;
         h = P.h;
         item = P.item;
-        if (left > 0) {
-            load(A, S, P, near);
-            cut(S, P.t);
-        }
+        if (left == 0) return;
+        load(A, S, P, near);
+        cut(S, P.at);
+        if (t0 == t1) skip(A, S, P, near);
     }
     __device__ void load(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
         const int i = b - P.b;
         x = i < kNear ? near[i] : reach_of<PROMPT>(attend_request(A, b, false), S);
     }
-    __device__ void cut(const Shape& S, int from)
+    // From unit `at` of the item on, as far as the share goes.
+    __device__ void cut(const Shape& S, int at)
     {
+        constexpr int extra = kExtra<PROMPT>;
         total = x.ctx_tiles + new_tiles<PROMPT>(x, S, item);
-        t0 = from;
-        t1 = total - from < left ? total : from + left;
+        took = extra + total - at < left ? extra + total - at : left;
+        t0 = at > extra ? at - extra : 0;
+        t1 = at + took > extra ? at + took - extra : 0;
+    }
+    // The next segment that has tiles.
+    __device__ void skip(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
+    {
+        do {
+            left -= took;
+            if (left <= 0) {
+                left = 0;
+                return;
+            }
+            if (++item == x.items) {
+                item = 0;
+                if (++h == A.kv_heads) {
+                    h = 0;
+                    do {
+                        ++b;
+                        load(A, S, P, near);
+                    } while (x.items == 0);
+                }
+            }
+            cut(S, 0);
+        } while (t0 == t1);
     }
     __device__ void next(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
-        left -= t1 - t0;
-        if (left <= 0) return;
-        if (++item == x.items) {
-            item = 0;
-            if (++h == A.kv_heads) {
-                h = 0;
-                do {
-                    ++b;
-                    load(A, S, P, near);
-                } while (x.items == 0);
-            }
-        }
-        cut(S, 0);
+        ++nth;
+        skip(A, S, P, near);
     }
     // Tiles [t0, last(s)) of this segment are stream s's, with prompts.
     __device__ int last(const Shape& S, int s) const
@@ -316,17 +345,17 @@ struct Count {
     static constexpr int value = N;
 };
 
-// This CTA's share of an item whose `total` tiles, from tile `begin` of the
-// line on, lie in several CTAs' shares.
+// This CTA's share of an item whose tiles lie in several CTAs' shares.
 template <int DP, bool BF16, bool PROMPT>
 __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const Scratch& W, uint32_t call, const Cuts& cuts,
                                           const Cut& cut, volatile int* stop)
 {
     constexpr int rows = PROMPT ? 2 * kTile : kTile;
     const int tid = threadIdx.x;
-    const int c0 = cuts.holder(cut.begin), c1 = cuts.holder(cut.begin + cut.total - 1), parts = c1 - c0 + 1;
-    // A CTA's second part begins after its share does.
-    const int first = 2 * c0 + (cuts.begin(c0) == cut.begin ? 0 : 1);
+    const long long tile0 = cut.begin + kExtra<PROMPT>;
+    const int c0 = cuts.holder(tile0), c1 = cuts.holder(tile0 + cut.total - 1), parts = c1 - c0 + 1;
+    // The first CTA's part is its second one where the tiles of an earlier item begin its share.
+    const int first = 2 * c0 + (cuts.begin(c0) >= cut.begin ? 0 : 1);
     auto part = [&](int c) { return c == 0 ? first : 2 * (c0 + c); };
     // All CTAs of the grid are resident, and none waits before it has raised its own flag.
     for (int c = tid; c < parts; c += kThreads) {
@@ -491,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 long long u = 0;
                 if (b < A.B) {
                     x = reach_of<PROMPT>(attend_request(A, b, pass == 0 && blockIdx.x == 0), S);
-                    u = tiles_of<PROMPT>(x, S) * A.kv_heads;
+                    u = units_of<PROMPT>(x, S) * A.kv_heads;
                 }
                 long long y = u;
 #pragma unroll
@@ -521,18 +550,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         z.rows = __shfl_sync(0xffffffffu, x.rows, src);
                         z.ctx_tiles = __shfl_sync(0xffffffffu, x.ctx_tiles, src);
                         z.items = __shfl_sync(0xffffffffu, x.items, src);
-                        const long long off = __shfl_sync(0xffffffffu, g0 - mine, src), per = tiles_of<PROMPT>(z, S);
+                        const long long off = __shfl_sync(0xffffffffu, g0 - mine, src), per = units_of<PROMPT>(z, S);
                         const int h = (int)quotient(off, per);
                         const long long o = off - h * per;
-                        // the last item with tiles_before <= o, 32 ways at a time
+                        // the last item with units_before <= o, 32 ways at a time
                         int lo = 0, span = z.items;
                         if (!PROMPT) {
-                            lo = (int)quotient(o, z.ctx_tiles + 1);
+                            lo = (int)quotient(o, z.ctx_tiles + 1 + kExtra<PROMPT>);
                             span = 1;
                         }
                         while (span > 1) {
                             const int step = (span + 31) / 32;
-                            const bool le = lane * step < span && tiles_before<PROMPT>(z, S, lo + lane * step) <= o;
+                            const bool le = lane * step < span && units_before<PROMPT>(z, S, lo + lane * step) <= o;
                             const int n = __popc(__ballot_sync(0xffffffffu, le));
                             const int end = lo + span;
                             lo += (n - 1) * step;
@@ -542,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                             plan.b = at + 32 * warp + src;
                             plan.h = h;
                             plan.item = lo;
-                            plan.t = (int)(o - tiles_before<PROMPT>(z, S, lo));
+                            plan.at = (int)(o - units_before<PROMPT>(z, S, lo));
                         }
                     }
                 }
@@ -736,10 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             const bool whole = w.t0 == 0 && w.t1 == w.total;
             if (!whole && tid == 0) {
                 // an item may fill the share: its cuts at both ends are one join
-                const long long end = plan.g1 - w.left + (w.t1 - w.t0);
-                cut[w.left == (int)(plan.g1 - plan.g0) ? 0 : 1] = Cut{w.x, w.b, w.h, w.item, w.total, end - w.t1};
+                const long long end = plan.g1 - w.left + w.took;
+                cut[w.nth == 0 ? 0 : 1] = Cut{w.x, w.b, w.h, w.item, w.total, end - w.t1 - kExtra<PROMPT>};
             }
-            const int slot = 2 * (int)blockIdx.x + (w.left == plan.g1 - plan.g0 ? 0 : 1);
+            const int slot = 2 * (int)blockIdx.x + (w.nth == 0 ? 0 : 1);
             constexpr int rows = PROMPT ? 2 * kTile : kTile;
             const int64_t out_row = (PROMPT ? (int64_t)w.x.base : (int64_t)w.b * A.N) + token;
             char* const out = static_cast<char*>(A.out) + ((out_row * A.q_heads + w.h * A.group + g) * A.dim) * 2;
@@ -785,14 +814,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 if (real) {
                     if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
+                        for (int e = 0; e < 32; e += 16) {
                             if (32 * c + e < A.dim) {
-                                uint4 y;
-                                y.x = pack2<BF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
-                                y.y = pack2<BF16>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                                y.z = pack2<BF16>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
-                                y.w = pack2<BF16>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
-                                *reinterpret_cast<uint4*>(out + (32 * c + e) * 2) = y;
+                                uint32_t y[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    y[i] = pack2<BF16>(__uint_as_float(o[e + 2 * i]), __uint_as_float(o[e + 2 * i + 1]));
+                                // a thread's row by whole sectors, where rows begin on one
+                                if (S.wide_out) {
+                                    store32(out + (32 * c + e) * 2, y);
+                                } else {
+                                    *reinterpret_cast<uint4*>(out + (32 * c + e) * 2) = make_uint4(y[0], y[1], y[2], y[3]);
+                                    if (32 * c + e + 8 < A.dim)
+                                        *reinterpret_cast<uint4*>(out + (32 * c + e + 8) * 2) = make_uint4(y[4], y[5], y[6], y[7]);
+                                }
                             }
                         }
                     } else {
@@ -1242,6 +1277,7 @@ int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)
     S.qbox = (int32_t)(S.tok < rows ? S.tok : rows);
     S.kbox = (int32_t)(kTile < rows ? kTile : rows);
     S.ctas = num_sms();
+    S.wide_out = A.dim % 16 == 0 && aligned(A.out, 32);
     S.log2_scale = (float)((double)A.scale * 1.4426950408889634);
     if (S.ctas < 1) return CLK_ECUDA;
     Maps M;

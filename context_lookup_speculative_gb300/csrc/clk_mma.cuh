@@ -191,6 +191,14 @@ __device__ __forceinline__ void tmem_loaded16(uint32_t* r)
 #undef CLK_R32
 #undef CLK_R16
 
+// 32 bytes to an address that is a multiple of 32.
+__device__ __forceinline__ void store32(void* p, const uint32_t* y)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+                 "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
