@@ -181,6 +181,15 @@ __device__ __forceinline__ int new_tiles(const Reach& x, const Shape& S, int ite
 template <bool PROMPT>
 constexpr int kExtra = PROMPT ? 4 : 3;
 
+// Items of at most so many tiles are not cut: joining parts takes 10,000
+// cycles and more.  They go to the CTA that holds their middle unit.
+// Measured on prompts without a limit, of 8 and of 16 tiles: one of 1,000
+// tokens 34.6, 21.8, 21.6 us; 16 of about 1,000 147, 140, 130 us; one of
+// 4,000 114, 114, 116 us.  256 requests of 64 to 512 tokens: without 63.0, of
+// 4 tiles 59.1 us.
+template <bool PROMPT>
+constexpr int kWhole = PROMPT ? 16 : 4;
+
 // Units of the items before `item` of one K/V head.
 template <bool PROMPT>
 __device__ __forceinline__ long long units_before(const Reach& x, const Shape& S, int item)
@@ -242,19 +251,18 @@ struct Walk {
     int b, h, item, t0, t1, total;
     int left;  // units of the share from this segment's on; 0 at the end
     int took;  // this segment's units
-    int nth;   // segments before this one
 
     __device__ void start(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
         left = (int)(P.g1 - P.g0);
-        took = nth = 0;
+        took = 0;
         b = P.b;
         h = P.h;
         item = P.item;
         if (left == 0) return;
         load(A, S, P, near);
         cut(S, P.at);
-        if (t0 == t1) skip(A, S, P, near);
+        if (t0 == t1) next(A, S, P, near);
     }
     __device__ void load(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
@@ -267,11 +275,17 @@ struct Walk {
         constexpr int extra = kExtra<PROMPT>;
         total = x.ctx_tiles + new_tiles<PROMPT>(x, S, item);
         took = extra + total - at < left ? extra + total - at : left;
-        t0 = at > extra ? at - extra : 0;
-        t1 = at + took > extra ? at + took - extra : 0;
+        if (total <= kWhole<PROMPT>) {
+            const int middle = (extra + total) / 2;
+            t0 = 0;
+            t1 = at <= middle && middle < at + took ? total : 0;
+        } else {
+            t0 = at > extra ? at - extra : 0;
+            t1 = at + took > extra ? at + took - extra : 0;
+        }
     }
     // The next segment that has tiles.
-    __device__ void skip(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
+    __device__ void next(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
         do {
             left -= took;
@@ -291,11 +305,6 @@ struct Walk {
             }
             cut(S, 0);
         } while (t0 == t1);
-    }
-    __device__ void next(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
-    {
-        ++nth;
-        skip(A, S, P, near);
     }
     // Tiles [t0, last(s)) of this segment are stream s's, with prompts.
     __device__ int last(const Shape& S, int s) const
@@ -332,7 +341,7 @@ struct Lay {
     static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
     static constexpr int oNear = oBad + 16 * kV;                      // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
-    static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: where the share begins, where it ends
+    static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: of items that end here, that begin here
     static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[8]
     static constexpr int oStop = oWalk + 8 * (int)sizeof(Walk<PROMPT>), oTmem = oStop + 4;
     static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;          // float2[2][128] for trees
@@ -354,9 +363,7 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
     const int tid = threadIdx.x;
     const long long tile0 = cut.begin + kExtra<PROMPT>;
     const int c0 = cuts.holder(tile0), c1 = cuts.holder(tile0 + cut.total - 1), parts = c1 - c0 + 1;
-    // The first CTA's part is its second one where the tiles of an earlier item begin its share.
-    const int first = 2 * c0 + (cuts.begin(c0) >= cut.begin ? 0 : 1);
-    auto part = [&](int c) { return c == 0 ? first : 2 * (c0 + c); };
+    auto part = [&](int c) { return 2 * (c0 + c) + (c == 0 ? 1 : 0); };
     // All CTAs of the grid are resident, and none waits before it has raised its own flag.
     for (int c = tid; c < parts; c += kThreads) {
         uint32_t seen;
@@ -517,11 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             long long before = 0;
             for (int at = 0; at < A.B; at += kThreads) {
                 const int b = at + tid;
-                long long u = 0;
+                long long each = 0;  // units of one K/V head
                 if (b < A.B) {
                     x = reach_of<PROMPT>(attend_request(A, b, pass == 0 && blockIdx.x == 0), S);
-                    u = units_of<PROMPT>(x, S) * A.kv_heads;
+                    each = units_of<PROMPT>(x, S);
                 }
+                const long long u = each * A.kv_heads;
                 long long y = u;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -550,28 +558,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         z.rows = __shfl_sync(0xffffffffu, x.rows, src);
                         z.ctx_tiles = __shfl_sync(0xffffffffu, x.ctx_tiles, src);
                         z.items = __shfl_sync(0xffffffffu, x.items, src);
-                        const long long off = __shfl_sync(0xffffffffu, g0 - mine, src), per = units_of<PROMPT>(z, S);
+                        const long long off = __shfl_sync(0xffffffffu, g0 - mine, src), per = __shfl_sync(0xffffffffu, each, src);
                         const int h = (int)quotient(off, per);
                         const long long o = off - h * per;
-                        // the last item with units_before <= o, 32 ways at a time
-                        int lo = 0, span = z.items;
+                        // the last item with units_before <= o, and those units
+                        int lo = 0;
+                        long long below = 0;
                         if (!PROMPT) {
                             lo = (int)quotient(o, z.ctx_tiles + 1 + kExtra<PROMPT>);
-                            span = 1;
+                            below = units_before<PROMPT>(z, S, lo);
                         }
-                        while (span > 1) {
-                            const int step = (span + 31) / 32;
-                            const bool le = lane * step < span && units_before<PROMPT>(z, S, lo + lane * step) <= o;
-                            const int n = __popc(__ballot_sync(0xffffffffu, le));
-                            const int end = lo + span;
-                            lo += (n - 1) * step;
+                        for (int span = PROMPT ? z.items : 1; span > 1;) {  // 32 ways at a time
+                            const int step = (span + 31) / 32, end = lo + span;
+                            const long long n = lane * step < span ? units_before<PROMPT>(z, S, lo + lane * step) : o + 1;
+                            const int last = __popc(__ballot_sync(0xffffffffu, n <= o)) - 1;
+                            below = __shfl_sync(0xffffffffu, n, last);
+                            lo += last * step;
                             span = lo + step < end ? step : end - lo;
                         }
                         if (lane == 0) {
                             plan.b = at + 32 * warp + src;
                             plan.h = h;
                             plan.item = lo;
-                            plan.at = (int)(o - units_before<PROMPT>(z, S, lo));
+                            plan.at = (int)(o - below);
                         }
                     }
                 }
@@ -766,9 +775,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             if (!whole && tid == 0) {
                 // an item may fill the share: its cuts at both ends are one join
                 const long long end = plan.g1 - w.left + w.took;
-                cut[w.nth == 0 ? 0 : 1] = Cut{w.x, w.b, w.h, w.item, w.total, end - w.t1 - kExtra<PROMPT>};
+                cut[w.t0 > 0 ? 0 : 1] = Cut{w.x, w.b, w.h, w.item, w.total, end - w.t1 - kExtra<PROMPT>};
             }
-            const int slot = 2 * (int)blockIdx.x + (w.nth == 0 ? 0 : 1);
+            // the part that begins an item is the CTA's second, so that it never meets the one that ends an item
+            const int slot = 2 * (int)blockIdx.x + (w.t0 > 0 ? 0 : 1);
             constexpr int rows = PROMPT ? 2 * kTile : kTile;
             const int64_t out_row = (PROMPT ? (int64_t)w.x.base : (int64_t)w.b * A.N) + token;
             char* const out = static_cast<char*>(A.out) + ((out_row * A.q_heads + w.h * A.group + g) * A.dim) * 2;
