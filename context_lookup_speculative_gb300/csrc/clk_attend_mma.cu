@@ -679,64 +679,76 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
 #pragma unroll
                     for (int c = 64; c < kTile; ++c) x[c] = 0xff800000u;
                 }
-                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < kTile; c += 8)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        m[e] = max3(m[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
-                const float top = max3(m[0], m[1], fmaxf(m[2], m[3]));
                 if (L::kApart && j > 0) {
                     // this stream's last product is done with O and the weights
                     if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
                     od ^= 1;
                     tmem_after();
                 }
-                const bool grow = top > ref + slack || (ref == -INFINITY && top > -INFINITY);
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float to = grow ? top : ref;
-                    const float fix = grow ? exp2_fast((ref - to) * cs) : 1.0f;
-                    ref = to;
-                    sum *= fix;
-                    if (j > 0) {
-                        // O is complete: weights over the scores mean that these scores' product was issued after
-                        // this stream's last P V; else it was waited for.
+                // The reference of the weights.  Where they lie apart from the scores it is not compared with every
+                // tile's maximum: the sum of the tile's weights shows when one has grown too large (over 2^15), and
+                // the tile is done again.  That spares the maximum's 64 instructions in nearly all tiles; a row's
+                // first tile always takes it.
+                bool look = !L::kApart || __any_sync(0xffffffffu, real && ref == -INFINITY);
+                float2 both;
+                for (;;) {
+                    if (look) {
+                        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < DP / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_load16(tO + 16 * c, o);
-                            tmem_load_wait();
-                            tmem_loaded16(o);
+                        for (int c = 0; c < kTile; c += 8)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
-                            tmem_store16(tO + 16 * c, o);
+                            for (int e = 0; e < 4; ++e)
+                                m[e] = max3(m[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+                        const float top = max3(m[0], m[1], fmaxf(m[2], m[3]));
+                        const bool grow = top > ref + slack;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float to = grow ? top : ref;
+                            const float fix = grow ? exp2_fast((ref - to) * cs) : 1.0f;
+                            ref = to;
+                            sum *= fix;
+                            if (j > 0) {
+                                // O is complete: weights over the scores mean that these scores' product was issued
+                                // after this stream's last P V; else it was waited for.
+#pragma unroll
+                                for (int c = 0; c < DP / 16; ++c) {
+                                    uint32_t o[16];
+                                    tmem_load16(tO + 16 * c, o);
+                                    tmem_load_wait();
+                                    tmem_loaded16(o);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                                    tmem_store16(tO + 16 * c, o);
+                                }
+                            }
                         }
                     }
-                }
-                const float shift = ref == -INFINITY ? 0.0f : lift - ref * cs;
-                // Weights, 64 keys at a time: the first half's product starts while the second is computed.
-                const uint64_t cs2 = pair(__float_as_uint(cs), __float_as_uint(cs));
-                const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
-                uint64_t part[2] = {0, 0};
+                    const float shift = ref == -INFINITY ? 0.0f : lift - ref * cs;
+                    const uint64_t cs2 = pair(__float_as_uint(cs), __float_as_uint(cs));
+                    const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
+                    uint64_t part[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t y[16];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t y[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 z = unpair(fma2(pair(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), cs2, shift2));
-                        const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
-                        part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                        y[e] = pack2<BF16>(p0, p1);
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 z = unpair(fma2(pair(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), cs2, shift2));
+                            const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
+                            part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                            y[e] = pack2<BF16>(p0, p1);
+                        }
+                        tmem_store16(tP + 16 * c, y);
+                        if (c == 1 && !L::kApart) {
+                            // the first half's product starts while the second half is computed
+                            tmem_store_wait();
+                            tmem_before();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
+                        }
                     }
-                    tmem_store16(tP + 16 * c, y);
-                    if (c == 1 && !L::kApart) {
-                        tmem_store_wait();
-                        tmem_before();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
-                    }
+                    both = unpair(add2(part[0], part[1]));
+                    if (look || !__any_sync(0xffffffffu, real && both.x + both.y > 32768.0f)) break;
+                    look = true;
                 }
-                const float2 both = unpair(add2(part[0], part[1]));
                 sum += both.x + both.y;
                 if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
                     // Rows of V that were not finite: NaN for those who see them.

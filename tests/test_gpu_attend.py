@@ -529,3 +529,24 @@ def test_keys_and_values_of_different_strides():
     t.v = t.v.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
     t.q = t.q.contiguous()
     t.run().check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("step", [2.0, 9.0, 60.0])
+def test_maxima_that_rise_tile_after_tile(kind, step):
+    """Every 128 keys the scores rise by `step` (log2 units), slowly and in jumps, in some rows only."""
+    D, n = 64, 1300
+    t = Tree(24, 2, 4, [n, n - 37], 2, 1, D, 128, kind, nodes=[4, 4], scale=math.log(2.0) / 8)
+    for s in range(2):
+        for i in range(-(-n // 128)):
+            # element 0 of the keys carries the level: scores = 8 * level * q0 / 8 log2 units
+            page = t.cache.table[s, i].long()
+            if page >= 0:
+                t.pool[0, page, 0] *= 0.1
+                t.pool[0, page, 0, :, 0] = step * i
+    t.q.mul_(0.1)
+    t.q[..., 0] = 1.0
+    t.q[:, 1, 0, 0] = -1.0  # a row whose scores fall
+    t.q[:, 2, 1, 0] = 0.0   # and one where they stay
+    t.k.mul_(0.1)
+    t.run().check()
