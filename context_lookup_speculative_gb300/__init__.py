@@ -552,19 +552,9 @@ class Cache:
         self.handle = h
         self.max_slots, self.max_pages, self.num_pages = max_slots, max_pages, num_pages
         self.page_tokens = page_tokens
-        at = [_P(), _P(), _P()]
-        _check("clk_cache_buffers", L.clk_cache_buffers(h, *(ctypes.byref(p) for p in at)))
-        words = self.workspace[:n.value // 4 * 4].view(torch.int32)
-
-        def view(p, *shape):
-            first = (p.value - base) // 4
-            size = 1
-            for x in shape:
-                size *= x
-            return words[first:first + size].view(*shape)
-
-        self.length, self.table = view(at[0], max_slots), view(at[1], max_slots, max_pages)
-        self.refs = view(at[2], num_pages)
+        self._at = [_P(), _P(), _P()]
+        _check("clk_cache_buffers", L.clk_cache_buffers(h, *(ctypes.byref(p) for p in self._at)))
+        self._views = [None, None, None]
         self.reset(stream)
 
     def __del__(self):
@@ -575,6 +565,27 @@ class Cache:
             except Exception:
                 pass
             self.handle = None
+
+    def _view(self, i: int, *shape):
+        if self._views[i] is None:
+            size = 1
+            for x in shape:
+                size *= x
+            first = self._at[i].value - self.workspace.data_ptr()
+            self._views[i] = self.workspace[first:first + 4 * size].view(torch.int32).view(shape)
+        return self._views[i]
+
+    @property
+    def length(self) -> torch.Tensor:
+        return self._view(0, self.max_slots)
+
+    @property
+    def table(self) -> torch.Tensor:
+        return self._view(1, self.max_slots, self.max_pages)
+
+    @property
+    def refs(self) -> torch.Tensor:
+        return self._view(2, self.num_pages)
 
     def reset(self, stream=None):
         """Every slot empty, every page free."""
