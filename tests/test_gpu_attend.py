@@ -550,3 +550,36 @@ def test_maxima_that_rise_tile_after_tile(kind, step):
     t.q[:, 2, 1, 0] = 0.0   # and one where they stay
     t.k.mul_(0.1)
     t.run().check()
+
+
+# -- the general kernel's shares: rows a warp, warps a tile, CTAs a row ---
+@pytest.mark.parametrize("kind,D", [("f32", 40), ("f32", 128), ("bf16", 250)])
+@pytest.mark.parametrize("B,N,G", [(1, 1, 1), (1, 1, 5), (1, 2, 2), (1, 4, 3), (1, 9, 3), (1, 16, 2), (1, 64, 1), (3, 5, 33), (1, 1, 70),
+                                   (40, 3, 4)])
+def test_shares_of_the_general_kernel_for_trees(B, N, G, kind, D):
+    ctx = [(700, 0, 64, 1, 513, 129)[b % 6] for b in range(B)]
+    nodes = [N if b % 3 == 0 else max(0, N - b % 4) for b in range(B)]
+    Tree(B + N + G, B, N, ctx, G, 1, D, 32, kind, nodes=nodes).run().check()
+
+
+@pytest.mark.parametrize("lens", [[1], [8], [300], [5] * 30, [33, 0, 420, 1]])
+@pytest.mark.parametrize("G", [1, 3, 40])
+@pytest.mark.parametrize("kind,D", [("f32", 40), ("f16", 200)])
+def test_shares_of_the_general_kernel_for_prompts(lens, G, kind, D):
+    Prompt(len(lens) + G, lens, G, 1, D, kind, ctx=[(130, 0, 64)[b % 3] for b in range(len(lens))]).run().check(rows=12)
+
+
+@pytest.mark.parametrize("D", [40, 160])
+def test_hidden_values_in_the_general_kernel(D):
+    """A new token that only some rows see holds NaN: the others' results are what they are without it."""
+    mask = [[1, 3, 5, 9, 17, 1, 1, 1]]  # token 3 is seen by itself alone
+    nodes = [8]
+    a = Tree(3, 1, 8, [200], 2, 1, D, 16, "f32", nodes=nodes, mask=mask)
+    a.run().check()
+    want = a.out.clone()
+    a.v[0, 3] = NAN
+    a.k[0, 4] = INF
+    a.run()
+    keep = [t for t in range(8) if t not in (3, 4)]
+    assert torch.equal(a.out[0, keep], want[0, keep])
+    assert a.out[0, 3].isnan().all()
