@@ -760,6 +760,8 @@ def prompt_attend(q, k, v, offsets, scale: float, out, scratch, cache: Optional[
     B = offsets.numel() - 1
     if cache is None and (slots is not None or pool is not None or ctx is not None):
         raise ValueError("slots, pool and ctx need a cache")
+    if cache is not None and (slots is None or pool is None):
+        raise ValueError("a cache needs slots and a pool")
     d = _pool_desc(cache, pool) if cache is not None else None
     a = _attn_desc(q, k, v, out, scale)
     _check("clk_prompt_attend",
