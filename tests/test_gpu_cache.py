@@ -304,3 +304,21 @@ def test_in_a_graph_and_on_another_stream():
         c.m.fork([0, 1], [2, 3])
         c.m.compact()
         c.check()
+
+
+@pytest.mark.parametrize("max_slots,max_pages", [(12, 9), (12, 170), (12, 171), (2000, 9)])
+def test_compaction_of_small_and_large_tables(max_slots, max_pages):
+    """One CTA rewrites small tables, one per slot large ones (the limit lies between 170 and 171)."""
+    c = Both(max_slots, max_pages, 70, 16, layers=1, heads=2, dim=8)
+    slots, counts = [4, 0, 9, 2], [3 * 16 + 5, 16, 33, 90]
+    assert c.grow(slots, counts) == []
+    c.append(slots, counts, packed=True)
+    assert c.m.fork([4, 2, 2], [1, 3, 11]) == []
+    clk.cache_fork(c.h, ints([4, 2, 2]), ints([1, 3, 11]), c.pool)
+    for gone in ([0, 4], [2], [1, 9]):
+        c.m.free(gone)
+        clk.cache_free(c.h, ints(gone))
+        moved = ints([-1])
+        clk.cache_compact(c.h, c.pool, moved)
+        assert moved.tolist() == [c.m.compact()]
+        c.check()
