@@ -41,10 +41,10 @@
 // key gets NaN for its sum.
 //
 // Bounds and figures.  Trees stream K and V: 64 requests of 2,000 to 32,000
-// tokens (heads 32/8 of 128, 4.8 GB) 692 us, 8 of 262,144 (16/2 heads) 317 us,
+// tokens (heads 32/8 of 128, 4.8 GB) 690 us, 8 of 262,144 (16/2 heads) 317 us,
 // 6.9 TB/s; one token over 2,048 rows 14 us, launch, planning and joining.
 // Prompts of rows of 128 are bound by the products: 25,000 tokens 3.1 ms,
-// 1,646 TFLOP/s of the causal half, a step of two row tiles 2,350 cycles of
+// 1,640 TFLOP/s of the causal half, a step of two row tiles 2,350 cycles of
 // which 2,048 are products.  Rows of 64 have half the products a weight, and
 // the softmax bounds them: 2,100 cycles a step, of which the products are
 // 1,024; so their P has columns of its own beside S (the next scores need not
