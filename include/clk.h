@@ -645,8 +645,8 @@ CLK_API int clk_tree_accept(int32_t B, int32_t N, const int32_t* d_tok, const in
  * (rows of a page past ctx, nodes off the mask, other requests): with one
  * rule, a row that does see a new token with an infinity or a NaN in its v
  * may be NaN in every element.  Scores, the softmax's maximum and sum and
- * the accumulators are float32; on the tensor cores (16-bit types, dim 64 to
- * 128) each weight is rounded to the inputs' type for the product with v, and
+ * the accumulators are float32; on the tensor cores (16-bit types, dim a
+ * multiple of 8 up to 128) each weight is rounded to the inputs' type for the product with v, and
  * the sum of weights is of the unrounded ones.  out must not overlap an input. */
 typedef struct clk_attn {
     int32_t dtype, q_heads, kv_heads, dim;

@@ -583,3 +583,11 @@ def test_hidden_values_in_the_general_kernel(D):
     keep = [t for t in range(8) if t not in (3, 4)]
     assert torch.equal(a.out[0, keep], want[0, keep])
     assert a.out[0, 3].isnan().all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [8, 16, 24, 32, 48, 56, 72, 104])
+def test_rows_that_do_not_fill_a_tile(kind, D):
+    """Tensor-core tiles of 64 or 128 columns, of which D are there."""
+    Tree(D, 3, 5, [300, 0, 129], 3, 2, D, 32, kind, nodes=[5, 3, 1]).run().check()
+    Prompt(D, [140, 1, 260], 3, 2, D, kind, ctx=[40, 200, 0]).run().check(rows=15)
