@@ -14,7 +14,7 @@
 // 8 layers of 8 heads of 128 in 16 bits, taken in, half of them freed and the
 // rest compacted: 853 us for 5.7 GB, 98% of the copy rate.  The end of a step
 // for 64 such requests of 16 drafted tokens (free, fork, masks, accept, grow,
-// append): 59 us, of which the fork's copy of the tails is 26 (20 at the copy
+// append): 56 us, of which the fork's copy of the tails is 23 (20 at the copy
 // rate) and the rest six launches' dependent loads; for one request 17 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -312,23 +312,21 @@ __device__ __forceinline__ void copy_page(const VecPool<V>& A, int64_t src, int6
     }
 }
 
-// A CTA moves kRows rows at a time in every head of planes p0 .. p1-1: their
+// A CTA moves `group` rows in every head of planes p0 .. p1-1: their
 // sources and places (in vectors, -1 for none) are found once, by as many
 // threads, and lie in shared memory.
-constexpr int kRows = 8;
+constexpr int kFewRows = 8, kMostRows = 32;
 
 template <typename V, typename Plane>
-__device__ __forceinline__ void move_rows(const int64_t* from, const int64_t* to, const VecPool<V>& A, int64_t src_head, int p0,
-                                          int p1, Plane plane_of)
+__device__ __forceinline__ void move_rows(const int64_t* from, const int64_t* to, int group, const VecPool<V>& A,
+                                          int64_t src_head, int p0, int p1, Plane plane_of)
 {
     const int wide = A.row < kCopyThreads ? A.row : kCopyThreads;
     const int tall = kCopyThreads / wide;
     const int c0 = threadIdx.x % wide, t0 = threadIdx.x / wide;
     if (t0 >= tall) return;
-    int live = 0;  // rows past the last one that moves need no turn
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-        if (to[r] >= 0) live = r + 1;
+    int live = group;  // rows past the last one that moves need no turn
+    while (live > 0 && to[live - 1] < 0) --live;
     const int lines = live * A.heads;
     for (int plane = p0; plane < p1; ++plane) {
         const V* src;
@@ -360,22 +358,22 @@ __device__ __forceinline__ void move_rows(const int64_t* from, const int64_t* to
 
 // Destination b shares the source's whole pages (the CTAs with blockIdx.y = 0
 // write the tables) and its tail's rows are copied: the tails of all
-// requests lie one after the other, kRows rows a CTA, so that tails of every
-// length balance; blockIdx.y takes a share of the planes.  (With 16 CTAs per
-// SM for eight the copy takes 34 us for 25: more CTAs find the same places.)
+// requests lie one after the other, `group` rows a CTA, so that tails of every
+// length balance; blockIdx.y takes a share of the planes.  (Measured with shares
+// for 4, 8 and 16 CTAs an SM: 23, 26 and 34 us. More CTAs find the same places.)
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) k_cache_fork(CacheDev C, const int32_t* src, const int32_t* dst, int32_t B,
-                                                             VecPool<V> A)
+                                                             VecPool<V> A, int32_t group)
 {
     chained();
-    __shared__ int64_t from[kRows], to[kRows];
+    __shared__ int64_t from[kMostRows], to[kMostRows];
     __shared__ int32_t before[kCopyThreads];
     const int rows = C.list[3 * (int64_t)C.num_pages + 2];
     const bool few = B <= kCopyThreads;
     if (few && threadIdx.x < B) before[threadIdx.x] = C.req[threadIdx.x].x;
     __syncthreads();
-    const int64_t at = (int64_t)blockIdx.x * kRows + threadIdx.x;
-    if (threadIdx.x < kRows) {
+    const int64_t at = (int64_t)blockIdx.x * group + threadIdx.x;
+    if (threadIdx.x < group) {
         int64_t a = -1, z = -1;
         if (at < rows) {
             // the last request whose rows start at or before this one
@@ -412,9 +410,9 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_fork(CacheDev C, const i
         }
     }
     __syncthreads();
-    if ((int64_t)blockIdx.x * kRows >= rows) return;
+    if ((int64_t)blockIdx.x * group >= rows) return;
     const int p0 = (int)((int64_t)A.planes * blockIdx.y / gridDim.y), p1 = (int)((int64_t)A.planes * (blockIdx.y + 1) / gridDim.y);
-    move_rows(from, to, A, A.head, p0, p1, [&](int plane, const V*& s, V*& d) { s = d = A.base + plane * A.plane; });
+    move_rows(from, to, group, A, A.head, p0, p1, [&](int plane, const V*& s, V*& d) { s = d = A.base + plane * A.plane; });
 }
 
 // Rows of the new tokens into the pages; blockIdx.y takes a share of the planes.
@@ -434,12 +432,12 @@ struct VecSrc {
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const int32_t* slots, int32_t B, VecPool<V> A,
                                                                int32_t layer0, int32_t planes, VecSrc<V> S, int64_t N, const int64_t* off,
-                                                               const int32_t* path, const int32_t* count)
+                                                               const int32_t* path, const int32_t* count, int32_t group)
 {
     chained();
-    __shared__ int64_t from[kRows], to[kRows];
+    __shared__ int64_t from[kMostRows], to[kMostRows];
     const int64_t total = off != nullptr ? N : (int64_t)B * N;
-    const int64_t first = (int64_t)blockIdx.x * kRows;
+    const int64_t first = (int64_t)blockIdx.x * group;
     __shared__ int64_t begin[kCopyThreads];
     const bool few = off != nullptr && B < kCopyThreads;
     if (few && threadIdx.x <= B) begin[threadIdx.x] = off[threadIdx.x];
@@ -456,7 +454,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
                 latch(C.status, CLK_EINVAL, s);
         }
     }
-    if (threadIdx.x < kRows) {
+    if (threadIdx.x < group) {
         const int64_t at = first + threadIdx.x;
         int64_t row = -1, place = -1;
         int b = -1;
@@ -503,7 +501,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
     }
     __syncthreads();
     const int p0 = (int)((int64_t)planes * blockIdx.y / gridDim.y), p1 = (int)((int64_t)planes * (blockIdx.y + 1) / gridDim.y);
-    move_rows(from, to, A, S.head, p0, p1, [&](int plane, const V*& s, V*& d) {
+    move_rows(from, to, group, A, S.head, p0, p1, [&](int plane, const V*& s, V*& d) {
         s = (plane & 1 ? S.v : S.k) + (plane >> 1) * S.layer;
         d = A.base + (2 * (int64_t)layer0 + plane) * A.plane;
     });
@@ -655,14 +653,32 @@ int with_vector(int bytes, F f)
     }
 }
 
-// Shares of the planes for `groups` groups of rows: until there are about
-// eight CTAs an SM, one wave (more would only find the same rows' places
-// again).
-unsigned plane_shares(int64_t groups, int32_t planes)
+// How `rows` rows, `bytes` each in all planes, are dealt out: groups of so
+// many, and shares of the planes until there are about four CTAs an SM.
+// Finding a group's places is a chain of loads, the same for every size, so a
+// CTA takes more rows where they are short, as long as the SMs have one each.
+// A cache's life by groups of 8 and of these: 64 prompts of 2,000 in one layer
+// of 4 heads of 64 94.6 and 60.6 us (32), of 8 heads of 128 141 and 136 (16);
+// with 8 layers 8 is best (853; 16 859, 32 865).  Eight CTAs an SM for four:
+// the end of a step for 64 requests 59 us for 56.
+struct Deal {
+    int32_t group;
+    int64_t groups;
+    unsigned shares;
+};
+
+Deal deal(int64_t rows, int64_t bytes, int32_t planes)
 {
-    const int64_t want = (8 * (int64_t)num_sms() + groups - 1) / groups;
-    return (unsigned)(want < 1 ? 1 : want < planes ? want : planes);
+    const int64_t sms = num_sms();
+    Deal d{kFewRows, 0, 1};
+    while (d.group < kMostRows && d.group * bytes < 65536 && rows * planes >= 2 * d.group * sms) d.group *= 2;
+    d.groups = (rows + d.group - 1) / d.group;
+    const int64_t want = (4 * sms + d.groups - 1) / (d.groups > 0 ? d.groups : 1);
+    d.shares = (unsigned)(want < 1 ? 1 : want < planes ? want : planes);
+    return d;
 }
+
+int64_t token_bytes(const clk_pool& p, int32_t planes) { return (int64_t)planes * p.heads * p.dim * dtype_bytes(p.dtype); }
 
 }  // namespace
 }  // namespace clk
@@ -778,12 +794,12 @@ extern "C" int clk_cache_fork(clk_cache* h, const int32_t* d_src, const int32_t*
     if (!ok_i32(d_src) || !ok_i32(d_dst)) return CLK_EINVAL;
     rc = launch_chained(k_cache_plan<true>, 1, kPlanThreads, (cudaStream_t)s, h->dev, d_src, d_dst, (const int32_t*)nullptr, B);
     if (rc != CLK_OK) return rc;
-    const int64_t groups = ((int64_t)B * (h->dev.page_tokens() - 1) + kRows - 1) / kRows;
-    const unsigned x = (unsigned)(groups > B ? groups : B);
+    const Deal deals = deal((int64_t)B * (h->dev.page_tokens() - 1), token_bytes(*pool, pool->planes), pool->planes);
+    const unsigned x = (unsigned)(deals.groups > B ? deals.groups : B);
     return with_vector(vector_bytes(*pool, 0), [&](auto v) {
         using V = decltype(v);
-        return launch_chained(k_cache_fork<V>, dim3(x, plane_shares(x, pool->planes)), kCopyThreads, (cudaStream_t)s, h->dev, d_src,
-                            d_dst, B, vec_pool<V>(*pool));
+        return launch_chained(k_cache_fork<V>, dim3(x, deals.shares), kCopyThreads, (cudaStream_t)s, h->dev, d_src, d_dst, B,
+                            vec_pool<V>(*pool), deals.group);
     });
 }
 
@@ -802,8 +818,9 @@ extern "C" int clk_cache_append(clk_cache* h, const int32_t* d_slots, int32_t B,
         return CLK_EINVAL;
     if ((d_off != nullptr && (!aligned(d_off, 8) || d_path != nullptr)) || !aligned(d_path, 4)) return CLK_EINVAL;
     const int64_t rows = d_off != nullptr ? N : (N > ((int64_t)1 << 40) / B ? -1 : N * B);
-    const int64_t blocks = rows < 0 ? -1 : (rows + kRows - 1) / kRows;
-    if (blocks < 0 || blocks > 0x7fffffff) return CLK_EINVAL;
+    if (rows < 0) return CLK_EINVAL;
+    const Deal deals = deal(rows, token_bytes(*pool, 2 * layers), 2 * layers);
+    if (deals.groups > 0x7fffffff) return CLK_EINVAL;
     const int64_t b = (int64_t)es;
     const int64_t more = (int64_t)(uintptr_t)d_k | (int64_t)(uintptr_t)d_v | layer_stride * b | row_stride * b | head_stride * b;
     return with_vector(vector_bytes(*pool, more), [&](auto v) {
@@ -811,9 +828,8 @@ extern "C" int clk_cache_append(clk_cache* h, const int32_t* d_slots, int32_t B,
         const int64_t w = (int64_t)sizeof(V);
         const VecSrc<V> src{static_cast<const V*>(d_k), static_cast<const V*>(d_v), layer_stride * b / w, row_stride * b / w,
                             head_stride * b / w};
-        return launch_chained(k_cache_append<V>, dim3((unsigned)blocks, plane_shares(blocks, 2 * layers)), kCopyThreads,
-                              (cudaStream_t)s, h->dev, d_slots, B, vec_pool<V>(*pool), layer0, 2 * layers, src, N, d_off, d_path,
-                              d_count);
+        return launch_chained(k_cache_append<V>, dim3((unsigned)deals.groups, deals.shares), kCopyThreads, (cudaStream_t)s, h->dev,
+                              d_slots, B, vec_pool<V>(*pool), layer0, 2 * layers, src, N, d_off, d_path, d_count, deals.group);
     });
 }
 

@@ -322,3 +322,25 @@ def test_compaction_of_small_and_large_tables(max_slots, max_pages):
         clk.cache_compact(c.h, c.pool, moved)
         assert moved.tolist() == [c.m.compact()]
         c.check()
+
+
+@pytest.mark.parametrize("layers,dim", [(1, 8), (2, 8), (4, 16), (2, 200)])
+def test_groups_of_rows_of_every_size(layers, dim):
+    """8, 16 or 32 rows a CTA, by their size and number: packed rows, paths, and tails of forks, ragged at every end."""
+    rng = np.random.default_rng(layers + dim)
+    c = Both(140, 5, 400, 16, layers=layers, heads=1, dim=dim)
+    slots = rng.permutation(70).tolist()
+    counts = [int(x) for x in rng.integers(0, 60, size=70)]
+    assert c.grow(slots, counts) == []
+    c.append(slots, counts, packed=True)
+    c.check()
+    dst = [70 + b for b in range(70)]
+    bad = c.m.fork(slots, dst)
+    assert bad == []
+    clk.cache_fork(c.h, ints(slots), ints(dst), c.pool)
+    c.check()
+    path = [sorted(rng.choice(13, size=1 + b % 5, replace=False).tolist()) for b in range(70)]
+    counts = [len(p) for p in path]
+    assert c.grow(dst, counts) == []
+    c.append(dst, counts, path=path)
+    c.check()
