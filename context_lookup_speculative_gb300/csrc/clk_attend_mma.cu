@@ -759,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     both = unpair(add2(part[0], part[1]));
                     if (look || !__any_sync(0xffffffffu, real && both.x + both.y > 32768.0f)) break;
                     look = true;
+                    tmem_store_wait();  // stores to the same columns follow: only this wait orders two of them
                 }
                 sum += both.x + both.y;
                 if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
