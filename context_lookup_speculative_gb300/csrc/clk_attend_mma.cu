@@ -398,6 +398,7 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
     const int all = used * quads;
     const int lo = (int)((long long)all * mine / parts), hi = (int)((long long)all * (mine + 1) / parts);
     const float4* const sums = reinterpret_cast<const float4*>(W.sums);
+    const float cs = S.log2_scale;
     // U elements of four columns a thread, F parts of each: eight loads in flight.
     auto rows_of = [&](auto fc, auto uc) {
         constexpr int F = decltype(fc)::value, U = decltype(uc)::value;
@@ -434,7 +435,7 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
                     float to = top[u];
 #pragma unroll
                     for (int e = 0; e < F; ++e) to = fmaxf(to, ml[u][e].x);
-                    const float f = top[u] == -INFINITY ? 0.0f : exp2_fast(top[u] - to);
+                    const float f = top[u] == -INFINITY ? 0.0f : exp2_fast((top[u] - to) * cs);
                     top[u] = to;
                     l[u] *= f;
                     o[u] = make_float4(o[u].x * f, o[u].y * f, o[u].z * f, o[u].w * f);
@@ -442,7 +443,7 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
                     for (int e = 0; e < F; ++e) {
                         // a part that saw nothing has no weight (and its reference is -inf)
                         const bool use = c + e < parts && !(ml[u][e].x == -INFINITY && ml[u][e].y == 0.0f);
-                        const float g = exp2_fast(ml[u][e].x - to);
+                        const float g = exp2_fast((ml[u][e].x - to) * cs);
                         l[u] += use ? ml[u][e].y * g : 0.0f;
                         o[u].x += use ? v[u][e].x * g : 0.0f;
                         o[u].y += use ? v[u][e].y * g : 0.0f;
@@ -636,7 +637,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         const int tk = row / A.group, g = row - tk * A.group;  // token of the row tile, head of the group
         const float cs = S.log2_scale;
         constexpr float lift = BF16 ? 0.0f : 7.0f;
-        const float slack = 8.0f / cs;
+        // A weight is exp2(x cs - ref cs).  One fused operation with ref cs computed beforehand is off by that product's
+        // rounding: up to here at most 2^-17 of a weight; in the millions by whole powers of two, each reference by
+        // another one, so that weights overflow or vanish.  Beyond, ref is taken off x itself, which is exact where it
+        // counts.  Likewise references are compared as scores wherever sums meet (streams, parts), not times cs.
+        constexpr float far_off = 256.0f;
         uint32_t sp = 0, od = 0;
         int gi = 0;
         bool ok = true;
@@ -656,13 +661,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 if (w.x.rows < 64) seen &= (1ull << w.x.rows) - 1;
             }
             float ref = -INFINITY, sum = 0.0f;
-            for (int j = 0; j < mine; ++j) {
-                const int jj = PROMPT ? j : 2 * j + s;
-                const int t = t0 + jj;
-                if (!(ok = warp_wait(base + L::oSFull + 8 * s, sp, stop))) break;
+            bool settled = false;  // every row has a reference, and none is far off
+            bool far = false;      // some row's is far off
+            uint32_t x[kTile];     // a tile's scores
+            float2 both;           // sums of its weights
+            int t = 0, n0 = 0;
+            bool cached = false;
+            auto away = [&] { return ref != -INFINITY && fabsf(ref * cs) > far_off; };
+            // Tile j's scores, those of hidden keys replaced.
+            auto fetch = [&](int j) -> bool {
+                t = t0 + (PROMPT ? j : 2 * j + s);
+                if (!warp_wait(base + L::oSFull + 8 * s, sp, stop)) return false;
                 sp ^= 1;
                 tmem_after();
-                uint32_t x[kTile];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_load(tS + 32 * c, x + 32 * c);
                 tmem_load_wait();
@@ -674,8 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     if (lane == 0) bar_arrive(base + L::oSFree + 8 * s);
                 }
                 // Hidden keys: a limit for most tiles, a mask for a tree's.
-                const bool cached = t < ctx_tiles;
-                const int n0 = (t - ctx_tiles) * kTile;
+                cached = t < ctx_tiles;
+                n0 = (t - ctx_tiles) * kTile;
                 if (cached || PROMPT) {
                     const int most = cached ? ctx - t * kTile : n0 + kTile - 1 > first ? token - n0 + 1 : kTile;
                     if (!cached ? n0 + kTile - 1 > first : most < kTile) {
@@ -692,80 +703,90 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 }
                 if (L::kApart && j > 0) {
                     // this stream's last product is done with O and the weights
-                    if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
+                    if (!warp_wait(base + L::oODone + 8 * s, od, stop)) return false;
                     od ^= 1;
                     tmem_after();
                 }
-                // The reference of the weights.  Where they lie apart from the scores it is not compared with every
-                // tile's maximum: the sum of the tile's weights shows when one has grown too large (over 2^15), and
-                // the tile is done again.  That spares the maximum's 64 instructions in nearly all tiles; a row's
-                // first tile always takes it.
-                bool look = !L::kApart || __any_sync(0xffffffffu, real && ref == -INFINITY);
-                float2 both;
-                for (;;) {
-                    if (look) {
-                        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                return true;
+            };
+            // The references follow tile j's maxima where these have grown by more than a factor of 2^8.
+            auto follow = [&](int j) {
+                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < kTile; c += 8)
+                for (int c = 0; c < kTile; c += 8)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                m[e] = max3(m[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
-                        const float top = max3(m[0], m[1], fmaxf(m[2], m[3]));
-                        const bool grow = top > ref + slack;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float to = grow ? top : ref;
-                            const float fix = grow ? exp2_fast((ref - to) * cs) : 1.0f;
-                            ref = to;
-                            sum *= fix;
-                            if (j > 0) {
-                                // O is complete: weights over the scores mean that these scores' product was issued
-                                // after this stream's last P V; else it was waited for.
+                    for (int e = 0; e < 4; ++e)
+                        m[e] = max3(m[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+                const float top = max3(m[0], m[1], fmaxf(m[2], m[3]));
+                const bool grow = (top - ref) * cs > 8.0f;
+                if (!__any_sync(0xffffffffu, grow)) return;
+                const float to = grow ? top : ref;
+                const float fix = grow ? exp2_fast((ref - to) * cs) : 1.0f;
+                ref = to;
+                sum *= fix;
+                if (j > 0) {
+                    // O is complete: weights over the scores mean that these scores' product was issued
+                    // after this stream's last P V; else it was waited for.
 #pragma unroll
-                                for (int c = 0; c < DP / 16; ++c) {
-                                    uint32_t o[16];
-                                    tmem_load16(tO + 16 * c, o);
-                                    tmem_load_wait();
-                                    tmem_loaded16(o);
+                    for (int c = 0; c < DP / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_load16(tO + 16 * c, o);
+                        tmem_load_wait();
+                        tmem_loaded16(o);
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
-                                    tmem_store16(tO + 16 * c, o);
-                                }
-                            }
-                        }
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                        tmem_store16(tO + 16 * c, o);
                     }
-                    const float shift = ref == -INFINITY ? 0.0f : lift - ref * cs;
-                    const uint64_t cs2 = pair(__float_as_uint(cs), __float_as_uint(cs));
-                    const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
-                    uint64_t part[2] = {0, 0};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t y[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 z = unpair(fma2(pair(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), cs2, shift2));
-                            const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
-                            part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                            y[e] = pack2<BF16>(p0, p1);
-                        }
-                        tmem_store16(tP + 16 * c, y);
-                        if (c == 1 && !L::kApart) {
-                            // the first half's product starts while the second half is computed
-                            tmem_store_wait();
-                            tmem_before();
-                            __syncwarp();
-                            if (lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
-                        }
-                    }
-                    both = unpair(add2(part[0], part[1]));
-                    if (look || !__any_sync(0xffffffffu, real && both.x + both.y > 32768.0f)) break;
-                    look = true;
-                    tmem_store_wait();  // stores to the same columns follow: only this wait orders two of them
                 }
+                settled = __all_sync(0xffffffffu, !real || fabsf(ref * cs) <= far_off);
+                far = __any_sync(0xffffffffu, real && away());
+            };
+            // References that are far off are taken off the scores (trees).
+            auto rebase = [&] {
+                const float off = away() ? ref : 0.0f;
+#pragma unroll
+                for (int c = 0; c < kTile; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) - off);
+            };
+            // The tile's weights, and their sums.  References that are far off are taken off the scores on the way
+            // (take_off), or were before.
+            auto weigh = [&](auto take_off, bool taken_off) {
+                constexpr bool kTake = decltype(take_off)::value != 0;
+                const bool apart = (kTake || taken_off) && away();
+                const float shift = ref == -INFINITY ? 0.0f : apart ? lift : lift - ref * cs;
+                const uint32_t off = __float_as_uint(apart ? -ref : 0.0f);
+                const uint64_t cs2 = pair(__float_as_uint(cs), __float_as_uint(cs)), off2 = pair(off, off);
+                const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
+                uint64_t part[2] = {0, 0};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t y[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        uint64_t v = pair(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]);
+                        if (kTake) v = add2(v, off2);
+                        const float2 z = unpair(fma2(v, cs2, shift2));
+                        const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
+                        part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                        y[e] = pack2<BF16>(p0, p1);
+                    }
+                    tmem_store16(tP + 16 * c, y);
+                    if (c == 1 && !L::kApart) {
+                        // the first half's product starts while the second half is computed
+                        tmem_store_wait();
+                        tmem_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
+                    }
+                }
+                both = unpair(add2(part[0], part[1]));
+            };
+            // Hands tile j's weights over.
+            auto give = [&](int j) -> bool {
                 sum += both.x + both.y;
                 if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
                     // Rows of V that were not finite: NaN for those who see them.
-                    const int vi = (gi + jj) % L::kV;
-                    if (!(ok = warp_wait(base + L::oVReady + 8 * vi, (uint32_t)((gi + jj) / L::kV & 1), stop))) break;
+                    const int i = gi + (PROMPT ? j : 2 * j + s), vi = i % L::kV;
+                    if (!warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(i / L::kV & 1), stop)) return false;
                     const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], bad[4 * vi + 2], bad[4 * vi + 3]};
                     if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
                         bool hit = false;
@@ -787,6 +808,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 tmem_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(base + L::oPReady + 8 * s);
+                return true;
+            };
+            int j = 0;
+            for (; j < mine; ++j) {
+                if (!(ok = fetch(j))) break;
+                // Where the weights lie apart from the scores, the reference is not compared with every tile's maximum:
+                // the sum of the tile's weights shows when one has grown too large (over 2^15), and the tile is done
+                // again.  That spares the maximum's 64 instructions in nearly all tiles; a row's first tile always
+                // takes it, and so do tiles with references that are far off.
+                bool look = !L::kApart || !settled;
+                for (;;) {
+                    if (look) {
+                        follow(j);
+                        if (far && PROMPT) break;
+                        if (far) rebase();
+                    }
+                    weigh(Count<0>{}, !PROMPT && far);
+                    if (look || !__any_sync(0xffffffffu, real && both.x + both.y > 32768.0f)) break;
+                    look = true;
+                    tmem_store_wait();  // stores to the same columns follow: only this wait orders two of them
+                }
+                if ((far && PROMPT) || !(ok = give(j))) break;
+            }
+            // With prompts, the rest of a segment with a reference that is far off goes through a loop of its own.  In the
+            // loop above, the subtraction costs every call time even where it is not taken: 16 chunks with rows of 64 take
+            // 296 us so, 283 with two loops, 281 without it.  (A prompt of 25,000: 2% more than without it either way.)
+            // Trees are bound by memory and have it there: a second loop would not fit their registers (256 requests
+            // 151 us, 110 so).
+            while (PROMPT && far) {
+                weigh(Count<1>{}, false);
+                if (!(ok = give(j)) || ++j == mine || !(ok = fetch(j))) break;
+                follow(j);
             }
             if (!ok) break;
             if (mine > 0) {
@@ -876,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 }
             }
             if (!whole && real && (PROMPT || s == 0))
-                W.ml[(int64_t)slot * rows + (PROMPT ? s * kTile : 0) + row] = make_float2(m * cs, l);
+                W.ml[(int64_t)slot * rows + (PROMPT ? s * kTile : 0) + row] = make_float2(m, l);
             // Neither stream's next sums may overwrite what the other still reads.
             tmem_before();
             if (!PROMPT) {
