@@ -34,7 +34,7 @@ constexpr int kCopyThreads = 256;
 constexpr int kFailed = -2;  // req[b].y of a request that a plan leaves as it was
 
 struct CacheLayout {
-    size_t len, refs, bits, table, req, list, total;
+    size_t len, firm, refs, bits, table, req, list, total;
 };
 
 int cache_layout(int32_t max_slots, int32_t max_pages, int32_t num_pages, CacheLayout* out)
@@ -45,6 +45,8 @@ int cache_layout(int32_t max_slots, int32_t max_pages, int32_t num_pages, CacheL
     CacheLayout L;
     size_t off = align_up(64 * sizeof(int32_t), kAlign);
     L.len = off;
+    off = align_up(off + (size_t)max_slots * sizeof(int32_t), kAlign);
+    L.firm = off;
     off = align_up(off + (size_t)max_slots * sizeof(int32_t), kAlign);
     L.refs = off;
     off = align_up(off + (size_t)num_pages * sizeof(int32_t), kAlign);
@@ -65,7 +67,7 @@ __global__ void k_cache_reset(CacheDev C)
 {
     const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
     for (int64_t i = at; i < 64; i += step) C.status[i] = 0;
-    for (int64_t i = at; i < C.max_slots; i += step) C.len[i] = 0;
+    for (int64_t i = at; i < C.max_slots; i += step) C.len[i] = C.firm[i] = 0;
     for (int64_t i = at; i < C.num_pages; i += step) C.refs[i] = 0;
     for (int64_t i = at; i < C.words(); i += step) {
         const int64_t left = C.num_pages - 32 * i;
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheDev C, const i
     // Pages of each request: req = (those of the requests before it, its own or kFailed).
     int2* const req = B <= kPlanThreads ? near : C.req;
     int want = 0;
+    int32_t firm = 0;  // FORK: the source's, fetched beside its length (of the thread's last request: a small batch's only one)
     for (int base = 0; base < B; base += kPlanThreads) {
         const int b = base + tid;
         int need = 0, state = kFailed;
@@ -164,6 +167,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheDev C, const i
                 who = b;
             } else if (FORK) {
                 const int32_t d = dst[b];
+                firm = C.firm[s];
                 if (!slot_ok(C, d)) {
                     err = CLK_EINVAL;
                     who = b;
@@ -181,6 +185,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheDev C, const i
                     err = CLK_ECAPACITY;
                 else
                     need = C.pages(now) - C.pages(old);
+                // an append that follows in spite of this writes nothing
+                if (err != CLK_OK) C.firm[s] = (int32_t)old;
             }
             if (err != CLK_OK)
                 latch(C.status, err, who);
@@ -224,10 +230,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheDev C, const i
             if (q.y >= 0) {
                 if (q.y > 0 && q.x + q.y > have) {
                     latch(C.status, CLK_ECAPACITY, FORK ? dst[b] : slots[b]);
+                    if (!FORK) C.firm[slots[b]] = C.len[slots[b]];
                 } else if (!FORK) {
                     C.len[slots[b]] += count[b];
                 } else {
                     const int32_t n = C.len[slots[b]];
+                    // The whole pages are shared from here on (forks of one source raise it to one value).
+                    const int32_t shared = max(B <= kPlanThreads ? firm : C.firm[slots[b]], n & ~part);
+                    C.firm[slots[b]] = C.firm[dst[b]] = shared;
                     tail = -1;
                     if (q.y > 0) {
                         tail = list[q.x];
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(CacheDev C, const i
     }
     if (FORK) {
         if (tid == 0) C.list[3 * (int64_t)C.num_pages + 2] = rows;
-        }
+    }
 }
 
 __global__ void __launch_bounds__(kCopyThreads) k_cache_free(CacheDev C, const int32_t* slots, int32_t B)
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_free(CacheDev C, const i
         if (page >= 0 && page < C.num_pages && atomicSub(C.refs + page, 1) == 1)
             atomicOr(C.bits + (page >> 5), 1u << (page & 31));
     }
-    if (threadIdx.x == 0) C.len[s] = 0;
+    if (threadIdx.x == 0) C.len[s] = C.firm[s] = 0;
 }
 
 // A pool in vectors of V: strides in vectors, and vectors per row.
@@ -417,10 +427,11 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_fork(CacheDev C, const i
 
 // Rows of the new tokens into the pages; blockIdx.y takes a share of the planes.
 
-// Whether n rows of a request with source rows base .. base + rows - 1 can go to the end of len tokens.
-__device__ __forceinline__ bool append_ok(int32_t n, int32_t len, int64_t base, int64_t rows, int64_t total)
+// Whether n rows of a request with source rows base .. base + rows - 1 can go to the end of a slot's tokens, of which
+// `room` follow the firm ones.
+__device__ __forceinline__ bool append_ok(int32_t n, int32_t room, int64_t base, int64_t rows, int64_t total)
 {
-    return n >= 0 && n <= len && n <= rows && base >= 0 && base <= total - rows;
+    return n >= 0 && n <= room && n <= rows && base >= 0 && base <= total - rows;
 }
 
 template <typename V>
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
             const int64_t base = off != nullptr ? off[b] : b * N, rows = off != nullptr ? off[b + 1] - base : N;
             if (!slot_ok(C, s))
                 latch(C.status, CLK_EINVAL, b);
-            else if (!append_ok(count[b], C.len[s], base, rows, total))
+            else if (!append_ok(count[b], C.len[s] - C.firm[s], base, rows, total))
                 latch(C.status, CLK_EINVAL, s);
         }
     }
@@ -482,8 +493,8 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
         }
         if (b >= 0) {
             const int32_t s = slots[b], n = count[b];
-            const int32_t len = slot_ok(C, s) ? C.len[s] : -1;
-            if (append_ok(n, len, base, rows, total) && i < n) {
+            const int32_t len = slot_ok(C, s) ? C.len[s] : -1, room = slot_ok(C, s) ? len - C.firm[s] : -1;
+            if (append_ok(n, room, base, rows, total) && i < n) {
                 const int64_t r = path != nullptr ? path[base + i] : i;
                 const int32_t pos = len - n + (int32_t)i;
                 const int32_t page =
@@ -712,6 +723,7 @@ extern "C" int clk_cache_create(clk_cache** h, int32_t max_slots, int32_t max_pa
     char* base = static_cast<char*>(d_workspace);
     c->dev = CacheDev{reinterpret_cast<int32_t*>(base),
                       reinterpret_cast<int32_t*>(base + L.len),
+                      reinterpret_cast<int32_t*>(base + L.firm),
                       reinterpret_cast<int32_t*>(base + L.refs),
                       reinterpret_cast<uint32_t*>(base + L.bits),
                       reinterpret_cast<int32_t*>(base + L.table),

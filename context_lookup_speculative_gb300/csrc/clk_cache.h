@@ -13,6 +13,8 @@ namespace clk {
 // Workspace (see clk_cache_workspace_bytes):
 //   status  int32[64]                     latched device error, as in LookupDev
 //   len     int32[max_slots]              tokens held
+//   firm    int32[max_slots]              rows from the first on that no append writes: those there when a grow
+//                                         last failed, and those of pages that a fork shared
 //   refs    int32[num_pages]              slots that hold the page
 //   bits    u32[ceil(num_pages / 128) * 4] bit p % 32 of word p / 32: page p is free
 //   table   int32[max_slots][max_pages]   pages held, -1 past the last
@@ -21,6 +23,7 @@ namespace clk {
 struct CacheDev {
     int32_t* status;
     int32_t* len;
+    int32_t* firm;
     int32_t* refs;
     uint32_t* bits;
     int32_t* table;

@@ -552,6 +552,12 @@ CLK_API int clk_cache_grow(clk_cache* h, const int32_t* d_slots, int32_t B, cons
 
 /* Writes K and V rows of `layers` layers from `layer0` on: request b's rows
  * i < d_count[b] go to its slot's last d_count[b] positions, len - count + i.
+ * Only rows that clk_cache_grow made room for are written, and none that
+ * another slot holds: d_count[b] is at most the slot's rows after those it had
+ * when a grow of it last failed (such a grow leaves nothing to write until one
+ * succeeds) and after the whole pages it has shared by clk_cache_fork, so that
+ * a source's rows are written before it is forked.  Within that, rows of
+ * several grows go in one call, and a call may be repeated or go layer by layer.
  * Row i is source row r = d_path[b*N + i] of request b, or r = i where d_path
  * is NULL (d_path: the accepted nodes of a tree, clk_tree_accept); 0 <= r <
  * the request's rows.  The request's rows start at row b*N of the source (N
@@ -559,10 +565,10 @@ CLK_API int clk_cache_grow(clk_cache* h, const int32_t* d_slots, int32_t B, cons
  * the total number of rows, d_path must be NULL and request b has
  * d_off[b+1] - d_off[b] rows).  Source element (layer l, row, head, d) lies
  * at d_k + l*layer_stride + row*row_stride + head*head_stride + d, and the
- * same for d_v (elements of the pool's type).  A count outside 0 .. min(len,
- * rows), offsets outside 0 .. N or falling, a path entry out of range or a
- * bad slot latches CLK_EINVAL; the rows concerned are not written.  Source
- * and pool must not overlap. */
+ * same for d_v (elements of the pool's type).  A count outside 0 .. min(rows
+ * that may be written, the request's rows), offsets outside 0 .. N or falling,
+ * a path entry out of range or a bad slot latches CLK_EINVAL; the rows
+ * concerned are not written.  Source and pool must not overlap. */
 CLK_API int clk_cache_append(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool, int32_t layer0,
                              int32_t layers, const void* d_k, const void* d_v, int64_t layer_stride,
                              int64_t row_stride, int64_t head_stride, int64_t N, const int64_t* d_off,
@@ -574,7 +580,8 @@ CLK_API int clk_cache_append(clk_cache* h, const int32_t* d_slots, int32_t B, co
  * of a batch; no slot is both a source and a destination of it.  A bad slot
  * or a destination that is not empty latches CLK_EINVAL, a lack of pages
  * CLK_ECAPACITY (as in clk_cache_grow), and that destination stays as it
- * was. */
+ * was: an empty slot, which a clk_cache_grow then fills as one, without the
+ * source's rows. */
 CLK_API int clk_cache_fork(clk_cache* h, const int32_t* d_src, const int32_t* d_dst, int32_t B, const clk_pool* pool,
                            clk_stream_t s);
 
