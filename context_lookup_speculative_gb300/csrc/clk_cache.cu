@@ -465,6 +465,21 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
                 latch(C.status, CLK_EINVAL, s);
         }
     }
+    // Where row i of request b comes from and goes to; both stay as they are for one that is not written.
+    auto find = [&](int b, int64_t i, int64_t base, int64_t rows, int64_t& row, int64_t& place) {
+        const int32_t s = slots[b], n = count[b];
+        const int32_t len = slot_ok(C, s) ? C.len[s] : -1, room = slot_ok(C, s) ? len - C.firm[s] : -1;
+        if (!append_ok(n, room, base, rows, total) || i >= n) return;
+        const int64_t r = path != nullptr ? path[base + i] : i;
+        const int32_t pos = len - n + (int32_t)i;
+        const int32_t page = (pos >> C.shift) < C.max_pages ? C.table[(int64_t)s * C.max_pages + (pos >> C.shift)] : -1;
+        if (r < 0 || r >= rows || page < 0 || page >= C.num_pages) {
+            latch(C.status, CLK_EINVAL, s);
+        } else {
+            row = (base + r) * S.row;
+            place = page * A.page + (int64_t)(pos & (C.page_tokens() - 1)) * A.tok;
+        }
+    };
     if (threadIdx.x < group) {
         const int64_t at = first + threadIdx.x;
         int64_t row = -1, place = -1;
@@ -491,31 +506,39 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
                 rows = starts[lo + 1] - base;
             }
         }
-        if (b >= 0) {
-            const int32_t s = slots[b], n = count[b];
-            const int32_t len = slot_ok(C, s) ? C.len[s] : -1, room = slot_ok(C, s) ? len - C.firm[s] : -1;
-            if (append_ok(n, room, base, rows, total) && i < n) {
-                const int64_t r = path != nullptr ? path[base + i] : i;
-                const int32_t pos = len - n + (int32_t)i;
-                const int32_t page =
-                    (pos >> C.shift) < C.max_pages ? C.table[(int64_t)s * C.max_pages + (pos >> C.shift)] : -1;
-                if (r < 0 || r >= rows || page < 0 || page >= C.num_pages) {
-                    latch(C.status, CLK_EINVAL, s);
-                } else {
-                    row = (base + r) * S.row;
-                    place = page * A.page + (int64_t)(pos & (C.page_tokens() - 1)) * A.tok;
-                }
-            }
-        }
+        if (b >= 0) find(b, i, base, rows, row, place);
         from[threadIdx.x] = row;
         to[threadIdx.x] = place;
     }
     __syncthreads();
     const int p0 = (int)((int64_t)planes * blockIdx.y / gridDim.y), p1 = (int)((int64_t)planes * (blockIdx.y + 1) / gridDim.y);
-    move_rows(from, to, group, A, S.head, p0, p1, [&](int plane, const V*& s, V*& d) {
+    auto planes_of = [&](int plane, const V*& s, V*& d) {
         s = (plane & 1 ? S.v : S.k) + (plane >> 1) * S.layer;
         d = A.base + (2 * (int64_t)layer0 + plane) * A.plane;
-    });
+    };
+    move_rows(from, to, group, A, S.head, p0, p1, planes_of);
+    if (off == nullptr || blockIdx.x != gridDim.x - 1) return;
+    // The search above relies on offsets that do not fall.  Where one does, it misses rows of the requests around it:
+    // the last CTAs write all good requests' rows, those that were found among them once more.
+    bool falls = false;
+    for (int b = threadIdx.x; b < B; b += kCopyThreads) falls |= starts[b + 1] < starts[b];
+    if (!__syncthreads_or(falls)) return;
+    for (int b = 0; b < B; ++b) {
+        const int64_t base = starts[b], rows = starts[b + 1] - base;
+        const int32_t s = slots[b], n = count[b];
+        if (!slot_ok(C, s) || !append_ok(n, C.len[s] - C.firm[s], base, rows, total)) continue;
+        for (int32_t i = 0; i < n; i += group) {
+            __syncthreads();  // the rows before are written
+            if (threadIdx.x < group) {
+                int64_t row = -1, place = -1;
+                find(b, (int64_t)i + threadIdx.x, base, rows, row, place);
+                from[threadIdx.x] = row;
+                to[threadIdx.x] = place;
+            }
+            __syncthreads();
+            move_rows(from, to, group, A, S.head, p0, p1, planes_of);
+        }
+    }
 }
 
 // Entries of all tables up to which one CTA rewrites them.  Measured with and
