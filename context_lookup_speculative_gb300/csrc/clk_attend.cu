@@ -109,7 +109,7 @@ struct Sizes {
 // 2,048 rows 31 us; 8 requests of 16 nodes over 2,000 rows 246 us; a prompt of
 // 1,000 tokens 519 us (16 TFLOP/s of the causal half).
 template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads, 1) k_attend_rows(Attend A, Rows G)
+__device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int b, int64_t t0, uint32_t rank)
 {
     using Z = Sizes<NC>;
     extern __shared__ __align__(16) float sm[];
@@ -119,29 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_rows(Attend A, Rows G)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int kh = blockIdx.y / G.head_blocks, h0 = kh * A.group + (blockIdx.y - kh * G.head_blocks) * G.hp;
     const int hp = min(G.hp, (kh + 1) * A.group - h0);
-    const uint32_t item = blockIdx.x / G.ways, rank = blockIdx.x - item * G.ways;
     const bool prompt = A.off != nullptr;
-    if (blockIdx.x == 0 && blockIdx.y == 0)  // what is wrong with a request is reported once
-        for (int i = tid; i < A.B; i += kThreads) attend_request(A, i, true);
-    int b;
-    int64_t t0;
-    if (prompt) {
-        // request b's blocks begin at off[b] / tok + b: never fewer than it needs
-        int lo = 0, hi = A.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (A.off[mid] / G.tok + mid <= item)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        b = lo;
-        t0 = (item - (A.off[b] / G.tok + b)) * G.tok;
-    } else {
-        const int per = (A.N + G.tok - 1) / G.tok;
-        b = (int)(item / per);
-        t0 = (int64_t)(item - b * per) * G.tok;
-    }
     const Request R = attend_request(A, b, false);
     // (the whole cluster leaves, or none of it)
     if (t0 < 0 || (prompt && t0 >= R.rows)) return;
@@ -416,6 +394,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_rows(Attend A, Rows G)
         }
     }
     cluster.sync();  // no CTA ends while its results are read
+}
+
+// A cluster's rows: those of tokens t0 .. t0 + tok - 1 of request b, by its
+// place in the grid.
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads, 1) k_attend_rows(Attend A, Rows G)
+{
+    const int tid = threadIdx.x;
+    const uint32_t item = blockIdx.x / G.ways, rank = blockIdx.x - item * G.ways;
+    if (blockIdx.x == 0 && blockIdx.y == 0)  // what is wrong with a request is reported once
+        for (int i = tid; i < A.B; i += kThreads) attend_request(A, i, true);
+    // Request b's blocks begin at off[b] / tok + b: never fewer than it needs, and all within the grid.  With offsets
+    // that rise an item is one request's at most; where one falls, several good requests may have it.
+    __shared__ int first;
+    bool falls;
+    int b = -1;
+    do {
+        int64_t t0;
+        falls = false;
+        if (A.off == nullptr) {
+            const int per = (A.N + G.tok - 1) / G.tok;
+            b = (int)(item / per);
+            t0 = (int64_t)(item - b * per) * G.tok;
+        } else {
+            if (tid == 0) first = A.B;
+            __syncthreads();
+            int mine = A.B;
+            for (int i = b + 1 + tid; i < A.B; i += kThreads) {
+                const int64_t lo = A.off[i], hi = A.off[i + 1];
+                falls |= hi < lo;
+                if (lo < 0 || hi <= lo || hi > A.T || mine < A.B) continue;
+                const uint32_t at = (uint32_t)lo / G.tok + i, blocks = ((uint32_t)(hi - lo) + G.tok - 1) / G.tok;
+                if (item >= at && item - at < blocks) mine = i;
+            }
+            if (mine < A.B) atomicMin(&first, mine);
+            falls = __syncthreads_or(falls);
+            b = first;
+            if (b == A.B) return;
+            t0 = (int64_t)(item - (uint32_t)A.off[b] / G.tok - b) * G.tok;
+        }
+        attend_rows<T, NC>(A, G, b, t0, rank);
+        if (falls) __syncthreads();  // shared memory is used again
+    } while (falls);
 }
 
 template <typename T, int NC>

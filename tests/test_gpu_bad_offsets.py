@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import context_lookup_speculative_gb300 as clk
+from test_gpu_attend import Prompt
 from test_gpu_cache import Both, ints
 
 pytestmark = pytest.mark.gpu
@@ -51,3 +52,40 @@ def test_many_packed_requests_around_a_bad_offset():
     c = Both(600, 3, 2000, 16, heads=1)
     append_packed(c, list(range(600)), off, rows, good)
     c.check(status=clk.EINVAL)
+
+
+def around(seed, lens, bad, off, G, D, kind, ctx=None, tail=4):
+    """Prompts of `lens` rows whose requests `bad` are empty; `off` is what the call is given."""
+    p = Prompt(seed, lens, G, 1, D, kind, ctx=ctx, tail=tail)
+    good = list(p.off)
+    assert all(lens[b] == 0 for b in bad)
+    assert all(off[b:b + 2] == good[b:b + 2] for b in range(len(lens)) if b not in bad)
+    p.off = off
+    p.run()
+    torch.cuda.synchronize()
+    if p.kw:
+        assert p.cache.status()[0] == clk.EINVAL
+        p.cache.status_clear()
+    p.off = good
+    p.check(rows=15)
+
+
+@pytest.mark.parametrize("kind,D", [("f32", 40), ("f32", 128), ("bf16", 200), ("bf16", 64), ("f16", 128)])
+@pytest.mark.parametrize("G", [1, 3, 40])
+def test_prompts_around_a_bad_offset(G, kind, D):
+    around(1, [0, 0, 10], [0, 1], [0, 1000000, 0, 10], G, D, kind)
+    around(2, [5, 0, 0, 7, 0, 0, 8], [1, 2, 4, 5], [0, 5, 1000, 5, 12, -4, 12, 20], G, D, kind)
+    around(3, [70, 0, 0, 90, 0, 0, 1], [1, 2, 4, 5], [0, 70, 1 << 40, 70, 160, -1, 160, 161], G, D, kind, ctx=[0, 0, 0, 130, 5, 0, 33])
+
+
+@pytest.mark.parametrize("kind,D", [("f32", 40), ("bf16", 64)])
+def test_many_prompts_around_a_bad_offset(kind, D):
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 30, size=700)
+    bad = (0, 1, 99, 100, 400, 401, 698, 699)
+    lens[list(bad)] = 0
+    off = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    T = off[-1] + 4
+    for at, x in ((1, T + 3), (100, -1), (401, 1 << 33), (699, -7)):
+        off[at] = x
+    around(4, lens.tolist(), bad, off, 2, D, kind)
