@@ -156,6 +156,7 @@ _SIGS = [
     ("clk_tree_masks", ctypes.c_int, [_I32, _I32, _P, _P, _P, _P]),
     ("clk_tree_accept", ctypes.c_int, [_I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     ("clk_attend_scratch_bytes", ctypes.c_int, [_I32, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]),
+    ("clk_attend_status", ctypes.c_int, [_P, ctypes.POINTER(_I32), _P]),
     ("clk_tree_attend", ctypes.c_int, [_P, _P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     ("clk_prompt_attend", ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _P, _I32, _P, _P, ctypes.c_size_t, _P]),
 ]
@@ -700,6 +701,15 @@ def attend_scratch(q_heads: int, kv_heads: int, dim: int, device="cuda") -> torc
     n = ctypes.c_size_t()
     _check("clk_attend_scratch_bytes", lib().clk_attend_scratch_bytes(q_heads, kv_heads, dim, ctypes.byref(n)))
     return torch.zeros(n.value, dtype=torch.uint8, device=device)
+
+
+def attend_status(scratch: torch.Tensor, stream=None) -> int:
+    """ECUDA where a wait inside an attention on this scratch has run out since it was zeroed, else OK
+    (clk_attend_status; synchronises)."""
+    st = _I32()
+    _check("clk_attend_status", lib().clk_attend_status(_ptr(scratch, torch.uint8, name="scratch"), ctypes.byref(st),
+                                                        _stream(stream)))
+    return st.value
 
 
 def _attn_desc(q, k, v, out, scale: float) -> AttnDesc:

@@ -576,6 +576,17 @@ extern "C" int clk_attend_scratch_bytes(int32_t q_heads, int32_t kv_heads, int32
     return CLK_OK;
 }
 
+extern "C" int clk_attend_status(const void* d_scratch, int32_t* dev_status, clk_stream_t s)
+{
+    if (d_scratch == nullptr || !aligned(d_scratch, 16) || dev_status == nullptr) return CLK_EINVAL;
+    const cudaStream_t cs = (cudaStream_t)s;
+    int32_t st = 0;
+    if (cudaMemcpyAsync(&st, d_scratch, sizeof st, cudaMemcpyDeviceToHost, cs) != cudaSuccess) return CLK_ECUDA;
+    if (cudaStreamSynchronize(cs) != cudaSuccess) return CLK_ECUDA;
+    *dev_status = st;
+    return CLK_OK;
+}
+
 extern "C" int clk_tree_attend(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool, int32_t layer,
                                const clk_attn* a, int32_t N, const int32_t* d_nodes, const int64_t* d_mask,
                                const int32_t* d_ctx, void* d_scratch, size_t scratch_bytes, clk_stream_t s)

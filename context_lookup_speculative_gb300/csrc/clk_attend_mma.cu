@@ -88,15 +88,18 @@ struct Shape {
     bool wide_out;     // rows of out are whole 32-byte sectors
 };
 
-// Scratch: a flag per CTA (a count of calls), row statistics and partial
-// sums, two parts a CTA.
+// Scratch: the status of calls since it was zeroed, a flag per CTA (a count of
+// calls), row statistics and partial sums, two parts a CTA.
 struct Scratch {
-    uint32_t* flag;  // [ctas]
-    float2* ml;      // [ctas][2][rows]
-    float* sums;     // [ctas][2][DP / 4][rows][4]
+    int32_t* status;  // latched as a cache's; a prompt without a cache has no other place for it
+    uint32_t* flag;   // [ctas]
+    float2* ml;       // [ctas][2][rows]
+    float* sums;      // [ctas][2][DP / 4][rows][4]
 };
 
 __host__ __device__ inline int pad_dim(int dim) { return dim <= 64 ? 64 : 128; }
+
+constexpr size_t kStatusBytes = 128;
 
 __host__ __device__ inline size_t flag_bytes(int ctas) { return ((size_t)ctas * sizeof(uint32_t) + 127) / 128 * 128; }
 
@@ -104,6 +107,8 @@ __host__ __device__ inline Scratch scratch_of(void* base, int ctas, int rows)
 {
     Scratch s;
     char* p = static_cast<char*>(base);
+    s.status = reinterpret_cast<int32_t*>(p);
+    p += kStatusBytes;
     s.flag = reinterpret_cast<uint32_t*>(p);
     p += flag_bytes(ctas);
     s.ml = reinterpret_cast<float2*>(p);
@@ -360,6 +365,13 @@ struct Lay {
     static_assert(kTotal <= 232448, "shared memory");
 };
 
+// A wait has run out: the call's results are not whole.
+__device__ __forceinline__ void gave_up(const Attend& A, const Scratch& W)
+{
+    latch(W.status, CLK_ECUDA, -1);
+    if (A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
+}
+
 template <int N>
 struct Count {
     static constexpr int value = N;
@@ -387,7 +399,7 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
     }
     __syncthreads();
     if (*stop != 0) {
-        if (tid == 0 && A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
+        if (tid == 0) gave_up(A, W);
         return;
     }
     const int quads = A.dim / 4;
@@ -1246,7 +1258,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     if (tid == 0) {
         // after the barrier above, the release covers the whole CTA's parts
         asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(W.flag + blockIdx.x), "r"(plan.call + 1) : "memory");
-        if (*stop != 0 && A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
+        if (*stop != 0) gave_up(A, W);
     }
     if (*stop != 0 || plan.g0 >= plan.g1) return;
     const Cuts cuts(plan.all, plan.ctas);
@@ -1351,7 +1363,7 @@ size_t attend_mma_scratch(int32_t q_heads, int32_t kv_heads, int32_t dim)
     if (!mma_dim(dim) || q_heads / kv_heads > kTile) return 0;
     const size_t rows = 2 * kTile;
     const int n = num_sms();
-    return flag_bytes(n) + (size_t)n * 2 * rows * (sizeof(float2) + (size_t)pad_dim(dim) * sizeof(float));
+    return kStatusBytes + flag_bytes(n) + (size_t)n * 2 * rows * (sizeof(float2) + (size_t)pad_dim(dim) * sizeof(float));
 }
 
 int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)

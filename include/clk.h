@@ -22,7 +22,8 @@
  *   returns CLK_ECUDA.  No C++ exception crosses this boundary.
  * - Asynchrony: every call that takes a clk_stream_t (a cudaStream_t) only
  *   enqueues work on that stream; none synchronises, except clk_status,
- *   clk_read_counters, clk_read_slot_info, clk_lookup_read_history and
+ *   clk_cache_status, clk_attend_status, clk_read_counters,
+ *   clk_read_slot_info, clk_lookup_read_history and
  *   clk_lookup_restore_state, which say so.
  * - Device errors: problems that can only be seen on the device (a history
  *   capacity overflow, a token outside [0, vocab), a bad slot index, a bad
@@ -669,8 +670,14 @@ typedef struct clk_attn {
  * this dim on the current device, for any batch.  16-byte aligned; zeroed once
  * before its first use (e.g. clk_verify_scratch_init) and left ready by every
  * call; calls that share it must not overlap on the GPU.  Zero it again after
- * a call that failed. */
+ * a call that failed (clk_attend_status). */
 CLK_API int clk_attend_scratch_bytes(int32_t q_heads, int32_t kv_heads, int32_t dim, size_t* bytes);
+
+/* Synchronises `s` and returns in *dev_status CLK_ECUDA where a wait inside an
+ * attention on this scratch has run out since it was zeroed (the CTAs of a
+ * launch wait for one another, two seconds or so at most; the rows of that
+ * call are not whole), else CLK_OK.  A call with a cache latches it there too. */
+CLK_API int clk_attend_status(const void* d_scratch, int32_t* dev_status, clk_stream_t s);
 
 /* Attention of a step's block: request b has d_nodes[b] new tokens (0 .. N,
  * N <= CLK_TREE_MAX), of which token n sees the slot's first ctx rows (plane
