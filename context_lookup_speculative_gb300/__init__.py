@@ -629,13 +629,15 @@ def cache_append(h: Cache, slots, pool, k, v, count, layer: int = 0, path=None, 
     b; or, with ``offsets`` (int64 [B+1]), [layers, T, kv_heads, dim]."""
     B = slots.numel()
     d = _pool_desc(h, pool)
-    if k.dim() != (4 if offsets is not None else 5) or k.shape != v.shape or k.stride() != v.stride() \
-            or not (k.is_cuda and v.is_cuda):
+    if k.dim() != (4 if offsets is not None else 5) or k.shape != v.shape or not (k.is_cuda and v.is_cuda) \
+            or (k.stride() != v.stride() and any(n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride()))):
         raise ValueError("k and v must be CUDA tensors of one shape and layout, "
                          "[layers, B, N, heads, dim] or, with offsets, [layers, T, heads, dim]")
     if offsets is None:
         layers, Bk, N, heads, dim = k.shape
         layer_st, req, row, head, one = k.stride()
+        if N == 1:  # the stride from request to request is that from row to row
+            row = req if B > 1 else 0
         if Bk != B or (B > 1 and req != N * row):
             raise ValueError("k and v must hold B requests of N rows, one request's rows after another's")
     else:
@@ -647,7 +649,7 @@ def cache_append(h: Cache, slots, pool, k, v, count, layer: int = 0, path=None, 
         raise ValueError("rows of k and v must be contiguous")
     _check("clk_cache_append",
            lib().clk_cache_append(h.handle, _ptr(slots, name="slots"), B, ctypes.byref(d), layer, layers,
-                                  k.data_ptr(), v.data_ptr(), layer_st, row, head, N,
+                                  k.data_ptr(), v.data_ptr(), layer_st if layers > 1 else 0, row, head if heads > 1 else 0, N,
                                   _ptr(offsets, torch.int64, (B + 1,), "offsets"),
                                   _ptr(path, shape=(B, N), name="path"), _ptr(count, shape=(B,), name="count"),
                                   _stream(stream)))
