@@ -609,7 +609,7 @@ def _pool_desc(h: Cache, pool: torch.Tensor) -> PoolDesc:
     planes, pages, heads, tokens, dim = pool.shape
     plane_st, page_st, head_st, tok_st, one = pool.stride()
     code = _POOL_DTYPES.get(pool.dtype)
-    if code is None or one != 1 or pages < h.num_pages or tokens != h.page_tokens:
+    if code is None or (one != 1 and dim > 1) or pages < h.num_pages or tokens != h.page_tokens:
         raise ValueError(f"pool must be bfloat16, float16 or float32 with contiguous rows, >= {h.num_pages} pages and "
                          f"{h.page_tokens} tokens a page, got {pool.dtype} {tuple(pool.shape)}")
     return PoolDesc(pool.data_ptr(), code, planes, heads, dim, plane_st, page_st, head_st, tok_st)

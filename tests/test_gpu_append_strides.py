@@ -1,5 +1,5 @@
-"""cache_append's sources: a stride of an axis of one element means nothing and
-refuses nothing.  GPU."""
+"""cache_append and the pool's layout: a stride of an axis of one element means
+nothing and refuses nothing.  GPU."""
 import pytest
 import torch
 
@@ -63,3 +63,16 @@ def test_layouts_that_differ_are_still_refused():
     for kk, vv in ((k, k.transpose(2, 3).contiguous().transpose(2, 3)), (apart, apart)):
         with pytest.raises(ValueError):
             clk.cache_append(h, ints([0, 1]), pool, kk, vv, ints([3, 3]))
+
+
+def test_a_pool_of_rows_of_one_element():
+    """Its last axis has one element, so that its stride is whatever it came with."""
+    P = 16
+    h = clk.Cache(2, 4, 8, P)
+    wide = torch.zeros((2, 8, 1, P, 1), dtype=torch.float32, device="cuda")
+    pool = wide.as_strided(wide.shape, wide.stride()[:4] + (5,))
+    clk.cache_grow(h, ints([1]), ints([20]))
+    k = torch.randn((1, 1, 20, 1, 1), device="cuda")
+    clk.cache_append(h, ints([1]), pool, k, -k, ints([20]))
+    assert h.status()[0] == 0
+    assert torch.equal(rows_of(h, wide, 0, 1, 0, 20), k[0, 0]) and torch.equal(rows_of(h, wide, 1, 1, 0, 20), -k[0, 0])
