@@ -688,7 +688,8 @@ def tree_masks(parent, nodes, mask, stream=None):
 
 def tree_accept(tok, parent, nodes, argmax, accept, path, emitted, out_tok, stream=None):
     """Greedy verification of trees (clk_tree_accept); argmax: the target's
-    answers at the nodes, e.g. verify_greedy's."""
+    answers at the nodes, verify_greedy's where N is 16 (or, a tree as N / 16
+    of its blocks, a multiple of it)."""
     B, N = tok.shape
     _check("clk_tree_accept",
            lib().clk_tree_accept(B, N, _ptr(tok, name="tok"), _ptr(parent, shape=(B, N), name="parent"),

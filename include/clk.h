@@ -622,8 +622,11 @@ CLK_API void clk_cache_destroy(clk_cache* h);
 CLK_API int clk_tree_masks(int32_t B, int32_t N, const int32_t* d_parent, const int32_t* d_nodes, int64_t* d_mask,
                            clk_stream_t s);
 
-/* Greedy verification of a tree, from the target's answers d_argmax [B,N]
- * (clk_verify_greedy's, at every node).  Node 0 is accepted; node n is
+/* Greedy verification of a tree, from the target's answers d_argmax [B,N] at
+ * every node.  clk_verify_greedy, which writes [B,16], makes them: with N = 16
+ * in one block a request, with N a multiple of 16 in N / 16 blocks (logits and
+ * argmax [B,N,..] seen as [B*N/16,16,..]; its other outputs do not count
+ * then).  Node 0 is accepted; node n is
  * accepted where its parent is and its token d_tok[b*N + n] (>= 0) is the
  * target's answer at the parent; of siblings that both match, the lowest.
  * Outputs: d_path [B,N] the accepted nodes from node 0 on, then -1; d_accept
