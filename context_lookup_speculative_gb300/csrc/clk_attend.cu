@@ -479,7 +479,8 @@ int launch_general(const Attend& A, cudaStream_t s)
     // of 256, 128 CTAs of 8 requests: shared by one 416, by two 232, by four
     // 253, by eight 373 us).
     G.ways = kWays;
-    while (G.ways > 1 && items * A.kv_heads * G.head_blocks * G.ways > 228) G.ways /= 2;
+    const int64_t most = num_sms() * 3 / 2;
+    while (G.ways > 1 && items * A.kv_heads * G.head_blocks * G.ways > most) G.ways /= 2;
     int64_t odd = A.dim;
     for (int64_t x : {A.k_req, A.k_row, A.k_head, A.v_req, A.v_row, A.v_head}) odd |= x;
     if (A.C.status != nullptr)

@@ -133,8 +133,10 @@ __device__ __forceinline__ long long quotient(long long a, long long b)
     return ((a | b) >> 31) == 0 ? (long long)quotient((uint32_t)a, (uint32_t)b) : a / b;
 }
 
-// sum over i < n of floor((a i + b) / m), for m > 0 and a n + b < 2^32 (a
-// step of Euclid's algorithm at a time).
+// sum over i < n of floor((a i + b) / m), for m > 0 and a n + b < 2^32: the
+// lattice points under a line.  The known reduction, as Euclid's algorithm
+// goes: whole parts of the slope and of the start are summed at once, what is
+// left of the line is read with its axes changed.
 __device__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b)
 {
     long long s = 0;
@@ -168,7 +170,6 @@ struct Reach {
     int32_t base;
 };
 
-template <bool PROMPT>
 __device__ __forceinline__ Reach reach_of(const Request& r, const Shape& S)
 {
     Reach x;
@@ -283,7 +284,7 @@ struct Walk {
     __device__ void load(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
     {
         const int i = b - P.b;
-        x = i < kNear ? near[i] : reach_of<PROMPT>(attend_request(A, b, false), S);
+        x = i < kNear ? near[i] : reach_of(attend_request(A, b, false), S);
     }
     // From unit `at` of the item on, as far as the share goes.
     __device__ void cut(const Shape& S, int at)
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 const int b = at + tid;
                 long long each = 0;  // units of one K/V head
                 if (b < A.B) {
-                    x = reach_of<PROMPT>(attend_request(A, b, pass == 0 && blockIdx.x == 0), S);
+                    x = reach_of(attend_request(A, b, pass == 0 && blockIdx.x == 0), S);
                     each = units_of<PROMPT>(x, S);
                 }
                 const long long u = each * A.kv_heads;
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 const int i = tid - plan.b;
                 if (i >= 0 && i < kNear) near[i] = x;
             } else if (tid < kNear && plan.b + tid < A.B) {
-                near[tid] = reach_of<PROMPT>(attend_request(A, plan.b + tid, false), S);
+                near[tid] = reach_of(attend_request(A, plan.b + tid, false), S);
             }
         }
     }

@@ -163,17 +163,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r)
 #undef CLK_IN
 }
 
-__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t* r)
-{
-#define CLK_IN(i) "r"(r[i])
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::CLK_R32(CLK_IN),
-        "r"(addr)
-        : "memory");
-#undef CLK_IN
-}
-
 // Keeps every use of r behind the wait before this call.
 __device__ __forceinline__ void tmem_loaded(uint32_t* r)
 {

@@ -658,7 +658,9 @@ CLK_API int clk_tree_accept(int32_t B, int32_t N, const int32_t* d_tok, const in
  * may be NaN in every element.  Scores, the softmax's maximum and sum and
  * the accumulators are float32; on the tensor cores (16-bit types, dim a
  * multiple of 8 up to 128) each weight is rounded to the inputs' type for the product with v, and
- * the sum of weights is of the unrounded ones.  out must not overlap an input. */
+ * the sum of weights is of the unrounded ones.  out must not overlap an input.
+ * There a call is a cooperative launch of one CTA per SM of the device: a
+ * process that is given fewer SMs gets CLK_ECUDA. */
 typedef struct clk_attn {
     int32_t dtype, q_heads, kv_heads, dim;
     float scale; /* finite */
