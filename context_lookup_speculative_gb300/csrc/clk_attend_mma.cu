@@ -250,6 +250,7 @@ struct Plan {
     int ctas;               // CTAs that have a share
     int b, h, item, at;     // where the share begins: unit `at` of the item
     uint32_t call;          // this CTA's flag before this call
+    long long began;        // when the CTA began, in its clocks
 };
 
 // An item whose tiles lie in several CTAs' shares.
@@ -380,7 +381,7 @@ struct Count {
 
 // This CTA's share of an item whose tiles lie in several CTAs' shares.
 template <int DP, bool BF16, bool PROMPT>
-__device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const Scratch& W, uint32_t call, const Cuts& cuts,
+__device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const Scratch& W, const Plan& plan, const Cuts& cuts,
                                           const Cut& cut, volatile int* stop)
 {
     constexpr int rows = PROMPT ? 2 * kTile : kTile;
@@ -388,14 +389,15 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
     const long long tile0 = cut.begin + kExtra<PROMPT>;
     const int c0 = cuts.holder(tile0), c1 = cuts.holder(tile0 + cut.total - 1), parts = c1 - c0 + 1;
     auto part = [&](int c) { return 2 * (c0 + c) + (c == 0 ? 1 : 0); };
-    // All CTAs of the grid are resident, and none waits before it has raised its own flag.
+    // All CTAs of the grid are resident, and none waits before it has raised its own flag.  Shares are equal but not
+    // equally long: a CTA waits, beyond the usual limit, for as long as its own share took.
     for (int c = tid; c < parts; c += kThreads) {
         uint32_t seen;
         const long long t0 = clock64();
         for (;;) {
             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(W.flag + c0 + c) : "memory");
-            if (seen != call || *stop != 0) break;
-            if (clock64() - t0 > kWaitClocks) *stop = 1;
+            if (seen != plan.call || *stop != 0) break;
+            if (clock64() - t0 > kWaitClocks + (t0 - plan.began)) *stop = 1;
         }
     }
     __syncthreads();
@@ -504,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     const Scratch W = scratch_of(scratch, S.ctas, PROMPT ? 2 * kTile : kTile);
 
     const uint32_t call = tid == 0 ? __ldcg(W.flag + blockIdx.x) : 0;
+    const long long began = clock64();
     // ---- Start: tensor memory, barriers and descriptors, while the requests' data is on its way. ----
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::oTmem) : "memory");
@@ -621,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             plan.g0 = busy ? cuts.begin(blockIdx.x) : all;
             plan.g1 = busy ? cuts.begin(blockIdx.x + 1) : all;
             plan.call = call;
+            plan.began = began;
             *stop = 0;
             cut[0].total = cut[1].total = 0;
         }
@@ -1265,7 +1269,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     const Cuts cuts(plan.all, plan.ctas);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i)
-        if (cut[i].total > 0) join_item<DP, BF16, PROMPT>(A, S, W, plan.call, cuts, cut[i], stop);
+        if (cut[i].total > 0) join_item<DP, BF16, PROMPT>(A, S, W, plan, cuts, cut[i], stop);
 }
 
 // ---------------------------------------------------------------------------

@@ -680,8 +680,8 @@ CLK_API int clk_attend_scratch_bytes(int32_t q_heads, int32_t kv_heads, int32_t 
 
 /* Synchronises `s` and returns in *dev_status CLK_ECUDA where a wait inside an
  * attention on this scratch has run out since it was zeroed (the CTAs of a
- * launch wait for one another, two seconds or so at most; the rows of that
- * call are not whole), else CLK_OK.  A call with a cache latches it there too. */
+ * launch wait for one another, at most about two seconds longer than their
+ * own share took; the rows of that call are not whole), else CLK_OK.  A call with a cache latches it there too. */
 CLK_API int clk_attend_status(const void* d_scratch, int32_t* dev_status, clk_stream_t s);
 
 /* Attention of a step's block: request b has d_nodes[b] new tokens (0 .. N,
