@@ -828,35 +828,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 return true;
             };
             int j = 0;
-            for (; j < mine; ++j) {
-                if (!(ok = fetch(j))) break;
-                // Where the weights lie apart from the scores, the reference is not compared with every tile's maximum:
-                // the sum of the tile's weights shows when one has grown too large (over 2^15), and the tile is done
-                // again.  That spares the maximum's 64 instructions in nearly all tiles; a row's first tile always
-                // takes it, and so do tiles with references that are far off.
-                bool look = !L::kApart || !settled;
-                for (;;) {
-                    if (look) {
-                        follow(j);
-                        if (far && PROMPT) break;
-                        if (far) rebase();
+            // The segment's tiles; with prompts, up to one with a reference that is far off (true).
+            auto tiles = [&]() -> bool {
+                for (; j < mine; ++j) {
+                    if (!(ok = fetch(j))) return false;
+                    // Where the weights lie apart from the scores, the reference is not compared with every tile's
+                    // maximum: the sum of the tile's weights shows when one has grown too large (over 2^15), and the tile
+                    // is done again.  That spares the maximum's 64 instructions in nearly all tiles; a row's first tile
+                    // always takes it, and so do tiles with references that are far off.
+                    bool look = !L::kApart || !settled;
+                    for (;;) {
+                        if (look) {
+                            follow(j);
+                            if (far && PROMPT) return true;
+                            if (far) rebase();
+                        }
+                        weigh(Count<0>{}, !PROMPT && far);
+                        if (look || !__any_sync(0xffffffffu, real && both.x + both.y > 32768.0f)) break;
+                        look = true;
+                        tmem_store_wait();  // stores to the same columns follow: only this wait orders two of them
                     }
-                    weigh(Count<0>{}, !PROMPT && far);
-                    if (look || !__any_sync(0xffffffffu, real && both.x + both.y > 32768.0f)) break;
-                    look = true;
-                    tmem_store_wait();  // stores to the same columns follow: only this wait orders two of them
+                    if (!(ok = give(j))) return false;
                 }
-                if ((far && PROMPT) || !(ok = give(j))) break;
-            }
+                return false;
+            };
             // With prompts, the rest of a segment with a reference that is far off goes through a loop of its own.  In the
             // loop above, the subtraction costs every call time even where it is not taken: 16 chunks with rows of 64 take
-            // 296 us so, 283 with two loops, 281 without it.  (A prompt of 25,000: 2% more than without it either way.)
+            // 296 us so, 284 with two loops, 283 without it; a prompt of 25,000 3,030, 2,975 and 2,980.
             // Trees are bound by memory and have it there: a second loop would not fit their registers (256 requests
             // 151 us, 110 so).
-            while (PROMPT && far) {
-                weigh(Count<1>{}, false);
-                if (!(ok = give(j)) || ++j == mine || !(ok = fetch(j))) break;
-                follow(j);
+            if (tiles()) {
+                for (;;) {
+                    weigh(Count<1>{}, false);
+                    if (!(ok = give(j)) || ++j == mine || !(ok = fetch(j))) break;
+                    follow(j);
+                }
             }
             if (!ok) break;
             if (mine > 0) {
