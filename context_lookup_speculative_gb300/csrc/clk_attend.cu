@@ -97,17 +97,17 @@ struct Sizes {
 // rows through scores, softmax and values: a lane scores two keys against
 // them (12 shared-memory passes for 32 multiply-adds) and then holds one of
 // every 32 columns of their results.  With 16 rows or fewer the warps without
-// rows take shares of the tile's keys (decoding 64 tokens over 2,000 rows of
-// 256: 1,046 -> 742 us), and a cluster's CTAs take every ways-th tile; their
+// rows take shares of the tile's keys (64 single tokens over 2,000 rows of 256:
+// 765 us, 1,074 without), and a cluster's CTAs take every ways-th tile; their
 // maxima, sums and results are joined in shared memory, in the order of
 // warps and ranks, so that a result does not depend on timing.
 //
 // Everything is float32, products too (tensor cores would round float32
 // inputs to 11 bits).  With many rows it is bound by the multiply-adds and
 // the shared-memory reads beside them, with few by a tile's latency.
-// Measured in float32, heads 32/8 of 128, launch included: one token over
-// 2,048 rows 31 us; 8 requests of 16 nodes over 2,000 rows 246 us; a prompt of
-// 1,000 tokens 519 us (16 TFLOP/s of the causal half).
+// Measured in float32, heads 32/8 of 128, replayed from a graph: one token over
+// 2,048 rows 23 us; 8 requests of 16 nodes over 2,000 rows 237 us; a prompt of
+// 1,000 tokens 522 us (16 TFLOP/s of the causal half).
 template <typename T, int NC>
 __device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int b, int64_t t0, uint32_t rank)
 {
@@ -475,9 +475,10 @@ int launch_general(const Attend& A, cudaStream_t s)
     G.tok = A.group < kRows ? kRows / A.group : 1;
     G.head_blocks = (A.group + G.hp - 1) / G.hp;
     const int64_t items = A.off != nullptr ? A.T / G.tok + A.B : (int64_t)A.B * ((A.N + G.tok - 1) / G.tok);
-    // Keys are shared while that leaves no more than 1.5 CTAs per SM (with rows
-    // of 256, 128 CTAs of 8 requests: shared by one 416, by two 232, by four
-    // 253, by eight 373 us).
+    // Keys are shared while that leaves no more than 1.5 CTAs per SM.  Float32
+    // rows of 256, 2,000 of them, shared by one, two, four and eight: 8 requests
+    // of 8 nodes, 64 CTAs, 407, 218, 239 and 301 us; of 16 nodes, 128 CTAs, 406,
+    // 429, 358 and 499.
     G.ways = kWays;
     const int64_t most = num_sms() * 3 / 2;
     while (G.ways > 1 && items * A.kv_heads * G.head_blocks * G.ways > most) G.ways /= 2;

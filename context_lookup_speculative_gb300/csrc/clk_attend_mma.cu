@@ -43,13 +43,13 @@
 // Bounds and figures.  Trees stream K and V: 64 requests of 2,000 to 32,000
 // tokens (heads 32/8 of 128, 4.8 GB) 690 us, 8 of 262,144 (16/2 heads) 317 us,
 // 6.9 TB/s; one token over 2,048 rows 14 us, launch, planning and joining.
-// Prompts of rows of 128 are bound by the products: 25,000 tokens 3.1 ms,
-// 1,640 TFLOP/s of the causal half, a step of two row tiles 2,350 cycles of
-// which 2,048 are products.  Rows of 64 have half the products a weight, and
-// the softmax bounds them: 2,100 cycles a step, of which the products are
-// 1,024; so their P has columns of its own beside S (the next scores need not
-// wait for the values' product) and the maximum is only looked for when a
-// tile's sum has grown too large.
+// Prompts of rows of 128 are bound by the products: 25,000 tokens 3.0 to
+// 3.1 ms, 1,640 to 1,720 TFLOP/s of the causal half, a step of two row tiles
+// 2,350 cycles of which 2,048 are products.  Rows of 64 have half the products
+// a weight, and the softmax bounds them: 2,100 cycles a step, of which the
+// products are 1,024; so their P has columns of its own beside S (the next
+// scores need not wait for the values' product) and the maximum is only looked
+// for when a tile's sum has grown too large.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -193,17 +193,20 @@ __device__ __forceinline__ int new_tiles(const Reach& x, const Shape& S, int ite
 // What an item costs besides its tiles (its result, the next one's start),
 // in tiles: about 6,000 cycles beside 2,100 a tile with prompts and 4,300
 // beside 1,800 with trees, rows of 64.  Counting it balances short items
-// with long ones: 16 prompts of 1,000 tokens on average 162 -> 102 us, 16
-// chunks behind prefixes 349 -> 293, 256 short requests 129 -> 114.
+// with long ones.  Measured without and with: 16 prompts of 500 to 1,500 tokens
+// (24/4 heads of 64) 141 and 117 us, the same behind prefixes of up to 8,192
+// (100 to 2,000 tokens) 561 and 460, 256 requests of 300 to 4,096 tokens and 13
+// nodes 128 and 117, one token over 2,048 rows (32/8 heads of 128) 13.7 and 13.1.
 template <bool PROMPT>
 constexpr int kExtra = PROMPT ? 4 : 3;
 
 // Items of at most so many tiles are not cut: joining parts takes 10,000
 // cycles and more.  They go to the CTA that holds their middle unit.
 // Measured on prompts without a limit, of 8 and of 16 tiles: one of 1,000
-// tokens 34.6, 21.8, 21.6 us; 16 of about 1,000 147, 140, 130 us; one of
-// 4,000 114, 114, 116 us.  256 requests of 64 to 512 tokens: without 63.0, of
-// 4 tiles 59.1 us.
+// tokens (32/8 heads of 128) 34.9, 22.2, 22.1 us, one of 4,000 118, 118, 120;
+// 16 of 500 to 1,500 221, 209, 208, with 24/4 heads of 64 126, 123, 117.  256
+// requests of 64 to 512 tokens and 13 nodes (24/4 heads of 64): without 67.9,
+// of 2 tiles 68.3, of 4 62.2 us.
 template <bool PROMPT>
 constexpr int kWhole = PROMPT ? 16 : 4;
 
@@ -1349,7 +1352,7 @@ bool mma_dim(int32_t dim) { return dim >= 8 && dim <= 128 && dim % 8 == 0; }
 
 // Rows of up to 128 elements of 16 bits in whole 16-byte vectors (the copies
 // fill them up to 64 or 128 with zeros: 8 requests of 16 nodes over 2,000 rows
-// of 40 take 27 us, 146 in the general kernel), groups of at most a row tile,
+// of 40, 32/8 heads, take 20 us, 136 in the general kernel), groups of at most a row tile,
 // and strides that tensor maps can take.  A scale that is not positive would
 // turn the running maximum around, and one at the end of the range would
 // leave it; both are left to the general kernel.

@@ -15,7 +15,7 @@
 // rest compacted: 853 us for 5.7 GB, 98% of the copy rate.  The end of a step
 // for 64 such requests of 16 drafted tokens (free, fork, masks, accept, grow,
 // append): 56 us, of which the fork's copy of the tails is 23 (20 at the copy
-// rate) and the rest six launches' dependent loads; for one request 17 us.
+// rate) and the rest six launches' dependent loads; for one request 18 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -542,8 +542,9 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_append(CacheDev C, const
 }
 
 // Entries of all tables up to which one CTA rewrites them.  Measured with and
-// without, a cache's life as above: 5 short prompts (220 entries) 24.1 and 24.8 us
-// and a launch less for the host; 64 slots of 125 pages 147.6 and 145.6.
+// without, a cache's life as above in one layer: 5 prompts of up to 700 tokens (220
+// entries) 24.3 and 25.3 us and a launch less for the host; 64 prompts of 2,000
+// in 125 pages each 235 and 232.
 constexpr int64_t kFewEntries = 2048;
 
 // Compaction, step 2, for entry i of slot s: the table follows, and rank[hole]
@@ -691,10 +692,10 @@ int with_vector(int bytes, F f)
 // many, and shares of the planes until there are about four CTAs an SM.
 // Finding a group's places is a chain of loads, the same for every size, so a
 // CTA takes more rows where they are short, as long as the SMs have one each.
-// A cache's life by groups of 8 and of these: 64 prompts of 2,000 in one layer
-// of 4 heads of 64 94.6 and 60.6 us (32), of 8 heads of 128 141 and 136 (16);
-// with 8 layers 8 is best (853; 16 859, 32 865).  Eight CTAs an SM for four:
-// the end of a step for 64 requests 59 us for 56.
+// A cache's life by groups of 8, of up to 16 and of up to 32: 64 prompts of 2,000
+// in one layer of 4 heads of 64 150, 102 and 80 us, of 8 heads of 128 235, 223
+// and 223; with 8 layers they take 8 anyway.  Eight CTAs an SM for four: the end
+// of a step for 64 requests 60 us for 56.
 struct Deal {
     int32_t group;
     int64_t groups;
