@@ -19,7 +19,10 @@ plus the fused launches ``propose_fuse_sched`` and ``verify_append`` that the
 
 Beside the step, the target's side of it: a paged K/V cache (``Cache`` and the
 ``cache_*`` calls), trees of drafted tokens (``tree_masks``, ``tree_accept``)
-and the attention that reads both (``tree_attend``, ``prompt_attend``).
+and the attention that reads both (``tree_attend``, ``prompt_attend``).  The
+cache may be one of 8-bit values with scales (``ScaledPool``), and queries and
+keys may be rotated by their positions on the way (``Rotary``,
+``tree_rotate``, ``cache_append_rotary``).
 """
 from __future__ import annotations
 
@@ -34,7 +37,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libclk.so")
 
 OK, EINVAL, ECAPACITY, ECUDA, ENOTIMPL, ESTATE = 0, -1, -2, -3, -4, -5
-BF16, F32, F16 = 0, 1, 2
+BF16, F32, F16, E4M3 = 0, 1, 2, 3
 SENT = -1
 BLOCK = 16
 MAX_BATCH = 8192
@@ -100,6 +103,25 @@ class AttnDesc(ctypes.Structure):
                [(n, _I64) for n in ("q_req", "q_row", "q_head", "k_req", "k_row", "k_head", "v_req", "v_row", "v_head")]
 
 
+class ScalesDesc(ctypes.Structure):
+    """clk_scales"""
+    _fields_ = [("d_base", _P), ("tokens", _I32), ("plane_stride", _I64), ("page_stride", _I64), ("head_stride", _I64),
+                ("block_stride", _I64)]
+
+
+class RotaryDesc(ctypes.Structure):
+    """clk_rotary"""
+    _fields_ = [("d_table", _P), ("positions", _I64), ("pairs", _I32), ("neighbours", _I32)]
+
+
+class TurnDesc(ctypes.Structure):
+    """clk_turn"""
+    _fields_ = [(n, _I32) for n in ("dtype", "q_heads", "kv_heads", "dim")] + \
+               [(n, _P) for n in ("d_q", "d_k", "d_q_out", "d_k_out")] + \
+               [(n, _I64) for n in ("q_req", "q_row", "q_head", "k_req", "k_row", "k_head", "qo_req", "qo_row", "qo_head",
+                                    "ko_req", "ko_row", "ko_head")]
+
+
 # (name, restype, argtypes) of every exported entry point
 _SIGS = [
     ("clk_params_default", None, [_P]),
@@ -159,6 +181,13 @@ _SIGS = [
     ("clk_attend_status", ctypes.c_int, [_P, ctypes.POINTER(_I32), _P]),
     ("clk_tree_attend", ctypes.c_int, [_P, _P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     ("clk_prompt_attend", ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _P, _I32, _P, _P, ctypes.c_size_t, _P]),
+    ("clk_cache_fork_scaled", ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _P]),
+    ("clk_cache_compact_scaled", ctypes.c_int, [_P, _P, _P, _P, _P]),
+    ("clk_tree_rotate", ctypes.c_int, [_P, _P, _I32, _P, _I32, _P, _P, _P, _P, _P]),
+    ("clk_cache_append_rotary", ctypes.c_int, [_P, _P, _I32, _P, _P, _I32, _I32, _I32, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P,
+                                               _P, _P, _P]),
+    ("clk_tree_attend_scaled", ctypes.c_int, [_P, _P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("clk_prompt_attend_scaled", ctypes.c_int, [_P, _P, _I32, _I64, _P, _P, _P, _P, _I32, _P, _P, ctypes.c_size_t, _P]),
 ]
 
 
@@ -534,8 +563,8 @@ class Cache:
     """Page tables of up to `max_slots` requests over the pages of a pool.
 
     The pool is the caller's tensor [2 * layers, >= num_pages, kv_heads,
-    page_tokens, dim] (any strides with the rows contiguous), handed to the
-    calls that move rows or read them.  ``length`` [max_slots], ``table``
+    page_tokens, dim] (any strides with the rows contiguous), or a ScaledPool
+    of 8-bit values, handed to the calls that move rows or read them.  ``length`` [max_slots], ``table``
     [max_slots, max_pages] and ``refs`` [num_pages] are int32 views of the
     workspace, to be read in stream order."""
 
@@ -603,7 +632,52 @@ class Cache:
         _check("clk_cache_status_clear", lib().clk_cache_status_clear(self.handle, _stream(stream)))
 
 
+class ScaledPool:
+    """A pool of 8-bit values and their scales (clk_scales).
+
+    ``data``: torch.float8_e4m3fn [2 * layers, >= num_pages, kv_heads,
+    page_tokens, dim] (any strides with the rows contiguous); ``scale``:
+    float32 [2 * layers, >= num_pages, kv_heads, page_tokens / T] (any
+    strides), one for each block of T = 16, 32, 64 or 128 tokens.  An element
+    stands for its value times its block's scale."""
+
+    def __init__(self, data: torch.Tensor, scale: torch.Tensor):
+        if data.dtype != torch.float8_e4m3fn or data.dim() != 5 or scale.dtype != torch.float32 or scale.dim() != 4:
+            raise ValueError("data must be float8_e4m3fn [planes, pages, heads, page_tokens, dim], "
+                             "scale float32 [planes, pages, heads, blocks]")
+        tokens, blocks = data.shape[3], scale.shape[3]
+        if not (data.is_cuda and scale.is_cuda) or data.device != scale.device:
+            raise ValueError("data and scale must be CUDA tensors of one device")
+        if data.shape[0] != scale.shape[0] or data.shape[2] != scale.shape[2] or scale.shape[1] < data.shape[1] \
+                or blocks < 1 or tokens % blocks != 0 or tokens // blocks not in (16, 32, 64, 128):
+            raise ValueError(f"scale must hold the blocks of 16, 32, 64 or 128 tokens of data's planes, pages and heads, "
+                             f"got {tuple(scale.shape)} for {tuple(data.shape)}")
+        if data.shape[4] > 1 and data.stride(4) != 1:
+            raise ValueError("rows of data must be contiguous")
+        self.data, self.scale = data, scale
+        p, g, hd, b = scale.stride()
+        self._desc = ScalesDesc(scale.data_ptr(), tokens // blocks, p, g, hd, b)
+
+    @staticmethod
+    def empty(layers: int, pages: int, kv_heads: int, page_tokens: int, dim: int, block: int = 16, device="cuda") -> "ScaledPool":
+        """A pool of zeros with scales of 1."""
+        shape = (2 * layers, pages, kv_heads)
+        return ScaledPool(torch.zeros(shape + (page_tokens, dim), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn),
+                          torch.ones(shape + (page_tokens // block,), dtype=torch.float32, device=device))
+
+
+def _pool8_desc(h: Cache, pool: ScaledPool) -> PoolDesc:
+    data = pool.data
+    planes, pages, heads, tokens, dim = data.shape
+    if pages < h.num_pages or tokens != h.page_tokens:
+        raise ValueError(f"pool must have >= {h.num_pages} pages and {h.page_tokens} tokens a page, got {tuple(data.shape)}")
+    plane_st, page_st, head_st, tok_st, _ = data.stride()
+    return PoolDesc(data.data_ptr(), E4M3, planes, heads, dim, plane_st, page_st, head_st, tok_st)
+
+
 def _pool_desc(h: Cache, pool: torch.Tensor) -> PoolDesc:
+    if not isinstance(pool, torch.Tensor):
+        raise ValueError("pool must be a tensor here")
     if not pool.is_cuda or pool.dim() != 5:
         raise ValueError("pool must be a CUDA tensor [planes, pages, heads, page_tokens, dim]")
     planes, pages, heads, tokens, dim = pool.shape
@@ -622,13 +696,8 @@ def cache_grow(h: Cache, slots, count, stream=None):
                                                   _ptr(count, shape=(B,), name="count"), _stream(stream)))
 
 
-def cache_append(h: Cache, slots, pool, k, v, count, layer: int = 0, path=None, offsets=None, stream=None):
-    """K and V rows into the slots' last count[b] positions (clk_cache_append).
-
-    k, v: [layers, B, N, kv_heads, dim], row ``path[b, i]`` (or i) of request
-    b; or, with ``offsets`` (int64 [B+1]), [layers, T, kv_heads, dim]."""
-    B = slots.numel()
-    d = _pool_desc(h, pool)
+def _append_rows(B: int, d: PoolDesc, k, v, offsets):
+    """Checks the rows of an append; their layers, N and strides (layer, row, head)."""
     if k.dim() != (4 if offsets is not None else 5) or k.shape != v.shape or not (k.is_cuda and v.is_cuda) \
             or (k.stride() != v.stride() and any(n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride()))):
         raise ValueError("k and v must be CUDA tensors of one shape and layout, "
@@ -643,13 +712,28 @@ def cache_append(h: Cache, slots, pool, k, v, count, layer: int = 0, path=None, 
     else:
         layers, N, heads, dim = k.shape
         layer_st, row, head, one = k.stride()
-    if k.dtype != pool.dtype or v.dtype != pool.dtype or heads != d.heads or dim != d.dim:
+    if k.dtype != v.dtype or _POOL_DTYPES.get(k.dtype) is None or (d.dtype != E4M3 and _POOL_DTYPES[k.dtype] != d.dtype) \
+            or heads != d.heads or dim != d.dim:
         raise ValueError("k and v must have the pool's type, heads and dim")
     if dim > 1 and one != 1:
         raise ValueError("rows of k and v must be contiguous")
+    return layers, N, layer_st if layers > 1 else 0, row, head if heads > 1 else 0
+
+
+def cache_append(h: Cache, slots, pool, k, v, count, layer: int = 0, path=None, offsets=None, stream=None):
+    """K and V rows into the slots' last count[b] positions (clk_cache_append).
+
+    k, v: [layers, B, N, kv_heads, dim], row ``path[b, i]`` (or i) of request
+    b; or, with ``offsets`` (int64 [B+1]), [layers, T, kv_heads, dim].  Into a
+    ScaledPool: cache_append_rotary without a rotation."""
+    if isinstance(pool, ScaledPool):
+        return cache_append_rotary(h, slots, pool, k, v, count, layer=layer, path=path, offsets=offsets, stream=stream)
+    B = slots.numel()
+    d = _pool_desc(h, pool)
+    layers, N, layer_st, row, head = _append_rows(B, d, k, v, offsets)
     _check("clk_cache_append",
            lib().clk_cache_append(h.handle, _ptr(slots, name="slots"), B, ctypes.byref(d), layer, layers,
-                                  k.data_ptr(), v.data_ptr(), layer_st if layers > 1 else 0, row, head if heads > 1 else 0, N,
+                                  k.data_ptr(), v.data_ptr(), layer_st, row, head, N,
                                   _ptr(offsets, torch.int64, (B + 1,), "offsets"),
                                   _ptr(path, shape=(B, N), name="path"), _ptr(count, shape=(B,), name="count"),
                                   _stream(stream)))
@@ -658,6 +742,12 @@ def cache_append(h: Cache, slots, pool, k, v, count, layer: int = 0, path=None, 
 def cache_fork(h: Cache, src, dst, pool, stream=None):
     """Slots dst[b] (empty) become copies of src[b] (clk_cache_fork)."""
     B = src.numel()
+    if isinstance(pool, ScaledPool):
+        d = _pool8_desc(h, pool)
+        _check("clk_cache_fork_scaled",
+               lib().clk_cache_fork_scaled(h.handle, _ptr(src, name="src"), _ptr(dst, shape=(B,), name="dst"), B, ctypes.byref(d),
+                                           ctypes.byref(pool._desc), _stream(stream)))
+        return
     d = _pool_desc(h, pool)
     _check("clk_cache_fork", lib().clk_cache_fork(h.handle, _ptr(src, name="src"), _ptr(dst, shape=(B,), name="dst"), B,
                                                   ctypes.byref(d), _stream(stream)))
@@ -671,9 +761,124 @@ def cache_free(h: Cache, slots, stream=None):
 def cache_compact(h: Cache, pool, moved=None, stream=None):
     """Moves the pages in use to the lowest numbers (clk_cache_compact);
     ``moved`` (int32 [1] or None) receives how many moved."""
+    if isinstance(pool, ScaledPool):
+        d = _pool8_desc(h, pool)
+        _check("clk_cache_compact_scaled",
+               lib().clk_cache_compact_scaled(h.handle, ctypes.byref(d), ctypes.byref(pool._desc),
+                                              _ptr(moved, shape=(1,), name="moved"), _stream(stream)))
+        return
     d = _pool_desc(h, pool)
     _check("clk_cache_compact", lib().clk_cache_compact(h.handle, ctypes.byref(d), _ptr(moved, shape=(1,), name="moved"),
                                                         _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Position rotation
+# ---------------------------------------------------------------------------
+class Rotary:
+    """The angles of a position rotation (clk_rotary).
+
+    ``table``: float32 [positions, 2, pairs] on the GPU, the cosines and sines
+    of every position's pairs (``Rotary.of`` makes one); ``neighbours``: pairs
+    are elements (2i, 2i + 1) instead of (i, i + pairs)."""
+
+    def __init__(self, table: torch.Tensor, neighbours: bool = False):
+        if not table.is_cuda or table.dtype != torch.float32 or table.dim() != 3 or table.shape[1] != 2 or not table.is_contiguous() \
+                or table.numel() == 0:
+            raise ValueError("table must be a contiguous float32 CUDA tensor [positions, 2, pairs]")
+        self.table, self.neighbours = table, bool(neighbours)
+        self._desc = RotaryDesc(table.data_ptr(), table.shape[0], table.shape[2], int(self.neighbours))
+
+    @staticmethod
+    def of(freq, positions: int, factor: float = 1.0, neighbours: bool = False, device="cuda") -> "Rotary":
+        """For angles position * freq[i] (radians; computed in 64 bits), cosines and sines times ``factor``."""
+        f = torch.as_tensor(freq, dtype=torch.float64, device=device)
+        a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
+        return Rotary((torch.stack([a.cos(), a.sin()], 1) * factor).float().contiguous(), neighbours)
+
+
+def _heads(t: torch.Tensor, lead, dtype, dim: int, name: str):
+    """Strides (request, row, head) of rows [lead.., heads, dim]."""
+    if not t.is_cuda or t.dtype != dtype or t.shape[:-2] != lead or t.shape[-1] != dim or (dim > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor {tuple(lead)} + (heads, {dim}) with contiguous rows")
+    st = t.stride()
+    return (st[0] if len(lead) == 2 else 0), st[-3], st[-2]
+
+
+def tree_rotate(h: Cache, slots, q, k, nodes, mask, rotary: Rotary, q_out, k_out, ctx=None, stream=None):
+    """Rotates q and k of drafted trees by their nodes' positions (clk_tree_rotate).
+
+    q [B, N, q_heads, dim], k [B, N, kv_heads, dim] (strided) into q_out and
+    k_out (their own tensors too); mask int64 [B, N] of tree_masks; ctx (int32
+    [B] or None: the slots' lengths)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, N, heads, dim]")
+    B, N = q.shape[:2]
+    code, D = _POOL_DTYPES.get(q.dtype), q.shape[3]
+    if code is None:
+        raise ValueError("q and k must have one type of bfloat16, float16 or float32")
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have q's and k's shapes")
+    lead = q.shape[:2]
+    qs, ks = _heads(q, lead, q.dtype, D, "q"), _heads(k, lead, q.dtype, D, "k")
+    qo, ko = _heads(q_out, lead, q.dtype, D, "q_out"), _heads(k_out, lead, q.dtype, D, "k_out")
+    t = TurnDesc(code, q.shape[2], k.shape[2], D, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *qs, *ks, *qo, *ko)
+    _check("clk_tree_rotate",
+           lib().clk_tree_rotate(h.handle, _ptr(slots, shape=(B,), name="slots"), B, ctypes.byref(t), N,
+                                 _ptr(nodes, shape=(B,), name="nodes"), _ptr(mask, torch.int64, (B, N), "mask"),
+                                 _ptr(ctx, shape=(B,), name="ctx"), ctypes.byref(rotary._desc), _stream(stream)))
+
+
+def _flat_rows(t: torch.Tensor, lead, dtype, dim: int, name: str):
+    """Strides (row, head) of rows [lead.., heads, dim] whose requests follow one another."""
+    req, row, head = _heads(t, lead, dtype, dim, name)
+    if len(lead) == 2:
+        if lead[1] == 1:
+            row = req if lead[0] > 1 else 0
+        elif lead[0] > 1 and req != lead[1] * row:
+            raise ValueError(f"{name} must hold one request's rows after another's")
+    return row, head
+
+
+def cache_append_rotary(h: Cache, slots, pool, k, v, count, rotary: Optional[Rotary] = None, layer: int = 0, path=None, offsets=None,
+                        q=None, q_out=None, k_out=None, stream=None):
+    """cache_append with the keys rotated by their positions on the way (rotary
+    None: as they are), into a pool of their type or a ScaledPool
+    (clk_cache_append_rotary).
+
+    With one layer and without path, q [B, N, q_heads, dim] (or [T, q_heads,
+    dim]) of the same tokens is rotated into q_out and the rotated keys are
+    also written to k_out (k's shape); either may be the source itself."""
+    B = slots.numel()
+    eight = isinstance(pool, ScaledPool)
+    d = _pool8_desc(h, pool) if eight else _pool_desc(h, pool)
+    layers, N, layer_st, row, head = _append_rows(B, d, k, v, offsets)
+    code, t = _POOL_DTYPES[k.dtype], None
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None or k_out is not None:
+        if rotary is None or layers != 1 or path is not None:
+            raise ValueError("q and k_out need a rotation, one layer and no path")
+        lead = k.shape[1:-2]
+        t = TurnDesc(code, 0, d.heads, d.dim)
+        if q is not None:
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+            t.q_heads, t.d_q, t.d_q_out = q.shape[-2], q.data_ptr(), q_out.data_ptr()
+            t.q_row, t.q_head = _flat_rows(q, lead, k.dtype, d.dim, "q")
+            t.qo_row, t.qo_head = _flat_rows(q_out, lead, k.dtype, d.dim, "q_out")
+        if k_out is not None:
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have k's shape")
+            t.d_k_out = k_out.data_ptr()
+            t.ko_row, t.ko_head = _flat_rows(k_out[0], lead, k.dtype, d.dim, "k_out")
+    _check("clk_cache_append_rotary",
+           lib().clk_cache_append_rotary(h.handle, _ptr(slots, name="slots"), B, ctypes.byref(d),
+                                         ctypes.byref(pool._desc) if eight else None, layer, layers, code, k.data_ptr(), v.data_ptr(),
+                                         layer_st, row, head, N, _ptr(offsets, torch.int64, (B + 1,), "offsets"),
+                                         _ptr(path, shape=(B, N), name="path"), _ptr(count, shape=(B,), name="count"),
+                                         ctypes.byref(rotary._desc) if rotary is not None else None,
+                                         ctypes.byref(t) if t is not None else None, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
@@ -747,12 +952,22 @@ def tree_attend(h: Cache, slots, pool, layer: int, q, k, v, nodes, mask, scale: 
 
     q [B, N, q_heads, dim], k and v [B, N, kv_heads, dim] of the new tokens
     (strided), mask int64 [B, N], out [B, N, q_heads, dim]; ctx (int32 [B] or
-    None: the slots' lengths) cached rows that are seen."""
+    None: the slots' lengths) cached rows that are seen.  The pool is of q's
+    type or a ScaledPool (clk_tree_attend_scaled)."""
     if not q.dim() == k.dim() == v.dim() == 4:
         raise ValueError("q, k and v must be [B, N, heads, dim]")
     B, N = q.shape[:2]
-    d = _pool_desc(h, pool)
     a = _attn_desc(q, k, v, out, scale)
+    if isinstance(pool, ScaledPool):
+        d = _pool8_desc(h, pool)
+        _check("clk_tree_attend_scaled",
+               lib().clk_tree_attend_scaled(h.handle, _ptr(slots, shape=(B,), name="slots"), B, ctypes.byref(d),
+                                            ctypes.byref(pool._desc), layer, ctypes.byref(a), N,
+                                            _ptr(nodes, shape=(B,), name="nodes"), _ptr(mask, torch.int64, (B, N), "mask"),
+                                            _ptr(ctx, shape=(B,), name="ctx"), _ptr(scratch, torch.uint8, name="scratch"),
+                                            scratch.numel(), _stream(stream)))
+        return
+    d = _pool_desc(h, pool)
     _check("clk_tree_attend",
            lib().clk_tree_attend(h.handle, _ptr(slots, shape=(B,), name="slots"), B, ctypes.byref(d), layer,
                                  ctypes.byref(a), N, _ptr(nodes, shape=(B,), name="nodes"),
@@ -766,8 +981,8 @@ def prompt_attend(q, k, v, offsets, scale: float, out, scratch, cache: Optional[
 
     q [T, q_heads, dim], k and v [T, kv_heads, dim] (strided), request b's
     rows offsets[b] .. offsets[b+1] (int64 [B+1]), out [T, q_heads, dim].
-    With cache, slots, pool and ctx (int32 [B]) the rows also see the slots'
-    first ctx cached rows."""
+    With cache, slots, pool (of q's type, or a ScaledPool) and ctx (int32 [B])
+    the rows also see the slots' first ctx cached rows."""
     if not q.dim() == k.dim() == v.dim() == 3:
         raise ValueError("q, k and v must be [T, heads, dim]")
     B = offsets.numel() - 1
@@ -775,8 +990,16 @@ def prompt_attend(q, k, v, offsets, scale: float, out, scratch, cache: Optional[
         raise ValueError("slots, pool and ctx need a cache")
     if cache is not None and (slots is None or pool is None):
         raise ValueError("a cache needs slots and a pool")
-    d = _pool_desc(cache, pool) if cache is not None else None
     a = _attn_desc(q, k, v, out, scale)
+    if isinstance(pool, ScaledPool):
+        d = _pool8_desc(cache, pool)
+        _check("clk_prompt_attend_scaled",
+               lib().clk_prompt_attend_scaled(ctypes.byref(a), _ptr(offsets, torch.int64, (B + 1,), "offsets"), B, q.shape[0],
+                                              cache.handle, _ptr(slots, shape=(B,), name="slots"), ctypes.byref(d),
+                                              ctypes.byref(pool._desc), layer, _ptr(ctx, shape=(B,), name="ctx"),
+                                              _ptr(scratch, torch.uint8, name="scratch"), scratch.numel(), _stream(stream)))
+        return
+    d = _pool_desc(cache, pool) if cache is not None else None
     _check("clk_prompt_attend",
            lib().clk_prompt_attend(ctypes.byref(a), _ptr(offsets, torch.int64, (B + 1,), "offsets"), B, q.shape[0],
                                    cache.handle if cache is not None else None, _ptr(slots, shape=(B,), name="slots"),

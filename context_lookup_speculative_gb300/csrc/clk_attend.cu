@@ -12,6 +12,7 @@
 #include "clk.h"
 #include "clk_attend.h"
 #include "clk_cache.h"
+#include "clk_eight.cuh"
 #include "clk_host.h"
 
 namespace clk {
@@ -73,6 +74,28 @@ __device__ __forceinline__ float4 to_f4(uint2 x)
 template <typename T>
 __device__ __forceinline__ float4 to_f4(float4 x) { return x; }
 
+// Four codes of 8 bits, in the place of four elements, and the elements that they stand for: rounded to the type.
+template <typename F>
+__device__ __forceinline__ F take4_codes(const uint8_t* p, int left, bool vec)
+{
+    uint32_t w;
+    if (vec)
+        w = *reinterpret_cast<const uint32_t*>(p);
+    else
+        w = p[0] | (left > 1 ? p[1] : 0u) << 8 | (left > 2 ? p[2] : 0u) << 16 | (left > 3 ? p[3] : 0u) << 24;
+    F x{};
+    reinterpret_cast<uint32_t&>(x.x) = w;
+    return x;
+}
+template <typename T, typename F>
+__device__ __forceinline__ float4 of_codes(F x, float scale)
+{
+    float f[4];
+    from_e4m3x4(reinterpret_cast<const uint32_t&>(x.x), f);
+    return make_float4(to_f(from_f<T>(f[0] * scale)), to_f(from_f<T>(f[1] * scale)), to_f(from_f<T>(f[2] * scale)),
+                       to_f(from_f<T>(f[3] * scale)));
+}
+
 // How a call is cut: a CTA's rows are `tok` tokens x `hp` heads of one K/V
 // head's group, a cluster of `ways` CTAs takes every ways-th tile of its keys.
 struct Rows {
@@ -108,13 +131,14 @@ struct Sizes {
 // Measured in float32, heads 32/8 of 128, replayed from a graph: one token over
 // 2,048 rows 23 us; 8 requests of 16 nodes over 2,000 rows 237 us; a prompt of
 // 1,000 tokens 522 us (16 TFLOP/s of the causal half).
-template <typename T, int NC>
+template <typename T, int NC, bool EIGHT>
 __device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int b, int64_t t0, uint32_t rank)
 {
     using Z = Sizes<NC>;
     extern __shared__ __align__(16) float sm[];
     __shared__ int64_t src[2][kKeys];     // offset in the pool, -2 - i for new token i, -1 for none
     __shared__ float stats[kRows][2];
+    __shared__ float scales[2][2][EIGHT ? kKeys : 1];  // of K's and V's cached rows
     float *const sk = sm, *const sv = sm + Z::kAtV, *const sq = sm + Z::kAtQ;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int kh = blockIdx.y / G.head_blocks, h0 = kh * A.group + (blockIdx.y - kh * G.head_blocks) * G.hp;
@@ -160,12 +184,20 @@ __device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int 
     }
     const int64_t fresh = prompt ? t0 + have / hp : R.rows;
     const int64_t keys = R.ctx + fresh, all = R.ctx + (prompt ? t0 + 1 : 0);  // keys below `all` are seen by every row
-    auto locate = [&](int64_t j) -> int64_t {
+    // (with 8 bits a cached row's scales are put at place `at` beside it)
+    auto locate = [&](int64_t j, int at) -> int64_t {
         if (j >= keys) return -1;
         if (j >= R.ctx) return -2 - (j - R.ctx);
         const int32_t page = A.C.table[(int64_t)R.slot * A.C.max_pages + (j >> A.C.shift)];
-        if (page >= 0 && page < A.C.num_pages)
-            return page * A.page_stride + kh * A.head_stride + (j & (A.C.page_tokens() - 1)) * A.tok_stride;
+        if (page >= 0 && page < A.C.num_pages) {
+            const int line = (int)(j & (A.C.page_tokens() - 1));
+            if (EIGHT) {
+                const int64_t i = page * A.scale_page + kh * A.scale_head + (line >> A.scale_shift) * A.scale_block;
+                scales[at][0][threadIdx.x] = A.ks[i];
+                scales[at][1][threadIdx.x] = A.vs[i];
+            }
+            return page * A.page_stride + kh * A.head_stride + line * A.tok_stride;
+        }
         latch(A.C.status, CLK_EINVAL, R.slot);
         return -1;
     };
@@ -181,10 +213,10 @@ __device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int 
     const int64_t step = (int64_t)G.ways * kKeys;
     const bool active = 4 * quad < have;
     int cur = 0;
-    if (tid < kKeys) src[0][tid] = locate((int64_t)rank * kKeys + tid);
+    if (tid < kKeys) src[0][tid] = locate((int64_t)rank * kKeys + tid, 0);
     for (int64_t j0 = (int64_t)rank * kKeys; j0 < keys; j0 += step, cur ^= 1) {
         __syncthreads();  // the last tile is done with, this one's places are known
-        if (tid < kKeys) src[cur ^ 1][tid] = locate(j0 + step + tid);
+        if (tid < kKeys) src[cur ^ 1][tid] = locate(j0 + step + tid, cur ^ 1);
         constexpr int kLanes = NC >= 4 ? 32 : NC * 8;        // lanes a row's vectors take
         constexpr int kPass = NC * 8 * kKeys / kThreads;     // vectors a lane takes of K, and of V
         constexpr int kOnce = kPass < 8 ? kPass : 8;
@@ -198,7 +230,12 @@ __device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int 
                 const int x = 4 * (NC == 8 ? lane + 32 * (i & 1) : lane % kLanes);
                 const int64_t o = src[cur][r];
                 kk[u] = vv[u] = typename Four<T>::type{};
-                if (o != -1 && x < A.dim) {
+                if (EIGHT && o >= 0) {
+                    if (x < A.dim) {
+                        kk[u] = take4_codes<typename Four<T>::type>(static_cast<const uint8_t*>(A.kc) + o + x, A.dim - x, G.vec);
+                        vv[u] = take4_codes<typename Four<T>::type>(static_cast<const uint8_t*>(A.vc) + o + x, A.dim - x, G.vec);
+                    }
+                } else if (o != -1 && x < A.dim) {
                     const T* const pk = o >= 0 ? static_cast<const T*>(A.kc) + o : static_cast<const T*>(A.k) + k0 + (-2 - o) * A.k_row;
                     const T* const pv = o >= 0 ? static_cast<const T*>(A.vc) + o : static_cast<const T*>(A.v) + v0 + (-2 - o) * A.v_row;
                     kk[u] = take4(pk + x, A.dim - x, G.vec);
@@ -210,8 +247,9 @@ __device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int 
                 const int i = i0 + u;
                 const int r = warp * (kKeys / 8) + (NC == 8 ? i >> 1 : i * (32 / kLanes) + lane / kLanes);
                 const int x = 4 * (NC == 8 ? lane + 32 * (i & 1) : lane % kLanes);
-                *reinterpret_cast<float4*>(sk + r * Z::kK + x) = to_f4<T>(kk[u]);
-                *reinterpret_cast<float4*>(sv + r * Z::kV + x) = to_f4<T>(vv[u]);
+                const bool codes = EIGHT && src[cur][r] >= 0;
+                *reinterpret_cast<float4*>(sk + r * Z::kK + x) = codes ? of_codes<T>(kk[u], scales[cur][0][EIGHT ? r : 0]) : to_f4<T>(kk[u]);
+                *reinterpret_cast<float4*>(sv + r * Z::kV + x) = codes ? of_codes<T>(vv[u], scales[cur][1][EIGHT ? r : 0]) : to_f4<T>(vv[u]);
             }
         }
         __syncthreads();
@@ -398,7 +436,7 @@ __device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int 
 
 // A cluster's rows: those of tokens t0 .. t0 + tok - 1 of request b, by its
 // place in the grid.
-template <typename T, int NC>
+template <typename T, int NC, bool EIGHT>
 __global__ void __launch_bounds__(kThreads, 1) k_attend_rows(Attend A, Rows G)
 {
     const int tid = threadIdx.x;
@@ -434,12 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_rows(Attend A, Rows G)
             if (b == A.B) return;
             t0 = (int64_t)(item - (uint32_t)A.off[b] / G.tok - b) * G.tok;
         }
-        attend_rows<T, NC>(A, G, b, t0, rank);
+        attend_rows<T, NC, EIGHT>(A, G, b, t0, rank);
         if (falls) __syncthreads();  // shared memory is used again
     } while (falls);
 }
 
-template <typename T, int NC>
+template <typename T, int NC, bool EIGHT>
 int launch_rows(const Attend& A, const Rows& G, int64_t items, cudaStream_t s)
 {
     constexpr int kBytes = Sizes<NC>::kTotal;
@@ -448,7 +486,7 @@ int launch_rows(const Attend& A, const Rows& G, int64_t items, cudaStream_t s)
     if (cudaGetDevice(&dev) != cudaSuccess) return CLK_ECUDA;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit) || dev > 63) {
-        if (cudaFuncSetAttribute(k_attend_rows<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(k_attend_rows<T, NC, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
             return CLK_ECUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
@@ -464,7 +502,7 @@ int launch_rows(const Attend& A, const Rows& G, int64_t items, cudaStream_t s)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, k_attend_rows<T, NC>, A, G));
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_attend_rows<T, NC, EIGHT>, A, G));
 }
 
 template <typename T>
@@ -487,10 +525,16 @@ int launch_general(const Attend& A, cudaStream_t s)
     if (A.C.status != nullptr)
         for (int64_t x : {A.page_stride, A.head_stride, A.tok_stride}) odd |= x;
     G.vec = odd % 4 == 0;
-    for (const void* x : {A.k, A.v, A.kc, A.vc}) G.vec = G.vec && aligned(x, 4 * sizeof(T));
-    if (A.dim <= 64) return launch_rows<T, 2>(A, G, items, s);
-    if (A.dim <= 128) return launch_rows<T, 4>(A, G, items, s);
-    return launch_rows<T, 8>(A, G, items, s);
+    for (const void* x : {A.k, A.v}) G.vec = G.vec && aligned(x, 4 * sizeof(T));
+    for (const void* x : {A.kc, A.vc}) G.vec = G.vec && aligned(x, A.ks != nullptr ? 4 : 4 * sizeof(T));
+    if (A.ks != nullptr) {
+        if (A.dim <= 64) return launch_rows<T, 2, true>(A, G, items, s);
+        if (A.dim <= 128) return launch_rows<T, 4, true>(A, G, items, s);
+        return launch_rows<T, 8, true>(A, G, items, s);
+    }
+    if (A.dim <= 64) return launch_rows<T, 2, false>(A, G, items, s);
+    if (A.dim <= 128) return launch_rows<T, 4, false>(A, G, items, s);
+    return launch_rows<T, 8, false>(A, G, items, s);
 }
 
 int launch_attend(const Attend& A, void* scratch, size_t bytes, cudaStream_t s)
@@ -508,8 +552,8 @@ int launch_attend(const Attend& A, void* scratch, size_t bytes, cudaStream_t s)
 }
 
 // Checks what both calls share and fills the common fields.
-int fill_attend(Attend& A, const clk_attn* a, clk_cache* h, const int32_t* d_slots, const clk_pool* pool, int32_t layer,
-                const int32_t* d_ctx, int32_t B)
+int fill_attend(Attend& A, const clk_attn* a, clk_cache* h, const int32_t* d_slots, const clk_pool* pool, const clk_scales* scales,
+                int32_t layer, const int32_t* d_ctx, int32_t B)
 {
     if (a == nullptr || B < 0 || B > CLK_MAX_BATCH) return CLK_EINVAL;
     const int es = dtype_bytes(a->dtype);
@@ -524,16 +568,26 @@ int fill_attend(Attend& A, const clk_attn* a, clk_cache* h, const int32_t* d_slo
     if (h != nullptr) {
         int rc = check_cache_batch(h, B);
         if (rc != CLK_OK) return rc;
-        if (check_pool(pool) != CLK_OK || pool->dtype != a->dtype || pool->heads != a->kv_heads || pool->dim != a->dim ||
-            layer < 0 || layer >= pool->planes / 2)
+        if (scales != nullptr ? check_pool8(pool, scales, h->dev.page_tokens()) != CLK_OK
+                              : check_pool(pool) != CLK_OK || pool->dtype != a->dtype)
             return CLK_EINVAL;
+        if (pool->heads != a->kv_heads || pool->dim != a->dim || layer < 0 || layer >= pool->planes / 2) return CLK_EINVAL;
         if (B > 0 && !ok_i32(d_slots)) return CLK_EINVAL;
         A.C = h->dev;
         A.slots = d_slots;
         A.ctx = d_ctx;
         const char* base = static_cast<const char*>(pool->d_base);
-        A.kc = base + 2 * (int64_t)layer * pool->plane_stride * es;
-        A.vc = base + (2 * (int64_t)layer + 1) * pool->plane_stride * es;
+        const int64_t ps = pool_bytes(pool->dtype), kp = 2 * (int64_t)layer;
+        A.kc = base + kp * pool->plane_stride * ps;
+        A.vc = base + (kp + 1) * pool->plane_stride * ps;
+        if (scales != nullptr) {
+            A.ks = scales->d_base + kp * scales->plane_stride;
+            A.vs = scales->d_base + (kp + 1) * scales->plane_stride;
+            A.scale_page = scales->page_stride;
+            A.scale_head = scales->head_stride;
+            A.scale_block = scales->block_stride;
+            while ((1 << A.scale_shift) < scales->tokens) ++A.scale_shift;
+        }
         A.page_stride = pool->page_stride;
         A.head_stride = pool->head_stride;
         A.tok_stride = pool->tok_stride;
@@ -589,13 +643,16 @@ extern "C" int clk_attend_status(const void* d_scratch, int32_t* dev_status, clk
     return CLK_OK;
 }
 
-extern "C" int clk_tree_attend(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool, int32_t layer,
-                               const clk_attn* a, int32_t N, const int32_t* d_nodes, const int64_t* d_mask,
-                               const int32_t* d_ctx, void* d_scratch, size_t scratch_bytes, clk_stream_t s)
+namespace clk {
+namespace {
+
+int tree_call(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool, const clk_scales* scales, int32_t layer,
+              const clk_attn* a, int32_t N, const int32_t* d_nodes, const int64_t* d_mask, const int32_t* d_ctx, void* d_scratch,
+              size_t scratch_bytes, cudaStream_t s)
 {
     if (h == nullptr) return CLK_ESTATE;
     Attend A;
-    const int rc = fill_attend(A, a, h, d_slots, pool, layer, d_ctx, B);
+    const int rc = fill_attend(A, a, h, d_slots, pool, scales, layer, d_ctx, B);
     if (rc != CLK_OK) return rc;
     if (N < 1 || N > CLK_TREE_MAX) return CLK_EINVAL;
     if (B == 0) return CLK_OK;
@@ -603,21 +660,56 @@ extern "C" int clk_tree_attend(clk_cache* h, const int32_t* d_slots, int32_t B, 
     A.nodes = d_nodes;
     A.mask = d_mask;
     A.N = N;
-    return launch_attend(A, d_scratch, scratch_bytes, (cudaStream_t)s);
+    return launch_attend(A, d_scratch, scratch_bytes, s);
 }
 
-extern "C" int clk_prompt_attend(const clk_attn* a, const int64_t* d_off, int32_t B, int64_t T, clk_cache* h,
-                                 const int32_t* d_slots, const clk_pool* pool, int32_t layer, const int32_t* d_ctx,
-                                 void* d_scratch, size_t scratch_bytes, clk_stream_t s)
+int prompt_call(const clk_attn* a, const int64_t* d_off, int32_t B, int64_t T, clk_cache* h, const int32_t* d_slots,
+                const clk_pool* pool, const clk_scales* scales, int32_t layer, const int32_t* d_ctx, void* d_scratch,
+                size_t scratch_bytes, cudaStream_t s)
 {
     Attend A;
     if (h == nullptr && d_ctx != nullptr) return CLK_EINVAL;
-    const int rc = fill_attend(A, a, h, d_slots, pool, layer, d_ctx, B);
+    const int rc = fill_attend(A, a, h, d_slots, pool, scales, layer, d_ctx, B);
     if (rc != CLK_OK) return rc;
     if (T < 0 || T > ((int64_t)1 << 30)) return CLK_EINVAL;
     if (B == 0 || T == 0) return CLK_OK;
     if (!attn_pointers(a) || d_off == nullptr || !aligned(d_off, 8)) return CLK_EINVAL;
     A.off = d_off;
     A.T = T;
-    return launch_attend(A, d_scratch, scratch_bytes, (cudaStream_t)s);
+    return launch_attend(A, d_scratch, scratch_bytes, s);
+}
+
+}  // namespace
+}  // namespace clk
+
+extern "C" int clk_tree_attend(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool, int32_t layer,
+                               const clk_attn* a, int32_t N, const int32_t* d_nodes, const int64_t* d_mask,
+                               const int32_t* d_ctx, void* d_scratch, size_t scratch_bytes, clk_stream_t s)
+{
+    return tree_call(h, d_slots, B, pool, nullptr, layer, a, N, d_nodes, d_mask, d_ctx, d_scratch, scratch_bytes, (cudaStream_t)s);
+}
+
+extern "C" int clk_tree_attend_scaled(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool,
+                                      const clk_scales* scales, int32_t layer, const clk_attn* a, int32_t N,
+                                      const int32_t* d_nodes, const int64_t* d_mask, const int32_t* d_ctx, void* d_scratch,
+                                      size_t scratch_bytes, clk_stream_t s)
+{
+    if (h != nullptr && scales == nullptr) return CLK_EINVAL;
+    return tree_call(h, d_slots, B, pool, scales, layer, a, N, d_nodes, d_mask, d_ctx, d_scratch, scratch_bytes, (cudaStream_t)s);
+}
+
+extern "C" int clk_prompt_attend(const clk_attn* a, const int64_t* d_off, int32_t B, int64_t T, clk_cache* h,
+                                 const int32_t* d_slots, const clk_pool* pool, int32_t layer, const int32_t* d_ctx,
+                                 void* d_scratch, size_t scratch_bytes, clk_stream_t s)
+{
+    return prompt_call(a, d_off, B, T, h, d_slots, pool, nullptr, layer, d_ctx, d_scratch, scratch_bytes, (cudaStream_t)s);
+}
+
+extern "C" int clk_prompt_attend_scaled(const clk_attn* a, const int64_t* d_off, int32_t B, int64_t T, clk_cache* h,
+                                        const int32_t* d_slots, const clk_pool* pool, const clk_scales* scales, int32_t layer,
+                                        const int32_t* d_ctx, void* d_scratch, size_t scratch_bytes, clk_stream_t s)
+{
+    if (h == nullptr) return CLK_ESTATE;
+    if (scales == nullptr) return CLK_EINVAL;
+    return prompt_call(a, d_off, B, T, h, d_slots, pool, scales, layer, d_ctx, d_scratch, scratch_bytes, (cudaStream_t)s);
 }

@@ -17,6 +17,10 @@ struct Attend {
     const int32_t* ctx;    // null: the slot's length (tree), 0 (prompt)
     const void *kc, *vc;   // the layer's two planes; null without a cache
     int64_t page_stride, head_stride, tok_stride;
+    // a pool in 8 bits: its scales in the two planes (null for one of q's type), a block's rows as a power of two
+    const float *ks, *vs;
+    int64_t scale_page, scale_head, scale_block;
+    int32_t scale_shift;
     const void *q, *k, *v;
     void* out;
     int64_t q_req, q_row, q_head, k_req, k_row, k_head, v_req, v_row, v_head;

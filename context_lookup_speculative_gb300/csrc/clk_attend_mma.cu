@@ -1358,6 +1358,7 @@ bool mma_dim(int32_t dim) { return dim >= 8 && dim <= 128 && dim % 8 == 0; }
 // leave it; both are left to the general kernel.
 bool attend_mma_takes(const Attend& A)
 {
+    if (A.ks != nullptr) return false;
     if (A.dtype == CLK_DTYPE_F32 || !mma_dim(A.dim) || A.group > kTile || !(A.scale >= 1e-20f && A.scale <= 1e20f))
         return false;
     for (const void* p : {A.q, A.k, A.v, (const void*)A.out, A.kc, A.vc})

@@ -650,11 +650,49 @@ __global__ void __launch_bounds__(kCopyThreads) k_compact_copy(CacheDev C, VecPo
     }
 }
 
+// The scales of pages that were copied, page by page: heads * blocks words in each plane.
+struct ScaleDev {
+    uint32_t* base;
+    int64_t plane, page, head, block;
+    int32_t planes, heads, blocks;
+};
+
+__device__ __forceinline__ void copy_scales(const ScaleDev& X, int64_t src, int64_t dst, int first, int step)
+{
+    const int each = X.heads * X.blocks, all = each * X.planes;
+    for (int i = first; i < all; i += step) {
+        const int plane = i / each, j = i - plane * each, head = j / X.blocks;
+        const int64_t at = plane * X.plane + head * X.head + (j - head * X.blocks) * X.block;
+        X.base[at + dst * X.page] = X.base[at + src * X.page];
+    }
+}
+
+// After k_cache_fork: the tails' pages.
+__global__ void __launch_bounds__(kCopyThreads) k_fork_scales(CacheDev C, const int32_t* src, ScaleDev X)
+{
+    chained();
+    const int b = blockIdx.x;
+    const int32_t tail = C.req[b].y;
+    if (tail < 0) return;
+    const int32_t s = src[b];
+    const int32_t page = C.table[(int64_t)s * C.max_pages + C.held(C.len[s]) - 1];
+    copy_scales(X, page, tail, threadIdx.x, kCopyThreads);
+}
+
+// After k_compact_copy: the pages that moved.
+__global__ void __launch_bounds__(kCopyThreads) k_compact_scales(CacheDev C, ScaleDev X)
+{
+    chained();
+    const int32_t *const holes = C.list, *const movers = C.list + C.num_pages;
+    const int32_t n = C.list[3 * (int64_t)C.num_pages];
+    for (int32_t r = blockIdx.x; r < n; r += gridDim.x) copy_scales(X, movers[r], holes[r], threadIdx.x, kCopyThreads);
+}
+
 // The widest vector that a pool (and a source's pointers and strides, in
 // bytes) can be moved in.
 int vector_bytes(const clk_pool& p, int64_t more)
 {
-    const int64_t es = dtype_bytes(p.dtype);
+    const int64_t es = pool_bytes(p.dtype);
     const int64_t all = (int64_t)(uintptr_t)p.d_base | p.plane_stride * es | p.page_stride * es | p.head_stride * es |
                         p.tok_stride * es | p.dim * es | more;
     const int64_t low = all & -all;
@@ -664,7 +702,7 @@ int vector_bytes(const clk_pool& p, int64_t more)
 template <typename V>
 VecPool<V> vec_pool(const clk_pool& p)
 {
-    const int64_t es = dtype_bytes(p.dtype), v = sizeof(V);
+    const int64_t es = pool_bytes(p.dtype), v = sizeof(V);
     return VecPool<V>{static_cast<V*>(p.d_base),
                       p.plane_stride * es / v,
                       p.page_stride * es / v,
@@ -684,6 +722,7 @@ int with_vector(int bytes, F f)
     case 8: return f(uint2{});
     case 4: return f(uint32_t{});
     case 2: return f(uint16_t{});
+    case 1: return f(uint8_t{});
     default: return CLK_EINVAL;
     }
 }
@@ -713,7 +752,40 @@ Deal deal(int64_t rows, int64_t bytes, int32_t planes)
     return d;
 }
 
-int64_t token_bytes(const clk_pool& p, int32_t planes) { return (int64_t)planes * p.heads * p.dim * dtype_bytes(p.dtype); }
+ScaleDev scale_dev(const clk_scales& x, const clk_pool& p, int32_t page_tokens)
+{
+    return ScaleDev{reinterpret_cast<uint32_t*>(x.d_base), x.plane_stride, x.page_stride, x.head_stride, x.block_stride, p.planes, p.heads,
+                    page_tokens / x.tokens};
+}
+
+int64_t token_bytes(const clk_pool& p, int32_t planes) { return (int64_t)planes * p.heads * p.dim * pool_bytes(p.dtype); }
+
+int fork_slots(clk_cache* h, const int32_t* d_src, const int32_t* d_dst, int32_t B, const clk_pool* pool, cudaStream_t s)
+{
+    if (B == 0) return CLK_OK;
+    if (!ok_i32(d_src) || !ok_i32(d_dst)) return CLK_EINVAL;
+    const int rc = launch_chained(k_cache_plan<true>, 1, kPlanThreads, s, h->dev, d_src, d_dst, (const int32_t*)nullptr, B);
+    if (rc != CLK_OK) return rc;
+    const Deal deals = deal((int64_t)B * (h->dev.page_tokens() - 1), token_bytes(*pool, pool->planes), pool->planes);
+    const unsigned x = (unsigned)(deals.groups > B ? deals.groups : B);
+    return with_vector(vector_bytes(*pool, 0), [&](auto v) {
+        using V = decltype(v);
+        return launch_chained(k_cache_fork<V>, dim3(x, deals.shares), kCopyThreads, s, h->dev, d_src, d_dst, B, vec_pool<V>(*pool),
+                              deals.group);
+    });
+}
+
+int compact_pages(clk_cache* h, const clk_pool* pool, int32_t* d_moved, cudaStream_t s)
+{
+    int rc;
+    const bool few = (int64_t)h->dev.max_slots * h->dev.max_pages <= kFewEntries;
+    if ((rc = launch_chained(k_compact_plan, 1, kPlanThreads, s, h->dev, d_moved, few)) != CLK_OK) return rc;
+    if (!few && (rc = launch_chained(k_compact_table, dim3((unsigned)h->dev.max_slots), kCopyThreads, s, h->dev)) != CLK_OK) return rc;
+    return with_vector(vector_bytes(*pool, 0), [&](auto v) {
+        using V = decltype(v);
+        return launch_chained(k_compact_copy<V>, dim3((unsigned)(8 * num_sms())), kCopyThreads, s, h->dev, vec_pool<V>(*pool));
+    });
+}
 
 }  // namespace
 }  // namespace clk
@@ -823,20 +895,22 @@ extern "C" int clk_cache_free(clk_cache* h, const int32_t* d_slots, int32_t B, c
 extern "C" int clk_cache_fork(clk_cache* h, const int32_t* d_src, const int32_t* d_dst, int32_t B, const clk_pool* pool,
                               clk_stream_t s)
 {
-    int rc = check_cache_batch(h, B);
+    const int rc = check_cache_batch(h, B);
     if (rc != CLK_OK) return rc;
     if (check_pool(pool) != CLK_OK) return CLK_EINVAL;
-    if (B == 0) return CLK_OK;
-    if (!ok_i32(d_src) || !ok_i32(d_dst)) return CLK_EINVAL;
-    rc = launch_chained(k_cache_plan<true>, 1, kPlanThreads, (cudaStream_t)s, h->dev, d_src, d_dst, (const int32_t*)nullptr, B);
+    return fork_slots(h, d_src, d_dst, B, pool, (cudaStream_t)s);
+}
+
+extern "C" int clk_cache_fork_scaled(clk_cache* h, const int32_t* d_src, const int32_t* d_dst, int32_t B, const clk_pool* pool,
+                                     const clk_scales* scales, clk_stream_t s)
+{
+    int rc = check_cache_batch(h, B);
     if (rc != CLK_OK) return rc;
-    const Deal deals = deal((int64_t)B * (h->dev.page_tokens() - 1), token_bytes(*pool, pool->planes), pool->planes);
-    const unsigned x = (unsigned)(deals.groups > B ? deals.groups : B);
-    return with_vector(vector_bytes(*pool, 0), [&](auto v) {
-        using V = decltype(v);
-        return launch_chained(k_cache_fork<V>, dim3(x, deals.shares), kCopyThreads, (cudaStream_t)s, h->dev, d_src, d_dst, B,
-                            vec_pool<V>(*pool), deals.group);
-    });
+    if (check_pool8(pool, scales, h->dev.page_tokens()) != CLK_OK) return CLK_EINVAL;
+    rc = fork_slots(h, d_src, d_dst, B, pool, (cudaStream_t)s);
+    if (rc != CLK_OK || B == 0) return rc;
+    return launch_chained(k_fork_scales, dim3((unsigned)B), kCopyThreads, (cudaStream_t)s, h->dev, d_src,
+                          scale_dev(*scales, *pool, h->dev.page_tokens()));
 }
 
 extern "C" int clk_cache_append(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool, int32_t layer0,
@@ -871,15 +945,20 @@ extern "C" int clk_cache_append(clk_cache* h, const int32_t* d_slots, int32_t B,
 
 extern "C" int clk_cache_compact(clk_cache* h, const clk_pool* pool, int32_t* d_moved, clk_stream_t s)
 {
-    int rc = check_cache_batch(h, 0);
+    const int rc = check_cache_batch(h, 0);
     if (rc != CLK_OK) return rc;
     if (check_pool(pool) != CLK_OK || !aligned(d_moved, 4)) return CLK_EINVAL;
-    cudaStream_t cs = (cudaStream_t)s;
-    const bool few = (int64_t)h->dev.max_slots * h->dev.max_pages <= kFewEntries;
-    if ((rc = launch_chained(k_compact_plan, 1, kPlanThreads, cs, h->dev, d_moved, few)) != CLK_OK) return rc;
-    if (!few && (rc = launch_chained(k_compact_table, dim3((unsigned)h->dev.max_slots), kCopyThreads, cs, h->dev)) != CLK_OK) return rc;
-    return with_vector(vector_bytes(*pool, 0), [&](auto v) {
-        using V = decltype(v);
-        return launch_chained(k_compact_copy<V>, dim3((unsigned)(8 * num_sms())), kCopyThreads, cs, h->dev, vec_pool<V>(*pool));
-    });
+    return compact_pages(h, pool, d_moved, (cudaStream_t)s);
+}
+
+extern "C" int clk_cache_compact_scaled(clk_cache* h, const clk_pool* pool, const clk_scales* scales, int32_t* d_moved,
+                                        clk_stream_t s)
+{
+    int rc = check_cache_batch(h, 0);
+    if (rc != CLK_OK) return rc;
+    if (check_pool8(pool, scales, h->dev.page_tokens()) != CLK_OK || !aligned(d_moved, 4)) return CLK_EINVAL;
+    rc = compact_pages(h, pool, d_moved, (cudaStream_t)s);
+    if (rc != CLK_OK) return rc;
+    return launch_chained(k_compact_scales, dim3((unsigned)(4 * num_sms())), kCopyThreads, (cudaStream_t)s, h->dev,
+                          scale_dev(*scales, *pool, h->dev.page_tokens()));
 }

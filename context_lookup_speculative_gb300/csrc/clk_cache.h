@@ -48,17 +48,37 @@ inline int dtype_bytes(int32_t dtype)
     return dtype == CLK_DTYPE_F32 ? 4 : dtype == CLK_DTYPE_BF16 || dtype == CLK_DTYPE_F16 ? 2 : 0;
 }
 
-// CLK_OK for a pool whose fields are usable.
-inline int check_pool(const clk_pool* p)
+// Bytes of an element of rows outside a pool, and of a pool's, 8 bits among them; 0 for another type.
+inline int row_bytes(int32_t dtype) { return dtype_bytes(dtype); }
+inline int pool_bytes(int32_t dtype) { return dtype == CLK_DTYPE_E4M3 ? 1 : dtype_bytes(dtype); }
+
+// CLK_OK for a pool whose fields are usable, its type aside.
+inline int check_pool_shape(const clk_pool* p)
 {
-    if (p == nullptr || p->d_base == nullptr) return CLK_EINVAL;
-    const int es = dtype_bytes(p->dtype);
-    if (es == 0 || !aligned(p->d_base, (size_t)es)) return CLK_EINVAL;
     if (p->planes < 2 || p->planes % 2 != 0 || p->planes > 65534 || p->heads < 1 || p->heads > 65535 || p->dim < 1 ||
         p->dim > 256)
         return CLK_EINVAL;
     if (p->plane_stride < 0 || p->page_stride < 0 || p->head_stride < 0 || p->tok_stride < 0) return CLK_EINVAL;
     return CLK_OK;
+}
+
+// CLK_OK for a pool (without scales) whose fields are usable.
+inline int check_pool(const clk_pool* p)
+{
+    if (p == nullptr || p->d_base == nullptr) return CLK_EINVAL;
+    const int es = dtype_bytes(p->dtype);
+    if (es == 0 || !aligned(p->d_base, (size_t)es)) return CLK_EINVAL;
+    return check_pool_shape(p);
+}
+
+// CLK_OK for a pool of 8 bits and scales that go with it.
+inline int check_pool8(const clk_pool* p, const clk_scales* x, int32_t page_tokens)
+{
+    if (p == nullptr || p->d_base == nullptr || p->dtype != CLK_DTYPE_E4M3) return CLK_EINVAL;
+    if (x == nullptr || x->d_base == nullptr || !aligned(x->d_base, 4)) return CLK_EINVAL;
+    if (x->tokens < 16 || x->tokens > page_tokens || (x->tokens & (x->tokens - 1)) != 0) return CLK_EINVAL;
+    if (x->plane_stride < 0 || x->page_stride < 0 || x->head_stride < 0 || x->block_stride < 0) return CLK_EINVAL;
+    return check_pool_shape(p);
 }
 
 }  // namespace clk

@@ -1,0 +1,40 @@
+// 8-bit values (e4m3) of a cache with scales: conversions, which round to
+// the nearest (ties to even) and take what is beyond the range to the largest.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace clk {
+
+// Two values as codes, `a` in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3(float a, float b)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Two codes (the low 16 bits) as float16, which holds them exactly.
+__device__ __forceinline__ uint32_t half_of_e4m3(uint32_t codes)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+    return r;
+}
+
+__device__ __forceinline__ float2 halves(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+__device__ __forceinline__ float from_e4m3(uint8_t code) { return halves(half_of_e4m3(code)).x; }
+
+__device__ __forceinline__ void from_e4m3x4(uint32_t codes, float* f)
+{
+    const float2 a = halves(half_of_e4m3(codes)), b = halves(half_of_e4m3(codes >> 16));
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
+}
+
+}  // namespace clk

@@ -74,7 +74,12 @@ enum {
     CLK_ESTATE = -5     /* call out of order (e.g. handle not set up) */
 };
 
-enum { CLK_DTYPE_BF16 = 0, CLK_DTYPE_F32 = 1, CLK_DTYPE_F16 = 2 /* pools and attention only */ };
+enum {
+    CLK_DTYPE_BF16 = 0,
+    CLK_DTYPE_F32 = 1,
+    CLK_DTYPE_F16 = 2, /* pools and attention only */
+    CLK_DTYPE_E4M3 = 3 /* pools with scales only: 8 bits, 4 of exponent and 3 of fraction, no infinities, at most 448 */
+};
 
 #define CLK_SENT (-1)
 #define CLK_BLOCK 16        /* slots in a verify block and in a lookup draft */
@@ -598,6 +603,104 @@ CLK_API int clk_cache_free(clk_cache* h, const int32_t* d_slots, int32_t B, clk_
  * number of pages moved. */
 CLK_API int clk_cache_compact(clk_cache* h, const clk_pool* pool, int32_t* d_moved, clk_stream_t s);
 
+/* A cache in 8 bits.  Its pool has dtype CLK_DTYPE_E4M3 and comes with scales,
+ * one float32 for each block of `tokens` rows of a page and head: that of
+ * (plane, page, head, block) lies at d_base + plane*plane_stride +
+ * page*page_stride + head*head_stride + block*block_stride (strides in
+ * floats, >= 0, any order), and token t of a page belongs to block t /
+ * tokens.  An element stands for its value times its block's scale.  Blocks
+ * do not span pages, so a page's scales go wherever the page goes. */
+typedef struct clk_scales {
+    float* d_base;
+    int32_t tokens; /* 16, 32, 64 or 128, at most the cache's page_tokens */
+    int64_t plane_stride, page_stride, head_stride, block_stride;
+} clk_scales;
+
+/* clk_cache_fork and clk_cache_compact of a pool with scales: those of the
+ * copied pages are copied too.  (The calls without scales refuse such a
+ * pool.) */
+CLK_API int clk_cache_fork_scaled(clk_cache* h, const int32_t* d_src, const int32_t* d_dst, int32_t B, const clk_pool* pool,
+                                  const clk_scales* scales, clk_stream_t s);
+CLK_API int clk_cache_compact_scaled(clk_cache* h, const clk_pool* pool, const clk_scales* scales, int32_t* d_moved,
+                                     clk_stream_t s);
+
+/* ---------------------------------------------------------------------- */
+/* Position rotation                                                       */
+/* ---------------------------------------------------------------------- */
+/* Pair i of a row at position p turns by an angle whose cosine and sine are
+ * c = d_table[p][0][i] and s = d_table[p][1][i] (float32 [positions, 2,
+ * pairs]; a factor of the model's own on cosines and sines goes into the
+ * table).  The pair is elements (i, i + pairs), or (2i, 2i + 1) where
+ * neighbours is 1; 2 * pairs is at most the rows' dim, and the elements past
+ * 2 * pairs stay as they are.  (x, y) becomes (x c - y s, y c + x s) in
+ * float32, every product and sum rounded, and is rounded once to where it
+ * goes: the results are a fixed function of the inputs. */
+typedef struct clk_rotary {
+    const float* d_table;
+    int64_t positions;
+    int32_t pairs;
+    int32_t neighbours;
+} clk_rotary;
+
+/* Queries and keys that a rotation reads and writes beside the pages.  Row r
+ * of request b: q head h at d_q + b*q_req + r*q_row + h*q_head, its result at
+ * d_q_out + b*qo_req + r*qo_row + h*qo_head, and k alike (element strides >=
+ * 0, rows of `dim` elements of type dtype: CLK_DTYPE_BF16, CLK_DTYPE_F16 or
+ * CLK_DTYPE_F32).  A result may lie in its source's place (same pointer and
+ * strides); else results overlap no input. */
+typedef struct clk_turn {
+    int32_t dtype, q_heads, kv_heads, dim; /* dim 1 .. 256 */
+    const void *d_q, *d_k;
+    void *d_q_out, *d_k_out;
+    int64_t q_req, q_row, q_head, k_req, k_row, k_head;
+    int64_t qo_req, qo_row, qo_head, ko_req, ko_row, ko_head;
+} clk_turn;
+
+/* Rotates the queries and keys of a step's trees: node n of request b stands
+ * at position ctx + (bits of d_mask[b*N + n] below d_nodes[b]) - 1 (its depth
+ * behind the cached rows; at least ctx), with ctx = d_ctx[b], or the slot's
+ * length where d_ctx is NULL, as in clk_tree_attend.  Rows n >= d_nodes[b]
+ * are not written.  A bad slot, ctx or node count latches CLK_EINVAL, and the
+ * request's rows are not written; nor is a row whose position is not below
+ * `positions` (CLK_EINVAL).  B <= CLK_MAX_BATCH. */
+CLK_API int clk_tree_rotate(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_turn* t, int32_t N,
+                            const int32_t* d_nodes, const int64_t* d_mask, const int32_t* d_ctx, const clk_rotary* rotary,
+                            clk_stream_t s);
+
+/* clk_cache_append with the keys rotated on the way, into a pool of the rows'
+ * type or of 8 bits.  Everything that it says of rows, counts, offsets and
+ * paths holds here.  B <= CLK_MAX_BATCH.
+ *
+ * rotary (nullable: no rotation): K's row for the slot's position p is turned
+ * by position p, which has to be below `positions`, or the request is left
+ * out (CLK_EINVAL).  V's rows are not turned.
+ *
+ * scales: NULL for a pool of type `dtype` (the rows'); else the pool is
+ * CLK_DTYPE_E4M3, rows of any of the three types.  A row's values (keys after
+ * their rotation, in float32) are divided by their block's scale and rounded
+ * once to 8 bits; values beyond the range become the largest, a NaN stays
+ * one.  The scale of a block (per layer, K or V, and head) that the call
+ * writes to is 2^e with the least e >= -120 for which the largest finite
+ * magnitude among the call's rows in it is at most 448 * 2^e; where the block
+ * holds rows before the call's first one, it is the larger of that and the
+ * scale that it had (one that is not finite or not positive counts as none),
+ * and if it grows, those rows become value * old / new, rounded.  So a
+ * repeated call changes nothing, and rows are rounded again only when larger
+ * ones join their block.
+ *
+ * turn (nullable): where d_q is not NULL, the same rows of q are turned too
+ * (by the same positions, into d_q_out), and where d_k_out is not NULL, the
+ * turned keys are also written there, rounded to `dtype`: what the attention
+ * of the same tokens reads.  Its d_k and its *_req and k strides are not
+ * used: source row x of the call is row x of q and of the results.  layers
+ * must be 1 and d_path NULL for it, and rotary given; rows that are not
+ * appended are not written. */
+CLK_API int clk_cache_append_rotary(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool,
+                                    const clk_scales* scales, int32_t layer0, int32_t layers, int32_t dtype, const void* d_k,
+                                    const void* d_v, int64_t layer_stride, int64_t row_stride, int64_t head_stride, int64_t N,
+                                    const int64_t* d_off, const int32_t* d_path, const int32_t* d_count,
+                                    const clk_rotary* rotary, const clk_turn* turn, clk_stream_t s);
+
 /* As clk_status and clk_status_clear, for the cache's status word. */
 CLK_API int clk_cache_status(clk_cache* h, int32_t* dev_status, int32_t* detail, clk_stream_t s);
 CLK_API int clk_cache_status_clear(clk_cache* h, clk_stream_t s);
@@ -707,6 +810,19 @@ CLK_API int clk_tree_attend(clk_cache* h, const int32_t* d_slots, int32_t B, con
 CLK_API int clk_prompt_attend(const clk_attn* a, const int64_t* d_off, int32_t B, int64_t T, clk_cache* h,
                               const int32_t* d_slots, const clk_pool* pool, int32_t layer, const int32_t* d_ctx,
                               void* d_scratch, size_t scratch_bytes, clk_stream_t s);
+
+/* The two attentions over a pool of 8 bits: a->dtype is q's, the new tokens' and
+ * out's type, the pool is CLK_DTYPE_E4M3, and each cached element is its
+ * value times its block's scale, rounded to a->dtype (which is exact where
+ * scales are powers of two in the type's range, as clk_cache_append_rotary
+ * makes them).  Everything else is as without scales. */
+CLK_API int clk_tree_attend_scaled(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool,
+                                   const clk_scales* scales, int32_t layer, const clk_attn* a, int32_t N,
+                                   const int32_t* d_nodes, const int64_t* d_mask, const int32_t* d_ctx, void* d_scratch,
+                                   size_t scratch_bytes, clk_stream_t s);
+CLK_API int clk_prompt_attend_scaled(const clk_attn* a, const int64_t* d_off, int32_t B, int64_t T, clk_cache* h,
+                                     const int32_t* d_slots, const clk_pool* pool, const clk_scales* scales, int32_t layer,
+                                     const int32_t* d_ctx, void* d_scratch, size_t scratch_bytes, clk_stream_t s);
 
 /* ---------------------------------------------------------------------- */
 /* Status, counters, inspection (these synchronise the stream)             */
