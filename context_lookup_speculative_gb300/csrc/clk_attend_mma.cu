@@ -62,6 +62,7 @@
 #include "clk.h"
 #include "clk_attend.h"
 #include "clk_cache.h"
+#include "clk_eight.cuh"
 #include "clk_host.h"
 #include "clk_mma.cuh"
 
@@ -69,9 +70,12 @@ namespace clk {
 namespace {
 
 constexpr int kTile = 128;     // keys of a tile, rows of a row tile
-constexpr int kWarps = 12;     // 8 softmax, 2 copies, 1 products, 1 V tiles
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kValueWarp = 11;
+// 8 softmax, 2 copies, 1 products, 1 V tiles; with a cache in 8 bits 4 that convert its tiles
+template <bool E8>
+constexpr int kWarps = E8 ? 16 : 12;
+template <bool E8>
+constexpr int kThreads = 32 * kWarps<E8>;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kValueWarp = 11, kConvertWarp = 12;
 constexpr int kNear = 4;            // requests whose data a CTA keeps
 
 struct Maps {
@@ -82,7 +86,7 @@ struct Maps {
 struct Shape {
     int32_t tok;    // tokens of a row tile: 128 / group
     int32_t block;  // tokens of an item: tok, or 2 tok for prompts
-    int32_t qbox, kbox;  // tokens of a box of q, rows of a box of new keys
+    int32_t qbox, kbox, vbox;  // tokens of a box of q, rows of a box of new keys, of new values
     int32_t ctas;
     float log2_scale;  // scale * log2(e)
     bool wide_out;     // rows of out are whole 32-byte sectors
@@ -338,7 +342,7 @@ struct Walk {
     }
 };
 
-template <int DP, bool PROMPT>
+template <int DP, bool PROMPT, bool E8>
 struct Lay {
     static constexpr int kHalves = DP / 64;
     static constexpr int kHalf = kTile * 128;  // bytes of 64 columns of a tile
@@ -348,19 +352,28 @@ struct Lay {
     // the weights lie over the scores.
     static constexpr bool kApart = DP == 64;
     static constexpr int kQ = PROMPT ? 2 : 1;                      // row tiles of an item
-    static constexpr int kQB = DP == 128 && PROMPT ? 1 : 2;        // items whose Q is held
-    static constexpr int kK = DP == 128 ? (PROMPT ? 3 : 2) : (PROMPT ? 5 : 4);  // K tiles in the ring
-    static constexpr int kV = DP == 128 ? 2 : (PROMPT ? 5 : 4);
-    static constexpr int kTiles = kQ * kQB + kK + kV;
+    static constexpr int kQB = DP == 128 && (PROMPT || E8) ? 1 : 2;  // items whose Q is held
+    // K tiles in the ring
+    static constexpr int kK = E8 ? (DP == 128 ? 2 : 3) : DP == 128 ? (PROMPT ? 3 : 2) : (PROMPT ? 5 : 4);
+    // V tiles in the ring; with a cache in 8 bits halves of 64 keys
+    static constexpr int kV = E8 ? (DP == 128 ? 3 : 6) : DP == 128 ? 2 : (PROMPT ? 5 : 4);
+    static constexpr int kVBytes = E8 ? kBytes / 2 : kBytes;
+    // tiles as the cache holds them, 8 bits
+    static constexpr int kG = E8 ? (DP == 128 ? (PROMPT ? 3 : 4) : (PROMPT ? 6 : 8)) : 0;
+    static constexpr int kGs = kG > 0 ? kG : 1;
+    static constexpr int kGBytes = kTile * DP;
+    static constexpr int oK = kQ * kQB * kBytes, oV = oK + kK * kBytes, oG = oV + kV * kVBytes;
     // after the tiles
-    static constexpr int oKFull = kTiles * kBytes, oKEmpty = oKFull + 8 * kK;
+    static constexpr int oKFull = oG + kG * kGBytes, oKEmpty = oKFull + 8 * kK;
     static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
-    static constexpr int oQFull = oVEmpty + 8 * kV, oQEmpty = oQFull + 8 * kQB;
+    static constexpr int oGFull = oVEmpty + 8 * kV, oGEmpty = oGFull + 8 * kG;
+    static constexpr int oQFull = oGEmpty + 8 * kG, oQEmpty = oQFull + 8 * kQB;
     static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
     static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
     static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
-    static constexpr int oNear = oBad + 16 * kV;                      // Reach[kNear]
+    static constexpr int oScale = oBad + 16 * kV;                     // float[kG][8]: of blocks of 16 keys
+    static constexpr int oNear = oScale + 32 * kG;                    // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
     static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: of items that end here, that begin here
     static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[8]
@@ -377,17 +390,44 @@ __device__ __forceinline__ void gave_up(const Attend& A, const Scratch& W)
     if (A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
 }
 
+// 16 codes as elements of the products' type, times their scale: rounded once (exact for scales that are powers of
+// two in the type's range).
+template <bool BF16>
+__device__ __forceinline__ void widen(uint4 codes, float scale, uint4& lo, uint4& hi)
+{
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t y[8];
+    const __half s = __float2half_rn(scale);
+    if (!BF16 && __half2float(s) == scale) {
+        const __half2 s2 = __half2half2(s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t h = half_of_e4m3(w[i / 2] >> 16 * (i & 1));
+            const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h), s2);
+            y[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = halves(half_of_e4m3(w[i / 2] >> 16 * (i & 1)));
+            y[i] = pack2<BF16>(f.x * scale, f.y * scale);
+        }
+    }
+    lo = make_uint4(y[0], y[1], y[2], y[3]);
+    hi = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
 template <int N>
 struct Count {
     static constexpr int value = N;
 };
 
 // This CTA's share of an item whose tiles lie in several CTAs' shares.
-template <int DP, bool BF16, bool PROMPT>
+template <int DP, bool BF16, bool PROMPT, bool E8>
 __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const Scratch& W, const Plan& plan, const Cuts& cuts,
                                           const Cut& cut, volatile int* stop)
 {
-    constexpr int rows = PROMPT ? 2 * kTile : kTile;
+    constexpr int rows = PROMPT ? 2 * kTile : kTile, kThreads = clk::kThreads<E8>;
     const int tid = threadIdx.x;
     const long long tile0 = cut.begin + kExtra<PROMPT>;
     const int c0 = cuts.holder(tile0), c1 = cuts.holder(tile0 + cut.total - 1), parts = c1 - c0 + 1;
@@ -492,11 +532,12 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
         rows_of(Count<8>{}, Count<1>{});
 }
 
-template <int DP, bool BF16, bool PROMPT>
-__global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ Maps M, const __grid_constant__ Attend A,
-                                                        const __grid_constant__ Shape S, void* scratch)
+template <int DP, bool BF16, bool PROMPT, bool E8>
+__global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constant__ Maps M, const __grid_constant__ Attend A,
+                                                            const __grid_constant__ Shape S, void* scratch)
 {
-    using L = Lay<DP, PROMPT>;
+    using L = Lay<DP, PROMPT, E8>;
+    constexpr int kThreads = clk::kThreads<E8>, kWarps = clk::kWarps<E8>;
     extern __shared__ __align__(1024) char sm[];
     // the shuffle tells the compiler that a warp has one role
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -519,13 +560,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char*>(&M) + lane * sizeof(CUtensorMap)) : "memory");
     } else if (tid == 32 * kValueWarp) {
         for (int i = 0; i < L::kK; ++i) {
-            bar_init(base + L::oKFull + 8 * i, 1);
+            bar_init(base + L::oKFull + 8 * i, E8 ? 4 : 1);
             bar_init(base + L::oKEmpty + 8 * i, 1);
         }
         for (int i = 0; i < L::kV; ++i) {
             bar_init(base + L::oVFull + 8 * i, 1);
-            bar_init(base + L::oVReady + 8 * i, 1);
+            bar_init(base + L::oVReady + 8 * i, E8 ? 4 : 1);
             bar_init(base + L::oVEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < L::kG; ++i) {
+            bar_init(base + L::oGFull + 8 * i, 1 + 32);  // the copies of a tile, and of its scales by a warp's lanes
+            bar_init(base + L::oGEmpty + 8 * i, 4);
         }
         for (int i = 0; i < L::kQB; ++i) {
             bar_init(base + L::oQFull + 8 * i, 1);
@@ -645,11 +690,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     __syncthreads();
     tmem_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::oTmem);
-    const uint32_t qs = base, ks = base + L::kQ * L::kQB * L::kBytes, vs = ks + L::kK * L::kBytes;
+    const uint32_t qs = base, ks = base + L::oK, vs = base + L::oV;
 
-    // Registers: 384 threads x 168 at launch; 256 x 208 + 128 x 80 after the split.
+    // Registers: 384 threads x 168 at launch; 256 x 208 + 128 x 80 after the split.  512 x 128; 256 x 192 + 256 x 64.
     if (warp < kCopyWarp) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (E8)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- Softmax: a thread per row. ----
         const int s = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
@@ -805,9 +853,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 sum += both.x + both.y;
                 if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
                     // Rows of V that were not finite: NaN for those who see them.
-                    const int i = gi + (PROMPT ? j : 2 * j + s), vi = i % L::kV;
-                    if (!warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(i / L::kV & 1), stop)) return false;
-                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], bad[4 * vi + 2], bad[4 * vi + 3]};
+                    const int i = gi + (PROMPT ? j : 2 * j + s), at = E8 ? 2 * i : i, vi = at % L::kV;
+                    if (!warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop)) return false;
+                    const int vj = E8 ? (at + 1) % L::kV : vi;
+                    if (E8 && !warp_wait(base + L::oVReady + 8 * vj, (uint32_t)((at + 1) / L::kV & 1), stop)) return false;
+                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], bad[4 * vj + (E8 ? 0 : 2)], bad[4 * vj + (E8 ? 1 : 3)]};
                     if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
                         bool hit = false;
 #pragma unroll
@@ -971,15 +1021,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     } else {
         Walk<PROMPT> w;
         w.start(A, S, plan, near);
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (E8)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == kCopyWarp || warp == kCopyWarp2) {
             // ---- Copies: two warps (a copy costs its warp about 65 cycles, and pages of 16 rows need 16 a tile). ----
             // With trees one brings K and the other V, so that small pages' copies go side by side (256 short requests,
             // pages of 16: 119 us, by alternate tiles 155); with prompts they take alternate tiles, which keeps K and
             // V in step (a 25,000-token prompt: 3.16 ms, by K and V 3.26).  The first also brings Q.
             const int odd = warp == kCopyWarp ? 0 : 1;
-            const bool brings_k = PROMPT || odd == 0, brings_v = PROMPT || odd == 1;
-            auto my = [&](int tile) { return !PROMPT || (tile & 1) == odd; };
+            // (With a cache in 8 bits they bring K and V apart too.)
+            constexpr bool kApartKV = !PROMPT || E8;
+            const bool brings_k = !kApartKV || odd == 0, brings_v = !kApartKV || odd == 1;
+            auto my = [&](int tile) { return kApartKV || (tile & 1) == odd; };
+            // With a cache in 8 bits: the runs' tiles before this one in the order in which they are converted, and
+            // places in use, with the phase that ends the last copy to each.
+            int g0 = 0;
+            uint32_t g_used = 0, g_phase = 0;
             int i = 0, seg = 0, nk = 0, nv = 0, nq = 0;  // n*: one past the last tile or item asked for
             bool ok = (base & 1023) == 0;  // the swizzle's period
             if (!ok) *stop = 1;
@@ -1000,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 int at = w.t0 * pages & ~31, now = batch(at), then = batch(at + 32);
                 const int z = PROMPT ? 0 : w.b, row0 = PROMPT ? w.x.base : 0;
                 // the first K goes out before the first V
-                if (!PROMPT && odd == 1 && seg == 0 && !(ok = warp_wait(base + L::oQFull, 0, stop))) break;
+                if (kApartKV && odd == 1 && seg == 0 && !(ok = warp_wait(base + L::oQFull, 0, stop))) break;
                 if (odd == 0) {
                     const int qi = seg % L::kQB;
                     const uint32_t qb = base + L::oQFull + 8 * qi;
@@ -1027,6 +1086,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
                     const uint32_t bytes = (uint32_t)L::kHalves * 128u * (uint32_t)(cached ? boxes << A.C.shift : S.kbox);
                     const int n0 = row0 + (t - w.x.ctx_tiles) * kTile;
+                    if (E8 && cached) {
+                        const int run = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0, r = t - w.t0;
+                        const int at8 = g0 + (odd == 0 ? (r > 0 ? 2 * r - 1 : 0) : r + 1 < run ? 2 * r + 2 : 2 * run - 1);
+                        const int gi = at8 % L::kGs;
+                        const uint32_t bar = base + L::oGFull + 8 * gi;
+                        if (!(ok = warp_wait(base + L::oGEmpty + 8 * gi, (uint32_t)(at8 / L::kGs & 1) ^ 1, stop))) break;
+                        g_used |= 1u << gi;
+                        g_phase = (g_phase & ~(1u << gi)) | (uint32_t)(at8 / L::kGs & 1) << gi;
+                        if (lane == 0) bar_expect(bar, (uint32_t)(boxes << A.C.shift) * DP);
+                        __syncwarp();
+                        if (page >= 0)
+                            copy_box(base + L::oG + gi * L::kGBytes + (lane << A.C.shift) * DP, odd == 0 ? &M.kc : &M.vc, 0, 0, w.h, page, bar);
+                        // the scales of 16 keys each; none for keys without a page (their rows become 0)
+                        const int from = __shfl_sync(0xffffffffu, page, 16 * lane >> A.C.shift & 31);
+                        if (lane < 8) {
+                            const bool there = from >= 0 && from < A.C.num_pages;
+                            const float* const src = (odd == 0 ? A.ks : A.vs) +
+                                                     (there ? from * A.scale_page + w.h * A.scale_head +
+                                                                  ((16 * lane & (A.C.page_tokens() - 1)) >> A.scale_shift) * A.scale_block
+                                                            : 0);
+                            copy_word(base + L::oScale + 32 * gi + 4 * lane, src, there);
+                        }
+                        copies_arrive(bar);
+                        continue;
+                    }
+                    if (E8) continue;  // new tokens' tiles are brought by those who convert
                     auto bring = [&](uint32_t bar, uint32_t dst, const CUtensorMap* pool, const CUtensorMap* fresh) {
                         if (lane == 0) bar_expect(bar, bytes);
                         __syncwarp();
@@ -1050,6 +1135,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         bring(base + L::oVFull + 8 * vi, vs + vi * L::kBytes, &M.vc, &M.v);
                     }
                 }
+                if (E8) {
+                    const int run = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0;
+                    g0 += run > 0 ? 2 * run : 0;
+                }
             }
             if (!ok) {
                 // Leave no copy in flight.
@@ -1062,6 +1151,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     if (my(j)) drain(base + L::oKFull + 8 * (j % L::kK), (uint32_t)(j / L::kK & 1));
                 for (int j = nv > L::kV ? nv - L::kV : 0; j < nv; ++j)
                     if (my(j)) drain(base + L::oVFull + 8 * (j % L::kV), (uint32_t)(j / L::kV & 1));
+                for (int j = 0; j < L::kG; ++j)
+                    if (g_used >> j & 1) drain(base + L::oGFull + 8 * j, g_phase >> j & 1);
+                if (E8) asm volatile("cp.async.wait_all;" ::: "memory");
             }
         } else if (warp == kMmaWarp) {
             // ---- Products: one lane issues them, the warp goes along. ----
@@ -1091,9 +1183,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                     __syncwarp();
                 };
                 // descriptors count in 16 bytes
-                const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, L::kHalf);
+                const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, E8 ? L::kHalf / 2 : L::kHalf);
                 auto wait_k = [&] { return warp_wait(base + L::oKFull + 8 * ki, kp, stop); };
-                auto wait_v = [&] { return warp_wait(base + L::oVReady + 8 * vi, vp, stop); };
+                // (with a cache in 8 bits halves of V are waited for as they are used)
+                auto wait_v = [&]() -> bool { return E8 || warp_wait(base + L::oVReady + 8 * vi, vp, stop); };
+                auto done_v = [&] {
+#pragma unroll
+                    for (int hf = 0; hf < (E8 ? 2 : 1); ++hf) {
+                        done(base + L::oVEmpty + 8 * vi);
+                        step(vi, vp, L::kV);
+                    }
+                };
                 // Stream s's scores with K tile ki.
                 auto scores = [&](int s) {
                     if (L::kApart) {
@@ -1117,19 +1217,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 // Stream s's weights with V tile vi.  Where the weights lie over the scores, the chain of one stream
                 // is what counts, and their first half's product does not wait for the second.
                 auto values = [&](int s, bool add) {
-                    const uint64_t v = v0 + vi * (L::kBytes / 16);
-                    constexpr int steps = L::kApart ? 8 : 4;  // 16 keys each
+                    constexpr int steps = E8 || !L::kApart ? 4 : 8;  // 16 keys each
+                    int vj = vi;
+                    uint32_t vq = vp;
 #pragma unroll
                     for (int part = 0; part < 8; part += steps) {
-                        if (!warp_wait(base + (part + steps < 8 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
+                        if (!L::kApart || part == 0)
+                            if (!warp_wait(base + (!L::kApart && part == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
+                        if (E8 && !warp_wait(base + L::oVReady + 8 * vj, vq, stop)) return false;
                         tmem_after();
+                        const uint64_t v = v0 + vj * (L::kVBytes / 16);
                         if (elect()) {
 #pragma unroll
                             for (int e = part; e < part + steps; ++e)
-                                mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * e, v + 128 * e, kind_o,
-                                       add || e > 0);
+                                mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * e, v + 128 * (E8 ? e - part : e),
+                                       kind_o, add || e > 0);
                         }
                         __syncwarp();
+                        if (E8) step(vj, vq, L::kV);
                     }
                     ps[s] ^= 1;
                     return true;
@@ -1151,7 +1256,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                         for (int j = 0; j < len; ++j) {
                             const bool more = j + 1 < len;
                             if (L::kApart && more && !(ok = wait_k())) break;
-                            if (!(ok = wait_v())) break;
+                            ok = wait_v();
+                            if (!ok) break;
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
                                 if (!ok) continue;
@@ -1166,8 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                                 }
                             }
                             if (!ok) break;
-                            done(base + L::oVEmpty + 8 * vi);
-                            step(vi, vp, L::kV);
+                            done_v();
                             if (more) {
                                 done(base + L::oKEmpty + 8 * ki);
                                 step(ki, kp, L::kK);
@@ -1189,8 +1294,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                             if (L::kApart && !(ok = ahead(j + 2))) break;
                             if (!(ok = wait_v() && values(s, j >= 2))) break;
                             if (L::kApart || j + 2 >= len) done(base + L::oODone + 8 * s);
-                            done(base + L::oVEmpty + 8 * vi);
-                            step(vi, vp, L::kV);
+                            done_v();
                             if (!L::kApart) ok = ahead(j + 2);
                         }
                     }
@@ -1204,6 +1308,133 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
                 }
             }
             __syncwarp();
+        } else if (E8 && warp >= kConvertWarp) {
+            // ---- Tiles of the cache: to 16 bits, times their scales. ----
+            const int me = tid - 32 * kConvertWarp;  // 0 .. 127
+            int i = 0, g = 0;
+            bool ok = true;
+            // `rows` rows from row `first` of the tile in place gi to a tile at dst; rows from `have` on become 0.
+            auto convert = [&](int gi, int first, auto rows_c, char* dst, int have) {
+                // 16 elements a turn, U turns in flight
+                constexpr int rows = decltype(rows_c)::value, chunks = DP / 16, turns = rows * chunks / 128, U = turns < 4 ? turns : 4;
+                static_assert(turns % U == 0, "whole groups of turns");
+                const char* const src = sm + L::oG + gi * L::kGBytes + first * DP;
+                const float* const scales = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
+#pragma unroll 1
+                for (int i0 = me; i0 < rows * chunks; i0 += U * 128) {
+                    uint4 x[U];
+                    float f[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        x[u] = *reinterpret_cast<const uint4*>(src + (i0 + u * 128) * 16);
+                        f[u] = scales[first + (i0 + u * 128) / chunks >> 4];
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int at = i0 + u * 128, r = at / chunks, c = at % chunks, c2 = 2 * c & 7;
+                        uint4 y0, y1;
+                        widen<BF16>(x[u], f[u], y0, y1);
+                        if (first + r >= have) y0 = y1 = make_uint4(0, 0, 0, 0);
+                        char* const row = dst + (c >> 2) * (rows * 128) + r * 128;
+                        char *const p0 = row + (c2 ^ (r & 7)) * 16, *const p1 = row + ((c2 + 1) ^ (r & 7)) * 16;
+                        // the two halves of a row lie in the same banks: their lanes store at different chunks
+                        const bool swap = c >= 4;
+                        *reinterpret_cast<uint4*>(swap ? p1 : p0) = swap ? y1 : y0;
+                        *reinterpret_cast<uint4*>(swap ? p0 : p1) = swap ? y0 : y1;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            };
+            // These warps write to both rings, or have it written, in the order of the tiles: they alone wait for every
+            // phase of their places.  (A wait tells a phase from the one before it, not from the one before that.)
+            const bool brings = warp == kConvertWarp;  // the tiles of new tokens
+            uint32_t k_used = 0, k_phase = 0, v_used = 0, v_phase = 0;  // places with copies, the phase that ends the last
+            auto keys = [&](int tile, int t) {
+                const int ki = tile % L::kK;
+                const uint32_t full = base + L::oKFull + 8 * ki;
+                const bool cached = t < w.x.ctx_tiles;
+                const int gi = g % L::kGs;
+                if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
+                if (!warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(tile / L::kK & 1) ^ 1, stop)) return false;
+                if (cached) {
+                    convert(gi, 0, Count<kTile>{}, sm + L::oK + ki * L::kBytes, kTile);
+                    if (lane == 0) {
+                        bar_arrive(full);
+                        bar_arrive(base + L::oGEmpty + 8 * gi);
+                    }
+                    ++g;
+                } else if (!brings) {
+                    if (lane == 0) bar_arrive(full);
+                } else {
+                    k_used |= 1u << ki;
+                    k_phase = (k_phase & ~(1u << ki)) | (uint32_t)(tile / L::kK & 1) << ki;
+                    if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.kbox) * 128u);
+                    __syncwarp();
+                    if (lane < L::kHalves)
+                        copy_box(ks + ki * L::kBytes + lane * L::kHalf, &M.k, 64 * lane, w.h,
+                                 (PROMPT ? w.x.base : 0) + (t - w.x.ctx_tiles) * kTile, PROMPT ? 0 : w.b, full);
+                }
+                return true;
+            };
+            auto values = [&](int tile, int t) {
+                const bool cached = t < w.x.ctx_tiles;
+                const int gi = g % L::kGs, n0 = (t - w.x.ctx_tiles) * kTile;
+                const int have = cached ? w.x.ctx - t * kTile : w.x.rows - n0;
+                if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int at = 2 * tile + hf, vi = at % L::kV;
+                    const uint32_t full = base + L::oVFull + 8 * vi;
+                    if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(at / L::kV & 1) ^ 1, stop)) return false;
+                    if (cached) {
+                        convert(gi, 64 * hf, Count<kTile / 2>{}, sm + L::oV + vi * L::kVBytes, have);
+                    } else if (have > 64 * hf) {
+                        if (brings) {
+                            v_phase = v_used >> vi & 1 ? v_phase ^ 1u << vi : v_phase;
+                            v_used |= 1u << vi;
+                            if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
+                            __syncwarp();
+                            if (lane < L::kHalves)
+                                copy_box(vs + vi * L::kVBytes + lane * (L::kHalf / 2), &M.v, 64 * lane, w.h,
+                                         (PROMPT ? w.x.base : 0) + n0 + 64 * hf, PROMPT ? 0 : w.b, full);
+                        }
+                        continue;  // the V warp hands it on
+                    } else {
+                        // a half without tokens
+                        for (int e = me; e < L::kVBytes / 16; e += 128)
+                            *reinterpret_cast<uint4*>(sm + L::oV + vi * L::kVBytes + 16 * e) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (me < 4) bad[4 * vi + me] = 0;
+                        __syncwarp();
+                    }
+                    if (lane == 0) bar_arrive(base + L::oVReady + 8 * vi);
+                }
+                if (cached) {
+                    if (lane == 0) bar_arrive(base + L::oGEmpty + 8 * gi);
+                    ++g;
+                }
+                return true;
+            };
+            for (; ok && w.left > 0; w.next(A, S, plan, near)) {
+                // K runs a tile ahead of V: the next scores wait for it
+                for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
+                    if (t == w.t0) ok = keys(i, t);
+                    if (ok && t + 1 < w.t1) ok = keys(i + 1, t + 1);
+                    if (ok) ok = values(i, t);
+                }
+            }
+            if (!ok && brings) {
+                // Leave no copy in flight.
+                const long long t0 = clock64();
+                auto drain = [&](uint32_t bar, uint32_t parity) {
+                    while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {}
+                };
+                for (int j = 0; j < L::kK; ++j)
+                    if (k_used >> j & 1) drain(base + L::oKFull + 8 * j, k_phase >> j & 1);
+                for (int j = 0; j < L::kV; ++j)
+                    if (v_used >> j & 1) drain(base + L::oVFull + 8 * j, v_phase >> j & 1);
+            }
         } else {
             // ---- V tiles: rows past the end, and rows that are not finite. ----
             // a value is not finite where its exponent is all ones: one more there carries into the sign
@@ -1219,7 +1450,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
             }
             int i = 0;
             bool ok = true;
-            for (; ok && w.left > 0; w.next(A, S, plan, near)) {
+            if (E8) {
+                // new tokens, by halves of 64 keys; the cache's rows are converted by other warps
+                uint32_t phase = 0;  // of each place's copies
+                for (; ok && w.left > 0; w.next(A, S, plan, near)) {
+                    i += w.t1 - w.t0;
+                    for (int t = w.t0 > w.x.ctx_tiles ? w.t0 : w.x.ctx_tiles; ok && t < w.t1; ++t) {
+                        const int n0 = (t - w.x.ctx_tiles) * kTile, have = w.x.rows - n0;
+                        const bool look = !PROMPT || n0 + kTile - 1 > w.item * S.block;
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int at = 2 * (i - (w.t1 - t)) + hf, vi = at % L::kV, left = have - 64 * hf;
+                            if (left <= 0) break;
+                            if (!(ok = warp_wait(base + L::oVFull + 8 * vi, phase >> vi & 1, stop))) break;
+                            phase ^= 1u << vi;
+                            if (left < 64 || look) {
+                                char* const tile = sm + L::oV + vi * L::kVBytes;
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const int r = 32 * u + lane;
+                                    const bool clear = r >= left;
+                                    bool odd = false;
+                                    if (look && 32 * u < left) {
+                                        uint32_t hit = 0;
+#pragma unroll
+                                        for (int c = 0; c < 8 * L::kHalves; ++c) {
+                                            const int p = (c & 8) * (L::kHalf / 16) + r * 128 + (((c & 7) + lane) & 7) * 16;
+                                            const uint4 x = *reinterpret_cast<const uint4*>(tile + p);
+                                            hit |= ((x.x & expo) + one) | ((x.y & expo) + one) | ((x.z & expo) + one) | ((x.w & expo) + one);
+                                        }
+                                        odd = !clear && (hit & 0x80008000u) != 0;
+                                    }
+                                    if (clear || odd)
+#pragma unroll
+                                        for (int c = 0; c < 8 * L::kHalves; ++c) {
+                                            const int p = (c & 8) * (L::kHalf / 16) + r * 128 + (((c & 7) + lane) & 7) * 16;
+                                            *reinterpret_cast<uint4*>(tile + p) = make_uint4(0, 0, 0, 0);
+                                        }
+                                    const uint32_t word = __ballot_sync(0xffffffffu, odd);
+                                    if (lane == 0) bad[4 * vi + u] = word;
+                                }
+                                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            }
+                            __syncwarp();
+                            if (lane < 4) bar_arrive(base + L::oVReady + 8 * vi);
+                        }
+                    }
+                }
+            }
+            for (; !E8 && ok && w.left > 0; w.next(A, S, plan, near)) {
                 for (int t = w.t0; t < w.t1; ++t, ++i) {
                     const int vi = i % L::kV;
                     if (!(ok = warp_wait(base + L::oVFull + 8 * vi, (uint32_t)(i / L::kV & 1), stop))) break;
@@ -1262,6 +1540,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         }
     }
 
+    // The joins run with equal shares of the registers again.
+    if (E8) {
+        if (warp < kCopyWarp)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    }
     // ---- Parts are written: raise the flag, join what was cut. ----
     tmem_before();
     __syncthreads();
@@ -1278,7 +1563,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     const Cuts cuts(plan.all, plan.ctas);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i)
-        if (cut[i].total > 0) join_item<DP, BF16, PROMPT>(A, S, W, plan, cuts, cut[i], stop);
+        if (cut[i].total > 0) join_item<DP, BF16, PROMPT, E8>(A, S, W, plan, cuts, cut[i], stop);
 }
 
 // ---------------------------------------------------------------------------
@@ -1303,39 +1588,44 @@ EncodeFn encoder()
 }
 
 // A map over [n3][n2][n1][dim] elements with the given strides (in
-// elements), copied in boxes of 64 x b1 x b2 (x 1).
+// elements), copied in boxes of b0 x b1 x b2 (x 1): 64 elements of 16 bits in
+// the swizzle, or rows of 8 bits as they are.
 bool encode(EncodeFn f, CUtensorMap* m, int32_t dtype, const void* base, int64_t dim, const int64_t n[3], const int64_t st[3],
-            int b1, int b2)
+            int b0, int b1, int b2)
 {
+    const cuuint64_t es = dtype == CLK_DTYPE_E4M3 ? 1 : 2;
     const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)n[0], (cuuint64_t)n[1], (cuuint64_t)n[2]};
     cuuint64_t strides[3];
     // the stride of an axis of one is not used; it still has to be a valid one
-    for (int i = 0; i < 3; ++i) strides[i] = n[i] > 1 ? (cuuint64_t)st[i] * 2 : 256;
-    const cuuint32_t box[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1}, one[4] = {1, 1, 1, 1};
-    return f(m, dtype == CLK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    for (int i = 0; i < 3; ++i) strides[i] = n[i] > 1 ? (cuuint64_t)st[i] * es : 256;
+    const cuuint32_t box[4] = {(cuuint32_t)b0, (cuuint32_t)b1, (cuuint32_t)b2, 1}, one[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = es == 1                    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : dtype == CLK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return f(m, type, 4, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             es == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A stride (in elements of 2 bytes) that a tensor map can take, for an axis of n.
-bool map_stride(int64_t st, int64_t n) { return n <= 1 || (st > 0 && st % 8 == 0 && st < ((int64_t)1 << 38)); }
+// A stride (in elements, so many to 16 bytes) that a tensor map can take, for an axis of n.
+bool map_stride(int64_t st, int64_t n, int per = 8) { return n <= 1 || (st > 0 && st % per == 0 && st < ((int64_t)1 << 38)); }
 
-template <int DP, bool BF16, bool PROMPT>
+template <int DP, bool BF16, bool PROMPT, bool E8>
 int launch_mma(const Attend& A, const Shape& S, const Maps& M, void* scratch, cudaStream_t s)
 {
-    using L = Lay<DP, PROMPT>;
+    using L = Lay<DP, PROMPT, E8>;
     static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CLK_ECUDA;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit) || dev > 63) {
-        if (cudaFuncSetAttribute(k_attend<DP, BF16, PROMPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) != cudaSuccess)
+        if (cudaFuncSetAttribute(k_attend<DP, BF16, PROMPT, E8>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) != cudaSuccess)
             return CLK_ECUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)S.ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads<E8>);
     cfg.dynamicSmemBytes = L::kTotal;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -1343,7 +1633,7 @@ int launch_mma(const Attend& A, const Shape& S, const Maps& M, void* scratch, cu
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, k_attend<DP, BF16, PROMPT>, M, A, S, scratch));
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_attend<DP, BF16, PROMPT, E8>, M, A, S, scratch));
 }
 
 bool mma_dim(int32_t dim) { return dim >= 8 && dim <= 128 && dim % 8 == 0; }
@@ -1358,7 +1648,6 @@ bool mma_dim(int32_t dim) { return dim >= 8 && dim <= 128 && dim % 8 == 0; }
 // leave it; both are left to the general kernel.
 bool attend_mma_takes(const Attend& A)
 {
-    if (A.ks != nullptr) return false;
     if (A.dtype == CLK_DTYPE_F32 || !mma_dim(A.dim) || A.group > kTile || !(A.scale >= 1e-20f && A.scale <= 1e20f))
         return false;
     for (const void* p : {A.q, A.k, A.v, (const void*)A.out, A.kc, A.vc})
@@ -1367,8 +1656,9 @@ bool attend_mma_takes(const Attend& A)
     if (!map_stride(A.q_req, reqs) || !map_stride(A.q_row, rows) || !map_stride(A.q_head, A.q_heads)) return false;
     if (!map_stride(A.k_req, reqs) || !map_stride(A.k_row, rows) || !map_stride(A.k_head, A.kv_heads)) return false;
     if (!map_stride(A.v_req, reqs) || !map_stride(A.v_row, rows) || !map_stride(A.v_head, A.kv_heads)) return false;
-    if (A.kc != nullptr && (!map_stride(A.page_stride, A.C.num_pages) || !map_stride(A.head_stride, A.kv_heads) ||
-                            !map_stride(A.tok_stride, 2)))
+    const int per = A.ks != nullptr ? 16 : 8;
+    if (A.kc != nullptr && (!map_stride(A.page_stride, A.C.num_pages, per) || !map_stride(A.head_stride, A.kv_heads, per) ||
+                            !map_stride(A.tok_stride, 2, per)))
         return false;
     return true;
 }
@@ -1392,6 +1682,8 @@ int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)
     const int64_t rows = prompt ? A.T : A.N, reqs = prompt ? 1 : A.B;
     S.qbox = (int32_t)(S.tok < rows ? S.tok : rows);
     S.kbox = (int32_t)(kTile < rows ? kTile : rows);
+    const bool eight = A.ks != nullptr;
+    S.vbox = eight && S.kbox > kTile / 2 ? kTile / 2 : S.kbox;
     S.ctas = num_sms();
     S.wide_out = A.dim % 16 == 0 && aligned(A.out, 32);
     S.log2_scale = (float)((double)A.scale * 1.4426950408889634);
@@ -1399,19 +1691,21 @@ int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)
     Maps M;
     const int64_t nq[3] = {A.q_heads, rows, reqs}, nk[3] = {A.kv_heads, rows, reqs};
     const int64_t sq[3] = {A.q_head, A.q_row, A.q_req}, sk[3] = {A.k_head, A.k_row, A.k_req}, sv[3] = {A.v_head, A.v_row, A.v_req};
-    bool ok = encode(f, &M.q, A.dtype, A.q, A.dim, nq, sq, A.group, S.qbox) &&
-              encode(f, &M.k, A.dtype, A.k, A.dim, nk, sk, 1, S.kbox) && encode(f, &M.v, A.dtype, A.v, A.dim, nk, sv, 1, S.kbox);
+    bool ok = encode(f, &M.q, A.dtype, A.q, A.dim, nq, sq, 64, A.group, S.qbox) &&
+              encode(f, &M.k, A.dtype, A.k, A.dim, nk, sk, 64, 1, S.kbox) && encode(f, &M.v, A.dtype, A.v, A.dim, nk, sv, 64, 1, S.vbox);
+    const bool wide = A.dim > 64, bf = A.dtype == CLK_DTYPE_BF16;
     if (A.kc != nullptr) {
         const int64_t np[3] = {A.C.page_tokens(), A.kv_heads, A.C.num_pages};
         const int64_t sp[3] = {A.tok_stride, A.head_stride, A.page_stride};
-        ok = ok && encode(f, &M.kc, A.dtype, A.kc, A.dim, np, sp, A.C.page_tokens(), 1) &&
-             encode(f, &M.vc, A.dtype, A.vc, A.dim, np, sp, A.C.page_tokens(), 1);
+        const int32_t type = eight ? CLK_DTYPE_E4M3 : A.dtype;
+        const int b0 = eight ? pad_dim(A.dim) : 64;
+        ok = ok && encode(f, &M.kc, type, A.kc, A.dim, np, sp, b0, A.C.page_tokens(), 1) &&
+             encode(f, &M.vc, type, A.vc, A.dim, np, sp, b0, A.C.page_tokens(), 1);
     } else {
         M.kc = M.vc = M.k;  // not read: no request has cached rows
     }
     if (!ok) return CLK_EINVAL;
-    const bool wide = A.dim > 64, bf = A.dtype == CLK_DTYPE_BF16;
-#define CLK_GO(D, T, P) return launch_mma<D, T, P>(A, S, M, scratch, s)
+#define CLK_GO(D, T, P) return eight ? launch_mma<D, T, P, true>(A, S, M, scratch, s) : launch_mma<D, T, P, false>(A, S, M, scratch, s)
     if (prompt) {
         if (wide) {
             if (bf) CLK_GO(128, true, true);

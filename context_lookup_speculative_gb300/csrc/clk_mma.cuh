@@ -69,6 +69,18 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const void* map, int x, i
         : "memory");
 }
 
+// Four bytes to shared memory, or zeros where there are none to read.
+__device__ __forceinline__ void copy_word(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+
+// Arrives on bar once the copy_words that this thread issued so far are done.
+__device__ __forceinline__ void copies_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Shared-memory operand descriptors for rows of 128 bytes in the 128-byte
 // swizzle.  by_row: the contraction runs along the 128-byte row (groups of
 // eight rows 1024 bytes apart).  Otherwise the row runs along the other
