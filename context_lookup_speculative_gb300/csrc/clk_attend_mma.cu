@@ -390,31 +390,27 @@ __device__ __forceinline__ void gave_up(const Attend& A, const Scratch& W)
     if (A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
 }
 
-// 16 codes as elements of the products' type, times their scale: rounded once (exact for scales that are powers of
-// two in the type's range).
-template <bool BF16>
-__device__ __forceinline__ void widen(uint4 codes, float scale, uint4& lo, uint4& hi)
+// Eight codes as elements of the products' type, times their scale: rounded once (exact for scales that are powers
+// of two in the type's range).  PLAIN: float16, and a scale that float16 holds.
+__device__ __forceinline__ bool fits_half(float scale) { return __half2float(__float2half_rn(scale)) == scale; }
+
+template <bool BF16, bool PLAIN>
+__device__ __forceinline__ uint4 widen(uint2 codes, float scale)
 {
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t y[8];
-    const __half s = __float2half_rn(scale);
-    if (!BF16 && __half2float(s) == scale) {
-        const __half2 s2 = __half2half2(s);
+    uint32_t y[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t h = half_of_e4m3(w[i / 2] >> 16 * (i & 1));
-            const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h), s2);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t h = half_of_e4m3((i < 2 ? codes.x : codes.y) >> 16 * (i & 1));
+        if (PLAIN) {
+            const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(scale));
             y[i] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = halves(half_of_e4m3(w[i / 2] >> 16 * (i & 1)));
-            y[i] = pack2<BF16>(f.x * scale, f.y * scale);
+        } else {
+            const float2 f = halves(h), p = unpair(mul2(pair(__float_as_uint(f.x), __float_as_uint(f.y)),
+                                                        pair(__float_as_uint(scale), __float_as_uint(scale))));
+            y[i] = pack2<BF16>(p.x, p.y);
         }
     }
-    lo = make_uint4(y[0], y[1], y[2], y[3]);
-    hi = make_uint4(y[4], y[5], y[6], y[7]);
+    return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 template <int N>
@@ -1313,35 +1309,55 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             const int me = tid - 32 * kConvertWarp;  // 0 .. 127
             int i = 0, g = 0;
             bool ok = true;
+            // A thread takes 16 elements at the same place of every `step`-th row: the swizzle of its two vectors is
+            // the same in all of them, and a block of 16 keys has one scale for a whole warp.  The two halves of a
+            // row lie in the same banks, so the lanes of the second take their eights of elements the other way round.
+            constexpr int chunks = DP / 16, step = 128 / chunks;
+            const int row0 = me / chunks, c = me % chunks, c2 = 2 * c & 7, odd = c >> 2;
+            const int at0 = row0 * 128 + ((c2 + odd) ^ (row0 & 7)) * 16, at1 = row0 * 128 + ((c2 + (odd ^ 1)) ^ (row0 & 7)) * 16;
+            const char* const mine = sm + L::oG + me * 16;
             // `rows` rows from row `first` of the tile in place gi to a tile at dst; rows from `have` on become 0.
             auto convert = [&](int gi, int first, auto rows_c, char* dst, int have) {
-                // 16 elements a turn, U turns in flight
-                constexpr int rows = decltype(rows_c)::value, chunks = DP / 16, turns = rows * chunks / 128, U = turns < 4 ? turns : 4;
-                static_assert(turns % U == 0, "whole groups of turns");
-                const char* const src = sm + L::oG + gi * L::kGBytes + first * DP;
-                const float* const scales = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
-#pragma unroll 1
-                for (int i0 = me; i0 < rows * chunks; i0 += U * 128) {
-                    uint4 x[U];
+                constexpr int rows = decltype(rows_c)::value, turns = rows / step, U = turns < 4 ? turns : 4;
+                static_assert(turns % U == 0 && step % 16 == 0, "whole groups of turns");
+                const char* const src = mine + gi * L::kGBytes + first * DP;
+                const float* const all = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
+                const float* const scales = all + ((first + row0) >> 4);
+                char* const to = dst + odd * (rows * 128);
+                const bool plain = !BF16 && __all_sync(0xffffffffu, fits_half(all[lane & 7]));
+                auto group = [&](int k0, auto plain_c) {
+                    constexpr bool kPlain = decltype(plain_c)::value != 0;
+                    uint2 x0[U], x1[U];
                     float f[U];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        x[u] = *reinterpret_cast<const uint4*>(src + (i0 + u * 128) * 16);
-                        f[u] = scales[first + (i0 + u * 128) / chunks >> 4];
+                        x0[u] = *reinterpret_cast<const uint2*>(src + (k0 + u) * 2048 + 8 * odd);
+                        x1[u] = *reinterpret_cast<const uint2*>(src + (k0 + u) * 2048 + 8 * (odd ^ 1));
+                        f[u] = scales[(k0 + u) * (step / 16)];
+                    }
+                    uint4 y0[U], y1[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        y0[u] = widen<BF16, kPlain>(x0[u], f[u]);
+                        y1[u] = widen<BF16, kPlain>(x1[u], f[u]);
+                    }
+                    if (have < kTile) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (first + row0 + (k0 + u) * step >= have) y0[u] = y1[u] = make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const int at = i0 + u * 128, r = at / chunks, c = at % chunks, c2 = 2 * c & 7;
-                        uint4 y0, y1;
-                        widen<BF16>(x[u], f[u], y0, y1);
-                        if (first + r >= have) y0 = y1 = make_uint4(0, 0, 0, 0);
-                        char* const row = dst + (c >> 2) * (rows * 128) + r * 128;
-                        char *const p0 = row + (c2 ^ (r & 7)) * 16, *const p1 = row + ((c2 + 1) ^ (r & 7)) * 16;
-                        // the two halves of a row lie in the same banks: their lanes store at different chunks
-                        const bool swap = c >= 4;
-                        *reinterpret_cast<uint4*>(swap ? p1 : p0) = swap ? y1 : y0;
-                        *reinterpret_cast<uint4*>(swap ? p0 : p1) = swap ? y0 : y1;
+                        *reinterpret_cast<uint4*>(to + (k0 + u) * (step * 128) + at0) = y0[u];
+                        *reinterpret_cast<uint4*>(to + (k0 + u) * (step * 128) + at1) = y1[u];
                     }
+                };
+#pragma unroll
+                for (int k0 = 0; k0 < turns; k0 += U) {
+                    if (plain)
+                        group(k0, Count<1>{});
+                    else
+                        group(k0, Count<0>{});
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
