@@ -342,7 +342,7 @@ struct Walk {
     }
 };
 
-template <int DP, bool PROMPT, bool E8>
+template <int DP, bool BF16, bool PROMPT, bool E8>
 struct Lay {
     static constexpr int kHalves = DP / 64;
     static constexpr int kHalf = kTile * 128;  // bytes of 64 columns of a tile
@@ -351,29 +351,42 @@ struct Lay {
     // columns), so that the next scores are computed while this tile's are exponentiated; with rows of 128
     // the weights lie over the scores.
     static constexpr bool kApart = DP == 64;
+    // Trees multiply the cache's K as it is, by a Q in parts of 8 bits.
+    static constexpr bool kDirect = E8 && !PROMPT;
+    static constexpr int kParts = kDirect ? (BF16 ? 2 : 3) : 0;
+    static constexpr int kPart = kTile * DP;                       // bytes of a tile of 8 bits
     static constexpr int kQ = PROMPT ? 2 : 1;                      // row tiles of an item
     static constexpr int kQB = DP == 128 && (PROMPT || E8) ? 1 : 2;  // items whose Q is held
     // K tiles in the ring
-    static constexpr int kK = E8 ? (DP == 128 ? 2 : 3) : DP == 128 ? (PROMPT ? 3 : 2) : (PROMPT ? 5 : 4);
-    // V tiles in the ring; with a cache in 8 bits halves of 64 keys
-    static constexpr int kV = E8 ? (DP == 128 ? 3 : 6) : DP == 128 ? 2 : (PROMPT ? 5 : 4);
+    static constexpr int kK = kDirect ? (DP == 128 ? (BF16 ? 3 : 2) : 6) : E8 ? (DP == 128 ? 2 : 3) : DP == 128 ? (PROMPT ? 3 : 2) : (PROMPT ? 5 : 4);
+    static constexpr int kKBytes = kDirect ? kPart : kBytes;
+    // V tiles in the ring; with a cache in 8 bits halves of 64 keys, an even number: each half has places of its own
+    static constexpr int kV = E8 ? (DP == 128 || kDirect ? 4 : 6) : DP == 128 ? 2 : (PROMPT ? 5 : 4);
     static constexpr int kVBytes = E8 ? kBytes / 2 : kBytes;
-    // tiles as the cache holds them, 8 bits
-    static constexpr int kG = E8 ? (DP == 128 ? (PROMPT ? 3 : 4) : (PROMPT ? 6 : 8)) : 0;
+    // tiles as the cache holds them, to be converted
+    static constexpr int kG = !E8 ? 0 : DP == 128 ? 2 : 6;
+    static_assert(!E8 || kV % 2 == 0, "places of halves");
     static constexpr int kGs = kG > 0 ? kG : 1;
-    static constexpr int kGBytes = kTile * DP;
-    static constexpr int oK = kQ * kQB * kBytes, oV = oK + kK * kBytes, oG = oV + kV * kVBytes;
+    static constexpr int oParts = kQ * kQB * kBytes;
+    static constexpr int oK = oParts + kQB * kParts * kPart, oV = oK + kK * kKBytes, oG = oV + kV * kVBytes;
     // after the tiles
-    static constexpr int oKFull = oG + kG * kGBytes, oKEmpty = oKFull + 8 * kK;
+    static constexpr int oKFull = oG + kG * kPart, oKEmpty = oKFull + 8 * kK;
     static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
     static constexpr int oGFull = oVEmpty + 8 * kV, oGEmpty = oGFull + 8 * kG;
-    static constexpr int oQFull = oGEmpty + 8 * kG, oQEmpty = oQFull + 8 * kQB;
+    static constexpr int oPartsReady = oGEmpty + 8 * kG, oFactorRead = oPartsReady + 8 * kQB;
+    static constexpr int oQFull = oFactorRead + 8 * kQB, oQEmpty = oQFull + 8 * kQB;
     static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
     static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
     static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
     static constexpr int oScale = oBad + 16 * kV;                     // float[kG][8]: of blocks of 16 keys
-    static constexpr int oNear = oScale + 32 * kG;                    // Reach[kNear]
+    // K's scales outlive its tile: the softmax warps read them.  A place is written again when the tile kScales before
+    // is weighed: the copy of a tile waits for the scores of the one kK before, which follow the weights of kK + 2.
+    static constexpr int kScales = kDirect ? 16 : 0;
+    static_assert(!kDirect || kScales >= kK + 2, "scales in use");
+    static constexpr int oKeyScale = oScale + 32 * kG;                // float[kScales][8]
+    static constexpr int oFactor = oKeyScale + 32 * kScales;          // float[kQB][128]: what a row of Q's parts is to be multiplied by
+    static constexpr int oNear = oFactor + (kDirect ? kQB * kTile * 4 : 0);  // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
     static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: of items that end here, that begin here
     static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[8]
@@ -532,7 +545,7 @@ template <int DP, bool BF16, bool PROMPT, bool E8>
 __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constant__ Maps M, const __grid_constant__ Attend A,
                                                             const __grid_constant__ Shape S, void* scratch)
 {
-    using L = Lay<DP, PROMPT, E8>;
+    using L = Lay<DP, BF16, PROMPT, E8>;
     constexpr int kThreads = clk::kThreads<E8>, kWarps = clk::kWarps<E8>;
     extern __shared__ __align__(1024) char sm[];
     // the shuffle tells the compiler that a warp has one role
@@ -556,12 +569,12 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char*>(&M) + lane * sizeof(CUtensorMap)) : "memory");
     } else if (tid == 32 * kValueWarp) {
         for (int i = 0; i < L::kK; ++i) {
-            bar_init(base + L::oKFull + 8 * i, E8 ? 4 : 1);
+            bar_init(base + L::oKFull + 8 * i, L::kDirect ? 1 + 32 : E8 ? 4 : 1);
             bar_init(base + L::oKEmpty + 8 * i, 1);
         }
         for (int i = 0; i < L::kV; ++i) {
             bar_init(base + L::oVFull + 8 * i, 1);
-            bar_init(base + L::oVReady + 8 * i, E8 ? 4 : 1);
+            bar_init(base + L::oVReady + 8 * i, E8 ? 2 : 1);
             bar_init(base + L::oVEmpty + 8 * i, 1);
         }
         for (int i = 0; i < L::kG; ++i) {
@@ -569,8 +582,10 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             bar_init(base + L::oGEmpty + 8 * i, 4);
         }
         for (int i = 0; i < L::kQB; ++i) {
+            bar_init(base + L::oPartsReady + 8 * i, 4);
+            bar_init(base + L::oFactorRead + 8 * i, 8);
             bar_init(base + L::oQFull + 8 * i, 1);
-            bar_init(base + L::oQEmpty + 8 * i, 1);
+            bar_init(base + L::oQEmpty + 8 * i, L::kDirect ? 1 + 4 : 1);  // the products', and the warps' that split it
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(base + L::oSFull + 8 * i, 1);
@@ -688,10 +703,10 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::oTmem);
     const uint32_t qs = base, ks = base + L::oK, vs = base + L::oV;
 
-    // Registers: 384 threads x 168 at launch; 256 x 208 + 128 x 80 after the split.  512 x 128; 256 x 192 + 256 x 64.
+    // Registers: 384 threads x 168 at launch; 256 x 208 + 128 x 80 after the split.  512 x 128; 256 x 200 + 256 x 56.
     if (warp < kCopyWarp) {
         if (E8)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- Softmax: a thread per row. ----
@@ -708,6 +723,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
         constexpr float far_off = 256.0f;
         uint32_t sp = 0, od = 0;
         int gi = 0;
+        int gk = 0, segment = 0;  // with Q in parts: cached tiles before this segment, segments
         bool ok = true;
         Walk<PROMPT>& w = reinterpret_cast<Walk<PROMPT>*>(sm + L::oWalk)[warp];
         if (lane == 0) w.start(A, S, plan, near);
@@ -724,6 +740,10 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 seen = (unsigned long long)A.mask[(int64_t)w.b * A.N + token];
                 if (w.x.rows < 64) seen &= (1ull << w.x.rows) - 1;
             }
+            // A warp without rows goes along without its share of the work (its rows of tensor memory are its own).
+            const bool idle = E8 && !__any_sync(0xffffffffu, real);
+            float factor = 0.0f;  // of this row's scores with the cache
+            bool has_factor = false;
             float ref = -INFINITY, sum = 0.0f;
             bool settled = false;  // every row has a reference, and none is far off
             bool far = false;      // some row's is far off
@@ -738,11 +758,37 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 if (!warp_wait(base + L::oSFull + 8 * s, sp, stop)) return false;
                 sp ^= 1;
                 tmem_after();
+                if (!idle) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_load(tS + 32 * c, x + 32 * c);
-                tmem_load_wait();
+                    for (int c = 0; c < 4; ++c) tmem_load(tS + 32 * c, x + 32 * c);
+                    tmem_load_wait();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_loaded(x + 32 * c);
+                    for (int c = 0; c < 4; ++c) tmem_loaded(x + 32 * c);
+                }
+                if (L::kDirect && t < ctx_tiles) {
+                    if (!has_factor) {
+                        const int qi = segment % L::kQB;
+                        factor = reinterpret_cast<const float*>(sm + L::oFactor)[qi * kTile + row];
+                        has_factor = true;
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(base + L::oFactorRead + 8 * qi);
+                    }
+                    if (!idle) {
+                        const float4* const ks = reinterpret_cast<const float4*>(sm + L::oKeyScale) + 2 * ((gk + t - t0) % (L::kDirect ? L::kScales : 1));
+                        const float4 a = ks[0], b = ks[1];
+                        const float k[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t f = __float_as_uint(factor * k[i]);
+#pragma unroll
+                            for (int c = 16 * i; c < 16 * i + 16; c += 2) {
+                                const float2 y = unpair(mul2(pair(x[c], x[c + 1]), pair(f, f)));
+                                x[c] = __float_as_uint(y.x);
+                                x[c + 1] = __float_as_uint(y.y);
+                            }
+                        }
+                    }
+                }
                 if (L::kApart) {
                     tmem_before();
                     __syncwarp();
@@ -751,7 +797,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 // Hidden keys: a limit for most tiles, a mask for a tree's.
                 cached = t < ctx_tiles;
                 n0 = (t - ctx_tiles) * kTile;
-                if (cached || PROMPT) {
+                if (idle) {
+                } else if (cached || PROMPT) {
                     const int most = cached ? ctx - t * kTile : n0 + kTile - 1 > first ? token - n0 + 1 : kTile;
                     if (!cached ? n0 + kTile - 1 > first : most < kTile) {
 #pragma unroll
@@ -850,10 +897,14 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
                     // Rows of V that were not finite: NaN for those who see them.
                     const int i = gi + (PROMPT ? j : 2 * j + s), at = E8 ? 2 * i : i, vi = at % L::kV;
+                    // (The place's phase before this one has ended: it was of the tile two before, whose product went before
+                    // these scores or has been waited for.)
                     if (!warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop)) return false;
                     const int vj = E8 ? (at + 1) % L::kV : vi;
-                    if (E8 && !warp_wait(base + L::oVReady + 8 * vj, (uint32_t)((at + 1) / L::kV & 1), stop)) return false;
-                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], bad[4 * vj + (E8 ? 0 : 2)], bad[4 * vj + (E8 ? 1 : 3)]};
+                    if (E8 && !L::kDirect && !warp_wait(base + L::oVReady + 8 * vj, (uint32_t)((at + 1) / L::kV & 1), stop)) return false;
+                    // (a tree's tokens are the first 64 keys)
+                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], L::kDirect ? 0 : bad[4 * vj + (E8 ? 0 : 2)],
+                                             L::kDirect ? 0 : bad[4 * vj + (E8 ? 1 : 3)]};
                     if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
                         bool hit = false;
 #pragma unroll
@@ -881,6 +932,13 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             auto tiles = [&]() -> bool {
                 for (; j < mine; ++j) {
                     if (!(ok = fetch(j))) return false;
+                    if (idle) {
+                        tmem_before();
+                        __syncwarp();
+                        if (!L::kApart && lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
+                        if (lane == 0) bar_arrive(base + L::oPReady + 8 * s);
+                        continue;
+                    }
                     // Where the weights lie apart from the scores, the reference is not compared with every tile's
                     // maximum: the sum of the tile's weights shows when one has grown too large (over 2^15), and the tile
                     // is done again.  That spares the maximum's 64 instructions in nearly all tiles; a row's first tile
@@ -914,6 +972,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 }
             }
             if (!ok) break;
+            if (L::kDirect && !has_factor && lane == 0) bar_arrive(base + L::oFactorRead + 8 * (segment % L::kQB));
             if (mine > 0) {
                 if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
                 od ^= 1;
@@ -1010,6 +1069,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 if (!(ok = warp_wait(base + L::oStatReady, 1, stop))) break;
             }
             gi += len;
+            ++segment;
+            gk += ctx_tiles > t0 ? (ctx_tiles < t0 + len ? ctx_tiles - t0 : len) : 0;
             __syncwarp();
             if (lane == 0) w.next(A, S, plan, near);
             __syncwarp();
@@ -1018,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
         Walk<PROMPT> w;
         w.start(A, S, plan, near);
         if (E8)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == kCopyWarp || warp == kCopyWarp2) {
@@ -1027,13 +1088,12 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             // pages of 16: 119 us, by alternate tiles 155); with prompts they take alternate tiles, which keeps K and
             // V in step (a 25,000-token prompt: 3.16 ms, by K and V 3.26).  The first also brings Q.
             const int odd = warp == kCopyWarp ? 0 : 1;
-            // (With a cache in 8 bits they bring K and V apart too.)
             constexpr bool kApartKV = !PROMPT || E8;
             const bool brings_k = !kApartKV || odd == 0, brings_v = !kApartKV || odd == 1;
             auto my = [&](int tile) { return kApartKV || (tile & 1) == odd; };
-            // With a cache in 8 bits: the runs' tiles before this one in the order in which they are converted, and
-            // places in use, with the phase that ends the last copy to each.
-            int g0 = 0;
+            // With a cache in 8 bits: tiles to be converted so far, cached tiles before this segment, and places in use, with
+            // the phase that ends the last copy to each.
+            int g = 0, g0 = 0;
             uint32_t g_used = 0, g_phase = 0;
             int i = 0, seg = 0, nk = 0, nv = 0, nq = 0;  // n*: one past the last tile or item asked for
             bool ok = (base & 1023) == 0;  // the swizzle's period
@@ -1055,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 int at = w.t0 * pages & ~31, now = batch(at), then = batch(at + 32);
                 const int z = PROMPT ? 0 : w.b, row0 = PROMPT ? w.x.base : 0;
                 // the first K goes out before the first V
-                if (kApartKV && odd == 1 && seg == 0 && !(ok = warp_wait(base + L::oQFull, 0, stop))) break;
+                if (!PROMPT && !E8 && odd == 1 && seg == 0 && !(ok = warp_wait(base + L::oQFull, 0, stop))) break;
                 if (odd == 0) {
                     const int qi = seg % L::kQB;
                     const uint32_t qb = base + L::oQFull + 8 * qi;
@@ -1082,30 +1142,52 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
                     const uint32_t bytes = (uint32_t)L::kHalves * 128u * (uint32_t)(cached ? boxes << A.C.shift : S.kbox);
                     const int n0 = row0 + (t - w.x.ctx_tiles) * kTile;
-                    if (E8 && cached) {
-                        const int run = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0, r = t - w.t0;
-                        const int at8 = g0 + (odd == 0 ? (r > 0 ? 2 * r - 1 : 0) : r + 1 < run ? 2 * r + 2 : 2 * run - 1);
-                        const int gi = at8 % L::kGs;
-                        const uint32_t bar = base + L::oGFull + 8 * gi;
-                        if (!(ok = warp_wait(base + L::oGEmpty + 8 * gi, (uint32_t)(at8 / L::kGs & 1) ^ 1, stop))) break;
-                        g_used |= 1u << gi;
-                        g_phase = (g_phase & ~(1u << gi)) | (uint32_t)(at8 / L::kGs & 1) << gi;
-                        if (lane == 0) bar_expect(bar, (uint32_t)(boxes << A.C.shift) * DP);
-                        __syncwarp();
-                        if (page >= 0)
-                            copy_box(base + L::oG + gi * L::kGBytes + (lane << A.C.shift) * DP, odd == 0 ? &M.kc : &M.vc, 0, 0, w.h, page, bar);
-                        // the scales of 16 keys each; none for keys without a page (their rows become 0)
+                    // what brings the scales of 16 keys each; none for keys without a page (their rows become 0)
+                    auto bring_scales = [&](const float* plane, uint32_t dst, uint32_t bar) {
                         const int from = __shfl_sync(0xffffffffu, page, 16 * lane >> A.C.shift & 31);
                         if (lane < 8) {
                             const bool there = from >= 0 && from < A.C.num_pages;
-                            const float* const src = (odd == 0 ? A.ks : A.vs) +
-                                                     (there ? from * A.scale_page + w.h * A.scale_head +
-                                                                  ((16 * lane & (A.C.page_tokens() - 1)) >> A.scale_shift) * A.scale_block
-                                                            : 0);
-                            copy_word(base + L::oScale + 32 * gi + 4 * lane, src, there);
+                            const float* const src =
+                                plane + (there ? from * A.scale_page + w.h * A.scale_head +
+                                                     ((16 * lane & (A.C.page_tokens() - 1)) >> A.scale_shift) * A.scale_block
+                                               : 0);
+                            copy_word(dst + 4 * lane, src, there);
                         }
                         copies_arrive(bar);
+                    };
+                    if (L::kDirect && odd == 0) {
+                        const int ki = i % L::kK;
+                        const uint32_t bar = base + L::oKFull + 8 * ki, dst = ks + ki * L::kKBytes;
+                        if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
+                        nk = i + 1;
+                        if (lane == 0) bar_expect(bar, cached ? (uint32_t)(boxes << A.C.shift) * DP : (uint32_t)(L::kHalves * S.kbox) * 128u);
+                        __syncwarp();
+                        if (cached) {
+                            if (page >= 0) copy_box(dst + (lane << A.C.shift) * DP, &M.kc, 0, 0, w.h, page, bar);
+                            bring_scales(A.ks, base + L::oKeyScale + 32 * ((g0 + t - w.t0) % (L::kDirect ? L::kScales : 1)), bar);
+                        } else {
+                            // (at most 64 rows of 64 columns a half)
+                            if (lane < L::kHalves) copy_box(dst + lane * (L::kHalf / 2), &M.k, 64 * lane, w.h, n0, z, bar);
+                            copies_arrive(bar);
+                        }
                         continue;
+                    }
+                    // Tiles to be converted, K before V.  One warp brings them all: it sees every phase of their places.
+                    if (E8 && cached && odd == (L::kDirect ? 1 : 0)) {
+#pragma unroll 1
+                        for (int v = L::kDirect ? 1 : 0; ok && v < 2; ++v, ++g) {
+                            const int gi = g % L::kGs;
+                            const uint32_t bar = base + L::oGFull + 8 * gi;
+                            if (!(ok = warp_wait(base + L::oGEmpty + 8 * gi, (uint32_t)(g / L::kGs & 1) ^ 1, stop))) break;
+                            g_used |= 1u << gi;
+                            g_phase = (g_phase & ~(1u << gi)) | (uint32_t)(g / L::kGs & 1) << gi;
+                            if (lane == 0) bar_expect(bar, (uint32_t)(boxes << A.C.shift) * DP);
+                            __syncwarp();
+                            if (page >= 0)
+                                copy_box(base + L::oG + gi * L::kPart + (lane << A.C.shift) * DP, v == 0 ? &M.kc : &M.vc, 0, 0, w.h, page, bar);
+                            bring_scales(v == 0 ? A.ks : A.vs, base + L::oScale + 32 * gi, bar);
+                        }
+                        if (!ok) break;
                     }
                     if (E8) continue;  // new tokens' tiles are brought by those who convert
                     auto bring = [&](uint32_t bar, uint32_t dst, const CUtensorMap* pool, const CUtensorMap* fresh) {
@@ -1133,7 +1215,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 }
                 if (E8) {
                     const int run = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0;
-                    g0 += run > 0 ? 2 * run : 0;
+                    g0 += run > 0 ? run : 0;
                 }
             }
             if (!ok) {
@@ -1162,7 +1244,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
                 uint32_t ps[2] = {0, 0}, fs[2] = {1, 1};  // phases of PReady and SFree
                 int seg = 0, qi = 0;
-                uint32_t qp = 0;
+                uint32_t qp = 0, pr = 0;  // phases of QFull, and of each PartsReady
                 bool ok = true;
                 // This warp's instructions bound the rate at which short products follow one another: ring places
                 // and phases are counted along, and a tile is waited for once for both streams.
@@ -1179,6 +1261,11 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     __syncwarp();
                 };
                 // descriptors count in 16 bytes
+                // Q's parts and the cache's K: 8 bits, 32 elements a product, rows of 128 or 64 bytes
+                constexpr uint32_t kind_8 = (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+                constexpr uint32_t kind_n = types | ((64 >> 3) << 17);  // 64 new keys
+                const uint64_t p0 = DP == 128 ? operand(base + L::oParts, 16) : operand_64(base + L::oParts);
+                const uint64_t c0 = DP == 128 ? operand(ks, 16) : operand_64(ks);
                 const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, E8 ? L::kHalf / 2 : L::kHalf);
                 auto wait_k = [&] { return warp_wait(base + L::oKFull + 8 * ki, kp, stop); };
                 // (with a cache in 8 bits halves of V are waited for as they are used)
@@ -1191,13 +1278,33 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     }
                 };
                 // Stream s's scores with K tile ki.
-                auto scores = [&](int s) {
+                auto scores = [&](int s, bool cached) {
                     if (L::kApart) {
                         if (!warp_wait(base + L::oSFree + 8 * s, fs[s], stop)) return false;
                         fs[s] ^= 1;
                     }
                     tmem_after();
-                    const uint64_t q = q0 + (qi * L::kQ + (PROMPT ? s : 0)) * (L::kBytes / 16), k = k0 + ki * (L::kBytes / 16);
+                    const uint64_t q = q0 + (qi * L::kQ + (PROMPT ? s : 0)) * (L::kBytes / 16), k = k0 + ki * (L::kKBytes / 16);
+                    if (L::kDirect) {
+                        const uint64_t p = p0 + qi * L::kParts * (L::kPart / 16), c = c0 + ki * (L::kKBytes / 16);
+                        if (elect()) {
+                            if (cached) {
+#pragma unroll
+                                for (int e = 0; e < L::kParts * (DP / 32); ++e) {
+                                    const int part = e / (DP / 32), at = e % (DP / 32) * 2;
+                                    mma_ss8(tm + 128 * s, p + part * (L::kPart / 16) + at, c + at, kind_8, e > 0);
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < DP / 16; ++e)
+                                    mma_ss(tm + 128 * s, q + (e / 4) * (L::kHalf / 16) + (e % 4) * 2, k + (e / 4) * (L::kHalf / 32) + (e % 4) * 2,
+                                           kind_n, e > 0);
+                            }
+                            mma_commit(base + L::oSFull + 8 * s);
+                        }
+                        __syncwarp();
+                        return true;
+                    }
                     if (elect()) {
 #pragma unroll
                         for (int e = 0; e < DP / 16; ++e) {
@@ -1239,12 +1346,16 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     const int len = same(w.left > 0 ? w.t1 - w.t0 : 0);
                     if (len == 0) break;
                     if (!(ok = warp_wait(base + L::oQFull + 8 * qi, qp, stop))) break;
+                    if (L::kDirect && same(w.t0 < w.x.ctx_tiles)) {
+                        if (!(ok = warp_wait(base + L::oPartsReady + 8 * qi, pr >> qi & 1, stop))) break;
+                        pr ^= 1u << qi;
+                    }
                     if (PROMPT) {
                         const int n[2] = {same(w.last(S, 0) - w.t0), same(w.last(S, 1) - w.t0)};
                         if (!(ok = wait_k())) break;
 #pragma unroll
                         for (int s = 0; s < 2; ++s)
-                            if (ok && n[s] > 0) ok = scores(s);
+                            if (ok && n[s] > 0) ok = scores(s, false);
                         if (!ok) break;
                         done(base + L::oKEmpty + 8 * ki);
                         step(ki, kp, L::kK);
@@ -1257,14 +1368,14 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
                                 if (!ok) continue;
-                                if (L::kApart && j + 1 < n[s]) ok = scores(s);
+                                if (L::kApart && j + 1 < n[s]) ok = scores(s, false);
                                 if (ok && j < n[s]) {
                                     ok = values(s, j > 0);
                                     if (ok && (L::kApart || j + 1 == n[s])) done(base + L::oODone + 8 * s);
                                 }
                                 if (!L::kApart && ok && more) {
                                     if (s == 0) ok = wait_k();
-                                    if (ok && j + 1 < n[s]) ok = scores(s);
+                                    if (ok && j + 1 < n[s]) ok = scores(s, false);
                                 }
                             }
                             if (!ok) break;
@@ -1278,7 +1389,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     } else {
                         auto ahead = [&](int j) {
                             if (j >= len) return true;
-                            if (!wait_k() || !scores(j & 1)) return false;
+                            if (!wait_k() || !scores(j & 1, w.t0 + j < w.x.ctx_tiles)) return false;
                             done(base + L::oKEmpty + 8 * ki);
                             step(ki, kp, L::kK);
                             if (j + 1 == len) done(base + L::oQEmpty + 8 * qi);
@@ -1305,51 +1416,49 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             }
             __syncwarp();
         } else if (E8 && warp >= kConvertWarp) {
-            // ---- Tiles of the cache: to 16 bits, times their scales. ----
+            // ---- Tiles of the cache: to 16 bits, times their scales.  Trees: V alone, and Q in parts of 8 bits. ----
             const int me = tid - 32 * kConvertWarp;  // 0 .. 127
-            int i = 0, g = 0;
-            bool ok = true;
-            // A thread takes 16 elements at the same place of every `step`-th row: the swizzle of its two vectors is
-            // the same in all of them, and a block of 16 keys has one scale for a whole warp.  The two halves of a
-            // row lie in the same banks, so the lanes of the second take their eights of elements the other way round.
-            constexpr int chunks = DP / 16, step = 128 / chunks;
-            const int row0 = me / chunks, c = me % chunks, c2 = 2 * c & 7, odd = c >> 2;
-            const int at0 = row0 * 128 + ((c2 + odd) ^ (row0 & 7)) * 16, at1 = row0 * 128 + ((c2 + (odd ^ 1)) ^ (row0 & 7)) * 16;
-            const char* const mine = sm + L::oG + me * 16;
-            // `rows` rows from row `first` of the tile in place gi to a tile at dst; rows from `have` on become 0.
-            auto convert = [&](int gi, int first, auto rows_c, char* dst, int have) {
-                constexpr int rows = decltype(rows_c)::value, turns = rows / step, U = turns < 4 ? turns : 4;
-                static_assert(turns % U == 0 && step % 16 == 0, "whole groups of turns");
-                const char* const src = mine + gi * L::kGBytes + first * DP;
+            // Two warps take a tile's first 64 keys, two the others.  A thread takes 16 elements at the same place of
+            // every `step`-th row: the swizzle of its vectors is the same in all of them.  Of eight lanes, whose
+            // vectors go out together, four take one half of row r and four that of row r ^ 5 (with rows of 64
+            // elements r and r + 1): their loads lie in 32 different banks, and so do both their stores.
+            constexpr int chunks = DP / 16, step = 64 / chunks;
+            const int team = me >> 6, you = me & 63;
+            const int c = (you & 3) + (DP == 128 ? 4 * (you >> 3 & 1) : 0);
+            const int row0 = DP == 128 ? (you >> 4) ^ ((you >> 2 & 1) * 5) : you / chunks;
+            const int c2 = 2 * c & 7, swizzle = row0 & 7;
+            const int at0 = row0 * 128 + (c2 ^ swizzle) * 16, at1 = row0 * 128 + ((c2 + 1) ^ swizzle) * 16;
+            const int from = (64 * team + row0) * DP + (DP == 128 ? c ^ swizzle : c) * 16;
+            // The team's half of the tile in place gi to rows from dst on, columns 64 .. of which lie `next` bytes
+            // further; keys from `have` on become 0.
+            auto convert = [&](int gi, char* dst, int next, int have) {
+                constexpr int turns = 64 / step, U = 4;
+                const char* const src = sm + L::oG + gi * L::kPart + from;
                 const float* const all = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
-                const float* const scales = all + ((first + row0) >> 4);
-                char* const to = dst + odd * (rows * 128);
+                char* const to = dst + (c >> 2) * next;
                 const bool plain = !BF16 && __all_sync(0xffffffffu, fits_half(all[lane & 7]));
                 auto group = [&](int k0, auto plain_c) {
                     constexpr bool kPlain = decltype(plain_c)::value != 0;
-                    uint2 x0[U], x1[U];
+                    uint4 x[U];
                     float f[U];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        x0[u] = *reinterpret_cast<const uint2*>(src + (k0 + u) * 2048 + 8 * odd);
-                        x1[u] = *reinterpret_cast<const uint2*>(src + (k0 + u) * 2048 + 8 * (odd ^ 1));
-                        f[u] = scales[(k0 + u) * (step / 16)];
+                        x[u] = *reinterpret_cast<const uint4*>(src + (k0 + u) * (step * DP));
+                        f[u] = all[4 * team + (k0 + u) * step / 16];
                     }
-                    uint4 y0[U], y1[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        y0[u] = widen<BF16, kPlain>(x0[u], f[u]);
-                        y1[u] = widen<BF16, kPlain>(x1[u], f[u]);
-                    }
-                    if (have < kTile) {
+                    if (have < kTile) {  // codes and scales of 0
 #pragma unroll
                         for (int u = 0; u < U; ++u)
-                            if (first + row0 + (k0 + u) * step >= have) y0[u] = y1[u] = make_uint4(0, 0, 0, 0);
+                            if (64 * team + row0 + (k0 + u) * step >= have) {
+                                x[u] = make_uint4(0, 0, 0, 0);
+                                f[u] = 0.0f;
+                            }
                     }
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        *reinterpret_cast<uint4*>(to + (k0 + u) * (step * 128) + at0) = y0[u];
-                        *reinterpret_cast<uint4*>(to + (k0 + u) * (step * 128) + at1) = y1[u];
+                        char* const row = to + (k0 + u) * (step * 128);
+                        *reinterpret_cast<uint4*>(row + at0) = widen<BF16, kPlain>(make_uint2(x[u].x, x[u].y), f[u]);
+                        *reinterpret_cast<uint4*>(row + at1) = widen<BF16, kPlain>(make_uint2(x[u].z, x[u].w), f[u]);
                     }
                 };
 #pragma unroll
@@ -1362,9 +1471,11 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             };
-            // These warps write to both rings, or have it written, in the order of the tiles: they alone wait for every
+            int i = 0, g = 0;
+            bool ok = true;
+            // These warps write to the rings, or have it written, in the order of the tiles: they alone wait for every
             // phase of their places.  (A wait tells a phase from the one before it, not from the one before that.)
-            const bool brings = warp == kConvertWarp;  // the tiles of new tokens
+            const bool brings = (warp & 1) == 0;  // the team's half of new tokens' V tiles; the first team K tiles too
             uint32_t k_used = 0, k_phase = 0, v_used = 0, v_phase = 0;  // places with copies, the phase that ends the last
             auto keys = [&](int tile, int t) {
                 const int ki = tile % L::kK;
@@ -1374,13 +1485,13 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
                 if (!warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(tile / L::kK & 1) ^ 1, stop)) return false;
                 if (cached) {
-                    convert(gi, 0, Count<kTile>{}, sm + L::oK + ki * L::kBytes, kTile);
+                    convert(gi, sm + L::oK + ki * L::kKBytes + team * (64 * 128), L::kHalf, kTile);
                     if (lane == 0) {
                         bar_arrive(full);
                         bar_arrive(base + L::oGEmpty + 8 * gi);
                     }
                     ++g;
-                } else if (!brings) {
+                } else if (warp != kConvertWarp) {
                     if (lane == 0) bar_arrive(full);
                 } else {
                     k_used |= 1u << ki;
@@ -1388,7 +1499,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.kbox) * 128u);
                     __syncwarp();
                     if (lane < L::kHalves)
-                        copy_box(ks + ki * L::kBytes + lane * L::kHalf, &M.k, 64 * lane, w.h,
+                        copy_box(ks + ki * L::kKBytes + lane * L::kHalf, &M.k, 64 * lane, w.h,
                                  (PROMPT ? w.x.base : 0) + (t - w.x.ctx_tiles) * kTile, PROMPT ? 0 : w.b, full);
                 }
                 return true;
@@ -1397,46 +1508,113 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 const bool cached = t < w.x.ctx_tiles;
                 const int gi = g % L::kGs, n0 = (t - w.x.ctx_tiles) * kTile;
                 const int have = cached ? w.x.ctx - t * kTile : w.x.rows - n0;
+                const int at = 2 * tile + team, vi = at % L::kV;
+                const uint32_t full = base + L::oVFull + 8 * vi;
+                char* const place = sm + L::oV + vi * L::kVBytes;
                 if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int at = 2 * tile + hf, vi = at % L::kV;
-                    const uint32_t full = base + L::oVFull + 8 * vi;
-                    if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(at / L::kV & 1) ^ 1, stop)) return false;
-                    if (cached) {
-                        convert(gi, 64 * hf, Count<kTile / 2>{}, sm + L::oV + vi * L::kVBytes, have);
-                    } else if (have > 64 * hf) {
-                        if (brings) {
-                            v_phase = v_used >> vi & 1 ? v_phase ^ 1u << vi : v_phase;
-                            v_used |= 1u << vi;
-                            if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
-                            __syncwarp();
-                            if (lane < L::kHalves)
-                                copy_box(vs + vi * L::kVBytes + lane * (L::kHalf / 2), &M.v, 64 * lane, w.h,
-                                         (PROMPT ? w.x.base : 0) + n0 + 64 * hf, PROMPT ? 0 : w.b, full);
-                        }
-                        continue;  // the V warp hands it on
-                    } else {
-                        // a half without tokens
-                        for (int e = me; e < L::kVBytes / 16; e += 128)
-                            *reinterpret_cast<uint4*>(sm + L::oV + vi * L::kVBytes + 16 * e) = make_uint4(0, 0, 0, 0);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (me < 4) bad[4 * vi + me] = 0;
-                        __syncwarp();
-                    }
-                    if (lane == 0) bar_arrive(base + L::oVReady + 8 * vi);
-                }
+                if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(at / L::kV & 1) ^ 1, stop)) return false;
                 if (cached) {
-                    if (lane == 0) bar_arrive(base + L::oGEmpty + 8 * gi);
+                    convert(gi, place, L::kHalf / 2, have);
+                    if (lane == 0) {
+                        bar_arrive(base + L::oVReady + 8 * vi);
+                        bar_arrive(base + L::oGEmpty + 8 * gi);
+                    }
                     ++g;
+                } else if (have > 64 * team) {
+                    // (the V warp hands it on)
+                    if (brings) {
+                        v_phase = v_used >> vi & 1 ? v_phase ^ 1u << vi : v_phase;
+                        v_used |= 1u << vi;
+                        if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
+                        __syncwarp();
+                        if (lane < L::kHalves)
+                            copy_box(vs + vi * L::kVBytes + lane * (L::kHalf / 2), &M.v, 64 * lane, w.h,
+                                     (PROMPT ? w.x.base : 0) + n0 + 64 * team, PROMPT ? 0 : w.b, full);
+                    }
+                } else {
+                    // a half without tokens
+                    for (int e = you; e < L::kVBytes / 16; e += 64) *reinterpret_cast<uint4*>(place + 16 * e) = make_uint4(0, 0, 0, 0);
+                    if (you < 4) bad[4 * vi + you] = 0;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(base + L::oVReady + 8 * vi);
                 }
                 return true;
             };
-            for (; ok && w.left > 0; w.next(A, S, plan, near)) {
-                // K runs a tile ahead of V: the next scores wait for it
+            // Row `me` of the item's Q in parts of 8 bits: q = factor (p0 + p1 (+ p2)), each part the rounding of what
+            // the parts before it leave, so that together they hold 9 (14) bits of an element, or 2^-19 of the row's
+            // largest where that is more: bfloat16 has 8, float16 11.  A row that is not finite gets the factor NaN.
+            auto split = [&](int seg) {
+                const int qi = seg % L::kQB;
+                if (!warp_wait(base + L::oQFull + 8 * qi, (uint32_t)(seg / L::kQB & 1), stop)) return false;
+                if (!warp_wait(base + L::oFactorRead + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop)) return false;
+                // (No phase of the two is left out, and none passes by: Q's place is free once these warps have been here.)
+                if (w.t0 >= w.x.ctx_tiles) {
+                    if (lane == 0) bar_arrive(base + L::oQEmpty + 8 * qi);
+                    return true;
+                }
+                const char* const raw = sm + qi * L::kBytes + me * 128;
+                auto load = [&](int i, float* f) {  // elements 8 i .. 8 i + 7
+                    const uint4 v = *reinterpret_cast<const uint4*>(raw + (i >> 3) * L::kHalf + ((i & 7) ^ (me & 7)) * 16);
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = BF16 ? make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)) : halves(u[e]);
+                        f[2 * e] = y.x;
+                        f[2 * e + 1] = y.y;
+                    }
+                };
+                float top = 0.0f;
+                bool finite = true;
+#pragma unroll 4
+                for (int i = 0; i < DP / 8; ++i) {
+                    float f[8];
+                    load(i, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        top = fmaxf(top, fabsf(f[e]));
+                        finite = finite && fabsf(f[e]) <= 3.4028234e38f;
+                    }
+                }
+                const float scale = scale_for(finite ? top : 0.0f), inv = 1.0f / scale;
+                char* const parts = sm + L::oParts + qi * L::kParts * L::kPart + me * DP;
+#pragma unroll 1
+                for (int i = 0; i < DP / 16; ++i) {
+                    float f[16];
+                    load(2 * i, f);
+                    load(2 * i + 1, f + 8);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = finite ? f[e] * inv : 0.0f;
+#pragma unroll
+                    for (int part = 0; part < L::kParts; ++part) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            y[e] = to_e4m3(f[4 * e], f[4 * e + 1]) | to_e4m3(f[4 * e + 2], f[4 * e + 3]) << 16;
+                            if (part + 1 < L::kParts) {
+                                float h[4];
+                                from_e4m3x4(y[e], h);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) f[4 * e + k] -= h[k];
+                            }
+                        }
+                        const int at = DP == 128 ? i ^ (me & 7) : i ^ (me >> 1 & 3);
+                        *reinterpret_cast<uint4*>(parts + part * L::kPart + 16 * at) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+                reinterpret_cast<float*>(sm + L::oFactor)[qi * kTile + me] = finite ? scale : NAN;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(base + L::oPartsReady + 8 * qi);
+                    bar_arrive(base + L::oQEmpty + 8 * qi);
+                }
+                return true;
+            };
+            for (int seg = 0; ok && w.left > 0; w.next(A, S, plan, near), ++seg) {
+                if (L::kDirect) ok = split(seg);
                 for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
-                    if (t == w.t0) ok = keys(i, t);
-                    if (ok && t + 1 < w.t1) ok = keys(i + 1, t + 1);
+                    if (!L::kDirect) ok = keys(i, t);
                     if (ok) ok = values(i, t);
                 }
             }
@@ -1508,7 +1686,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                             }
                             __syncwarp();
-                            if (lane < 4) bar_arrive(base + L::oVReady + 8 * vi);
+                            if (lane < 2) bar_arrive(base + L::oVReady + 8 * vi);
                         }
                     }
                 }
@@ -1604,10 +1782,9 @@ EncodeFn encoder()
 }
 
 // A map over [n3][n2][n1][dim] elements with the given strides (in
-// elements), copied in boxes of b0 x b1 x b2 (x 1): 64 elements of 16 bits in
-// the swizzle, or rows of 8 bits as they are.
+// elements), copied in boxes of b0 x b1 x b2 (x 1).
 bool encode(EncodeFn f, CUtensorMap* m, int32_t dtype, const void* base, int64_t dim, const int64_t n[3], const int64_t st[3],
-            int b0, int b1, int b2)
+            int b0, int b1, int b2, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
 {
     const cuuint64_t es = dtype == CLK_DTYPE_E4M3 ? 1 : 2;
     const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)n[0], (cuuint64_t)n[1], (cuuint64_t)n[2]};
@@ -1619,7 +1796,7 @@ bool encode(EncodeFn f, CUtensorMap* m, int32_t dtype, const void* base, int64_t
                                      : dtype == CLK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     return f(m, type, 4, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             es == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1629,7 +1806,7 @@ bool map_stride(int64_t st, int64_t n, int per = 8) { return n <= 1 || (st > 0 &
 template <int DP, bool BF16, bool PROMPT, bool E8>
 int launch_mma(const Attend& A, const Shape& S, const Maps& M, void* scratch, cudaStream_t s)
 {
-    using L = Lay<DP, PROMPT, E8>;
+    using L = Lay<DP, BF16, PROMPT, E8>;
     static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CLK_ECUDA;
@@ -1715,8 +1892,11 @@ int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)
         const int64_t sp[3] = {A.tok_stride, A.head_stride, A.page_stride};
         const int32_t type = eight ? CLK_DTYPE_E4M3 : A.dtype;
         const int b0 = eight ? pad_dim(A.dim) : 64;
-        ok = ok && encode(f, &M.kc, type, A.kc, A.dim, np, sp, b0, A.C.page_tokens(), 1) &&
-             encode(f, &M.vc, type, A.vc, A.dim, np, sp, b0, A.C.page_tokens(), 1);
+        // rows of 64 bytes: an operand of the products has their swizzle, what is converted lies as it is
+        const CUtensorMapSwizzle vs = b0 * (eight ? 1 : 2) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+        const CUtensorMapSwizzle ks = vs == CU_TENSOR_MAP_SWIZZLE_NONE && !prompt ? CU_TENSOR_MAP_SWIZZLE_64B : vs;
+        ok = ok && encode(f, &M.kc, type, A.kc, A.dim, np, sp, b0, A.C.page_tokens(), 1, ks) &&
+             encode(f, &M.vc, type, A.vc, A.dim, np, sp, b0, A.C.page_tokens(), 1, vs);
     } else {
         M.kc = M.vc = M.k;  // not read: no request has cached rows
     }

@@ -37,4 +37,14 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t codes, float* f)
     f[3] = b.y;
 }
 
+// The least power of two (at least 2^-120) with which `top` is at most 448 = 1.75 * 2^8.
+__device__ __forceinline__ float scale_for(float top)
+{
+    constexpr int least = 127 - 120;
+    const uint32_t bits = __float_as_uint(top);
+    int e = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    if (e < least) e = least;
+    return __uint_as_float((uint32_t)e << 23);
+}
+
 }  // namespace clk

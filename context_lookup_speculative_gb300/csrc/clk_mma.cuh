@@ -92,6 +92,13 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t next)
            (1ull << 46) | (2ull << 61);
 }
 
+// The same for rows of 64 bytes in the 64-byte swizzle (groups of eight rows
+// 512 bytes apart), the contraction along them.
+__device__ __forceinline__ uint64_t operand_64(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | ((uint64_t)(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
+}
+
 // One lane of a converged warp, always the same one.  Products are issued
 // inside `if (elect())`: the compiler knows that one thread runs there and
 // keeps their operands in uniform registers.  (With a lane's own predicate on
@@ -110,6 +117,16 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"(add)
+        : "memory");
+}
+
+// The same for operands of 8 bits, 32 elements of the contraction.
+__device__ __forceinline__ void mma_ss8(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, uint32_t add)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(kind), "r"(add)
         : "memory");
 }

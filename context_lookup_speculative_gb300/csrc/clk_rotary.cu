@@ -38,7 +38,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostRows = 128;  // of a block
-constexpr int kLeast = 127 - 120;  // exponent field of the least scale, 2^-120
 
 struct Turn {
     CacheDev C;
@@ -238,15 +237,6 @@ __device__ __forceinline__ Piece piece_of(const Turn& A, int e)
 __host__ __device__ inline int pieces(const Turn& A)
 {
     return A.layers * A.kv_heads * (A.v != nullptr ? 2 : 1) + (A.q != nullptr ? A.q_heads : 0);
-}
-
-// The least power of two with which `top` is at most 448: 448 = 1.75 * 2^8.
-__device__ __forceinline__ float scale_for(float top)
-{
-    const uint32_t bits = __float_as_uint(top);
-    int e = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    if (e < kLeast) e = kLeast;
-    return __uint_as_float((uint32_t)e << 23);
 }
 
 // The block's scale from its rows' largest finite magnitude, and what its earlier rows had (0: they need no change).
