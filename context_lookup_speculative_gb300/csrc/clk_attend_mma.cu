@@ -390,7 +390,7 @@ struct Lay {
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
     static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: of items that end here, that begin here
     static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[8]
-    static constexpr int oStop = oWalk + 8 * (int)sizeof(Walk<PROMPT>), oTmem = oStop + 4;
+    static constexpr int oStop = oWalk + (E8 ? 12 : 8) * (int)sizeof(Walk<PROMPT>), oTmem = oStop + 4;
     static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;          // float2[2][128] for trees
     static constexpr int kTotal = oStat + (PROMPT ? 0 : 2 * kTile * 8);
     static_assert(kTotal <= 232448, "shared memory");
@@ -1076,12 +1076,13 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             __syncwarp();
         }
     } else {
+        // (the converting warps keep their way through the share in shared memory too)
         Walk<PROMPT> w;
-        w.start(A, S, plan, near);
-        if (E8)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        else
+        if (!E8 || warp < kConvertWarp) w.start(A, S, plan, near);
+        if (!E8)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kCopyWarp || warp == kCopyWarp2) {
             // ---- Copies: two warps (a copy costs its warp about 65 cycles, and pages of 16 rows need 16 a tile). ----
             // With trees one brings K and the other V, so that small pages' copies go side by side (256 short requests,
@@ -1418,6 +1419,9 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
         } else if (E8 && warp >= kConvertWarp) {
             // ---- Tiles of the cache: to 16 bits, times their scales.  Trees: V alone, and Q in parts of 8 bits. ----
             const int me = tid - 32 * kConvertWarp;  // 0 .. 127
+            Walk<PROMPT>& w = reinterpret_cast<Walk<PROMPT>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
+            if (lane == 0) w.start(A, S, plan, near);
+            __syncwarp();
             // Two warps take a tile's first 64 keys, two the others.  A thread takes 16 elements at the same place of
             // every `step`-th row: the swizzle of its vectors is the same in all of them.  Of eight lanes, whose
             // vectors go out together, four take one half of row r and four that of row r ^ 5 (with rows of 64
@@ -1432,42 +1436,37 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             // The team's half of the tile in place gi to rows from dst on, columns 64 .. of which lie `next` bytes
             // further; keys from `have` on become 0.
             auto convert = [&](int gi, char* dst, int next, int have) {
-                constexpr int turns = 64 / step, U = 4;
+                constexpr int turns = 64 / step;
                 const char* const src = sm + L::oG + gi * L::kPart + from;
                 const float* const all = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
                 char* const to = dst + (c >> 2) * next;
                 const bool plain = !BF16 && __all_sync(0xffffffffu, fits_half(all[lane & 7]));
-                auto group = [&](int k0, auto plain_c) {
+                uint4 x[turns];
+                const float4 four = reinterpret_cast<const float4*>(all)[team];
+                float f[4] = {four.x, four.y, four.z, four.w};  // of 16 keys each
+#pragma unroll
+                for (int u = 0; u < turns; ++u) x[u] = *reinterpret_cast<const uint4*>(src + u * (step * DP));
+                if (have < kTile) {  // codes of 0, and scales that are none of a key's
+#pragma unroll
+                    for (int u = 0; u < turns; ++u)
+                        if (64 * team + row0 + u * step >= have) x[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (64 * team + 16 * u >= have) f[u] = 0.0f;
+                }
+                auto all_turns = [&](auto plain_c) {
                     constexpr bool kPlain = decltype(plain_c)::value != 0;
-                    uint4 x[U];
-                    float f[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        x[u] = *reinterpret_cast<const uint4*>(src + (k0 + u) * (step * DP));
-                        f[u] = all[4 * team + (k0 + u) * step / 16];
-                    }
-                    if (have < kTile) {  // codes and scales of 0
-#pragma unroll
-                        for (int u = 0; u < U; ++u)
-                            if (64 * team + row0 + (k0 + u) * step >= have) {
-                                x[u] = make_uint4(0, 0, 0, 0);
-                                f[u] = 0.0f;
-                            }
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        char* const row = to + (k0 + u) * (step * 128);
-                        *reinterpret_cast<uint4*>(row + at0) = widen<BF16, kPlain>(make_uint2(x[u].x, x[u].y), f[u]);
-                        *reinterpret_cast<uint4*>(row + at1) = widen<BF16, kPlain>(make_uint2(x[u].z, x[u].w), f[u]);
+                    for (int u = 0; u < turns; ++u) {
+                        char* const row = to + u * (step * 128);
+                        *reinterpret_cast<uint4*>(row + at0) = widen<BF16, kPlain>(make_uint2(x[u].x, x[u].y), f[u * step / 16]);
+                        *reinterpret_cast<uint4*>(row + at1) = widen<BF16, kPlain>(make_uint2(x[u].z, x[u].w), f[u * step / 16]);
                     }
                 };
-#pragma unroll
-                for (int k0 = 0; k0 < turns; k0 += U) {
-                    if (plain)
-                        group(k0, Count<1>{});
-                    else
-                        group(k0, Count<0>{});
-                }
+                if (plain)
+                    all_turns(Count<1>{});
+                else
+                    all_turns(Count<0>{});
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             };
@@ -1476,7 +1475,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             // These warps write to the rings, or have it written, in the order of the tiles: they alone wait for every
             // phase of their places.  (A wait tells a phase from the one before it, not from the one before that.)
             const bool brings = (warp & 1) == 0;  // the team's half of new tokens' V tiles; the first team K tiles too
-            uint32_t k_used = 0, k_phase = 0, v_used = 0, v_phase = 0;  // places with copies, the phase that ends the last
+            // places with copies (bits 0 .. of K, 16 .. of V) and the phase that ends the last (8 .., 24 ..)
+            uint32_t copies = 0;
             auto keys = [&](int tile, int t) {
                 const int ki = tile % L::kK;
                 const uint32_t full = base + L::oKFull + 8 * ki;
@@ -1494,8 +1494,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 } else if (warp != kConvertWarp) {
                     if (lane == 0) bar_arrive(full);
                 } else {
-                    k_used |= 1u << ki;
-                    k_phase = (k_phase & ~(1u << ki)) | (uint32_t)(tile / L::kK & 1) << ki;
+                    copies = (copies & ~(0x100u << ki)) | 1u << ki | (uint32_t)(tile / L::kK & 1) << (8 + ki);
                     if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.kbox) * 128u);
                     __syncwarp();
                     if (lane < L::kHalves)
@@ -1523,8 +1522,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 } else if (have > 64 * team) {
                     // (the V warp hands it on)
                     if (brings) {
-                        v_phase = v_used >> vi & 1 ? v_phase ^ 1u << vi : v_phase;
-                        v_used |= 1u << vi;
+                        copies ^= (copies >> (16 + vi) & 1) << (24 + vi);
+                        copies |= 0x10000u << vi;
                         if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
                         __syncwarp();
                         if (lane < L::kHalves)
@@ -1611,12 +1610,15 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 }
                 return true;
             };
-            for (int seg = 0; ok && w.left > 0; w.next(A, S, plan, near), ++seg) {
+            for (int seg = 0; ok && w.left > 0; ++seg) {
                 if (L::kDirect) ok = split(seg);
                 for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
                     if (!L::kDirect) ok = keys(i, t);
                     if (ok) ok = values(i, t);
                 }
+                __syncwarp();
+                if (lane == 0) w.next(A, S, plan, near);
+                __syncwarp();
             }
             if (!ok && brings) {
                 // Leave no copy in flight.
@@ -1625,9 +1627,9 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {}
                 };
                 for (int j = 0; j < L::kK; ++j)
-                    if (k_used >> j & 1) drain(base + L::oKFull + 8 * j, k_phase >> j & 1);
+                    if (copies >> j & 1) drain(base + L::oKFull + 8 * j, copies >> (8 + j) & 1);
                 for (int j = 0; j < L::kV; ++j)
-                    if (v_used >> j & 1) drain(base + L::oVFull + 8 * j, v_phase >> j & 1);
+                    if (copies >> (16 + j) & 1) drain(base + L::oVFull + 8 * j, copies >> (24 + j) & 1);
             }
         } else {
             // ---- V tiles: rows past the end, and rows that are not finite. ----
