@@ -1441,32 +1441,42 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 const float* const all = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
                 char* const to = dst + (c >> 2) * next;
                 const bool plain = !BF16 && __all_sync(0xffffffffu, fits_half(all[lane & 7]));
-                uint4 x[turns];
-                const float4 four = reinterpret_cast<const float4*>(all)[team];
-                float f[4] = {four.x, four.y, four.z, four.w};  // of 16 keys each
+                // Two turns a pass, the next pass's codes on their way.  (All of them unrolled were 10 KB of instructions,
+                // which with the softmax's do not stay in the instruction cache: three quarters of the requests hit, and
+                // every warp waited: 64 requests 636 us.)
+                uint4 x[2];
+                float f[2];
+                auto load = [&](int u) {
 #pragma unroll
-                for (int u = 0; u < turns; ++u) x[u] = *reinterpret_cast<const uint4*>(src + u * (step * DP));
-                if (have < kTile) {  // codes of 0, and scales that are none of a key's
-#pragma unroll
-                    for (int u = 0; u < turns; ++u)
-                        if (64 * team + row0 + u * step >= have) x[u] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (64 * team + 16 * u >= have) f[u] = 0.0f;
-                }
-                auto all_turns = [&](auto plain_c) {
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = *reinterpret_cast<const uint4*>(src + (u + e) * (step * DP));
+                        f[e] = all[4 * team + (u + e) * step / 16];
+                        if (64 * team + row0 + (u + e) * step >= have) {
+                            x[e] = make_uint4(0, 0, 0, 0);
+                            f[e] = 0.0f;
+                        }
+                    }
+                };
+                auto passes = [&](auto plain_c) {
                     constexpr bool kPlain = decltype(plain_c)::value != 0;
+                    load(0);
+#pragma unroll 1
+                    for (int u = 0; u < turns; u += 2) {
+                        const uint4 y[2] = {x[0], x[1]};
+                        const float h[2] = {f[0], f[1]};
+                        if (u + 2 < turns) load(u + 2);
 #pragma unroll
-                    for (int u = 0; u < turns; ++u) {
-                        char* const row = to + u * (step * 128);
-                        *reinterpret_cast<uint4*>(row + at0) = widen<BF16, kPlain>(make_uint2(x[u].x, x[u].y), f[u * step / 16]);
-                        *reinterpret_cast<uint4*>(row + at1) = widen<BF16, kPlain>(make_uint2(x[u].z, x[u].w), f[u * step / 16]);
+                        for (int e = 0; e < 2; ++e) {
+                            char* const row = to + (u + e) * (step * 128);
+                            *reinterpret_cast<uint4*>(row + at0) = widen<BF16, kPlain>(make_uint2(y[e].x, y[e].y), h[e]);
+                            *reinterpret_cast<uint4*>(row + at1) = widen<BF16, kPlain>(make_uint2(y[e].z, y[e].w), h[e]);
+                        }
                     }
                 };
                 if (plain)
-                    all_turns(Count<1>{});
+                    passes(Count<1>{});
                 else
-                    all_turns(Count<0>{});
+                    passes(Count<0>{});
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             };
