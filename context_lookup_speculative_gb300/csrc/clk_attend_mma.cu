@@ -58,9 +58,11 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "clk.h"
 #include "clk_attend.h"
+#include "clk_attend_work.cuh"
 #include "clk_cache.h"
 #include "clk_eight.cuh"
 #include "clk_host.h"
@@ -69,281 +71,17 @@
 namespace clk {
 namespace {
 
-constexpr int kTile = 128;     // keys of a tile, rows of a row tile
-// 8 softmax, 2 copies, 1 products, 1 V tiles; with a cache in 8 bits 4 that convert its tiles
+// 8 softmax, 2 copies, 1 products, 1 V tiles; with a cache in 8 bits (E8: prompts; trees over one have a kernel of
+// their own) 4 that convert its tiles
 template <bool E8>
 constexpr int kWarps = E8 ? 16 : 12;
 template <bool E8>
 constexpr int kThreads = 32 * kWarps<E8>;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kValueWarp = 11, kConvertWarp = 12;
-constexpr int kNear = 4;            // requests whose data a CTA keeps
 
-struct Maps {
-    CUtensorMap q, k, v, kc, vc;
-};
-
-// How a call's rows are tiled.
-struct Shape {
-    int32_t tok;    // tokens of a row tile: 128 / group
-    int32_t block;  // tokens of an item: tok, or 2 tok for prompts
-    int32_t qbox, kbox, vbox;  // tokens of a box of q, rows of a box of new keys, of new values
-    int32_t ctas;
-    float log2_scale;  // scale * log2(e)
-    bool wide_out;     // rows of out are whole 32-byte sectors
-};
-
-// Scratch: the status of calls since it was zeroed, a flag per CTA (a count of
-// calls), row statistics and partial sums, two parts a CTA.
-struct Scratch {
-    int32_t* status;  // latched as a cache's; a prompt without a cache has no other place for it
-    uint32_t* flag;   // [ctas]
-    float2* ml;       // [ctas][2][rows]
-    float* sums;      // [ctas][2][DP / 4][rows][4]
-};
-
-__host__ __device__ inline int pad_dim(int dim) { return dim <= 64 ? 64 : 128; }
-
-constexpr size_t kStatusBytes = 128;
-
-__host__ __device__ inline size_t flag_bytes(int ctas) { return ((size_t)ctas * sizeof(uint32_t) + 127) / 128 * 128; }
-
-__host__ __device__ inline Scratch scratch_of(void* base, int ctas, int rows)
-{
-    Scratch s;
-    char* p = static_cast<char*>(base);
-    s.status = reinterpret_cast<int32_t*>(p);
-    p += kStatusBytes;
-    s.flag = reinterpret_cast<uint32_t*>(p);
-    p += flag_bytes(ctas);
-    s.ml = reinterpret_cast<float2*>(p);
-    p += (size_t)ctas * 2 * rows * sizeof(float2);
-    s.sums = reinterpret_cast<float*>(p);
-    return s;
-}
-
-// a / b for a >= 0, b > 0.  Small numbers go by a reciprocal that is off by
-// at most one, which is a fifth of the integer division's latency.
-__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b)
-{
-    if (a >= (1u << 22)) return a / b;
-    uint32_t q = (uint32_t)__fdividef((float)a, (float)b);
-    const int r = (int)(a - q * b);
-    q += r >= (int)b ? 1 : r < 0 ? -1 : 0;
-    return q;
-}
-
-__device__ __forceinline__ long long quotient(long long a, long long b)
-{
-    return ((a | b) >> 31) == 0 ? (long long)quotient((uint32_t)a, (uint32_t)b) : a / b;
-}
-
-// sum over i < n of floor((a i + b) / m), for m > 0 and a n + b < 2^32: the
-// lattice points under a line.  The known reduction, as Euclid's algorithm
-// goes: whole parts of the slope and of the start are summed at once, what is
-// left of the line is read with its axes changed.
-__device__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b)
-{
-    long long s = 0;
-    while (n > 0) {
-        if (a >= m) {
-            const uint32_t q = quotient(a, m);
-            s += ((long long)n * (n - 1) >> 1) * q;
-            a -= q * m;
-        }
-        if (b >= m) {
-            const uint32_t q = quotient(b, m);
-            s += (long long)n * q;
-            b -= q * m;
-        }
-        const uint32_t y = a * n + b;
-        if (y < m) break;
-        n = quotient(y, m);
-        b = y - n * m;
-        const uint32_t u = m;
-        m = a;
-        a = u;
-    }
-    return s;
-}
-
-// A request's tiles: per K/V head, `items` row tiles; item i has ctx_tiles
-// tiles of cached keys and new_tiles(i) of new ones.
-struct Reach {
-    int32_t ctx, rows, slot;
-    int32_t ctx_tiles, items;
-    int32_t base;
-};
-
-__device__ __forceinline__ Reach reach_of(const Request& r, const Shape& S)
-{
-    Reach x;
-    x.ctx = r.ctx;
-    x.rows = r.rows;
-    x.slot = r.slot;
-    x.base = (int32_t)r.base;  // at most 2^30 rows
-    x.ctx_tiles = (r.ctx + kTile - 1) / kTile;
-    x.items = (r.rows + S.block - 1) / S.block;
-    return x;
-}
-
-template <bool PROMPT>
-__device__ __forceinline__ int new_tiles(const Reach& x, const Shape& S, int item)
-{
-    if (!PROMPT) return 1;  // at most 64 new tokens
-    const int end = (item + 1) * S.block < x.rows ? (item + 1) * S.block : x.rows;
-    return (end - 1) / kTile + 1;
-}
-
-// What an item costs besides its tiles (its result, the next one's start),
-// in tiles: about 6,000 cycles beside 2,100 a tile with prompts and 4,300
-// beside 1,800 with trees, rows of 64.  Counting it balances short items
-// with long ones.  Measured without and with: 16 prompts of 500 to 1,500 tokens
-// (24/4 heads of 64) 141 and 117 us, the same behind prefixes of up to 8,192
-// (100 to 2,000 tokens) 561 and 460, 256 requests of 300 to 4,096 tokens and 13
-// nodes 128 and 117, one token over 2,048 rows (32/8 heads of 128) 13.7 and 13.1.
-template <bool PROMPT>
-constexpr int kExtra = PROMPT ? 4 : 3;
-
-// Items of at most so many tiles are not cut: joining parts takes 10,000
-// cycles and more.  They go to the CTA that holds their middle unit.
-// Measured on prompts without a limit, of 8 and of 16 tiles: one of 1,000
-// tokens (32/8 heads of 128) 34.9, 22.2, 22.1 us, one of 4,000 118, 118, 120;
-// 16 of 500 to 1,500 221, 209, 208, with 24/4 heads of 64 126, 123, 117.  256
-// requests of 64 to 512 tokens and 13 nodes (24/4 heads of 64): without 67.9,
-// of 2 tiles 68.3, of 4 62.2 us.
-template <bool PROMPT>
-constexpr int kWhole = PROMPT ? 16 : 4;
-
-// Units of the items before `item` of one K/V head.
-template <bool PROMPT>
-__device__ __forceinline__ long long units_before(const Reach& x, const Shape& S, int item)
-{
-    if (!PROMPT) return (long long)item * (x.ctx_tiles + 1 + kExtra<PROMPT>);
-    if (item <= 0) return 0;
-    const bool all = item >= x.items;
-    const int whole = all ? x.items - 1 : item;
-    long long n = (long long)item * (x.ctx_tiles + kExtra<PROMPT>) + whole + floor_sum(whole, kTile, S.block, S.block - 1);
-    if (all) n += (x.rows - 1) / kTile + 1;
-    return n;
-}
-
-template <bool PROMPT>
-__device__ __forceinline__ long long units_of(const Reach& x, const Shape& S)
-{
-    return x.items == 0 ? 0 : units_before<PROMPT>(x, S, x.items);
-}
-
-// `all` units in shares of q or q + 1: the first r CTAs have one more.
-struct Cuts {
-    long long q;
-    int r;
-    __device__ Cuts(long long all, int ctas)
-    {
-        q = ctas > 0 ? quotient(all, ctas) : 0;
-        r = (int)(all - q * ctas);
-    }
-    __device__ long long begin(int c) const { return q * c + (c < r ? c : r); }
-    // the CTA whose share holds unit g
-    __device__ int holder(long long g) const
-    {
-        const long long big = (q + 1) * r;
-        return (int)(g < big ? quotient(g, q + 1) : r + quotient(g - big, q));
-    }
-};
-
-// What a CTA knows after planning (in shared memory).
-struct Plan {
-    long long all, g0, g1;  // units in all, this CTA's share
-    int ctas;               // CTAs that have a share
-    int b, h, item, at;     // where the share begins: unit `at` of the item
-    uint32_t call;          // this CTA's flag before this call
-    long long began;        // when the CTA began, in its clocks
-};
-
-// An item whose tiles lie in several CTAs' shares.
-struct Cut {
-    Reach x;
-    int b, h, item, total;  // total: its tiles, 0 for none
-    long long begin;        // its first unit
-};
-
-// The CTA's way through its share, segment by segment (an item's tiles t0 ..
-// t1-1), the same in every warp.  The softmax warps keep theirs in shared
-// memory: their registers are full.
-template <bool PROMPT>
-struct Walk {
-    Reach x;
-    int b, h, item, t0, t1, total;
-    int left;  // units of the share from this segment's on; 0 at the end
-    int took;  // this segment's units
-
-    __device__ void start(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
-    {
-        left = (int)(P.g1 - P.g0);
-        took = 0;
-        b = P.b;
-        h = P.h;
-        item = P.item;
-        if (left == 0) return;
-        load(A, S, P, near);
-        cut(S, P.at);
-        if (t0 == t1) next(A, S, P, near);
-    }
-    __device__ void load(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
-    {
-        const int i = b - P.b;
-        x = i < kNear ? near[i] : reach_of(attend_request(A, b, false), S);
-    }
-    // From unit `at` of the item on, as far as the share goes.
-    __device__ void cut(const Shape& S, int at)
-    {
-        constexpr int extra = kExtra<PROMPT>;
-        total = x.ctx_tiles + new_tiles<PROMPT>(x, S, item);
-        took = extra + total - at < left ? extra + total - at : left;
-        if (total <= kWhole<PROMPT>) {
-            const int middle = (extra + total) / 2;
-            t0 = 0;
-            t1 = at <= middle && middle < at + took ? total : 0;
-        } else {
-            t0 = at > extra ? at - extra : 0;
-            t1 = at + took > extra ? at + took - extra : 0;
-        }
-    }
-    // The next segment that has tiles.
-    __device__ void next(const Attend& A, const Shape& S, const Plan& P, const Reach* near)
-    {
-        do {
-            left -= took;
-            if (left <= 0) {
-                left = 0;
-                return;
-            }
-            if (++item == x.items) {
-                item = 0;
-                if (++h == A.kv_heads) {
-                    h = 0;
-                    do {
-                        ++b;
-                        load(A, S, P, near);
-                    } while (x.items == 0);
-                }
-            }
-            cut(S, 0);
-        } while (t0 == t1);
-    }
-    // Tiles [t0, last(s)) of this segment are stream s's, with prompts.
-    __device__ int last(const Shape& S, int s) const
-    {
-        const int first = item * S.block + s * S.tok;
-        if (first >= x.rows) return t0;
-        const int end = first + S.tok < x.rows ? first + S.tok : x.rows;
-        const int n = x.ctx_tiles + (end - 1) / kTile + 1;
-        return n < t0 ? t0 : n < t1 ? n : t1;
-    }
-};
-
-template <int DP, bool BF16, bool PROMPT, bool E8>
+template <int DP, bool PROMPT, bool E8>
 struct Lay {
+    using K = typename std::conditional<PROMPT, Prompts, Trees>::type;
     static constexpr int kHalves = DP / 64;
     static constexpr int kHalf = kTile * 128;  // bytes of 64 columns of a tile
     static constexpr int kBytes = kHalves * kHalf;
@@ -351,202 +89,46 @@ struct Lay {
     // columns), so that the next scores are computed while this tile's are exponentiated; with rows of 128
     // the weights lie over the scores.
     static constexpr bool kApart = DP == 64;
-    // Trees multiply the cache's K as it is, by a Q in parts of 8 bits.
-    static constexpr bool kDirect = E8 && !PROMPT;
-    static constexpr int kParts = kDirect ? (BF16 ? 2 : 3) : 0;
     static constexpr int kPart = kTile * DP;                       // bytes of a tile of 8 bits
     static constexpr int kQ = PROMPT ? 2 : 1;                      // row tiles of an item
-    static constexpr int kQB = DP == 128 && (PROMPT || E8) ? 1 : 2;  // items whose Q is held
+    static constexpr int kQB = DP == 128 && PROMPT ? 1 : 2;        // items whose Q is held
     // K tiles in the ring
-    static constexpr int kK = kDirect ? (DP == 128 ? (BF16 ? 3 : 2) : 6) : E8 ? (DP == 128 ? 2 : 3) : DP == 128 ? (PROMPT ? 3 : 2) : (PROMPT ? 5 : 4);
-    static constexpr int kKBytes = kDirect ? kPart : kBytes;
+    static constexpr int kK = E8 ? (DP == 128 ? 2 : 3) : DP == 128 ? (PROMPT ? 3 : 2) : (PROMPT ? 5 : 4);
     // V tiles in the ring; with a cache in 8 bits halves of 64 keys, an even number: each half has places of its own
-    static constexpr int kV = E8 ? (DP == 128 || kDirect ? 4 : 6) : DP == 128 ? 2 : (PROMPT ? 5 : 4);
+    static constexpr int kV = E8 ? (DP == 128 ? 4 : 6) : DP == 128 ? 2 : (PROMPT ? 5 : 4);
     static constexpr int kVBytes = E8 ? kBytes / 2 : kBytes;
     // tiles as the cache holds them, to be converted
     static constexpr int kG = !E8 ? 0 : DP == 128 ? 2 : 6;
     static_assert(!E8 || kV % 2 == 0, "places of halves");
     static constexpr int kGs = kG > 0 ? kG : 1;
-    static constexpr int oParts = kQ * kQB * kBytes;
-    static constexpr int oK = oParts + kQB * kParts * kPart, oV = oK + kK * kKBytes, oG = oV + kV * kVBytes;
+    static constexpr int oK = kQ * kQB * kBytes, oV = oK + kK * kBytes, oG = oV + kV * kVBytes;
     // after the tiles
     static constexpr int oKFull = oG + kG * kPart, oKEmpty = oKFull + 8 * kK;
     static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
     static constexpr int oGFull = oVEmpty + 8 * kV, oGEmpty = oGFull + 8 * kG;
-    static constexpr int oPartsReady = oGEmpty + 8 * kG, oFactorRead = oPartsReady + 8 * kQB;
-    static constexpr int oQFull = oFactorRead + 8 * kQB, oQEmpty = oQFull + 8 * kQB;
+    static constexpr int oQFull = oGEmpty + 8 * kG, oQEmpty = oQFull + 8 * kQB;
     static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
     static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
     static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
     static constexpr int oScale = oBad + 16 * kV;                     // float[kG][8]: of blocks of 16 keys
-    // K's scales outlive its tile: the softmax warps read them.  A place is written again when the tile kScales before
-    // is weighed: the copy of a tile waits for the scores of the one kK before, which follow the weights of kK + 2.
-    static constexpr int kScales = kDirect ? 16 : 0;
-    static_assert(!kDirect || kScales >= kK + 2, "scales in use");
-    static constexpr int oKeyScale = oScale + 32 * kG;                // float[kScales][8]
-    static constexpr int oFactor = oKeyScale + 32 * kScales;          // float[kQB][128]: what a row of Q's parts is to be multiplied by
-    static constexpr int oNear = oFactor + (kDirect ? kQB * kTile * 4 : 0);  // Reach[kNear]
+    static constexpr int oNear = oScale + 32 * kG;                    // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
     static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: of items that end here, that begin here
     static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[8]
-    static constexpr int oStop = oWalk + (E8 ? 12 : 8) * (int)sizeof(Walk<PROMPT>), oTmem = oStop + 4;
+    static constexpr int oStop = oWalk + (E8 ? 12 : 8) * (int)sizeof(Walk<K>), oTmem = oStop + 4;
     static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;          // float2[2][128] for trees
     static constexpr int kTotal = oStat + (PROMPT ? 0 : 2 * kTile * 8);
     static_assert(kTotal <= 232448, "shared memory");
 };
 
-// A wait has run out: the call's results are not whole.
-__device__ __forceinline__ void gave_up(const Attend& A, const Scratch& W)
-{
-    latch(W.status, CLK_ECUDA, -1);
-    if (A.C.status != nullptr) latch(A.C.status, CLK_ECUDA, -1);
-}
-
-// Eight codes as elements of the products' type, times their scale: rounded once (exact for scales that are powers
-// of two in the type's range).  PLAIN: float16, and a scale that float16 holds.
-__device__ __forceinline__ bool fits_half(float scale) { return __half2float(__float2half_rn(scale)) == scale; }
-
-template <bool BF16, bool PLAIN>
-__device__ __forceinline__ uint4 widen(uint2 codes, float scale)
-{
-    uint32_t y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t h = half_of_e4m3((i < 2 ? codes.x : codes.y) >> 16 * (i & 1));
-        if (PLAIN) {
-            const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(scale));
-            y[i] = *reinterpret_cast<const uint32_t*>(&p);
-        } else {
-            const float2 f = halves(h), p = unpair(mul2(pair(__float_as_uint(f.x), __float_as_uint(f.y)),
-                                                        pair(__float_as_uint(scale), __float_as_uint(scale))));
-            y[i] = pack2<BF16>(p.x, p.y);
-        }
-    }
-    return make_uint4(y[0], y[1], y[2], y[3]);
-}
-
-template <int N>
-struct Count {
-    static constexpr int value = N;
-};
-
-// This CTA's share of an item whose tiles lie in several CTAs' shares.
-template <int DP, bool BF16, bool PROMPT, bool E8>
-__device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const Scratch& W, const Plan& plan, const Cuts& cuts,
-                                          const Cut& cut, volatile int* stop)
-{
-    constexpr int rows = PROMPT ? 2 * kTile : kTile, kThreads = clk::kThreads<E8>;
-    const int tid = threadIdx.x;
-    const long long tile0 = cut.begin + kExtra<PROMPT>;
-    const int c0 = cuts.holder(tile0), c1 = cuts.holder(tile0 + cut.total - 1), parts = c1 - c0 + 1;
-    auto part = [&](int c) { return 2 * (c0 + c) + (c == 0 ? 1 : 0); };
-    // All CTAs of the grid are resident, and none waits before it has raised its own flag.  Shares are equal but not
-    // equally long: a CTA waits, beyond the usual limit, for as long as its own share took.
-    for (int c = tid; c < parts; c += kThreads) {
-        uint32_t seen;
-        const long long t0 = clock64();
-        for (;;) {
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(W.flag + c0 + c) : "memory");
-            if (seen != plan.call || *stop != 0) break;
-            if (clock64() - t0 > kWaitClocks + (t0 - plan.began)) *stop = 1;
-        }
-    }
-    __syncthreads();
-    if (*stop != 0) {
-        if (tid == 0) gave_up(A, W);
-        return;
-    }
-    const int quads = A.dim / 4;
-    const int left = cut.x.rows - cut.item * S.block, tokens = left < S.block ? left : S.block;
-    const int used = tokens * A.group;   // rows of the item, tile after tile
-    const int full = S.tok * A.group;    // rows in use of a whole row tile
-    const int mine = (int)blockIdx.x - c0;
-    const int all = used * quads;
-    const int lo = (int)((long long)all * mine / parts), hi = (int)((long long)all * (mine + 1) / parts);
-    const float4* const sums = reinterpret_cast<const float4*>(W.sums);
-    const float cs = S.log2_scale;
-    // U elements of four columns a thread, F parts of each: eight loads in flight.
-    auto rows_of = [&](auto fc, auto uc) {
-        constexpr int F = decltype(fc)::value, U = decltype(uc)::value;
-        for (int i0 = lo + tid; i0 < hi; i0 += U * kThreads) {
-            float top[U], l[U];
-            float4 o[U];
-            int64_t at[U];
-            int row[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * kThreads < hi ? i0 + u * kThreads : i0;
-                const int q = (int)quotient((uint32_t)i, (uint32_t)used), r = i - q * used;
-                row[u] = r < full ? r : kTile + r - full;
-                at[u] = (int64_t)q * rows + row[u];
-                top[u] = -INFINITY;
-                l[u] = 0.0f;
-                o[u] = make_float4(0, 0, 0, 0);
-            }
-            // in the order of the parts
-            for (int c = 0; c < parts; c += F) {
-                float2 ml[U][F];
-                float4 v[U][F];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int e = 0; e < F; ++e) {
-                        // past the end the last part is read again, with no weight
-                        const int64_t p = part(c + e < parts ? c + e : parts - 1);
-                        ml[u][e] = __ldcg(W.ml + p * rows + row[u]);
-                        v[u][e] = __ldcg(sums + p * (DP / 4) * rows + at[u]);
-                    }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float to = top[u];
-#pragma unroll
-                    for (int e = 0; e < F; ++e) to = fmaxf(to, ml[u][e].x);
-                    const float f = top[u] == -INFINITY ? 0.0f : exp2_fast((top[u] - to) * cs);
-                    top[u] = to;
-                    l[u] *= f;
-                    o[u] = make_float4(o[u].x * f, o[u].y * f, o[u].z * f, o[u].w * f);
-#pragma unroll
-                    for (int e = 0; e < F; ++e) {
-                        // a part that saw nothing has no weight (and its reference is -inf)
-                        const bool use = c + e < parts && !(ml[u][e].x == -INFINITY && ml[u][e].y == 0.0f);
-                        const float g = exp2_fast((ml[u][e].x - to) * cs);
-                        l[u] += use ? ml[u][e].y * g : 0.0f;
-                        o[u].x += use ? v[u][e].x * g : 0.0f;
-                        o[u].y += use ? v[u][e].y * g : 0.0f;
-                        o[u].z += use ? v[u][e].z * g : 0.0f;
-                        o[u].w += use ? v[u][e].w * g : 0.0f;
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * kThreads;
-                if (i >= hi) break;
-                const int q = (int)quotient((uint32_t)i, (uint32_t)used), r = i - q * used;
-                const float inv = l[u] == 0.0f ? 0.0f : 1.0f / l[u];
-                const int rt = (int)quotient((uint32_t)r, (uint32_t)A.group);
-                const int tok = cut.item * S.block + rt, head = cut.h * A.group + r - rt * A.group;
-                const int64_t out_row = (PROMPT ? (int64_t)cut.x.base : (int64_t)cut.b * A.N) + tok;
-                uint2 y;
-                y.x = pack2<BF16>(o[u].x * inv, o[u].y * inv);
-                y.y = pack2<BF16>(o[u].z * inv, o[u].w * inv);
-                *reinterpret_cast<uint2*>(static_cast<char*>(A.out) + ((out_row * A.q_heads + head) * A.dim + 4 * q) * 2) = y;
-            }
-        }
-    };
-    if (parts <= 2)
-        rows_of(Count<2>{}, Count<4>{});
-    else
-        rows_of(Count<8>{}, Count<1>{});
-}
-
 template <int DP, bool BF16, bool PROMPT, bool E8>
 __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constant__ Maps M, const __grid_constant__ Attend A,
                                                             const __grid_constant__ Shape S, void* scratch)
 {
-    using L = Lay<DP, BF16, PROMPT, E8>;
-    constexpr int kThreads = clk::kThreads<E8>, kWarps = clk::kWarps<E8>;
+    using L = Lay<DP, PROMPT, E8>;
+    using K = typename L::K;
+    constexpr int kThreads = clk::kThreads<E8>;
     extern __shared__ __align__(1024) char sm[];
     // the shuffle tells the compiler that a warp has one role
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -569,7 +151,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char*>(&M) + lane * sizeof(CUtensorMap)) : "memory");
     } else if (tid == 32 * kValueWarp) {
         for (int i = 0; i < L::kK; ++i) {
-            bar_init(base + L::oKFull + 8 * i, L::kDirect ? 1 + 32 : E8 ? 4 : 1);
+            bar_init(base + L::oKFull + 8 * i, E8 ? 4 : 1);
             bar_init(base + L::oKEmpty + 8 * i, 1);
         }
         for (int i = 0; i < L::kV; ++i) {
@@ -582,10 +164,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             bar_init(base + L::oGEmpty + 8 * i, 4);
         }
         for (int i = 0; i < L::kQB; ++i) {
-            bar_init(base + L::oPartsReady + 8 * i, 4);
-            bar_init(base + L::oFactorRead + 8 * i, 8);
             bar_init(base + L::oQFull + 8 * i, 1);
-            bar_init(base + L::oQEmpty + 8 * i, L::kDirect ? 1 + 4 : 1);  // the products', and the warps' that split it
+            bar_init(base + L::oQEmpty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(base + L::oSFull + 8 * i, 1);
@@ -599,103 +179,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 
-    // ---- Plan: all requests' tiles, this CTA's share, where it begins. ----
-    {
-        long long* const sums = reinterpret_cast<long long*>(sm);  // the rings are not in use yet
-        const bool once = A.B <= kThreads;  // the batch is seen in one pass
-        long long all = 0;
-        int ctas = 0;
-        Cuts cuts(0, 0);
-        Reach x{};
-        for (int pass = 0;; ++pass) {
-            long long before = 0;
-            for (int at = 0; at < A.B; at += kThreads) {
-                const int b = at + tid;
-                long long each = 0;  // units of one K/V head
-                if (b < A.B) {
-                    x = reach_of(attend_request(A, b, pass == 0 && blockIdx.x == 0), S);
-                    each = units_of<PROMPT>(x, S);
-                }
-                const long long u = each * A.kv_heads;
-                long long y = u;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const long long z = __shfl_up_sync(0xffffffffu, y, d);
-                    if (lane >= d) y += z;
-                }
-                if (lane == 31) sums[warp] = y;
-                __syncthreads();
-                long long mine = before + y - u;
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w < warp) mine += sums[w];
-                    before += sums[w];
-                }
-                if (once) all = before;
-                if (once || pass == 1) {
-                    // The warp that has the share's first request finds the place in it.
-                    if (at == 0) {
-                        ctas = all < S.ctas ? (int)all : S.ctas;
-                        cuts = Cuts(all, ctas);
-                    }
-                    const long long g0 = (int)blockIdx.x < ctas ? cuts.begin(blockIdx.x) : all;
-                    const unsigned who = __ballot_sync(0xffffffffu, u > 0 && mine <= g0 && g0 < mine + u);
-                    if (who != 0) {
-                        const int src = __ffs((int)who) - 1;
-                        Reach z;
-                        z.rows = __shfl_sync(0xffffffffu, x.rows, src);
-                        z.ctx_tiles = __shfl_sync(0xffffffffu, x.ctx_tiles, src);
-                        z.items = __shfl_sync(0xffffffffu, x.items, src);
-                        const long long off = __shfl_sync(0xffffffffu, g0 - mine, src), per = __shfl_sync(0xffffffffu, each, src);
-                        const int h = (int)quotient(off, per);
-                        const long long o = off - h * per;
-                        // the last item with units_before <= o, and those units
-                        int lo = 0;
-                        long long below = 0;
-                        if (!PROMPT) {
-                            lo = (int)quotient(o, z.ctx_tiles + 1 + kExtra<PROMPT>);
-                            below = units_before<PROMPT>(z, S, lo);
-                        }
-                        for (int span = PROMPT ? z.items : 1; span > 1;) {  // 32 ways at a time
-                            const int step = (span + 31) / 32, end = lo + span;
-                            const long long n = lane * step < span ? units_before<PROMPT>(z, S, lo + lane * step) : o + 1;
-                            const int last = __popc(__ballot_sync(0xffffffffu, n <= o)) - 1;
-                            below = __shfl_sync(0xffffffffu, n, last);
-                            lo += last * step;
-                            span = lo + step < end ? step : end - lo;
-                        }
-                        if (lane == 0) {
-                            plan.b = at + 32 * warp + src;
-                            plan.h = h;
-                            plan.item = lo;
-                            plan.at = (int)(o - below);
-                        }
-                    }
-                }
-                __syncthreads();
-            }
-            if (pass == 0) all = before;
-            if (once || pass == 1) break;
-        }
-        const bool busy = (int)blockIdx.x < ctas;
-        if (tid == 0) {
-            plan.all = all;
-            plan.ctas = ctas;
-            plan.g0 = busy ? cuts.begin(blockIdx.x) : all;
-            plan.g1 = busy ? cuts.begin(blockIdx.x + 1) : all;
-            plan.call = call;
-            plan.began = began;
-            *stop = 0;
-            cut[0].total = cut[1].total = 0;
-        }
-        if (busy) {
-            if (once) {
-                const int i = tid - plan.b;
-                if (i >= 0 && i < kNear) near[i] = x;
-            } else if (tid < kNear && plan.b + tid < A.B) {
-                near[tid] = reach_of(attend_request(A, plan.b + tid, false), S);
-            }
-        }
-    }
+    make_plan<K, kThreads>(A, S, reinterpret_cast<long long*>(sm), plan, near, cut, stop, call, began);  // the rings are not in use yet
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the planning scratch lies where tiles go
     tmem_before();
     __syncthreads();
@@ -723,9 +207,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
         constexpr float far_off = 256.0f;
         uint32_t sp = 0, od = 0;
         int gi = 0;
-        int gk = 0, segment = 0;  // with Q in parts: cached tiles before this segment, segments
         bool ok = true;
-        Walk<PROMPT>& w = reinterpret_cast<Walk<PROMPT>*>(sm + L::oWalk)[warp];
+        Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[warp];
         if (lane == 0) w.start(A, S, plan, near);
         __syncwarp();
         while (ok && w.left > 0) {
@@ -740,10 +223,6 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 seen = (unsigned long long)A.mask[(int64_t)w.b * A.N + token];
                 if (w.x.rows < 64) seen &= (1ull << w.x.rows) - 1;
             }
-            // A warp without rows goes along without its share of the work (its rows of tensor memory are its own).
-            const bool idle = E8 && !__any_sync(0xffffffffu, real);
-            float factor = 0.0f;  // of this row's scores with the cache
-            bool has_factor = false;
             float ref = -INFINITY, sum = 0.0f;
             bool settled = false;  // every row has a reference, and none is far off
             bool far = false;      // some row's is far off
@@ -758,37 +237,11 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 if (!warp_wait(base + L::oSFull + 8 * s, sp, stop)) return false;
                 sp ^= 1;
                 tmem_after();
-                if (!idle) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_load(tS + 32 * c, x + 32 * c);
-                    tmem_load_wait();
+                for (int c = 0; c < 4; ++c) tmem_load(tS + 32 * c, x + 32 * c);
+                tmem_load_wait();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_loaded(x + 32 * c);
-                }
-                if (L::kDirect && t < ctx_tiles) {
-                    if (!has_factor) {
-                        const int qi = segment % L::kQB;
-                        factor = reinterpret_cast<const float*>(sm + L::oFactor)[qi * kTile + row];
-                        has_factor = true;
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(base + L::oFactorRead + 8 * qi);
-                    }
-                    if (!idle) {
-                        const float4* const ks = reinterpret_cast<const float4*>(sm + L::oKeyScale) + 2 * ((gk + t - t0) % (L::kDirect ? L::kScales : 1));
-                        const float4 a = ks[0], b = ks[1];
-                        const float k[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t f = __float_as_uint(factor * k[i]);
-#pragma unroll
-                            for (int c = 16 * i; c < 16 * i + 16; c += 2) {
-                                const float2 y = unpair(mul2(pair(x[c], x[c + 1]), pair(f, f)));
-                                x[c] = __float_as_uint(y.x);
-                                x[c + 1] = __float_as_uint(y.y);
-                            }
-                        }
-                    }
-                }
+                for (int c = 0; c < 4; ++c) tmem_loaded(x + 32 * c);
                 if (L::kApart) {
                     tmem_before();
                     __syncwarp();
@@ -797,8 +250,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 // Hidden keys: a limit for most tiles, a mask for a tree's.
                 cached = t < ctx_tiles;
                 n0 = (t - ctx_tiles) * kTile;
-                if (idle) {
-                } else if (cached || PROMPT) {
+                if (cached || PROMPT) {
                     const int most = cached ? ctx - t * kTile : n0 + kTile - 1 > first ? token - n0 + 1 : kTile;
                     if (!cached ? n0 + kTile - 1 > first : most < kTile) {
 #pragma unroll
@@ -897,14 +349,10 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
                     // Rows of V that were not finite: NaN for those who see them.
                     const int i = gi + (PROMPT ? j : 2 * j + s), at = E8 ? 2 * i : i, vi = at % L::kV;
-                    // (The place's phase before this one has ended: it was of the tile two before, whose product went before
-                    // these scores or has been waited for.)
                     if (!warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop)) return false;
                     const int vj = E8 ? (at + 1) % L::kV : vi;
-                    if (E8 && !L::kDirect && !warp_wait(base + L::oVReady + 8 * vj, (uint32_t)((at + 1) / L::kV & 1), stop)) return false;
-                    // (a tree's tokens are the first 64 keys)
-                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], L::kDirect ? 0 : bad[4 * vj + (E8 ? 0 : 2)],
-                                             L::kDirect ? 0 : bad[4 * vj + (E8 ? 1 : 3)]};
+                    if (E8 && !warp_wait(base + L::oVReady + 8 * vj, (uint32_t)((at + 1) / L::kV & 1), stop)) return false;
+                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], bad[4 * vj + (E8 ? 0 : 2)], bad[4 * vj + (E8 ? 1 : 3)]};
                     if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
                         bool hit = false;
 #pragma unroll
@@ -932,13 +380,6 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             auto tiles = [&]() -> bool {
                 for (; j < mine; ++j) {
                     if (!(ok = fetch(j))) return false;
-                    if (idle) {
-                        tmem_before();
-                        __syncwarp();
-                        if (!L::kApart && lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
-                        if (lane == 0) bar_arrive(base + L::oPReady + 8 * s);
-                        continue;
-                    }
                     // Where the weights lie apart from the scores, the reference is not compared with every tile's
                     // maximum: the sum of the tile's weights shows when one has grown too large (over 2^15), and the tile
                     // is done again.  That spares the maximum's 64 instructions in nearly all tiles; a row's first tile
@@ -972,7 +413,6 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 }
             }
             if (!ok) break;
-            if (L::kDirect && !has_factor && lane == 0) bar_arrive(base + L::oFactorRead + 8 * (segment % L::kQB));
             if (mine > 0) {
                 if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
                 od ^= 1;
@@ -983,7 +423,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             if (!whole && tid == 0) {
                 // an item may fill the share: its cuts at both ends are one join
                 const long long end = plan.g1 - w.left + w.took;
-                cut[w.t0 > 0 ? 0 : 1] = Cut{w.x, w.b, w.h, w.item, w.total, end - w.t1 - kExtra<PROMPT>};
+                cut[w.t0 > 0 ? 0 : 1] = Cut{w.x, w.b, w.h, w.item, w.total, end - w.t1 - K::extra};
             }
             // the part that begins an item is the CTA's second, so that it never meets the one that ends an item
             const int slot = 2 * (int)blockIdx.x + (w.t0 > 0 ? 0 : 1);
@@ -1069,15 +509,13 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 if (!(ok = warp_wait(base + L::oStatReady, 1, stop))) break;
             }
             gi += len;
-            ++segment;
-            gk += ctx_tiles > t0 ? (ctx_tiles < t0 + len ? ctx_tiles - t0 : len) : 0;
             __syncwarp();
             if (lane == 0) w.next(A, S, plan, near);
             __syncwarp();
         }
     } else {
         // (the converting warps keep their way through the share in shared memory too)
-        Walk<PROMPT> w;
+        Walk<K> w;
         if (!E8 || warp < kConvertWarp) w.start(A, S, plan, near);
         if (!E8)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -1092,9 +530,9 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             constexpr bool kApartKV = !PROMPT || E8;
             const bool brings_k = !kApartKV || odd == 0, brings_v = !kApartKV || odd == 1;
             auto my = [&](int tile) { return kApartKV || (tile & 1) == odd; };
-            // With a cache in 8 bits: tiles to be converted so far, cached tiles before this segment, and places in use, with
-            // the phase that ends the last copy to each.
-            int g = 0, g0 = 0;
+            // With a cache in 8 bits: tiles to be converted so far, and places in use, with the phase that ends the last
+            // copy to each.
+            int g = 0;
             uint32_t g_used = 0, g_phase = 0;
             int i = 0, seg = 0, nk = 0, nv = 0, nq = 0;  // n*: one past the last tile or item asked for
             bool ok = (base & 1023) == 0;  // the swizzle's period
@@ -1116,7 +554,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 int at = w.t0 * pages & ~31, now = batch(at), then = batch(at + 32);
                 const int z = PROMPT ? 0 : w.b, row0 = PROMPT ? w.x.base : 0;
                 // the first K goes out before the first V
-                if (!PROMPT && !E8 && odd == 1 && seg == 0 && !(ok = warp_wait(base + L::oQFull, 0, stop))) break;
+                if (!PROMPT && odd == 1 && seg == 0 && !(ok = warp_wait(base + L::oQFull, 0, stop))) break;
                 if (odd == 0) {
                     const int qi = seg % L::kQB;
                     const uint32_t qb = base + L::oQFull + 8 * qi;
@@ -1156,27 +594,10 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                         }
                         copies_arrive(bar);
                     };
-                    if (L::kDirect && odd == 0) {
-                        const int ki = i % L::kK;
-                        const uint32_t bar = base + L::oKFull + 8 * ki, dst = ks + ki * L::kKBytes;
-                        if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
-                        nk = i + 1;
-                        if (lane == 0) bar_expect(bar, cached ? (uint32_t)(boxes << A.C.shift) * DP : (uint32_t)(L::kHalves * S.kbox) * 128u);
-                        __syncwarp();
-                        if (cached) {
-                            if (page >= 0) copy_box(dst + (lane << A.C.shift) * DP, &M.kc, 0, 0, w.h, page, bar);
-                            bring_scales(A.ks, base + L::oKeyScale + 32 * ((g0 + t - w.t0) % (L::kDirect ? L::kScales : 1)), bar);
-                        } else {
-                            // (at most 64 rows of 64 columns a half)
-                            if (lane < L::kHalves) copy_box(dst + lane * (L::kHalf / 2), &M.k, 64 * lane, w.h, n0, z, bar);
-                            copies_arrive(bar);
-                        }
-                        continue;
-                    }
                     // Tiles to be converted, K before V.  One warp brings them all: it sees every phase of their places.
-                    if (E8 && cached && odd == (L::kDirect ? 1 : 0)) {
+                    if (E8 && cached && odd == 0) {
 #pragma unroll 1
-                        for (int v = L::kDirect ? 1 : 0; ok && v < 2; ++v, ++g) {
+                        for (int v = 0; ok && v < 2; ++v, ++g) {
                             const int gi = g % L::kGs;
                             const uint32_t bar = base + L::oGFull + 8 * gi;
                             if (!(ok = warp_wait(base + L::oGEmpty + 8 * gi, (uint32_t)(g / L::kGs & 1) ^ 1, stop))) break;
@@ -1214,10 +635,6 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                         bring(base + L::oVFull + 8 * vi, vs + vi * L::kBytes, &M.vc, &M.v);
                     }
                 }
-                if (E8) {
-                    const int run = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0;
-                    g0 += run > 0 ? run : 0;
-                }
             }
             if (!ok) {
                 // Leave no copy in flight.
@@ -1245,7 +662,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
                 uint32_t ps[2] = {0, 0}, fs[2] = {1, 1};  // phases of PReady and SFree
                 int seg = 0, qi = 0;
-                uint32_t qp = 0, pr = 0;  // phases of QFull, and of each PartsReady
+                uint32_t qp = 0;
                 bool ok = true;
                 // This warp's instructions bound the rate at which short products follow one another: ring places
                 // and phases are counted along, and a tile is waited for once for both streams.
@@ -1262,11 +679,6 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     __syncwarp();
                 };
                 // descriptors count in 16 bytes
-                // Q's parts and the cache's K: 8 bits, 32 elements a product, rows of 128 or 64 bytes
-                constexpr uint32_t kind_8 = (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
-                constexpr uint32_t kind_n = types | ((64 >> 3) << 17);  // 64 new keys
-                const uint64_t p0 = DP == 128 ? operand(base + L::oParts, 16) : operand_64(base + L::oParts);
-                const uint64_t c0 = DP == 128 ? operand(ks, 16) : operand_64(ks);
                 const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, E8 ? L::kHalf / 2 : L::kHalf);
                 auto wait_k = [&] { return warp_wait(base + L::oKFull + 8 * ki, kp, stop); };
                 // (with a cache in 8 bits halves of V are waited for as they are used)
@@ -1279,33 +691,13 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     }
                 };
                 // Stream s's scores with K tile ki.
-                auto scores = [&](int s, bool cached) {
+                auto scores = [&](int s) {
                     if (L::kApart) {
                         if (!warp_wait(base + L::oSFree + 8 * s, fs[s], stop)) return false;
                         fs[s] ^= 1;
                     }
                     tmem_after();
-                    const uint64_t q = q0 + (qi * L::kQ + (PROMPT ? s : 0)) * (L::kBytes / 16), k = k0 + ki * (L::kKBytes / 16);
-                    if (L::kDirect) {
-                        const uint64_t p = p0 + qi * L::kParts * (L::kPart / 16), c = c0 + ki * (L::kKBytes / 16);
-                        if (elect()) {
-                            if (cached) {
-#pragma unroll
-                                for (int e = 0; e < L::kParts * (DP / 32); ++e) {
-                                    const int part = e / (DP / 32), at = e % (DP / 32) * 2;
-                                    mma_ss8(tm + 128 * s, p + part * (L::kPart / 16) + at, c + at, kind_8, e > 0);
-                                }
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < DP / 16; ++e)
-                                    mma_ss(tm + 128 * s, q + (e / 4) * (L::kHalf / 16) + (e % 4) * 2, k + (e / 4) * (L::kHalf / 32) + (e % 4) * 2,
-                                           kind_n, e > 0);
-                            }
-                            mma_commit(base + L::oSFull + 8 * s);
-                        }
-                        __syncwarp();
-                        return true;
-                    }
+                    const uint64_t q = q0 + (qi * L::kQ + (PROMPT ? s : 0)) * (L::kBytes / 16), k = k0 + ki * (L::kBytes / 16);
                     if (elect()) {
 #pragma unroll
                         for (int e = 0; e < DP / 16; ++e) {
@@ -1347,16 +739,12 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     const int len = same(w.left > 0 ? w.t1 - w.t0 : 0);
                     if (len == 0) break;
                     if (!(ok = warp_wait(base + L::oQFull + 8 * qi, qp, stop))) break;
-                    if (L::kDirect && same(w.t0 < w.x.ctx_tiles)) {
-                        if (!(ok = warp_wait(base + L::oPartsReady + 8 * qi, pr >> qi & 1, stop))) break;
-                        pr ^= 1u << qi;
-                    }
                     if (PROMPT) {
                         const int n[2] = {same(w.last(S, 0) - w.t0), same(w.last(S, 1) - w.t0)};
                         if (!(ok = wait_k())) break;
 #pragma unroll
                         for (int s = 0; s < 2; ++s)
-                            if (ok && n[s] > 0) ok = scores(s, false);
+                            if (ok && n[s] > 0) ok = scores(s);
                         if (!ok) break;
                         done(base + L::oKEmpty + 8 * ki);
                         step(ki, kp, L::kK);
@@ -1369,14 +757,14 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
                                 if (!ok) continue;
-                                if (L::kApart && j + 1 < n[s]) ok = scores(s, false);
+                                if (L::kApart && j + 1 < n[s]) ok = scores(s);
                                 if (ok && j < n[s]) {
                                     ok = values(s, j > 0);
                                     if (ok && (L::kApart || j + 1 == n[s])) done(base + L::oODone + 8 * s);
                                 }
                                 if (!L::kApart && ok && more) {
                                     if (s == 0) ok = wait_k();
-                                    if (ok && j + 1 < n[s]) ok = scores(s, false);
+                                    if (ok && j + 1 < n[s]) ok = scores(s);
                                 }
                             }
                             if (!ok) break;
@@ -1390,7 +778,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     } else {
                         auto ahead = [&](int j) {
                             if (j >= len) return true;
-                            if (!wait_k() || !scores(j & 1, w.t0 + j < w.x.ctx_tiles)) return false;
+                            if (!wait_k() || !scores(j & 1)) return false;
                             done(base + L::oKEmpty + 8 * ki);
                             step(ki, kp, L::kK);
                             if (j + 1 == len) done(base + L::oQEmpty + 8 * qi);
@@ -1417,9 +805,9 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             }
             __syncwarp();
         } else if (E8 && warp >= kConvertWarp) {
-            // ---- Tiles of the cache: to 16 bits, times their scales.  Trees: V alone, and Q in parts of 8 bits. ----
+            // ---- Tiles of the cache: to 16 bits, times their scales. ----
             const int me = tid - 32 * kConvertWarp;  // 0 .. 127
-            Walk<PROMPT>& w = reinterpret_cast<Walk<PROMPT>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
+            Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
             if (lane == 0) w.start(A, S, plan, near);
             __syncwarp();
             // Two warps take a tile's first 64 keys, two the others.  A thread takes 16 elements at the same place of
@@ -1495,7 +883,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
                 if (!warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(tile / L::kK & 1) ^ 1, stop)) return false;
                 if (cached) {
-                    convert(gi, sm + L::oK + ki * L::kKBytes + team * (64 * 128), L::kHalf, kTile);
+                    convert(gi, sm + L::oK + ki * L::kBytes + team * (64 * 128), L::kHalf, kTile);
                     if (lane == 0) {
                         bar_arrive(full);
                         bar_arrive(base + L::oGEmpty + 8 * gi);
@@ -1508,7 +896,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.kbox) * 128u);
                     __syncwarp();
                     if (lane < L::kHalves)
-                        copy_box(ks + ki * L::kKBytes + lane * L::kHalf, &M.k, 64 * lane, w.h,
+                        copy_box(ks + ki * L::kBytes + lane * L::kHalf, &M.k, 64 * lane, w.h,
                                  (PROMPT ? w.x.base : 0) + (t - w.x.ctx_tiles) * kTile, PROMPT ? 0 : w.b, full);
                 }
                 return true;
@@ -1550,82 +938,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 }
                 return true;
             };
-            // Row `me` of the item's Q in parts of 8 bits: q = factor (p0 + p1 (+ p2)), each part the rounding of what
-            // the parts before it leave, so that together they hold 9 (14) bits of an element, or 2^-19 of the row's
-            // largest where that is more: bfloat16 has 8, float16 11.  A row that is not finite gets the factor NaN.
-            auto split = [&](int seg) {
-                const int qi = seg % L::kQB;
-                if (!warp_wait(base + L::oQFull + 8 * qi, (uint32_t)(seg / L::kQB & 1), stop)) return false;
-                if (!warp_wait(base + L::oFactorRead + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop)) return false;
-                // (No phase of the two is left out, and none passes by: Q's place is free once these warps have been here.)
-                if (w.t0 >= w.x.ctx_tiles) {
-                    if (lane == 0) bar_arrive(base + L::oQEmpty + 8 * qi);
-                    return true;
-                }
-                const char* const raw = sm + qi * L::kBytes + me * 128;
-                auto load = [&](int i, float* f) {  // elements 8 i .. 8 i + 7
-                    const uint4 v = *reinterpret_cast<const uint4*>(raw + (i >> 3) * L::kHalf + ((i & 7) ^ (me & 7)) * 16);
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = BF16 ? make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)) : halves(u[e]);
-                        f[2 * e] = y.x;
-                        f[2 * e + 1] = y.y;
-                    }
-                };
-                float top = 0.0f;
-                bool finite = true;
-#pragma unroll 4
-                for (int i = 0; i < DP / 8; ++i) {
-                    float f[8];
-                    load(i, f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        top = fmaxf(top, fabsf(f[e]));
-                        finite = finite && fabsf(f[e]) <= 3.4028234e38f;
-                    }
-                }
-                const float scale = scale_for(finite ? top : 0.0f), inv = 1.0f / scale;
-                char* const parts = sm + L::oParts + qi * L::kParts * L::kPart + me * DP;
-#pragma unroll 1
-                for (int i = 0; i < DP / 16; ++i) {
-                    float f[16];
-                    load(2 * i, f);
-                    load(2 * i + 1, f + 8);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = finite ? f[e] * inv : 0.0f;
-#pragma unroll
-                    for (int part = 0; part < L::kParts; ++part) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            y[e] = to_e4m3(f[4 * e], f[4 * e + 1]) | to_e4m3(f[4 * e + 2], f[4 * e + 3]) << 16;
-                            if (part + 1 < L::kParts) {
-                                float h[4];
-                                from_e4m3x4(y[e], h);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) f[4 * e + k] -= h[k];
-                            }
-                        }
-                        const int at = DP == 128 ? i ^ (me & 7) : i ^ (me >> 1 & 3);
-                        *reinterpret_cast<uint4*>(parts + part * L::kPart + 16 * at) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                }
-                reinterpret_cast<float*>(sm + L::oFactor)[qi * kTile + me] = finite ? scale : NAN;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(base + L::oPartsReady + 8 * qi);
-                    bar_arrive(base + L::oQEmpty + 8 * qi);
-                }
-                return true;
-            };
-            for (int seg = 0; ok && w.left > 0; ++seg) {
-                if (L::kDirect) ok = split(seg);
-                for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
-                    if (!L::kDirect) ok = keys(i, t);
-                    if (ok) ok = values(i, t);
-                }
+            while (ok && w.left > 0) {
+                for (int t = w.t0; ok && t < w.t1; ++t, ++i) ok = keys(i, t) && values(i, t);
                 __syncwarp();
                 if (lane == 0) w.next(A, S, plan, near);
                 __syncwarp();
@@ -1769,56 +1083,16 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
     const Cuts cuts(plan.all, plan.ctas);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i)
-        if (cut[i].total > 0) join_item<DP, BF16, PROMPT, E8>(A, S, W, plan, cuts, cut[i], stop);
+        if (cut[i].total > 0) join_item<DP, BF16, K, kThreads>(A, S, W, plan, cuts, cut[i], stop);
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encoder()
-{
-    static std::atomic<void*> found{nullptr};
-    void* p = found.load(std::memory_order_acquire);
-    if (p == nullptr) {
-        cudaDriverEntryPointQueryResult st;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
-            st != cudaDriverEntryPointSuccess)
-            return nullptr;
-        found.store(p, std::memory_order_release);
-    }
-    return reinterpret_cast<EncodeFn>(p);
-}
-
-// A map over [n3][n2][n1][dim] elements with the given strides (in
-// elements), copied in boxes of b0 x b1 x b2 (x 1).
-bool encode(EncodeFn f, CUtensorMap* m, int32_t dtype, const void* base, int64_t dim, const int64_t n[3], const int64_t st[3],
-            int b0, int b1, int b2, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
-{
-    const cuuint64_t es = dtype == CLK_DTYPE_E4M3 ? 1 : 2;
-    const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)n[0], (cuuint64_t)n[1], (cuuint64_t)n[2]};
-    cuuint64_t strides[3];
-    // the stride of an axis of one is not used; it still has to be a valid one
-    for (int i = 0; i < 3; ++i) strides[i] = n[i] > 1 ? (cuuint64_t)st[i] * es : 256;
-    const cuuint32_t box[4] = {(cuuint32_t)b0, (cuuint32_t)b1, (cuuint32_t)b2, 1}, one[4] = {1, 1, 1, 1};
-    const CUtensorMapDataType type = es == 1                    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : dtype == CLK_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return f(m, type, 4, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A stride (in elements, so many to 16 bytes) that a tensor map can take, for an axis of n.
-bool map_stride(int64_t st, int64_t n, int per = 8) { return n <= 1 || (st > 0 && st % per == 0 && st < ((int64_t)1 << 38)); }
-
 template <int DP, bool BF16, bool PROMPT, bool E8>
 int launch_mma(const Attend& A, const Shape& S, const Maps& M, void* scratch, cudaStream_t s)
 {
-    using L = Lay<DP, BF16, PROMPT, E8>;
+    using L = Lay<DP, PROMPT, E8>;
     static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CLK_ECUDA;
@@ -1913,21 +1187,15 @@ int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)
         M.kc = M.vc = M.k;  // not read: no request has cached rows
     }
     if (!ok) return CLK_EINVAL;
-#define CLK_GO(D, T, P) return eight ? launch_mma<D, T, P, true>(A, S, M, scratch, s) : launch_mma<D, T, P, false>(A, S, M, scratch, s)
-    if (prompt) {
-        if (wide) {
-            if (bf) CLK_GO(128, true, true);
-            CLK_GO(128, false, true);
-        }
-        if (bf) CLK_GO(64, true, true);
-        CLK_GO(64, false, true);
-    }
+    if (eight && !prompt) return attend_tree8_launch(A, S, M, scratch, s);
+#define CLK_GO(D, T) return eight ? launch_mma<D, T, true, true>(A, S, M, scratch, s) : prompt ? launch_mma<D, T, true, false>(A, S, M, scratch, s) \
+                                                                                             : launch_mma<D, T, false, false>(A, S, M, scratch, s)
     if (wide) {
-        if (bf) CLK_GO(128, true, false);
-        CLK_GO(128, false, false);
+        if (bf) CLK_GO(128, true);
+        CLK_GO(128, false);
     }
-    if (bf) CLK_GO(64, true, false);
-    CLK_GO(64, false, false);
+    if (bf) CLK_GO(64, true);
+    CLK_GO(64, false);
 #undef CLK_GO
 }
 

@@ -1,0 +1,919 @@
+// Attention of drafted trees over a paged cache in 8 bits on the tensor cores
+// (sm_103a).
+//
+// Items, shares and joins are those of clk_attend_work.cuh, rows and streams
+// those of the kernel over 16 bits (clk_attend_mma.cu): rows are (token, head
+// of the group) pairs, and two groups of four softmax warps take alternate
+// tiles of 128 keys.
+//
+// K goes to the tensor cores as the cache holds it: scores are the sum of
+// products of 8 bits with Q in two parts (bfloat16) or three (float16), each
+// the rounding to 8 bits of what the parts before it leave of the row over its
+// own power of two.  Such products are exact and are summed in float32.  A
+// block's scale and the row's power of two multiply the scores in the softmax.
+// V is brought to 16 bits by eight warps, times its scales: weights are too
+// far apart for parts of 8 bits.  New tokens' K and V stay in their own type.
+//
+// What bounds it: beside a tile's 32 KB from DRAM (rows of 128) shared memory
+// passes them in, once more to those who convert V and 32 KB back, 32 KB to the
+// products with P and 64 KB (96 KB) to those with Q's parts: 176 KB (208 KB),
+// 1,375 (1,625) cycles at 128 bytes a cycle, where DRAM needs 1,400.
+//
+// The code of all roles has to stay in the instruction cache, which the
+// unrolled loops of the 16-bit kernel together with a conversion did not:
+// three quarters of the fetches hit and everything waited.  So a softmax thread
+// goes through its row by 32 columns at a time, twice (maximum, weights), in
+// loops, with which all threads fit 96 registers.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "clk.h"
+#include "clk_attend.h"
+#include "clk_attend_work.cuh"
+#include "clk_cache.h"
+#include "clk_eight.cuh"
+#include "clk_host.h"
+#include "clk_mma.cuh"
+
+namespace clk {
+namespace {
+
+// 8 softmax, 2 copies, 1 products, 1 new V tiles, 8 that convert
+constexpr int kWarps = 20, kThreads = 32 * kWarps;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kValueWarp = 11, kConvertWarp = 12;
+
+template <int DP, bool BF16>
+struct Lay {
+    static constexpr int kHalves = DP / 64;
+    static constexpr int kHalf = kTile * 128;  // bytes of 64 columns of a tile of 16 bits
+    static constexpr int kBytes = kHalves * kHalf;
+    static constexpr int kPart = kTile * DP;   // bytes of a tile of 8 bits
+    // Rows of 64 leave room in tensor memory for weights beside the scores; with rows of 128 they lie over them.
+    static constexpr bool kApart = DP == 64;
+    static constexpr int kParts = BF16 ? 2 : 3;            // of Q
+    static constexpr int kQB = DP == 128 ? 1 : 2;          // items whose Q is held
+    static constexpr int kK = DP == 128 ? (BF16 ? 3 : 2) : 6;  // K tiles in the ring (8 bits, or 64 new tokens)
+    static constexpr int kV = 4;                           // V tiles' halves of 64 keys, 16 bits: two for each of the teams that convert
+    static constexpr int kVBytes = kBytes / 2;
+    static constexpr int kG = DP == 128 ? 2 : 6;           // V tiles as the cache holds them: an even number, tile i's place is i % kG
+    static_assert(kG % 2 == 0, "a place belongs to tiles of one parity");
+    // K's scales outlive its tile: the softmax warps read them.  A place is written again when the tile kScales before is
+    // weighed: the copy of a tile waits for the scores of the one kK before, which follow the weights of kK + 2.
+    static constexpr int kScales = 16;
+    static_assert(kScales >= kK + 2, "scales in use");
+    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oG = oV + kV * kVBytes;
+    // after the tiles
+    static constexpr int oKFull = oG + kG * kPart, oKEmpty = oKFull + 8 * kK;
+    static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
+    static constexpr int oGFull = oVEmpty + 8 * kV, oGEmpty = oGFull + 8 * kG;
+    static constexpr int oPartsReady = oGEmpty + 8 * kG, oFactorRead = oPartsReady + 8 * kQB;
+    static constexpr int oQFull = oFactorRead + 8 * kQB, oQEmpty = oQFull + 8 * kQB;
+    static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
+    static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
+    static constexpr int oBars = oDrain + 8;  // end of the barriers
+    static constexpr int oBad = (oBars + 15) / 16 * 16;        // uint32[kV][4]
+    static constexpr int oScale = oBad + 16 * kV;              // float[kG][8]: V's, of blocks of 16 keys
+    static constexpr int oKeyScale = oScale + 32 * kG;         // float[kScales][8]: K's
+    static constexpr int oFactor = oKeyScale + 32 * kScales;   // float[kQB][128]: what a row of Q's parts is to be multiplied by
+    static constexpr int oNear = oFactor + kQB * kTile * 4;    // Reach[kNear]
+    static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);
+    static constexpr int oCut = oPlan + (int)sizeof(Plan);     // Cut[2]: of items that end here, that begin here
+    static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[16]: softmax and converting warps
+    static constexpr int oStop = oWalk + 16 * (int)sizeof(Walk<Trees8>), oTmem = oStop + 4;
+    static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;   // float2[2][128]
+    static constexpr int kTotal = oStat + 2 * kTile * 8;
+    static_assert(kTotal <= 232448, "shared memory");
+};
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_constant__ Maps M, const __grid_constant__ Attend A,
+                                                              const __grid_constant__ Shape S, void* scratch)
+{
+    using L = Lay<DP, BF16>;
+    using K = Trees8;
+    extern __shared__ __align__(1024) char sm[];
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t base = smem_addr(sm);
+    Plan& plan = *reinterpret_cast<Plan*>(sm + L::oPlan);
+    Reach* const near = reinterpret_cast<Reach*>(sm + L::oNear);
+    Cut* const cut = reinterpret_cast<Cut*>(sm + L::oCut);
+    volatile int* const stop = reinterpret_cast<volatile int*>(sm + L::oStop);
+    volatile uint32_t* const bad = reinterpret_cast<volatile uint32_t*>(sm + L::oBad);
+    const Scratch W = scratch_of(scratch, S.ctas, kTile);
+
+    const uint32_t call = tid == 0 ? __ldcg(W.flag + blockIdx.x) : 0;
+    const long long began = clock64();
+    // ---- Start: tensor memory, barriers and descriptors, while the requests' data is on its way. ----
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::oTmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (warp == kCopyWarp) {
+        if (lane < 5)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char*>(&M) + lane * sizeof(CUtensorMap)) : "memory");
+    } else if (tid == 32 * kValueWarp) {
+        for (int i = 0; i < L::kK; ++i) {
+            bar_init(base + L::oKFull + 8 * i, 1 + 32);  // the copies of a tile, and of its scales by a warp's lanes
+            bar_init(base + L::oKEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < L::kV; ++i) {
+            bar_init(base + L::oVFull + 8 * i, 1);
+            bar_init(base + L::oVReady + 8 * i, 2);
+            bar_init(base + L::oVEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < L::kG; ++i) {
+            bar_init(base + L::oGFull + 8 * i, 1 + 32);
+            bar_init(base + L::oGEmpty + 8 * i, 4);
+        }
+        for (int i = 0; i < L::kQB; ++i) {
+            bar_init(base + L::oPartsReady + 8 * i, 4);
+            bar_init(base + L::oFactorRead + 8 * i, 8);
+            bar_init(base + L::oQFull + 8 * i, 1);
+            bar_init(base + L::oQEmpty + 8 * i, 1 + 4);  // the products', and the warps' that split it
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(base + L::oSFull + 8 * i, 1);
+            bar_init(base + L::oSFree + 8 * i, 4);
+            bar_init(base + L::oPHalf + 8 * i, 4);
+            bar_init(base + L::oPReady + 8 * i, 4);
+            bar_init(base + L::oODone + 8 * i, 1);
+        }
+        bar_init(base + L::oStatReady, 8);
+        bar_init(base + L::oDrain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    make_plan<K, kThreads>(A, S, reinterpret_cast<long long*>(sm), plan, near, cut, stop, call, began);  // the rings are not in use yet
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the planning scratch lies where tiles go
+    tmem_before();
+    __syncthreads();
+    tmem_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::oTmem);
+    const uint32_t qs = base, ks = base + L::oK, vs = base + L::oV;
+
+    // Every wait below tells a phase of its barrier from the one before it, and no others.  So whoever waits on a barrier
+    // passes all its phases in order, and no phase ends before those have passed the one before it who wait for both.
+    if (warp < kCopyWarp) {
+        // ---- Softmax: a thread per row. ----
+        const int s = warp >> 2, row = tid & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t tS = lanes + 128 * s, tO = lanes + 256 + s * DP, tP = L::kApart ? lanes + 384 + 64 * s : tS;
+        const int tk = row / A.group, g = row - tk * A.group;  // token of the row tile, head of the group
+        const float cs = S.log2_scale;
+        constexpr float lift = BF16 ? 0.0f : 7.0f;
+        // References that are farther off than this are taken off the scores before these are multiplied by cs, as in the
+        // kernel over 16 bits: the product of the two would be off by whole powers of two.
+        constexpr float far_off = 256.0f;
+        uint32_t sp = 0, od = 0;
+        int gi = 0, gk = 0, seg = 0;  // tiles, cached tiles and segments before this segment
+        bool ok = true;
+        Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[warp];
+        if (lane == 0) w.start(A, S, plan, near);
+        __syncwarp();
+        while (ok && w.left > 0) {
+            const int len = w.t1 - w.t0, t0 = w.t0, mine = (len + 1 - s) / 2;
+            const int token = w.item * S.block + tk;
+            const int ctx = w.x.ctx, ctx_tiles = w.x.ctx_tiles;
+            const bool real = tk < S.tok && token < w.x.rows;
+            unsigned long long seen = 0;
+            if (real && w.t1 > ctx_tiles) {
+                seen = (unsigned long long)A.mask[(int64_t)w.b * A.N + token];
+                if (w.x.rows < 64) seen &= (1ull << w.x.rows) - 1;
+            }
+            // A warp without rows goes along without its share of the work (its rows of tensor memory are its own).
+            const bool idle = !__any_sync(0xffffffffu, real);
+            float factor = 0.0f;  // of this row's scores with the cache
+            bool has_factor = false;
+            float ref = -INFINITY, sum = 0.0f;
+            for (int j = 0; j < mine; ++j) {
+                const int t = t0 + 2 * j + s;
+                const bool cached = t < ctx_tiles;
+                if (!(ok = warp_wait(base + L::oSFull + 8 * s, sp, stop))) break;
+                sp ^= 1;
+                tmem_after();
+                if (cached && !has_factor) {
+                    const int qi = seg % L::kQB;
+                    factor = reinterpret_cast<const float*>(sm + L::oFactor)[qi * kTile + row];
+                    has_factor = true;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(base + L::oFactorRead + 8 * qi);
+                }
+                if (idle) {
+                    if (L::kApart && j > 0) {
+                        if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
+                        od ^= 1;
+                    }
+                    tmem_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(base + (L::kApart ? L::oSFree : L::oPHalf) + 8 * s);
+                        bar_arrive(base + L::oPReady + 8 * s);
+                    }
+                    continue;
+                }
+                const float2* const scales = reinterpret_cast<const float2*>(sm + L::oKeyScale) + 4 * ((gk + t - t0) % L::kScales);
+                const int most = ctx - t * kTile;
+                // What the row sees of the tile's columns 32 c ..
+                auto visible = [&](int c) -> uint32_t {
+                    if (!cached) return c < 2 ? (uint32_t)(seen >> (32 * c)) : 0u;
+                    const int n = most - 32 * c;
+                    return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
+                };
+                auto factors = [&](int c) { return cached ? make_float2(factor * scales[c].x, factor * scales[c].y) : make_float2(1.0f, 1.0f); };
+                // ---- The row's reference follows the maximum where that has grown by more than a factor of 2^8. ----
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tmem_load(tS + 32 * c, x);
+                    const uint32_t vis = visible(c);
+                    const float2 f = factors(c);
+                    tmem_load_wait();
+                    tmem_loaded(x);
+                    if (__any_sync(0xffffffffu, vis != 0xffffffffu)) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(vis >> e & 1)) x[e] = 0xff800000u;
+                    }
+                    float m[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[e] = fmaxf(__uint_as_float(x[8 * e]), __uint_as_float(x[8 * e + 1]));
+#pragma unroll
+                    for (int i = 2; i < 8; i += 2)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[e] = max3(m[e], __uint_as_float(x[8 * e + i]), __uint_as_float(x[8 * e + i + 1]));
+                    top = max3(top, fmaxf(m[0], m[1]) * f.x, fmaxf(m[2], m[3]) * f.y);
+                }
+                if (L::kApart && j > 0) {
+                    // this stream's last product is done with O and the weights
+                    if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
+                    od ^= 1;
+                    tmem_after();
+                }
+                const bool grow = (top - ref) * cs > 8.0f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? top : ref;
+                    const float fix = grow ? exp2_fast((ref - to) * cs) : 1.0f;
+                    ref = to;
+                    sum *= fix;
+                    if (j > 0) {
+                        // O is complete: weights over the scores mean that these scores' product was issued after this
+                        // stream's last P V; else it was waited for.
+#pragma unroll 1
+                        for (int c = 0; c < DP / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_load16(tO + 16 * c, o);
+                            tmem_load_wait();
+                            tmem_loaded16(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                            tmem_store16(tO + 16 * c, o);
+                        }
+                    }
+                }
+                // ---- Weights exp2((x f - off) cs + shift), their sum, and P. ----
+                const bool away = ref != -INFINITY && fabsf(ref * cs) > far_off;
+                const float shift = ref == -INFINITY ? 0.0f : away ? lift : lift - ref * cs;
+                const uint32_t off = __float_as_uint(away ? -ref : 0.0f);
+                const uint64_t cs2 = pair(__float_as_uint(cs), __float_as_uint(cs)), off2 = pair(off, off);
+                const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
+                uint64_t part[2] = {0, 0};
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tmem_load(tS + 32 * c, x);
+                    const uint32_t vis = visible(c);
+                    const float2 f = factors(c);
+                    const uint64_t f2[2] = {pair(__float_as_uint(f.x), __float_as_uint(f.x)), pair(__float_as_uint(f.y), __float_as_uint(f.y))};
+                    tmem_load_wait();
+                    tmem_loaded(x);
+                    if (L::kApart && c == 3) {
+                        // the next scores may come
+                        tmem_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(base + L::oSFree + 8 * s);
+                    }
+                    const bool hides = __any_sync(0xffffffffu, vis != 0xffffffffu);
+                    uint32_t y[16];
+                    auto weigh = [&](auto hides_c) {
+                        constexpr bool kHides = decltype(hides_c)::value != 0;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint64_t v = fma2(pair(x[2 * e], x[2 * e + 1]), f2[e / 8], off2);
+                            float2 z = unpair(fma2(v, cs2, shift2));
+                            if (kHides) {
+                                if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
+                                if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
+                            }
+                            const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
+                            part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                            y[e] = pack2<BF16>(p0, p1);
+                        }
+                    };
+                    if (hides)
+                        weigh(Count<1>{});
+                    else
+                        weigh(Count<0>{});
+                    tmem_store16(tP + 16 * c, y);
+                    if (c == 1 && !L::kApart) {
+                        // the first half's product starts while the second half is computed
+                        tmem_store_wait();
+                        tmem_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
+                    }
+                }
+                const float2 both = unpair(add2(part[0], part[1]));
+                sum += both.x + both.y;
+                if (!cached) {
+                    // Rows of V that were not finite: NaN for those who see them.  (The place's phase before this one has
+                    // ended: it was of the tile two before, whose product went before these scores or has been waited for.)
+                    const int at = 2 * (gi + 2 * j + s), vi = at % L::kV;
+                    if (!(ok = warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop))) break;
+                    const uint32_t odd0 = bad[4 * vi], odd1 = bad[4 * vi + 1];  // (a tree's tokens are the first 64 keys)
+                    if ((odd0 & (uint32_t)seen) != 0 || (odd1 & (uint32_t)(seen >> 32)) != 0) sum = NAN;
+                }
+                tmem_store_wait();
+                tmem_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(base + L::oPReady + 8 * s);
+            }
+            if (!ok) break;
+            if (!has_factor && lane == 0) bar_arrive(base + L::oFactorRead + 8 * (seg % L::kQB));
+            if (mine > 0) {
+                if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
+                od ^= 1;
+                tmem_after();
+            }
+            // ---- The segment's result: to the output, or as a part. ----
+            const bool whole = w.t0 == 0 && w.t1 == w.total;
+            if (!whole && tid == 0) {
+                // an item may fill the share: its cuts at both ends are one join
+                const long long end = plan.g1 - w.left + w.took;
+                cut[w.t0 > 0 ? 0 : 1] = Cut{w.x, w.b, w.h, w.item, w.total, end - w.t1 - K::extra};
+            }
+            // the part that begins an item is the CTA's second, so that it never meets the one that ends an item
+            const int slot = 2 * (int)blockIdx.x + (w.t0 > 0 ? 0 : 1);
+            const int64_t out_row = (int64_t)w.b * A.N + token;
+            char* const out = static_cast<char*>(A.out) + ((out_row * A.q_heads + w.h * A.group + g) * A.dim) * 2;
+            // both streams' statistics, to weigh their sums
+            float2* const stat = reinterpret_cast<float2*>(sm + L::oStat);
+            stat[s * kTile + row] = make_float2(ref, sum);
+            tmem_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(base + L::oStatReady);
+            if (!(ok = warp_wait(base + L::oStatReady, 0, stop))) break;
+            tmem_after();
+            const float2 a = stat[row], b = stat[kTile + row];
+            const float m = fmaxf(a.x, b.x);
+            const float w0 = a.x == -INFINITY ? 0.0f : exp2_fast((a.x - m) * cs);
+            const float w1 = b.x == -INFINITY ? 0.0f : exp2_fast((b.x - m) * cs);
+            const float l = a.y * w0 + b.y * w1;
+            // a stream without a visible key has no sum of products (or one of zeros)
+            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+#pragma unroll 1
+            for (int c = s * (DP / 32); !idle && c < (s + 1) * (DP / 32); ++c) {
+                uint32_t o[16], o1[16] = {};
+                tmem_load16(lanes + 256 + 16 * c, o);
+                if (len > 1) tmem_load16(lanes + 256 + DP + 16 * c, o1);
+                tmem_load_wait();
+                tmem_loaded16(o);
+                tmem_loaded16(o1);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float v = 0.0f;
+                    if (w0 != 0.0f) v = __uint_as_float(o[e]) * w0;
+                    if (len > 1 && w1 != 0.0f) v = fmaf(__uint_as_float(o1[e]), w1, v);
+                    if (l != l) v = l;
+                    o[e] = __float_as_uint(v * inv);
+                }
+                if (!real) continue;
+                if (whole) {
+                    if (16 * c < A.dim) {  // (a multiple of 16)
+                        uint32_t y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = pack2<BF16>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        // a thread's row by whole sectors, where rows begin on one
+                        if (S.wide_out) {
+                            store32(out + 16 * c * 2, y);
+                        } else {
+                            *reinterpret_cast<uint4*>(out + 16 * c * 2) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(out + 16 * c * 2 + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+                        }
+                    }
+                } else {
+                    float4* const to = reinterpret_cast<float4*>(W.sums) + (int64_t)slot * (DP / 4) * kTile + row;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        to[(int64_t)(4 * c + e / 4) * kTile] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                                           __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                }
+            }
+            if (!whole && real && s == 0) W.ml[(int64_t)slot * kTile + row] = make_float2(m, l);
+            // Neither stream's next sums may overwrite what the other still reads.
+            tmem_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(base + L::oStatReady);
+            if (!(ok = warp_wait(base + L::oStatReady, 1, stop))) break;
+            gi += len;
+            ++seg;
+            gk += ctx_tiles > t0 ? (ctx_tiles < t0 + len ? ctx_tiles - t0 : len) : 0;
+            __syncwarp();
+            if (lane == 0) w.next(A, S, plan, near);
+            __syncwarp();
+        }
+    } else if (warp == kCopyWarp || warp == kCopyWarp2) {
+        // ---- Copies: one warp brings Q and K, and new tokens' K; one V. ----
+        const bool is_k = warp == kCopyWarp;
+        Walk<K> w;
+        w.start(A, S, plan, near);
+        int i = 0, seg = 0, gk = 0;
+        // places with copies and the phase that ends the last (K or V), and Q's
+        uint32_t used = 0, phase = 0;
+        int nq = 0;
+        uint32_t turn = 0;  // V: whose place's next copy is of an odd phase
+        bool ok = (base & 1023) == 0;  // the swizzle's period
+        if (!ok) *stop = 1;
+        const int pages = kTile >> A.C.shift;  // of a tile
+        for (; ok && w.left > 0; w.next(A, S, plan, near), ++seg) {
+            const int32_t* const table = A.C.table + (int64_t)w.x.slot * A.C.max_pages;
+            // Page numbers come 32 at a time, a batch ahead of the one in use: a tile's pages lie in one batch.
+            auto batch = [&](int first) {
+                const int64_t p = (int64_t)first + lane;
+                if ((p << A.C.shift) >= w.x.ctx) return -1;
+                int32_t page = table[p];
+                if (page < 0 || page >= A.C.num_pages) {
+                    latch(A.C.status, CLK_EINVAL, w.x.slot);
+                    page = A.C.num_pages;  // reads as zeros
+                }
+                return page;
+            };
+            int at = w.t0 * pages & ~31, now = batch(at), then = batch(at + 32);
+            if (is_k) {
+                const int qi = seg % L::kQB;
+                const uint32_t qb = base + L::oQFull + 8 * qi;
+                if (!(ok = warp_wait(base + L::oQEmpty + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop))) break;
+                ++nq;
+                if (lane == 0) bar_expect(qb, (uint32_t)L::kHalves * (uint32_t)(S.qbox * A.group) * 128u);
+                __syncwarp();
+                if (lane < L::kHalves)
+                    copy_box(qs + qi * L::kBytes + lane * L::kHalf, &M.q, 64 * lane, w.h * A.group, w.item * S.block, w.b, qb);
+            }
+            for (int t = w.t0; t < w.t1; ++t, ++i) {
+                const bool cached = t < w.x.ctx_tiles;
+                if (cached && t * pages - at >= 32) {
+                    at += 32;
+                    now = then;
+                    then = batch(at + 32);
+                }
+                int page = __shfl_sync(0xffffffffu, now, (t * pages - at + lane) & 31);
+                if (!cached || lane >= pages) page = -1;
+                const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, page >= 0)) << A.C.shift) * DP;
+                // The tile's rows, and the scales of 16 keys each: 0 for keys without a page.
+                auto bring = [&](uint32_t bar, uint32_t dst, const CUtensorMap* map, const float* plane, uint32_t scales) {
+                    if (lane == 0) bar_expect(bar, bytes);
+                    __syncwarp();
+                    if (page >= 0) copy_box(dst + (lane << A.C.shift) * DP, map, 0, 0, w.h, page, bar);
+                    const int from = __shfl_sync(0xffffffffu, page, 16 * lane >> A.C.shift & 31);
+                    if (lane < 8) {
+                        const bool there = from >= 0 && from < A.C.num_pages;
+                        const int64_t block = (16 * lane & (A.C.page_tokens() - 1)) >> A.scale_shift;
+                        copy_word(scales + 4 * lane, plane + (there ? from * A.scale_page + w.h * A.scale_head + block * A.scale_block : 0), there);
+                    }
+                    copies_arrive(bar);
+                };
+                if (is_k) {
+                    const int ki = i % L::kK;
+                    const uint32_t bar = base + L::oKFull + 8 * ki, dst = ks + ki * L::kPart;
+                    if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
+                    used |= 1u << ki;
+                    phase = (phase & ~(1u << ki)) | (uint32_t)(i / L::kK & 1) << ki;
+                    if (cached) {
+                        bring(bar, dst, &M.kc, A.ks, base + L::oKeyScale + 32 * ((gk + t - w.t0) % L::kScales));
+                    } else {
+                        // at most 64 rows, 64 columns a half
+                        if (lane == 0) bar_expect(bar, (uint32_t)(L::kHalves * S.kbox) * 128u);
+                        __syncwarp();
+                        if (lane < L::kHalves) copy_box(dst + lane * (L::kHalf / 2), &M.k, 64 * lane, w.h, 0, w.b, bar);
+                        copies_arrive(bar);
+                    }
+                } else if (cached) {
+                    const int vi = i % L::kG;
+                    if (!(ok = warp_wait(base + L::oGEmpty + 8 * vi, (turn >> vi & 1) ^ 1, stop))) break;
+                    used |= 1u << vi;
+                    phase = (phase & ~(1u << vi)) | (turn & 1u << vi);
+                    turn ^= 1u << vi;
+                    bring(base + L::oGFull + 8 * vi, base + L::oG + vi * L::kPart, &M.vc, A.vs, base + L::oScale + 32 * vi);
+                }
+            }
+            const int run = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0;
+            gk += run > 0 ? run : 0;
+        }
+        if (!ok) {
+            // Leave no copy in flight.
+            const long long t0 = clock64();
+            auto drain = [&](uint32_t bar, uint32_t parity) {
+                while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {}
+            };
+            for (int j = nq > L::kQB ? nq - L::kQB : 0; j < nq; ++j) drain(base + L::oQFull + 8 * (j % L::kQB), (uint32_t)(j / L::kQB & 1));
+            for (int j = 0; j < (is_k ? L::kK : L::kG); ++j)
+                if (used >> j & 1) drain(base + (is_k ? L::oKFull : L::oGFull) + 8 * j, phase >> j & 1);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- Products: one lane issues them, the warp goes along. ----
+        Walk<K> w;
+        w.start(A, S, plan, near);
+        // Shuffled values are the same in every lane for the compiler too.
+        auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+        const uint32_t tm = (uint32_t)same((int)tmem);
+        constexpr uint32_t types = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((kTile >> 4) << 24);
+        constexpr uint32_t kind_n = types | ((64 >> 3) << 17);               // scores of 64 new keys
+        constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
+        constexpr uint32_t kind_8 = (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);  // 8 bits, 32 elements a product
+        uint32_t ps[2] = {0, 0}, fs[2] = {1, 1};  // phases of PReady and SFree
+        int qi = 0, ki = 0, vi = 0;
+        uint32_t qp = 0, kp = 0, vp = 0, parts_phase = 0;
+        bool ok = true;
+        auto step = [](int& i, uint32_t& phase, int n) {
+            if (++i == n) {
+                i = 0;
+                phase ^= 1;
+            }
+        };
+        auto done = [](uint32_t bar) {
+            if (elect()) mma_commit(bar);
+            __syncwarp();
+        };
+        // descriptors count in 16 bytes
+        const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, L::kHalf / 2);
+        const uint64_t p0 = DP == 128 ? operand(base + L::oParts, 16) : operand_64(base + L::oParts);
+        const uint64_t c0 = DP == 128 ? k0 : operand_64(ks);
+        // Stream s's scores with K tile ki.
+        auto scores = [&](int s, bool cached) {
+            if (!warp_wait(base + L::oKFull + 8 * ki, kp, stop)) return false;
+            if (L::kApart) {
+                if (!warp_wait(base + L::oSFree + 8 * s, fs[s], stop)) return false;
+                fs[s] ^= 1;
+            }
+            tmem_after();
+            const uint64_t q = q0 + qi * (L::kBytes / 16), k = k0 + ki * (L::kPart / 16);
+            const uint64_t p = p0 + qi * L::kParts * (L::kPart / 16), c = c0 + ki * (L::kPart / 16);
+            if (elect()) {
+                if (cached) {
+#pragma unroll
+                    for (int e = 0; e < L::kParts * (DP / 32); ++e) {
+                        const int part = e / (DP / 32), at = e % (DP / 32) * 2;
+                        mma_ss8(tm + 128 * s, p + part * (L::kPart / 16) + at, c + at, kind_8, e > 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < DP / 16; ++e)
+                        mma_ss(tm + 128 * s, q + (e / 4) * (L::kHalf / 16) + (e % 4) * 2, k + (e / 4) * (L::kHalf / 32) + (e % 4) * 2, kind_n,
+                               e > 0);
+                }
+                mma_commit(base + L::oSFull + 8 * s);
+                mma_commit(base + L::oKEmpty + 8 * ki);
+            }
+            __syncwarp();
+            step(ki, kp, L::kK);
+            return true;
+        };
+        // Stream s's weights with the next V tile, by halves of 64 keys.
+        auto values = [&](int s, bool add) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                if (!L::kApart || part == 0)
+                    if (!warp_wait(base + (!L::kApart && part == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
+                if (!warp_wait(base + L::oVReady + 8 * vi, vp, stop)) return false;
+                tmem_after();
+                const uint64_t v = v0 + vi * (L::kVBytes / 16);
+                if (elect()) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)  // 16 keys each
+                        mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * (4 * part + e), v + 128 * e, kind_o,
+                               add || part + e > 0);
+                    mma_commit(base + L::oVEmpty + 8 * vi);
+                }
+                __syncwarp();
+                step(vi, vp, L::kV);
+            }
+            ps[s] ^= 1;
+            return true;
+        };
+        for (; ok; w.next(A, S, plan, near)) {
+            const int len = same(w.left > 0 ? w.t1 - w.t0 : 0), run = same(w.x.ctx_tiles - w.t0);
+            if (len == 0) break;
+            if (!(ok = warp_wait(base + L::oQFull + 8 * qi, qp, stop))) break;
+            if (run > 0) {
+                if (!(ok = warp_wait(base + L::oPartsReady + 8 * qi, parts_phase >> qi & 1, stop))) break;
+                parts_phase ^= 1u << qi;
+            }
+            auto ahead = [&](int j) {
+                if (j >= len) return true;
+                if (!scores(j & 1, j < run)) return false;
+                if (j + 1 == len) done(base + L::oQEmpty + 8 * qi);
+                return true;
+            };
+            ok = ahead(0) && ahead(1);
+            for (int j = 0; ok && j < len; ++j) {
+                const int s = j & 1;
+                if (L::kApart && !(ok = ahead(j + 2))) break;
+                if (!(ok = values(s, j >= 2))) break;
+                if (L::kApart || j + 2 >= len) done(base + L::oODone + 8 * s);
+                if (!L::kApart) ok = ahead(j + 2);
+            }
+            step(qi, qp, L::kQB);
+        }
+        if (!ok) {
+            // Products in flight end before tensor memory is given up.
+            done(base + L::oDrain);
+            const long long t0 = clock64();
+            while (!bar_try(base + L::oDrain, 0) && clock64() - t0 < kWaitClocks) {}
+        }
+        __syncwarp();
+    } else if (warp >= kConvertWarp) {
+        // ---- V tiles of the cache: to 16 bits, times their scales; and Q in parts. ----
+        Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
+        if (lane == 0) w.start(A, S, plan, near);
+        __syncwarp();
+        // A team is two warps: one half (64 keys) of every other tile.  A thread takes 16 elements at the same place of
+        // every `step`-th row: the swizzle of its vectors is the same in all of them.  Of eight lanes, whose vectors go
+        // out together, four take one half of row r and four that of row r ^ 5 (with rows of 64 elements r and r + 1):
+        // their loads lie in 32 different banks, and so do both their stores.
+        constexpr int chunks = DP / 16, step = 64 / chunks, turns = 64 / step;
+        const int team = (warp - kConvertWarp) >> 1, half = team & 1, parity = team >> 1, you = tid & 63;
+        const int c = (you & 3) + (DP == 128 ? 4 * (you >> 3 & 1) : 0);
+        const int row0 = DP == 128 ? (you >> 4) ^ ((you >> 2 & 1) * 5) : you / chunks;
+        const int c2 = 2 * c & 7, swizzle = row0 & 7;
+        const int at0 = (c >> 2) * (L::kHalf / 2) + row0 * 128 + (c2 ^ swizzle) * 16, at1 = at0 ^ 16;
+        const int from = (64 * half + row0) * DP + (DP == 128 ? c ^ swizzle : c) * 16;
+        uint32_t phase = 0;  // of the staged tiles' places
+        // places with copies of new tokens, the phase that ends the last
+        uint32_t v_used = 0, v_phase = 0;
+        auto convert = [&](int gi, char* dst, int have) {
+            const char* const src = sm + L::oG + gi * L::kPart + from;
+            const float* const scales = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
+            char* const to0 = dst + at0;
+            char* const to1 = dst + at1;
+            const bool plain = !BF16 && __all_sync(0xffffffffu, fits_half(scales[lane & 7]));
+            // Two turns a pass, the next pass's codes on their way; keys from `have` on become 0.
+            uint4 x[2];
+            float f[2];
+            auto load = [&](int u) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[e] = *reinterpret_cast<const uint4*>(src + (u + e) * (step * DP));
+                    f[e] = scales[4 * half + (u + e) * step / 16];
+                    if (64 * half + row0 + (u + e) * step >= have) {
+                        x[e] = make_uint4(0, 0, 0, 0);
+                        f[e] = 0.0f;
+                    }
+                }
+            };
+            auto passes = [&](auto plain_c) {
+                constexpr bool kPlain = decltype(plain_c)::value != 0;
+                load(0);
+#pragma unroll 1
+                for (int u = 0; u < turns; u += 2) {
+                    const uint4 y[2] = {x[0], x[1]};
+                    const float h[2] = {f[0], f[1]};
+                    if (u + 2 < turns) load(u + 2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        *reinterpret_cast<uint4*>(to0 + (u + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(y[e].x, y[e].y), h[e]);
+                        *reinterpret_cast<uint4*>(to1 + (u + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(y[e].z, y[e].w), h[e]);
+                    }
+                }
+            };
+            if (plain)
+                passes(Count<1>{});
+            else
+                passes(Count<0>{});
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
+        auto values = [&](int tile, int t) {
+            const bool cached = t < w.x.ctx_tiles;
+            const int gi = tile % L::kG, have = cached ? w.x.ctx - t * kTile : w.x.rows;
+            const int at = 2 * tile + half, vi = at % L::kV;
+            const uint32_t full = base + L::oVFull + 8 * vi;
+            char* const place = sm + L::oV + vi * L::kVBytes;
+            if (cached) {
+                if (!warp_wait(base + L::oGFull + 8 * gi, phase >> gi & 1, stop)) return false;
+                phase ^= 1u << gi;
+            }
+            if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(at / L::kV & 1) ^ 1, stop)) return false;
+            if (cached) {
+                convert(gi, place, have);
+                if (lane == 0) {
+                    bar_arrive(base + L::oVReady + 8 * vi);
+                    bar_arrive(base + L::oGEmpty + 8 * gi);
+                }
+            } else if (half == 0) {
+                // new tokens, at most 64 (the V warp hands them on)
+                if ((warp & 1) == 0) {
+                    v_phase = v_used >> vi & 1 ? v_phase ^ 1u << vi : v_phase;
+                    v_used |= 1u << vi;
+                    if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
+                    __syncwarp();
+                    if (lane < L::kHalves) copy_box(vs + vi * L::kVBytes + lane * (L::kHalf / 2), &M.v, 64 * lane, w.h, 0, w.b, full);
+                }
+            } else {
+                for (int e = you; e < L::kVBytes / 16; e += 64) *reinterpret_cast<uint4*>(place + 16 * e) = make_uint4(0, 0, 0, 0);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive(base + L::oVReady + 8 * vi);
+            }
+            return true;
+        };
+        // Row `me` of the item's Q in parts of 8 bits: q = factor (p0 + p1 (+ p2)), each part the rounding of what the
+        // parts before it leave, so that together they hold 9 (14) bits of an element, or 2^-18 of the row's largest where
+        // that is more: bfloat16 has 8, float16 11.  A row that is not finite gets the factor NaN.
+        auto split = [&](int seg) {
+            const int me = tid - 32 * kConvertWarp, qi = seg % L::kQB;
+            if (!warp_wait(base + L::oQFull + 8 * qi, (uint32_t)(seg / L::kQB & 1), stop)) return false;
+            if (!warp_wait(base + L::oFactorRead + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop)) return false;
+            // (No phase of the two is left out, and none passes by: Q's place is free once these warps have been here.)
+            if (w.t0 >= w.x.ctx_tiles) {
+                if (lane == 0) bar_arrive(base + L::oQEmpty + 8 * qi);
+                return true;
+            }
+            const char* const raw = sm + qi * L::kBytes + me * 128;
+            auto load = [&](int i, float* f) {  // elements 8 i .. 8 i + 7
+                const uint4 v = *reinterpret_cast<const uint4*>(raw + (i >> 3) * L::kHalf + ((i & 7) ^ (me & 7)) * 16);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y = BF16 ? make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)) : halves(u[e]);
+                    f[2 * e] = y.x;
+                    f[2 * e + 1] = y.y;
+                }
+            };
+            float top = 0.0f;
+            bool finite = true;
+#pragma unroll 1
+            for (int i = 0; i < DP / 8; ++i) {
+                float f[8];
+                load(i, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    top = fmaxf(top, fabsf(f[e]));
+                    finite = finite && fabsf(f[e]) <= 3.4028234e38f;
+                }
+            }
+            const float scale = scale_for(finite ? top : 0.0f), inv = 1.0f / scale;
+            char* const parts = sm + L::oParts + qi * L::kParts * L::kPart + me * DP;
+#pragma unroll 1
+            for (int i = 0; i < DP / 8; ++i) {
+                float f[8];
+                load(i, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = finite ? f[e] * inv : 0.0f;
+                const int at = 16 * (DP == 128 ? i / 2 ^ (me & 7) : i / 2 ^ (me >> 1 & 3)) + 8 * (i & 1);
+#pragma unroll
+                for (int part = 0; part < L::kParts; ++part) {
+                    uint32_t y[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        y[e] = to_e4m3(f[4 * e], f[4 * e + 1]) | to_e4m3(f[4 * e + 2], f[4 * e + 3]) << 16;
+                        if (part + 1 < L::kParts) {
+                            float h[4];
+                            from_e4m3x4(y[e], h);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) f[4 * e + k] -= h[k];
+                        }
+                    }
+                    *reinterpret_cast<uint2*>(parts + part * L::kPart + at) = make_uint2(y[0], y[1]);
+                }
+            }
+            reinterpret_cast<float*>(sm + L::oFactor)[qi * kTile + me] = finite ? scale : NAN;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(base + L::oPartsReady + 8 * qi);
+                bar_arrive(base + L::oQEmpty + 8 * qi);
+            }
+            return true;
+        };
+        int i = 0;
+        bool ok = true;
+        for (int seg = 0; ok && w.left > 0; ++seg) {
+            if (parity == 0) ok = split(seg);
+            for (int t = w.t0; ok && t < w.t1; ++t, ++i)
+                if ((i & 1) == parity) ok = values(i, t);
+            __syncwarp();
+            if (lane == 0) w.next(A, S, plan, near);
+            __syncwarp();
+        }
+        if (!ok) {
+            // Leave no copy in flight.
+            const long long t0 = clock64();
+            for (int j = 0; j < L::kV; ++j)
+                while ((v_used >> j & 1) && !bar_try(base + L::oVFull + 8 * j, v_phase >> j & 1) && clock64() - t0 < kWaitClocks) {}
+        }
+    } else {
+        // ---- New tokens' V: rows past the end, and rows that are not finite. ----
+        // a value is not finite where its exponent is all ones: one more there carries into the sign
+        constexpr uint32_t expo = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
+        // Rows past the node counts are 0; the requests are dealt out to the CTAs.
+        for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
+            const int rows = attend_request(A, b, false).rows;
+            const int64_t row = (int64_t)A.q_heads * A.dim / 8;
+            uint4* const out = static_cast<uint4*>(A.out) + ((int64_t)b * A.N + rows) * row;
+            for (int64_t e = lane; e < (A.N - rows) * row; e += 32) out[e] = make_uint4(0, 0, 0, 0);
+        }
+        Walk<K> w;
+        w.start(A, S, plan, near);
+        int i = 0;
+        bool ok = true;
+        uint32_t phase = 0;  // of each place's copies
+        for (; ok && w.left > 0; w.next(A, S, plan, near)) {
+            i += w.t1 - w.t0;
+            if (w.t1 <= w.x.ctx_tiles) continue;
+            const int vi = 2 * (i - 1) % L::kV;  // the segment's last tile
+            if (!(ok = warp_wait(base + L::oVFull + 8 * vi, phase >> vi & 1, stop))) break;
+            phase ^= 1u << vi;
+            char* const tile = sm + L::oV + vi * L::kVBytes;
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+                const int r = 32 * u + lane;
+                uint32_t hit = 0;
+#pragma unroll
+                for (int c = 0; c < 8 * L::kHalves; ++c) {
+                    // lanes start at different chunks of their rows: no two in one bank
+                    const int p = (c & 8) * (L::kHalf / 16) + r * 128 + (((c & 7) + lane) & 7) * 16;
+                    const uint4 x = *reinterpret_cast<const uint4*>(tile + p);
+                    hit |= ((x.x & expo) + one) | ((x.y & expo) + one) | ((x.z & expo) + one) | ((x.w & expo) + one);
+                }
+                const bool clear = r >= w.x.rows, odd = !clear && (hit & 0x80008000u) != 0;
+                if (clear || odd)
+#pragma unroll
+                    for (int c = 0; c < 8 * L::kHalves; ++c)
+                        *reinterpret_cast<uint4*>(tile + (c & 8) * (L::kHalf / 16) + r * 128 + (((c & 7) + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                const uint32_t word = __ballot_sync(0xffffffffu, odd);
+                if (lane == 0) bad[4 * vi + u] = word;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane < 2) bar_arrive(base + L::oVReady + 8 * vi);
+        }
+    }
+
+    // ---- Parts are written: raise the flag, join what was cut. ----
+    tmem_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tmem_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+    if (tid == 0) {
+        // after the barrier above, the release covers the whole CTA's parts
+        asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(W.flag + blockIdx.x), "r"(plan.call + 1) : "memory");
+        if (*stop != 0) gave_up(A, W);
+    }
+    if (*stop != 0 || plan.g0 >= plan.g1) return;
+    const Cuts cuts(plan.all, plan.ctas);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+        if (cut[i].total > 0) join_item<DP, BF16, K, kThreads>(A, S, W, plan, cuts, cut[i], stop);
+}
+
+template <int DP, bool BF16>
+int launch(const Attend& A, const Shape& S, const Maps& M, void* scratch, cudaStream_t s)
+{
+    using L = Lay<DP, BF16>;
+    static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return CLK_ECUDA;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit) || dev > 63) {
+        if (cudaFuncSetAttribute(k_attend_tree8<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) != cudaSuccess)
+            return CLK_ECUDA;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)S.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kTotal;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // the joins wait on one another
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_attend_tree8<DP, BF16>, M, A, S, scratch));
+}
+
+}  // namespace
+
+int attend_tree8_launch(const Attend& A, const Shape& S, const Maps& M, void* scratch, cudaStream_t s)
+{
+    const bool bf = A.dtype == CLK_DTYPE_BF16;
+    if (A.dim > 64) return bf ? launch<128, true>(A, S, M, scratch, s) : launch<128, false>(A, S, M, scratch, s);
+    return bf ? launch<64, true>(A, S, M, scratch, s) : launch<64, false>(A, S, M, scratch, s);
+}
+
+}  // namespace clk

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "clk_mma.cuh"
+
 namespace clk {
 
 // Two values as codes, `a` in the low byte.
@@ -45,6 +47,29 @@ __device__ __forceinline__ float scale_for(float top)
     int e = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
     if (e < least) e = least;
     return __uint_as_float((uint32_t)e << 23);
+}
+
+// Eight codes as elements of the products' type, times their scale: rounded once (exact for scales that are powers
+// of two in the type's range).  PLAIN: float16, and a scale that float16 holds.
+__device__ __forceinline__ bool fits_half(float scale) { return __half2float(__float2half_rn(scale)) == scale; }
+
+template <bool BF16, bool PLAIN>
+__device__ __forceinline__ uint4 widen(uint2 codes, float scale)
+{
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t h = half_of_e4m3((i < 2 ? codes.x : codes.y) >> 16 * (i & 1));
+        if (PLAIN) {
+            const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(scale));
+            y[i] = *reinterpret_cast<const uint32_t*>(&p);
+        } else {
+            const float2 f = halves(h), p = unpair(mul2(pair(__float_as_uint(f.x), __float_as_uint(f.y)),
+                                                        pair(__float_as_uint(scale), __float_as_uint(scale))));
+            y[i] = pack2<BF16>(p.x, p.y);
+        }
+    }
+    return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 }  // namespace clk
