@@ -231,6 +231,33 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             int t = 0, n0 = 0;
             bool cached = false;
             auto away = [&] { return ref != -INFINITY && fabsf(ref * cs) > far_off; };
+            // Rows of V that were not finite: NaN for those who see them.  (A half of a tile has a place of its own where the
+            // cache is in 8 bits, and is gone once the first half's weights are given: there this comes before.)
+            auto look_at = [&](int j) -> bool {
+                if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
+                    const int i = gi + (PROMPT ? j : 2 * j + s), at = E8 ? 2 * i : i, vi = at % L::kV;
+                    if (!warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop)) return false;
+                    const int vj = E8 ? (at + 1) % L::kV : vi;
+                    if (E8 && !warp_wait(base + L::oVReady + 8 * vj, (uint32_t)((at + 1) / L::kV & 1), stop)) return false;
+                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], bad[4 * vj + (E8 ? 0 : 2)], bad[4 * vj + (E8 ? 1 : 3)]};
+                    if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
+                        bool hit = false;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t vis;
+                            if (PROMPT) {
+                                const int upto = token - n0 + 1 - 32 * u;
+                                vis = upto >= 32 ? 0xffffffffu : upto > 0 ? (1u << upto) - 1u : 0u;
+                            } else {
+                                vis = u < 2 ? (uint32_t)(seen >> (32 * u)) : 0u;
+                            }
+                            hit |= (odd[u] & vis) != 0;
+                        }
+                        if (hit) sum = NAN;
+                    }
+                }
+                return true;
+            };
             // Tile j's scores, those of hidden keys replaced.
             auto fetch = [&](int j) -> bool {
                 t = t0 + (PROMPT ? j : 2 * j + s);
@@ -270,6 +297,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     od ^= 1;
                     tmem_after();
                 }
+                if (E8 && !look_at(j)) return false;
                 return true;
             };
             // The references follow tile j's maxima where these have grown by more than a factor of 2^8.
@@ -346,29 +374,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             // Hands tile j's weights over.
             auto give = [&](int j) -> bool {
                 sum += both.x + both.y;
-                if (!cached && (!PROMPT || n0 + kTile - 1 > first - (PROMPT ? s * S.tok : 0))) {
-                    // Rows of V that were not finite: NaN for those who see them.
-                    const int i = gi + (PROMPT ? j : 2 * j + s), at = E8 ? 2 * i : i, vi = at % L::kV;
-                    if (!warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop)) return false;
-                    const int vj = E8 ? (at + 1) % L::kV : vi;
-                    if (E8 && !warp_wait(base + L::oVReady + 8 * vj, (uint32_t)((at + 1) / L::kV & 1), stop)) return false;
-                    const uint32_t odd[4] = {bad[4 * vi], bad[4 * vi + 1], bad[4 * vj + (E8 ? 0 : 2)], bad[4 * vj + (E8 ? 1 : 3)]};
-                    if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
-                        bool hit = false;
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            uint32_t vis;
-                            if (PROMPT) {
-                                const int upto = token - n0 + 1 - 32 * u;
-                                vis = upto >= 32 ? 0xffffffffu : upto > 0 ? (1u << upto) - 1u : 0u;
-                            } else {
-                                vis = u < 2 ? (uint32_t)(seen >> (32 * u)) : 0u;
-                            }
-                            hit |= (odd[u] & vis) != 0;
-                        }
-                        if (hit) sum = NAN;
-                    }
-                }
+                if (!E8 && !look_at(j)) return false;
                 tmem_store_wait();
                 tmem_before();
                 __syncwarp();

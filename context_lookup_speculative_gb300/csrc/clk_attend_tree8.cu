@@ -42,9 +42,16 @@
 namespace clk {
 namespace {
 
-// 8 softmax, 2 copies, 1 products, 1 new V tiles, 8 that convert
-constexpr int kWarps = 20, kThreads = 32 * kWarps;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kValueWarp = 11, kConvertWarp = 12;
+// 8 softmax, 1 copies, 1 products, 8 that convert
+constexpr int kWarps = 18, kThreads = 32 * kWarps;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kConvertWarp = 10;
+
+// A team's half of a tile of V, for those who convert it.
+struct Tile8 {
+    int32_t page[4];  // of its blocks of 16 keys
+    int32_t have;     // keys of the tile
+    int32_t h, slot, pad;
+};
 
 template <int DP, bool BF16>
 struct Lay {
@@ -59,27 +66,29 @@ struct Lay {
     static constexpr int kK = DP == 128 ? (BF16 ? 3 : 2) : 6;  // K tiles in the ring (8 bits, or 64 new tokens)
     static constexpr int kV = 4;                           // V tiles' halves of 64 keys, 16 bits: two for each of the teams that convert
     static constexpr int kVBytes = kBytes / 2;
-    static constexpr int kG = DP == 128 ? 2 : 6;           // V tiles as the cache holds them: an even number, tile i's place is i % kG
-    static_assert(kG % 2 == 0, "a place belongs to tiles of one parity");
+    // V as the cache holds it, on its way through the threads that convert it: a ring of eight 16-byte pieces for each, and
+    // of their scales.  A place is filled again as soon as its thread has read it.
+    static constexpr int kPieces = 8;
+    static constexpr int kRing = 8;  // tiles of a team whose page numbers are held
     // K's scales outlive its tile: the softmax warps read them.  A place is written again when the tile kScales before is
     // weighed: the copy of a tile waits for the scores of the one kK before, which follow the weights of kK + 2.
     static constexpr int kScales = 16;
     static_assert(kScales >= kK + 2, "scales in use");
-    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oG = oV + kV * kVBytes;
+    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oPieces = oV + kV * kVBytes;
     // after the tiles
-    static constexpr int oKFull = oG + kG * kPart, oKEmpty = oKFull + 8 * kK;
+    static constexpr int oPieceScale = oPieces + 256 * kPieces * 16;
+    static constexpr int oKFull = oPieceScale + 256 * kPieces * 4, oKEmpty = oKFull + 8 * kK;
     static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
-    static constexpr int oGFull = oVEmpty + 8 * kV, oGEmpty = oGFull + 8 * kG;
-    static constexpr int oPartsReady = oGEmpty + 8 * kG, oFactorRead = oPartsReady + 8 * kQB;
+    static constexpr int oPartsReady = oVEmpty + 8 * kV, oFactorRead = oPartsReady + 8 * kQB;
     static constexpr int oQFull = oFactorRead + 8 * kQB, oQEmpty = oQFull + 8 * kQB;
     static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
     static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
     static constexpr int oBad = (oBars + 15) / 16 * 16;        // uint32[kV][4]
-    static constexpr int oScale = oBad + 16 * kV;              // float[kG][8]: V's, of blocks of 16 keys
-    static constexpr int oKeyScale = oScale + 32 * kG;         // float[kScales][8]: K's
+    static constexpr int oKeyScale = oBad + 16 * kV;           // float[kScales][8]: K's, of blocks of 16 keys
     static constexpr int oFactor = oKeyScale + 32 * kScales;   // float[kQB][128]: what a row of Q's parts is to be multiplied by
-    static constexpr int oNear = oFactor + kQB * kTile * 4;    // Reach[kNear]
+    static constexpr int oTiles = oFactor + kQB * kTile * 4;   // Tile8[8][kRing]: of each converting warp
+    static constexpr int oNear = oTiles + 8 * kRing * (int)sizeof(Tile8);  // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);
     static constexpr int oCut = oPlan + (int)sizeof(Plan);     // Cut[2]: of items that end here, that begin here
     static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[16]: softmax and converting warps
@@ -114,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
     } else if (warp == kCopyWarp) {
         if (lane < 5)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char*>(&M) + lane * sizeof(CUtensorMap)) : "memory");
-    } else if (tid == 32 * kValueWarp) {
+    } else if (tid == 32 * kConvertWarp) {
         for (int i = 0; i < L::kK; ++i) {
             bar_init(base + L::oKFull + 8 * i, 1 + 32);  // the copies of a tile, and of its scales by a warp's lanes
             bar_init(base + L::oKEmpty + 8 * i, 1);
@@ -123,10 +132,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             bar_init(base + L::oVFull + 8 * i, 1);
             bar_init(base + L::oVReady + 8 * i, 2);
             bar_init(base + L::oVEmpty + 8 * i, 1);
-        }
-        for (int i = 0; i < L::kG; ++i) {
-            bar_init(base + L::oGFull + 8 * i, 1 + 32);
-            bar_init(base + L::oGEmpty + 8 * i, 4);
         }
         for (int i = 0; i < L::kQB; ++i) {
             bar_init(base + L::oPartsReady + 8 * i, 4);
@@ -163,9 +168,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         const int tk = row / A.group, g = row - tk * A.group;  // token of the row tile, head of the group
         const float cs = S.log2_scale;
         constexpr float lift = BF16 ? 0.0f : 7.0f;
-        // References that are farther off than this are taken off the scores before these are multiplied by cs, as in the
-        // kernel over 16 bits: the product of the two would be off by whole powers of two.
-        constexpr float far_off = 256.0f;
+        // A weight is exp2(x cs - M) with a whole number M, so that the multiply-add is exact up to its last rounding
+        // however far the scores are off zero.  It follows a row's scores where the weights of 32 columns have grown
+        // beyond 2^15 together: up to there they cost no precision in floating point.  (float16 weights carry a factor of
+        // 2^7 at first, so that small ones keep their bits.)
+        constexpr float most_sum = 32768.0f;
         uint32_t sp = 0, od = 0;
         int gi = 0, gk = 0, seg = 0;  // tiles, cached tiles and segments before this segment
         bool ok = true;
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             const bool idle = !__any_sync(0xffffffffu, real);
             float factor = 0.0f;  // of this row's scores with the cache
             bool has_factor = false;
-            float ref = -INFINITY, sum = 0.0f;
+            float M = -INFINITY, sum = 0.0f;
             for (int j = 0; j < mine; ++j) {
                 const int t = t0 + 2 * j + s;
                 const bool cached = t < ctx_tiles;
@@ -221,101 +228,124 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     const int n = most - 32 * c;
                     return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
                 };
-                auto factors = [&](int c) { return cached ? make_float2(factor * scales[c].x, factor * scales[c].y) : make_float2(1.0f, 1.0f); };
-                // ---- The row's reference follows the maximum where that has grown by more than a factor of 2^8. ----
-                float top = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tmem_load(tS + 32 * c, x);
-                    const uint32_t vis = visible(c);
-                    const float2 f = factors(c);
-                    tmem_load_wait();
-                    tmem_loaded(x);
-                    if (__any_sync(0xffffffffu, vis != 0xffffffffu)) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(vis >> e & 1)) x[e] = 0xff800000u;
-                    }
-                    float m[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) m[e] = fmaxf(__uint_as_float(x[8 * e]), __uint_as_float(x[8 * e + 1]));
-#pragma unroll
-                    for (int i = 2; i < 8; i += 2)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) m[e] = max3(m[e], __uint_as_float(x[8 * e + i]), __uint_as_float(x[8 * e + i + 1]));
-                    top = max3(top, fmaxf(m[0], m[1]) * f.x, fmaxf(m[2], m[3]) * f.y);
-                }
+                auto factors = [&](int c) { return cached ? make_float2(factor * scales[c].x * cs, factor * scales[c].y * cs) : make_float2(cs, cs); };
                 if (L::kApart && j > 0) {
                     // this stream's last product is done with O and the weights
                     if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
                     od ^= 1;
                     tmem_after();
                 }
-                const bool grow = (top - ref) * cs > 8.0f;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float to = grow ? top : ref;
-                    const float fix = grow ? exp2_fast((ref - to) * cs) : 1.0f;
-                    ref = to;
-                    sum *= fix;
-                    if (j > 0) {
-                        // O is complete: weights over the scores mean that these scores' product was issued after this
-                        // stream's last P V; else it was waited for.
-#pragma unroll 1
-                        for (int c = 0; c < DP / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_load16(tO + 16 * c, o);
-                            tmem_load_wait();
-                            tmem_loaded16(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
-                            tmem_store16(tO + 16 * c, o);
-                        }
-                    }
+                if (!cached) {
+                    // Rows of V that were not finite: NaN for those who see them.  (The place's phase before this one has
+                    // ended: it was of the tile two before, whose product went before these scores or has been waited for.
+                    // And this one's next may only begin once the first half's weights are given, below.)
+                    const int at = 2 * (gi + 2 * j + s), vi = at % L::kV;
+                    if (!(ok = warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop))) break;
+                    const uint32_t odd0 = bad[4 * vi], odd1 = bad[4 * vi + 1];  // (a tree's tokens are the first 64 keys)
+                    if ((odd0 & (uint32_t)seen) != 0 || (odd1 & (uint32_t)(seen >> 32)) != 0) sum = NAN;
                 }
-                // ---- Weights exp2((x f - off) cs + shift), their sum, and P. ----
-                const bool away = ref != -INFINITY && fabsf(ref * cs) > far_off;
-                const float shift = ref == -INFINITY ? 0.0f : away ? lift : lift - ref * cs;
-                const uint32_t off = __float_as_uint(away ? -ref : 0.0f);
-                const uint64_t cs2 = pair(__float_as_uint(cs), __float_as_uint(cs)), off2 = pair(off, off);
-                const uint64_t shift2 = pair(__float_as_uint(shift), __float_as_uint(shift));
-                uint64_t part[2] = {0, 0};
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                // Columns 32 c .. gave too large weights to some row, or are a row's first visible ones: M follows, and what
+                // was summed up with the old one.
+                auto follow = [&](int c, float chunk) -> bool {
                     uint32_t x[32];
                     tmem_load(tS + 32 * c, x);
                     const uint32_t vis = visible(c);
                     const float2 f = factors(c);
-                    const uint64_t f2[2] = {pair(__float_as_uint(f.x), __float_as_uint(f.x)), pair(__float_as_uint(f.y), __float_as_uint(f.y))};
                     tmem_load_wait();
                     tmem_loaded(x);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (vis >> e & 1) top = fmaxf(top, __uint_as_float(x[e]) * (e < 16 ? f.x : f.y));
+                    const float up = ceilf(top);
+                    const bool none = M == -INFINITY, grow = none ? up != -INFINITY : chunk > most_sum;
+                    const float to = grow ? (fabsf(up) < 1048576.0f ? up - lift : up) : M;
+                    const float fix = grow && !none ? exp2f(M - to) : 1.0f;
+                    M = to;
+                    if (!__any_sync(0xffffffffu, fix != 1.0f)) return true;
+                    sum *= fix;
+                    const int tile = gi + 2 * j + s, vi = 2 * tile % L::kV, first = !L::kApart && c >= 2 ? 2 : 0;
+                    if (first > 0) {
+                        // the product with the first half's weights may be under way: its V's place is free after it
+                        if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(2 * tile / L::kV & 1), stop)) return false;
+                        tmem_after();
+                    }
+                    if (j > 0 || first > 0) {
+                        // O is complete: weights over the scores mean that these scores' product was issued after this
+                        // stream's last P V; else it was waited for.
+#pragma unroll 1
+                        for (int i = 0; i < DP / 16; ++i) {
+                            uint32_t o[16];
+                            tmem_load16(tO + 16 * i, o);
+                            tmem_load_wait();
+                            tmem_loaded16(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                            tmem_store16(tO + 16 * i, o);
+                        }
+                    }
+                    // weights of this tile that no product has taken yet (fix is a power of two)
+#pragma unroll 1
+                    for (int i = first; i < c; ++i) {
+                        uint32_t y[16];
+                        tmem_load16(tP + 16 * i, y);
+                        tmem_load_wait();
+                        tmem_loaded16(y);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] = times<BF16>(y[e], fix);
+                        tmem_store16(tP + 16 * i, y);
+                    }
+                    tmem_store_wait();
+                    return true;
+                };
+#pragma unroll 1
+                for (int c = 0; ok && c < 4; ++c) {
+                    const uint32_t vis = visible(c);
+                    const float2 f = factors(c);
+                    const uint64_t f2[2] = {pair(__float_as_uint(f.x), __float_as_uint(f.x)), pair(__float_as_uint(f.y), __float_as_uint(f.y))};
+                    const bool hides = __any_sync(0xffffffffu, vis != 0xffffffffu);
+                    uint32_t y[16];
+                    float chunk;
+                    for (int again = 0;; ++again) {
+                        uint32_t x[32];
+                        tmem_load(tS + 32 * c, x);
+                        const uint32_t off = __float_as_uint(M == -INFINITY ? 0.0f : -M);
+                        const uint64_t off2 = pair(off, off);
+                        tmem_load_wait();
+                        tmem_loaded(x);
+                        uint64_t part[2] = {0, 0};
+                        auto weigh = [&](auto hides_c) {
+                            constexpr bool kHides = decltype(hides_c)::value != 0;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float2 z = unpair(fma2(pair(x[2 * e], x[2 * e + 1]), f2[e / 8], off2));
+                                if (kHides) {
+                                    if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
+                                    if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
+                                }
+                                const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
+                                part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                                y[e] = pack2<BF16>(p0, p1);
+                            }
+                        };
+                        if (hides)
+                            weigh(Count<1>{});
+                        else
+                            weigh(Count<0>{});
+                        const float2 both = unpair(add2(part[0], part[1]));
+                        chunk = both.x + both.y;
+                        const bool off_scale = real && (chunk > most_sum || (M == -INFINITY && vis != 0));
+                        if (again > 0 || !__any_sync(0xffffffffu, off_scale)) break;
+                        if (!(ok = follow(c, chunk))) break;
+                    }
+                    if (!ok) break;
+                    sum += chunk;
                     if (L::kApart && c == 3) {
                         // the next scores may come
                         tmem_before();
                         __syncwarp();
                         if (lane == 0) bar_arrive(base + L::oSFree + 8 * s);
                     }
-                    const bool hides = __any_sync(0xffffffffu, vis != 0xffffffffu);
-                    uint32_t y[16];
-                    auto weigh = [&](auto hides_c) {
-                        constexpr bool kHides = decltype(hides_c)::value != 0;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint64_t v = fma2(pair(x[2 * e], x[2 * e + 1]), f2[e / 8], off2);
-                            float2 z = unpair(fma2(v, cs2, shift2));
-                            if (kHides) {
-                                if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
-                                if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
-                            }
-                            const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
-                            part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                            y[e] = pack2<BF16>(p0, p1);
-                        }
-                    };
-                    if (hides)
-                        weigh(Count<1>{});
-                    else
-                        weigh(Count<0>{});
                     tmem_store16(tP + 16 * c, y);
                     if (c == 1 && !L::kApart) {
                         // the first half's product starts while the second half is computed
@@ -325,16 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                         if (lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
                     }
                 }
-                const float2 both = unpair(add2(part[0], part[1]));
-                sum += both.x + both.y;
-                if (!cached) {
-                    // Rows of V that were not finite: NaN for those who see them.  (The place's phase before this one has
-                    // ended: it was of the tile two before, whose product went before these scores or has been waited for.)
-                    const int at = 2 * (gi + 2 * j + s), vi = at % L::kV;
-                    if (!(ok = warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop))) break;
-                    const uint32_t odd0 = bad[4 * vi], odd1 = bad[4 * vi + 1];  // (a tree's tokens are the first 64 keys)
-                    if ((odd0 & (uint32_t)seen) != 0 || (odd1 & (uint32_t)(seen >> 32)) != 0) sum = NAN;
-                }
+                if (!ok) break;
                 tmem_store_wait();
                 tmem_before();
                 __syncwarp();
@@ -360,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             char* const out = static_cast<char*>(A.out) + ((out_row * A.q_heads + w.h * A.group + g) * A.dim) * 2;
             // both streams' statistics, to weigh their sums
             float2* const stat = reinterpret_cast<float2*>(sm + L::oStat);
-            stat[s * kTile + row] = make_float2(ref, sum);
+            stat[s * kTile + row] = make_float2(M, sum);
             tmem_before();
             __syncwarp();
             if (lane == 0) bar_arrive(base + L::oStatReady);
@@ -368,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             tmem_after();
             const float2 a = stat[row], b = stat[kTile + row];
             const float m = fmaxf(a.x, b.x);
-            const float w0 = a.x == -INFINITY ? 0.0f : exp2_fast((a.x - m) * cs);
-            const float w1 = b.x == -INFINITY ? 0.0f : exp2_fast((b.x - m) * cs);
+            const float w0 = a.x == -INFINITY ? 0.0f : exp2f(a.x - m);
+            const float w1 = b.x == -INFINITY ? 0.0f : exp2f(b.x - m);
             const float l = a.y * w0 + b.y * w1;
             // a stream without a visible key has no sum of products (or one of zeros)
             const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
@@ -424,16 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             if (lane == 0) w.next(A, S, plan, near);
             __syncwarp();
         }
-    } else if (warp == kCopyWarp || warp == kCopyWarp2) {
-        // ---- Copies: one warp brings Q and K, and new tokens' K; one V. ----
-        const bool is_k = warp == kCopyWarp;
+    } else if (warp == kCopyWarp) {
+        // ---- Copies: Q and K, and new tokens' K. ----
         Walk<K> w;
         w.start(A, S, plan, near);
         int i = 0, seg = 0, gk = 0;
-        // places with copies and the phase that ends the last (K or V), and Q's
-        uint32_t used = 0, phase = 0;
-        int nq = 0;
-        uint32_t turn = 0;  // V: whose place's next copy is of an odd phase
+        int nq = 0, nk = 0;  // one past the last item or tile asked for
         bool ok = (base & 1023) == 0;  // the swizzle's period
         if (!ok) *stop = 1;
         const int pages = kTile >> A.C.shift;  // of a tile
@@ -451,16 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                 return page;
             };
             int at = w.t0 * pages & ~31, now = batch(at), then = batch(at + 32);
-            if (is_k) {
-                const int qi = seg % L::kQB;
-                const uint32_t qb = base + L::oQFull + 8 * qi;
-                if (!(ok = warp_wait(base + L::oQEmpty + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop))) break;
-                ++nq;
-                if (lane == 0) bar_expect(qb, (uint32_t)L::kHalves * (uint32_t)(S.qbox * A.group) * 128u);
-                __syncwarp();
-                if (lane < L::kHalves)
-                    copy_box(qs + qi * L::kBytes + lane * L::kHalf, &M.q, 64 * lane, w.h * A.group, w.item * S.block, w.b, qb);
-            }
+            const int qi = seg % L::kQB;
+            const uint32_t qb = base + L::oQFull + 8 * qi;
+            if (!(ok = warp_wait(base + L::oQEmpty + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop))) break;
+            ++nq;
+            if (lane == 0) bar_expect(qb, (uint32_t)L::kHalves * (uint32_t)(S.qbox * A.group) * 128u);
+            __syncwarp();
+            if (lane < L::kHalves)
+                copy_box(qs + qi * L::kBytes + lane * L::kHalf, &M.q, 64 * lane, w.h * A.group, w.item * S.block, w.b, qb);
             for (int t = w.t0; t < w.t1; ++t, ++i) {
                 const bool cached = t < w.x.ctx_tiles;
                 if (cached && t * pages - at >= 32) {
@@ -470,43 +485,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                 }
                 int page = __shfl_sync(0xffffffffu, now, (t * pages - at + lane) & 31);
                 if (!cached || lane >= pages) page = -1;
-                const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, page >= 0)) << A.C.shift) * DP;
-                // The tile's rows, and the scales of 16 keys each: 0 for keys without a page.
-                auto bring = [&](uint32_t bar, uint32_t dst, const CUtensorMap* map, const float* plane, uint32_t scales) {
-                    if (lane == 0) bar_expect(bar, bytes);
-                    __syncwarp();
-                    if (page >= 0) copy_box(dst + (lane << A.C.shift) * DP, map, 0, 0, w.h, page, bar);
+                const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0)), ki = i % L::kK;
+                const uint32_t bar = base + L::oKFull + 8 * ki, dst = ks + ki * L::kPart;
+                if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
+                nk = i + 1;
+                if (lane == 0) bar_expect(bar, cached ? (uint32_t)(boxes << A.C.shift) * DP : (uint32_t)(L::kHalves * S.kbox) * 128u);
+                __syncwarp();
+                if (cached) {
+                    if (page >= 0) copy_box(dst + (lane << A.C.shift) * DP, &M.kc, 0, 0, w.h, page, bar);
+                    // the scales of 16 keys each: 0 for keys without a page
                     const int from = __shfl_sync(0xffffffffu, page, 16 * lane >> A.C.shift & 31);
                     if (lane < 8) {
                         const bool there = from >= 0 && from < A.C.num_pages;
                         const int64_t block = (16 * lane & (A.C.page_tokens() - 1)) >> A.scale_shift;
-                        copy_word(scales + 4 * lane, plane + (there ? from * A.scale_page + w.h * A.scale_head + block * A.scale_block : 0), there);
+                        copy_word(base + L::oKeyScale + 32 * ((gk + t - w.t0) % L::kScales) + 4 * lane,
+                                  A.ks + (there ? from * A.scale_page + w.h * A.scale_head + block * A.scale_block : 0), there);
                     }
-                    copies_arrive(bar);
-                };
-                if (is_k) {
-                    const int ki = i % L::kK;
-                    const uint32_t bar = base + L::oKFull + 8 * ki, dst = ks + ki * L::kPart;
-                    if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
-                    used |= 1u << ki;
-                    phase = (phase & ~(1u << ki)) | (uint32_t)(i / L::kK & 1) << ki;
-                    if (cached) {
-                        bring(bar, dst, &M.kc, A.ks, base + L::oKeyScale + 32 * ((gk + t - w.t0) % L::kScales));
-                    } else {
-                        // at most 64 rows, 64 columns a half
-                        if (lane == 0) bar_expect(bar, (uint32_t)(L::kHalves * S.kbox) * 128u);
-                        __syncwarp();
-                        if (lane < L::kHalves) copy_box(dst + lane * (L::kHalf / 2), &M.k, 64 * lane, w.h, 0, w.b, bar);
-                        copies_arrive(bar);
-                    }
-                } else if (cached) {
-                    const int vi = i % L::kG;
-                    if (!(ok = warp_wait(base + L::oGEmpty + 8 * vi, (turn >> vi & 1) ^ 1, stop))) break;
-                    used |= 1u << vi;
-                    phase = (phase & ~(1u << vi)) | (turn & 1u << vi);
-                    turn ^= 1u << vi;
-                    bring(base + L::oGFull + 8 * vi, base + L::oG + vi * L::kPart, &M.vc, A.vs, base + L::oScale + 32 * vi);
+                } else if (lane < L::kHalves) {
+                    // at most 64 rows, 64 columns a half
+                    copy_box(dst + lane * (L::kHalf / 2), &M.k, 64 * lane, w.h, 0, w.b, bar);
                 }
+                copies_arrive(bar);
             }
             const int run = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0;
             gk += run > 0 ? run : 0;
@@ -518,9 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                 while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {}
             };
             for (int j = nq > L::kQB ? nq - L::kQB : 0; j < nq; ++j) drain(base + L::oQFull + 8 * (j % L::kQB), (uint32_t)(j / L::kQB & 1));
-            for (int j = 0; j < (is_k ? L::kK : L::kG); ++j)
-                if (used >> j & 1) drain(base + (is_k ? L::oKFull : L::oGFull) + 8 * j, phase >> j & 1);
+            for (int j = nk > L::kK ? nk - L::kK : 0; j < nk; ++j) drain(base + L::oKFull + 8 * (j % L::kK), (uint32_t)(j / L::kK & 1));
             asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+        // Rows past the node counts are 0; the requests are dealt out to the CTAs.
+        for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
+            const int rows = attend_request(A, b, false).rows;
+            const int64_t row = (int64_t)A.q_heads * A.dim / 8;
+            uint4* const out = static_cast<uint4*>(A.out) + ((int64_t)b * A.N + rows) * row;
+            for (int64_t e = lane; e < (A.N - rows) * row; e += 32) out[e] = make_uint4(0, 0, 0, 0);
         }
     } else if (warp == kMmaWarp) {
         // ---- Products: one lane issues them, the warp goes along. ----
@@ -634,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             while (!bar_try(base + L::oDrain, 0) && clock64() - t0 < kWaitClocks) {}
         }
         __syncwarp();
-    } else if (warp >= kConvertWarp) {
+    } else {
         // ---- V tiles of the cache: to 16 bits, times their scales; and Q in parts. ----
         Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
         if (lane == 0) w.start(A, S, plan, near);
@@ -649,84 +654,151 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         const int row0 = DP == 128 ? (you >> 4) ^ ((you >> 2 & 1) * 5) : you / chunks;
         const int c2 = 2 * c & 7, swizzle = row0 & 7;
         const int at0 = (c >> 2) * (L::kHalf / 2) + row0 * 128 + (c2 ^ swizzle) * 16, at1 = at0 ^ 16;
-        const int from = (64 * half + row0) * DP + (DP == 128 ? c ^ swizzle : c) * 16;
-        uint32_t phase = 0;  // of the staged tiles' places
-        // places with copies of new tokens, the phase that ends the last
-        uint32_t v_used = 0, v_phase = 0;
-        auto convert = [&](int gi, char* dst, int have) {
-            const char* const src = sm + L::oG + gi * L::kPart + from;
-            const float* const scales = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
-            char* const to0 = dst + at0;
-            char* const to1 = dst + at1;
-            const bool plain = !BF16 && __all_sync(0xffffffffu, fits_half(scales[lane & 7]));
-            // Two turns a pass, the next pass's codes on their way; keys from `have` on become 0.
-            uint4 x[2];
-            float f[2];
-            auto load = [&](int u) {
+        const uint32_t pieces = base + L::oPieces + (team * L::kPieces * 64 + you) * 16, scales = base + L::oPieceScale + (team * L::kPieces * 64 + you) * 4;
+        Tile8* const tiles = reinterpret_cast<Tile8*>(sm + L::oTiles) + (warp - kConvertWarp) * L::kRing;
+        // V comes past shared memory's other users: each thread asks for its own pieces, a ring of four pairs of turns ahead
+        // of those it converts (with rows of 128 a tile of the team's, with rows of 64 two), and for the page numbers as far
+        // ahead again.
+        constexpr int pairs = turns / 2, lead = 4 / pairs;  // pairs of turns a tile; tiles between asking and converting
+        Walk<K> a;
+        a.start(A, S, plan, near);
+        int ta = a.t0, ia = 0, asked = 0;  // the place of `a`, and tiles whose pages were asked for
+        // The page numbers of the team's next cached tile.
+        auto pages = [&] {
+            while (a.left > 0) {
+                const int end = a.t1 < a.x.ctx_tiles ? a.t1 : a.x.ctx_tiles;
+                if (ta < end && (ia & 1) != parity) {
+                    ++ta;
+                    ++ia;
+                }
+                if (ta < end) {
+                    Tile8* const to = tiles + asked % L::kRing;
+                    const int have = a.x.ctx - ta * kTile, key = 64 * half + 16 * lane;
+                    if (lane < 4) {
+                        const int32_t* const entry = A.C.table + (int64_t)a.x.slot * A.C.max_pages;
+                        copy_word(smem_addr(to->page + lane), entry + (key < have ? (ta * kTile + key) >> A.C.shift : 0), key < have);
+                    }
+                    if (lane == 0) {
+                        to->have = have;
+                        to->h = a.h;
+                        to->slot = a.x.slot;
+                    }
+                    ++asked;
+                    ++ta;
+                    ++ia;
+                    break;
+                }
+                ia += a.t1 - ta;
+                a.next(A, S, plan, near);
+                ta = a.t0;
+            }
+        };
+        // The pieces of turns 2 k and 2 k + 1 of tile n, and their scales.
+        auto ask = [&](int n, int k) {
+            if (n < asked) {
+                const Tile8& x = tiles[n % L::kRing];
+                const int have = x.have, mask = A.C.page_tokens() - 1;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[e] = *reinterpret_cast<const uint4*>(src + (u + e) * (step * DP));
-                    f[e] = scales[4 * half + (u + e) * step / 16];
-                    if (64 * half + row0 + (u + e) * step >= have) {
+                    const int u = 2 * k + e, block = u * step / 16, key = 64 * half + u * step + row0;
+                    const int page = x.page[block];
+                    bool there = 64 * half + 16 * block < have;
+                    if (there && (page < 0 || page >= A.C.num_pages)) {
+                        latch(A.C.status, CLK_EINVAL, x.slot);
+                        there = false;
+                    }
+                    const int64_t row = there && 16 * c < A.dim ? page * A.page_stride + x.h * A.head_stride + (key & mask) * A.tok_stride + 16 * c : 0;
+                    const int64_t scale = there ? page * A.scale_page + x.h * A.scale_head + ((key & mask) >> A.scale_shift) * A.scale_block : 0;
+                    const int place = u % L::kPieces + (DP == 64 ? (n & 1) * turns : 0);
+                    copy_vector(pieces + place * 1024, static_cast<const char*>(A.vc) + row, there && 16 * c < A.dim);
+                    copy_word(scales + place * 256, A.vs + scale, there);
+                }
+            }
+            copies_commit();
+        };
+        auto convert = [&](int n, char* dst, int have) {
+            char* const to0 = dst + at0;
+            char* const to1 = dst + at1;
+            pages();
+#pragma unroll 1
+            for (int k = 0; k < pairs; ++k) {
+                copies_wait<3>();
+                __syncwarp();  // other lanes' page numbers
+                uint4 x[2];
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int u = 2 * k + e, place = u + (DP == 64 ? (n & 1) * turns : 0);
+                    x[e] = shared_vector(pieces + place * 1024);
+                    f[e] = shared_word(scales + place * 256);
+                    if (64 * half + row0 + u * step >= have) {  // keys from `have` on become 0
                         x[e] = make_uint4(0, 0, 0, 0);
                         f[e] = 0.0f;
                     }
                 }
-            };
-            auto passes = [&](auto plain_c) {
-                constexpr bool kPlain = decltype(plain_c)::value != 0;
-                load(0);
-#pragma unroll 1
-                for (int u = 0; u < turns; u += 2) {
-                    const uint4 y[2] = {x[0], x[1]};
-                    const float h[2] = {f[0], f[1]};
-                    if (u + 2 < turns) load(u + 2);
+                ask(n + lead, k);
+                auto turns_of = [&](auto plain_c) {
+                    constexpr bool kPlain = decltype(plain_c)::value != 0;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        *reinterpret_cast<uint4*>(to0 + (u + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(y[e].x, y[e].y), h[e]);
-                        *reinterpret_cast<uint4*>(to1 + (u + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(y[e].z, y[e].w), h[e]);
+                        *reinterpret_cast<uint4*>(to0 + (2 * k + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(x[e].x, x[e].y), f[e]);
+                        *reinterpret_cast<uint4*>(to1 + (2 * k + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(x[e].z, x[e].w), f[e]);
                     }
-                }
-            };
-            if (plain)
-                passes(Count<1>{});
-            else
-                passes(Count<0>{});
+                };
+                if (!BF16 && __all_sync(0xffffffffu, fits_half(f[0]) && fits_half(f[1])))
+                    turns_of(Count<1>{});
+                else
+                    turns_of(Count<0>{});
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
         };
-        auto values = [&](int tile, int t) {
+        uint32_t v_used = 0, v_phase = 0;  // the place of new tokens' V: in use, the phase that ends its next copy
+        auto values = [&](int tile, int t, int& n) {
             const bool cached = t < w.x.ctx_tiles;
-            const int gi = tile % L::kG, have = cached ? w.x.ctx - t * kTile : w.x.rows;
             const int at = 2 * tile + half, vi = at % L::kV;
             const uint32_t full = base + L::oVFull + 8 * vi;
             char* const place = sm + L::oV + vi * L::kVBytes;
-            if (cached) {
-                if (!warp_wait(base + L::oGFull + 8 * gi, phase >> gi & 1, stop)) return false;
-                phase ^= 1u << gi;
-            }
             if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(at / L::kV & 1) ^ 1, stop)) return false;
             if (cached) {
-                convert(gi, place, have);
-                if (lane == 0) {
-                    bar_arrive(base + L::oVReady + 8 * vi);
-                    bar_arrive(base + L::oGEmpty + 8 * gi);
-                }
+                convert(n, place, w.x.ctx - t * kTile);
+                ++n;
             } else if (half == 0) {
-                // new tokens, at most 64 (the V warp hands them on)
+                // New tokens, at most 64, in their own type: rows past the end and rows that are not finite become 0, and
+                // the latter are noted.
                 if ((warp & 1) == 0) {
-                    v_phase = v_used >> vi & 1 ? v_phase ^ 1u << vi : v_phase;
-                    v_used |= 1u << vi;
+                    v_used = 1;
                     if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
                     __syncwarp();
                     if (lane < L::kHalves) copy_box(vs + vi * L::kVBytes + lane * (L::kHalf / 2), &M.v, 64 * lane, w.h, 0, w.b, full);
                 }
+                if (!warp_wait(full, v_phase, stop)) return false;
+                v_phase ^= 1;
+                v_used = 0;
+                // a value is not finite where its exponent is all ones: one more there carries into the sign
+                constexpr uint32_t expo = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
+                uint32_t hit = 0;
+#pragma unroll 1
+                for (int c = 0; c < 8 * L::kHalves; ++c) {
+                    // lanes start at different chunks of their rows: no two in one bank
+                    const uint4 x = *reinterpret_cast<const uint4*>(place + (c & 8) * (L::kHalf / 16) + you * 128 + (((c & 7) + lane) & 7) * 16);
+                    hit |= ((x.x & expo) + one) | ((x.y & expo) + one) | ((x.z & expo) + one) | ((x.w & expo) + one);
+                }
+                const bool clear = you >= w.x.rows, odd = !clear && (hit & 0x80008000u) != 0;
+                if (clear || odd)
+#pragma unroll 1
+                    for (int c = 0; c < 8 * L::kHalves; ++c)
+                        *reinterpret_cast<uint4*>(place + (c & 8) * (L::kHalf / 16) + you * 128 + (((c & 7) + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                const uint32_t word = __ballot_sync(0xffffffffu, odd);
+                if (lane == 0) bad[4 * vi + (you >> 5)] = word;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
             } else {
                 for (int e = you; e < L::kVBytes / 16; e += 64) *reinterpret_cast<uint4*>(place + 16 * e) = make_uint4(0, 0, 0, 0);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) bar_arrive(base + L::oVReady + 8 * vi);
             }
+            if (lane == 0) bar_arrive(base + L::oVReady + 8 * vi);
             return true;
         };
         // Row `me` of the item's Q in parts of 8 bits: q = factor (p0 + p1 (+ p2)), each part the rounding of what the
@@ -798,67 +870,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             }
             return true;
         };
-        int i = 0;
+        // The first tiles' pages, then their pieces.
+        for (int n = 0; n < 2 * lead; ++n) pages();
+        copies_commit();
+        copies_wait<0>();
+        __syncwarp();
+        for (int n = 0; n < lead; ++n)
+            for (int k = 0; k < pairs; ++k) ask(n, k);
+        int i = 0, n = 0;
         bool ok = true;
         for (int seg = 0; ok && w.left > 0; ++seg) {
             if (parity == 0) ok = split(seg);
             for (int t = w.t0; ok && t < w.t1; ++t, ++i)
-                if ((i & 1) == parity) ok = values(i, t);
+                if ((i & 1) == parity) ok = values(i, t, n);
             __syncwarp();
             if (lane == 0) w.next(A, S, plan, near);
             __syncwarp();
         }
-        if (!ok) {
+        copies_wait<0>();
+        if (!ok && v_used != 0) {
             // Leave no copy in flight.
             const long long t0 = clock64();
-            for (int j = 0; j < L::kV; ++j)
-                while ((v_used >> j & 1) && !bar_try(base + L::oVFull + 8 * j, v_phase >> j & 1) && clock64() - t0 < kWaitClocks) {}
-        }
-    } else {
-        // ---- New tokens' V: rows past the end, and rows that are not finite. ----
-        // a value is not finite where its exponent is all ones: one more there carries into the sign
-        constexpr uint32_t expo = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
-        // Rows past the node counts are 0; the requests are dealt out to the CTAs.
-        for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
-            const int rows = attend_request(A, b, false).rows;
-            const int64_t row = (int64_t)A.q_heads * A.dim / 8;
-            uint4* const out = static_cast<uint4*>(A.out) + ((int64_t)b * A.N + rows) * row;
-            for (int64_t e = lane; e < (A.N - rows) * row; e += 32) out[e] = make_uint4(0, 0, 0, 0);
-        }
-        Walk<K> w;
-        w.start(A, S, plan, near);
-        int i = 0;
-        bool ok = true;
-        uint32_t phase = 0;  // of each place's copies
-        for (; ok && w.left > 0; w.next(A, S, plan, near)) {
-            i += w.t1 - w.t0;
-            if (w.t1 <= w.x.ctx_tiles) continue;
-            const int vi = 2 * (i - 1) % L::kV;  // the segment's last tile
-            if (!(ok = warp_wait(base + L::oVFull + 8 * vi, phase >> vi & 1, stop))) break;
-            phase ^= 1u << vi;
-            char* const tile = sm + L::oV + vi * L::kVBytes;
-#pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                const int r = 32 * u + lane;
-                uint32_t hit = 0;
-#pragma unroll
-                for (int c = 0; c < 8 * L::kHalves; ++c) {
-                    // lanes start at different chunks of their rows: no two in one bank
-                    const int p = (c & 8) * (L::kHalf / 16) + r * 128 + (((c & 7) + lane) & 7) * 16;
-                    const uint4 x = *reinterpret_cast<const uint4*>(tile + p);
-                    hit |= ((x.x & expo) + one) | ((x.y & expo) + one) | ((x.z & expo) + one) | ((x.w & expo) + one);
-                }
-                const bool clear = r >= w.x.rows, odd = !clear && (hit & 0x80008000u) != 0;
-                if (clear || odd)
-#pragma unroll
-                    for (int c = 0; c < 8 * L::kHalves; ++c)
-                        *reinterpret_cast<uint4*>(tile + (c & 8) * (L::kHalf / 16) + r * 128 + (((c & 7) + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
-                const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                if (lane == 0) bad[4 * vi + u] = word;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane < 2) bar_arrive(base + L::oVReady + 8 * vi);
+            while (!bar_try(base + L::oVFull + 8 * (2 * parity), v_phase) && clock64() - t0 < kWaitClocks) {}
         }
     }
 

@@ -140,6 +140,7 @@ __device__ __forceinline__ int new_tiles(const Reach& x, const Shape& S, int ite
 // What the kinds of calls differ in.
 struct Trees {
     static constexpr bool prompt = false;
+    static constexpr bool in_log2 = false;  // a part's reference is a score, not yet times log2_scale
     // What an item costs besides its tiles (its result, the next one's start),
     // in tiles: about 6,000 cycles beside 2,100 a tile with prompts and 4,300
     // beside 1,800 with trees, rows of 64.  Counting it balances short items
@@ -159,11 +160,11 @@ struct Trees {
 };
 // Tiles of a cache in 8 bits take half the time.
 struct Trees8 {
-    static constexpr bool prompt = false;
+    static constexpr bool prompt = false, in_log2 = true;
     static constexpr int extra = 5, whole = 6;
 };
 struct Prompts {
-    static constexpr bool prompt = true;
+    static constexpr bool prompt = true, in_log2 = false;
     static constexpr int extra = 4, whole = 16;
 };
 
@@ -444,7 +445,7 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
     const int all = used * quads;
     const int lo = (int)((long long)all * mine / parts), hi = (int)((long long)all * (mine + 1) / parts);
     const float4* const sums = reinterpret_cast<const float4*>(W.sums);
-    const float cs = S.log2_scale;
+    const float cs = K::in_log2 ? 1.0f : S.log2_scale;
     // U elements of four columns a thread, F parts of each: eight loads in flight.
     auto rows_of = [&](auto fc, auto uc) {
         constexpr int F = decltype(fc)::value, U = decltype(uc)::value;

@@ -75,6 +75,34 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const void* src, bool th
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
+// 16 bytes, past L1.
+__device__ __forceinline__ void copy_vector(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// This thread's copies so far are a group; waits for all groups but the last N.
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 shared_vector(uint32_t at)
+{
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+    return x;
+}
+
+__device__ __forceinline__ float shared_word(uint32_t at)
+{
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
+
 // Arrives on bar once the copy_words that this thread issued so far are done.
 __device__ __forceinline__ void copies_arrive(uint32_t bar)
 {
@@ -278,6 +306,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     else
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
+}
+
+// Two 16-bit values times a float32 power of two.
+template <bool BF16>
+__device__ __forceinline__ uint32_t times(uint32_t x, float f)
+{
+    if (BF16) return pack2<true>(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+    float a, b;
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n" : "=f"(a), "=f"(b) : "r"(x));
+    return pack2<false>(a * f, b * f);
 }
 
 }  // namespace clk
