@@ -1168,7 +1168,8 @@ int attend_mma_launch(const Attend& A, void* scratch, cudaStream_t s)
     S.qbox = (int32_t)(S.tok < rows ? S.tok : rows);
     S.kbox = (int32_t)(kTile < rows ? kTile : rows);
     const bool eight = A.ks != nullptr;
-    S.vbox = eight && S.kbox > kTile / 2 ? kTile / 2 : S.kbox;
+    const int vrows = !eight ? kTile : prompt ? kTile / 2 : kTile / 4;  // of V's places
+    S.vbox = S.kbox < vrows ? S.kbox : vrows;
     S.ctas = num_sms();
     S.wide_out = A.dim % 16 == 0 && aligned(A.out, 32);
     S.log2_scale = (float)((double)A.scale * 1.4426950408889634);

@@ -42,16 +42,9 @@
 namespace clk {
 namespace {
 
-// 8 softmax, 1 copies, 1 products, 8 that convert
-constexpr int kWarps = 18, kThreads = 32 * kWarps;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kConvertWarp = 10;
-
-// A team's half of a tile of V, for those who convert it.
-struct Tile8 {
-    int32_t page[4];  // of its blocks of 16 keys
-    int32_t have;     // keys of the tile
-    int32_t h, slot, pad;
-};
+// 8 softmax, 2 copies, 1 products, 8 that convert
+constexpr int kWarps = 19, kThreads = 32 * kWarps;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kConvertWarp = 11;
 
 template <int DP, bool BF16>
 struct Lay {
@@ -64,31 +57,29 @@ struct Lay {
     static constexpr int kParts = BF16 ? 2 : 3;            // of Q
     static constexpr int kQB = DP == 128 ? 1 : 2;          // items whose Q is held
     static constexpr int kK = DP == 128 ? (BF16 ? 3 : 2) : 6;  // K tiles in the ring (8 bits, or 64 new tokens)
-    static constexpr int kV = 4;                           // V tiles' halves of 64 keys, 16 bits: two for each of the teams that convert
-    static constexpr int kVBytes = kBytes / 2;
-    // V as the cache holds it, on its way through the threads that convert it: a ring of eight 16-byte pieces for each, and
-    // of their scales.  A place is filled again as soon as its thread has read it.
-    static constexpr int kPieces = 8;
-    static constexpr int kRing = 8;  // tiles of a team whose page numbers are held
+    static constexpr int kV = 4;                           // quarters of a V tile of 16 bits, 32 keys, one for each team that converts
+    static constexpr int kVBytes = kBytes / 4;
+    static constexpr int kG = DP == 128 ? 4 : 8;           // V tiles as the cache holds them
     // K's scales outlive its tile: the softmax warps read them.  A place is written again when the tile kScales before is
     // weighed: the copy of a tile waits for the scores of the one kK before, which follow the weights of kK + 2.
     static constexpr int kScales = 16;
     static_assert(kScales >= kK + 2, "scales in use");
-    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oPieces = oV + kV * kVBytes;
+    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oG = oV + kV * kVBytes;
     // after the tiles
-    static constexpr int oPieceScale = oPieces + 256 * kPieces * 16;
-    static constexpr int oKFull = oPieceScale + 256 * kPieces * 4, oKEmpty = oKFull + 8 * kK;
+    static constexpr int oKFull = oG + kG * kPart, oKEmpty = oKFull + 8 * kK;
     static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
-    static constexpr int oPartsReady = oVEmpty + 8 * kV, oFactorRead = oPartsReady + 8 * kQB;
+    static constexpr int oGFull = oVEmpty + 8 * kV, oGEmpty = oGFull + 8 * kG;
+    static constexpr int oPartsReady = oGEmpty + 8 * kG, oFactorRead = oPartsReady + 8 * kQB;
     static constexpr int oQFull = oFactorRead + 8 * kQB, oQEmpty = oQFull + 8 * kQB;
     static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
-    static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
+    static constexpr int oHalfDone = oODone + 16, oLook = oHalfDone + 16;
+    static constexpr int oStatReady = oLook + 16, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
-    static constexpr int oBad = (oBars + 15) / 16 * 16;        // uint32[kV][4]
-    static constexpr int oKeyScale = oBad + 16 * kV;           // float[kScales][8]: K's, of blocks of 16 keys
+    static constexpr int oBad = (oBars + 15) / 16 * 16;        // uint32[kV]
+    static constexpr int oScale = oBad + 4 * kV;               // float[kG][8]: V's, of blocks of 16 keys
+    static constexpr int oKeyScale = oScale + 32 * kG;         // float[kScales][8]: K's
     static constexpr int oFactor = oKeyScale + 32 * kScales;   // float[kQB][128]: what a row of Q's parts is to be multiplied by
-    static constexpr int oTiles = oFactor + kQB * kTile * 4;   // Tile8[8][kRing]: of each converting warp
-    static constexpr int oNear = oTiles + 8 * kRing * (int)sizeof(Tile8);  // Reach[kNear]
+    static constexpr int oNear = oFactor + kQB * kTile * 4;    // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);
     static constexpr int oCut = oPlan + (int)sizeof(Plan);     // Cut[2]: of items that end here, that begin here
     static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[16]: softmax and converting warps
@@ -133,6 +124,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             bar_init(base + L::oVReady + 8 * i, 2);
             bar_init(base + L::oVEmpty + 8 * i, 1);
         }
+        for (int i = 0; i < L::kG; ++i) {
+            bar_init(base + L::oGFull + 8 * i, 1 + 32);
+            bar_init(base + L::oGEmpty + 8 * i, 8);
+        }
         for (int i = 0; i < L::kQB; ++i) {
             bar_init(base + L::oPartsReady + 8 * i, 4);
             bar_init(base + L::oFactorRead + 8 * i, 8);
@@ -145,6 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             bar_init(base + L::oPHalf + 8 * i, 4);
             bar_init(base + L::oPReady + 8 * i, 4);
             bar_init(base + L::oODone + 8 * i, 1);
+            bar_init(base + L::oHalfDone + 8 * i, 1);
+            bar_init(base + L::oLook + 8 * i, 2);
         }
         bar_init(base + L::oStatReady, 8);
         bar_init(base + L::oDrain, 1);
@@ -169,11 +166,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         const float cs = S.log2_scale;
         constexpr float lift = BF16 ? 0.0f : 7.0f;
         // A weight is exp2(x cs - M) with a whole number M, so that the multiply-add is exact up to its last rounding
-        // however far the scores are off zero.  It follows a row's scores where the weights of 32 columns have grown
+        // however far the scores are off zero.  It follows a row's scores where the weights of 64 columns have grown
         // beyond 2^15 together: up to there they cost no precision in floating point.  (float16 weights carry a factor of
         // 2^7 at first, so that small ones keep their bits.)
         constexpr float most_sum = 32768.0f;
-        uint32_t sp = 0, od = 0;
+        uint32_t sp = 0, od = 0, look = 0;  // phases of SFull (and HalfDone), ODone, Look
         int gi = 0, gk = 0, seg = 0;  // tiles, cached tiles and segments before this segment
         bool ok = true;
         Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[warp];
@@ -207,11 +204,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     __syncwarp();
                     if (lane == 0) bar_arrive(base + L::oFactorRead + 8 * qi);
                 }
+                if (L::kApart && j > 0) {
+                    // this stream's last product is done with O and the weights
+                    if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
+                    od ^= 1;
+                    tmem_after();
+                }
+                if (!cached) {
+                    if (!(ok = warp_wait(base + L::oLook + 8 * s, look, stop))) break;
+                    look ^= 1;
+                    // rows of V that were not finite: NaN for those who see them (a tree's tokens are the first 64 keys)
+                    if ((bad[0] & (uint32_t)seen) != 0 || (bad[1] & (uint32_t)(seen >> 32)) != 0) sum = NAN;
+                }
                 if (idle) {
-                    if (L::kApart && j > 0) {
-                        if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
-                        od ^= 1;
-                    }
                     tmem_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -220,43 +225,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     }
                     continue;
                 }
-                const float2* const scales = reinterpret_cast<const float2*>(sm + L::oKeyScale) + 4 * ((gk + t - t0) % L::kScales);
+                const float4* const scales = reinterpret_cast<const float4*>(sm + L::oKeyScale) + 2 * ((gk + t - t0) % L::kScales);
                 const int most = ctx - t * kTile;
+                const bool plain = cached && most >= kTile;  // the row sees all of the tile
                 // What the row sees of the tile's columns 32 c ..
                 auto visible = [&](int c) -> uint32_t {
                     if (!cached) return c < 2 ? (uint32_t)(seen >> (32 * c)) : 0u;
                     const int n = most - 32 * c;
                     return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
                 };
-                auto factors = [&](int c) { return cached ? make_float2(factor * scales[c].x * cs, factor * scales[c].y * cs) : make_float2(cs, cs); };
-                if (L::kApart && j > 0) {
-                    // this stream's last product is done with O and the weights
-                    if (!(ok = warp_wait(base + L::oODone + 8 * s, od, stop))) break;
-                    od ^= 1;
-                    tmem_after();
-                }
-                if (!cached) {
-                    // Rows of V that were not finite: NaN for those who see them.  (The place's phase before this one has
-                    // ended: it was of the tile two before, whose product went before these scores or has been waited for.
-                    // And this one's next may only begin once the first half's weights are given, below.)
-                    const int at = 2 * (gi + 2 * j + s), vi = at % L::kV;
-                    if (!(ok = warp_wait(base + L::oVReady + 8 * vi, (uint32_t)(at / L::kV & 1), stop))) break;
-                    const uint32_t odd0 = bad[4 * vi], odd1 = bad[4 * vi + 1];  // (a tree's tokens are the first 64 keys)
-                    if ((odd0 & (uint32_t)seen) != 0 || (odd1 & (uint32_t)(seen >> 32)) != 0) sum = NAN;
-                }
-                // Columns 32 c .. gave too large weights to some row, or are a row's first visible ones: M follows, and what
+                // The columns' factors, 16 at a time, from 64 h on.
+                auto factors = [&](int h) {
+                    const float f = factor * cs;
+                    return cached ? make_float4(f * scales[h].x, f * scales[h].y, f * scales[h].z, f * scales[h].w) : make_float4(cs, cs, cs, cs);
+                };
+                // Columns 64 h .. gave too large weights to some row, or are a row's first visible ones: M follows, and what
                 // was summed up with the old one.
-                auto follow = [&](int c, float chunk) -> bool {
-                    uint32_t x[32];
-                    tmem_load(tS + 32 * c, x);
-                    const uint32_t vis = visible(c);
-                    const float2 f = factors(c);
-                    tmem_load_wait();
-                    tmem_loaded(x);
+                auto follow = [&](int h, float chunk) -> bool {
+                    const float4 f4 = factors(h);
+                    const float f[4] = {f4.x, f4.y, f4.z, f4.w};
                     float top = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (vis >> e & 1) top = fmaxf(top, __uint_as_float(x[e]) * (e < 16 ? f.x : f.y));
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t x[32];
+                        tmem_load(tS + 64 * h + 32 * i, x);
+                        const uint32_t vis = visible(2 * h + i);
+                        tmem_load_wait();
+                        tmem_loaded(x);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (vis >> e & 1) top = fmaxf(top, __uint_as_float(x[e]) * f[2 * i + e / 16]);
+                    }
                     const float up = ceilf(top);
                     const bool none = M == -INFINITY, grow = none ? up != -INFINITY : chunk > most_sum;
                     const float to = grow ? (fabsf(up) < 1048576.0f ? up - lift : up) : M;
@@ -264,13 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     M = to;
                     if (!__any_sync(0xffffffffu, fix != 1.0f)) return true;
                     sum *= fix;
-                    const int tile = gi + 2 * j + s, vi = 2 * tile % L::kV, first = !L::kApart && c >= 2 ? 2 : 0;
-                    if (first > 0) {
-                        // the product with the first half's weights may be under way: its V's place is free after it
-                        if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(2 * tile / L::kV & 1), stop)) return false;
+                    const bool half = !L::kApart && h > 0;
+                    if (half) {
+                        // The product with the first half's weights may be under way.  (The one of the stream's tile before
+                        // this went before these scores, and its next needs these weights: no other phase is waited for.)
+                        if (!warp_wait(base + L::oHalfDone + 8 * s, sp ^ 1, stop)) return false;
                         tmem_after();
                     }
-                    if (j > 0 || first > 0) {
+                    if (j > 0 || half) {
                         // O is complete: weights over the scores mean that these scores' product was issued after this
                         // stream's last P V; else it was waited for.
 #pragma unroll 1
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     }
                     // weights of this tile that no product has taken yet (fix is a power of two)
 #pragma unroll 1
-                    for (int i = first; i < c; ++i) {
+                    for (int i = 0; L::kApart && i < 2 * h; ++i) {
                         uint32_t y[16];
                         tmem_load16(tP + 16 * i, y);
                         tmem_load_wait();
@@ -299,60 +299,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     return true;
                 };
 #pragma unroll 1
-                for (int c = 0; ok && c < 4; ++c) {
-                    const uint32_t vis = visible(c);
-                    const float2 f = factors(c);
-                    const uint64_t f2[2] = {pair(__float_as_uint(f.x), __float_as_uint(f.x)), pair(__float_as_uint(f.y), __float_as_uint(f.y))};
-                    const bool hides = __any_sync(0xffffffffu, vis != 0xffffffffu);
-                    uint32_t y[16];
+                for (int h = 0; h < 2; ++h) {
                     float chunk;
                     for (int again = 0;; ++again) {
-                        uint32_t x[32];
-                        tmem_load(tS + 32 * c, x);
+                        uint32_t x[64];
+                        tmem_load(tS + 64 * h, x);
+                        tmem_load(tS + 64 * h + 32, x + 32);
+                        const float4 f4 = factors(h);
+                        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
                         const uint32_t off = __float_as_uint(M == -INFINITY ? 0.0f : -M);
                         const uint64_t off2 = pair(off, off);
                         tmem_load_wait();
                         tmem_loaded(x);
+                        tmem_loaded(x + 32);
                         uint64_t part[2] = {0, 0};
                         auto weigh = [&](auto hides_c) {
                             constexpr bool kHides = decltype(hides_c)::value != 0;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float2 z = unpair(fma2(pair(x[2 * e], x[2 * e + 1]), f2[e / 8], off2));
-                                if (kHides) {
-                                    if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
-                                    if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t vis = kHides ? visible(2 * h + i) : 0u;
+                                uint32_t y[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const uint32_t g = __float_as_uint(f[2 * i + e / 8]);
+                                    float2 z = unpair(fma2(pair(x[32 * i + 2 * e], x[32 * i + 2 * e + 1]), pair(g, g), off2));
+                                    if (kHides) {
+                                        if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
+                                        if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
+                                    }
+                                    const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
+                                    part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                                    y[e] = pack2<BF16>(p0, p1);
                                 }
-                                const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
-                                part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                                y[e] = pack2<BF16>(p0, p1);
+                                // (Weights over the scores: those of columns 64 h .. lie over columns 32 h .., which have been
+                                // read.  A second time these weights are stored again, so the scores must be elsewhere still.)
+                                if (L::kApart || h > 0)
+                                    tmem_store16(tP + 32 * h + 16 * i, y);
+                                else
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) x[16 * i + e] = y[e];
                             }
                         };
-                        if (hides)
-                            weigh(Count<1>{});
-                        else
+                        if (plain)
                             weigh(Count<0>{});
+                        else
+                            weigh(Count<1>{});
                         const float2 both = unpair(add2(part[0], part[1]));
                         chunk = both.x + both.y;
-                        const bool off_scale = real && (chunk > most_sum || (M == -INFINITY && vis != 0));
-                        if (again > 0 || !__any_sync(0xffffffffu, off_scale)) break;
-                        if (!(ok = follow(c, chunk))) break;
+                        const bool off_scale = real && (chunk > most_sum || M == -INFINITY);
+                        if (again > 0 || !__any_sync(0xffffffffu, off_scale)) {
+                            if (!L::kApart && h == 0) {
+                                tmem_store16(tP, x);
+                                tmem_store16(tP + 16, x + 16);
+                            }
+                            break;
+                        }
+                        if (L::kApart || h > 0) tmem_store_wait();  // stores to the same columns follow: only this orders two of them
+                        if (!(ok = follow(h, chunk))) break;
                     }
                     if (!ok) break;
                     sum += chunk;
-                    if (L::kApart && c == 3) {
-                        // the next scores may come
+                    if (L::kApart ? h == 1 : h == 0) {
+                        // the next scores may come; or the first half's product starts while the second half is computed
+                        if (!L::kApart) tmem_store_wait();
                         tmem_before();
                         __syncwarp();
-                        if (lane == 0) bar_arrive(base + L::oSFree + 8 * s);
-                    }
-                    tmem_store16(tP + 16 * c, y);
-                    if (c == 1 && !L::kApart) {
-                        // the first half's product starts while the second half is computed
-                        tmem_store_wait();
-                        tmem_before();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(base + L::oPHalf + 8 * s);
+                        if (lane == 0) bar_arrive(base + (L::kApart ? L::oSFree : L::oPHalf) + 8 * s);
                     }
                 }
                 if (!ok) break;
@@ -445,12 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             if (lane == 0) w.next(A, S, plan, near);
             __syncwarp();
         }
-    } else if (warp == kCopyWarp) {
-        // ---- Copies: Q and K, and new tokens' K. ----
+    } else if (warp == kCopyWarp || warp == kCopyWarp2) {
+        // ---- Copies: one warp brings Q and K, and new tokens' K; one V. ----
+        const bool is_k = warp == kCopyWarp;
         Walk<K> w;
         w.start(A, S, plan, near);
         int i = 0, seg = 0, gk = 0;
-        int nq = 0, nk = 0;  // one past the last item or tile asked for
+        int nq = 0, nk = 0;  // one past the last item, or tile of K or V, asked for
+        int g = 0;           // V tiles so far
         bool ok = (base & 1023) == 0;  // the swizzle's period
         if (!ok) *stop = 1;
         const int pages = kTile >> A.C.shift;  // of a tile
@@ -468,14 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                 return page;
             };
             int at = w.t0 * pages & ~31, now = batch(at), then = batch(at + 32);
-            const int qi = seg % L::kQB;
-            const uint32_t qb = base + L::oQFull + 8 * qi;
-            if (!(ok = warp_wait(base + L::oQEmpty + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop))) break;
-            ++nq;
-            if (lane == 0) bar_expect(qb, (uint32_t)L::kHalves * (uint32_t)(S.qbox * A.group) * 128u);
-            __syncwarp();
-            if (lane < L::kHalves)
-                copy_box(qs + qi * L::kBytes + lane * L::kHalf, &M.q, 64 * lane, w.h * A.group, w.item * S.block, w.b, qb);
+            if (is_k) {
+                const int qi = seg % L::kQB;
+                const uint32_t qb = base + L::oQFull + 8 * qi;
+                if (!(ok = warp_wait(base + L::oQEmpty + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop))) break;
+                ++nq;
+                if (lane == 0) bar_expect(qb, (uint32_t)L::kHalves * (uint32_t)(S.qbox * A.group) * 128u);
+                __syncwarp();
+                if (lane < L::kHalves)
+                    copy_box(qs + qi * L::kBytes + lane * L::kHalf, &M.q, 64 * lane, w.h * A.group, w.item * S.block, w.b, qb);
+            }
             for (int t = w.t0; t < w.t1; ++t, ++i) {
                 const bool cached = t < w.x.ctx_tiles;
                 if (cached && t * pages - at >= 32) {
@@ -485,21 +501,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                 }
                 int page = __shfl_sync(0xffffffffu, now, (t * pages - at + lane) & 31);
                 if (!cached || lane >= pages) page = -1;
-                const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0)), ki = i % L::kK;
-                const uint32_t bar = base + L::oKFull + 8 * ki, dst = ks + ki * L::kPart;
-                if (!(ok = warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(i / L::kK & 1) ^ 1, stop))) break;
-                nk = i + 1;
-                if (lane == 0) bar_expect(bar, cached ? (uint32_t)(boxes << A.C.shift) * DP : (uint32_t)(L::kHalves * S.kbox) * 128u);
+                if (!is_k && !cached) continue;  // new tokens' V is brought by those who convert
+                const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, page >= 0)) << A.C.shift) * DP;
+                const int n = is_k ? i : g, rings = is_k ? L::kK : L::kG, at_ring = n % rings;
+                const uint32_t bar = base + (is_k ? L::oKFull : L::oGFull) + 8 * at_ring, empty = base + (is_k ? L::oKEmpty : L::oGEmpty) + 8 * at_ring;
+                const uint32_t dst = base + (is_k ? L::oK : L::oG) + at_ring * L::kPart;
+                if (!(ok = warp_wait(empty, (uint32_t)(n / rings & 1) ^ 1, stop))) break;
+                nk = n + 1;
+                ++g;
+                if (lane == 0) bar_expect(bar, cached ? bytes : (uint32_t)(L::kHalves * S.kbox) * 128u);
                 __syncwarp();
                 if (cached) {
-                    if (page >= 0) copy_box(dst + (lane << A.C.shift) * DP, &M.kc, 0, 0, w.h, page, bar);
+                    if (page >= 0) copy_box(dst + (lane << A.C.shift) * DP, is_k ? &M.kc : &M.vc, 0, 0, w.h, page, bar);
                     // the scales of 16 keys each: 0 for keys without a page
                     const int from = __shfl_sync(0xffffffffu, page, 16 * lane >> A.C.shift & 31);
                     if (lane < 8) {
                         const bool there = from >= 0 && from < A.C.num_pages;
                         const int64_t block = (16 * lane & (A.C.page_tokens() - 1)) >> A.scale_shift;
-                        copy_word(base + L::oKeyScale + 32 * ((gk + t - w.t0) % L::kScales) + 4 * lane,
-                                  A.ks + (there ? from * A.scale_page + w.h * A.scale_head + block * A.scale_block : 0), there);
+                        copy_word(base + (is_k ? L::oKeyScale + 32 * ((gk + t - w.t0) % L::kScales) : L::oScale + 32 * at_ring) + 4 * lane,
+                                  (is_k ? A.ks : A.vs) + (there ? from * A.scale_page + w.h * A.scale_head + block * A.scale_block : 0), there);
                     }
                 } else if (lane < L::kHalves) {
                     // at most 64 rows, 64 columns a half
@@ -517,11 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                 while (!bar_try(bar, parity) && clock64() - t0 < kWaitClocks) {}
             };
             for (int j = nq > L::kQB ? nq - L::kQB : 0; j < nq; ++j) drain(base + L::oQFull + 8 * (j % L::kQB), (uint32_t)(j / L::kQB & 1));
-            for (int j = nk > L::kK ? nk - L::kK : 0; j < nk; ++j) drain(base + L::oKFull + 8 * (j % L::kK), (uint32_t)(j / L::kK & 1));
+            const int rings = is_k ? L::kK : L::kG;
+            for (int j = nk > rings ? nk - rings : 0; j < nk; ++j)
+                drain(base + (is_k ? L::oKFull : L::oGFull) + 8 * (j % rings), (uint32_t)(j / rings & 1));
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
         // Rows past the node counts are 0; the requests are dealt out to the CTAs.
-        for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
+        for (int b = blockIdx.x; !is_k && b < A.B; b += gridDim.x) {
             const int rows = attend_request(A, b, false).rows;
             const int64_t row = (int64_t)A.q_heads * A.dim / 8;
             uint4* const out = static_cast<uint4*>(A.out) + ((int64_t)b * A.N + rows) * row;
@@ -539,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
         constexpr uint32_t kind_8 = (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);  // 8 bits, 32 elements a product
         uint32_t ps[2] = {0, 0}, fs[2] = {1, 1};  // phases of PReady and SFree
-        int qi = 0, ki = 0, vi = 0;
-        uint32_t qp = 0, kp = 0, vp = 0, parts_phase = 0;
+        int qi = 0, ki = 0;
+        uint32_t qp = 0, kp = 0, parts_phase = 0;
         bool ok = true;
         auto step = [](int& i, uint32_t& phase, int n) {
             if (++i == n) {
@@ -553,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             __syncwarp();
         };
         // descriptors count in 16 bytes
-        const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, L::kHalf / 2);
+        const uint64_t q0 = operand(qs, 16), k0 = operand(ks, 16), v0 = operand(vs, L::kHalf / 4);
         const uint64_t p0 = DP == 128 ? operand(base + L::oParts, 16) : operand_64(base + L::oParts);
         const uint64_t c0 = DP == 128 ? k0 : operand_64(ks);
         // Stream s's scores with K tile ki.
@@ -586,25 +608,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             step(ki, kp, L::kK);
             return true;
         };
-        // Stream s's weights with the next V tile, by halves of 64 keys.
+        // Stream s's weights with the next V tile, by quarters of 32 keys.
+        uint32_t vp = 0;
         auto values = [&](int s, bool add) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                if (!L::kApart || part == 0)
+            for (int part = 0; part < 4; ++part) {
+                if (part == 0 || (!L::kApart && part == 2))
                     if (!warp_wait(base + (!L::kApart && part == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
-                if (!warp_wait(base + L::oVReady + 8 * vi, vp, stop)) return false;
+                if (!warp_wait(base + L::oVReady + 8 * part, vp, stop)) return false;
                 tmem_after();
-                const uint64_t v = v0 + vi * (L::kVBytes / 16);
                 if (elect()) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)  // 16 keys each
-                        mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * (4 * part + e), v + 128 * e, kind_o,
-                               add || part + e > 0);
-                    mma_commit(base + L::oVEmpty + 8 * vi);
+                    for (int e = 0; e < 2; ++e)  // 16 keys each
+                        mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * (2 * part + e),
+                               v0 + part * (L::kVBytes / 16) + 128 * e, kind_o, add || part + e > 0);
+                    mma_commit(base + L::oVEmpty + 8 * part);
+                    if (!L::kApart && part == 1) mma_commit(base + L::oHalfDone + 8 * s);
                 }
                 __syncwarp();
-                step(vi, vp, L::kV);
             }
+            vp ^= 1;
             ps[s] ^= 1;
             return true;
         };
@@ -644,168 +667,107 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
         if (lane == 0) w.start(A, S, plan, near);
         __syncwarp();
-        // A team is two warps: one half (64 keys) of every other tile.  A thread takes 16 elements at the same place of
-        // every `step`-th row: the swizzle of its vectors is the same in all of them.  Of eight lanes, whose vectors go
-        // out together, four take one half of row r and four that of row r ^ 5 (with rows of 64 elements r and r + 1):
-        // their loads lie in 32 different banks, and so do both their stores.
-        constexpr int chunks = DP / 16, step = 64 / chunks, turns = 64 / step;
-        const int team = (warp - kConvertWarp) >> 1, half = team & 1, parity = team >> 1, you = tid & 63;
+        // A team is two warps: a quarter (32 keys) of every tile.  A thread takes 16 elements at the same place of every
+        // `step`-th row: the swizzle of its vectors is the same in all of them.  Of eight lanes, whose vectors go out
+        // together, four take one half of row r and four that of row r ^ 5 (with rows of 64 elements r and r + 1): their
+        // loads lie in 32 different banks, and so do both their stores.
+        constexpr int chunks = DP / 16, step = 64 / chunks, turns = 32 / step;
+        const int me = tid - 32 * kConvertWarp, team = me >> 6, you = me & 63;
         const int c = (you & 3) + (DP == 128 ? 4 * (you >> 3 & 1) : 0);
         const int row0 = DP == 128 ? (you >> 4) ^ ((you >> 2 & 1) * 5) : you / chunks;
         const int c2 = 2 * c & 7, swizzle = row0 & 7;
-        const int at0 = (c >> 2) * (L::kHalf / 2) + row0 * 128 + (c2 ^ swizzle) * 16, at1 = at0 ^ 16;
-        const uint32_t pieces = base + L::oPieces + (team * L::kPieces * 64 + you) * 16, scales = base + L::oPieceScale + (team * L::kPieces * 64 + you) * 4;
-        Tile8* const tiles = reinterpret_cast<Tile8*>(sm + L::oTiles) + (warp - kConvertWarp) * L::kRing;
-        // V comes past shared memory's other users: each thread asks for its own pieces, a ring of four pairs of turns ahead
-        // of those it converts (with rows of 128 a tile of the team's, with rows of 64 two), and for the page numbers as far
-        // ahead again.
-        constexpr int pairs = turns / 2, lead = 4 / pairs;  // pairs of turns a tile; tiles between asking and converting
-        Walk<K> a;
-        a.start(A, S, plan, near);
-        int ta = a.t0, ia = 0, asked = 0;  // the place of `a`, and tiles whose pages were asked for
-        // The page numbers of the team's next cached tile.
-        auto pages = [&] {
-            while (a.left > 0) {
-                const int end = a.t1 < a.x.ctx_tiles ? a.t1 : a.x.ctx_tiles;
-                if (ta < end && (ia & 1) != parity) {
-                    ++ta;
-                    ++ia;
-                }
-                if (ta < end) {
-                    Tile8* const to = tiles + asked % L::kRing;
-                    const int have = a.x.ctx - ta * kTile, key = 64 * half + 16 * lane;
-                    if (lane < 4) {
-                        const int32_t* const entry = A.C.table + (int64_t)a.x.slot * A.C.max_pages;
-                        copy_word(smem_addr(to->page + lane), entry + (key < have ? (ta * kTile + key) >> A.C.shift : 0), key < have);
-                    }
-                    if (lane == 0) {
-                        to->have = have;
-                        to->h = a.h;
-                        to->slot = a.x.slot;
-                    }
-                    ++asked;
-                    ++ta;
-                    ++ia;
-                    break;
-                }
-                ia += a.t1 - ta;
-                a.next(A, S, plan, near);
-                ta = a.t0;
-            }
-        };
-        // The pieces of turns 2 k and 2 k + 1 of tile n, and their scales.
-        auto ask = [&](int n, int k) {
-            if (n < asked) {
-                const Tile8& x = tiles[n % L::kRing];
-                const int have = x.have, mask = A.C.page_tokens() - 1;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int u = 2 * k + e, block = u * step / 16, key = 64 * half + u * step + row0;
-                    const int page = x.page[block];
-                    bool there = 64 * half + 16 * block < have;
-                    if (there && (page < 0 || page >= A.C.num_pages)) {
-                        latch(A.C.status, CLK_EINVAL, x.slot);
-                        there = false;
-                    }
-                    const int64_t row = there && 16 * c < A.dim ? page * A.page_stride + x.h * A.head_stride + (key & mask) * A.tok_stride + 16 * c : 0;
-                    const int64_t scale = there ? page * A.scale_page + x.h * A.scale_head + ((key & mask) >> A.scale_shift) * A.scale_block : 0;
-                    const int place = u % L::kPieces + (DP == 64 ? (n & 1) * turns : 0);
-                    copy_vector(pieces + place * 1024, static_cast<const char*>(A.vc) + row, there && 16 * c < A.dim);
-                    copy_word(scales + place * 256, A.vs + scale, there);
-                }
-            }
-            copies_commit();
-        };
-        auto convert = [&](int n, char* dst, int have) {
-            char* const to0 = dst + at0;
-            char* const to1 = dst + at1;
-            pages();
+        const int at0 = (c >> 2) * (L::kHalf / 4) + row0 * 128 + (c2 ^ swizzle) * 16, at1 = at0 ^ 16;
+        const int from = (32 * team + row0) * DP + (DP == 128 ? c ^ swizzle : c) * 16;
+        const uint32_t full = base + L::oVFull + 8 * team;
+        char* const place = sm + L::oV + team * L::kVBytes;
+        int g = 0;                             // V tiles of the cache so far
+        uint32_t v_phase = 0, v_used = 0;      // of new tokens' copies; one is in flight
+        auto convert = [&](int gi, int have) {
+            const char* const src = sm + L::oG + gi * L::kPart + from;
+            const float* const scales = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi + 2 * team;
+            const bool plain = !BF16 && fits_half(scales[0]) && fits_half(scales[1]);
+            // Two turns a pass; keys from `have` on become 0.
+            auto passes = [&](auto plain_c) {
+                constexpr bool kPlain = decltype(plain_c)::value != 0;
 #pragma unroll 1
-            for (int k = 0; k < pairs; ++k) {
-                copies_wait<3>();
-                __syncwarp();  // other lanes' page numbers
-                uint4 x[2];
-                float f[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int u = 2 * k + e, place = u + (DP == 64 ? (n & 1) * turns : 0);
-                    x[e] = shared_vector(pieces + place * 1024);
-                    f[e] = shared_word(scales + place * 256);
-                    if (64 * half + row0 + u * step >= have) {  // keys from `have` on become 0
-                        x[e] = make_uint4(0, 0, 0, 0);
-                        f[e] = 0.0f;
-                    }
-                }
-                ask(n + lead, k);
-                auto turns_of = [&](auto plain_c) {
-                    constexpr bool kPlain = decltype(plain_c)::value != 0;
+                for (int u = 0; u < turns; u += 2) {
+                    uint4 x[2];
+                    float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        *reinterpret_cast<uint4*>(to0 + (2 * k + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(x[e].x, x[e].y), f[e]);
-                        *reinterpret_cast<uint4*>(to1 + (2 * k + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(x[e].z, x[e].w), f[e]);
+                        x[e] = *reinterpret_cast<const uint4*>(src + (u + e) * (step * DP));
+                        f[e] = scales[(u + e) * step / 16];
+                        if (32 * team + row0 + (u + e) * step >= have) {
+                            x[e] = make_uint4(0, 0, 0, 0);
+                            f[e] = 0.0f;
+                        }
                     }
-                };
-                if (!BF16 && __all_sync(0xffffffffu, fits_half(f[0]) && fits_half(f[1])))
-                    turns_of(Count<1>{});
-                else
-                    turns_of(Count<0>{});
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        *reinterpret_cast<uint4*>(place + at0 + (u + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(x[e].x, x[e].y), f[e]);
+                        *reinterpret_cast<uint4*>(place + at1 + (u + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(x[e].z, x[e].w), f[e]);
+                    }
+                }
+            };
+            if (plain)
+                passes(Count<1>{});
+            else
+                passes(Count<0>{});
         };
-        uint32_t v_used = 0, v_phase = 0;  // the place of new tokens' V: in use, the phase that ends its next copy
-        auto values = [&](int tile, int t, int& n) {
+        auto values = [&](int tile, int t) {
             const bool cached = t < w.x.ctx_tiles;
-            const int at = 2 * tile + half, vi = at % L::kV;
-            const uint32_t full = base + L::oVFull + 8 * vi;
-            char* const place = sm + L::oV + vi * L::kVBytes;
-            if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(at / L::kV & 1) ^ 1, stop)) return false;
+            const int gi = g % L::kG, rows = w.x.rows;
+            if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kG & 1), stop)) return false;
+            if (!warp_wait(base + L::oVEmpty + 8 * team, (uint32_t)(tile & 1) ^ 1, stop)) return false;
             if (cached) {
-                convert(n, place, w.x.ctx - t * kTile);
-                ++n;
-            } else if (half == 0) {
+                convert(gi, w.x.ctx - t * kTile);
+                ++g;
+            } else if (rows > 32 * team) {
                 // New tokens, at most 64, in their own type: rows past the end and rows that are not finite become 0, and
-                // the latter are noted.
-                if ((warp & 1) == 0) {
+                // the latter are noted.  The first warp brings them and looks.
+                if ((me & 32) == 0) {
                     v_used = 1;
                     if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
                     __syncwarp();
-                    if (lane < L::kHalves) copy_box(vs + vi * L::kVBytes + lane * (L::kHalf / 2), &M.v, 64 * lane, w.h, 0, w.b, full);
-                }
-                if (!warp_wait(full, v_phase, stop)) return false;
-                v_phase ^= 1;
-                v_used = 0;
-                // a value is not finite where its exponent is all ones: one more there carries into the sign
-                constexpr uint32_t expo = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
-                uint32_t hit = 0;
-#pragma unroll 1
-                for (int c = 0; c < 8 * L::kHalves; ++c) {
+                    if (lane < L::kHalves) copy_box(smem_addr(place) + lane * (L::kHalf / 4), &M.v, 64 * lane, w.h, 32 * team, w.b, full);
+                    if (!warp_wait(full, v_phase, stop)) return false;
+                    v_phase ^= 1;
+                    v_used = 0;
+                    // a value is not finite where its exponent is all ones: one more there carries into the sign
+                    constexpr uint32_t expo = BF16 ? 0x7f807f80u : 0x7c007c00u, one = BF16 ? 0x00800080u : 0x04000400u;
                     // lanes start at different chunks of their rows: no two in one bank
-                    const uint4 x = *reinterpret_cast<const uint4*>(place + (c & 8) * (L::kHalf / 16) + you * 128 + (((c & 7) + lane) & 7) * 16);
-                    hit |= ((x.x & expo) + one) | ((x.y & expo) + one) | ((x.z & expo) + one) | ((x.w & expo) + one);
-                }
-                const bool clear = you >= w.x.rows, odd = !clear && (hit & 0x80008000u) != 0;
-                if (clear || odd)
+                    auto vector = [&](int c) { return reinterpret_cast<uint4*>(place + (c >> 3) * (L::kHalf / 4) + lane * 128 + ((c + lane) & 7) * 16); };
+                    uint32_t hit = 0;
 #pragma unroll 1
-                    for (int c = 0; c < 8 * L::kHalves; ++c)
-                        *reinterpret_cast<uint4*>(place + (c & 8) * (L::kHalf / 16) + you * 128 + (((c & 7) + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
-                const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                if (lane == 0) bad[4 * vi + (you >> 5)] = word;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
+                    for (int c = 0; c < 8 * L::kHalves; ++c) {
+                        const uint4 x = *vector(c);
+                        hit |= ((x.x & expo) + one) | ((x.y & expo) + one) | ((x.z & expo) + one) | ((x.w & expo) + one);
+                    }
+                    const bool clear = 32 * team + lane >= rows, odd = !clear && (hit & 0x80008000u) != 0;
+                    if (clear || odd)
+#pragma unroll 1
+                        for (int c = 0; c < 8 * L::kHalves; ++c) *vector(c) = make_uint4(0, 0, 0, 0);
+                    const uint32_t word = __ballot_sync(0xffffffffu, odd);
+                    if (lane == 0) bad[team] = word;
+                }
             } else {
                 for (int e = you; e < L::kVBytes / 16; e += 64) *reinterpret_cast<uint4*>(place + 16 * e) = make_uint4(0, 0, 0, 0);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
+                if (you == 0 && team < 2) bad[team] = 0;
             }
-            if (lane == 0) bar_arrive(base + L::oVReady + 8 * vi);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if (cached) bar_arrive(base + L::oGEmpty + 8 * gi);
+                if (!cached && team < 2 && (me & 32) == 0) bar_arrive(base + L::oLook + 8 * ((t - w.t0) & 1));
+                bar_arrive(base + L::oVReady + 8 * team);
+            }
             return true;
         };
         // Row `me` of the item's Q in parts of 8 bits: q = factor (p0 + p1 (+ p2)), each part the rounding of what the
         // parts before it leave, so that together they hold 9 (14) bits of an element, or 2^-18 of the row's largest where
         // that is more: bfloat16 has 8, float16 11.  A row that is not finite gets the factor NaN.
         auto split = [&](int seg) {
-            const int me = tid - 32 * kConvertWarp, qi = seg % L::kQB;
+            const int qi = seg % L::kQB;
             if (!warp_wait(base + L::oQFull + 8 * qi, (uint32_t)(seg / L::kQB & 1), stop)) return false;
             if (!warp_wait(base + L::oFactorRead + 8 * qi, (uint32_t)(seg / L::kQB & 1) ^ 1, stop)) return false;
             // (No phase of the two is left out, and none passes by: Q's place is free once these warps have been here.)
@@ -870,28 +832,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             }
             return true;
         };
-        // The first tiles' pages, then their pieces.
-        for (int n = 0; n < 2 * lead; ++n) pages();
-        copies_commit();
-        copies_wait<0>();
-        __syncwarp();
-        for (int n = 0; n < lead; ++n)
-            for (int k = 0; k < pairs; ++k) ask(n, k);
-        int i = 0, n = 0;
+        int i = 0;
         bool ok = true;
         for (int seg = 0; ok && w.left > 0; ++seg) {
-            if (parity == 0) ok = split(seg);
-            for (int t = w.t0; ok && t < w.t1; ++t, ++i)
-                if ((i & 1) == parity) ok = values(i, t, n);
+            if (team < 2) ok = split(seg);
+            for (int t = w.t0; ok && t < w.t1; ++t, ++i) ok = values(i, t);
             __syncwarp();
             if (lane == 0) w.next(A, S, plan, near);
             __syncwarp();
         }
-        copies_wait<0>();
         if (!ok && v_used != 0) {
             // Leave no copy in flight.
             const long long t0 = clock64();
-            while (!bar_try(base + L::oVFull + 8 * (2 * parity), v_phase) && clock64() - t0 < kWaitClocks) {}
+            while (!bar_try(full, v_phase) && clock64() - t0 < kWaitClocks) {}
         }
     }
 
