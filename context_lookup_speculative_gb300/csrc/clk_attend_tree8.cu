@@ -42,9 +42,9 @@
 namespace clk {
 namespace {
 
-// 8 softmax, 2 copies, 1 products, 8 that convert
-constexpr int kWarps = 19, kThreads = 32 * kWarps;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kConvertWarp = 11;
+// 8 softmax, 2 copies, 1 products, 8 that convert (and one that fills its warpgroup)
+constexpr int kWarps = 20, kThreads = 32 * kWarps;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kConvertWarp = 12;
 
 template <int DP, bool BF16>
 struct Lay {
@@ -157,6 +157,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
 
     // Every wait below tells a phase of its barrier from the one before it, and no others.  So whoever waits on a barrier
     // passes all its phases in order, and no phase ends before those have passed the one before it who wait for both.
+    // Registers: 640 threads x 96 at launch; 256 x 144 + 384 x 64 after the split.
+    if (warp < kCopyWarp)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < kCopyWarp) {
         // ---- Softmax: a thread per row. ----
         const int s = warp >> 2, row = tid & 127;
@@ -662,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             while (!bar_try(base + L::oDrain, 0) && clock64() - t0 < kWaitClocks) {}
         }
         __syncwarp();
-    } else {
+    } else if (warp >= kConvertWarp) {
         // ---- V tiles of the cache: to 16 bits, times their scales; and Q in parts. ----
         Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
         if (lane == 0) w.start(A, S, plan, near);
@@ -848,6 +853,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         }
     }
 
+    // The joins run with equal shares of the registers again.
+    if (warp < kCopyWarp)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    else
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // ---- Parts are written: raise the flag, join what was cut. ----
     tmem_before();
     __syncthreads();
