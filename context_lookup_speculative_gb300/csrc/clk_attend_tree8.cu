@@ -60,7 +60,7 @@ struct Lay {
     static constexpr int kV = 4;                           // quarters of a V tile of 16 bits, 32 keys, one for each team that converts
     static constexpr int kVBytes = kBytes / 4;
     static constexpr int kG = DP == 128 ? 4 : 8;           // V tiles as the cache holds them
-    // K's scales outlive its tile: the softmax warps read them.  A place is written again when the tile kScales before is
+    // Scales outlive their tiles: the softmax warps read them.  A place is written again when the tile kScales before is
     // weighed: the copy of a tile waits for the scores of the one kK before, which follow the weights of kK + 2.
     static constexpr int kScales = 16;
     static_assert(kScales >= kK + 2, "scales in use");
@@ -76,9 +76,8 @@ struct Lay {
     static constexpr int oStatReady = oLook + 16, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
     static constexpr int oBad = (oBars + 15) / 16 * 16;        // uint32[kV]
-    static constexpr int oScale = oBad + 4 * kV;               // float[kG][8]: V's, of blocks of 16 keys
-    static constexpr int oKeyScale = oScale + 32 * kG;         // float[kScales][8]: K's
-    static constexpr int oFactor = oKeyScale + 32 * kScales;   // float[kQB][128]: what a row of Q's parts is to be multiplied by
+    static constexpr int oScale = oBad + 4 * kV;               // float[kScales][2][8]: K's and V's, of blocks of 16 keys
+    static constexpr int oFactor = oScale + 64 * kScales;      // float[kQB][128]: what a row of Q's parts is to be multiplied by
     static constexpr int oNear = oFactor + kQB * kTile * 4;    // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);
     static constexpr int oCut = oPlan + (int)sizeof(Plan);     // Cut[2]: of items that end here, that begin here
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             bar_init(base + L::oVEmpty + 8 * i, 1);
         }
         for (int i = 0; i < L::kG; ++i) {
-            bar_init(base + L::oGFull + 8 * i, 1 + 32);
+            bar_init(base + L::oGFull + 8 * i, 1);
             bar_init(base + L::oGEmpty + 8 * i, 8);
         }
         for (int i = 0; i < L::kQB; ++i) {
@@ -169,12 +168,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         const uint32_t tS = lanes + 128 * s, tO = lanes + 256 + s * DP, tP = L::kApart ? lanes + 384 + 64 * s : tS;
         const int tk = row / A.group, g = row - tk * A.group;  // token of the row tile, head of the group
         const float cs = S.log2_scale;
-        constexpr float lift = BF16 ? 0.0f : 7.0f;
-        // A weight is exp2(x cs - M) with a whole number M, so that the multiply-add is exact up to its last rounding
-        // however far the scores are off zero.  It follows a row's scores where the weights of 64 columns have grown
-        // beyond 2^15 together: up to there they cost no precision in floating point.  (float16 weights carry a factor of
-        // 2^7 at first, so that small ones keep their bits.)
-        constexpr float most_sum = 32768.0f;
+        // A weight is p = exp2(z - M), z = x cs, with a whole number M.  V's codes are multiplied by t = p v, v the scale of
+        // their 16 keys, in float16.  Where v = 2^k, t = exp2(z + k - M) comes out of the exponential itself, and the sum of
+        // p is that of t times 2^-k: no multiplication an element.  M follows a row where its weights have grown too large;
+        // up to there size costs no precision in floating point.  (The largest t starts at up to 2^4, so that small weights
+        // keep their bits, and may grow to where 16 of them add up to 2^15.  What is below 2^-25 is lost: the largest t's
+        // 2^-28 a key.)  The largest p starts at up to 2^100: V's scales may be as small as 2^-100.  That t stays a normal
+        // number where p matters, however far V's scales lie apart, takes k of -60 to 30 and M not far above the scores;
+        // else p and t are computed each.
+        constexpr float lift = 4.0f, lift_sum = 100.0f, most_sum = 0x1p120f, most_weight = 32768.0f;
         uint32_t sp = 0, od = 0, look = 0;  // phases of SFull (and HalfDone), ODone, Look
         int gi = 0, gk = 0, seg = 0;  // tiles, cached tiles and segments before this segment
         bool ok = true;
@@ -196,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             float factor = 0.0f;  // of this row's scores with the cache
             bool has_factor = false;
             float M = -INFINITY, sum = 0.0f;
+            bool wide = false;  // M is far above the scores
             for (int j = 0; j < mine; ++j) {
                 const int t = t0 + 2 * j + s;
                 const bool cached = t < ctx_tiles;
@@ -230,26 +233,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     }
                     continue;
                 }
-                const float4* const scales = reinterpret_cast<const float4*>(sm + L::oKeyScale) + 2 * ((gk + t - t0) % L::kScales);
+                const float4* const scales = reinterpret_cast<const float4*>(sm + L::oScale) + 4 * ((gk + t - t0) % L::kScales);
                 const int most = ctx - t * kTile;
-                const bool plain = cached && most >= kTile;  // the row sees all of the tile
+                // plain: the rows see all of the tile, and exponents of V's scales can go into the weights' without loss
+                bool plain = cached && most >= kTile;
+                if (plain) {
+                    const uint32_t v = reinterpret_cast<const uint32_t*>(scales)[8 + (lane & 7)];
+                    plain = __all_sync(0xffffffffu, (v & 0x7fffffu) == 0 && v >= (127u - 60 << 23) && v <= (127u + 30 << 23) && !wide);
+                }
                 // What the row sees of the tile's columns 32 c ..
                 auto visible = [&](int c) -> uint32_t {
                     if (!cached) return c < 2 ? (uint32_t)(seen >> (32 * c)) : 0u;
                     const int n = most - 32 * c;
                     return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
                 };
-                // The columns' factors, 16 at a time, from 64 h on.
+                // The columns' factors, 16 at a time, from 64 h on; and V's scales there.
+                const float f0 = factor * cs;
                 auto factors = [&](int h) {
-                    const float f = factor * cs;
-                    return cached ? make_float4(f * scales[h].x, f * scales[h].y, f * scales[h].z, f * scales[h].w) : make_float4(cs, cs, cs, cs);
+                    return cached ? make_float4(f0 * scales[h].x, f0 * scales[h].y, f0 * scales[h].z, f0 * scales[h].w) : make_float4(cs, cs, cs, cs);
                 };
-                // Columns 64 h .. gave too large weights to some row, or are a row's first visible ones: M follows, and what
-                // was summed up with the old one.
-                auto follow = [&](int h, float chunk) -> bool {
-                    const float4 f4 = factors(h);
-                    const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-                    float top = -INFINITY;
+                auto units = [&](int h) { return cached ? scales[2 + h] : make_float4(1.0f, 1.0f, 1.0f, 1.0f); };
+                // Columns 64 h .. gave too large weights to some row (large), or are a row's first: M follows, and what was
+                // summed up with the old one.
+                auto follow = [&](int h, bool large) -> bool {
+                    const float4 f4 = factors(h), v4 = units(h);
+                    const float f[4] = {f4.x, f4.y, f4.z, f4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
+                    float top = -INFINITY, heavy = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t x[32];
@@ -258,16 +267,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                         tmem_load_wait();
                         tmem_loaded(x);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (vis >> e & 1) top = fmaxf(top, __uint_as_float(x[e]) * f[2 * i + e / 16]);
+                        for (int q = 0; q < 2; ++q) {
+                            float m = -INFINITY;
+#pragma unroll
+                            for (int e = 16 * q; e < 16 * q + 16; ++e)
+                                if (vis >> e & 1) m = fmaxf(m, __uint_as_float(x[e]) * f[2 * i + q]);
+                            top = fmaxf(top, m);
+                            heavy = fmaxf(heavy, m + __log2f(fabsf(v[2 * i + q])));
+                        }
                     }
-                    const float up = ceilf(top);
-                    const bool none = M == -INFINITY, grow = none ? up != -INFINITY : chunk > most_sum;
-                    const float to = grow ? (fabsf(up) < 1048576.0f ? up - lift : up) : M;
-                    const float fix = grow && !none ? exp2f(M - to) : 1.0f;
-                    M = to;
+                    const bool none = M == -INFINITY;
+                    // whole numbers; a sum beyond 2^20 has no use for a part of one
+                    float m = fmaxf(ceilf(heavy) - lift, ceilf(top) - lift_sum);
+                    if (top == -INFINITY || !(none || large)) m = M;
+                    const float fix = none ? 1.0f : exp2f(M - m);
+                    if (!none) sum *= fix;
+                    M = m;
+                    wide = M > top + 30.0f;
                     if (!__any_sync(0xffffffffu, fix != 1.0f)) return true;
-                    sum *= fix;
                     const bool half = !L::kApart && h > 0;
                     if (half) {
                         // The product with the first half's weights may be under way.  (The one of the stream's tile before
@@ -279,14 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                         // O is complete: weights over the scores mean that these scores' product was issued after this
                         // stream's last P V; else it was waited for.
 #pragma unroll 1
-                        for (int i = 0; i < DP / 16; ++i) {
-                            uint32_t o[16];
-                            tmem_load16(tO + 16 * i, o);
+                        for (int i = 0; i < DP / 32; ++i) {
+                            uint32_t o[32];
+                            tmem_load(tO + 32 * i, o);
                             tmem_load_wait();
-                            tmem_loaded16(o);
+                            tmem_loaded(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
-                            tmem_store16(tO + 16 * i, o);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                            tmem_store16(tO + 32 * i, o);
+                            tmem_store16(tO + 32 * i + 16, o + 16);
                         }
                     }
                     // weights of this tile that no product has taken yet (fix is a power of two)
@@ -297,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                         tmem_load_wait();
                         tmem_loaded16(y);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] = times<BF16>(y[e], fix);
+                        for (int e = 0; e < 16; ++e) y[e] = BF16 && !cached ? times<true>(y[e], fix) : times<false>(y[e], fix);
                         tmem_store16(tP + 16 * i, y);
                     }
                     tmem_store_wait();
@@ -310,31 +328,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                         uint32_t x[64];
                         tmem_load(tS + 64 * h, x);
                         tmem_load(tS + 64 * h + 32, x + 32);
-                        const float4 f4 = factors(h);
-                        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-                        const uint32_t off = __float_as_uint(M == -INFINITY ? 0.0f : -M);
-                        const uint64_t off2 = pair(off, off);
-                        tmem_load_wait();
-                        tmem_loaded(x);
-                        tmem_loaded(x + 32);
-                        uint64_t part[2] = {0, 0};
-                        auto weigh = [&](auto hides_c) {
-                            constexpr bool kHides = decltype(hides_c)::value != 0;
+                        const float4 f4 = factors(h), v4 = units(h);
+                        const float f[4] = {f4.x, f4.y, f4.z, f4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
+                        const float off = M == -INFINITY ? 0.0f : -M;
+                        float sums[4];  // of t
+                        // Weights of columns 64 h .., kPlain: seen all, V's scales powers of two.
+                        auto weigh = [&](auto plain_c) {
+                            constexpr bool kPlain = decltype(plain_c)::value != 0;
+                            float off16[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) off16[q] = kPlain ? off + (float)((int)(__float_as_uint(v[q]) >> 23) - 127) : off;
+                            tmem_load_wait();
+                            tmem_loaded(x);
+                            tmem_loaded(x + 32);
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint32_t vis = kHides ? visible(2 * h + i) : 0u;
+                                const uint32_t vis = kPlain ? 0u : visible(2 * h + i);
                                 uint32_t y[16];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const uint32_t g = __float_as_uint(f[2 * i + e / 8]);
-                                    float2 z = unpair(fma2(pair(x[32 * i + 2 * e], x[32 * i + 2 * e + 1]), pair(g, g), off2));
-                                    if (kHides) {
-                                        if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
-                                        if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
+                                for (int q = 0; q < 2; ++q) {
+                                    const uint32_t a = __float_as_uint(f[2 * i + q]), b = __float_as_uint(off16[2 * i + q]);
+                                    const uint64_t a2 = pair(a, a), b2 = pair(b, b);
+                                    uint64_t part[2] = {0, 0};
+#pragma unroll
+                                    for (int e = 8 * q; e < 8 * q + 8; ++e) {
+                                        float2 z = unpair(fma2(pair(x[32 * i + 2 * e], x[32 * i + 2 * e + 1]), a2, b2));
+                                        if (!kPlain) {
+                                            if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
+                                            if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
+                                        }
+                                        float2 t = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                                        part[e & 1] = add2(part[e & 1], pair(__float_as_uint(t.x), __float_as_uint(t.y)));
+                                        if (!kPlain) {
+                                            t.x *= v[2 * i + q];
+                                            t.y *= v[2 * i + q];
+                                        }
+                                        y[e] = pack2<false>(t.x, t.y);
+                                        if (!kPlain && BF16 && !cached) y[e] = pack2<true>(t.x, t.y);
                                     }
-                                    const float p0 = exp2_fast(z.x), p1 = exp2_fast(z.y);
-                                    part[e & 1] = add2(part[e & 1], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                                    y[e] = pack2<BF16>(p0, p1);
+                                    const float2 both = unpair(add2(part[0], part[1]));
+                                    sums[2 * i + q] = both.x + both.y;
                                 }
                                 // (Weights over the scores: those of columns 64 h .. lie over columns 32 h .., which have been
                                 // read.  A second time these weights are stored again, so the scores must be elsewhere still.)
@@ -345,14 +378,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                                     for (int e = 0; e < 16; ++e) x[16 * i + e] = y[e];
                             }
                         };
-                        if (plain)
-                            weigh(Count<0>{});
-                        else
+                        float heaviest;
+                        if (plain) {
                             weigh(Count<1>{});
-                        const float2 both = unpair(add2(part[0], part[1]));
-                        chunk = both.x + both.y;
-                        const bool off_scale = real && (chunk > most_sum || M == -INFINITY);
-                        if (again > 0 || !__any_sync(0xffffffffu, off_scale)) {
+                            heaviest = fmaxf(fmaxf(sums[0], sums[1]), fmaxf(sums[2], sums[3]));
+                            // p = t 2^-k
+                            chunk = 0.0f;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) chunk = fmaf(sums[q], __uint_as_float((254u << 23) - __float_as_uint(v[q])), chunk);
+                        } else {
+                            weigh(Count<0>{});
+                            heaviest = 0.0f;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) heaviest = fmaxf(heaviest, sums[q] * fabsf(v[q]));
+                            chunk = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                        }
+                        const bool large = chunk > most_sum || heaviest > (BF16 && !cached ? 0x1p60f : most_weight);
+                        if (again > 0 || !__any_sync(0xffffffffu, real && (large || M == -INFINITY))) {
                             if (!L::kApart && h == 0) {
                                 tmem_store16(tP, x);
                                 tmem_store16(tP + 16, x + 16);
@@ -360,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                             break;
                         }
                         if (L::kApart || h > 0) tmem_store_wait();  // stores to the same columns follow: only this orders two of them
-                        if (!(ok = follow(h, chunk))) break;
+                        if (!(ok = follow(h, large))) break;
                     }
                     if (!ok) break;
                     sum += chunk;
@@ -518,19 +560,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                 __syncwarp();
                 if (cached) {
                     if (page >= 0) copy_box(dst + (lane << A.C.shift) * DP, is_k ? &M.kc : &M.vc, 0, 0, w.h, page, bar);
-                    // the scales of 16 keys each: 0 for keys without a page
-                    const int from = __shfl_sync(0xffffffffu, page, 16 * lane >> A.C.shift & 31);
-                    if (lane < 8) {
-                        const bool there = from >= 0 && from < A.C.num_pages;
-                        const int64_t block = (16 * lane & (A.C.page_tokens() - 1)) >> A.scale_shift;
-                        copy_word(base + (is_k ? L::oKeyScale + 32 * ((gk + t - w.t0) % L::kScales) : L::oScale + 32 * at_ring) + 4 * lane,
-                                  (is_k ? A.ks : A.vs) + (there ? from * A.scale_page + w.h * A.scale_head + block * A.scale_block : 0), there);
+                    // K brings the scales of 16 keys each of both: 0 for keys without a page
+                    // or past the end
+                    const int from = __shfl_sync(0xffffffffu, page, 16 * (lane & 7) >> A.C.shift & 31);
+                    if (is_k && lane < 16) {
+                        const bool there = from >= 0 && from < A.C.num_pages && t * kTile + 16 * (lane & 7) < w.x.ctx;
+                        const int64_t block = (16 * (lane & 7) & (A.C.page_tokens() - 1)) >> A.scale_shift;
+                        copy_word(base + L::oScale + 64 * ((gk + t - w.t0) % L::kScales) + 4 * lane,
+                                  (lane < 8 ? A.ks : A.vs) + (there ? from * A.scale_page + w.h * A.scale_head + block * A.scale_block : 0), there);
                     }
                 } else if (lane < L::kHalves) {
                     // at most 64 rows, 64 columns a half
                     copy_box(dst + lane * (L::kHalf / 2), &M.k, 64 * lane, w.h, 0, w.b, bar);
                 }
-                copies_arrive(bar);
+                if (is_k) copies_arrive(bar);
             }
             const int run = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0;
             gk += run > 0 ? run : 0;
@@ -563,7 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         const uint32_t tm = (uint32_t)same((int)tmem);
         constexpr uint32_t types = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((kTile >> 4) << 24);
         constexpr uint32_t kind_n = types | ((64 >> 3) << 17);               // scores of 64 new keys
-        constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // V's rows run along the output
+        constexpr uint32_t kind_v = (1u << 4) | ((kTile >> 4) << 24) | (1u << 16) | ((DP >> 3) << 17);  // V's codes in float16; rows run along the output
+        constexpr uint32_t kind_o = types | (1u << 16) | ((DP >> 3) << 17);  // new tokens' V in its own type
         constexpr uint32_t kind_8 = (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);  // 8 bits, 32 elements a product
         uint32_t ps[2] = {0, 0}, fs[2] = {1, 1};  // phases of PReady and SFree
         int qi = 0, ki = 0;
@@ -615,7 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         };
         // Stream s's weights with the next V tile, by quarters of 32 keys.
         uint32_t vp = 0;
-        auto values = [&](int s, bool add) {
+        auto values = [&](int s, bool add, bool cached) {
+            const uint32_t kind = cached ? kind_v : kind_o;
 #pragma unroll
             for (int part = 0; part < 4; ++part) {
                 if (part == 0 || (!L::kApart && part == 2))
@@ -626,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 2; ++e)  // 16 keys each
                         mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * (2 * part + e),
-                               v0 + part * (L::kVBytes / 16) + 128 * e, kind_o, add || part + e > 0);
+                               v0 + part * (L::kVBytes / 16) + 128 * e, kind, add || part + e > 0);
                     mma_commit(base + L::oVEmpty + 8 * part);
                     if (!L::kApart && part == 1) mma_commit(base + L::oHalfDone + 8 * s);
                 }
@@ -654,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             for (int j = 0; ok && j < len; ++j) {
                 const int s = j & 1;
                 if (L::kApart && !(ok = ahead(j + 2))) break;
-                if (!(ok = values(s, j >= 2))) break;
+                if (!(ok = values(s, j >= 2, j < run))) break;
                 if (L::kApart || j + 2 >= len) done(base + L::oODone + 8 * s);
                 if (!L::kApart) ok = ahead(j + 2);
             }
@@ -668,56 +713,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         }
         __syncwarp();
     } else if (warp >= kConvertWarp) {
-        // ---- V tiles of the cache: to 16 bits, times their scales; and Q in parts. ----
+        // ---- V tiles of the cache: codes to float16; and Q in parts. ----
         Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
         if (lane == 0) w.start(A, S, plan, near);
         __syncwarp();
-        // A team is two warps: a quarter (32 keys) of every tile.  A thread takes 16 elements at the same place of every
-        // `step`-th row: the swizzle of its vectors is the same in all of them.  Of eight lanes, whose vectors go out
-        // together, four take one half of row r and four that of row r ^ 5 (with rows of 64 elements r and r + 1): their
-        // loads lie in 32 different banks, and so do both their stores.
-        constexpr int chunks = DP / 16, step = 64 / chunks, turns = 32 / step;
-        const int me = tid - 32 * kConvertWarp, team = me >> 6, you = me & 63;
-        const int c = (you & 3) + (DP == 128 ? 4 * (you >> 3 & 1) : 0);
-        const int row0 = DP == 128 ? (you >> 4) ^ ((you >> 2 & 1) * 5) : you / chunks;
-        const int c2 = 2 * c & 7, swizzle = row0 & 7;
-        const int at0 = (c >> 2) * (L::kHalf / 4) + row0 * 128 + (c2 ^ swizzle) * 16, at1 = at0 ^ 16;
-        const int from = (32 * team + row0) * DP + (DP == 128 ? c ^ swizzle : c) * 16;
+        // Two warps have a quarter (32 keys) of every tile.  Of eight lanes, whose vectors go out together, four take one half of
+        // row r and four that of row r ^ 5 (with rows of 64 elements r and r + 1): their loads of 16 codes lie in 32 different
+        // banks, and so do both their stores.
+        const int me = tid - 32 * kConvertWarp, team = me >> 6, second = me >> 5 & 1;
+        const int c = (lane & 3) + (DP == 128 ? 4 * (lane >> 3 & 1) : 0);
+        const int row0 = DP == 128 ? (lane >> 4) ^ ((lane >> 2 & 1) * 5) : lane >> 2;
+        const int c2 = 2 * c & 7;
+        const int at0 = row0 * 128 + (c2 ^ row0) * 16, from = row0 * DP + (DP == 128 ? c ^ row0 : c) * 16;  // in eight rows
         const uint32_t full = base + L::oVFull + 8 * team;
         char* const place = sm + L::oV + team * L::kVBytes;
         int g = 0;                             // V tiles of the cache so far
         uint32_t v_phase = 0, v_used = 0;      // of new tokens' copies; one is in flight
         auto convert = [&](int gi, int have) {
-            const char* const src = sm + L::oG + gi * L::kPart + from;
-            const float* const scales = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi + 2 * team;
-            const bool plain = !BF16 && fits_half(scales[0]) && fits_half(scales[1]);
-            // Two turns a pass; keys from `have` on become 0.
-            auto passes = [&](auto plain_c) {
-                constexpr bool kPlain = decltype(plain_c)::value != 0;
-#pragma unroll 1
-                for (int u = 0; u < turns; u += 2) {
-                    uint4 x[2];
-                    float f[2];
+            const char* const src = sm + L::oG + gi * L::kPart + (32 * team + 16 * second) * DP;
+            char* const to = place + (c >> 2) * (L::kHalf / 4) + 2048 * second;
+            // Eight rows in one turn (rows of 64) or two: the second takes rows 2 on, the third bit of the swizzle's.
+            constexpr int turns = DP / 32;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[e] = *reinterpret_cast<const uint4*>(src + (u + e) * (step * DP));
-                        f[e] = scales[(u + e) * step / 16];
-                        if (32 * team + row0 + (u + e) * step >= have) {
-                            x[e] = make_uint4(0, 0, 0, 0);
-                            f[e] = 0.0f;
-                        }
-                    }
+            for (int u = 0; u < turns; ++u) {
+                const int eight = DP == 128 ? u >> 1 : u, flip = DP == 128 && (u & 1) ? 2 * 128 + 2 * 16 : 0;
+                uint4 x = *reinterpret_cast<const uint4*>(src + eight * 8 * DP + (from ^ flip));
+                if (have < kTile && 32 * team + 16 * second + 8 * eight + (row0 ^ (flip != 0 ? 2 : 0)) >= have) x = make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t y[8];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        *reinterpret_cast<uint4*>(place + at0 + (u + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(x[e].x, x[e].y), f[e]);
-                        *reinterpret_cast<uint4*>(place + at1 + (u + e) * (step * 128)) = widen<BF16, kPlain>(make_uint2(x[e].z, x[e].w), f[e]);
-                    }
-                }
-            };
-            if (plain)
-                passes(Count<1>{});
-            else
-                passes(Count<0>{});
+                for (int i = 0; i < 8; ++i) y[i] = half_of_e4m3(w[i / 2] >> 16 * (i & 1));
+                *reinterpret_cast<uint4*>(to + eight * 1024 + (at0 ^ flip)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(to + eight * 1024 + (at0 ^ flip ^ 16)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
         };
         auto values = [&](int tile, int t) {
             const bool cached = t < w.x.ctx_tiles;
@@ -730,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             } else if (rows > 32 * team) {
                 // New tokens, at most 64, in their own type: rows past the end and rows that are not finite become 0, and
                 // the latter are noted.  The first warp brings them and looks.
-                if ((me & 32) == 0) {
+                if (second == 0) {
                     v_used = 1;
                     if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
                     __syncwarp();
@@ -756,14 +784,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     if (lane == 0) bad[team] = word;
                 }
             } else {
-                for (int e = you; e < L::kVBytes / 16; e += 64) *reinterpret_cast<uint4*>(place + 16 * e) = make_uint4(0, 0, 0, 0);
-                if (you == 0 && team < 2) bad[team] = 0;
+                for (int e = me & 63; e < L::kVBytes / 16; e += 64) *reinterpret_cast<uint4*>(place + 16 * e) = make_uint4(0, 0, 0, 0);
+                if ((me & 63) == 0 && team < 2) bad[team] = 0;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
                 if (cached) bar_arrive(base + L::oGEmpty + 8 * gi);
-                if (!cached && team < 2 && (me & 32) == 0) bar_arrive(base + L::oLook + 8 * ((t - w.t0) & 1));
+                if (!cached && team < 2 && second == 0) bar_arrive(base + L::oLook + 8 * ((t - w.t0) & 1));
                 bar_arrive(base + L::oVReady + 8 * team);
             }
             return true;
