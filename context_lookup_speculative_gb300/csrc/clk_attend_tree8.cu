@@ -42,9 +42,9 @@
 namespace clk {
 namespace {
 
-// 8 softmax, 2 copies, 1 products, 8 that convert (and one that fills its warpgroup)
-constexpr int kWarps = 20, kThreads = 32 * kWarps;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kConvertWarp = 12;
+// 16 softmax, 2 copies, 1 products, 4 that convert (and one that fills its warpgroup)
+constexpr int kWarps = 24, kThreads = 32 * kWarps;
+constexpr int kCopyWarp = 16, kMmaWarp = 17, kCopyWarp2 = 18, kConvertWarp = 20;
 
 template <int DP, bool BF16>
 struct Lay {
@@ -57,34 +57,35 @@ struct Lay {
     static constexpr int kParts = BF16 ? 2 : 3;            // of Q
     static constexpr int kQB = DP == 128 ? 1 : 2;          // items whose Q is held
     static constexpr int kK = DP == 128 ? (BF16 ? 3 : 2) : 6;  // K tiles in the ring (8 bits, or 64 new tokens)
-    static constexpr int kV = 4;                           // quarters of a V tile of 16 bits, 32 keys, one for each team that converts
-    static constexpr int kVBytes = kBytes / 4;
-    static constexpr int kG = DP == 128 ? 4 : 8;           // V tiles as the cache holds them
+    static constexpr int kV = DP == 128 ? 1 : 2;          // V tiles of 16 bits
+    static constexpr int kVBytes = kBytes / 4;             // 32 keys of one
+    static constexpr int kG = DP == 128 ? 4 : 6;           // V tiles as the cache holds them
     // Scales outlive their tiles: the softmax warps read them.  A place is written again when the tile kScales before is
     // weighed: the copy of a tile waits for the scores of the one kK before, which follow the weights of kK + 2.
     static constexpr int kScales = 16;
     static_assert(kScales >= kK + 2, "scales in use");
-    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oG = oV + kV * kVBytes;
+    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oG = oV + kV * kBytes;
     // after the tiles
     static constexpr int oKFull = oG + kG * kPart, oKEmpty = oKFull + 8 * kK;
-    static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 8 * kV, oVEmpty = oVReady + 8 * kV;
-    static constexpr int oGFull = oVEmpty + 8 * kV, oGEmpty = oGFull + 8 * kG;
+    static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 32, oVEmpty = oVReady + 16 * kV;  // of quarters; of halves
+    static constexpr int oGFull = oVEmpty + 16 * kV, oGEmpty = oGFull + 8 * kG;
     static constexpr int oPartsReady = oGEmpty + 8 * kG, oFactorRead = oPartsReady + 8 * kQB;
     static constexpr int oQFull = oFactorRead + 8 * kQB, oQEmpty = oQFull + 8 * kQB;
     static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
-    static constexpr int oHalfDone = oODone + 16, oLook = oHalfDone + 16;
-    static constexpr int oStatReady = oLook + 16, oDrain = oStatReady + 8;
+    static constexpr int oLook = oODone + 16, oPair = oLook + 16;
+    static constexpr int oStatReady = oPair + 64, oDrain = oStatReady + 8;
     static constexpr int oBars = oDrain + 8;  // end of the barriers
-    static constexpr int oBad = (oBars + 15) / 16 * 16;        // uint32[kV]
-    static constexpr int oScale = oBad + 4 * kV;               // float[kScales][2][8]: K's and V's, of blocks of 16 keys
+    static constexpr int oBad = (oBars + 15) / 16 * 16;        // uint32[2]
+    static constexpr int oAgree = oBad + 16;               // uint32[8][2][2]: a pair's wishes, by phases
+    static constexpr int oScale = oAgree + 128;                // float[kScales][2][8]: K's and V's, of blocks of 16 keys
     static constexpr int oFactor = oScale + 64 * kScales;      // float[kQB][128]: what a row of Q's parts is to be multiplied by
     static constexpr int oNear = oFactor + kQB * kTile * 4;    // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);
     static constexpr int oCut = oPlan + (int)sizeof(Plan);     // Cut[2]: of items that end here, that begin here
-    static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[16]: softmax and converting warps
-    static constexpr int oStop = oWalk + 16 * (int)sizeof(Walk<Trees8>), oTmem = oStop + 4;
-    static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;   // float2[2][128]
-    static constexpr int kTotal = oStat + 2 * kTile * 8;
+    static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[20]: softmax and converting warps
+    static constexpr int oStop = oWalk + 20 * (int)sizeof(Walk<Trees8>), oTmem = oStop + 4;
+    static constexpr int oStat = (oTmem + 4 + 15) / 16 * 16;   // float2[2][2][128]: of streams, of halves of their tiles
+    static constexpr int kTotal = oStat + 4 * kTile * 8;
     static_assert(kTotal <= 232448, "shared memory");
 };
 
@@ -118,31 +119,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             bar_init(base + L::oKFull + 8 * i, 1 + 32);  // the copies of a tile, and of its scales by a warp's lanes
             bar_init(base + L::oKEmpty + 8 * i, 1);
         }
-        for (int i = 0; i < L::kV; ++i) {
-            bar_init(base + L::oVFull + 8 * i, 1);
+        for (int i = 0; i < 4; ++i) bar_init(base + L::oVFull + 8 * i, 1);
+        for (int i = 0; i < 2 * L::kV; ++i) {
             bar_init(base + L::oVReady + 8 * i, 2);
             bar_init(base + L::oVEmpty + 8 * i, 1);
         }
         for (int i = 0; i < L::kG; ++i) {
             bar_init(base + L::oGFull + 8 * i, 1);
-            bar_init(base + L::oGEmpty + 8 * i, 8);
+            bar_init(base + L::oGEmpty + 8 * i, 4);
         }
         for (int i = 0; i < L::kQB; ++i) {
             bar_init(base + L::oPartsReady + 8 * i, 4);
-            bar_init(base + L::oFactorRead + 8 * i, 8);
+            bar_init(base + L::oFactorRead + 8 * i, 16);
             bar_init(base + L::oQFull + 8 * i, 1);
             bar_init(base + L::oQEmpty + 8 * i, 1 + 4);  // the products', and the warps' that split it
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(base + L::oSFull + 8 * i, 1);
-            bar_init(base + L::oSFree + 8 * i, 4);
+            bar_init(base + L::oSFree + 8 * i, 8);
             bar_init(base + L::oPHalf + 8 * i, 4);
             bar_init(base + L::oPReady + 8 * i, 4);
             bar_init(base + L::oODone + 8 * i, 1);
-            bar_init(base + L::oHalfDone + 8 * i, 1);
             bar_init(base + L::oLook + 8 * i, 2);
         }
-        bar_init(base + L::oStatReady, 8);
+        for (int i = 0; i < 8; ++i) bar_init(base + L::oPair + 8 * i, 2);
+        bar_init(base + L::oStatReady, 16);
         bar_init(base + L::oDrain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -156,16 +157,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
 
     // Every wait below tells a phase of its barrier from the one before it, and no others.  So whoever waits on a barrier
     // passes all its phases in order, and no phase ends before those have passed the one before it who wait for both.
-    // Registers: 640 threads x 96 at launch; 256 x 144 + 384 x 64 after the split.
+    // Registers: 768 threads x 80 at launch; 512 x 88 + 256 x 64 after the split.
     if (warp < kCopyWarp)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < kCopyWarp) {
-        // ---- Softmax: a thread per row. ----
-        const int s = warp >> 2, row = tid & 127;
+        // ---- Softmax: two threads per row, each with 64 of a tile's columns. ----
+        const int s = warp >> 3, h = warp >> 2 & 1, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-        const uint32_t tS = lanes + 128 * s, tO = lanes + 256 + s * DP, tP = L::kApart ? lanes + 384 + 64 * s : tS;
+        // this half's scores, the stream's sums, this half's weights
+        const uint32_t tS = lanes + 128 * s + 64 * h, tO = lanes + 256 + s * DP, tP = L::kApart ? lanes + 384 + 64 * s + 32 * h : tS;
         const int tk = row / A.group, g = row - tk * A.group;  // token of the row tile, head of the group
         const float cs = S.log2_scale;
         // A weight is p = exp2(z - M), z = x cs, with a whole number M.  V's codes are multiplied by t = p v, v the scale of
@@ -177,7 +179,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         // number where p matters, however far V's scales lie apart, takes k of -60 to 30 and M not far above the scores;
         // else p and t are computed each.
         constexpr float lift = 4.0f, lift_sum = 100.0f, most_sum = 0x1p120f, most_weight = 32768.0f;
-        uint32_t sp = 0, od = 0, look = 0;  // phases of SFull (and HalfDone), ODone, Look
+        uint32_t sp = 0, od = 0, look = 0, pp = 0;  // phases of SFull, ODone, Look, Pair
+        // The two warps with the same rows meet: < 0 if one gave up, else whether one wished.
+        auto agree = [&](bool wish) -> int {
+            const int pair = 4 * s + (warp & 3);
+            volatile uint32_t* const at = reinterpret_cast<volatile uint32_t*>(sm + L::oAgree) + 4 * pair + 2 * pp;
+            const bool any = __any_sync(0xffffffffu, wish);
+            __syncwarp();
+            if (lane == 0) {
+                at[h] = any;
+                bar_arrive(base + L::oPair + 8 * pair);
+            }
+            if (!warp_wait(base + L::oPair + 8 * pair, pp, stop)) return -1;
+            pp ^= 1;
+            return (int)(at[0] | at[1]);
+        };
+        float2* const stat = reinterpret_cast<float2*>(sm + L::oStat);
         int gi = 0, gk = 0, seg = 0;  // tiles, cached tiles and segments before this segment
         bool ok = true;
         Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[warp];
@@ -228,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     tmem_before();
                     __syncwarp();
                     if (lane == 0) {
-                        bar_arrive(base + (L::kApart ? L::oSFree : L::oPHalf) + 8 * s);
-                        bar_arrive(base + L::oPReady + 8 * s);
+                        if (L::kApart) bar_arrive(base + L::oSFree + 8 * s);
+                        bar_arrive(base + (h == 0 ? L::oPHalf : L::oPReady) + 8 * s);
                     }
                     continue;
                 }
@@ -241,184 +258,146 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     const uint32_t v = reinterpret_cast<const uint32_t*>(scales)[8 + (lane & 7)];
                     plain = __all_sync(0xffffffffu, (v & 0x7fffffu) == 0 && v >= (127u - 60 << 23) && v <= (127u + 30 << 23) && !wide);
                 }
-                // What the row sees of the tile's columns 32 c ..
+                // What the row sees of this half's columns 32 c ..
                 auto visible = [&](int c) -> uint32_t {
-                    if (!cached) return c < 2 ? (uint32_t)(seen >> (32 * c)) : 0u;
-                    const int n = most - 32 * c;
+                    if (!cached) return h == 0 ? (uint32_t)(seen >> (32 * c)) : 0u;
+                    const int n = most - 64 * h - 32 * c;
                     return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
                 };
-                // The columns' factors, 16 at a time, from 64 h on; and V's scales there.
-                const float f0 = factor * cs;
-                auto factors = [&](int h) {
-                    return cached ? make_float4(f0 * scales[h].x, f0 * scales[h].y, f0 * scales[h].z, f0 * scales[h].w) : make_float4(cs, cs, cs, cs);
-                };
-                auto units = [&](int h) { return cached ? scales[2 + h] : make_float4(1.0f, 1.0f, 1.0f, 1.0f); };
-                // Columns 64 h .. gave too large weights to some row (large), or are a row's first: M follows, and what was
-                // summed up with the old one.
-                auto follow = [&](int h, bool large) -> bool {
-                    const float4 f4 = factors(h), v4 = units(h);
-                    const float f[4] = {f4.x, f4.y, f4.z, f4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
+                // The columns' factors, 16 at a time; and V's scales there.
+                float f[4], v[4];
+                {
+                    const float4 f4 = scales[h], v4 = scales[2 + h];
+                    const float f0 = factor * cs;
+                    f[0] = cached ? f0 * f4.x : cs, f[1] = cached ? f0 * f4.y : cs, f[2] = cached ? f0 * f4.z : cs, f[3] = cached ? f0 * f4.w : cs;
+                    v[0] = cached ? v4.x : 1.0f, v[1] = cached ? v4.y : 1.0f, v[2] = cached ? v4.z : 1.0f, v[3] = cached ? v4.w : 1.0f;
+                }
+                // Some row of the pair got too large weights, or these are its first: M follows, and what was summed up with
+                // the old one.
+                auto follow = [&]() -> bool {
                     float top = -INFINITY, heavy = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < 2; ++i) {
                         uint32_t x[32];
-                        tmem_load(tS + 64 * h + 32 * i, x);
-                        const uint32_t vis = visible(2 * h + i);
+                        tmem_load(tS + 32 * i, x);
+                        const uint32_t vis = visible(i);
                         tmem_load_wait();
                         tmem_loaded(x);
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
+                            const float fq = i == 0 ? f[q] : f[2 + q], vq = i == 0 ? v[q] : v[2 + q];
                             float m = -INFINITY;
 #pragma unroll
                             for (int e = 16 * q; e < 16 * q + 16; ++e)
-                                if (vis >> e & 1) m = fmaxf(m, __uint_as_float(x[e]) * f[2 * i + q]);
+                                if (vis >> e & 1) m = fmaxf(m, __uint_as_float(x[e]) * fq);
                             top = fmaxf(top, m);
-                            heavy = fmaxf(heavy, m + __log2f(fabsf(v[2 * i + q])));
+                            heavy = fmaxf(heavy, m + __log2f(fabsf(vq)));
                         }
                     }
+                    stat[(2 * s + h) * kTile + row] = make_float2(top, heavy);
+                    if (agree(false) < 0) return false;
+                    const float2 other = stat[(2 * s + 1 - h) * kTile + row];
+                    top = fmaxf(top, other.x);
+                    heavy = fmaxf(heavy, other.y);
+                    // whole numbers: what is rescaled keeps its digits
                     const bool none = M == -INFINITY;
-                    // whole numbers; a sum beyond 2^20 has no use for a part of one
                     float m = fmaxf(ceilf(heavy) - lift, ceilf(top) - lift_sum);
-                    if (top == -INFINITY || !(none || large)) m = M;
+                    m = top == -INFINITY ? M : none ? m : fmaxf(M, m);
                     const float fix = none ? 1.0f : exp2f(M - m);
                     if (!none) sum *= fix;
                     M = m;
                     wide = M > top + 30.0f;
                     if (!__any_sync(0xffffffffu, fix != 1.0f)) return true;
-                    const bool half = !L::kApart && h > 0;
-                    if (half) {
-                        // The product with the first half's weights may be under way.  (The one of the stream's tile before
-                        // this went before these scores, and its next needs these weights: no other phase is waited for.)
-                        if (!warp_wait(base + L::oHalfDone + 8 * s, sp ^ 1, stop)) return false;
-                        tmem_after();
-                    }
-                    if (j > 0 || half) {
-                        // O is complete: weights over the scores mean that these scores' product was issued after this
-                        // stream's last P V; else it was waited for.
+                    // O is complete: weights over the scores mean that these scores' product was issued after this stream's
+                    // last P V; else it was waited for.  Each warp takes half of its columns.
+                    if (j > 0)
 #pragma unroll 1
                         for (int i = 0; i < DP / 32; ++i) {
-                            uint32_t o[32];
-                            tmem_load(tO + 32 * i, o);
+                            uint32_t o[16];
+                            const uint32_t at = tO + h * (DP / 2) + 16 * i;
+                            tmem_load16(at, o);
                             tmem_load_wait();
-                            tmem_loaded(o);
+                            tmem_loaded16(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
-                            tmem_store16(tO + 32 * i, o);
-                            tmem_store16(tO + 32 * i + 16, o + 16);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                            tmem_store16(at, o);
                         }
-                    }
-                    // weights of this tile that no product has taken yet (fix is a power of two)
-#pragma unroll 1
-                    for (int i = 0; L::kApart && i < 2 * h; ++i) {
-                        uint32_t y[16];
-                        tmem_load16(tP + 16 * i, y);
-                        tmem_load_wait();
-                        tmem_loaded16(y);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] = BF16 && !cached ? times<true>(y[e], fix) : times<false>(y[e], fix);
-                        tmem_store16(tP + 16 * i, y);
-                    }
                     tmem_store_wait();
-                    return true;
+                    return true;  // (weights are given away after the pair has met again)
                 };
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    float chunk;
-                    for (int again = 0;; ++again) {
-                        uint32_t x[64];
-                        tmem_load(tS + 64 * h, x);
-                        tmem_load(tS + 64 * h + 32, x + 32);
-                        const float4 f4 = factors(h), v4 = units(h);
-                        const float f[4] = {f4.x, f4.y, f4.z, f4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
-                        const float off = M == -INFINITY ? 0.0f : -M;
-                        float sums[4];  // of t
-                        // Weights of columns 64 h .., kPlain: seen all, V's scales powers of two.
-                        auto weigh = [&](auto plain_c) {
-                            constexpr bool kPlain = decltype(plain_c)::value != 0;
-                            float off16[4];
+                float chunk;
+                uint32_t y[32];
+                for (int again = 0;; ++again) {
+                    const float off = M == -INFINITY ? 0.0f : -M;
+                    float heaviest = 0.0f;
+                    chunk = 0.0f;
+                    // The weights; kPlain: seen all, V's scales powers of two.
+                    auto weigh = [&](auto plain_c) {
+                        constexpr bool kPlain = decltype(plain_c)::value != 0;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) off16[q] = kPlain ? off + (float)((int)(__float_as_uint(v[q]) >> 23) - 127) : off;
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t x[32];
+                            tmem_load(tS + 32 * i, x);
+                            const uint32_t vis = kPlain ? 0u : visible(i);
                             tmem_load_wait();
                             tmem_loaded(x);
-                            tmem_loaded(x + 32);
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t vis = kPlain ? 0u : visible(2 * h + i);
-                                uint32_t y[16];
+                            for (int q = 0; q < 2; ++q) {
+                                const float vq = v[2 * i + q];
+                                const uint32_t a = __float_as_uint(f[2 * i + q]);
+                                const uint32_t b = __float_as_uint(kPlain ? off + (float)((int)(__float_as_uint(vq) >> 23) - 127) : off);
+                                const uint64_t a2 = pair(a, a), b2 = pair(b, b);
+                                uint64_t part[2] = {0, 0};
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    const uint32_t a = __float_as_uint(f[2 * i + q]), b = __float_as_uint(off16[2 * i + q]);
-                                    const uint64_t a2 = pair(a, a), b2 = pair(b, b);
-                                    uint64_t part[2] = {0, 0};
-#pragma unroll
-                                    for (int e = 8 * q; e < 8 * q + 8; ++e) {
-                                        float2 z = unpair(fma2(pair(x[32 * i + 2 * e], x[32 * i + 2 * e + 1]), a2, b2));
-                                        if (!kPlain) {
-                                            if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
-                                            if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
-                                        }
-                                        float2 t = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                                        part[e & 1] = add2(part[e & 1], pair(__float_as_uint(t.x), __float_as_uint(t.y)));
-                                        if (!kPlain) {
-                                            t.x *= v[2 * i + q];
-                                            t.y *= v[2 * i + q];
-                                        }
-                                        y[e] = pack2<false>(t.x, t.y);
-                                        if (!kPlain && BF16 && !cached) y[e] = pack2<true>(t.x, t.y);
+                                for (int e = 8 * q; e < 8 * q + 8; ++e) {
+                                    float2 z = unpair(fma2(pair(x[2 * e], x[2 * e + 1]), a2, b2));
+                                    if (!kPlain) {
+                                        if (!(vis >> (2 * e) & 1)) z.x = -INFINITY;
+                                        if (!(vis >> (2 * e + 1) & 1)) z.y = -INFINITY;
                                     }
-                                    const float2 both = unpair(add2(part[0], part[1]));
-                                    sums[2 * i + q] = both.x + both.y;
+                                    float2 t = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                                    part[e & 1] = add2(part[e & 1], pair(__float_as_uint(t.x), __float_as_uint(t.y)));
+                                    if (!kPlain) {
+                                        t.x *= vq;
+                                        t.y *= vq;
+                                    }
+                                    y[16 * i + e] = pack2<false>(t.x, t.y);
+                                    if (!kPlain && BF16 && !cached) y[16 * i + e] = pack2<true>(t.x, t.y);
                                 }
-                                // (Weights over the scores: those of columns 64 h .. lie over columns 32 h .., which have been
-                                // read.  A second time these weights are stored again, so the scores must be elsewhere still.)
-                                if (L::kApart || h > 0)
-                                    tmem_store16(tP + 32 * h + 16 * i, y);
-                                else
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) x[16 * i + e] = y[e];
+                                const float2 both = unpair(add2(part[0], part[1]));
+                                const float t16 = both.x + both.y;
+                                // sums of t, and of p = t 2^-k; or the other way round
+                                heaviest = fmaxf(heaviest, kPlain ? t16 : t16 * fabsf(vq));
+                                chunk = kPlain ? fmaf(t16, __uint_as_float((254u << 23) - __float_as_uint(vq)), chunk) : chunk + t16;
                             }
-                        };
-                        float heaviest;
-                        if (plain) {
-                            weigh(Count<1>{});
-                            heaviest = fmaxf(fmaxf(sums[0], sums[1]), fmaxf(sums[2], sums[3]));
-                            // p = t 2^-k
-                            chunk = 0.0f;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) chunk = fmaf(sums[q], __uint_as_float((254u << 23) - __float_as_uint(v[q])), chunk);
-                        } else {
-                            weigh(Count<0>{});
-                            heaviest = 0.0f;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) heaviest = fmaxf(heaviest, sums[q] * fabsf(v[q]));
-                            chunk = (sums[0] + sums[1]) + (sums[2] + sums[3]);
                         }
-                        const bool large = chunk > most_sum || heaviest > (BF16 && !cached ? 0x1p60f : most_weight);
-                        if (again > 0 || !__any_sync(0xffffffffu, real && (large || M == -INFINITY))) {
-                            if (!L::kApart && h == 0) {
-                                tmem_store16(tP, x);
-                                tmem_store16(tP + 16, x + 16);
-                            }
-                            break;
-                        }
-                        if (L::kApart || h > 0) tmem_store_wait();  // stores to the same columns follow: only this orders two of them
-                        if (!(ok = follow(h, large))) break;
-                    }
+                    };
+                    if (plain)
+                        weigh(Count<1>{});
+                    else
+                        weigh(Count<0>{});
+                    const bool large = chunk > most_sum || heaviest > (BF16 && !cached ? 0x1p60f : most_weight);
+                    const int wish = agree(again == 0 && real && (large || M == -INFINITY));
+                    ok = wish >= 0;
+                    if (wish <= 0) break;
+                    ok = follow();
                     if (!ok) break;
-                    sum += chunk;
-                    if (L::kApart ? h == 1 : h == 0) {
-                        // the next scores may come; or the first half's product starts while the second half is computed
-                        if (!L::kApart) tmem_store_wait();
-                        tmem_before();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(base + (L::kApart ? L::oSFree : L::oPHalf) + 8 * s);
-                    }
+                    plain = plain && !__any_sync(0xffffffffu, wide);
                 }
                 if (!ok) break;
+                sum += chunk;
+                if (L::kApart) {
+                    // the next scores may come
+                    tmem_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(base + L::oSFree + 8 * s);
+                }
+                tmem_store16(tP, y);
+                tmem_store16(tP + 16, y + 16);
                 tmem_store_wait();
                 tmem_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(base + L::oPReady + 8 * s);
+                if (lane == 0) bar_arrive(base + (h == 0 ? L::oPHalf : L::oPReady) + 8 * s);
             }
             if (!ok) break;
             if (!has_factor && lane == 0) bar_arrive(base + L::oFactorRead + 8 * (seg % L::kQB));
@@ -439,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             const int64_t out_row = (int64_t)w.b * A.N + token;
             char* const out = static_cast<char*>(A.out) + ((out_row * A.q_heads + w.h * A.group + g) * A.dim) * 2;
             // both streams' statistics, to weigh their sums
-            float2* const stat = reinterpret_cast<float2*>(sm + L::oStat);
-            stat[s * kTile + row] = make_float2(M, sum);
+            stat[(2 * s + h) * kTile + row] = make_float2(M, sum);
             tmem_before();
             __syncwarp();
             if (lane == 0) bar_arrive(base + L::oStatReady);
             if (!(ok = warp_wait(base + L::oStatReady, 0, stop))) break;
             tmem_after();
-            const float2 a = stat[row], b = stat[kTile + row];
+            const float2 a = make_float2(stat[row].x, stat[row].y + stat[kTile + row].y);
+            const float2 b = make_float2(stat[2 * kTile + row].x, stat[2 * kTile + row].y + stat[3 * kTile + row].y);
             const float m = fmaxf(a.x, b.x);
             const float w0 = a.x == -INFINITY ? 0.0f : exp2f(a.x - m);
             const float w1 = b.x == -INFINITY ? 0.0f : exp2f(b.x - m);
@@ -454,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             // a stream without a visible key has no sum of products (or one of zeros)
             const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1
-            for (int c = s * (DP / 32); !idle && c < (s + 1) * (DP / 32); ++c) {
+            for (int c = (2 * s + h) * (DP / 64); !idle && c < (2 * s + h + 1) * (DP / 64); ++c) {
                 uint32_t o[16], o1[16] = {};
                 tmem_load16(lanes + 256 + 16 * c, o);
                 if (len > 1) tmem_load16(lanes + 256 + DP + 16 * c, o1);
@@ -491,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                                                                            __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                 }
             }
-            if (!whole && real && s == 0) W.ml[(int64_t)slot * kTile + row] = make_float2(m, l);
+            if (!whole && real && s == 0 && h == 0) W.ml[(int64_t)slot * kTile + row] = make_float2(m, l);
             // Neither stream's next sums may overwrite what the other still reads.
             tmem_before();
             __syncwarp();
@@ -657,27 +636,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             step(ki, kp, L::kK);
             return true;
         };
-        // Stream s's weights with the next V tile, by quarters of 32 keys.
+        // Stream s's weights with the next V tile, by halves of 64 keys.
+        int vi = 0;
         uint32_t vp = 0;
         auto values = [&](int s, bool add, bool cached) {
             const uint32_t kind = cached ? kind_v : kind_o;
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
-                if (part == 0 || (!L::kApart && part == 2))
-                    if (!warp_wait(base + (!L::kApart && part == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
-                if (!warp_wait(base + L::oVReady + 8 * part, vp, stop)) return false;
+            for (int half = 0; half < 2; ++half) {
+                if (!warp_wait(base + (half == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
+                if (!warp_wait(base + L::oVReady + 16 * vi + 8 * half, vp, stop)) return false;
                 tmem_after();
                 if (elect()) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)  // 16 keys each
-                        mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s : 128 * s) + 8 * (2 * part + e),
-                               v0 + part * (L::kVBytes / 16) + 128 * e, kind, add || part + e > 0);
-                    mma_commit(base + L::oVEmpty + 8 * part);
-                    if (!L::kApart && part == 1) mma_commit(base + L::oHalfDone + 8 * s);
+                    for (int e = 0; e < 4; ++e)  // 16 keys each
+                        mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s + 32 * half : 128 * s + 64 * half) + 8 * e,
+                               v0 + (4 * vi + 2 * half + e / 2) * (L::kVBytes / 16) + 128 * (e & 1), kind, add || half + e > 0);
+                    mma_commit(base + L::oVEmpty + 16 * vi + 8 * half);
                 }
                 __syncwarp();
             }
-            vp ^= 1;
+            step(vi, vp, L::kV);
             ps[s] ^= 1;
             return true;
         };
@@ -714,31 +692,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         __syncwarp();
     } else if (warp >= kConvertWarp) {
         // ---- V tiles of the cache: codes to float16; and Q in parts. ----
-        Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[8 + warp - kConvertWarp];
+        Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[16 + warp - kConvertWarp];
         if (lane == 0) w.start(A, S, plan, near);
         __syncwarp();
-        // Two warps have a quarter (32 keys) of every tile.  Of eight lanes, whose vectors go out together, four take one half of
+        // A warp has a quarter (32 keys) of every tile.  Of eight lanes, whose vectors go out together, four take one half of
         // row r and four that of row r ^ 5 (with rows of 64 elements r and r + 1): their loads of 16 codes lie in 32 different
         // banks, and so do both their stores.
-        const int me = tid - 32 * kConvertWarp, team = me >> 6, second = me >> 5 & 1;
+        const int me = tid - 32 * kConvertWarp, team = me >> 5;
         const int c = (lane & 3) + (DP == 128 ? 4 * (lane >> 3 & 1) : 0);
         const int row0 = DP == 128 ? (lane >> 4) ^ ((lane >> 2 & 1) * 5) : lane >> 2;
         const int c2 = 2 * c & 7;
         const int at0 = row0 * 128 + (c2 ^ row0) * 16, from = row0 * DP + (DP == 128 ? c ^ row0 : c) * 16;  // in eight rows
         const uint32_t full = base + L::oVFull + 8 * team;
-        char* const place = sm + L::oV + team * L::kVBytes;
         int g = 0;                             // V tiles of the cache so far
         uint32_t v_phase = 0, v_used = 0;      // of new tokens' copies; one is in flight
-        auto convert = [&](int gi, int have) {
-            const char* const src = sm + L::oG + gi * L::kPart + (32 * team + 16 * second) * DP;
-            char* const to = place + (c >> 2) * (L::kHalf / 4) + 2048 * second;
+        auto convert = [&](char* place, int gi, int have) {
+            const char* const src = sm + L::oG + gi * L::kPart + 32 * team * DP;
+            char* const to = place + (c >> 2) * (L::kHalf / 4);
             // Eight rows in one turn (rows of 64) or two: the second takes rows 2 on, the third bit of the swizzle's.
-            constexpr int turns = DP / 32;
+            constexpr int turns = DP / 16;
 #pragma unroll
             for (int u = 0; u < turns; ++u) {
                 const int eight = DP == 128 ? u >> 1 : u, flip = DP == 128 && (u & 1) ? 2 * 128 + 2 * 16 : 0;
                 uint4 x = *reinterpret_cast<const uint4*>(src + eight * 8 * DP + (from ^ flip));
-                if (have < kTile && 32 * team + 16 * second + 8 * eight + (row0 ^ (flip != 0 ? 2 : 0)) >= have) x = make_uint4(0, 0, 0, 0);
+                if (have < kTile && 32 * team + 8 * eight + (row0 ^ (flip != 0 ? 2 : 0)) >= have) x = make_uint4(0, 0, 0, 0);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                 uint32_t y[8];
 #pragma unroll
@@ -751,14 +728,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             const bool cached = t < w.x.ctx_tiles;
             const int gi = g % L::kG, rows = w.x.rows;
             if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kG & 1), stop)) return false;
-            if (!warp_wait(base + L::oVEmpty + 8 * team, (uint32_t)(tile & 1) ^ 1, stop)) return false;
+            const int vi = tile % L::kV;
+            const uint32_t phase = (uint32_t)(tile / L::kV & 1), half = 8 * (team >> 1);
+            char* const place = sm + L::oV + (4 * vi + team) * L::kVBytes;
+            if (!warp_wait(base + L::oVEmpty + 16 * vi + half, phase ^ 1, stop)) return false;
+            // What was noted of new tokens before has been looked at when both halves of the tile before are done with.
+            if (!cached && tile > 0) {
+                const int x = (tile - 1) % L::kV;
+                if (!warp_wait(base + L::oVEmpty + 16 * x + 8, (uint32_t)((tile - 1) / L::kV & 1), stop)) return false;
+            }
             if (cached) {
-                convert(gi, w.x.ctx - t * kTile);
+                convert(place, gi, w.x.ctx - t * kTile);
                 ++g;
             } else if (rows > 32 * team) {
                 // New tokens, at most 64, in their own type: rows past the end and rows that are not finite become 0, and
-                // the latter are noted.  The first warp brings them and looks.
-                if (second == 0) {
+                // the latter are noted.
+                {
                     v_used = 1;
                     if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
                     __syncwarp();
@@ -784,15 +769,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     if (lane == 0) bad[team] = word;
                 }
             } else {
-                for (int e = me & 63; e < L::kVBytes / 16; e += 64) *reinterpret_cast<uint4*>(place + 16 * e) = make_uint4(0, 0, 0, 0);
-                if ((me & 63) == 0 && team < 2) bad[team] = 0;
+                for (int e = lane; e < L::kVBytes / 16; e += 32) *reinterpret_cast<uint4*>(place + 16 * e) = make_uint4(0, 0, 0, 0);
+                if (lane == 0 && team < 2) bad[team] = 0;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
                 if (cached) bar_arrive(base + L::oGEmpty + 8 * gi);
-                if (!cached && team < 2 && second == 0) bar_arrive(base + L::oLook + 8 * ((t - w.t0) & 1));
-                bar_arrive(base + L::oVReady + 8 * team);
+                if (!cached && team < 2) bar_arrive(base + L::oLook + 8 * ((t - w.t0) & 1));
+                bar_arrive(base + L::oVReady + 16 * vi + half);
             }
             return true;
         };
@@ -868,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         int i = 0;
         bool ok = true;
         for (int seg = 0; ok && w.left > 0; ++seg) {
-            if (team < 2) ok = split(seg);
+            ok = split(seg);
             for (int t = w.t0; ok && t < w.t1; ++t, ++i) ok = values(i, t);
             __syncwarp();
             if (lane == 0) w.next(A, S, plan, near);
@@ -883,9 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
 
     // The joins run with equal shares of the registers again.
     if (warp < kCopyWarp)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
     // ---- Parts are written: raise the flag, join what was cut. ----
     tmem_before();
     __syncthreads();
