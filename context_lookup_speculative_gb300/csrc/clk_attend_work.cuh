@@ -158,10 +158,14 @@ struct Trees {
     // of 2 tiles 68.3, of 4 62.2 us.
     static constexpr int whole = 4;
 };
-// Tiles of a cache in 8 bits take half the time.
+// Tiles of a cache in 8 bits take half the time.  Measured with 3, 5 and 8 more
+// units: 64 requests of 2,000 to 32,000 tokens and 16 nodes (32/8 heads of 128)
+// 516, 511, 509 us, 256 of 300 to 4,096 and 13 nodes (24/4 heads of 64) 207,
+// 204, 192; one token over 2,048 rows 20.5, 22.6, 22.5.  Uncut items of up to 12
+// tiles made no difference.
 struct Trees8 {
     static constexpr bool prompt = false, in_log2 = true;
-    static constexpr int extra = 5, whole = 6;
+    static constexpr int extra = 8, whole = 6;
 };
 struct Prompts {
     static constexpr bool prompt = true, in_log2 = false;
