@@ -154,7 +154,7 @@ __device__ void count_blocks(const Turn& A, int64_t* before)
 }
 
 // The rows of block `unit`; threads below the block's rows take one each.
-__device__ __forceinline__ void find_rows(const Turn& A, const int64_t* before, int64_t unit, Rows& R)
+__device__ __forceinline__ void find_rows(const Turn& A, const int64_t* before, int64_t unit, Rows& R, bool report)
 {
     const int tid = threadIdx.x, T = 1 << A.shift;
     if (tid >= T) return;
@@ -182,7 +182,7 @@ __device__ __forceinline__ void find_rows(const Turn& A, const int64_t* before, 
                 q = lo * A.q_req + n * A.q_row;
                 ko = lo * A.ko_req + n * A.ko_row;
                 qo = lo * A.qo_req + n * A.qo_row;
-            } else if (blockIdx.y == 0) {
+            } else if (report) {
                 latch(A.C.status, CLK_EINVAL, x.slot);
             }
         }
@@ -201,7 +201,7 @@ __device__ __forceinline__ void find_rows(const Turn& A, const int64_t* before, 
                 ko = (x.base + r) * A.ko_row;
                 qo = (x.base + r) * A.qo_row;
                 to = page * A.page + (line + tid) * A.tok;
-            } else if (blockIdx.y == 0) {
+            } else if (report) {
                 latch(A.C.status, CLK_EINVAL, x.slot);
             }
         }
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) k_turn_any(const __grid_constant__ T
     const int e0 = (int)((int64_t)all * blockIdx.y / gridDim.y), e1 = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         __syncthreads();  // the last block's rows are done with
-        find_rows(A, before, u, R);
+        find_rows(A, before, u, R, blockIdx.y == 0);
         __syncthreads();
         for (int e = e0 + warp; e < e1; e += kWarps) {
             const Piece P = piece_of(A, e);
@@ -412,10 +412,110 @@ __device__ __forceinline__ uint2 packed8(const float* f, const Divide& by)
     return make_uint2(w[0], w[1]);
 }
 
-constexpr int kSteps = 4;  // of a warp over its 16 rows: it holds four or more at a time
+constexpr int kSteps = 4;  // vectors of a row's two halves that a lane holds at a time
 
-template <bool BF16, bool NEIGHBOURS, bool EIGHT>
-__global__ void __launch_bounds__(kThreads, 2) k_turn_rows(const __grid_constant__ Turn A)
+// Pieces of all blocks, one after the other; every CTA takes an equal run of them.
+struct Share {
+    int64_t at, end;
+    int all, e0, e1;  // pieces of a block; those taken of this one
+    __device__ Share(int64_t units, int pieces)
+    {
+        all = pieces;
+        // (units < 2^40 and gridDim.x < 2^11)
+        at = units * all * (int64_t)blockIdx.x / gridDim.x;
+        end = units * all * ((int64_t)blockIdx.x + 1) / gridDim.x;
+    }
+    __device__ bool next(int64_t* unit)
+    {
+        if (at >= end) return false;
+        *unit = at / all;
+        e0 = (int)(at - *unit * all);
+        e1 = end - at < all - e0 ? e0 + (int)(end - at) : all;
+        at += e1 - e0;
+        return true;
+    }
+};
+
+// A warp has the same rows of a block's every head, so its lanes hold their part of the table for all of them.
+template <bool BF16, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kThreads, 3) k_turn_rows(const __grid_constant__ Turn A)
+{
+    chained();
+    extern __shared__ int64_t before[];
+    __shared__ Rows R;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    count_blocks(A, before);
+    const int wide = A.dim / 16, tall = 32 / wide, j = lane % wide, r0 = lane / wide;  // lanes of a row, rows of a warp
+    const int turning = A.pairs / 8;
+    const int steps = (16 + tall - 1) / tall, groups = kWarps / steps;  // warps of a head, heads at a time
+    const int group = warp / steps, row = (warp - group * steps) * tall + r0;
+    const bool mine = r0 < tall && row < 16 && group < groups;
+    // vectors of 8 elements that this lane holds of a row
+    const int va = !NEIGHBOURS && j < turning ? j : 2 * j, vb = !NEIGHBOURS && j < turning ? j + turning : 2 * j + 1;
+    Share share(before[A.B], pieces(A));
+    for (int64_t u; share.next(&u);) {
+        __syncthreads();  // the last block's rows are done with
+        find_rows(A, before, u, R, share.e0 == 0);
+        __syncthreads();
+        if (mine && R.k[row] >= 0) {
+            float c[8], s[8];
+            if (j < turning) {
+                const float4* const cs = reinterpret_cast<const float4*>(A.table + R.pos[row] * 2 * A.pairs) + 2 * j;
+                const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1), s0 = __ldg(cs + 2 * turning), s1 = __ldg(cs + 2 * turning + 1);
+                c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+                s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+            }
+            const int64_t k = R.k[row], q = R.q[row], ko = R.ko[row], qo = R.qo[row], to = R.to[row];
+            for (int e = share.e0 + group; e < share.e1; e += kSteps * groups) {
+                uint4 a[kSteps], b[kSteps];
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    if (e + i * groups >= share.e1) break;
+                    const Piece P = piece_of(A, e + i * groups);
+                    const uint16_t* const src = P.kind == 2 ? static_cast<const uint16_t*>(A.q) + P.head * A.q_head + q
+                                                            : static_cast<const uint16_t*>(P.kind == 1 ? A.v : A.k) + P.layer * A.layer + P.head * A.k_head + k;
+                    a[i] = __ldcs(reinterpret_cast<const uint4*>(src) + va);
+                    b[i] = __ldcs(reinterpret_cast<const uint4*>(src) + vb);
+                }
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    if (e + i * groups >= share.e1) break;
+                    const Piece P = piece_of(A, e + i * groups);
+                    if (P.kind != 1 && j < turning) {
+                        float x[8], y[8];
+                        unpack<BF16>(a[i], x);
+                        unpack<BF16>(b[i], y);
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) {
+                            if (NEIGHBOURS)
+                                p < 4 ? turn(x[2 * p & 7], x[2 * p + 1 & 7], c[p], s[p]) : turn(y[2 * p & 7], y[2 * p + 1 & 7], c[p], s[p]);
+                            else
+                                turn(x[p], y[p], c[p], s[p]);
+                        }
+                        a[i] = packed<BF16>(x);
+                        b[i] = packed<BF16>(y);
+                    }
+                    if (A.pool != nullptr && P.kind != 2) {
+                        const int64_t plane = 2 * ((int64_t)A.layer0 + P.layer) + P.kind;
+                        uint4* const out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.pool) + plane * A.plane + P.head * A.head + to);
+                        out[va] = a[i];
+                        out[vb] = b[i];
+                    }
+                    uint16_t* const out = P.kind == 2 ? static_cast<uint16_t*>(A.q_out) + P.head * A.qo_head + qo
+                                          : P.kind == 0 && A.k_out != nullptr ? static_cast<uint16_t*>(A.k_out) + P.head * A.ko_head + ko : nullptr;
+                    if (out != nullptr) {
+                        reinterpret_cast<uint4*>(out)[va] = a[i];
+                        reinterpret_cast<uint4*>(out)[vb] = b[i];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// The same into 8 bits: a warp holds up to kSteps * 32 / (dim / 16) rows of a block and head, a team of them all.
+template <bool BF16, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kThreads, 2) k_turn_rows8(const __grid_constant__ Turn A)
 {
     chained();
     extern __shared__ int64_t before[];
@@ -423,22 +523,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows(const __grid_constant
     __shared__ float tops[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     count_blocks(A, before);
-    const int64_t units = before[A.B];
     const int wide = A.dim / 16, tall = 32 / wide, j = lane % wide, r0 = lane / wide;  // lanes of a row, rows at a time
     const int turning = A.pairs / 8;
     const bool mine = r0 < tall;
     // vectors of 8 elements that this lane holds of a row
     const int va = !NEIGHBOURS && j < turning ? j : 2 * j, vb = !NEIGHBOURS && j < turning ? j + turning : 2 * j + 1;
-    const int per = EIGHT ? 1 << (A.shift - 4) : 1;  // warps of a team
+    int shift = 31 - __clz(kSteps * tall);  // log2(rows of a warp)
+    shift = shift < A.shift ? shift : A.shift;
+    const int rows = 1 << shift;
+    const int per = 1 << (A.shift - shift);  // warps of a team
     const int team = warp / per, part = warp - team * per, teams = kWarps / per;
-    const int all = pieces(A);
-    const int e0 = (int)((int64_t)all * blockIdx.y / gridDim.y), e1 = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    Share share(before[A.B], pieces(A));
+    for (int64_t u; share.next(&u);) {
         __syncthreads();  // the last block's rows are done with
-        find_rows(A, before, u, R);
+        find_rows(A, before, u, R, share.e0 == 0);
         __syncthreads();
         int flip = 0;
-        for (int e = e0 + team; e < e1; e += teams, flip ^= 1) {
+        for (int e = share.e0 + team; e < share.e1; e += teams, flip ^= 1) {
             const Piece P = piece_of(A, e);
             const bool turned = P.kind != 1 && j < turning, paged = A.pool != nullptr && P.kind != 2;
             const uint16_t* const src =
@@ -450,8 +551,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows(const __grid_constant
             uint4 a[kSteps], b[kSteps];
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int r = 16 * part + i * tall + r0;
-                const int64_t from = mine && i * tall + r0 < 16 ? (P.kind == 2 ? R.q[r] : R.k[r]) : -1;
+                const int r = rows * part + i * tall + r0;
+                const int64_t from = mine && i * tall + r0 < rows ? (P.kind == 2 ? R.q[r] : R.k[r]) : -1;
                 a[i] = b[i] = make_uint4(0, 0, 0, 0);
                 if (from >= 0) {
                     a[i] = *reinterpret_cast<const uint4*>(src + from + 8 * va);
@@ -462,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows(const __grid_constant
             float top = 0.0f;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int r = 16 * part + i * tall + r0;
-                const bool real = mine && i * tall + r0 < 16 && R.k[r] >= 0;
+                const int r = rows * part + i * tall + r0;
+                const bool real = mine && i * tall + r0 < rows && R.k[r] >= 0;
                 unpack<BF16>(a[i], x[i]);
                 unpack<BF16>(b[i], y[i]);
                 if (real && turned) {
@@ -479,30 +580,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows(const __grid_constant
                             turn(x[i][p], y[i][p], c[p], s[p]);
                     }
                 }
-                if (EIGHT) {
 #pragma unroll
-                    for (int p = 0; p < 8; ++p) top = fmaxf(top, fmaxf(fabsf(x[i][p]), fabsf(y[i][p])));
-                }
+                for (int p = 0; p < 8; ++p) top = fmaxf(top, fmaxf(fabsf(x[i][p]), fabsf(y[i][p])));
             }
-            if (!EIGHT || out != nullptr) {
+            if (out != nullptr) {
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
-                    const int r = 16 * part + i * tall + r0;
-                    if (!(mine && i * tall + r0 < 16 && R.k[r] >= 0)) continue;
+                    const int r = rows * part + i * tall + r0;
+                    if (!(mine && i * tall + r0 < rows && R.k[r] >= 0)) continue;
                     const uint4 xa = packed<BF16>(x[i]), xb = packed<BF16>(y[i]);
-                    if (!EIGHT && paged) {
-                        uint16_t* const to = static_cast<uint16_t*>(A.pool) + plane * A.plane + P.head * A.head + R.to[r];
-                        *reinterpret_cast<uint4*>(to + 8 * va) = xa;
-                        *reinterpret_cast<uint4*>(to + 8 * vb) = xb;
-                    }
-                    if (out != nullptr) {
-                        uint16_t* const to = out + (P.kind == 2 ? R.qo[r] : R.ko[r]);
-                        *reinterpret_cast<uint4*>(to + 8 * va) = xa;
-                        *reinterpret_cast<uint4*>(to + 8 * vb) = xb;
-                    }
+                    uint16_t* const to = out + (P.kind == 2 ? R.qo[r] : R.ko[r]);
+                    *reinterpret_cast<uint4*>(to + 8 * va) = xa;
+                    *reinterpret_cast<uint4*>(to + 8 * vb) = xb;
                 }
             }
-            if (!EIGHT || !paged) continue;
+            if (!paged) continue;
             // ---- 8 bits: the team's largest magnitude, the scale, the codes. ----
             auto over_team = [&](float m) {
 #pragma unroll
@@ -537,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows(const __grid_constant
             const Divide by(s);
             uint8_t* const pool = static_cast<uint8_t*>(A.pool) + plane * A.plane + P.head * A.head;
             if (old != 0.0f && mine) {
-                for (int i = r0; i < 16; i += tall) {
-                    const int r = 16 * part + i;
+                for (int i = r0; i < rows; i += tall) {
+                    const int r = rows * part + i;
                     if (r >= R.first) break;
                     uint2* const p = reinterpret_cast<uint2*>(pool + R.start + r * A.tok + 16 * j);
 #pragma unroll
@@ -555,8 +647,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows(const __grid_constant
             }
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int r = 16 * part + i * tall + r0;
-                if (!(mine && i * tall + r0 < 16 && R.k[r] >= 0)) continue;
+                const int r = rows * part + i * tall + r0;
+                if (!(mine && i * tall + r0 < rows && R.k[r] >= 0)) continue;
                 *reinterpret_cast<uint2*>(pool + R.to[r] + 8 * va) = packed8(x[i], by);
                 *reinterpret_cast<uint2*>(pool + R.to[r] + 8 * vb) = packed8(y[i], by);
             }
@@ -591,19 +683,26 @@ bool fast_rows(const Turn& A, int es, bool eight)
     return true;
 }
 
+// resident: CTAs an SM, 0 for k_turn_any's grid of blocks and shares of their heads.
 template <typename K>
-int launch_turn(K kern, const Turn& A, int64_t units, cudaStream_t s)
+int launch_turn(K kern, const Turn& A, int64_t units, int resident, cudaStream_t s)
 {
     const size_t bytes = ((size_t)A.B + 1) * sizeof(int64_t);
     if (bytes > 32768 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return CLK_ECUDA;
-    // Blocks are dealt out to four CTAs an SM; where there are fewer, their heads go to several CTAs.
-    const int64_t most = 4 * (int64_t)num_sms();
     const int all = pieces(A);
-    int64_t y = most / (units < 1 ? 1 : units);
-    const int64_t useful = (all + kWarps - 1) / kWarps;
-    if (y > useful) y = useful;
-    if (y < 1) y = 1;
-    const int64_t x = units < most ? units : most;
+    int64_t x, y = 1;
+    if (resident > 0) {
+        const int64_t most = resident * (int64_t)num_sms(), useful = (all + kWarps - 1) / kWarps;
+        x = units >= most || units * useful >= most ? most : units * useful;
+    } else {
+        // Blocks are dealt out to four CTAs an SM; where there are fewer, their heads go to several CTAs.
+        const int64_t most = 4 * (int64_t)num_sms();
+        y = most / (units < 1 ? 1 : units);
+        const int64_t useful = (all + kWarps - 1) / kWarps;
+        if (y > useful) y = useful;
+        if (y < 1) y = 1;
+        x = units < most ? units : most;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(x < 1 ? 1 : x), (unsigned)y);
     cfg.blockDim = dim3(kThreads);
@@ -622,11 +721,15 @@ int launch_kind(const Turn& A, int32_t dtype, bool neighbours, int64_t units, cu
 {
     if (fast_rows(A, dtype_bytes(dtype), EIGHT)) {
         const bool bf = dtype == CLK_DTYPE_BF16;
-        if (neighbours) return bf ? launch_turn(k_turn_rows<true, true, EIGHT>, A, units, s) : launch_turn(k_turn_rows<false, true, EIGHT>, A, units, s);
-        return bf ? launch_turn(k_turn_rows<true, false, EIGHT>, A, units, s) : launch_turn(k_turn_rows<false, false, EIGHT>, A, units, s);
+#define CLK_GO(NEIGHBOURS) \
+    return bf ? launch_turn(EIGHT ? k_turn_rows8<true, NEIGHBOURS> : k_turn_rows<true, NEIGHBOURS>, A, units, EIGHT ? 2 : 3, s) \
+              : launch_turn(EIGHT ? k_turn_rows8<false, NEIGHBOURS> : k_turn_rows<false, NEIGHBOURS>, A, units, EIGHT ? 2 : 3, s)
+        if (neighbours) CLK_GO(true);
+        CLK_GO(false);
+#undef CLK_GO
     }
 #define CLK_GO(T) \
-    return neighbours ? launch_turn(k_turn_any<T, true, EIGHT>, A, units, s) : launch_turn(k_turn_any<T, false, EIGHT>, A, units, s)
+    return neighbours ? launch_turn(k_turn_any<T, true, EIGHT>, A, units, 0, s) : launch_turn(k_turn_any<T, false, EIGHT>, A, units, 0, s)
     switch (dtype) {
     case CLK_DTYPE_BF16: CLK_GO(__nv_bfloat16);
     case CLK_DTYPE_F16: CLK_GO(__half);
