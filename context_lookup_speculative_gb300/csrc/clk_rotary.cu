@@ -513,9 +513,17 @@ __global__ void __launch_bounds__(kThreads, 3) k_turn_rows(const __grid_constant
     }
 }
 
-// The same into 8 bits: a warp holds up to kSteps * 32 / (dim / 16) rows of a block and head, a team of them all.
-template <bool BF16, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kThreads, 2) k_turn_rows8(const __grid_constant__ Turn A)
+// log2(the rows of a block and head that a warp holds by `steps`)
+__host__ __device__ inline int team_shift(int dim, int steps)
+{
+    int n = 0;
+    while (2 << n <= steps * (32 / (dim / 16))) ++n;
+    return n;
+}
+
+// The same into 8 bits: a warp holds rows of a block and head, a team of at most kWarps warps them all.
+template <bool BF16, bool NEIGHBOURS, int STEPS>
+__global__ void __launch_bounds__(kThreads, STEPS == 2 ? 3 : 2) k_turn_rows8(const __grid_constant__ Turn A)
 {
     chained();
     extern __shared__ int64_t before[];
@@ -528,10 +536,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows8(const __grid_constan
     const bool mine = r0 < tall;
     // vectors of 8 elements that this lane holds of a row
     const int va = !NEIGHBOURS && j < turning ? j : 2 * j, vb = !NEIGHBOURS && j < turning ? j + turning : 2 * j + 1;
-    int shift = 31 - __clz(kSteps * tall);  // log2(rows of a warp)
-    shift = shift < A.shift ? shift : A.shift;
+    const int shift = min(team_shift(A.dim, STEPS), A.shift);  // log2(rows of a warp)
     const int rows = 1 << shift;
     const int per = 1 << (A.shift - shift);  // warps of a team
+    if (per > kWarps) return;  // (the host chose STEPS so that they are not)
     const int team = warp / per, part = warp - team * per, teams = kWarps / per;
     Share share(before[A.B], pieces(A));
     for (int64_t u; share.next(&u);) {
@@ -548,9 +556,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows8(const __grid_constan
             uint16_t* const out = P.kind == 2 ? static_cast<uint16_t*>(A.q_out) + P.head * A.qo_head
                                   : P.kind == 0 && A.k_out != nullptr ? static_cast<uint16_t*>(A.k_out) + P.head * A.ko_head : nullptr;
             const int64_t plane = 2 * ((int64_t)A.layer0 + P.layer) + P.kind;
-            uint4 a[kSteps], b[kSteps];
+            uint4 a[STEPS], b[STEPS];
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
+            for (int i = 0; i < STEPS; ++i) {
                 const int r = rows * part + i * tall + r0;
                 const int64_t from = mine && i * tall + r0 < rows ? (P.kind == 2 ? R.q[r] : R.k[r]) : -1;
                 a[i] = b[i] = make_uint4(0, 0, 0, 0);
@@ -559,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows8(const __grid_constan
                     b[i] = *reinterpret_cast<const uint4*>(src + from + 8 * vb);
                 }
             }
-            float x[kSteps][8], y[kSteps][8];
+            float x[STEPS][8], y[STEPS][8];
             float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
+            for (int i = 0; i < STEPS; ++i) {
                 const int r = rows * part + i * tall + r0;
                 const bool real = mine && i * tall + r0 < rows && R.k[r] >= 0;
                 unpack<BF16>(a[i], x[i]);
@@ -585,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows8(const __grid_constan
             }
             if (out != nullptr) {
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
+                for (int i = 0; i < STEPS; ++i) {
                     const int r = rows * part + i * tall + r0;
                     if (!(mine && i * tall + r0 < rows && R.k[r] >= 0)) continue;
                     const uint4 xa = packed<BF16>(x[i]), xb = packed<BF16>(y[i]);
@@ -605,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows8(const __grid_constan
             if (!(top <= FLT_MAX)) {  // infinities do not count
                 top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i)
+                for (int i = 0; i < STEPS; ++i)
 #pragma unroll
                     for (int p = 0; p < 8; ++p) {
                         if (fabsf(x[i][p]) <= FLT_MAX) top = fmaxf(top, fabsf(x[i][p]));
@@ -646,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_turn_rows8(const __grid_constan
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
+            for (int i = 0; i < STEPS; ++i) {
                 const int r = rows * part + i * tall + r0;
                 if (!(mine && i * tall + r0 < rows && R.k[r] >= 0)) continue;
                 *reinterpret_cast<uint2*>(pool + R.to[r] + 8 * va) = packed8(x[i], by);
@@ -721,10 +729,14 @@ int launch_kind(const Turn& A, int32_t dtype, bool neighbours, int64_t units, cu
 {
     if (fast_rows(A, dtype_bytes(dtype), EIGHT)) {
         const bool bf = dtype == CLK_DTYPE_BF16;
-#define CLK_GO(NEIGHBOURS) \
-    return bf ? launch_turn(EIGHT ? k_turn_rows8<true, NEIGHBOURS> : k_turn_rows<true, NEIGHBOURS>, A, units, EIGHT ? 2 : 3, s) \
-              : launch_turn(EIGHT ? k_turn_rows8<false, NEIGHBOURS> : k_turn_rows<false, NEIGHBOURS>, A, units, EIGHT ? 2 : 3, s)
-        if (neighbours) CLK_GO(true);
+        const bool two = EIGHT && A.shift - team_shift(A.dim, 2) <= 3;  // 2^3 warps
+#define CLK_GO(NEIGHBOURS)                                                                                                      \
+    if (!EIGHT) return launch_turn(bf ? k_turn_rows<true, NEIGHBOURS> : k_turn_rows<false, NEIGHBOURS>, A, units, 3, s);        \
+    if (two) return launch_turn(bf ? k_turn_rows8<true, NEIGHBOURS, 2> : k_turn_rows8<false, NEIGHBOURS, 2>, A, units, 3, s);   \
+    return launch_turn(bf ? k_turn_rows8<true, NEIGHBOURS, 4> : k_turn_rows8<false, NEIGHBOURS, 4>, A, units, 2, s)
+        if (neighbours) {
+            CLK_GO(true);
+        }
         CLK_GO(false);
 #undef CLK_GO
     }
