@@ -403,12 +403,12 @@ __device__ __forceinline__ uint4 packed(const float* f)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint2 packed8(const float* f, const Divide& by)
+__device__ __forceinline__ uint2 packed8(const float* f)
 {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        w[i] = to_e4m3(by(f[4 * i]), by(f[4 * i + 1])) | to_e4m3(by(f[4 * i + 2]), by(f[4 * i + 3])) << 16;
+        w[i] = to_e4m3(f[4 * i], f[4 * i + 1]) | to_e4m3(f[4 * i + 2], f[4 * i + 3]) << 16;
     return make_uint2(w[0], w[1]);
 }
 
@@ -588,8 +588,10 @@ __global__ void __launch_bounds__(kThreads, STEPS == 2 ? 3 : 2) k_turn_rows8(con
                             turn(x[i][p], y[i][p], c[p], s[p]);
                     }
                 }
+                if (paged) {
 #pragma unroll
-                for (int p = 0; p < 8; ++p) top = fmaxf(top, fmaxf(fabsf(x[i][p]), fabsf(y[i][p])));
+                    for (int p = 0; p < 8; ++p) top = fmaxf(top, fmaxf(fabsf(x[i][p]), fabsf(y[i][p])));
+                }
             }
             if (out != nullptr) {
 #pragma unroll
@@ -648,17 +650,28 @@ __global__ void __launch_bounds__(kThreads, STEPS == 2 ? 3 : 2) k_turn_rows8(con
                         from_e4m3x4(w.x, f);
                         from_e4m3x4(w.y, f + 4);
 #pragma unroll
-                        for (int i2 = 0; i2 < 8; ++i2) f[i2] *= old;
-                        p[h] = packed8(f, by);
+                        for (int i2 = 0; i2 < 8; ++i2) f[i2] = by(f[i2] * old);
+                        p[h] = packed8(f);
                     }
                 }
+            }
+            if (by.whole) {
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) x[i][p] *= by.inv, y[i][p] *= by.inv;
+            } else {
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) x[i][p] = by(x[i][p]), y[i][p] = by(y[i][p]);
             }
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
                 const int r = rows * part + i * tall + r0;
                 if (!(mine && i * tall + r0 < rows && R.k[r] >= 0)) continue;
-                *reinterpret_cast<uint2*>(pool + R.to[r] + 8 * va) = packed8(x[i], by);
-                *reinterpret_cast<uint2*>(pool + R.to[r] + 8 * vb) = packed8(y[i], by);
+                *reinterpret_cast<uint2*>(pool + R.to[r] + 8 * va) = packed8(x[i]);
+                *reinterpret_cast<uint2*>(pool + R.to[r] + 8 * vb) = packed8(y[i]);
             }
         }
     }
