@@ -173,12 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         // A weight is p = exp2(z - M), z = x cs, with a whole number M.  V's codes are multiplied by t = p v, v the scale of
         // their 16 keys, in float16.  Where v = 2^k, t = exp2(z + k - M) comes out of the exponential itself, and the sum of
         // p is that of t times 2^-k: no multiplication an element.  M follows a row where its weights have grown too large;
-        // up to there size costs no precision in floating point.  (The largest t starts at up to 2^4, so that small weights
-        // keep their bits, and may grow to where 16 of them add up to 2^15.  What is below 2^-25 is lost: the largest t's
-        // 2^-28 a key.)  The largest p starts at up to 2^100: V's scales may be as small as 2^-100.  That t stays a normal
-        // number where p matters, however far V's scales lie apart, takes k of -60 to 30 and M not far above the scores;
-        // else p and t are computed each.
-        constexpr float lift = 4.0f, lift_sum = 100.0f, most_sum = 0x1p120f, most_weight = 32768.0f;
+        // up to there size costs no precision in floating point.  (The largest t starts at 2^5 to 2^6, so that small weights
+        // keep their bits, and may grow to where 16 of them add up to 2^15.  Rounding loses at most 2^-25 a key: 2^-30 of
+        // the largest.  Starting at 2^4, 2^6 and 2^7 measured 507, 511, 520 us with 64 requests of 2,000 to 32,000 tokens.)
+        // The largest p starts at up to 2^100: V's scales may be as small as 2^-100.  That t stays a normal number where p
+        // matters, however far V's scales lie apart, takes k of -60 to 30 and M not far above the scores; else p and t are
+        // computed each.
+        constexpr float lift = 6.0f, lift_sum = 100.0f, most_sum = 0x1p120f, most_weight = 32768.0f;
         uint32_t sp = 0, od = 0, look = 0, pp = 0;  // phases of SFull, ODone, Look, Pair
         // The two warps with the same rows meet: < 0 if one gave up, else whether one wished.
         auto agree = [&](bool wish) -> int {

@@ -814,12 +814,14 @@ CLK_API int clk_prompt_attend(const clk_attn* a, const int64_t* d_off, int32_t B
 /* The two attentions over a pool of 8 bits: a->dtype is q's, the new tokens' and
  * out's type, the pool is CLK_DTYPE_E4M3, and each cached element is its
  * value times its block's scale.  On the tensor cores (16-bit types, dim a
- * multiple of 16 up to 128) that is rounded to a->dtype for the products
- * (trees: V's only), which changes nothing where scales are powers of two in
- * the type's range, as clk_cache_append_rotary makes them; and for trees q's
- * elements are held to 9 bits (bfloat16; its own are 8) or 14 (float16; 11),
- * or to 2^-18 of the row's largest where that is more.  Everything else is as
- * without scales. */
+ * multiple of 16 up to 128) prompts round that to a->dtype for the products,
+ * which changes nothing where scales are powers of two in the type's range, as
+ * clk_cache_append_rotary makes them.  Trees multiply the values as they are:
+ * q's elements are held to 9 bits (bfloat16; its own are 8) or 14 (float16;
+ * 11), or to 2^-18 of the row's largest where that is more, and weights of
+ * cached tokens, times V's scales, to float16, their largest at 2^5 or more;
+ * V's scales may be any from 2^-100 to 2^90.  Everything else is as without
+ * scales. */
 CLK_API int clk_tree_attend_scaled(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool,
                                    const clk_scales* scales, int32_t layer, const clk_attn* a, int32_t N,
                                    const int32_t* d_nodes, const int64_t* d_mask, const int32_t* d_ctx, void* d_scratch,

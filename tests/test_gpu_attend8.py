@@ -125,6 +125,27 @@ def test_scales_far_from_one():
         t.run().check()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lo,hi,odd", [(-100, 60, False), (-100, -100, False), (40, 60, False), (-60, 30, False), (-40, 40, True)])
+def test_v_scales_far_apart(lo, hi, odd, D, monkeypatch):
+    """V's scales from 2^lo to 2^hi within a request (odd: no powers of two, some negative).  A weight times its scale
+    is rounded to float16, by half a step of 2^-24 at least where the largest is 2^5 or more: over all keys at most
+    keys * 2^-30 * 448 times the largest scale."""
+    import test_gpu_attend
+
+    t = Tree8(abs(D + hi), 2, 5, [700, 260], 3, 2, D, 32, "bf16", nodes=[5, 2], T=16)
+    g = torch.Generator(device="cuda").manual_seed(hi)
+    v = t.pool8.scale[1]
+    v.copy_(torch.exp2(torch.randint(lo, hi + 1, v.shape, generator=g, device="cuda").float()))
+    if odd:
+        v.mul_(torch.rand(v.shape, generator=g, device="cuda") * 2.5 - 1)
+    t.pool = (t.pool8.data.double().unflatten(3, (2, 16)) * t.pool8.scale[..., None, None].double()).flatten(3, 4)
+    more = 2.0 ** -30 * 448 * float(v.abs().max())
+    monkeypatch.setattr(test_gpu_attend, "tolerance", lambda kind, ref, size, keys, vmax: tolerance(kind, ref, size, keys, vmax) + keys * more)
+    t.k.mul_(4)
+    t.run().check()
+
+
 def test_large_scores():
     for kind, D in (("bf16", 64), ("f16", 128)):
         t = Tree8(5, 2, 4, [700, 300], 2, 1, D, 16, kind, nodes=[4, 4], amp=8.0)
