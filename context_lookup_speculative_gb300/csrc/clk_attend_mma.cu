@@ -834,36 +834,40 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 const char* const src = sm + L::oG + gi * L::kPart + from;
                 const float* const all = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
                 char* const to = dst + (c >> 2) * next;
-                const bool plain = !BF16 && __all_sync(0xffffffffu, fits_half(all[lane & 7]));
+                const bool plain = __all_sync(0xffffffffu, fits<BF16>(all[lane & 7]));
                 // Two turns a pass, the next pass's codes on their way.  (All of them unrolled were 10 KB of instructions,
                 // which with the softmax's do not stay in the instruction cache: three quarters of the requests hit, and
                 // every warp waited: 64 requests 636 us.)
-                uint4 x[2];
-                float f[2];
-                auto load = [&](int u) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[e] = *reinterpret_cast<const uint4*>(src + (u + e) * (step * DP));
-                        f[e] = all[4 * team + (u + e) * step / 16];
-                        if (64 * team + row0 + (u + e) * step >= have) {
-                            x[e] = make_uint4(0, 0, 0, 0);
-                            f[e] = 0.0f;
-                        }
-                    }
-                };
                 auto passes = [&](auto plain_c) {
                     constexpr bool kPlain = decltype(plain_c)::value != 0;
+                    constexpr int pass = kPlain ? 2 : 1;
+                    uint4 x[pass];
+                    float f[pass];
+                    auto load = [&](int u) {
+#pragma unroll
+                        for (int e = 0; e < pass; ++e) {
+                            x[e] = *reinterpret_cast<const uint4*>(src + (u + e) * (step * DP));
+                            f[e] = all[4 * team + (u + e) * step / 16];
+                            if (have < kTile && 64 * team + row0 + (u + e) * step >= have) {
+                                x[e] = make_uint4(0, 0, 0, 0);
+                                f[e] = 0.0f;
+                            }
+                        }
+                    };
                     load(0);
 #pragma unroll 1
-                    for (int u = 0; u < turns; u += 2) {
-                        const uint4 y[2] = {x[0], x[1]};
-                        const float h[2] = {f[0], f[1]};
-                        if (u + 2 < turns) load(u + 2);
+                    for (int u = 0; u < turns; u += pass) {
+                        uint4 y[pass];
+                        float h[pass];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int e = 0; e < pass; ++e) y[e] = x[e], h[e] = f[e];
+                        if (u + pass < turns) load(u + pass);
+#pragma unroll
+                        for (int e = 0; e < pass; ++e) {
                             char* const row = to + (u + e) * (step * 128);
-                            *reinterpret_cast<uint4*>(row + at0) = widen<BF16, kPlain>(make_uint2(y[e].x, y[e].y), h[e]);
-                            *reinterpret_cast<uint4*>(row + at1) = widen<BF16, kPlain>(make_uint2(y[e].z, y[e].w), h[e]);
+                            const uint32_t mult = pack2<BF16>(h[e], h[e]);
+                            *reinterpret_cast<uint4*>(row + at0) = widen<BF16, kPlain>(make_uint2(y[e].x, y[e].y), h[e], mult);
+                            *reinterpret_cast<uint4*>(row + at1) = widen<BF16, kPlain>(make_uint2(y[e].z, y[e].w), h[e], mult);
                         }
                     }
                 };
@@ -881,21 +885,34 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             const bool brings = (warp & 1) == 0;  // the team's half of new tokens' V tiles; the first team K tiles too
             // places with copies (bits 0 .. of K, 16 .. of V) and the phase that ends the last (8 .., 24 ..)
             uint32_t copies = 0;
-            auto keys = [&](int tile, int t) {
-                const int ki = tile % L::kK;
-                const uint32_t full = base + L::oKFull + 8 * ki;
-                const bool cached = t < w.x.ctx_tiles;
-                const int gi = g % L::kGs;
-                if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
-                if (!warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(tile / L::kK & 1) ^ 1, stop)) return false;
-                if (cached) {
-                    convert(gi, sm + L::oK + ki * L::kBytes + team * (64 * 128), L::kHalf, kTile);
+            // A tile of the cache: K, then V.  With rows of 64 the conversion's instructions are there once, with rows of 128
+            // twice: 8 prompts of 100 to 1,500 tokens behind up to 8,192 (24/4 heads of 64) 343 and 376 us, 4,000 tokens
+            // behind 25,000 (32/8 heads of 128) 1,842 and 1,757.
+            auto both = [&](int tile, int t) {
+                const int ki = tile % L::kK, at = 2 * tile + team, vi = at % L::kV;
+#pragma unroll(DP == 64 ? 1 : 2)
+                for (int v = 0; v < 2; ++v) {
+                    const int gi = g % L::kGs;
+                    const uint32_t empty = v == 0 ? base + L::oKEmpty + 8 * ki : base + L::oVEmpty + 8 * vi;
+                    const int turn = v == 0 ? tile / L::kK : at / L::kV;
+                    if (!warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
+                    if (!warp_wait(empty, (uint32_t)(turn & 1) ^ 1, stop)) return false;
+                    convert(gi, sm + (v == 0 ? L::oK + ki * L::kBytes + team * (64 * 128) : L::oV + vi * L::kVBytes),
+                            v == 0 ? L::kHalf : L::kHalf / 2, v == 0 ? kTile : w.x.ctx - t * kTile);
                     if (lane == 0) {
-                        bar_arrive(full);
+                        bar_arrive(v == 0 ? base + L::oKFull + 8 * ki : base + L::oVReady + 8 * vi);
                         bar_arrive(base + L::oGEmpty + 8 * gi);
                     }
                     ++g;
-                } else if (warp != kConvertWarp) {
+                }
+                return true;
+            };
+            // A tile of new tokens.
+            auto keys = [&](int tile, int t) {
+                const int ki = tile % L::kK;
+                const uint32_t full = base + L::oKFull + 8 * ki;
+                if (!warp_wait(base + L::oKEmpty + 8 * ki, (uint32_t)(tile / L::kK & 1) ^ 1, stop)) return false;
+                if (warp != kConvertWarp) {
                     if (lane == 0) bar_arrive(full);
                 } else {
                     copies = (copies & ~(0x100u << ki)) | 1u << ki | (uint32_t)(tile / L::kK & 1) << (8 + ki);
@@ -908,22 +925,12 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 return true;
             };
             auto values = [&](int tile, int t) {
-                const bool cached = t < w.x.ctx_tiles;
-                const int gi = g % L::kGs, n0 = (t - w.x.ctx_tiles) * kTile;
-                const int have = cached ? w.x.ctx - t * kTile : w.x.rows - n0;
+                const int n0 = (t - w.x.ctx_tiles) * kTile, have = w.x.rows - n0;
                 const int at = 2 * tile + team, vi = at % L::kV;
                 const uint32_t full = base + L::oVFull + 8 * vi;
                 char* const place = sm + L::oV + vi * L::kVBytes;
-                if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
                 if (!warp_wait(base + L::oVEmpty + 8 * vi, (uint32_t)(at / L::kV & 1) ^ 1, stop)) return false;
-                if (cached) {
-                    convert(gi, place, L::kHalf / 2, have);
-                    if (lane == 0) {
-                        bar_arrive(base + L::oVReady + 8 * vi);
-                        bar_arrive(base + L::oGEmpty + 8 * gi);
-                    }
-                    ++g;
-                } else if (have > 64 * team) {
+                if (have > 64 * team) {
                     // (the V warp hands it on)
                     if (brings) {
                         copies ^= (copies >> (16 + vi) & 1) << (24 + vi);
@@ -945,7 +952,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 return true;
             };
             while (ok && w.left > 0) {
-                for (int t = w.t0; ok && t < w.t1; ++t, ++i) ok = keys(i, t) && values(i, t);
+                for (int t = w.t0; ok && t < w.t1; ++t, ++i) ok = t < w.x.ctx_tiles ? both(i, t) : keys(i, t) && values(i, t);
                 __syncwarp();
                 if (lane == 0) w.next(A, S, plan, near);
                 __syncwarp();

@@ -3,27 +3,42 @@
 //
 // Items, shares and joins are those of clk_attend_work.cuh, rows and streams
 // those of the kernel over 16 bits (clk_attend_mma.cu): rows are (token, head
-// of the group) pairs, and two groups of four softmax warps take alternate
-// tiles of 128 keys.
+// of the group) pairs, and two groups of softmax warps take alternate tiles of
+// 128 keys.
 //
-// K goes to the tensor cores as the cache holds it: scores are the sum of
-// products of 8 bits with Q in two parts (bfloat16) or three (float16), each
-// the rounding to 8 bits of what the parts before it leave of the row over its
-// own power of two.  Such products are exact and are summed in float32.  A
-// block's scale and the row's power of two multiply the scores in the softmax.
-// V is brought to 16 bits by eight warps, times its scales: weights are too
-// far apart for parts of 8 bits.  New tokens' K and V stay in their own type.
+// Nothing that the cache holds is multiplied by its scale.  K goes to the
+// tensor cores as it is: scores are the sum of products of 8 bits with Q in two
+// parts (bfloat16) or three (float16), each the rounding to 8 bits of what the
+// parts before it leave of the row over its own power of two.  Such products
+// are exact and are summed in float32.  K's scale and the row's power of two
+// multiply the scores in the softmax.  V's codes become float16, which holds
+// them exactly (one instruction a pair), and its scales go into the weights,
+// where a power of two costs nothing: it is part of the exponent.  (Multiplied
+// into V instead, V took four times the instructions, and with K in 16 bits too
+// eight: 64 requests of 2,000 to 32,000 tokens, 32/8 heads of 128, 1,083 us
+// with both in 16 bits, 640 and after some steps 511 with V alone, 512 so.)
+// New tokens' K and V stay in their own type.
 //
-// What bounds it: beside a tile's 32 KB from DRAM (rows of 128) shared memory
-// passes them in, once more to those who convert V and 32 KB back, 32 KB to the
-// products with P and 64 KB (96 KB) to those with Q's parts: 176 KB (208 KB),
-// 1,375 (1,625) cycles at 128 bytes a cycle, where DRAM needs 1,400.
+// A row's 128 columns belong to two threads in two warps, so that a tile's
+// weights take half as long: each has its own sum, but both have the reference
+// M, which O shares.  So the pair meets once a tile before it gives its weights
+// away; where a row of either asks for it, both take up the new M.  (With one
+// thread a row eight requests of 262,144 tokens took 322 us, with two 278; 256
+// of 300 to 4,096 tokens with heads of 64, though, 185 and 198.)
 //
-// The code of all roles has to stay in the instruction cache, which the
-// unrolled loops of the 16-bit kernel together with a conversion did not:
-// three quarters of the fetches hit and everything waited.  So a softmax thread
-// goes through its row by 32 columns at a time, twice (maximum, weights), in
-// loops, with which all threads fit 96 registers.
+// What bounds it: 128 keys of 128 elements take DRAM 1,400 cycles of an SM.  The
+// products take 1,050 (bfloat16; 1,300 float16), those with Q's parts from
+// shared memory as long as it needs to pass their operands; shared memory as a
+// whole passes 176 KB (208 KB) at 128 bytes a cycle, 1,375 (1,625).  A tile
+// measures 2,300: a stream's scores wait for its products with V (they lie where
+// the weights were), its softmax (some 2,300 cycles, of which 900 are weights
+// and the rest waits, loads of scales, the meeting and the way to tensor memory)
+// for the scores, and two streams do not quite fill that.  With heads of 64 the
+// tile's fixed costs are the same and its bytes half.
+//
+// The code of all roles has to stay in the instruction cache; where loops of
+// the conversion were unrolled, three quarters of the fetches hit and everything
+// waited.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -2,6 +2,7 @@
 // the nearest (ties to even) and take what is beyond the range to the largest.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -50,23 +51,32 @@ __device__ __forceinline__ float scale_for(float top)
 }
 
 // Eight codes as elements of the products' type, times their scale: rounded once (exact for scales that are powers
-// of two in the type's range).  PLAIN: float16, and a scale that float16 holds.
-__device__ __forceinline__ bool fits_half(float scale) { return __half2float(__float2half_rn(scale)) == scale; }
+// of two in the type's range).  PLAIN: a scale that the type holds, which is `mult` twice.  (A product is then one
+// instruction a pair, and the same: codes are exact in both types.)
+template <bool BF16>
+__device__ __forceinline__ bool fits(float scale)
+{
+    if (BF16) return (__float_as_uint(scale) & 0xffffu) == 0;
+    return __half2float(__float2half_rn(scale)) == scale;
+}
 
 template <bool BF16, bool PLAIN>
-__device__ __forceinline__ uint4 widen(uint2 codes, float scale)
+__device__ __forceinline__ uint4 widen(uint2 codes, float scale, uint32_t mult)
 {
     uint32_t y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t h = half_of_e4m3((i < 2 ? codes.x : codes.y) >> 16 * (i & 1));
-        if (PLAIN) {
-            const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(scale));
+        const float2 f = halves(h);
+        if (!PLAIN) {
+            y[i] = pack2<BF16>(f.x * scale, f.y * scale);
+        } else if (BF16) {
+            const uint32_t w = pack2<true>(f.x, f.y);
+            const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&mult));
             y[i] = *reinterpret_cast<const uint32_t*>(&p);
         } else {
-            const float2 f = halves(h), p = unpair(mul2(pair(__float_as_uint(f.x), __float_as_uint(f.y)),
-                                                        pair(__float_as_uint(scale), __float_as_uint(scale))));
-            y[i] = pack2<BF16>(p.x, p.y);
+            const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&mult));
+            y[i] = *reinterpret_cast<const uint32_t*>(&p);
         }
     }
     return make_uint4(y[0], y[1], y[2], y[3]);

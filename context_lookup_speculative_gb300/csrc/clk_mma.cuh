@@ -75,34 +75,6 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const void* src, bool th
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
-// 16 bytes, past L1.
-__device__ __forceinline__ void copy_vector(uint32_t dst, const void* src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-
-// This thread's copies so far are a group; waits for all groups but the last N.
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint4 shared_vector(uint32_t at)
-{
-    uint4 x;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
-    return x;
-}
-
-__device__ __forceinline__ float shared_word(uint32_t at)
-{
-    float x;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
-    return x;
-}
-
 // Arrives on bar once the copy_words that this thread issued so far are done.
 __device__ __forceinline__ void copies_arrive(uint32_t bar)
 {
