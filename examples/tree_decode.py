@@ -16,7 +16,11 @@ that cached prefix.  Then every step
 
 At the end half of the requests are freed and the pool is compacted.
 
-    python examples/tree_decode.py [--requests 4] [--document 600] [--tokens 64] [--no-tree]
+With --cache8 the pages hold 8-bit values with scales, and the calls rotate:
+prompts' queries and keys on their way into the pages (cache_append_rotary), a
+step's at their nodes' positions (tree_rotate).
+
+    python examples/tree_decode.py [--requests 4] [--document 600] [--tokens 64] [--no-tree] [--cache8]
 """
 from __future__ import annotations
 
@@ -58,13 +62,15 @@ class Target:
         u, v = x.float().chunk(2, -1)
         return torch.cat([u * c - v * s, u * s + v * c], -1).to(self.dtype)
 
-    def forward(self, tok, pos, attend):
-        """Logits of tok at pos; attend(layer, q, k, v) is the attention."""
+    def forward(self, tok, pos, attend, turned=True):
+        """Logits of tok at pos; attend(layer, q, k, v) is the attention (not turned: it rotates q and k itself)."""
         h = self.embed[tok.long()]
         for i in range(self.layers):
             x = torch.nn.functional.rms_norm(h, h.shape[-1:])
             q, k, v = (x @ self.qkv[i]).unflatten(-1, (-1, self.dim)).split([self.q_heads, self.kv_heads, self.kv_heads], -2)
-            o = attend(i, self.rotate(q, pos), self.rotate(k, pos), v)
+            if turned:
+                q, k = self.rotate(q, pos), self.rotate(k, pos)
+            o = attend(i, q, k, v)
             h = h + o.flatten(-2) @ self.proj[i]
         return torch.nn.functional.rms_norm(h, h.shape[-1:]).float() @ self.head.float()
 
@@ -72,12 +78,13 @@ class Target:
 class Decoder:
     """The target's cache, the lookup's histories and the buffers of a step."""
 
-    def __init__(self, target, max_slots, max_tokens, page_tokens=16, pages=None):
+    def __init__(self, target, max_slots, max_tokens, page_tokens=16, pages=None, cache8=False):
         self.t = target
         per = -(-max_tokens // page_tokens)
         self.cache = clk.Cache(max_slots, per, pages or max_slots * per, page_tokens)
-        self.pool = torch.zeros((2 * target.layers, self.cache.num_pages, target.kv_heads, page_tokens, target.dim),
-                                dtype=target.dtype, device="cuda")
+        shape = (target.layers, self.cache.num_pages, target.kv_heads, page_tokens, target.dim)
+        self.rotary = clk.Rotary.of(target.freq, max_tokens) if cache8 else None
+        self.pool = clk.ScaledPool.empty(*shape) if cache8 else torch.zeros((2 * shape[0],) + shape[1:], dtype=target.dtype, device="cuda")
         self.lookup = clk.Lookup(max_slots, max_tokens + NODES, target.vocab)
         self.scratch = clk.attend_scratch(target.q_heads, target.kv_heads, target.dim)
         self.scale = 1 / math.sqrt(target.dim)
@@ -96,14 +103,18 @@ class Decoder:
         clk.cache_grow(self.cache, slots, count)
 
         def attend(layer, q, k, v):
-            out = torch.empty_like(q)
+            out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+            if self.rotary is not None:  # q and k are rotated where they are
+                clk.cache_append_rotary(self.cache, slots, self.pool, k[None], v[None], count, rotary=self.rotary, layer=layer,
+                                        offsets=off, q=q, q_out=q, k_out=k[None])
             clk.prompt_attend(q, k, v, off, self.scale, out, self.scratch, cache=self.cache, slots=slots, pool=self.pool,
                               layer=layer, ctx=ctx)
-            clk.cache_append(self.cache, slots, self.pool, k[None].contiguous(), v[None].contiguous(), count, layer=layer,
-                             offsets=off)
+            if self.rotary is None:
+                clk.cache_append(self.cache, slots, self.pool, k[None].contiguous(), v[None].contiguous(), count, layer=layer,
+                                 offsets=off)
             return out
 
-        return t.forward(tok, pos, attend)[off[1:] - 1].argmax(-1).to(torch.int32)
+        return t.forward(tok, pos, attend, self.rotary is None)[off[1:] - 1].argmax(-1).to(torch.int32)
 
     def start(self, slots, histories, last):
         """Histories for the lookup: everything that is in the cache, then the token that follows."""
@@ -141,12 +152,14 @@ class Decoder:
         length = self.cache.length[self.slots.long()]
 
         def attend(layer, q, k, v):
-            out = torch.empty_like(q)
+            out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+            if self.rotary is not None:
+                clk.tree_rotate(self.cache, self.slots, q, k, nodes, self.mask, self.rotary, q, k)
             clk.tree_attend(self.cache, self.slots, self.pool, layer, q, k, v, nodes, self.mask, self.scale, out, self.scratch)
             self.kv[0, layer], self.kv[1, layer] = k, v
             return out
 
-        logits = t.forward(self.tok.clamp(min=0), length[:, None] + self.depth, attend)
+        logits = t.forward(self.tok.clamp(min=0), length[:, None] + self.depth, attend, self.rotary is None)
         clk.verify_greedy(logits, self.tok, nodes, self.argmax, self.accept, self.emitted, self.out_tok, self.vscratch)
         clk.tree_accept(self.tok, self.parent, nodes, self.argmax, self.accept, self.path, self.emitted, self.out_tok)
         clk.cache_grow(self.cache, self.slots, self.emitted)
@@ -155,10 +168,10 @@ class Decoder:
         self.tok[:, 0] = torch.gather(self.out_tok, 1, (self.emitted[:, None] - 1).long())[:, 0]
 
 
-def run(requests=4, document=600, tokens=64, tree=True, dtype=torch.bfloat16, seed=0):
+def run(requests=4, document=600, tokens=64, tree=True, dtype=torch.bfloat16, seed=0, cache8=False):
     """Decodes; returns each request's tokens, the number of steps and the pool's state."""
     t = Target(dtype=dtype, seed=seed)
-    d = Decoder(t, requests + 1, document + 64 + tokens + 2 * NODES)
+    d = Decoder(t, requests + 1, document + 64 + tokens + 2 * NODES, cache8=cache8)
     g = torch.Generator().manual_seed(seed + 1)
     doc = torch.randint(0, t.vocab, (document,), generator=g, dtype=torch.int32)
     questions = [torch.randint(0, t.vocab, (8 + 5 * r,), generator=g, dtype=torch.int32) for r in range(requests)]
@@ -189,8 +202,9 @@ def main():
     p.add_argument("--document", type=int, default=600)
     p.add_argument("--tokens", type=int, default=64)
     p.add_argument("--no-tree", action="store_true", help="one token a step")
+    p.add_argument("--cache8", action="store_true", help="a cache in 8 bits; the calls rotate")
     a = p.parse_args()
-    r = run(a.requests, a.document, a.tokens, not a.no_tree)
+    r = run(a.requests, a.document, a.tokens, not a.no_tree, cache8=a.cache8)
     made = sum(map(len, r["tokens"]))
     print(f"{made} tokens of {a.requests} requests in {r['steps']} steps ({made / a.requests / r['steps']:.2f} a step); "
           f"{r['moved']} pages moved, {r['used']} in use; status {r['status']}")
