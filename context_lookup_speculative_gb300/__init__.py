@@ -830,14 +830,17 @@ def tree_rotate(h: Cache, slots, q, k, nodes, mask, rotary: Rotary, q_out, k_out
 
 
 def _flat_rows(t: torch.Tensor, lead, dtype, dim: int, name: str):
-    """Strides (row, head) of rows [lead.., heads, dim] whose requests follow one another."""
-    req, row, head = _heads(t, lead, dtype, dim, name)
+    """Strides (row, head) of rows [.., lead.., heads, dim] whose requests follow one another; one of what comes before."""
+    st, shape = t.stride(), t.shape
+    if not t.is_cuda or t.dtype != dtype or shape[-2 - len(lead):-2] != lead or shape[-1] != dim or (dim > 1 and st[-1] != 1):
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor {tuple(lead)} + (heads, {dim}) with contiguous rows")
+    row = st[-3]
     if len(lead) == 2:
         if lead[1] == 1:
-            row = req if lead[0] > 1 else 0
-        elif lead[0] > 1 and req != lead[1] * row:
+            row = st[-4] if lead[0] > 1 else 0
+        elif lead[0] > 1 and st[-4] != lead[1] * row:
             raise ValueError(f"{name} must hold one request's rows after another's")
-    return row, head
+    return row, st[-2]
 
 
 def cache_append_rotary(h: Cache, slots, pool, k, v, count, rotary: Optional[Rotary] = None, layer: int = 0, path=None, offsets=None,
@@ -853,25 +856,28 @@ def cache_append_rotary(h: Cache, slots, pool, k, v, count, rotary: Optional[Rot
     eight = isinstance(pool, ScaledPool)
     d = _pool8_desc(h, pool) if eight else _pool_desc(h, pool)
     layers, N, layer_st, row, head = _append_rows(B, d, k, v, offsets)
-    code, t = _POOL_DTYPES[k.dtype], None
+    shape, dtype = k.shape, k.dtype
+    code, t = _POOL_DTYPES[dtype], None
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
     if q is not None or k_out is not None:
         if rotary is None or layers != 1 or path is not None:
             raise ValueError("q and k_out need a rotation, one layer and no path")
-        lead = k.shape[1:-2]
-        t = TurnDesc(code, 0, d.heads, d.dim)
+        lead, dim = shape[1:-2], shape[-1]
+        q_heads = q_at = q_row = q_head = qo_at = qo_row = qo_head = ko_at = ko_row = ko_head = 0
         if q is not None:
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
-            t.q_heads, t.d_q, t.d_q_out = q.shape[-2], q.data_ptr(), q_out.data_ptr()
-            t.q_row, t.q_head = _flat_rows(q, lead, k.dtype, d.dim, "q")
-            t.qo_row, t.qo_head = _flat_rows(q_out, lead, k.dtype, d.dim, "q_out")
+            if q_out.shape != q.shape or q.dim() != len(lead) + 2:
+                raise ValueError("q must be one layer's rows, and q_out must have q's shape")
+            q_heads, q_at, qo_at = q.shape[-2], q.data_ptr(), q_out.data_ptr()
+            q_row, q_head = _flat_rows(q, lead, dtype, dim, "q")
+            qo_row, qo_head = (q_row, q_head) if q_out is q else _flat_rows(q_out, lead, dtype, dim, "q_out")
         if k_out is not None:
-            if k_out.shape != k.shape:
+            if k_out.shape != shape:
                 raise ValueError("k_out must have k's shape")
-            t.d_k_out = k_out.data_ptr()
-            t.ko_row, t.ko_head = _flat_rows(k_out[0], lead, k.dtype, d.dim, "k_out")
+            ko_at = k_out.data_ptr()
+            ko_row, ko_head = _flat_rows(k_out, lead, dtype, dim, "k_out")
+        t = TurnDesc(code, q_heads, shape[-2], dim, q_at, 0, qo_at, ko_at, 0, q_row, q_head, 0, 0, 0, 0, qo_row, qo_head,
+                     0, ko_row, ko_head)
     _check("clk_cache_append_rotary",
            lib().clk_cache_append_rotary(h.handle, _ptr(slots, name="slots"), B, ctypes.byref(d),
                                          ctypes.byref(pool._desc) if eight else None, layer, layers, code, k.data_ptr(), v.data_ptr(),
