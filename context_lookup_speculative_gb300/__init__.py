@@ -813,16 +813,18 @@ def tree_rotate(h: Cache, slots, q, k, nodes, mask, rotary: Rotary, q_out, k_out
     [B] or None: the slots' lengths)."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must be [B, N, heads, dim]")
-    B, N = q.shape[:2]
-    code, D = _POOL_DTYPES.get(q.dtype), q.shape[3]
+    shape, k_shape, dtype = q.shape, k.shape, q.dtype
+    B, N, q_heads, D = shape
+    code = _POOL_DTYPES.get(dtype)
     if code is None:
         raise ValueError("q and k must have one type of bfloat16, float16 or float32")
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+    if q_out.shape != shape or k_out.shape != k_shape:
         raise ValueError("q_out and k_out must have q's and k's shapes")
-    lead = q.shape[:2]
-    qs, ks = _heads(q, lead, q.dtype, D, "q"), _heads(k, lead, q.dtype, D, "k")
-    qo, ko = _heads(q_out, lead, q.dtype, D, "q_out"), _heads(k_out, lead, q.dtype, D, "k_out")
-    t = TurnDesc(code, q.shape[2], k.shape[2], D, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *qs, *ks, *qo, *ko)
+    lead = shape[:2]
+    qs, ks = _heads(q, lead, dtype, D, "q"), _heads(k, lead, dtype, D, "k")
+    qo = qs if q_out is q else _heads(q_out, lead, dtype, D, "q_out")
+    ko = ks if k_out is k else _heads(k_out, lead, dtype, D, "k_out")
+    t = TurnDesc(code, q_heads, k_shape[2], D, q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *qs, *ks, *qo, *ko)
     _check("clk_tree_rotate",
            lib().clk_tree_rotate(h.handle, _ptr(slots, shape=(B,), name="slots"), B, ctypes.byref(t), N,
                                  _ptr(nodes, shape=(B,), name="nodes"), _ptr(mask, torch.int64, (B, N), "mask"),

@@ -1,24 +1,38 @@
 // Position rotation: queries and keys of drafted trees, and keys on their way
 // into the pages of a cache, of the rows' type or in 8 bits.
 //
-// Work is dealt out in blocks: rows of one request that lie in one aligned
+// Work is counted in blocks: rows of one request that lie in one aligned
 // block of `tokens` positions of its slot (16 where the pool has no scales),
-// or 16 nodes of a tree.  Every CTA counts the requests' blocks (a prefix sum
-// over the batch, so offsets may fall and requests may be left out) and takes
-// every gridDim.x-th; blockIdx.y takes a share of the heads.  What a block's
-// rows are and where they go is found once, by a thread per row, and lies in
-// shared memory.
+// or 16 nodes of a tree; and in pieces, the heads of a block.  Every CTA counts
+// the requests' blocks (a prefix sum over the batch, so offsets may fall and
+// requests may be left out) and takes an equal run of all pieces.  What a
+// block's rows are and where they go is found once, by a thread per row, and
+// lies in shared memory.
 //
-// Fast rows (16 bits, dim a multiple of 16 up to 128, whole aligned vectors):
-// a lane holds two vectors of 8 elements that turn together (j and j + pairs
-// / 8, or neighbours), so that no value crosses lanes, and a warp all 16 rows
-// of a block and head.  With scales a team of tokens / 16 warps takes a block
-// and head: the rows stay in registers between the search for their largest
-// magnitude and their rounding, so every row is read once.  Other rows go
-// element by element (k_turn_any), read twice where there are scales.
+// Fast rows (16 bits, dim a multiple of 16 up to 128, whole aligned vectors): a
+// lane holds two vectors of 8 elements that turn together (j and j + pairs / 8,
+// or neighbours), so that no value crosses lanes.  Without scales (k_turn_rows)
+// a warp has the same rows of every head and keeps their part of the table in
+// registers, four heads' loads in flight.  (With all 16 rows of a head to a warp
+// every head read the table again, and blocks went to CTAs whole: 256 trees of
+// 32 nodes, 48/8 heads of 128, 53.5 us, now 35.7; 16 prompts of 100 to 2,000
+// tokens, 32/8 heads of 128, 92 and 75.)  With scales (k_turn_rows8) a team of
+// warps takes a block and head: the rows stay in registers between the search
+// for their largest magnitude and their rounding, so every row is read once.
+// Where a warp holds half as many rows 24 warps fit an SM instead of 16 (64
+// prompts of 100 to 2,000 tokens, 24/4 heads of 64: 132 us, then 125, and 117
+// with one multiplication an element where the scale is a power of two).
+// Other rows go element by element (k_turn_any), read twice where there are
+// scales.
 //
-// All of it is bound by memory: rows in, rows out, and 8 bytes a pair and
-// position of the table, which the heads of a position share in L1 and L2.
+// All of it would be bound by memory: rows in, rows out, and 8 bytes a pair and
+// position of the table, which the heads of a position share.  Trees reach 5.0,
+// prompts 5.7 TB/s (73 and 84% of a copy), into 8 bits 4.8 (71%): there 62
+// million warp instructions take half of the issue slots, and chains of loads,
+// a barrier of the team and stores the rest.  Slower: the next piece's rows on
+// their way to shared memory (136 us against 132), the next block's rows looked
+// up meanwhile (145 against 135), q's heads in a launch of their own (128
+// against 117).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
