@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         // the largest.  Starting at 2^4, 2^6 and 2^7 measured 507, 511, 520 us with 64 requests of 2,000 to 32,000 tokens.)
         // The largest p starts at up to 2^100: V's scales may be as small as 2^-100.  That t stays a normal number where p
         // matters, however far V's scales lie apart, takes k of -60 to 30 and M not far above the scores; else p and t are
-        // computed each.
-        constexpr float lift = 6.0f, lift_sum = 100.0f, most_sum = 0x1p120f, most_weight = 32768.0f;
+        // computed each.  (Then M may move by more than a float32's exponent, and a sum of p with it in two steps.)
+        constexpr float lift = 6.0f, lift_sum = 100.0f, most_sum = 0x1p110f, most_weight = 32768.0f;
         uint32_t sp = 0, od = 0, look = 0, pp = 0;  // phases of SFull, ODone, Look, Pair
         // The two warps with the same rows meet: < 0 if one gave up, else whether one wished.
         auto agree = [&](bool wish) -> int {
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                     float m = fmaxf(ceilf(heavy) - lift, ceilf(top) - lift_sum);
                     m = top == -INFINITY ? M : none ? m : fmaxf(M, m);
                     const float fix = none ? 1.0f : exp2f(M - m);
-                    if (!none) sum *= fix;
+                    if (!none) sum = moved(sum, M - m);
                     M = m;
                     wide = M > top + 30.0f;
                     if (!__any_sync(0xffffffffu, fix != 1.0f)) return true;
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             const float m = fmaxf(a.x, b.x);
             const float w0 = a.x == -INFINITY ? 0.0f : exp2f(a.x - m);
             const float w1 = b.x == -INFINITY ? 0.0f : exp2f(b.x - m);
-            const float l = a.y * w0 + b.y * w1;
+            const float l = (a.x == -INFINITY ? a.y * w0 : moved(a.y, a.x - m)) + (b.x == -INFINITY ? b.y * w1 : moved(b.y, b.x - m));
             // a stream without a visible key has no sum of products (or one of zeros)
             const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1

@@ -415,6 +415,13 @@ __device__ __forceinline__ void make_plan(const Attend& A, const Shape& S, long 
     }
 }
 
+// x 2^d, d <= 0, where 2^d may be less than a float32 holds.
+__device__ __forceinline__ float moved(float x, float d)
+{
+    const float half = exp2_fast(0.5f * d);
+    return x * half * half;
+}
+
 // This CTA's share of an item whose tiles lie in several CTAs' shares.
 template <int DP, bool BF16, typename K, int THREADS>
 __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const Scratch& W, const Plan& plan, const Cuts& cuts,
@@ -487,15 +494,16 @@ __device__ __forceinline__ void join_item(const Attend& A, const Shape& S, const
 #pragma unroll
                     for (int e = 0; e < F; ++e) to = fmaxf(to, ml[u][e].x);
                     const float f = top[u] == -INFINITY ? 0.0f : exp2_fast((top[u] - to) * cs);
+                    const float top_was = top[u];
                     top[u] = to;
-                    l[u] *= f;
+                    l[u] = !K::in_log2 ? l[u] * f : top_was == -INFINITY ? 0.0f : moved(l[u], top_was - to);
                     o[u] = make_float4(o[u].x * f, o[u].y * f, o[u].z * f, o[u].w * f);
 #pragma unroll
                     for (int e = 0; e < F; ++e) {
                         // a part that saw nothing has no weight (and its reference is -inf)
                         const bool use = c + e < parts && !(ml[u][e].x == -INFINITY && ml[u][e].y == 0.0f);
                         const float g = exp2_fast((ml[u][e].x - to) * cs);
-                        l[u] += use ? ml[u][e].y * g : 0.0f;
+                        l[u] += !use ? 0.0f : K::in_log2 ? moved(ml[u][e].y, ml[u][e].x - to) : ml[u][e].y * g;
                         o[u].x += use ? v[u][e].x * g : 0.0f;
                         o[u].y += use ? v[u][e].y * g : 0.0f;
                         o[u].z += use ? v[u][e].z * g : 0.0f;

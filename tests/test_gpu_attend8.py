@@ -146,6 +146,26 @@ def test_v_scales_far_apart(lo, hi, odd, D, monkeypatch):
     t.run().check()
 
 
+@pytest.mark.parametrize("first,then", [(-100, 60), (60, -100), (-100, 90), (90, -60)])
+@pytest.mark.parametrize("D,n", [(64, 700), (128, 700), (64, 5000), (128, 5000)])
+def test_v_scales_that_change_along_the_context(first, then, D, n, monkeypatch):
+    """The first half of a context's V has scales of 2^first, the other of 2^then: tiles, streams and parts of one row with
+    references far apart, whose sums of weights count alike.  Tolerance as for scales far apart."""
+    import test_gpu_attend
+
+    t = Tree8(D + n, 2, 3, [n, 130], 4, 1, D, 64, "bf16", nodes=[3, 1], T=64)
+    for s, length in enumerate([n, 130]):
+        slot = int(t.slots[s])
+        pages = t.cache.table[slot, :-(-length // 64)].long()
+        half = len(pages) // 2
+        t.pool8.scale[1][pages[:half]] = 2.0 ** first
+        t.pool8.scale[1][pages[half:]] = 2.0 ** then
+    t.pool = (t.pool8.data.double() * t.pool8.scale[..., None].double())
+    more = 2.0 ** -30 * 448 * 2.0 ** max(first, then)
+    monkeypatch.setattr(test_gpu_attend, "tolerance", lambda kind, ref, size, keys, vmax: tolerance(kind, ref, size, keys, vmax) + keys * more)
+    t.run().check()
+
+
 def test_large_scores():
     for kind, D in (("bf16", 64), ("f16", 128)):
         t = Tree8(5, 2, 4, [700, 300], 2, 1, D, 16, kind, nodes=[4, 4], amp=8.0)
