@@ -58,7 +58,7 @@
 // 4,800 of the softmax, which together do not stay in the instruction cache (84%
 // of the fetches hit).  So a step takes 4,700 cycles: 4,000 tokens behind 25,000
 // (32/8 heads of 128) 1,725 us, 1,030 TFLOP/s, where 16 bits reach 1,700; 8
-// prompts of 100 to 1,500 behind up to 8,192 (24/4 heads of 64) 341 us, 630
+// prompts of 100 to 1,500 behind up to 8,192 (24/4 heads of 64) 351 us, 610
 // TFLOP/s, where they reach 1,020.
 #include <cuda.h>
 #include <cuda_bf16.h>
