@@ -71,19 +71,20 @@ struct Lay {
     static constexpr bool kApart = DP == 64;
     static constexpr int kParts = BF16 ? 2 : 3;            // of Q
     static constexpr int kQB = DP == 128 ? 1 : 2;          // items whose Q is held
-    static constexpr int kK = DP == 128 ? (BF16 ? 3 : 2) : 6;  // K tiles in the ring (8 bits, or 64 new tokens)
-    static constexpr int kV = DP == 128 ? 1 : 2;          // V tiles of 16 bits
-    static constexpr int kVBytes = kBytes / 4;             // 32 keys of one
-    static constexpr int kG = DP == 128 ? 4 : 6;           // V tiles as the cache holds them
+    static constexpr int kK = DP == 128 ? (BF16 ? 3 : 2) : 7;  // K tiles in the ring (8 bits, or 64 new tokens)
+    static constexpr int kVBytes = kBytes / 4;             // 32 keys of the V tile of 16 bits
+    static constexpr int kG = DP == 128 ? 4 : 7;           // V tiles as the cache holds them
+    // (Rows of 64: 256 requests of 300 to 4,096 tokens took 198 us with seven tiles of each, 199 with six, 213 with four of K.
+    // A second V tile of 16 bits made no difference.)
     // Scales outlive their tiles: the softmax warps read them.  A place is written again when the tile kScales before is
     // weighed: the copy of a tile waits for the scores of the one kK before, which follow the weights of kK + 2.
     static constexpr int kScales = 16;
     static_assert(kScales >= kK + 2, "scales in use");
-    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oG = oV + kV * kBytes;
+    static constexpr int oParts = kQB * kBytes, oK = oParts + kQB * kParts * kPart, oV = oK + kK * kPart, oG = oV + kBytes;
     // after the tiles
     static constexpr int oKFull = oG + kG * kPart, oKEmpty = oKFull + 8 * kK;
-    static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 32, oVEmpty = oVReady + 16 * kV;  // of quarters; of halves
-    static constexpr int oGFull = oVEmpty + 16 * kV, oGEmpty = oGFull + 8 * kG;
+    static constexpr int oVFull = oKEmpty + 8 * kK, oVReady = oVFull + 32, oVEmpty = oVReady + 16;  // of quarters; of halves
+    static constexpr int oGFull = oVEmpty + 16, oGEmpty = oGFull + 8 * kG;
     static constexpr int oPartsReady = oGEmpty + 8 * kG, oFactorRead = oPartsReady + 8 * kQB;
     static constexpr int oQFull = oFactorRead + 8 * kQB, oQEmpty = oQFull + 8 * kQB;
     static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             bar_init(base + L::oKEmpty + 8 * i, 1);
         }
         for (int i = 0; i < 4; ++i) bar_init(base + L::oVFull + 8 * i, 1);
-        for (int i = 0; i < 2 * L::kV; ++i) {
+        for (int i = 0; i < 2; ++i) {
             bar_init(base + L::oVReady + 8 * i, 2);
             bar_init(base + L::oVEmpty + 8 * i, 1);
         }
@@ -653,25 +654,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             return true;
         };
         // Stream s's weights with the next V tile, by halves of 64 keys.
-        int vi = 0;
         uint32_t vp = 0;
         auto values = [&](int s, bool add, bool cached) {
             const uint32_t kind = cached ? kind_v : kind_o;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if (!warp_wait(base + (half == 0 ? L::oPHalf : L::oPReady) + 8 * s, ps[s], stop)) return false;
-                if (!warp_wait(base + L::oVReady + 16 * vi + 8 * half, vp, stop)) return false;
+                if (!warp_wait(base + L::oVReady + 8 * half, vp, stop)) return false;
                 tmem_after();
                 if (elect()) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)  // 16 keys each
                         mma_ts(tm + 256 + s * DP, tm + (L::kApart ? 384 + 64 * s + 32 * half : 128 * s + 64 * half) + 8 * e,
-                               v0 + (4 * vi + 2 * half + e / 2) * (L::kVBytes / 16) + 128 * (e & 1), kind, add || half + e > 0);
-                    mma_commit(base + L::oVEmpty + 16 * vi + 8 * half);
+                               v0 + (2 * half + e / 2) * (L::kVBytes / 16) + 128 * (e & 1), kind, add || half + e > 0);
+                    mma_commit(base + L::oVEmpty + 8 * half);
                 }
                 __syncwarp();
             }
-            step(vi, vp, L::kV);
+            vp ^= 1;
             ps[s] ^= 1;
             return true;
         };
@@ -744,15 +744,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             const bool cached = t < w.x.ctx_tiles;
             const int gi = g % L::kG, rows = w.x.rows;
             if (cached && !warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kG & 1), stop)) return false;
-            const int vi = tile % L::kV;
-            const uint32_t phase = (uint32_t)(tile / L::kV & 1), half = 8 * (team >> 1);
-            char* const place = sm + L::oV + (4 * vi + team) * L::kVBytes;
-            if (!warp_wait(base + L::oVEmpty + 16 * vi + half, phase ^ 1, stop)) return false;
+            const uint32_t phase = (uint32_t)(tile & 1) ^ 1, half = 8 * (team >> 1);
+            char* const place = sm + L::oV + team * L::kVBytes;
+            if (!warp_wait(base + L::oVEmpty + half, phase, stop)) return false;
             // What was noted of new tokens before has been looked at when both halves of the tile before are done with.
-            if (!cached && tile > 0) {
-                const int x = (tile - 1) % L::kV;
-                if (!warp_wait(base + L::oVEmpty + 16 * x + 8, (uint32_t)((tile - 1) / L::kV & 1), stop)) return false;
-            }
+            if (!cached && !warp_wait(base + L::oVEmpty + 8, phase, stop)) return false;
             if (cached) {
                 convert(place, gi, w.x.ctx - t * kTile);
                 ++g;
@@ -793,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
             if (lane == 0) {
                 if (cached) bar_arrive(base + L::oGEmpty + 8 * gi);
                 if (!cached && team < 2) bar_arrive(base + L::oLook + 8 * ((t - w.t0) & 1));
-                bar_arrive(base + L::oVReady + 16 * vi + half);
+                bar_arrive(base + L::oVReady + half);
             }
             return true;
         };
