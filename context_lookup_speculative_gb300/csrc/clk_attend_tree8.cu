@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                 }
                 if (!real) continue;
                 if (whole) {
-                    if (16 * c < A.dim) {  // (a multiple of 16)
+                    if (16 * c < A.dim) {  // (a multiple of 8)
                         uint32_t y[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) y[i] = pack2<BF16>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
                             store32(out + 16 * c * 2, y);
                         } else {
                             *reinterpret_cast<uint4*>(out + 16 * c * 2) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4*>(out + 16 * c * 2 + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+                            if (16 * c + 8 < A.dim) *reinterpret_cast<uint4*>(out + 16 * c * 2 + 16) = make_uint4(y[4], y[5], y[6], y[7]);
                         }
                     }
                 } else {

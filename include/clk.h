@@ -814,7 +814,7 @@ CLK_API int clk_prompt_attend(const clk_attn* a, const int64_t* d_off, int32_t B
 /* The two attentions over a pool of 8 bits: a->dtype is q's, the new tokens' and
  * out's type, the pool is CLK_DTYPE_E4M3, and each cached element is its
  * value times its block's scale.  On the tensor cores (16-bit types, dim a
- * multiple of 16 up to 128) prompts round that to a->dtype for the products,
+ * multiple of 8 up to 128, the pool's strides multiples of 16) prompts round that to a->dtype for the products,
  * which changes nothing where scales are powers of two in the type's range, as
  * clk_cache_append_rotary makes them.  Trees multiply the values as they are:
  * q's elements are held to 9 bits (bfloat16; its own are 8) or 14 (float16;
