@@ -74,7 +74,8 @@ __device__ __forceinline__ float4 to_f4(uint2 x)
 template <typename T>
 __device__ __forceinline__ float4 to_f4(float4 x) { return x; }
 
-// Four codes of 8 bits, in the place of four elements, and the elements that they stand for: rounded to the type.
+// Four codes of 8 bits, in the place of four elements, and the elements that they stand for, in float32 (a 16-bit type
+// need not hold them: rows at the top of float16's range stand for more than its largest).
 template <typename F>
 __device__ __forceinline__ F take4_codes(const uint8_t* p, int left, bool vec)
 {
@@ -87,13 +88,12 @@ __device__ __forceinline__ F take4_codes(const uint8_t* p, int left, bool vec)
     reinterpret_cast<uint32_t&>(x.x) = w;
     return x;
 }
-template <typename T, typename F>
+template <typename F>
 __device__ __forceinline__ float4 of_codes(F x, float scale)
 {
     float f[4];
     from_e4m3x4(reinterpret_cast<const uint32_t&>(x.x), f);
-    return make_float4(to_f(from_f<T>(f[0] * scale)), to_f(from_f<T>(f[1] * scale)), to_f(from_f<T>(f[2] * scale)),
-                       to_f(from_f<T>(f[3] * scale)));
+    return make_float4(f[0] * scale, f[1] * scale, f[2] * scale, f[3] * scale);
 }
 
 // How a call is cut: a CTA's rows are `tok` tokens x `hp` heads of one K/V
@@ -248,8 +248,8 @@ __device__ __forceinline__ void attend_rows(const Attend& A, const Rows& G, int 
                 const int r = warp * (kKeys / 8) + (NC == 8 ? i >> 1 : i * (32 / kLanes) + lane / kLanes);
                 const int x = 4 * (NC == 8 ? lane + 32 * (i & 1) : lane % kLanes);
                 const bool codes = EIGHT && src[cur][r] >= 0;
-                *reinterpret_cast<float4*>(sk + r * Z::kK + x) = codes ? of_codes<T>(kk[u], scales[cur][0][EIGHT ? r : 0]) : to_f4<T>(kk[u]);
-                *reinterpret_cast<float4*>(sv + r * Z::kV + x) = codes ? of_codes<T>(vv[u], scales[cur][1][EIGHT ? r : 0]) : to_f4<T>(vv[u]);
+                *reinterpret_cast<float4*>(sk + r * Z::kK + x) = codes ? of_codes(kk[u], scales[cur][0][EIGHT ? r : 0]) : to_f4<T>(kk[u]);
+                *reinterpret_cast<float4*>(sv + r * Z::kV + x) = codes ? of_codes(vv[u], scales[cur][1][EIGHT ? r : 0]) : to_f4<T>(vv[u]);
             }
         }
         __syncthreads();

@@ -816,7 +816,8 @@ CLK_API int clk_prompt_attend(const clk_attn* a, const int64_t* d_off, int32_t B
  * value times its block's scale.  On the tensor cores (16-bit types, dim a
  * multiple of 8 up to 128, the pool's strides multiples of 16) prompts round that to a->dtype for the products,
  * which changes nothing where scales are powers of two in the type's range, as
- * clk_cache_append_rotary makes them.  Trees multiply the values as they are:
+ * clk_cache_append_rotary makes them.  The general kernel does not round it.
+ * Trees multiply the values as they are:
  * q's elements are held to 9 bits (bfloat16; its own are 8) or 14 (float16;
  * 11), or to 2^-18 of the row's largest where that is more, and weights of
  * cached tokens, times V's scales, to float16, their largest at 2^5 or more;
