@@ -118,11 +118,13 @@ struct Lay {
     static constexpr int oGFull = oVEmpty + 8 * kV, oGEmpty = oGFull + 8 * kG;
     static constexpr int oQFull = oGEmpty + 8 * kG, oQEmpty = oQFull + 8 * kQB;
     static constexpr int oSFull = oQEmpty + 8 * kQB, oSFree = oSFull + 16, oPReady = oSFree + 16, oPHalf = oPReady + 16, oODone = oPHalf + 16;
-    static constexpr int oStatReady = oODone + 16, oDrain = oStatReady + 8;
+    static constexpr int oStatReady = oODone + 16, oRaised = oStatReady + 8, oRaisedRead = oRaised + (E8 ? 16 : 0);
+    static constexpr int oDrain = oRaisedRead + (E8 ? 16 : 0);
     static constexpr int oBars = oDrain + 8;  // end of the barriers
     static constexpr int oBad = (oBars + 15) / 16 * 16;               // uint32[kV][4]
     static constexpr int oScale = oBad + 16 * kV;                     // float[kG][8]: of blocks of 16 keys
-    static constexpr int oNear = oScale + 32 * kG;                    // Reach[kNear]
+    static constexpr int oRaise = oScale + 32 * kG;                   // uint32[2]: of segments (see kRaised)
+    static constexpr int oNear = oRaise + (E8 ? 16 : 0);              // Reach[kNear]
     static constexpr int oPlan = oNear + kNear * (int)sizeof(Reach);  // Plan, stop flag, tmem address
     static constexpr int oCut = oPlan + (int)sizeof(Plan);            // Cut[2]: of items that end here, that begin here
     static constexpr int oWalk = (oCut + 2 * (int)sizeof(Cut) + 7) / 8 * 8;  // Walk[8]
@@ -139,6 +141,13 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
     using L = Lay<DP, PROMPT, E8>;
     using K = typename L::K;
     constexpr int kThreads = clk::kThreads<E8>;
+    // A cache in 8 bits may hold more than float16's largest.  Where a segment's scales reach beyond 2^7 (448 times that is
+    // in range), its cached K and V are converted divided by a power of two each, the least that is enough; scores are
+    // multiplied by K's, O counts in V's.  One warp looks through the scales ahead of the others, so that a tile of other
+    // segments costs nothing.  (8 prompts of 100 to 1,500 tokens behind up to 8,192, 24/4 heads of 64, 356 us without and
+    // with it, 406 with a look at every tile in the loops below; 4,000 behind 25,000, 32/8 heads of 128, 1,317, 1,322, 1,436.)
+    constexpr bool kRaised = E8 && !BF16;
+    auto power = [](uint32_t e) { return __uint_as_float(127 + e << 23); };
     extern __shared__ __align__(1024) char sm[];
     // the shuffle tells the compiler that a warp has one role
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -185,6 +194,10 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             bar_init(base + L::oODone + 8 * i, 1);
         }
         bar_init(base + L::oStatReady, 8);
+        for (int i = 0; kRaised && i < 2; ++i) {
+            bar_init(base + L::oRaised + 8 * i, 1);
+            bar_init(base + L::oRaisedRead + 8 * i, 8 + 4);  // the softmax warps', and those that convert
+        }
         bar_init(base + L::oDrain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -216,7 +229,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
         // counts.  Likewise references are compared as scores wherever sums meet (streams, parts), not times cs.
         constexpr float far_off = 256.0f;
         uint32_t sp = 0, od = 0;
-        int gi = 0;
+        int gi = 0, seg = 0;
         bool ok = true;
         Walk<K>& w = reinterpret_cast<Walk<K>*>(sm + L::oWalk)[warp];
         if (lane == 0) w.start(A, S, plan, near);
@@ -233,6 +246,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 seen = (unsigned long long)A.mask[(int64_t)w.b * A.N + token];
                 if (w.x.rows < 64) seen &= (1ull << w.x.rows) - 1;
             }
+            const uint32_t* const raise = reinterpret_cast<const uint32_t*>(sm + L::oRaise) + (seg & 1);
+            if (kRaised && !(ok = warp_wait(base + L::oRaised + 8 * (seg & 1), (uint32_t)(seg >> 1 & 1), stop))) break;
             float ref = -INFINITY, sum = 0.0f;
             bool settled = false;  // every row has a reference, and none is far off
             bool far = false;      // some row's is far off
@@ -309,6 +324,29 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 }
                 if (E8 && !look_at(j)) return false;
                 return true;
+            };
+            // A divided tile's scores times K's power of two; O, which counts in V's up to the cache's end (and is complete, as
+            // in follow), times V's before new tokens.
+            auto adjust = [&](int j) {
+                const uint32_t over = *raise;
+                if (cached) {
+                    const float up = power(over & 255);
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * up);
+                } else if (t == ctx_tiles && j > 0 && over >> 8 != 0) {
+                    const float up = power(over >> 8);
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 16) {
+                        uint32_t o[16];
+                        tmem_load16(tO + c, o);
+                        tmem_load_wait();
+                        tmem_loaded16(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * up);
+                        tmem_store16(tO + c, o);
+                    }
+                    tmem_store_wait();
+                }
             };
             // The references follow tile j's maxima where these have grown by more than a factor of 2^8.
             auto follow = [&](int j) {
@@ -421,7 +459,19 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             // 296 us so, 284 with two loops, 283 without it; a prompt of 25,000 3,030, 2,975 and 2,980.
             // Trees are bound by memory and have it there: a second loop would not fit their registers (256 requests
             // 151 us, 110 so).
-            if (tiles()) {
+            // That loop is also taken by segments whose K or V were divided, from their first tile on.
+            if (kRaised) {
+                const bool raised = *raise != 0 && mine > 0;
+                if (raised || tiles()) {
+                    for (bool held = !raised;; held = false) {
+                        if (!held && !(ok = fetch(j))) break;
+                        adjust(j);
+                        follow(j);
+                        weigh(Count<1>{}, false);
+                        if (!(ok = give(j)) || ++j == mine) break;
+                    }
+                }
+            } else if (tiles()) {
                 for (;;) {
                     weigh(Count<1>{}, false);
                     if (!(ok = give(j)) || ++j == mine || !(ok = fetch(j))) break;
@@ -463,7 +513,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 l = a.y * w0 + c.y * w1;
                 // a stream without a visible key has no sum of products (or one of zeros)
             }
-            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            // a part that ends in the cache counts in V's power of two
+            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : kRaised && t0 + mine <= ctx_tiles ? power(*raise >> 8) : 1.0f;
             const int c0 = PROMPT ? 0 : s * (DP / 64), c1 = PROMPT ? DP / 32 : (s + 1) * (DP / 64);
             const uint32_t tA = PROMPT ? tO : lanes + 256, tB = lanes + 256 + DP;
             for (int c = c0; c < c1; ++c) {
@@ -526,7 +577,11 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             }
             gi += len;
             __syncwarp();
-            if (lane == 0) w.next(A, S, plan, near);
+            if (lane == 0) {
+                if (kRaised) bar_arrive(base + L::oRaisedRead + 8 * (seg & 1));
+                w.next(A, S, plan, near);
+            }
+            ++seg;
             __syncwarp();
         }
     } else {
@@ -537,7 +592,39 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == kCopyWarp || warp == kCopyWarp2) {
+        if (kRaised && warp == kCopyWarp2) {
+            // ---- Scales beyond 2^7, segment by segment (this warp has nothing to copy). ----
+            for (int seg = 0; w.left > 0; w.next(A, S, plan, near), ++seg) {
+                // A lane has one of eight blocks of 16 keys of every other tile, of K or of V.
+                const int key = 16 * (lane & 7), tiles = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0;
+                const float* const plane = (lane & 8 ? A.vs : A.ks) + w.h * A.scale_head + ((key & (A.C.page_tokens() - 1)) >> A.scale_shift) * A.scale_block;
+                const int32_t* const table = A.C.table + (int64_t)w.x.slot * A.C.max_pages;
+                uint32_t top = 0;  // as an integer: positive floats are in order
+                for (int u = lane >> 4; u < tiles; u += 16) {
+                    int32_t page[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int64_t at = (int64_t)(w.t0 + u + 2 * e) * kTile + key;
+                        page[e] = u + 2 * e < tiles && at < w.x.ctx ? table[at >> A.C.shift] : -1;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (page[e] >= 0 && page[e] < A.C.num_pages) {
+                            const uint32_t bits = __float_as_uint(plane[page[e] * A.scale_page]) & 0x7fffffffu;
+                            if (bits < 0x7f800000u && bits > top) top = bits;
+                        }
+                }
+                const int e = (int)(top + 0x7fffffu >> 23) - (127 + 7);
+                const uint32_t over = e > 0 ? (uint32_t)e : 0u;
+                const uint32_t both = __reduce_max_sync(0xffffffffu, lane & 8 ? 0u : over) | __reduce_max_sync(0xffffffffu, lane & 8 ? over : 0u) << 8;
+                if (!warp_wait(base + L::oRaisedRead + 8 * (seg & 1), (uint32_t)(seg >> 1 & 1) ^ 1, stop)) break;
+                if (lane == 0) {
+                    reinterpret_cast<uint32_t*>(sm + L::oRaise)[seg & 1] = both;
+                    bar_arrive(base + L::oRaised + 8 * (seg & 1));
+                }
+                __syncwarp();
+            }
+        } else if (warp == kCopyWarp || warp == kCopyWarp2) {
             // ---- Copies: two warps (a copy costs its warp about 65 cycles, and pages of 16 rows need 16 a tile). ----
             // With trees one brings K and the other V, so that small pages' copies go side by side (256 short requests,
             // pages of 16: 119 us, by alternate tiles 155); with prompts they take alternate tiles, which keeps K and
@@ -597,11 +684,11 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
                     const uint32_t bytes = (uint32_t)L::kHalves * 128u * (uint32_t)(cached ? boxes << A.C.shift : S.kbox);
                     const int n0 = row0 + (t - w.x.ctx_tiles) * kTile;
-                    // what brings the scales of 16 keys each; none for keys without a page (their rows become 0)
+                    // what brings the scales of 16 keys each; 0 for keys without a page or past the end (their rows become 0)
                     auto bring_scales = [&](const float* plane, uint32_t dst, uint32_t bar) {
                         const int from = __shfl_sync(0xffffffffu, page, 16 * lane >> A.C.shift & 31);
                         if (lane < 8) {
-                            const bool there = from >= 0 && from < A.C.num_pages;
+                            const bool there = from >= 0 && from < A.C.num_pages && t * kTile + 16 * lane < w.x.ctx;
                             const float* const src =
                                 plane + (there ? from * A.scale_page + w.h * A.scale_head +
                                                      ((16 * lane & (A.C.page_tokens() - 1)) >> A.scale_shift) * A.scale_block
@@ -838,13 +925,13 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             const int at0 = row0 * 128 + (c2 ^ swizzle) * 16, at1 = row0 * 128 + ((c2 + 1) ^ swizzle) * 16;
             const int from = (64 * team + row0) * DP + (DP == 128 ? c ^ swizzle : c) * 16;
             // The team's half of the tile in place gi to rows from dst on, columns 64 .. of which lie `next` bytes
-            // further; keys from `have` on become 0.
-            auto convert = [&](int gi, char* dst, int next, int have) {
+            // further; keys from `have` on become 0.  `over`: the power of two that they are divided by.
+            auto convert = [&](int gi, char* dst, int next, int have, uint32_t over) {
                 constexpr int turns = 64 / step;
                 const char* const src = sm + L::oG + gi * L::kPart + from;
                 const float* const all = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
                 char* const to = dst + (c >> 2) * next;
-                const bool plain = __all_sync(0xffffffffu, fits<BF16>(all[lane & 7]));
+                const bool plain = __all_sync(0xffffffffu, fits<BF16>(all[lane & 7]) && (!kRaised || over == 0));
                 // Two turns a pass, the next pass's codes on their way.  (All of them unrolled were 10 KB of instructions,
                 // which with the softmax's do not stay in the instruction cache: three quarters of the requests hit, and
                 // every warp waited: 64 requests 636 us.)
@@ -858,6 +945,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                         for (int e = 0; e < pass; ++e) {
                             x[e] = *reinterpret_cast<const uint4*>(src + (u + e) * (step * DP));
                             f[e] = all[4 * team + (u + e) * step / 16];
+                            if (kRaised && !kPlain) f[e] *= __uint_as_float(127 - over << 23);
                             if (have < kTile && 64 * team + row0 + (u + e) * step >= have) {
                                 x[e] = make_uint4(0, 0, 0, 0);
                                 f[e] = 0.0f;
@@ -898,7 +986,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             // A tile of the cache: K, then V.  With rows of 64 the conversion's instructions are there once, with rows of 128
             // twice: 8 prompts of 100 to 1,500 tokens behind up to 8,192 (24/4 heads of 64) 343 and 376 us, 4,000 tokens
             // behind 25,000 (32/8 heads of 128) 1,842 and 1,757.
-            auto both = [&](int tile, int t) {
+            auto both = [&](int tile, int t, uint32_t over) {
                 const int ki = tile % L::kK, at = 2 * tile + team, vi = at % L::kV;
 #pragma unroll(DP == 64 ? 1 : 2)
                 for (int v = 0; v < 2; ++v) {
@@ -908,7 +996,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     if (!warp_wait(base + L::oGFull + 8 * gi, (uint32_t)(g / L::kGs & 1), stop)) return false;
                     if (!warp_wait(empty, (uint32_t)(turn & 1) ^ 1, stop)) return false;
                     convert(gi, sm + (v == 0 ? L::oK + ki * L::kBytes + team * (64 * 128) : L::oV + vi * L::kVBytes),
-                            v == 0 ? L::kHalf : L::kHalf / 2, v == 0 ? kTile : w.x.ctx - t * kTile);
+                            v == 0 ? L::kHalf : L::kHalf / 2, v == 0 ? kTile : w.x.ctx - t * kTile, over >> 8 * v & 255);
                     if (lane == 0) {
                         bar_arrive(v == 0 ? base + L::oKFull + 8 * ki : base + L::oVReady + 8 * vi);
                         bar_arrive(base + L::oGEmpty + 8 * gi);
@@ -961,8 +1049,15 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 }
                 return true;
             };
-            while (ok && w.left > 0) {
-                for (int t = w.t0; ok && t < w.t1; ++t, ++i) ok = t < w.x.ctx_tiles ? both(i, t) : keys(i, t) && values(i, t);
+            for (int seg = 0; ok && w.left > 0; ++seg) {
+                uint32_t over = 0;
+                if (kRaised) {
+                    if (!(ok = warp_wait(base + L::oRaised + 8 * (seg & 1), (uint32_t)(seg >> 1 & 1), stop))) break;
+                    over = reinterpret_cast<const uint32_t*>(sm + L::oRaise)[seg & 1];
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(base + L::oRaisedRead + 8 * (seg & 1));
+                }
+                for (int t = w.t0; ok && t < w.t1; ++t, ++i) ok = t < w.x.ctx_tiles ? both(i, t, over) : keys(i, t) && values(i, t);
                 __syncwarp();
                 if (lane == 0) w.next(A, S, plan, near);
                 __syncwarp();

@@ -813,16 +813,23 @@ CLK_API int clk_prompt_attend(const clk_attn* a, const int64_t* d_off, int32_t B
 
 /* The two attentions over a pool of 8 bits: a->dtype is q's, the new tokens' and
  * out's type, the pool is CLK_DTYPE_E4M3, and each cached element is its
- * value times its block's scale.  On the tensor cores (16-bit types, dim a
- * multiple of 8 up to 128, the pool's strides multiples of 16) prompts round that to a->dtype for the products,
- * which changes nothing where scales are powers of two in the type's range, as
- * clk_cache_append_rotary makes them.  The general kernel does not round it.
- * Trees multiply the values as they are:
- * q's elements are held to 9 bits (bfloat16; its own are 8) or 14 (float16;
- * 11), or to 2^-18 of the row's largest where that is more, and weights of
- * cached tokens, times V's scales, to float16, their largest at 2^5 or more;
- * V's scales may be any from 2^-100 to 2^90.  Everything else is as without
- * scales. */
+ * value times its block's scale (a product beyond float32's largest is an
+ * infinity).  float32, rows of more than 128 elements and whatever else the
+ * tensor cores do not take: that product in float32.  On the tensor cores
+ * (16-bit types, dim a multiple of 8 up to 128, the pool's strides multiples
+ * of 16):
+ *   Prompts round it to a->dtype for the products.  bfloat16 holds it exactly
+ * where scales are powers of two, as clk_cache_append_rotary makes them.  For
+ * float16, K and V are divided by a power of two each where a request's scales
+ * reach beyond 2^7, so that rows at the top of the type's range and beyond it
+ * are read as what they stand for; what is below 2^-14 of the type, so divided,
+ * is rounded to a multiple of 2^-24.
+ *   Trees multiply the values as they are: q's elements are held to 9 bits
+ * (bfloat16; its own are 8) or 14 (float16; 11), or to 2^-18 of the row's
+ * largest where that is more, and weights of cached tokens, times V's scales,
+ * to float16, their largest at 2^5 or more; V's scales may be any from 2^-100
+ * to 2^90.
+ * Everything else is as without scales. */
 CLK_API int clk_tree_attend_scaled(clk_cache* h, const int32_t* d_slots, int32_t B, const clk_pool* pool,
                                    const clk_scales* scales, int32_t layer, const clk_attn* a, int32_t N,
                                    const int32_t* d_nodes, const int64_t* d_mask, const int32_t* d_ctx, void* d_scratch,

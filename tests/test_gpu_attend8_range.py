@@ -71,3 +71,43 @@ def test_the_general_kernel_does_not_round_what_the_cache_holds(D, kind):
     """Scales that are no powers of two: with products in float32 the tolerances need no term for it."""
     Tree8(1, 3, 6, [300, 20, 129], 3, 2, D, 64, kind, nodes=[6, 6, 6], T=32, odd=True, pad8=3).run().check()
     Prompt8(2, [40, 200], 3, 2, D, kind, ctx=[300, 20], P=64, T=64, odd=True, pad8=1).run().check(rows=15)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("D,pad8", [(64, 0), (128, 0), (40, 8), (96, 0)])
+def test_prompts_over_rows_at_the_top(D, pad8, rotated, kind):
+    prompts(kind, D, rotated, pad8)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,ctx,P,T", [([200, 3], [700, 129], 32, 32), ([60], [5000], 64, 16), ([300, 20, 7], [257, 1500, 128], 128, 128)])
+def test_prompts_over_values_past_the_type(lens, ctx, P, T, D, kind):
+    """Blocks of keys and values of up to 229,376 beside blocks of size one, changing from tile to tile, in items that are
+    whole and in parts.  Codes are multiples of 2^-9 and scales 2^-8 or more, so that float16 holds the values times 2^-2."""
+    p = Prompt8(D + P, lens, 3, 2, D, kind, ctx=ctx, P=P, T=T)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    pages = p.pool8.scale.shape[1]
+    for x in (0, 1):
+        big = torch.rand((pages, 1, 1), generator=g, device="cuda") < (0.3 if P < 128 else 0.5)
+        high = torch.exp2(torch.randint(7, 10, p.pool8.scale[x].shape, generator=g, device="cuda").float())
+        p.pool8.scale[x] = torch.where(big, high, p.pool8.scale[x])
+    p.pool = stands(p.pool8)
+    assert float(p.pool.abs().max()) > 2 * TOP
+    p.scale = 1 / (2.0 ** 9 * 100 * math.sqrt(D))
+    p.run().check(rows=15)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("plane,exponent", [(0, 8), (1, 8), (0, 40)])
+def test_keys_or_values_past_the_type(plane, exponent, D, kind):
+    """One of the two alone, in one block of a long prefix; keys of 2^40 times the others, whose scores hardly count then."""
+    p = Prompt8(D + exponent, [50, 130], 4, 1, D, kind, ctx=[4001, 600], P=64, T=32)
+    for slot, n in zip(p.slots, (4001, 600)):
+        for page in p.cache.table[int(slot), :-(-n // 64)].tolist()[1::7]:
+            p.pool8.scale[plane, page, :, 0] = 2.0 ** exponent
+    p.pool = stands(p.pool8)
+    p.scale = 1 / math.sqrt(D) if plane else 1 / (2.0 ** exponent * 100 * math.sqrt(D))
+    p.run().check(rows=15)
