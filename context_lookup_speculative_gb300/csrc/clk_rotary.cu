@@ -40,6 +40,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "clk.h"
 #include "clk_cache.h"
 #include "clk_device.cuh"
@@ -719,11 +721,22 @@ bool fast_rows(const Turn& A, int es, bool eight)
 }
 
 // resident: CTAs an SM, 0 for k_turn_any's grid of blocks and shares of their heads.
-template <typename K>
-int launch_turn(K kern, const Turn& A, int64_t units, int resident, cudaStream_t s)
+template <void (*kern)(Turn)>
+int launch_turn(const Turn& A, int64_t units, int resident, cudaStream_t s)
 {
     const size_t bytes = ((size_t)A.B + 1) * sizeof(int64_t);
-    if (bytes > 32768 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return CLK_ECUDA;
+    if (bytes > 32768) {
+        // The limit is the kernel's, not the call's: the largest batch's, so that calls from other threads may rely on it.
+        static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return CLK_ECUDA;
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (!(ready.load(std::memory_order_relaxed) & bit) || dev > 63) {
+            constexpr int most = (CLK_MAX_BATCH + 1) * (int)sizeof(int64_t);
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return CLK_ECUDA;
+            ready.fetch_or(bit, std::memory_order_relaxed);
+        }
+    }
     const int all = pieces(A);
     int64_t x, y = 1;
     if (resident > 0) {
@@ -757,18 +770,20 @@ int launch_kind(const Turn& A, int32_t dtype, bool neighbours, int64_t units, cu
     if (fast_rows(A, dtype_bytes(dtype), EIGHT)) {
         const bool bf = dtype == CLK_DTYPE_BF16;
         const bool two = EIGHT && A.shift - team_shift(A.dim, 2) <= 3;  // 2^3 warps
-#define CLK_GO(NEIGHBOURS)                                                                                                      \
-    if (!EIGHT) return launch_turn(bf ? k_turn_rows<true, NEIGHBOURS> : k_turn_rows<false, NEIGHBOURS>, A, units, 3, s);        \
-    if (two) return launch_turn(bf ? k_turn_rows8<true, NEIGHBOURS, 2> : k_turn_rows8<false, NEIGHBOURS, 2>, A, units, 3, s);   \
-    return launch_turn(bf ? k_turn_rows8<true, NEIGHBOURS, 4> : k_turn_rows8<false, NEIGHBOURS, 4>, A, units, 2, s)
-        if (neighbours) {
-            CLK_GO(true);
-        }
-        CLK_GO(false);
+#define CLK_GO(BF, NEIGHBOURS)                                                                   \
+    do {                                                                                         \
+        if (!EIGHT) return launch_turn<k_turn_rows<BF, NEIGHBOURS>>(A, units, 3, s);             \
+        if (two) return launch_turn<k_turn_rows8<BF, NEIGHBOURS, 2>>(A, units, 3, s);            \
+        return launch_turn<k_turn_rows8<BF, NEIGHBOURS, 4>>(A, units, 2, s);                     \
+    } while (0)
+        if (bf && neighbours) CLK_GO(true, true);
+        if (bf) CLK_GO(true, false);
+        if (neighbours) CLK_GO(false, true);
+        CLK_GO(false, false);
 #undef CLK_GO
     }
 #define CLK_GO(T) \
-    return neighbours ? launch_turn(k_turn_any<T, true, EIGHT>, A, units, 0, s) : launch_turn(k_turn_any<T, false, EIGHT>, A, units, 0, s)
+    return neighbours ? launch_turn<k_turn_any<T, true, EIGHT>>(A, units, 0, s) : launch_turn<k_turn_any<T, false, EIGHT>>(A, units, 0, s)
     switch (dtype) {
     case CLK_DTYPE_BF16: CLK_GO(__nv_bfloat16);
     case CLK_DTYPE_F16: CLK_GO(__half);
