@@ -530,12 +530,15 @@ __global__ void __launch_bounds__(kThreads, 3) k_turn_rows(const __grid_constant
 }
 
 // log2(the rows of a block and head that a warp holds by `steps`)
-__host__ __device__ inline int team_shift(int dim, int steps)
+__host__ __device__ constexpr int team_shift(int dim, int steps)
 {
     int n = 0;
     while (2 << n <= steps * (32 / (dim / 16))) ++n;
     return n;
 }
+
+// Rows of 128 elements are the longest: with four steps a team's warps hold any block (with two, where the host says so).
+static_assert(kWarps << team_shift(128, 4) >= kMostRows, "warps of a team");
 
 // The same into 8 bits: a warp holds rows of a block and head, a team of at most kWarps warps them all.
 template <bool BF16, bool NEIGHBOURS, int STEPS>
@@ -554,8 +557,7 @@ __global__ void __launch_bounds__(kThreads, STEPS == 2 ? 3 : 2) k_turn_rows8(con
     const int va = !NEIGHBOURS && j < turning ? j : 2 * j, vb = !NEIGHBOURS && j < turning ? j + turning : 2 * j + 1;
     const int shift = min(team_shift(A.dim, STEPS), A.shift);  // log2(rows of a warp)
     const int rows = 1 << shift;
-    const int per = 1 << (A.shift - shift);  // warps of a team
-    if (per > kWarps) return;  // (the host chose STEPS so that they are not)
+    const int per = 1 << (A.shift - shift);  // warps of a team, at most kWarps
     const int team = warp / per, part = warp - team * per, teams = kWarps / per;
     Share share(before[A.B], pieces(A));
     for (int64_t u; share.next(&u);) {
@@ -769,7 +771,7 @@ int launch_kind(const Turn& A, int32_t dtype, bool neighbours, int64_t units, cu
 {
     if (fast_rows(A, dtype_bytes(dtype), EIGHT)) {
         const bool bf = dtype == CLK_DTYPE_BF16;
-        const bool two = EIGHT && A.shift - team_shift(A.dim, 2) <= 3;  // 2^3 warps
+        const bool two = EIGHT && 1 << A.shift <= kWarps << team_shift(A.dim, 2);
 #define CLK_GO(BF, NEIGHBOURS)                                                                   \
     do {                                                                                         \
         if (!EIGHT) return launch_turn<k_turn_rows<BF, NEIGHBOURS>>(A, units, 3, s);             \
