@@ -879,6 +879,8 @@ extern "C" int clk_cache_append_rotary(clk_cache* h, const int32_t* d_slots, int
         for (int64_t st : {turn->q_row, turn->q_head, turn->qo_row, turn->qo_head, turn->ko_row, turn->ko_head})
             if (st < 0) return CLK_EINVAL;
     }
+    // (a block's pieces, and a little more, are counted in 32 bits)
+    if (2 * (int64_t)layers * pool->heads + (side && turn->d_q != nullptr ? turn->q_heads : 0) > (1 << 30)) return CLK_EINVAL;
     if (B == 0 || N == 0 || layers == 0) return CLK_OK;
     if (!ok_i32(d_slots) || !ok_i32(d_count) || d_k == nullptr || d_v == nullptr || !aligned(d_k, (size_t)es) || !aligned(d_v, (size_t)es))
         return CLK_EINVAL;

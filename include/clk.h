@@ -669,7 +669,8 @@ CLK_API int clk_tree_rotate(clk_cache* h, const int32_t* d_slots, int32_t B, con
 
 /* clk_cache_append with the keys rotated on the way, into a pool of the rows'
  * type or of 8 bits.  Everything that it says of rows, counts, offsets and
- * paths holds here.  B <= CLK_MAX_BATCH.
+ * paths holds here.  B <= CLK_MAX_BATCH; 2 * layers * heads of the pool plus
+ * the query heads are at most 2^30.
  *
  * rotary (nullable: no rotation): K's row for the slot's position p is turned
  * by position p, which has to be below `positions`, or the request is left
