@@ -654,9 +654,13 @@ class ScaledPool:
                              f"got {tuple(scale.shape)} for {tuple(data.shape)}")
         if data.shape[4] > 1 and data.stride(4) != 1:
             raise ValueError("rows of data must be contiguous")
-        self.data, self.scale = data, scale
+        self._data, self._scale = data, scale
         p, g, hd, b = scale.stride()
         self._desc = ScalesDesc(scale.data_ptr(), tokens // blocks, p, g, hd, b)
+
+    # (not to be replaced: the calls have their addresses)
+    data = property(lambda self: self._data)
+    scale = property(lambda self: self._scale)
 
     @staticmethod
     def empty(layers: int, pages: int, kv_heads: int, page_tokens: int, dim: int, block: int = 16, device="cuda") -> "ScaledPool":
@@ -667,7 +671,7 @@ class ScaledPool:
 
 
 def _pool8_desc(h: Cache, pool: ScaledPool) -> PoolDesc:
-    data = pool.data
+    data = pool._data
     planes, pages, heads, tokens, dim = data.shape
     if pages < h.num_pages or tokens != h.page_tokens:
         raise ValueError(f"pool must have >= {h.num_pages} pages and {h.page_tokens} tokens a page, got {tuple(data.shape)}")
@@ -786,8 +790,12 @@ class Rotary:
         if not table.is_cuda or table.dtype != torch.float32 or table.dim() != 3 or table.shape[1] != 2 or not table.is_contiguous() \
                 or table.numel() == 0:
             raise ValueError("table must be a contiguous float32 CUDA tensor [positions, 2, pairs]")
-        self.table, self.neighbours = table, bool(neighbours)
+        self._table, self._neighbours = table, bool(neighbours)
         self._desc = RotaryDesc(table.data_ptr(), table.shape[0], table.shape[2], int(self.neighbours))
+
+    # (not to be replaced: the calls have the address)
+    table = property(lambda self: self._table)
+    neighbours = property(lambda self: self._neighbours)
 
     @staticmethod
     def of(freq, positions: int, factor: float = 1.0, neighbours: bool = False, device="cuda") -> "Rotary":
