@@ -1178,16 +1178,17 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
         }
     }
 
-    // The joins run with equal shares of the registers again.
+    // ---- Parts are written: raise the flag, join what was cut. ----
+    tmem_before();
+    __syncthreads();
+    // The joins run with equal shares of the registers again.  (Behind the barrier: a warp without work would else take back
+    // what it gave before the softmax warps have it, and one of them would wait for registers for ever.)
     if (E8) {
         if (warp < kCopyWarp)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     }
-    // ---- Parts are written: raise the flag, join what was cut. ----
-    tmem_before();
-    __syncthreads();
     if (warp == kMmaWarp) {
         tmem_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

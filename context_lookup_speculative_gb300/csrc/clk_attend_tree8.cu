@@ -878,14 +878,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         }
     }
 
-    // The joins run with equal shares of the registers again.
+    // ---- Parts are written: raise the flag, join what was cut. ----
+    tmem_before();
+    __syncthreads();
+    // The joins run with equal shares of the registers again.  (Behind the barrier: a warp without work would else take back
+    // what it gave before the softmax warps have it, and one of them would wait for registers for ever.)
     if (warp < kCopyWarp)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     else
         asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
-    // ---- Parts are written: raise the flag, join what was cut. ----
-    tmem_before();
-    __syncthreads();
     if (warp == kMmaWarp) {
         tmem_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
