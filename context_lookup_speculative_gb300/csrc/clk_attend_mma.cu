@@ -138,6 +138,7 @@ template <int DP, bool BF16, bool PROMPT, bool E8>
 __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constant__ Maps M, const __grid_constant__ Attend A,
                                                             const __grid_constant__ Shape S, void* scratch)
 {
+    static_assert(PROMPT || !E8, "trees over a cache in 8 bits have a kernel of their own");
     using L = Lay<DP, PROMPT, E8>;
     using K = typename L::K;
     constexpr int kThreads = clk::kThreads<E8>;
@@ -592,9 +593,9 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (kRaised && warp == kCopyWarp2) {
+        if (E8 && warp == kCopyWarp2) {
             // ---- Scales beyond 2^7, segment by segment (this warp has nothing to copy). ----
-            for (int seg = 0; w.left > 0; w.next(A, S, plan, near), ++seg) {
+            for (int seg = 0; kRaised && w.left > 0; w.next(A, S, plan, near), ++seg) {
                 // A lane has one of eight blocks of 16 keys of every other tile, of K or of V.
                 const int key = 16 * (lane & 7), tiles = (w.t1 < w.x.ctx_tiles ? w.t1 : w.x.ctx_tiles) - w.t0;
                 const float* const plane = (lane & 8 ? A.vs : A.ks) + w.h * A.scale_head + ((key & (A.C.page_tokens() - 1)) >> A.scale_shift) * A.scale_block;
@@ -629,10 +630,10 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
             // With trees one brings K and the other V, so that small pages' copies go side by side (256 short requests,
             // pages of 16: 119 us, by alternate tiles 155); with prompts they take alternate tiles, which keeps K and
             // V in step (a 25,000-token prompt: 3.16 ms, by K and V 3.26).  The first also brings Q.
+            // With a cache in 8 bits one warp copies all that is not converted.
             const int odd = warp == kCopyWarp ? 0 : 1;
-            constexpr bool kApartKV = !PROMPT || E8;
-            const bool brings_k = !kApartKV || odd == 0, brings_v = !kApartKV || odd == 1;
-            auto my = [&](int tile) { return kApartKV || (tile & 1) == odd; };
+            const bool brings_k = PROMPT || odd == 0, brings_v = PROMPT || odd == 1;
+            auto my = [&](int tile) { return !PROMPT || E8 || (tile & 1) == odd; };
             // With a cache in 8 bits: tiles to be converted so far, and places in use, with the phase that ends the last
             // copy to each.
             int g = 0;
@@ -697,8 +698,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                         }
                         copies_arrive(bar);
                     };
-                    // Tiles to be converted, K before V.  One warp brings them all: it sees every phase of their places.
-                    if (E8 && cached && odd == 0) {
+                    // Tiles to be converted, K before V: one warp sees every phase of their places.
+                    if (E8 && cached) {
 #pragma unroll 1
                         for (int v = 0; ok && v < 2; ++v, ++g) {
                             const int gi = g % L::kGs;
@@ -932,9 +933,9 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                 const float* const all = reinterpret_cast<const float*>(sm + L::oScale) + 8 * gi;
                 char* const to = dst + (c >> 2) * next;
                 const bool plain = __all_sync(0xffffffffu, fits<BF16>(all[lane & 7]) && (!kRaised || over == 0));
-                // Two turns a pass, the next pass's codes on their way.  (All of them unrolled were 10 KB of instructions,
-                // which with the softmax's do not stay in the instruction cache: three quarters of the requests hit, and
-                // every warp waited: 64 requests 636 us.)
+                // Two turns a pass, the next pass's codes on their way.  (More of them unrolled are instructions that with the
+                // softmax's do not stay in the instruction cache, and every warp waits: 4,000 tokens behind 25,000, 32/8 heads
+                // of 128, took 1,920 us with four turns a pass, 1,844 with two, 1,892 with one, when this was measured.)
                 auto passes = [&](auto plain_c) {
                     constexpr bool kPlain = decltype(plain_c)::value != 0;
                     constexpr int pass = kPlain ? 2 : 1;
@@ -1017,8 +1018,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.kbox) * 128u);
                     __syncwarp();
                     if (lane < L::kHalves)
-                        copy_box(ks + ki * L::kBytes + lane * L::kHalf, &M.k, 64 * lane, w.h,
-                                 (PROMPT ? w.x.base : 0) + (t - w.x.ctx_tiles) * kTile, PROMPT ? 0 : w.b, full);
+                        copy_box(ks + ki * L::kBytes + lane * L::kHalf, &M.k, 64 * lane, w.h, w.x.base + (t - w.x.ctx_tiles) * kTile, 0, full);
                 }
                 return true;
             };
@@ -1036,8 +1036,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                         if (lane == 0) bar_expect(full, (uint32_t)(L::kHalves * S.vbox) * 128u);
                         __syncwarp();
                         if (lane < L::kHalves)
-                            copy_box(vs + vi * L::kVBytes + lane * (L::kHalf / 2), &M.v, 64 * lane, w.h,
-                                     (PROMPT ? w.x.base : 0) + n0 + 64 * team, PROMPT ? 0 : w.b, full);
+                            copy_box(vs + vi * L::kVBytes + lane * (L::kHalf / 2), &M.v, 64 * lane, w.h, w.x.base + n0 + 64 * team, 0, full);
                     }
                 } else {
                     // a half without tokens
@@ -1095,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
                     i += w.t1 - w.t0;
                     for (int t = w.t0 > w.x.ctx_tiles ? w.t0 : w.x.ctx_tiles; ok && t < w.t1; ++t) {
                         const int n0 = (t - w.x.ctx_tiles) * kTile, have = w.x.rows - n0;
-                        const bool look = !PROMPT || n0 + kTile - 1 > w.item * S.block;
+                        const bool look = n0 + kTile - 1 > w.item * S.block;
                         for (int hf = 0; hf < 2; ++hf) {
                             const int at = 2 * (i - (w.t1 - t)) + hf, vi = at % L::kV, left = have - 64 * hf;
                             if (left <= 0) break;
