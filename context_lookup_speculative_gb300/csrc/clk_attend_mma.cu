@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kThreads<E8>, 1) k_attend(const __grid_constan
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 
-    make_plan<K, kThreads>(A, S, reinterpret_cast<long long*>(sm), plan, near, cut, stop, call, began);  // the rings are not in use yet
+    // (the rings are not in use yet)
+    make_plan<K, kThreads>(A, S, reinterpret_cast<long long*>(sm), plan, near, cut, stop, call, began, E8 ? __shfl_sync(0xffffffffu, tid >> 5, 0) : warp);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the planning scratch lies where tiles go
     tmem_before();
     __syncthreads();

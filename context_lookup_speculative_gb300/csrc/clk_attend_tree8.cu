@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_tree8(const __grid_const
         bar_init(base + L::oDrain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    make_plan<K, kThreads>(A, S, reinterpret_cast<long long*>(sm), plan, near, cut, stop, call, began);  // the rings are not in use yet
+    // (the rings are not in use yet)
+    make_plan<K, kThreads>(A, S, reinterpret_cast<long long*>(sm), plan, near, cut, stop, call, began, __shfl_sync(0xffffffffu, tid >> 5, 0));
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the planning scratch lies where tiles go
     tmem_before();
     __syncthreads();
