@@ -48,8 +48,7 @@ inline int dtype_bytes(int32_t dtype)
     return dtype == CLK_DTYPE_F32 ? 4 : dtype == CLK_DTYPE_BF16 || dtype == CLK_DTYPE_F16 ? 2 : 0;
 }
 
-// Bytes of an element of rows outside a pool, and of a pool's, 8 bits among them; 0 for another type.
-inline int row_bytes(int32_t dtype) { return dtype_bytes(dtype); }
+// The same for a pool, which may be of 8 bits.
 inline int pool_bytes(int32_t dtype) { return dtype == CLK_DTYPE_E4M3 ? 1 : dtype_bytes(dtype); }
 
 // CLK_OK for a pool whose fields are usable, its type aside.

@@ -806,7 +806,7 @@ extern "C" int clk_tree_rotate(clk_cache* h, const int32_t* d_slots, int32_t B, 
     const int rc = check_cache_batch(h, B);
     if (rc != CLK_OK) return rc;
     if (B > CLK_MAX_BATCH || N < 1 || N > CLK_TREE_MAX || t == nullptr || rotary == nullptr) return CLK_EINVAL;
-    const int es = row_bytes(t->dtype);
+    const int es = dtype_bytes(t->dtype);
     if (es == 0 || t->dim < 1 || t->dim > 256 || t->kv_heads < 1 || t->q_heads < 1 || t->q_heads > 65535 || t->kv_heads > 65535)
         return CLK_EINVAL;
     if (check_rotary(rotary, t->dim) != CLK_OK) return CLK_EINVAL;
@@ -860,7 +860,7 @@ extern "C" int clk_cache_append_rotary(clk_cache* h, const int32_t* d_slots, int
 {
     const int rc = check_cache_batch(h, B);
     if (rc != CLK_OK) return rc;
-    const int es = row_bytes(dtype);
+    const int es = dtype_bytes(dtype);
     if (B > CLK_MAX_BATCH || es == 0) return CLK_EINVAL;
     const bool eight = scales != nullptr;
     if (eight ? check_pool8(pool, scales, h->dev.page_tokens()) != CLK_OK : check_pool(pool) != CLK_OK || pool->dtype != dtype) return CLK_EINVAL;
