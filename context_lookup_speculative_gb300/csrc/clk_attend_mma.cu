@@ -57,9 +57,9 @@
 // tiles converts the tiles again: 3,800 of a step's 9,400 instructions, beside
 // 4,800 of the softmax, which together do not stay in the instruction cache (84%
 // of the fetches hit).  So a step takes 4,700 cycles: 4,000 tokens behind 25,000
-// (32/8 heads of 128) 1,725 us, 1,030 TFLOP/s, where 16 bits reach 1,700; 8
-// prompts of 100 to 1,500 behind up to 8,192 (24/4 heads of 64) 351 us, 610
-// TFLOP/s, where they reach 1,020.
+// (32/8 heads of 128) 1,694 us, 1,045 TFLOP/s, where 16 bits reach 1,700; 8
+// prompts of 100 to 1,500 behind up to 8,192 (24/4 heads of 64) 330 to 357 us, 600
+// to 650 TFLOP/s, where they reach 1,020.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -16,7 +16,8 @@
 // where a power of two costs nothing: it is part of the exponent.  (Multiplied
 // into V instead, V took four times the instructions, and with K in 16 bits too
 // eight: 64 requests of 2,000 to 32,000 tokens, 32/8 heads of 128, 1,083 us
-// with both in 16 bits, 640 and after some steps 511 with V alone, 506 so.)
+// with both in 16 bits, 640 and after some steps 511 with V alone, 506 to 515
+// so.)
 // New tokens' K and V stay in their own type.
 //
 // A row's 128 columns belong to two threads in two warps, so that a tile's
@@ -24,7 +25,8 @@
 // M, which O shares.  So the pair meets once a tile before it gives its weights
 // away; where a row of either asks for it, both take up the new M.  (With one
 // thread a row eight requests of 262,144 tokens took 322 us, with two 278; 256
-// of 300 to 4,096 tokens with heads of 64, though, 185 and 202.)
+// of 300 to 4,096 tokens with heads of 64, though, 185 and 202, and 191 after
+// later steps.)
 //
 // What bounds it: 128 keys of 128 elements take DRAM 1,400 cycles of an SM.  The
 // products take 1,050 (bfloat16; 1,300 float16), those with Q's parts from

@@ -158,11 +158,13 @@ struct Trees {
     // of 2 tiles 68.3, of 4 62.2 us.
     static constexpr int whole = 4;
 };
-// Tiles of a cache in 8 bits take half the time.  Measured with 3, 5 and 8 more
-// units: 64 requests of 2,000 to 32,000 tokens and 16 nodes (32/8 heads of 128)
-// 516, 511, 509 us, 256 of 300 to 4,096 and 13 nodes (24/4 heads of 64) 207,
-// 204, 192; one token over 2,048 rows 20.5, 22.6, 22.5.  Uncut items of up to 12
-// tiles made no difference.
+// Over a cache in 8 bits an item's ends (its Q in parts before its first scores)
+// cost more beside its tiles.  Measured with 3, 5 and 8 more units: 64 requests
+// of 2,000 to 32,000 tokens and 16 nodes (32/8 heads of 128) 525, 519, 517 us,
+// 256 of 300 to 4,096 and 13 nodes (24/4 heads of 64) 204, 202, 195; one token
+// over 2,048 rows 24.7, 28.7, 26.6.  Items of up to 4, 6 and 12 tiles uncut: 256
+// requests of 64 to 512 tokens and 13 nodes 111, 103, 102, 64 of 64 to 1,024 and
+// 16 nodes (32/8 heads of 128) 81, 81, 77, the 256 longer ones 195, 195, 196.
 struct Trees8 {
     static constexpr bool prompt = false, in_log2 = true;
     static constexpr int extra = 8, whole = 6;
